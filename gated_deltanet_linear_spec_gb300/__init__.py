@@ -2,7 +2,9 @@
 
 The functions here mirror the C entry points in ``include/gdn.h`` one for one
 (``gdn_conv_update``, ``gdn_recurrent_step``, ``gdn_chunk_prefill``, ``gdn_mixed_batch``,
-``gdn_workspace_bytes``) and only marshal arguments: torch CUDA tensors become device
+``gdn_workspace_bytes``, and the paged key-value cache's ``gdn_paged_attention``, ``gdn_kv_append``,
+``gdn_kv_reserve``, ``gdn_kv_release``, ``gdn_kv_fork``, ``gdn_kv_copy_pages``, ``gdn_kv_compact``,
+``gdn_copy_slots``) and only marshal arguments: torch CUDA tensors become device
 pointers, the current torch stream becomes the ``cudaStream_t``, and a negative return code
 becomes a ``GdnError``.  Every step of the path runs in the library's CUDA kernels; there is
 no fallback, and a missing library raises at the first call.
@@ -25,6 +27,7 @@ GDN_QKV_PACKED, GDN_QKV_PER_KHEAD = 0, 1
 GDN_CONV_ROLLED, GDN_CONV_PER_SLOT = 0, 1
 STATUS_SLOT_RANGE, STATUS_NUM_ACCEPTED, STATUS_TOKEN_RANGE, STATUS_ROW_RANGE = 0x1, 0x2, 0x4, 0x8
 STATUS_WAIT_TIMEOUT = 0x10
+STATUS_PAGE_RANGE, STATUS_PAGE_SHARED, STATUS_NO_PAGES = 0x20, 0x40, 0x80
 ERRORS = {-1: "NULL_ARG", -2: "SPEC_PAIR", -3: "SHAPE", -4: "CONSERVATION", -5: "WORKSPACE",
           -6: "DTYPE", -7: "CUDA", -8: "ALIGN"}
 
@@ -61,8 +64,28 @@ class _Rows(ctypes.Structure):
                 ("spec_cols", ctypes.c_int32)]
 
 
+class _KvCache(ctypes.Structure):
+    _fields_ = [("k_pool", ctypes.c_void_p), ("v_pool", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
+                ("block_table", ctypes.c_void_p), ("refcount", ctypes.c_void_p), ("num_pages", ctypes.c_int32),
+                ("num_table_rows", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class _KvRows(ctypes.Structure):
+    _fields_ = [("num_seqs", ctypes.c_int32), ("num_tokens", ctypes.c_int32), ("query_start_loc", ctypes.c_void_p),
+                ("token_indx", ctypes.c_void_p), ("table_rows", ctypes.c_void_p), ("kv_lens", ctypes.c_void_p),
+                ("max_query_len", ctypes.c_int32)]
+
+
+class _AttnDesc(ctypes.Structure):
+    _fields_ = [("num_q_heads", ctypes.c_int32), ("scale", ctypes.c_float), ("window", ctypes.c_int32),
+                ("num_sinks", ctypes.c_int32)]
+
+
 EXPORTS = ("gdn_workspace_bytes", "gdn_prefill_workspace_bytes", "gdn_conv_update", "gdn_recurrent_step", "gdn_chunk_prefill",
-           "gdn_mixed_batch", "gdn_mixed_batch_static_workspace", "gdn_status_string")
+           "gdn_mixed_batch", "gdn_mixed_batch_static_workspace", "gdn_status_string", "gdn_kv_append", "gdn_paged_attention",
+           "gdn_attention_workspace_bytes", "gdn_kv_reserve", "gdn_kv_release", "gdn_kv_fork", "gdn_kv_copy_pages",
+           "gdn_kv_compact", "gdn_kv_workspace_bytes", "gdn_copy_slots")
 # include/gdn_testing.h: hooks that let tests drive the kernels' failure paths
 TESTING_EXPORTS = ("gdn_testing_set_prefill_faults",)
 STATIC_WORKSPACE_BYTES = 16 << 20
@@ -101,6 +124,21 @@ def library() -> ctypes.CDLL:
             lib.gdn_mixed_batch_static_workspace.restype = ctypes.c_int
             lib.gdn_mixed_batch_static_workspace.argtypes = [P(_LayerDesc), P(_LayerParams), P(_Pools), VP, VP, VP,
                                                              I32, P(_Rows), I32, I32, P(_Rows), VP, VP, VP]
+            I64, SZ = ctypes.c_int64, ctypes.c_size_t
+            for name, res, args in (
+                    ("gdn_kv_append", ctypes.c_int, [P(_KvCache), P(_KvRows), VP, I64, VP, I64, I32, VP, VP]),
+                    ("gdn_paged_attention", ctypes.c_int, [P(_AttnDesc), P(_KvCache), P(_KvRows), VP, I64, I32, VP,
+                                                           I64, VP, SZ, VP, VP]),
+                    ("gdn_attention_workspace_bytes", SZ, [P(_AttnDesc), P(_KvCache), P(_KvRows)]),
+                    ("gdn_kv_reserve", ctypes.c_int, [P(_KvCache), I32, VP, VP, VP, VP, SZ, VP, VP]),
+                    ("gdn_kv_release", ctypes.c_int, [P(_KvCache), I32, VP, VP, VP, VP, VP]),
+                    ("gdn_kv_fork", ctypes.c_int, [P(_KvCache), I32, VP, VP, VP, VP, SZ, VP, VP]),
+                    ("gdn_kv_copy_pages", ctypes.c_int, [P(_KvCache), I32, VP, VP, VP, VP]),
+                    ("gdn_kv_compact", ctypes.c_int, [P(_KvCache), VP, VP, SZ, VP, VP]),
+                    ("gdn_kv_workspace_bytes", SZ, [P(_KvCache), I32]),
+                    ("gdn_copy_slots", ctypes.c_int, [P(_LayerDesc), P(_Pools), I32, VP, VP, VP, VP])):
+                fn = getattr(lib, name)
+                fn.restype, fn.argtypes = res, args
             lib.gdn_testing_set_prefill_faults.restype = ctypes.c_int
             lib.gdn_testing_set_prefill_faults.argtypes = [ctypes.c_uint64, I32]
             _lib = lib
@@ -200,6 +238,110 @@ class Rows:
                      _ptr(self.num_accepted_tokens, i32, "num_accepted_tokens"), cols)
 
 
+def _int32(t: Optional[torch.Tensor], name: str, count: Optional[int] = None) -> Optional[int]:
+    if t is not None and count is not None and t.numel() != count:
+        raise ValueError(f"{name}: expected {count} entries, got {t.numel()}")
+    return _ptr(t, torch.int32, name)
+
+
+def _token_rows(t: torch.Tensor, dtype: torch.dtype, heads: int, dim: int, name: str):
+    """Pointer and token stride of a [tokens, heads, dim] tensor; the token dimension may be strided."""
+    if not t.is_cuda:
+        raise TypeError(f"{name}: expected a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
+        raise ValueError(f"{name}: expected [tokens, {heads}, {dim}], got {tuple(t.shape)}")
+    st = t.stride()
+    if (dim > 1 and st[2] != 1) or (heads > 1 and st[1] != dim):
+        raise TypeError(f"{name}: the heads of a token must be contiguous")
+    return t.data_ptr(), (st[0] if t.shape[0] > 1 else 0)
+
+
+@dataclass(frozen=True)
+class KvCache:
+    """The paged key-value cache of an attention layer (``gdn_kv_cache``): pools
+    [num_pages, num_kv_heads, page_size, head_dim], whose page dimension may be strided (K and V as
+    halves of one allocation), the block table [table rows, max_pages] and the pages' holder
+    counts, both int32.  The tensors stay the caller's; the descriptor is checked once, here."""
+    k_pool: torch.Tensor
+    v_pool: torch.Tensor
+    block_table: torch.Tensor
+    refcount: Optional[torch.Tensor] = None
+
+    def __post_init__(self):
+        k, v = self.k_pool, self.v_pool
+        if not (k.is_cuda and v.is_cuda):
+            raise TypeError("k_pool, v_pool: expected CUDA tensors")
+        if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype:
+            raise ValueError("k_pool and v_pool: one [num_pages, num_kv_heads, page_size, head_dim] shape and dtype")
+        for t, name in ((k, "k_pool"), (v, "v_pool")):
+            if not t[:1].is_contiguous():
+                raise TypeError(f"{name}: a page must be contiguous")
+        if k.shape[0] > 1 and k.stride(0) != v.stride(0):
+            raise ValueError("k_pool and v_pool: expected one page stride")
+        if self.block_table.dim() != 2:
+            raise ValueError("block_table: expected [table rows, max_pages]")
+        pages, heads, size, dim = k.shape
+        if max(pages, heads, size, dim, *self.block_table.shape) >= 1 << 31:
+            raise ValueError("a dimension does not fit 32 bits")
+        desc = _KvCache(k.data_ptr(), v.data_ptr(), k.stride(0) if pages > 1 else 0,
+                        _int32(self.block_table, "block_table"), _int32(self.refcount, "refcount", pages), pages,
+                        self.block_table.shape[0], self.block_table.shape[1], size, heads, dim, _dtype_code(k.dtype))
+        object.__setattr__(self, "_desc", desc)
+        object.__setattr__(self, "_ref", ctypes.byref(desc))
+
+    @property
+    def dtype(self) -> torch.dtype:
+        return self.k_pool.dtype
+
+
+@dataclass(frozen=True)
+class KvRows:
+    """The rows of one subset as an attention layer sees them (``gdn_kv_rows``, int32 CUDA tensors):
+    row n's new tokens are the last of its ``kv_lens[n]`` tokens, its pages those of table row
+    ``table_rows[n]`` (None: n).  ``from_rows`` takes the GDN layers' rows over."""
+    query_start_loc: torch.Tensor
+    num_tokens: int
+    kv_lens: torch.Tensor
+    max_query_len: int
+    table_rows: Optional[torch.Tensor] = None
+    token_indx: Optional[torch.Tensor] = None
+
+    def __post_init__(self):
+        n = self.query_start_loc.numel() - 1
+        desc = _KvRows(n, int(self.num_tokens), _int32(self.query_start_loc, "query_start_loc"),
+                       _int32(self.token_indx, "token_indx", int(self.num_tokens)),
+                       _int32(self.table_rows, "table_rows", n), _int32(self.kv_lens, "kv_lens", n),
+                       int(self.max_query_len))
+        object.__setattr__(self, "_desc", desc)
+        object.__setattr__(self, "_ref", ctypes.byref(desc))
+
+    @classmethod
+    def from_rows(cls, rows: "Rows", kv_lens: torch.Tensor, max_query_len: int,
+                  table_rows: Optional[torch.Tensor] = None) -> "KvRows":
+        return cls(rows.query_start_loc, rows.num_tokens, kv_lens, max_query_len, table_rows, rows.token_indx)
+
+    @property
+    def num_seqs(self) -> int:
+        return self.query_start_loc.numel() - 1
+
+
+@dataclass(frozen=True)
+class Attention:
+    """``gdn_attn_desc``: scale <= 0 selects 1/sqrt(head_dim), window <= 0 none; with a window the
+    first ``num_sinks`` positions stay visible."""
+    num_q_heads: int
+    scale: float = 0.0
+    window: int = 0
+    num_sinks: int = 0
+
+    def __post_init__(self):
+        desc = _AttnDesc(self.num_q_heads, float(self.scale), self.window, self.num_sinks)
+        object.__setattr__(self, "_desc", desc)
+        object.__setattr__(self, "_ref", ctypes.byref(desc))
+
+
 def _rows_ref(r: Optional[Rows]):
     return None if r is None else ctypes.byref(r.c())
 
@@ -208,6 +350,14 @@ def _stream(stream) -> Optional[int]:
     if stream is None:
         stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _scratch(nbytes: int, device, stream) -> torch.Tensor:
+    """A workspace that its allocator keeps until the work on ``stream`` is done with it."""
+    ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
+    if stream is not None:
+        ws.record_stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
+    return ws
 
 
 def _check(rc: int) -> None:
@@ -305,6 +455,109 @@ def gdn_mixed_batch_static_workspace(layer: Layer, params: Params, pools: Pools,
     _check(rc)
 
 
+# ------------------------------------------------------------------------------------------
+# The paged key-value cache
+
+def gdn_kv_append(cache: KvCache, rows: KvRows, k: torch.Tensor, v: torch.Tensor,
+                  status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Writes the new tokens' k, v [num_global_tokens, num_kv_heads, head_dim] into the rows' pages."""
+    _, heads, _, dim = cache.k_pool.shape
+    kp, ks = _token_rows(k, cache.dtype, heads, dim, "k")
+    vp, vs = _token_rows(v, cache.dtype, heads, dim, "v")
+    if k.shape[0] != v.shape[0]:
+        raise ValueError("k and v: expected one token count")
+    _check(library().gdn_kv_append(cache._ref, rows._ref, kp, ks, vp, vs, k.shape[0],
+                                   _ptr(status, torch.int32, "status"), _stream(stream)))
+
+
+def gdn_attention_workspace_bytes(attn: Attention, cache: KvCache, rows: KvRows) -> int:
+    return int(library().gdn_attention_workspace_bytes(attn._ref, cache._ref, rows._ref))
+
+
+def gdn_paged_attention(attn: Attention, cache: KvCache, rows: KvRows, q: torch.Tensor, out: torch.Tensor,
+                        workspace: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                        stream=None) -> None:
+    """Causal attention of the rows' new tokens over their pages (which already hold them);
+    q, out [num_global_tokens, num_q_heads, head_dim]."""
+    dim = cache.k_pool.shape[3]
+    qp, qs = _token_rows(q, cache.dtype, attn.num_q_heads, dim, "q")
+    op, os_ = _token_rows(out, cache.dtype, attn.num_q_heads, dim, "out")
+    if q.shape[0] != out.shape[0]:
+        raise ValueError("q and out: expected one token count")
+    if workspace is None:
+        workspace = _scratch(gdn_attention_workspace_bytes(attn, cache, rows), q.device, stream)
+    _check(library().gdn_paged_attention(attn._ref, cache._ref, rows._ref, qp, qs, q.shape[0], op, os_,
+                                         _ptr(workspace, torch.uint8, "workspace"), workspace.numel(),
+                                         _ptr(status, torch.int32, "status"), _stream(stream)))
+
+
+def gdn_kv_workspace_bytes(cache: KvCache, count: int) -> int:
+    """Workspace of gdn_kv_reserve and gdn_kv_fork over ``count`` rows, and of gdn_kv_compact."""
+    return int(library().gdn_kv_workspace_bytes(cache._ref, int(count)))
+
+
+def _kv_workspace(cache: KvCache, count: int, workspace: Optional[torch.Tensor], stream) -> torch.Tensor:
+    return _scratch(gdn_kv_workspace_bytes(cache, count), cache.k_pool.device, stream) if workspace is None else workspace
+
+
+def gdn_kv_reserve(cache: KvCache, table_rows: Optional[torch.Tensor], from_lens: torch.Tensor, to_lens: torch.Tensor,
+                   workspace: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                   stream=None) -> None:
+    """Gives each listed table row free pages for its tokens [from_lens, to_lens)."""
+    n = from_lens.numel()
+    ws = _kv_workspace(cache, n, workspace, stream)
+    _check(library().gdn_kv_reserve(cache._ref, n, _int32(table_rows, "table_rows", n), _int32(from_lens, "from_lens"),
+                                    _int32(to_lens, "to_lens", n), _ptr(ws, torch.uint8, "workspace"), ws.numel(),
+                                    _ptr(status, torch.int32, "status"), _stream(stream)))
+
+
+def gdn_kv_release(cache: KvCache, table_rows: torch.Tensor, first_page: Optional[torch.Tensor] = None,
+                   last_page: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                   stream=None) -> None:
+    """Gives back the pages of entries [first_page, last_page) of each listed table row."""
+    n = table_rows.numel()
+    _check(library().gdn_kv_release(cache._ref, n, _int32(table_rows, "table_rows"),
+                                    _int32(first_page, "first_page", n), _int32(last_page, "last_page", n),
+                                    _ptr(status, torch.int32, "status"), _stream(stream)))
+
+
+def gdn_kv_fork(cache: KvCache, src_rows: torch.Tensor, dst_rows: torch.Tensor, lens: torch.Tensor,
+                workspace: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Table row dst_rows[i] becomes a holder of the first lens[i] tokens of src_rows[i]."""
+    n = src_rows.numel()
+    ws = _kv_workspace(cache, n, workspace, stream)
+    _check(library().gdn_kv_fork(cache._ref, n, _int32(src_rows, "src_rows"), _int32(dst_rows, "dst_rows", n),
+                                 _int32(lens, "lens", n), _ptr(ws, torch.uint8, "workspace"), ws.numel(),
+                                 _ptr(status, torch.int32, "status"), _stream(stream)))
+
+
+def gdn_kv_copy_pages(cache: KvCache, src_pages: torch.Tensor, dst_pages: torch.Tensor,
+                      status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Copies page src_pages[i] onto dst_pages[i] in both pools."""
+    n = src_pages.numel()
+    _check(library().gdn_kv_copy_pages(cache._ref, n, _int32(src_pages, "src_pages"),
+                                       _int32(dst_pages, "dst_pages", n), _ptr(status, torch.int32, "status"),
+                                       _stream(stream)))
+
+
+def gdn_kv_compact(cache: KvCache, num_live: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                   status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Moves the live pages to ids 1..M; ``num_live`` (int32, one entry) receives M."""
+    ws = _kv_workspace(cache, 0, workspace, stream)
+    _check(library().gdn_kv_compact(cache._ref, _int32(num_live, "num_live", 1), _ptr(ws, torch.uint8, "workspace"),
+                                    ws.numel(), _ptr(status, torch.int32, "status"), _stream(stream)))
+
+
+def gdn_copy_slots(layer: Layer, pools: Pools, src_slots: torch.Tensor, dst_slots: torch.Tensor,
+                   status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Copies GDN state: slot src_slots[i] of both pools onto dst_slots[i] (a NULL source reads as zeros)."""
+    n = src_slots.numel()
+    act = layer.act_dtype
+    _check(library().gdn_copy_slots(ctypes.byref(layer.c()), ctypes.byref(pools.c(act)), n,
+                                    _int32(src_slots, "src_slots"), _int32(dst_slots, "dst_slots", n),
+                                    _ptr(status, torch.int32, "status"), _stream(stream)))
+
+
 def gdn_testing_set_prefill_faults(wait_ns: int = 0, drop_copy_chunk: int = -1) -> None:
     """Test hook (include/gdn_testing.h): the wall-clock limit of the chunked prefill's bounded
     waits (0 = the default, one second) and a chunk whose record copy the scan leaves out on
@@ -316,4 +569,7 @@ __all__ = ["Layer", "Params", "Pools", "Rows", "GdnError", "library", "LIB_PATH"
            "gdn_workspace_bytes", "gdn_prefill_workspace_bytes", "mixed_batch_workspace_bytes", "STATUS_WAIT_TIMEOUT", "gdn_conv_update", "gdn_recurrent_step", "gdn_chunk_prefill",
            "gdn_mixed_batch", "gdn_mixed_batch_static_workspace", "STATIC_WORKSPACE_BYTES",
            "TESTING_EXPORTS", "gdn_testing_set_prefill_faults", "GDN_F32", "GDN_BF16", "STATUS_SLOT_RANGE", "STATUS_NUM_ACCEPTED",
-           "STATUS_TOKEN_RANGE", "STATUS_ROW_RANGE"]
+           "STATUS_TOKEN_RANGE", "STATUS_ROW_RANGE", "KvCache", "KvRows", "Attention", "gdn_kv_append",
+           "gdn_paged_attention", "gdn_attention_workspace_bytes", "gdn_kv_reserve", "gdn_kv_release", "gdn_kv_fork",
+           "gdn_kv_copy_pages", "gdn_kv_compact", "gdn_kv_workspace_bytes", "gdn_copy_slots", "STATUS_PAGE_RANGE",
+           "STATUS_PAGE_SHARED", "STATUS_NO_PAGES"]

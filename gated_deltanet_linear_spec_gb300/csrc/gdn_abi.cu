@@ -166,6 +166,14 @@ RecLaunch rec_args(const gdn_layer_desc* d, const gdn_layer_params* prm, const g
 
 }  // namespace
 
+// The layer and pools of gdn_copy_slots (gdn_kv_abi.cu); the conv pool is optional there.
+namespace gdn {
+int check_layer_pools(const gdn_layer_desc* layer, const gdn_pools* pools) {
+  const int rc = check_layer(layer);
+  return rc ? rc : check_pools(pools, pools && pools->conv_pool);
+}
+}  // namespace gdn
+
 // A named NVTX range around each compute entry point (shows in Nsight timelines; without a tool
 // attached the push and pop are no-ops).
 struct NvtxRange {

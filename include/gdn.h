@@ -75,6 +75,10 @@ typedef enum {
                                         longer than spec_cols (row skipped)                            */
 #define GDN_STATUS_WAIT_TIMEOUT 0x10u /* a bounded wait inside a tensor-core kernel gave up; that
                                          block's results are missing (never expected in practice)  */
+#define GDN_STATUS_PAGE_RANGE 0x20u  /* a page id >= num_pages, a table row or a page range outside the table, or a
+                                        page released more often than it was held (that entry is skipped)  */
+#define GDN_STATUS_PAGE_SHARED 0x40u /* an append met a page that several rows hold (that token is skipped)  */
+#define GDN_STATUS_NO_PAGES 0x80u    /* reserve/fork: the free pages did not cover a row (that row is skipped)  */
 
 typedef enum { GDN_F32 = 0, GDN_BF16 = 1 } gdn_dtype;
 
@@ -285,6 +289,154 @@ int gdn_mixed_batch_static_workspace(const gdn_layer_desc* layer, const gdn_laye
                                      int32_t num_actual_tokens, const gdn_rows* non_spec, int32_t num_decodes,
                                      int32_t num_prefills, const gdn_rows* spec, void* out, uint32_t* d_status,
                                      void* stream);
+
+/* ------------------------------------------------------------------------------------------
+ * The paged key-value cache of the full-attention layers.
+ *
+ * A hybrid model interleaves GDN layers with full-attention layers over the same batch of
+ * decode, verify and prefill rows.  The attention layers keep their keys and values in pages:
+ * fixed blocks of page_size tokens in one pool, listed per sequence in a block table.  Nothing
+ * here reads device memory on the host, so a whole step -- reserving pages, appending,
+ * attending -- can be captured in a CUDA graph.
+ *
+ * Page ids <= 0 are NULL: they hold no tokens (no attention sees them, nothing is written).
+ * Page 0 is reserved as NULL.  refcount[p] counts the table entries that hold page p; a page is
+ * free when it is 0.  Pages are handed out lowest id first, in the order of the rows of a call
+ * and of the entries of a row, so the result of every call is determined by its inputs.
+ */
+typedef struct {
+  void* k_pool;          /* [num_pages, num_kv_heads, page_size, head_dim] dtype                    */
+  void* v_pool;          /* the same shape                                                          */
+  int64_t page_stride;   /* elements from one page to the next in both pools; 0 = dense; its bytes a
+                            multiple of 16 (a larger stride lets K and V share one allocation)       */
+  int32_t* block_table;  /* [num_table_rows, max_pages] page id of each page_size tokens of a row   */
+  int32_t* refcount;     /* [num_pages]; NULL where a call says that it may be                      */
+  int32_t num_pages;     /* 2..2^28 (page 0 is NULL)                                                */
+  int32_t num_table_rows;
+  int32_t max_pages;     /* entries of a table row; max_pages <= 2^20, max_pages * page_size < 2^31  */
+  int32_t page_size;     /* tokens of a page: 16, 32, 64, 128 or 256                                */
+  int32_t num_kv_heads;  /* Hkv, 1..1024                                                            */
+  int32_t head_dim;      /* d, a multiple of 16, <= 256                                             */
+  gdn_dtype dtype;       /* GDN_BF16 or GDN_F32: pools, q, k, v and out                             */
+} gdn_kv_cache;
+
+/*
+ * The rows of one subset of the batch as an attention layer sees them.  query_start_loc and
+ * token_indx are those of gdn_rows.  Row n owns table row table_rows[n]; its L =
+ * query_start_loc[n+1] - query_start_loc[n] new tokens are the last L of its kv_lens[n] tokens,
+ * i.e. token t is at position kv_lens[n] - L + t.  After a verify step that accepted fewer
+ * tokens the next step's kv_lens simply counts from the accepted ones.
+ * A row with L > max_query_len, kv_lens[n] < L or kv_lens[n] > max_pages * page_size, or a table
+ * row out of range is skipped (GDN_STATUS_ROW_RANGE, GDN_STATUS_PAGE_RANGE).
+ */
+typedef struct {
+  int32_t num_seqs;               /* may be 0                                                  */
+  int32_t num_tokens;             /* query_start_loc[num_seqs]                                 */
+  const int32_t* query_start_loc; /* [num_seqs+1]                                              */
+  const int32_t* token_indx;      /* [num_tokens] global token of each local token; NULL = identity */
+  const int32_t* table_rows;      /* [num_seqs]; NULL = identity                               */
+  const int32_t* kv_lens;         /* [num_seqs]                                                */
+  int32_t max_query_len;          /* no row is longer (1 for decode rows, drafts + 1 for verify) */
+} gdn_kv_rows;
+
+typedef struct {
+  int32_t num_q_heads; /* Hq, a multiple of Hkv; q-head h reads kv-head h / (Hq/Hkv)          */
+  float scale;         /* multiplies q.k; <= 0 selects 1/sqrt(d)                              */
+  int32_t window;      /* > 0: a query at position p sees keys p-window+1 .. p; <= 0: all up to p */
+  int32_t num_sinks;   /* with a window: positions below this stay visible (>= 0)             */
+} gdn_attn_desc;
+
+/*
+ * Writes the new tokens' keys and values into the rows' pages: position p of row n goes to page
+ * block_table[table_rows[n]][p / page_size], slot p % page_size, as bit copies.  Pages must have
+ * been reserved; a NULL entry is not written.  With refcount given, a page that several rows
+ * hold is not written either (GDN_STATUS_PAGE_SHARED): gdn_kv_fork leaves no row such a page at
+ * the end of its tokens.
+ *   k, v [num_global_tokens, Hkv, d] dtype, read at token_indx; k_stride, v_stride: elements from
+ *   one token to the next (0 = dense), their bytes a multiple of 16 -- slices of one fused
+ *   projection need no copy.
+ */
+int gdn_kv_append(const gdn_kv_cache* cache, const gdn_kv_rows* rows, const void* k, int64_t k_stride, const void* v,
+                  int64_t v_stride, int32_t num_global_tokens, uint32_t* d_status, void* stream);
+
+/*
+ * Causal attention of the rows' new tokens over the cache (whose pages already hold them).  The
+ * query of q-head h at position p of row n sees the row's key j when j <= p, and (window <= 0 or
+ * j > p - window or j < num_sinks), and the page of j is not NULL:
+ *   out = sum_j e^(s_j - m) v_j / sum_j e^(s_j - m),  s_j = scale q.k_j,  m = max_j s_j,
+ * in fp32, rounded once to dtype; a query that sees no key gives 0.  What a query does not see
+ * never reaches its result, whatever it holds (infinities and NaN included).
+ *   q, out [num_global_tokens, Hq, d] dtype, read and written at token_indx; q_stride,
+ *   out_stride: elements from one token to the next (0 = dense), their bytes a multiple of 16.
+ * The cache's refcount is not used and may be NULL.
+ * workspace: at least gdn_attention_workspace_bytes(attn, cache, rows) bytes, 256-byte aligned
+ * (may be NULL when that is 0); it holds the partial results of rows whose cache is split.
+ */
+int gdn_paged_attention(const gdn_attn_desc* attn, const gdn_kv_cache* cache, const gdn_kv_rows* rows, const void* q,
+                        int64_t q_stride, int32_t num_global_tokens, void* out, int64_t out_stride, void* workspace,
+                        size_t workspace_bytes, uint32_t* d_status, void* stream);
+
+/* Depends only on the host-side values of the descriptors and on the device; 0 for invalid descriptors. */
+size_t gdn_attention_workspace_bytes(const gdn_attn_desc* attn, const gdn_kv_cache* cache, const gdn_kv_rows* rows);
+
+/*
+ * Makes room: for each of the `count` table rows listed, the entries of tokens
+ * [from_lens[i], to_lens[i]) that begin a page -- entries ceil(from/page_size) ..
+ * ceil(to/page_size)-1 -- and hold no page get a free one (refcount 1).  A row gets all of them
+ * or none: when the needs of the rows up to and with it exceed the free pages it is left as it
+ * was (GDN_STATUS_NO_PAGES).  table_rows must not repeat.  NULL table_rows = identity.
+ * workspace (reserve, fork, compact): at least gdn_kv_workspace_bytes(cache, count) bytes,
+ * 256-byte aligned.
+ */
+int gdn_kv_reserve(const gdn_kv_cache* cache, int32_t count, const int32_t* table_rows, const int32_t* from_lens,
+                   const int32_t* to_lens, void* workspace, size_t workspace_bytes, uint32_t* d_status, void* stream);
+
+/*
+ * Gives pages back: entries [first_page[i], last_page[i]) of each listed table row become NULL
+ * and their pages lose a holder.  NULL first_page = 0, NULL last_page = max_pages, so both NULL
+ * frees whole rows; a finished window's old pages or a rolled-back tail are given back by range.
+ * table_rows must not repeat.
+ */
+int gdn_kv_release(const gdn_kv_cache* cache, int32_t count, const int32_t* table_rows, const int32_t* first_page,
+                   const int32_t* last_page, uint32_t* d_status, void* stream);
+
+/*
+ * Forks sequences: table row dst_rows[i] becomes a holder of the first lens[i] tokens of
+ * src_rows[i].  Pages that these tokens fill are shared; the tokens of a partly filled last page
+ * are copied into a free page, so both rows can append.  NULL entries stay NULL.  A dst row must
+ * hold no page in the entries it gets (else it is skipped, GDN_STATUS_PAGE_RANGE); dst rows must
+ * be distinct and not among the src rows.  When the free pages do not cover the needs of the
+ * rows up to and with i, row i is skipped (GDN_STATUS_NO_PAGES).  A hybrid model's sequence also
+ * has GDN state: gdn_copy_slots copies that.
+ */
+int gdn_kv_fork(const gdn_kv_cache* cache, int32_t count, const int32_t* src_rows, const int32_t* dst_rows,
+                const int32_t* lens, void* workspace, size_t workspace_bytes, uint32_t* d_status, void* stream);
+
+/* Copies page src_pages[i] onto dst_pages[i] in both pools (pairs with a NULL side are skipped;
+ * dst pages distinct and not among the src pages).  block_table and refcount are not used (may be NULL). */
+int gdn_kv_copy_pages(const gdn_kv_cache* cache, int32_t count, const int32_t* src_pages, const int32_t* dst_pages,
+                      uint32_t* d_status, void* stream);
+
+/*
+ * Moves the M live pages (refcount > 0) to ids 1..M, so that the pool's tail is free in one
+ * piece: the live pages with ids above M, lowest first, go to the free ids up to M, lowest
+ * first.  Every entry of the block table and refcount follow.  num_live (device, may be NULL)
+ * receives M.  Pages must be moved while nothing else uses the cache (one stream orders that).
+ */
+int gdn_kv_compact(const gdn_kv_cache* cache, int32_t* num_live, void* workspace, size_t workspace_bytes,
+                   uint32_t* d_status, void* stream);
+
+/* Workspace of gdn_kv_reserve and gdn_kv_fork over `count` rows and of gdn_kv_compact (any count);
+ * 0 for an invalid descriptor or a negative count. */
+size_t gdn_kv_workspace_bytes(const gdn_kv_cache* cache, int32_t count);
+
+/*
+ * Copies GDN state: slot src_slots[i] of both pools (conv history and SSM state; conv_pool may be
+ * NULL) onto dst_slots[i].  A NULL source reads as zeros, a NULL destination is not written, as
+ * in every call of this library; dst slots distinct and not among the src slots.
+ */
+int gdn_copy_slots(const gdn_layer_desc* layer, const gdn_pools* pools, int32_t count, const int32_t* src_slots,
+                   const int32_t* dst_slots, uint32_t* d_status, void* stream);
 
 /* Static text for a gdn_error value. */
 const char* gdn_status_string(int code);
