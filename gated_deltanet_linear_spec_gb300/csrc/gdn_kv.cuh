@@ -125,6 +125,11 @@ cudaError_t launch_kv_fork(const PageRowsLaunch& p, cudaStream_t s);
 cudaError_t launch_kv_compact(const PageRowsLaunch& p, int32_t* num_live, cudaStream_t s);
 cudaError_t launch_copy_items(const CopyLaunch& p, cudaStream_t s);
 
+// Rows of up to 64 queries per kv-head (bf16, d = 64, 128, 256): split over the cache's length.
+bool attn_split_supported(const AttnLaunch& p, gdn_dtype dtype);
+size_t attn_split_workspace(const AttnLaunch& p);
+cudaError_t launch_attn_split(const AttnLaunch& p, cudaStream_t s);
+// Every other layout.
 cudaError_t launch_attn_scalar(const AttnLaunch& p, gdn_dtype dtype, cudaStream_t s);
 
 }  // namespace gdn

@@ -35,7 +35,7 @@ int check_shape(const gdn_kv_cache* c) {
   if (c->num_kv_heads < 1 || c->num_kv_heads > 1024) return GDN_ERR_SHAPE;
   if (c->head_dim < 16 || c->head_dim > 256 || c->head_dim % 16) return GDN_ERR_SHAPE;
   const int64_t dense = (int64_t)c->num_kv_heads * c->page_size * c->head_dim;
-  if (c->page_stride != 0 && (c->page_stride < dense || c->page_stride > ((int64_t)1 << 40))) return GDN_ERR_SHAPE;
+  if (c->page_stride != 0 && (c->page_stride < dense || c->page_stride >= ((int64_t)1 << 38))) return GDN_ERR_SHAPE;
   if (c->page_stride * es_of(c->dtype) % 16) return GDN_ERR_ALIGN;
   return GDN_OK;
 }
@@ -164,7 +164,9 @@ int gdn_kv_append(const gdn_kv_cache* cache, const gdn_kv_rows* rows, const void
 
 size_t gdn_attention_workspace_bytes(const gdn_attn_desc* attn, const gdn_kv_cache* cache, const gdn_kv_rows* rows) {
   if (check_shape(cache) || check_table(cache) || check_attn(attn, cache) || check_kv_rows(rows)) return 0;
-  return 0;
+  if (rows->num_seqs == 0 || rows->max_query_len == 0) return 0;
+  const AttnLaunch p = attn_args(attn, cache, rows);
+  return attn_split_supported(p, cache->dtype) ? round256(attn_split_workspace(p)) : 0;
 }
 
 int gdn_paged_attention(const gdn_attn_desc* attn, const gdn_kv_cache* cache, const gdn_kv_rows* rows, const void* q,
@@ -194,6 +196,7 @@ int gdn_paged_attention(const gdn_attn_desc* attn, const gdn_kv_cache* cache, co
   p.num_global = num_global_tokens;
   p.ws = workspace;
   p.status = d_status;
+  if (attn_split_supported(p, cache->dtype)) return cuda_rc(launch_attn_split(p, (cudaStream_t)stream));
   return cuda_rc(launch_attn_scalar(p, cache->dtype, (cudaStream_t)stream));
 }
 
