@@ -11,13 +11,11 @@
 // the CTAs, so results do not depend on timing.
 //
 // A CTA: one warp fetches pages by TMA into a ring of stages (up to 192 KB in flight; a NULL page is
-// fetched from past the pool and reads as zeros), eight warps compute.  They work transposed,
-//   S^T = K Q^T  (tokens x queries),  O^T += V^T P^T  (d x queries),
-// so that the tokens fill the m = 16 side of mma.m16n8k16 and 8 queries cost 8 columns, not 16 rows.
-// Each warp takes 16 tokens of a tile and up to NQW queries with a running maximum and sum of its
-// own; the warps meet only where a unit ends.  The weights enter the second product as a bf16 pair
-// (hi + lo), so they keep 16 bits: the product is nearly free here, and one bf16 would cost as much
-// accuracy as the output's own rounding.
+// fetched from past the pool and reads as zeros) and the queries of the next unit; 4 or 8 warps
+// compute, each 32 tokens of a tile against 16 queries with mma.m16n8k16 and a running maximum and
+// sum of its own, and meet only where a unit ends.  The weights enter the second product as a bf16
+// pair (hi + lo), so they keep 16 bits: the product is nearly free here, and one bf16 would cost as
+// much accuracy as the output's own rounding.
 #include "gdn_tma.cuh"
 
 namespace gdn {
@@ -25,30 +23,31 @@ namespace gdn {
 namespace {
 
 constexpr int kSplitCtas = 152;  // one per SM
-constexpr uint32_t kSmemBytes = 229600;  // dynamic, behind the alignment: ring and merge buffer
+constexpr uint32_t kSmemBytes = 230400;  // dynamic, behind the alignment: ring, merge buffer, queries
 constexpr int kJoinWarps = 8;
 
-template <int D, int NQW, int WQ>
+// WQ groups of 16 queries x DS slices of the values' columns x KG groups of 32 tokens, a warp each.
+template <int D, int WQ, int DS, int KG>
 struct Cfg {
-  // 8 computing warps; 4 where two tiles at a time would leave the ring too short (d = 256, <= 8 queries)
-  static constexpr int kWarps = D == 256 && WQ == 1 ? 4 : 8;
+  static constexpr int kWarps = WQ * DS * KG;
   static constexpr int kThreads = 32 * (kWarps + 1);
-  static constexpr int kTN = WQ <= 2 ? 64 : WQ == 4 ? 32 : 16;      // tokens of a tile
-  static constexpr int kKT = kTN / 16;                              // 16-token steps of a tile
-  static constexpr int kKG = kWarps / WQ;                           // token groups of warps
-  static constexpr int kTG = kKG / kKT;                             // tiles worked on at a time
-  static constexpr int kNQ = NQW * WQ;                              // queries of a unit, at most
+  static constexpr int kTN = D == 256 ? 32 : 64;                    // tokens of a tile
+  static constexpr int kKT = kTN / 32;                              // 32-token steps of a tile
+  static constexpr int kTG = KG / kKT;                              // tiles worked on at a time
+  static constexpr int kNQ = 16 * WQ;                               // queries of a unit, at most
+  static constexpr int kDV = D / DS;                                // value columns of a warp
   static constexpr uint32_t kHalf = (uint32_t)kTN * D * 2;          // K (or V) bytes of a stage
-  static constexpr int kSlots = kWarps / 2 > WQ ? kWarps / 2 : WQ;  // of the merge buffer, a warp's output each
-  static constexpr uint32_t kMerge = (uint32_t)kSlots * NQW * D * 4;
-  static constexpr int kFit = (int)((kSmemBytes - kMerge) / (2 * kHalf));
+  static constexpr int kSP = D == 64 && KG > 1 ? KG / 2 : 1;        // token groups that merge at a time
+  static constexpr int kSlots = kSP * WQ * DS;                      // of the merge buffer, a warp's output each
+  static constexpr uint32_t kMerge = (uint32_t)kSlots * 16 * kDV * 4;
+  static constexpr uint32_t kPitch = D * 2 + 16;                    // bytes of a query: rows 16 bytes apart mod 128
+  static constexpr uint32_t kQ = kNQ * kPitch;                      // one of two buffers
+  static constexpr int kFit = (int)((kSmemBytes - kMerge - 2 * kQ) / (2 * kHalf));
   // A multiple of kTG: a stage is always worked on by the same warps, so none can miss a phase of its barrier.
   static constexpr int kStages = (kFit < 16 ? kFit : 16) / kTG * kTG;
-  static constexpr int kNT = NQW / 8;                               // n = 8 tiles of a warp
-  static constexpr int kMT = D / 16;
-  static_assert(kKT * kTG == kKG && kStages > kTG, "ring too short");
   static constexpr uint32_t kRing = (uint32_t)kStages * 2 * kHalf;
-  static_assert(kRing + kMerge <= kSmemBytes, "shared memory");
+  static_assert(kKT * kTG == KG && kStages > kTG, "ring too short");
+  static_assert(kRing + kMerge + 2 * kQ <= kSmemBytes && kRing % 1024 == 0, "shared memory");
 };
 
 struct SplitParams {
@@ -91,11 +90,6 @@ __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t a) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(a));
-}
-__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
-  uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-  return y;
 }
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -181,7 +175,8 @@ __device__ void find_share(const AttnLaunch& p, int ctas, int cta, Share& out) {
   out = s_share;
 }
 
-// Walks the units of a share: (row, head, tiles [j0, j0 + len) of the unit).
+// Walks the units of a share: (row, head, tiles [j0, j0 + len) of the unit).  A warp holds 32 rows,
+// one per lane, so that going on to the next row waits for no memory.  All lanes call together.
 template <int TN>
 struct Walk {
   const AttnLaunch& p;
@@ -190,7 +185,8 @@ struct Walk {
   Unit u;
   __device__ Walk(const AttnLaunch& launch, const Share& s) : p(launch), left(s.last - s.first), n(s.row), len(0) {
     if (left <= 0) return;
-    u = unit_of<TN>(p, n, nullptr);
+    fill();
+    pick();
     h = (int)(s.into / u.tiles);
     j0 = (int)(s.into - (int64_t)h * u.tiles);
     len = (int)min((int64_t)(u.tiles - j0), left);
@@ -207,35 +203,125 @@ struct Walk {
           left = 0;
           return;
         }
-        u = unit_of<TN>(p, n, nullptr);
+        if (n == base + 32) fill();
+        pick();
       } while (u.tiles == 0);
     }
     len = (int)min((int64_t)u.tiles, left);
   }
   __device__ int tile_at(int j) const { return (j < u.sink_tiles ? j : u.first_tile + j - u.sink_tiles) * TN; }
+
+ private:
+  int base;
+  Unit mine;
+  __device__ void fill() {
+    base = n;
+    mine.tiles = 0;
+    const int row = n + (threadIdx.x & 31);
+    if (row < p.rows.num_seqs) mine = unit_of<TN>(p, row, nullptr);
+  }
+  __device__ void pick() {
+    const int src = n - base;
+    u.r.bos = __shfl_sync(0xffffffffu, mine.r.bos, src);
+    u.r.len = __shfl_sync(0xffffffffu, mine.r.len, src);
+    u.r.kv = __shfl_sync(0xffffffffu, mine.r.kv, src);
+    u.r.trow = __shfl_sync(0xffffffffu, mine.r.trow, src);
+    u.sink_tiles = __shfl_sync(0xffffffffu, mine.sink_tiles, src);
+    u.first_tile = __shfl_sync(0xffffffffu, mine.first_tile, src);
+    u.tiles = __shfl_sync(0xffffffffu, mine.tiles, src);
+  }
 };
 
-template <int D, int NQW, int WQ>
-__global__ void __launch_bounds__(Cfg<D, NQW, WQ>::kThreads, 1)
+// One 32-token step's second product, O += P V.  PART: some query does not see some token, so the
+// values must not reach it whatever they hold.
+template <bool PART, int TN, int DV>
+__device__ __forceinline__ void values_step(float (&o)[DV / 8][4], const uint32_t (&ph)[2][4], const uint32_t (&pl)[2][4],
+                                            uint32_t vbase, int col0, int b, const int (&pos)[2], int pmax, int window,
+                                            int sinks) {
+  const int lane = threadIdx.x & 31, c2 = (lane & 3) * 2;
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    // lanes 0-7, 8-15, 16-23, 24-31 point at (tokens 0-7, left 8 columns), (8-15, left), (0-7, right),
+    // (8-15, right); the transposing load puts two tokens of a column into a register
+    const int r = (lane & 7) + (((lane >> 3) & 1) << 3);
+    const uint32_t base = vbase + (half * 16 + r) * 128;
+    const int t0 = b + half * 16;
+    uint32_t m0 = 0xffffffffu, m1 = 0xffffffffu;
+    if (PART) {  // tokens past the row's end hold anything
+      m0 = (t0 + c2 <= pmax ? 0xffffu : 0u) | (t0 + c2 + 1 <= pmax ? 0xffff0000u : 0u);
+      m1 = (t0 + c2 + 8 <= pmax ? 0xffffu : 0u) | (t0 + c2 + 9 <= pmax ? 0xffff0000u : 0u);
+    }
+#pragma unroll
+    for (int i = 0; i < DV / 16; ++i) {
+      const int chunk = col0 / 8 + i * 2 + (lane >> 4);
+      uint32_t v[4];
+      ldsm4t(v, base + (chunk >> 3) * TN * 128 + (((chunk & 7) ^ (r & 7)) << 4));
+      if (PART) {
+        v[0] &= m0;
+        v[1] &= m1;
+        v[2] &= m0;
+        v[3] &= m1;
+        const bool odd = not_finite2(v[0]) || not_finite2(v[1]) || not_finite2(v[2]) || not_finite2(v[3]);
+        if (__any_sync(0xffffffffu, odd)) {
+          // An infinity or NaN that some query of the step must not see (0 times it is NaN): one token
+          // at a time, added only where it is seen.
+#pragma unroll 1
+          for (int t = 0; t < 16; ++t) {
+            const uint32_t keep = ((t & 7) >> 1) == (lane & 3) ? ((t & 1) ? 0xffff0000u : 0xffffu) : 0u;
+            const uint32_t lo = t < 8 ? keep : 0u, hi = t < 8 ? 0u : keep;
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+              float x[4] = {0.f, 0.f, 0.f, 0.f};
+              mma16816(x, ph[half], v[2 * n] & lo, v[2 * n + 1] & hi);
+              mma16816(x, pl[half], v[2 * n] & lo, v[2 * n + 1] & hi);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int at = pos[e >> 1], tk = t0 + t;
+                if (tk <= at && (window <= 0 || tk > at - window || tk < sinks)) o[2 * i + n][e] += x[e];
+              }
+            }
+          }
+          continue;
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        mma16816(o[2 * i + n], ph[half], v[2 * n], v[2 * n + 1]);
+        mma16816(o[2 * i + n], pl[half], v[2 * n], v[2 * n + 1]);
+      }
+    }
+  }
+}
+
+template <int D, int WQ, int DS, int KG>
+__global__ void __launch_bounds__(Cfg<D, WQ, DS, KG>::kThreads, 1)
     split_kernel(SplitParams P, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
-  using C = Cfg<D, NQW, WQ>;
-  constexpr int TN = C::kTN, S = C::kStages, NT = C::kNT, MT = C::kMT;
+  using C = Cfg<D, WQ, DS, KG>;
+  constexpr int TN = C::kTN, S = C::kStages, DV = C::kDV;
   extern __shared__ uint8_t raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   float* merge = reinterpret_cast<float*>(ring + C::kRing);
-  __shared__ uint64_t full[S], empty[S];
-  __shared__ uint32_t held[S];                    // per stage: which of the tile's pages hold tokens
-  __shared__ float sm_m[C::kWarps][NQW], sm_l[C::kWarps][NQW];
+  uint8_t* qbuf = ring + C::kRing + C::kMerge;
+  __shared__ uint64_t full[S], empty[S], qfull[2], qempty[2];
+  __shared__ uint32_t held[S];  // per stage: which of the tile's pages hold tokens
+  __shared__ float sm_m[C::kSlots][16], sm_l[C::kSlots][16];
   __shared__ int dead;
   const AttnLaunch& p = P.a;
   const KvDev& kv = p.cache;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // The warp's number comes from a shuffle, so that the compiler takes it as one value of the warp and
+  // infers no range for it: with threadIdx.x / 32 nvcc 13.0 took the receiving groups' slots of the
+  // merge buffer below to lie outside it.
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (tid == 0) {
     for (int i = 0; i < S; ++i) {
       tc::mbar_init(&full[i], 1);
-      tc::mbar_init(&empty[i], C::kKT * WQ);
+      tc::mbar_init(&empty[i], C::kKT * WQ * DS);
+    }
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&qfull[i], 1);
+      tc::mbar_init(&qempty[i], C::kWarps);
     }
     tc::mbar_init_fence();
     dead = 0;
@@ -250,20 +336,60 @@ __global__ void __launch_bounds__(Cfg<D, NQW, WQ>::kThreads, 1)
   const int ps = kv.page_size;
   const int box = min(ps, TN);       // tokens of one copy
   const int boxes = TN / box;        // pages of a tile
+  const int shift = __ffs(ps) - 1;
 
   if (warp == C::kWarps) {
     // ---- the fetching warp: lane = (page of the tile, 64-column block, K or V) ----
     constexpr int CB = D / 64;
     const int bi = lane / (2 * CB), cb = (lane >> 1) % CB, is_v = lane & 1;
     const bool active = bi < boxes;
-    int it = 0;
+    int it = 0, seg = 0;
     bool ok = true;
-    for (Walk<TN> w(p, share); w.valid() && ok; w.next()) {
+    for (Walk<TN> w(p, share); w.valid() && ok; w.next(), ++seg) {
+      // the unit's queries
+      const int nq = w.u.r.len * p.G, qb = seg & 1;
+      int g[2];
+      int rows = 0;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int qi = lane + 32 * u;
+        g[u] = -1;
+        if (qi < nq) g[u] = global_token(RowsDev{nullptr, p.rows.tok}, w.u.r.bos + qi / p.G, p.num_global, p.status);
+        rows += __popc(__ballot_sync(0xffffffffu, g[u] >= 0));
+      }
+      ok = seg < 2 || tc::mbar_wait(&qempty[qb], ((seg >> 1) - 1) & 1, P.wait_ns);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      if (lane == 0) tc::expect_tx(&qfull[qb], (uint32_t)rows * D * 2);
+      __syncwarp();
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int qi = lane + 32 * u;
+        if (g[u] >= 0)
+          tc::bulk_g2s(qbuf + qb * C::kQ + qi * C::kPitch,
+                       static_cast<const __nv_bfloat16*>(p.q) + (int64_t)g[u] * p.q_stride +
+                           (int64_t)(w.h * p.G + qi % p.G) * D,
+                       D * 2, &qfull[qb]);
+      }
+      // 32 table entries are held, one per lane, and the 32 behind them are on their way
       const int32_t* row = kv.table + (int64_t)w.u.r.trow * kv.max_pages;
+      const int entries = (w.u.r.kv + ps - 1) >> shift;
+      int eb = -64, ids = 0, ahead = 0;
       for (int j = w.j0; j < w.j0 + w.len; ++j, ++it) {
         const int pos = w.tile_at(j) + bi * box;
-        int page = 0;
-        if (active && pos < w.u.r.kv) page = page_or_null(__ldg(row + pos / ps), kv, p.status);
+        const int e = w.tile_at(j) >> shift;
+        if (e >= eb + 32) {
+          if (e < eb + 64) {
+            ids = ahead;
+            eb += 32;
+          } else {
+            eb = e;
+            ids = eb + lane < entries ? __ldg(row + eb + lane) : 0;
+          }
+          ahead = eb + 32 + lane < entries ? __ldg(row + eb + 32 + lane) : 0;
+        }
+        int page = __shfl_sync(0xffffffffu, ids, active ? (pos >> shift) - eb : 0);
+        page = active && pos < w.u.r.kv ? page_or_null(page, kv, p.status) : 0;
         const int s = it % S;
         ok = it < S || tc::mbar_wait(&empty[s], ((it / S) - 1) & 1, P.wait_ns);
         ok = __all_sync(0xffffffffu, ok);
@@ -278,13 +404,15 @@ __global__ void __launch_bounds__(Cfg<D, NQW, WQ>::kThreads, 1)
         __syncwarp();
         if (active) {
           uint8_t* dst = ring + (size_t)s * 2 * C::kHalf + is_v * C::kHalf + (size_t)(cb * TN + bi * box) * 128;
-          tc::tma_page(dst, is_v ? &vmap : &kmap, cb * 64, pos % ps, w.h, page > 0 ? page : kv.num_pages, &full[s]);
+          tc::tma_page(dst, is_v ? &vmap : &kmap, cb * 64, pos & (ps - 1), w.h, page > 0 ? page : kv.num_pages,
+                       &full[s]);
         }
       }
     }
     // No copy may be in flight when the CTA ends.  Computing warps wait for every stage they use, so
     // this passes at once unless a wait gave up.
     for (int i = max(0, it - S); i < it; ++i) ok &= tc::mbar_wait(&full[i % S], (i / S) & 1, P.wait_ns);
+    for (int i = max(0, seg - 2); i < seg; ++i) ok &= tc::mbar_wait(&qfull[i & 1], (i >> 1) & 1, P.wait_ns);
     if (!ok && lane == 0) {
       dead = 1;
       set_status(p.status, GDN_STATUS_WAIT_TIMEOUT);
@@ -293,300 +421,231 @@ __global__ void __launch_bounds__(Cfg<D, NQW, WQ>::kThreads, 1)
   }
 
   // ---- computing warps ----
-  const int wq = warp % WQ, kg = warp / WQ;   // query group, token group
+  const int ds = warp % DS, wq = (warp / DS) % WQ, kg = warp / (DS * WQ);
   const int kt = kg % C::kKT, tg = kg / C::kKT;
   const int r8 = lane >> 2, c2 = (lane & 3) * 2;
+  const int bshift = __ffs(box) - 1;
   const float sl2 = p.scale * 1.4426950408889634f;
-  int it = 0;
+  int it = 0, seg = 0;
   bool ok = true;
-  for (Walk<TN> w(p, share); w.valid(); w.next()) {
+  for (Walk<TN> w(p, share); w.valid(); w.next(), ++seg) {
     const KvRow row = w.u.r;
     const int nq = row.len * p.G;
     const int pmin = row.kv - row.len, pmax = row.kv - 1;
-    // Q^T as the B operand: query lane / 4, two neighbouring k per register
-    uint32_t qf[NT][MT][2];
+    float o[DV / 8][4], m[2], l[2];
+    int pos[2];  // the positions of this thread's two queries, r8 and r8 + 8 of the group's 16
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int qi = wq * NQW + nt * 8 + r8;
-      int g = -1;
-      if (qi < nq) {
-        const int t = qi / p.G;
-        g = global_token(RowsDev{nullptr, p.rows.tok}, row.bos + t, p.num_global, p.status);
-      }
-      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + (int64_t)max(g, 0) * p.q_stride +
-                               (int64_t)(w.h * p.G + qi % p.G) * D + c2;
+    for (int i = 0; i < DV / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
 #pragma unroll
-      for (int k = 0; k < MT; ++k) {
-        qf[nt][k][0] = g >= 0 ? __ldg(reinterpret_cast<const uint32_t*>(q + k * 16)) : 0u;
-        qf[nt][k][1] = g >= 0 ? __ldg(reinterpret_cast<const uint32_t*>(q + k * 16 + 8)) : 0u;
-      }
+    for (int e = 0; e < 2; ++e) {
+      m[e] = -INFINITY;
+      l[e] = 0.f;
+      pos[e] = min(pmin + (wq * 16 + r8 + 8 * e) / p.G, pmax);
     }
-    float o[NT][MT][4], m[NT][2], l[NT][2];
-    int pos_q[NT][2];  // the positions of this thread's query columns
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-      for (int i = 0; i < MT; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
-      m[nt][0] = m[nt][1] = -INFINITY;
-      l[nt][0] = l[nt][1] = 0.f;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) pos_q[nt][e] = min(pmin + (wq * NQW + nt * 8 + c2 + e) / p.G, pmax);
-    }
+    ok = __all_sync(0xffffffffu, ok && tc::mbar_wait(&qfull[seg & 1], (seg >> 1) & 1, P.wait_ns));
+    const uint32_t qbase =
+        tc::smem_addr(qbuf + (seg & 1) * C::kQ) + (wq * 16 + (lane & 15)) * C::kPitch + (lane >> 4) * 16;
 
     for (int j = w.j0; j < w.j0 + w.len; ++j, ++it) {
       if (C::kTG > 1 && it % C::kTG != tg) continue;
       const int s = it % S;
       ok = __all_sync(0xffffffffu, ok && tc::mbar_wait(&full[s], (it / S) & 1, P.wait_ns));
-      const int b = w.tile_at(j) + kt * 16;  // first token of this warp's step
-      const bool some = ok && b <= pmax && (held[s] >> (kt * 16 / box) & 1u);
-      if (some) {
-        const uint32_t kbase = tc::smem_addr(ring + (size_t)s * 2 * C::kHalf) + kt * 16 * 128;
+      const int b = w.tile_at(j) + kt * 32;  // first token of this warp's step
+      // a page is 16 tokens or more: the step's two halves may differ in whether theirs is NULL
+      const uint32_t hm = held[s];
+      const bool have0 = hm >> (kt * 32 >> bshift) & 1u, have1 = hm >> ((kt * 32 + 16) >> bshift) & 1u;
+      if (ok && b <= pmax && (have0 || have1)) {
+        const uint32_t kbase = tc::smem_addr(ring + (size_t)s * 2 * C::kHalf) + kt * 32 * 128;
         const uint32_t vbase = kbase + C::kHalf;
-        // S^T: lanes 0-15 point at rows 0-15 of the left 8 columns, lanes 16-31 of the right 8
-        float sc[NT][4];
+        // S = Q K^T.  K as the B operand: lanes 0-7, 8-15, 16-23, 24-31 point at (tokens 0-7, left 8
+        // columns), (0-7, right), (8-15, left), (8-15, right) of 16 tokens.
+        float sc[4][4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
+        for (int n = 0; n < 4; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.f;
         {
-          const int r = lane & 15;
+          const int r = (lane & 7) + ((lane >> 4) << 3);
           const uint32_t base = kbase + r * 128;
 #pragma unroll
-          for (int k = 0; k < MT; ++k) {
-            uint32_t a[4];
-            ldsm4(a, base + (k >> 2) * TN * 128 + ((((k & 3) * 2 + (lane >> 4)) ^ (r & 7)) << 4));
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma16816(sc[nt], a, qf[nt][k][0], qf[nt][k][1]);
+          for (int k = 0; k < D / 16; ++k) {
+            uint32_t a[4], k0[4], k1[4];
+            const uint32_t at =
+                base + (k >> 2) * TN * 128 + ((((k & 3) * 2 + ((lane >> 3) & 1)) ^ (r & 7)) << 4);
+            ldsm4(a, qbase + k * 32);
+            ldsm4(k0, at);
+            ldsm4(k1, at + 16 * 128);
+            mma16816(sc[0], a, k0[0], k0[1]);
+            mma16816(sc[1], a, k0[2], k0[3]);
+            mma16816(sc[2], a, k1[0], k1[1]);
+            mma16816(sc[3], a, k1[2], k1[3]);
           }
         }
-        // which of the step's tokens a query sees; `part`: not every query sees every token
-        const bool part = b + 15 > pmin || (p.window > 0 && b <= pmax - p.window && b + 15 >= p.sinks);
-        uint32_t vmask0 = 0xffffffffu, vmask1 = 0xffffffffu;
-        bool vis[NT][4];
+        // not every query sees every token?
+        const bool part = b + 31 > pmin || !have0 || !have1 ||
+                          (p.window > 0 && b <= pmax - p.window && b + 31 >= p.sinks);
+        if (part) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
+          for (int n = 0; n < 4; ++n)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float x = sc[nt][e] * sl2;
-            vis[nt][e] = true;
-            if (part) {
-              const int tok = b + r8 + (e >> 1) * 8, at = pos_q[nt][e & 1];
-              vis[nt][e] = tok <= at && (p.window <= 0 || tok > at - p.window || tok < p.sinks);
-              if (!vis[nt][e]) x = -INFINITY;
+            for (int e = 0; e < 4; ++e) {
+              const int tok = b + n * 8 + c2 + (e & 1), at = pos[e >> 1];
+              const bool sees = tok <= at && (p.window <= 0 || tok > at - p.window || tok < p.sinks) &&
+                                (n < 2 ? have0 : have1);
+              if (!sees) sc[n][e] = -INFINITY;
             }
-            sc[nt][e] = x;
-          }
         }
-        float mx[NT][2];
-        bool grew = false;
+        // running maximum (of the raw scores; scale > 0), sum and output
+        float mx[2];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int e = 0; e < 2; ++e) {
+          float x = m[e];
+#pragma unroll
+          for (int n = 0; n < 4; ++n) x = fmaxf(x, fmaxf(sc[n][2 * e], sc[n][2 * e + 1]));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+          mx[e] = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+        }
+        if (__any_sync(0xffffffffu, mx[0] > m[0] || mx[1] > m[1])) {
+          float f[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float x = fmaxf(sc[nt][e], sc[nt][e + 2]);
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-            mx[nt][e] = fmaxf(m[nt][e], x);
-            grew |= mx[nt][e] > m[nt][e];
+            f[e] = m[e] == -INFINITY ? 0.f : ex2((m[e] - mx[e]) * sl2);
+            m[e] = mx[e];
+            l[e] *= f[e];
           }
-        if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            float a[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              a[e] = m[nt][e] == -INFINITY ? 0.f : ex2(m[nt][e] - mx[nt][e]);
-              m[nt][e] = mx[nt][e];
-              l[nt][e] *= a[e];
-            }
-#pragma unroll
-            for (int i = 0; i < MT; ++i) {
-              o[nt][i][0] *= a[0];
-              o[nt][i][1] *= a[1];
-              o[nt][i][2] *= a[0];
-              o[nt][i][3] *= a[1];
-            }
+          for (int i = 0; i < DV / 8; ++i) {
+            o[i][0] *= f[0];
+            o[i][1] *= f[0];
+            o[i][2] *= f[1];
+            o[i][3] *= f[1];
           }
         }
-        // P^T as the B operand: transposed 8 x 8 blocks of the score fragments, as hi + lo
-        uint32_t ph[NT][2], pl[NT][2];
+        // P as the A operand: the score fragments are already in its layout
+        uint32_t ph[2][4], pl[2][4];
+        float ms[2];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
+        for (int e = 0; e < 2; ++e) ms[e] = m[e] == -INFINITY ? 0.f : -m[e] * sl2;
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
           float e4[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float mm = m[nt][e & 1];
-            e4[e] = ex2(sc[nt][e] - (mm == -INFINITY ? 0.f : mm));
-          }
-          l[nt][0] += e4[0] + e4[2];
-          l[nt][1] += e4[1] + e4[3];
+          for (int e = 0; e < 4; ++e) e4[e] = ex2(fmaf(sc[n][e], sl2, ms[e >> 1]));
+          l[0] += e4[0] + e4[1];
+          l[1] += e4[2] + e4[3];
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
             const uint32_t hi = pack2(e4[2 * hf], e4[2 * hf + 1]);
-            const uint32_t lo = pack2(e4[2 * hf] - bf_lo(hi), e4[2 * hf + 1] - bf_hi(hi));
-            ph[nt][hf] = transpose8(hi);
-            pl[nt][hf] = transpose8(lo);
+            ph[n >> 1][(n & 1) * 2 + hf] = hi;
+            pl[n >> 1][(n & 1) * 2 + hf] = pack2(e4[2 * hf] - bf_lo(hi), e4[2 * hf + 1] - bf_hi(hi));
           }
         }
-        if (part) {
-          // tokens past the row's end hold anything: their values do not enter the products
-          const int tok = b + c2;
-          vmask0 = (tok <= pmax ? 0xffffu : 0u) | (tok + 1 <= pmax ? 0xffff0000u : 0u);
-          vmask1 = (tok + 8 <= pmax ? 0xffffu : 0u) | (tok + 9 <= pmax ? 0xffff0000u : 0u);
-        }
-        // O^T += V^T P^T: lanes 0-7, 8-15, 16-23, 24-31 point at (tokens 0-7, left 8 columns),
-        // (0-7, right), (8-15, left), (8-15, right); the transposing load makes d the row
-        const int r = (lane & 7) + ((lane >> 4) << 3);
-        const uint32_t base = vbase + r * 128;
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-          uint32_t a[4];
-          ldsm4t(a, base + (i >> 2) * TN * 128 + ((((i & 3) * 2 + ((lane >> 3) & 1)) ^ (r & 7)) << 4));
-          if (part) {
-            a[0] &= vmask0;
-            a[1] &= vmask0;
-            a[2] &= vmask1;
-            a[3] &= vmask1;
-            const bool odd = not_finite2(a[0]) || not_finite2(a[1]) || not_finite2(a[2]) || not_finite2(a[3]);
-            if (__any_sync(0xffffffffu, odd)) {
-              // An infinity or NaN that some query of the step must not see (0 times it is NaN): one
-              // token at a time, added only where it is seen.
-#pragma unroll 1
-              for (int t = 0; t < 16; ++t) {
-                const uint32_t half = (t & 1) ? 0xffff0000u : 0xffffu;
-                const uint32_t keep = ((t & 7) >> 1) == (lane & 3) ? half : 0u;
-                uint32_t one[4];
-                one[0] = t < 8 ? a[0] & keep : 0u;
-                one[1] = t < 8 ? a[1] & keep : 0u;
-                one[2] = t < 8 ? 0u : a[2] & keep;
-                one[3] = t < 8 ? 0u : a[3] & keep;
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                  float x[4] = {0.f, 0.f, 0.f, 0.f};
-                  mma16816(x, one, ph[nt][0], ph[nt][1]);
-                  mma16816(x, one, pl[nt][0], pl[nt][1]);
-#pragma unroll
-                  for (int e = 0; e < 4; ++e) {
-                    const int at = pos_q[nt][e & 1], tk = b + t;
-                    if (tk <= at && (p.window <= 0 || tk > at - p.window || tk < p.sinks)) o[nt][i][e] += x[e];
-                  }
-                }
-              }
-              continue;
-            }
-          }
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            mma16816(o[nt][i], a, ph[nt][0], ph[nt][1]);
-            mma16816(o[nt][i], a, pl[nt][0], pl[nt][1]);
-          }
-        }
+        if (part)
+          values_step<true, TN, DV>(o, ph, pl, vbase, ds * DV, b, pos, pmax, p.window, p.sinks);
+        else
+          values_step<false, TN, DV>(o, ph, pl, vbase, ds * DV, b, pos, pmax, p.window, p.sinks);
       }
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&empty[s]);
     }
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(&qempty[seg & 1]);
 
-    // ---- the unit's piece ends: join the warps of a query group, token groups pairwise ----
+    // ---- the unit's piece ends: join the warps of a query group and column slice ----
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], 4);
-        l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], 8);
-        l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], 16);
-      }
+    for (int e = 0; e < 2; ++e) {
+      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
+      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+    }
     if (!ok && lane == 0) {
       dead = 1;
       set_status(p.status, GDN_STATUS_WAIT_TIMEOUT);
     }
-#pragma unroll
-    for (int step = C::kKG / 2; step >= 1; step >>= 1) {
+    // token groups hand theirs down, kSP of them at a time, through the merge buffer: the upper ones
+    // give, the ones just below them receive, until group 0 holds all
+#pragma unroll 1
+    for (int live = KG; live > 1;) {
+      const int take = min(live >> 1, C::kSP);
+      const int gives = kg - (live - take), receives = gives + take;
       compute_bar<C::kWarps>();
-      if (kg >= step && kg < 2 * step) {
-        const int slot = (kg - step) * WQ + wq;
-        float4* b4 = reinterpret_cast<float4*>(merge) + (size_t)slot * NT * MT * 32 + lane;
+      if (gives >= 0 && gives < take) {
+        const int slot = (gives * WQ + wq) * DS + ds;
+        float4* b4 = reinterpret_cast<float4*>(merge) + slot * (DV / 8) * 32 + lane;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int i = 0; i < MT; ++i)
-            b4[(nt * MT + i) * 32] = make_float4(o[nt][i][0], o[nt][i][1], o[nt][i][2], o[nt][i][3]);
-        if (lane < 4)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              sm_m[slot][nt * 8 + c2 + e] = m[nt][e];
-              sm_l[slot][nt * 8 + c2 + e] = l[nt][e];
-            }
-      }
-      compute_bar<C::kWarps>();
-      if (kg < step) {
-        const int slot = kg * WQ + wq;
-        const float4* b4 = reinterpret_cast<const float4*>(merge) + (size_t)slot * NT * MT * 32 + lane;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float a[2], c[2];
+        for (int i = 0; i < DV / 8; ++i) b4[i * 32] = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
+        if ((lane & 3) == 0)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float m2 = sm_m[slot][nt * 8 + c2 + e], mn = fmaxf(m[nt][e], m2);
-            a[e] = m[nt][e] == -INFINITY ? 0.f : ex2(m[nt][e] - mn);
-            c[e] = m2 == -INFINITY ? 0.f : ex2(m2 - mn);
-            l[nt][e] = l[nt][e] * a[e] + sm_l[slot][nt * 8 + c2 + e] * c[e];
-            m[nt][e] = mn;
+            sm_m[slot][r8 + 8 * e] = m[e];
+            sm_l[slot][r8 + 8 * e] = l[e];
           }
+      }
+      compute_bar<C::kWarps>();
+      if (receives >= 0 && receives < take) {
+        const int slot = (receives * WQ + wq) * DS + ds;
+        const float4* b4 = reinterpret_cast<const float4*>(merge) + slot * (DV / 8) * 32 + lane;
+        float f[2], g[2];
 #pragma unroll
-          for (int i = 0; i < MT; ++i) {
-            const float4 v = b4[(nt * MT + i) * 32];
-            o[nt][i][0] = o[nt][i][0] * a[0] + v.x * c[0];
-            o[nt][i][1] = o[nt][i][1] * a[1] + v.y * c[1];
-            o[nt][i][2] = o[nt][i][2] * a[0] + v.z * c[0];
-            o[nt][i][3] = o[nt][i][3] * a[1] + v.w * c[1];
-          }
+        for (int e = 0; e < 2; ++e) {
+          const float m2 = sm_m[slot][r8 + 8 * e], mn = fmaxf(m[e], m2);
+          f[e] = m[e] == -INFINITY ? 0.f : ex2((m[e] - mn) * sl2);
+          g[e] = m2 == -INFINITY ? 0.f : ex2((m2 - mn) * sl2);
+          l[e] = l[e] * f[e] + sm_l[slot][r8 + 8 * e] * g[e];
+          m[e] = mn;
+        }
+#pragma unroll
+        for (int i = 0; i < DV / 8; ++i) {
+          const float4 v = b4[i * 32];
+          o[i][0] = o[i][0] * f[0] + v.x * g[0];
+          o[i][1] = o[i][1] * f[0] + v.y * g[0];
+          o[i][2] = o[i][2] * f[1] + v.z * g[1];
+          o[i][3] = o[i][3] * f[1] + v.w * g[1];
         }
       }
+      live -= take;
     }
     compute_bar<C::kWarps>();
     if (kg == 0 && !*(volatile int*)&dead) {
       const bool whole = w.j0 == 0 && w.len == w.u.tiles;
       // rows of queries in shared memory, then 16-byte stores
-      float* mine = merge + (size_t)wq * NQW * D;
+      float* mine = merge + (size_t)(wq * DS + ds) * 16 * DV;
+      float f[2];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float f[2];
+      for (int e = 0; e < 2; ++e) f[e] = !whole ? 1.f : l[e] == 0.f ? 0.f : 1.f / l[e];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) f[e] = !whole ? 1.f : l[nt][e] == 0.f ? 0.f : 1.f / l[nt][e];
+      for (int i = 0; i < DV / 8; ++i)
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            mine[(nt * 8 + c2 + (e & 1)) * D + i * 16 + r8 + (e >> 1) * 8] = o[nt][i][e] * f[e & 1];
-      }
+        for (int e = 0; e < 2; ++e)
+          *reinterpret_cast<float2*>(mine + (r8 + 8 * e) * DV + i * 8 + c2) =
+              make_float2(o[i][2 * e] * f[e], o[i][2 * e + 1] * f[e]);
       __syncwarp();
       if (whole) {
 #pragma unroll 1
-        for (int v = lane; v < NQW * D / 8; v += 32) {
-          const int q = v / (D / 8), d0 = (v % (D / 8)) * 8, qi = wq * NQW + q;
+        for (int v = lane; v < 16 * DV / 8; v += 32) {
+          const int q = v / (DV / 8), d0 = (v % (DV / 8)) * 8, qi = wq * 16 + q;
           if (qi >= nq) continue;
           const int t = qi / p.G;
           const int g = p.rows.tok ? __ldg(p.rows.tok + row.bos + t) : row.bos + t;
           if (g < 0 || g >= p.num_global) continue;
           *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + (int64_t)g * p.out_stride +
-                                    (int64_t)(w.h * p.G + qi - t * p.G) * D + d0) = tc::pack8(mine + q * D + d0);
+                                    (int64_t)(w.h * p.G + qi - t * p.G) * D + ds * DV + d0) =
+              tc::pack8(mine + q * DV + d0);
         }
       } else {
         const int slot = 2 * blockIdx.x + (w.j0 == 0 ? 1 : 0);
-        float4* dst = reinterpret_cast<float4*>(P.part + ((size_t)slot * C::kNQ + wq * NQW) * D);
 #pragma unroll 1
-        for (int v = lane; v < NQW * D / 4; v += 32) dst[v] = reinterpret_cast<const float4*>(mine)[v];
-        if (lane < 4)
+        for (int v = lane; v < 16 * DV / 4; v += 32) {
+          const int q = v / (DV / 4), d0 = (v % (DV / 4)) * 4;
+          if (wq * 16 + q < nq)
+            *reinterpret_cast<float4*>(P.part + ((size_t)slot * C::kNQ + wq * 16 + q) * D + ds * DV + d0) =
+                *reinterpret_cast<const float4*>(mine + q * DV + d0);
+        }
+        if (ds == 0 && (lane & 3) == 0)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float* st = P.stats + ((size_t)slot * C::kNQ + wq * NQW + nt * 8 + c2 + e) * 2;
-              st[0] = m[nt][e];
-              st[1] = l[nt][e];
-            }
-        if (w.j0 == 0 && wq == 0 && lane == 0) {
+          for (int e = 0; e < 2; ++e) {
+            float* st = P.stats + ((size_t)slot * C::kNQ + wq * 16 + r8 + 8 * e) * 2;
+            st[0] = m[e];
+            st[1] = l[e];
+          }
+        if (w.j0 == 0 && tid == 0) {
           // the CTA that holds the unit's last tile
           const int64_t used = min((int64_t)kSplitCtas, share.total);
           const int64_t end = share.last - w.left + w.u.tiles - 1;
@@ -606,6 +665,7 @@ __global__ void __launch_bounds__(Cfg<D, NQW, WQ>::kThreads, 1)
 // query, its warps over the pieces.
 template <int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(SplitParams P, int queries) {
+  const float sl2 = P.a.scale * 1.4426950408889634f;
   __shared__ float so[kJoinWarps][D];
   __shared__ float sl[kJoinWarps], sm[kJoinWarps];
   const AttnLaunch& p = P.a;
@@ -625,7 +685,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(SplitParams P, in
 #pragma unroll
     for (int i = 0; i < E; ++i) v[i] = P.part[at * D + lane + 32 * i];
     const float mn = fmaxf(m, m2);
-    const float a = m == -INFINITY ? 0.f : ex2(m - mn), b = m2 == -INFINITY ? 0.f : ex2(m2 - mn);
+    const float a = m == -INFINITY ? 0.f : ex2((m - mn) * sl2), b = m2 == -INFINITY ? 0.f : ex2((m2 - mn) * sl2);
     l = l * a + l2 * b;
 #pragma unroll
     for (int i = 0; i < E; ++i) o[i] = o[i] * a + v[i] * b;
@@ -644,7 +704,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(SplitParams P, in
   float L = 0.f, f[kJoinWarps];
 #pragma unroll
   for (int i = 0; i < kJoinWarps; ++i) {
-    f[i] = sm[i] == -INFINITY ? 0.f : ex2(sm[i] - M);
+    f[i] = sm[i] == -INFINITY ? 0.f : ex2((sm[i] - M) * sl2);
     L += sl[i] * f[i];
   }
   const float inv = L == 0.f ? 0.f : 1.f / L;
@@ -660,13 +720,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(SplitParams P, in
   }
 }
 
-template <int D, int NQW, int WQ>
+template <int D, int WQ, int DS, int KG>
 cudaError_t launch_cfg(const AttnLaunch& a, cudaStream_t s) {
-  using C = Cfg<D, NQW, WQ>;
+  using C = Cfg<D, WQ, DS, KG>;
   static std::atomic<uint64_t> done{0};
-  const int smem = (int)(C::kRing + C::kMerge + 1024);
+  const int smem = (int)(C::kRing + C::kMerge + 2 * C::kQ + 1024);
   cudaError_t e = once_per_device(done, [&] {
-    return cudaFuncSetAttribute(split_kernel<D, NQW, WQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    return cudaFuncSetAttribute(split_kernel<D, WQ, DS, KG>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   });
   if (e != cudaSuccess) return e;
   CUtensorMap kmap, vmap;
@@ -678,7 +738,7 @@ cudaError_t launch_cfg(const AttnLaunch& a, cudaStream_t s) {
   P.stats = reinterpret_cast<float*>(P.info + 8 * kSplitCtas);
   P.part = P.stats + (size_t)4 * kSplitCtas * C::kNQ;
   P.wait_ns = kDefaultWaitNs;
-  split_kernel<D, NQW, WQ><<<kSplitCtas, C::kThreads, smem, s>>>(P, kmap, vmap);
+  split_kernel<D, WQ, DS, KG><<<kSplitCtas, C::kThreads, smem, s>>>(P, kmap, vmap);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(kSplitCtas, a.rows.max_q * a.G);
@@ -692,7 +752,7 @@ cudaError_t launch_cfg(const AttnLaunch& a, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, join_kernel<D>, P, (int)C::kNQ);
 }
 
-int query_slots(int64_t queries) { return queries <= 8 ? 8 : queries <= 16 ? 16 : queries <= 32 ? 32 : 64; }
+int query_slots(int64_t queries) { return queries <= 16 ? 16 : queries <= 32 ? 32 : 64; }
 
 }  // namespace
 
@@ -707,21 +767,17 @@ size_t attn_split_workspace(const AttnLaunch& a) {
 }
 
 cudaError_t launch_attn_split(const AttnLaunch& a, cudaStream_t s) {
-  const int q = query_slots((int64_t)a.rows.max_q * a.G);
-  // 16 queries per warp where their accumulators fit the registers (d <= 128), else 8
-  switch (a.cache.d * 128 + q) {
-    case 64 * 128 + 8: return launch_cfg<64, 8, 1>(a, s);
-    case 64 * 128 + 16: return launch_cfg<64, 16, 1>(a, s);
-    case 64 * 128 + 32: return launch_cfg<64, 16, 2>(a, s);
-    case 64 * 128 + 64: return launch_cfg<64, 16, 4>(a, s);
-    case 128 * 128 + 8: return launch_cfg<128, 8, 1>(a, s);
-    case 128 * 128 + 16: return launch_cfg<128, 16, 1>(a, s);
-    case 128 * 128 + 32: return launch_cfg<128, 16, 2>(a, s);
-    case 128 * 128 + 64: return launch_cfg<128, 16, 4>(a, s);
-    case 256 * 128 + 8: return launch_cfg<256, 8, 1>(a, s);
-    case 256 * 128 + 16: return launch_cfg<256, 8, 2>(a, s);
-    case 256 * 128 + 32: return launch_cfg<256, 8, 4>(a, s);
-    case 256 * 128 + 64: return launch_cfg<256, 8, 8>(a, s);
+  // d = 256: two warps share a query group's output columns (16 x 256 accumulators do not fit one)
+  switch (a.cache.d + query_slots((int64_t)a.rows.max_q * a.G)) {
+    case 64 + 16: return launch_cfg<64, 1, 1, 8>(a, s);
+    case 64 + 32: return launch_cfg<64, 2, 1, 4>(a, s);
+    case 64 + 64: return launch_cfg<64, 4, 1, 2>(a, s);
+    case 128 + 16: return launch_cfg<128, 1, 1, 4>(a, s);
+    case 128 + 32: return launch_cfg<128, 2, 1, 4>(a, s);
+    case 128 + 64: return launch_cfg<128, 4, 1, 2>(a, s);
+    case 256 + 16: return launch_cfg<256, 1, 2, 2>(a, s);
+    case 256 + 32: return launch_cfg<256, 2, 2, 2>(a, s);
+    case 256 + 64: return launch_cfg<256, 4, 2, 1>(a, s);
     default: return cudaErrorInvalidValue;
   }
 }
