@@ -4,57 +4,53 @@
 // the cache bound the kernel: 4 flops per query per element against 2 bytes, far under the tensor
 // cores' ratio.  What matters is that every SM streams its share of the cache without a pause.
 //
-// Work.  A unit is one (row, kv-head): the TN-token tiles that its queries see, window and first
-// tokens included.  All units' tiles laid end to end are cut into equal shares, one per CTA, so
-// ragged lengths and a single long row load the SMs alike.  A share's piece of a unit that is not the
-// whole unit leaves (m, l, o) in the workspace; the join kernel adds a unit's pieces in the order of
-// the CTAs, so results do not depend on timing.
+// Work.  A unit is one (row, kv-head): the 32-token tiles that its queries see, window and first
+// tokens included.  All units' tiles laid end to end are dealt out evenly, so ragged lengths and a
+// single long row load the SMs alike.  A share's piece of a unit that is not the whole unit leaves
+// (m, l, o) in the workspace; the join kernel adds a unit's pieces in the order of the CTAs, so
+// results do not depend on timing.
 //
-// A CTA: one warp fetches pages by TMA into a ring of stages (up to 192 KB in flight; a NULL page is
-// fetched from past the pool and reads as zeros) and the queries of the next unit; 4 or 8 warps
-// compute, each 32 tokens of a tile against 16 queries with mma.m16n8k16 and a running maximum and
-// sum of its own, and meet only where a unit ends.  The weights enter the second product as a bf16
-// pair (hi + lo), so they keep 16 bits: the product is nearly free here, and one bf16 would cost as
-// much accuracy as the output's own rounding.
+// A CTA is small: one warp fetches pages by TMA into a short ring of stages (a NULL page is fetched
+// from past the pool and reads as zeros) and the queries of the next unit; one warp per 16 queries
+// computes, 32 tokens a step, with mma.m16n8k16 and a running maximum and sum of its own.  No warp
+// waits for another, and the 2 to 6 CTAs of an SM cover one another's starts and ends of units
+// (with 8 warps sharing a tile and meeting at every unit's end a 64 x 4-token verify batch took
+// 159 us).  The weights enter the second product as a bf16 pair (hi + lo), so they keep 16 bits: the
+// product is nearly free here, and one bf16 would cost as much accuracy as the output's own rounding.
 #include "gdn_tma.cuh"
 
 namespace gdn {
 
 namespace {
 
-constexpr int kSplitCtas = 152;  // one per SM
-constexpr uint32_t kSmemBytes = 230400;  // dynamic, behind the alignment: ring, merge buffer, queries
+constexpr int kSms = 152;
+constexpr int kTN = 32;       // tokens of a tile
 constexpr int kJoinWarps = 8;
 
-// WQ groups of 16 queries x DS slices of the values' columns x KG groups of 32 tokens, a warp each.
-template <int D, int WQ, int DS, int KG>
+// WQ groups of 16 queries x DS slices of the values' columns, a warp each; OCC CTAs per SM; QB buffers
+// for queries.
+template <int D, int WQ, int DS, int OCC, int QB>
 struct Cfg {
-  static constexpr int kWarps = WQ * DS * KG;
+  static constexpr int kWarps = WQ * DS;
   static constexpr int kThreads = 32 * (kWarps + 1);
-  static constexpr int kTN = D == 256 ? 32 : 64;                    // tokens of a tile
-  static constexpr int kKT = kTN / 32;                              // 32-token steps of a tile
-  static constexpr int kTG = KG / kKT;                              // tiles worked on at a time
+  static constexpr int kCtas = kSms * OCC;
   static constexpr int kNQ = 16 * WQ;                               // queries of a unit, at most
   static constexpr int kDV = D / DS;                                // value columns of a warp
   static constexpr uint32_t kHalf = (uint32_t)kTN * D * 2;          // K (or V) bytes of a stage
-  static constexpr int kSP = D == 64 && KG > 1 ? KG / 2 : 1;        // token groups that merge at a time
-  static constexpr int kSlots = kSP * WQ * DS;                      // of the merge buffer, a warp's output each
-  static constexpr uint32_t kMerge = (uint32_t)kSlots * 16 * kDV * 4;
   static constexpr uint32_t kPitch = D * 2 + 16;                    // bytes of a query: rows 16 bytes apart mod 128
-  static constexpr uint32_t kQ = kNQ * kPitch;                      // one of two buffers
-  static constexpr int kFit = (int)((kSmemBytes - kMerge - 2 * kQ) / (2 * kHalf));
-  // A multiple of kTG: a stage is always worked on by the same warps, so none can miss a phase of its barrier.
-  static constexpr int kStages = (kFit < 16 ? kFit : 16) / kTG * kTG;
+  static constexpr uint32_t kQ = kNQ * kPitch;
+  static constexpr uint32_t kRoom = 233472 / OCC - 1024;            // shared memory of a CTA
+  static constexpr uint32_t kSmall = D == 256 && WQ == 2 ? 384 : 1024;        // struct Small
+  static constexpr int kStages = (int)((kRoom - QB * kQ - kSmall) / (2 * kHalf));
   static constexpr uint32_t kRing = (uint32_t)kStages * 2 * kHalf;
-  static_assert(kKT * kTG == KG && kStages > kTG, "ring too short");
-  static_assert(kRing + kMerge + 2 * kQ <= kSmemBytes && kRing % 1024 == 0, "shared memory");
+  static_assert(kStages >= 2, "ring too short");
 };
 
 struct SplitParams {
   AttnLaunch a;
-  float* part;     // [2 * kSplitCtas][kNQ][D]
-  float* stats;    // [2 * kSplitCtas][kNQ][2]: m (log2 units), l
-  int32_t* info;   // [kSplitCtas][8]: the unit that begins in a CTA and ends in another
+  float* part;     // [2 * CTAs][kNQ][D]
+  float* stats;    // [2 * CTAs][kNQ][2]: m (of the scores before their scale), l
+  int32_t* info;   // [CTAs][8]: the unit that begins in a CTA and ends in another
   uint64_t wait_ns;
 };
 
@@ -64,15 +60,14 @@ struct Unit {
 };
 
 // The tiles that row n's queries see; 0 for an empty or bad row.
-template <int TN>
 __device__ __forceinline__ Unit unit_of(const AttnLaunch& p, int n, uint32_t* st) {
   Unit u;
   u.tiles = u.sink_tiles = u.first_tile = 0;
   if (!load_kv_row(p.rows, p.cache, n, u.r, st) || u.r.len == 0) return u;
   const int low = p.window > 0 ? max(0, u.r.kv - u.r.len - p.window + 1) : 0;
-  u.sink_tiles = (min(p.sinks, low) + TN - 1) / TN;
-  u.first_tile = max(low / TN, u.sink_tiles);
-  u.tiles = u.sink_tiles + (u.r.kv + TN - 1) / TN - u.first_tile;
+  u.sink_tiles = (min(p.sinks, low) + kTN - 1) / kTN;
+  u.first_tile = max(low / kTN, u.sink_tiles);
+  u.tiles = u.sink_tiles + (u.r.kv + kTN - 1) / kTN - u.first_tile;
   return u;
 }
 
@@ -92,7 +87,7 @@ __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t a) {
                : "r"(a));
 }
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -108,27 +103,38 @@ __device__ __forceinline__ float bf_hi(uint32_t x) { return __uint_as_float(x & 
 __device__ __forceinline__ bool not_finite2(uint32_t x) {
   return (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u;
 }
-template <int WARPS>
-__device__ __forceinline__ void compute_bar() {
-  asm volatile("bar.sync 1, %0;" ::"n"(32 * WARPS) : "memory");
+// The tiles dealt to the CTAs: the first `more` CTAs get each + 1, the others each.
+struct Deal {
+  int64_t each;
+  int more;
+  __device__ int64_t first(int cta) const { return each * cta + min(cta, more); }
+  __device__ int owner(int64_t tile) const;
+};
+
+// 64-bit quotient; in 32 bits where that does.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+__device__ __forceinline__ int Deal::owner(int64_t tile) const {
+  const int64_t head = (each + 1) * more;
+  return (int)(tile < head ? quotient(tile, each + 1) : more + quotient(tile - head, each));
 }
 
-// The CTA's share of all tiles, and where it begins.
+// A CTA's share of the tiles, and where it begins.
 struct Share {
-  int64_t total, first, last;
+  Deal deal;
+  int64_t first, last;
   int row;
   int64_t into;  // tiles of row `row` before the share
 };
 
-template <int TN, int THREADS>
-__device__ void find_share(const AttnLaunch& p, int ctas, int cta, Share& out) {
-  __shared__ int64_t s_part[THREADS / 32];
-  __shared__ Share s_share;
+template <int THREADS>
+__device__ void find_share(const AttnLaunch& p, int ctas, int cta, int64_t* s_part, Share& share) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (p.rows.num_seqs + THREADS - 1) / THREADS;
   const int n0 = min(tid * per, p.rows.num_seqs), n1 = min(n0 + per, p.rows.num_seqs);
   int64_t mine = 0;
-  for (int n = n0; n < n1; ++n) mine += unit_of<TN>(p, n, cta == 0 ? p.status : nullptr).tiles;
+  for (int n = n0; n < n1; ++n) mine += unit_of(p, n, cta == 0 ? p.status : nullptr).tiles;
   mine *= p.cache.Hkv;
   int64_t inc = mine;
 #pragma unroll
@@ -138,46 +144,40 @@ __device__ void find_share(const AttnLaunch& p, int ctas, int cta, Share& out) {
   }
   if (lane == 31) s_part[warp] = inc;
   __syncthreads();
-  int64_t before = 0, total = 0;
+  int64_t before = inc - mine, total = 0;
 #pragma unroll
   for (int i = 0; i < THREADS / 32; ++i) {
     if (i < warp) before += s_part[i];
     total += s_part[i];
   }
-  before += inc - mine;
-  const int64_t used = min((int64_t)ctas, total);  // a share holds a tile at least
-  int64_t first = total, last = total;
-  if (cta < used) {
-    first = total * cta / used;
-    last = total * (cta + 1) / used;
-  }
-  if (tid == 0) {
-    s_share.total = total;
-    s_share.first = first;
-    s_share.last = last;
-    s_share.row = 0;
-    s_share.into = 0;
-  }
-  __syncthreads();
-  if (first < last && first >= before && first < before + mine) {  // one thread
-    int64_t at = before;
-    for (int n = n0; n < n1; ++n) {
-      const int64_t t = (int64_t)unit_of<TN>(p, n, nullptr).tiles * p.cache.Hkv;
-      if (first < at + t) {
-        s_share.row = n;
-        s_share.into = first - at;
-        break;
+  Share mine_of;
+  mine_of.deal.each = quotient(total, ctas);
+  mine_of.deal.more = (int)(total - mine_of.deal.each * ctas);
+  mine_of.first = mine_of.deal.first(cta);
+  mine_of.last = mine_of.deal.first(cta + 1);
+  mine_of.row = 0;
+  mine_of.into = 0;
+  const int64_t first = mine_of.first;
+  if (first == mine_of.last) {  // no tile: any thread's copy will do
+    if (tid == 0) share = mine_of;
+  } else if (first >= before && first < before + mine) {  // one thread
+    int n = n0;
+    if (per > 1) {
+      for (; n < n1; ++n) {
+        const int64_t t = (int64_t)unit_of(p, n, nullptr).tiles * p.cache.Hkv;
+        if (first < before + t) break;
+        before += t;
       }
-      at += t;
     }
+    mine_of.row = n;
+    mine_of.into = first - before;
+    share = mine_of;
   }
   __syncthreads();
-  out = s_share;
 }
 
 // Walks the units of a share: (row, head, tiles [j0, j0 + len) of the unit).  A warp holds 32 rows,
 // one per lane, so that going on to the next row waits for no memory.  All lanes call together.
-template <int TN>
 struct Walk {
   const AttnLaunch& p;
   int64_t left;
@@ -187,7 +187,7 @@ struct Walk {
     if (left <= 0) return;
     fill();
     pick();
-    h = (int)(s.into / u.tiles);
+    h = (int)quotient(s.into, u.tiles);
     j0 = (int)(s.into - (int64_t)h * u.tiles);
     len = (int)min((int64_t)(u.tiles - j0), left);
   }
@@ -209,7 +209,7 @@ struct Walk {
     }
     len = (int)min((int64_t)u.tiles, left);
   }
-  __device__ int tile_at(int j) const { return (j < u.sink_tiles ? j : u.first_tile + j - u.sink_tiles) * TN; }
+  __device__ int tile_at(int j) const { return (j < u.sink_tiles ? j : u.first_tile + j - u.sink_tiles) * kTN; }
 
  private:
   int base;
@@ -218,7 +218,7 @@ struct Walk {
     base = n;
     mine.tiles = 0;
     const int row = n + (threadIdx.x & 31);
-    if (row < p.rows.num_seqs) mine = unit_of<TN>(p, row, nullptr);
+    if (row < p.rows.num_seqs) mine = unit_of(p, row, nullptr);
   }
   __device__ void pick() {
     const int src = n - base;
@@ -234,7 +234,7 @@ struct Walk {
 
 // One 32-token step's second product, O += P V.  PART: some query does not see some token, so the
 // values must not reach it whatever they hold.
-template <bool PART, int TN, int DV>
+template <bool PART, int DV>
 __device__ __forceinline__ void values_step(float (&o)[DV / 8][4], const uint32_t (&ph)[2][4], const uint32_t (&pl)[2][4],
                                             uint32_t vbase, int col0, int b, const int (&pos)[2], int pmax, int window,
                                             int sinks) {
@@ -251,91 +251,101 @@ __device__ __forceinline__ void values_step(float (&o)[DV / 8][4], const uint32_
       m0 = (t0 + c2 <= pmax ? 0xffffu : 0u) | (t0 + c2 + 1 <= pmax ? 0xffff0000u : 0u);
       m1 = (t0 + c2 + 8 <= pmax ? 0xffffu : 0u) | (t0 + c2 + 9 <= pmax ? 0xffff0000u : 0u);
     }
+    // Two 16-column blocks at a time: the four accumulators take their hi products, then their lo
+    // ones, so no product waits for the one just before it.
 #pragma unroll
-    for (int i = 0; i < DV / 16; ++i) {
-      const int chunk = col0 / 8 + i * 2 + (lane >> 4);
-      uint32_t v[4];
-      ldsm4t(v, base + (chunk >> 3) * TN * 128 + (((chunk & 7) ^ (r & 7)) << 4));
-      if (PART) {
-        v[0] &= m0;
-        v[1] &= m1;
-        v[2] &= m0;
-        v[3] &= m1;
-        const bool odd = not_finite2(v[0]) || not_finite2(v[1]) || not_finite2(v[2]) || not_finite2(v[3]);
-        if (__any_sync(0xffffffffu, odd)) {
-          // An infinity or NaN that some query of the step must not see (0 times it is NaN): one token
-          // at a time, added only where it is seen.
-#pragma unroll 1
-          for (int t = 0; t < 16; ++t) {
-            const uint32_t keep = ((t & 7) >> 1) == (lane & 3) ? ((t & 1) ? 0xffff0000u : 0xffffu) : 0u;
-            const uint32_t lo = t < 8 ? keep : 0u, hi = t < 8 ? 0u : keep;
+    for (int i = 0; i < DV / 16; i += 2) {
+      uint32_t v[2][4];
+      bool odd = false;
 #pragma unroll
-            for (int n = 0; n < 2; ++n) {
-              float x[4] = {0.f, 0.f, 0.f, 0.f};
-              mma16816(x, ph[half], v[2 * n] & lo, v[2 * n + 1] & hi);
-              mma16816(x, pl[half], v[2 * n] & lo, v[2 * n + 1] & hi);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int at = pos[e >> 1], tk = t0 + t;
-                if (tk <= at && (window <= 0 || tk > at - window || tk < sinks)) o[2 * i + n][e] += x[e];
-              }
-            }
-          }
-          continue;
+      for (int u = 0; u < 2; ++u) {
+        const int chunk = col0 / 8 + (i + u) * 2 + (lane >> 4);
+        ldsm4t(v[u], base + (chunk >> 3) * kTN * 128 + (((chunk & 7) ^ (r & 7)) << 4));
+        if (PART) {
+          v[u][0] &= m0;
+          v[u][1] &= m1;
+          v[u][2] &= m0;
+          v[u][3] &= m1;
+          odd |= not_finite2(v[u][0]) || not_finite2(v[u][1]) || not_finite2(v[u][2]) || not_finite2(v[u][3]);
         }
       }
+      if (PART && __any_sync(0xffffffffu, odd)) {
+        // An infinity or NaN that some query of the step must not see (0 times it is NaN): one token
+        // at a time, added only where it is seen.
+#pragma unroll 1
+        for (int t = 0; t < 16; ++t) {
+          const uint32_t keep = ((t & 7) >> 1) == (lane & 3) ? ((t & 1) ? 0xffff0000u : 0xffffu) : 0u;
+          const uint32_t lo = t < 8 ? keep : 0u, hi = t < 8 ? 0u : keep;
 #pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        mma16816(o[2 * i + n], ph[half], v[2 * n], v[2 * n + 1]);
-        mma16816(o[2 * i + n], pl[half], v[2 * n], v[2 * n + 1]);
+          for (int n = 0; n < 4; ++n) {
+            float x[4] = {0.f, 0.f, 0.f, 0.f};
+            mma16816(x, ph[half], v[n >> 1][2 * (n & 1)] & lo, v[n >> 1][2 * (n & 1) + 1] & hi);
+            mma16816(x, pl[half], v[n >> 1][2 * (n & 1)] & lo, v[n >> 1][2 * (n & 1) + 1] & hi);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int at = pos[e >> 1], tk = t0 + t;
+              if (tk <= at && (window <= 0 || tk > at - window || tk < sinks)) o[2 * i + n][e] += x[e];
+            }
+          }
+        }
+        continue;
       }
+#pragma unroll
+      for (int n = 0; n < 4; ++n) mma16816(o[2 * i + n], ph[half], v[n >> 1][2 * (n & 1)], v[n >> 1][2 * (n & 1) + 1]);
+#pragma unroll
+      for (int n = 0; n < 4; ++n) mma16816(o[2 * i + n], pl[half], v[n >> 1][2 * (n & 1)], v[n >> 1][2 * (n & 1) + 1]);
     }
   }
 }
 
-template <int D, int WQ, int DS, int KG>
-__global__ void __launch_bounds__(Cfg<D, WQ, DS, KG>::kThreads, 1)
+// What a CTA keeps in shared memory behind its ring and queries.
+template <typename C, int QB>
+struct Small {
+  uint64_t full[C::kStages], empty[C::kStages], qfull[QB], qempty[QB];
+  int64_t part[C::kThreads / 32];
+  Share share;
+  uint32_t held[C::kStages];  // per stage: which halves of the tile lie in pages that hold tokens
+  int qtok[QB][C::kNQ];       // the queries' global tokens, -1 for none
+  int dead;
+};
+
+template <int D, int WQ, int DS, int OCC, int QB>
+__global__ void __launch_bounds__(Cfg<D, WQ, DS, OCC, QB>::kThreads, OCC)
     split_kernel(SplitParams P, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
-  using C = Cfg<D, WQ, DS, KG>;
-  constexpr int TN = C::kTN, S = C::kStages, DV = C::kDV;
-  extern __shared__ uint8_t raw[];
-  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-  float* merge = reinterpret_cast<float*>(ring + C::kRing);
-  uint8_t* qbuf = ring + C::kRing + C::kMerge;
-  __shared__ uint64_t full[S], empty[S], qfull[2], qempty[2];
-  __shared__ uint32_t held[S];  // per stage: which of the tile's pages hold tokens
-  __shared__ float sm_m[C::kSlots][16], sm_l[C::kSlots][16];
-  __shared__ int dead;
+  using C = Cfg<D, WQ, DS, OCC, QB>;
+  constexpr int S = C::kStages, DV = C::kDV;
+  static_assert(sizeof(Small<C, QB>) <= C::kSmall, "shared memory");
+  extern __shared__ __align__(1024) uint8_t ring[];
+  uint8_t* qbuf = ring + C::kRing;
+  Small<C, QB>& sm = *reinterpret_cast<Small<C, QB>*>(qbuf + QB * C::kQ);
   const AttnLaunch& p = P.a;
   const KvDev& kv = p.cache;
-  // The warp's number comes from a shuffle, so that the compiler takes it as one value of the warp and
-  // infers no range for it: with threadIdx.x / 32 nvcc 13.0 took the receiving groups' slots of the
-  // merge buffer below to lie outside it.
+  // The warp's number comes from a shuffle, so that the compiler takes it as one value of the warp.
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (tid == 0) {
     for (int i = 0; i < S; ++i) {
-      tc::mbar_init(&full[i], 1);
-      tc::mbar_init(&empty[i], C::kKT * WQ * DS);
+      tc::mbar_init(&sm.full[i], 1);
+      tc::mbar_init(&sm.empty[i], C::kWarps);
     }
-    for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(&qfull[i], 1);
-      tc::mbar_init(&qempty[i], C::kWarps);
+    for (int i = 0; i < QB; ++i) {
+      tc::mbar_init(&sm.qfull[i], 1);
+      tc::mbar_init(&sm.qempty[i], C::kWarps);
     }
     tc::mbar_init_fence();
-    dead = 0;
+    sm.dead = 0;
     P.info[blockIdx.x * 8] = 0;
   }
   if (tid == 32 * C::kWarps) {
     tc::prefetch_map(&kmap);
     tc::prefetch_map(&vmap);
   }
-  Share share;
-  find_share<TN, C::kThreads>(p, kSplitCtas, blockIdx.x, share);
+  find_share<C::kThreads>(p, C::kCtas, blockIdx.x, sm.part, sm.share);
+  const Share& share = sm.share;
   const int ps = kv.page_size;
-  const int box = min(ps, TN);       // tokens of one copy
-  const int boxes = TN / box;        // pages of a tile
+  const int box = min(ps, kTN);      // tokens of one copy
+  const int boxes = kTN / box;       // pages of a tile
   const int shift = __ffs(ps) - 1;
 
   if (warp == C::kWarps) {
@@ -345,9 +355,15 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, KG>::kThreads, 1)
     const bool active = bi < boxes;
     int it = 0, seg = 0;
     bool ok = true;
-    for (Walk<TN> w(p, share); w.valid() && ok; w.next(), ++seg) {
+    for (Walk w(p, share); w.valid() && ok; w.next(), ++seg) {
+      // 32 table entries are held, one per lane, and the 32 behind them are on their way
+      const int32_t* row = kv.table + (int64_t)w.u.r.trow * kv.max_pages;
+      const int entries = (w.u.r.kv + ps - 1) >> shift;
+      int eb = w.tile_at(w.j0) >> shift;
+      int ids = eb + lane < entries ? __ldg(row + eb + lane) : 0;
+      int ahead = eb + 32 + lane < entries ? __ldg(row + eb + 32 + lane) : 0;
       // the unit's queries
-      const int nq = w.u.r.len * p.G, qb = seg & 1;
+      const int nq = w.u.r.len * p.G, qb = seg % QB;
       int g[2];
       int rows = 0;
 #pragma unroll
@@ -357,10 +373,14 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, KG>::kThreads, 1)
         if (qi < nq) g[u] = global_token(RowsDev{nullptr, p.rows.tok}, w.u.r.bos + qi / p.G, p.num_global, p.status);
         rows += __popc(__ballot_sync(0xffffffffu, g[u] >= 0));
       }
-      ok = seg < 2 || tc::mbar_wait(&qempty[qb], ((seg >> 1) - 1) & 1, P.wait_ns);
+      ok = seg < QB || tc::mbar_wait(&sm.qempty[qb], ((seg / QB) - 1) & 1, P.wait_ns);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      if (lane == 0) tc::expect_tx(&qfull[qb], (uint32_t)rows * D * 2);
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        if (lane + 32 * u < C::kNQ) sm.qtok[qb][lane + 32 * u] = g[u];
+      __syncwarp();
+      if (lane == 0) tc::expect_tx(&sm.qfull[qb], (uint32_t)rows * D * 2);
       __syncwarp();
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
@@ -369,12 +389,8 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, KG>::kThreads, 1)
           tc::bulk_g2s(qbuf + qb * C::kQ + qi * C::kPitch,
                        static_cast<const __nv_bfloat16*>(p.q) + (int64_t)g[u] * p.q_stride +
                            (int64_t)(w.h * p.G + qi % p.G) * D,
-                       D * 2, &qfull[qb]);
+                       D * 2, &sm.qfull[qb]);
       }
-      // 32 table entries are held, one per lane, and the 32 behind them are on their way
-      const int32_t* row = kv.table + (int64_t)w.u.r.trow * kv.max_pages;
-      const int entries = (w.u.r.kv + ps - 1) >> shift;
-      int eb = -64, ids = 0, ahead = 0;
       for (int j = w.j0; j < w.j0 + w.len; ++j, ++it) {
         const int pos = w.tile_at(j) + bi * box;
         const int e = w.tile_at(j) >> shift;
@@ -391,44 +407,43 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, KG>::kThreads, 1)
         int page = __shfl_sync(0xffffffffu, ids, active ? (pos >> shift) - eb : 0);
         page = active && pos < w.u.r.kv ? page_or_null(page, kv, p.status) : 0;
         const int s = it % S;
-        ok = it < S || tc::mbar_wait(&empty[s], ((it / S) - 1) & 1, P.wait_ns);
+        ok = it < S || tc::mbar_wait(&sm.empty[s], ((it / S) - 1) & 1, P.wait_ns);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         const uint32_t have = __ballot_sync(0xffffffffu, page > 0 && cb == 0 && is_v == 0);
         uint32_t mask = 0;
         for (int i = 0; i < boxes; ++i) mask |= (have >> (i * 2 * CB) & 1u) << i;
         if (lane == 0) {
-          held[s] = mask;
-          tc::expect_tx(&full[s], 2 * C::kHalf);
+          sm.held[s] = mask;
+          tc::expect_tx(&sm.full[s], 2 * C::kHalf);
         }
         __syncwarp();
         if (active) {
-          uint8_t* dst = ring + (size_t)s * 2 * C::kHalf + is_v * C::kHalf + (size_t)(cb * TN + bi * box) * 128;
+          uint8_t* dst = ring + (size_t)s * 2 * C::kHalf + is_v * C::kHalf + (size_t)(cb * kTN + bi * box) * 128;
           tc::tma_page(dst, is_v ? &vmap : &kmap, cb * 64, pos & (ps - 1), w.h, page > 0 ? page : kv.num_pages,
-                       &full[s]);
+                       &sm.full[s]);
         }
       }
     }
     // No copy may be in flight when the CTA ends.  Computing warps wait for every stage they use, so
     // this passes at once unless a wait gave up.
-    for (int i = max(0, it - S); i < it; ++i) ok &= tc::mbar_wait(&full[i % S], (i / S) & 1, P.wait_ns);
-    for (int i = max(0, seg - 2); i < seg; ++i) ok &= tc::mbar_wait(&qfull[i & 1], (i >> 1) & 1, P.wait_ns);
+    for (int i = max(0, it - S); i < it; ++i) ok &= tc::mbar_wait(&sm.full[i % S], (i / S) & 1, P.wait_ns);
+    for (int i = max(0, seg - QB); i < seg; ++i) ok &= tc::mbar_wait(&sm.qfull[i % QB], (i / QB) & 1, P.wait_ns);
     if (!ok && lane == 0) {
-      dead = 1;
+      sm.dead = 1;
       set_status(p.status, GDN_STATUS_WAIT_TIMEOUT);
     }
     return;
   }
 
   // ---- computing warps ----
-  const int ds = warp % DS, wq = (warp / DS) % WQ, kg = warp / (DS * WQ);
-  const int kt = kg % C::kKT, tg = kg / C::kKT;
+  const int ds = warp % DS, wq = warp / DS;
   const int r8 = lane >> 2, c2 = (lane & 3) * 2;
   const int bshift = __ffs(box) - 1;
   const float sl2 = p.scale * 1.4426950408889634f;
   int it = 0, seg = 0;
   bool ok = true;
-  for (Walk<TN> w(p, share); w.valid(); w.next(), ++seg) {
+  for (Walk w(p, share); w.valid(); w.next(), ++seg) {
     const KvRow row = w.u.r;
     const int nq = row.len * p.G;
     const int pmin = row.kv - row.len, pmax = row.kv - 1;
@@ -442,20 +457,19 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, KG>::kThreads, 1)
       l[e] = 0.f;
       pos[e] = min(pmin + (wq * 16 + r8 + 8 * e) / p.G, pmax);
     }
-    ok = __all_sync(0xffffffffu, ok && tc::mbar_wait(&qfull[seg & 1], (seg >> 1) & 1, P.wait_ns));
+    ok = __all_sync(0xffffffffu, ok && tc::mbar_wait(&sm.qfull[seg % QB], (seg / QB) & 1, P.wait_ns));
     const uint32_t qbase =
-        tc::smem_addr(qbuf + (seg & 1) * C::kQ) + (wq * 16 + (lane & 15)) * C::kPitch + (lane >> 4) * 16;
+        tc::smem_addr(qbuf + (seg % QB) * C::kQ) + (wq * 16 + (lane & 15)) * C::kPitch + (lane >> 4) * 16;
 
     for (int j = w.j0; j < w.j0 + w.len; ++j, ++it) {
-      if (C::kTG > 1 && it % C::kTG != tg) continue;
       const int s = it % S;
-      ok = __all_sync(0xffffffffu, ok && tc::mbar_wait(&full[s], (it / S) & 1, P.wait_ns));
-      const int b = w.tile_at(j) + kt * 32;  // first token of this warp's step
+      ok = __all_sync(0xffffffffu, ok && tc::mbar_wait(&sm.full[s], (it / S) & 1, P.wait_ns));
+      const int b = w.tile_at(j);
       // a page is 16 tokens or more: the step's two halves may differ in whether theirs is NULL
-      const uint32_t hm = held[s];
-      const bool have0 = hm >> (kt * 32 >> bshift) & 1u, have1 = hm >> ((kt * 32 + 16) >> bshift) & 1u;
-      if (ok && b <= pmax && (have0 || have1)) {
-        const uint32_t kbase = tc::smem_addr(ring + (size_t)s * 2 * C::kHalf) + kt * 32 * 128;
+      const uint32_t hm = sm.held[s];
+      const bool have0 = hm & 1u, have1 = hm >> (16 >> bshift) & 1u;
+      if (ok && (have0 || have1)) {
+        const uint32_t kbase = tc::smem_addr(ring + (size_t)s * 2 * C::kHalf);
         const uint32_t vbase = kbase + C::kHalf;
         // S = Q K^T.  K as the B operand: lanes 0-7, 8-15, 16-23, 24-31 point at (tokens 0-7, left 8
         // columns), (0-7, right), (8-15, left), (8-15, right) of 16 tokens.
@@ -469,7 +483,7 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, KG>::kThreads, 1)
           for (int k = 0; k < D / 16; ++k) {
             uint32_t a[4], k0[4], k1[4];
             const uint32_t at =
-                base + (k >> 2) * TN * 128 + ((((k & 3) * 2 + ((lane >> 3) & 1)) ^ (r & 7)) << 4);
+                base + (k >> 2) * kTN * 128 + ((((k & 3) * 2 + ((lane >> 3) & 1)) ^ (r & 7)) << 4);
             ldsm4(a, qbase + k * 32);
             ldsm4(k0, at);
             ldsm4(k1, at + 16 * 128);
@@ -539,125 +553,57 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, KG>::kThreads, 1)
           }
         }
         if (part)
-          values_step<true, TN, DV>(o, ph, pl, vbase, ds * DV, b, pos, pmax, p.window, p.sinks);
+          values_step<true, DV>(o, ph, pl, vbase, ds * DV, b, pos, pmax, p.window, p.sinks);
         else
-          values_step<false, TN, DV>(o, ph, pl, vbase, ds * DV, b, pos, pmax, p.window, p.sinks);
+          values_step<false, DV>(o, ph, pl, vbase, ds * DV, b, pos, pmax, p.window, p.sinks);
       }
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&empty[s]);
+      if (lane == 0) tc::mbar_arrive(&sm.empty[s]);
     }
-    __syncwarp();
-    if (lane == 0) tc::mbar_arrive(&qempty[seg & 1]);
-
-    // ---- the unit's piece ends: join the warps of a query group and column slice ----
+    // ---- the unit's piece ends ----
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
       l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
     }
     if (!ok && lane == 0) {
-      dead = 1;
+      sm.dead = 1;
       set_status(p.status, GDN_STATUS_WAIT_TIMEOUT);
     }
-    // token groups hand theirs down, kSP of them at a time, through the merge buffer: the upper ones
-    // give, the ones just below them receive, until group 0 holds all
-#pragma unroll 1
-    for (int live = KG; live > 1;) {
-      const int take = min(live >> 1, C::kSP);
-      const int gives = kg - (live - take), receives = gives + take;
-      compute_bar<C::kWarps>();
-      if (gives >= 0 && gives < take) {
-        const int slot = (gives * WQ + wq) * DS + ds;
-        float4* b4 = reinterpret_cast<float4*>(merge) + slot * (DV / 8) * 32 + lane;
-#pragma unroll
-        for (int i = 0; i < DV / 8; ++i) b4[i * 32] = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
-        if ((lane & 3) == 0)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            sm_m[slot][r8 + 8 * e] = m[e];
-            sm_l[slot][r8 + 8 * e] = l[e];
-          }
-      }
-      compute_bar<C::kWarps>();
-      if (receives >= 0 && receives < take) {
-        const int slot = (receives * WQ + wq) * DS + ds;
-        const float4* b4 = reinterpret_cast<const float4*>(merge) + slot * (DV / 8) * 32 + lane;
-        float f[2], g[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float m2 = sm_m[slot][r8 + 8 * e], mn = fmaxf(m[e], m2);
-          f[e] = m[e] == -INFINITY ? 0.f : ex2((m[e] - mn) * sl2);
-          g[e] = m2 == -INFINITY ? 0.f : ex2((m2 - mn) * sl2);
-          l[e] = l[e] * f[e] + sm_l[slot][r8 + 8 * e] * g[e];
-          m[e] = mn;
-        }
-#pragma unroll
-        for (int i = 0; i < DV / 8; ++i) {
-          const float4 v = b4[i * 32];
-          o[i][0] = o[i][0] * f[0] + v.x * g[0];
-          o[i][1] = o[i][1] * f[0] + v.y * g[0];
-          o[i][2] = o[i][2] * f[1] + v.z * g[1];
-          o[i][3] = o[i][3] * f[1] + v.w * g[1];
-        }
-      }
-      live -= take;
-    }
-    compute_bar<C::kWarps>();
-    if (kg == 0 && !*(volatile int*)&dead) {
+    if (ok) {
       const bool whole = w.j0 == 0 && w.len == w.u.tiles;
-      // rows of queries in shared memory, then 16-byte stores
-      float* mine = merge + (size_t)(wq * DS + ds) * 16 * DV;
-      float f[2];
+      const int slot = 2 * blockIdx.x + (w.j0 == 0 ? 1 : 0);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) f[e] = !whole ? 1.f : l[e] == 0.f ? 0.f : 1.f / l[e];
+      for (int e = 0; e < 2; ++e) {
+        const int qi = wq * 16 + r8 + 8 * e;
+        const int g = sm.qtok[seg % QB][qi];
+        if (whole && g >= 0) {
+          const float f = l[e] == 0.f ? 0.f : 1.f / l[e];
+          __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + (int64_t)g * p.out_stride +
+                               (int64_t)(w.h * p.G + qi % p.G) * D + ds * DV + c2;
 #pragma unroll
-      for (int i = 0; i < DV / 8; ++i)
+          for (int i = 0; i < DV / 8; ++i)
+            *reinterpret_cast<uint32_t*>(out + i * 8) = pack2(o[i][2 * e] * f, o[i][2 * e + 1] * f);
+        } else if (!whole && qi < nq) {
+          float* part = P.part + ((size_t)slot * C::kNQ + qi) * D + ds * DV + c2;
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-          *reinterpret_cast<float2*>(mine + (r8 + 8 * e) * DV + i * 8 + c2) =
-              make_float2(o[i][2 * e] * f[e], o[i][2 * e + 1] * f[e]);
-      __syncwarp();
-      if (whole) {
-#pragma unroll 1
-        for (int v = lane; v < 16 * DV / 8; v += 32) {
-          const int q = v / (DV / 8), d0 = (v % (DV / 8)) * 8, qi = wq * 16 + q;
-          if (qi >= nq) continue;
-          const int t = qi / p.G;
-          const int g = p.rows.tok ? __ldg(p.rows.tok + row.bos + t) : row.bos + t;
-          if (g < 0 || g >= p.num_global) continue;
-          *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + (int64_t)g * p.out_stride +
-                                    (int64_t)(w.h * p.G + qi - t * p.G) * D + ds * DV + d0) =
-              tc::pack8(mine + q * DV + d0);
-        }
-      } else {
-        const int slot = 2 * blockIdx.x + (w.j0 == 0 ? 1 : 0);
-#pragma unroll 1
-        for (int v = lane; v < 16 * DV / 4; v += 32) {
-          const int q = v / (DV / 4), d0 = (v % (DV / 4)) * 4;
-          if (wq * 16 + q < nq)
-            *reinterpret_cast<float4*>(P.part + ((size_t)slot * C::kNQ + wq * 16 + q) * D + ds * DV + d0) =
-                *reinterpret_cast<const float4*>(mine + q * DV + d0);
-        }
-        if (ds == 0 && (lane & 3) == 0)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float* st = P.stats + ((size_t)slot * C::kNQ + wq * 16 + r8 + 8 * e) * 2;
-            st[0] = m[e];
-            st[1] = l[e];
-          }
-        if (w.j0 == 0 && tid == 0) {
-          // the CTA that holds the unit's last tile
-          const int64_t used = min((int64_t)kSplitCtas, share.total);
-          const int64_t end = share.last - w.left + w.u.tiles - 1;
-          int32_t* info = P.info + blockIdx.x * 8;
-          info[1] = row.bos;
-          info[2] = nq;
-          info[3] = w.h;
-          info[4] = (int)(((end + 1) * used - 1) / share.total);
-          info[0] = 1;
+          for (int i = 0; i < DV / 8; ++i)
+            *reinterpret_cast<float2*>(part + i * 8) = make_float2(o[i][2 * e], o[i][2 * e + 1]);
+          if (ds == 0 && c2 == 0)
+            *reinterpret_cast<float2*>(P.stats + ((size_t)slot * C::kNQ + qi) * 2) = make_float2(m[e], l[e]);
         }
       }
+      if (!whole && w.j0 == 0 && tid == 0) {
+        int32_t* info = P.info + blockIdx.x * 8;
+        info[1] = row.bos;
+        info[2] = nq;
+        info[3] = w.h;
+        info[4] = share.deal.owner(share.last - w.left + w.u.tiles - 1);  // the CTA with the unit's last tile
+        info[0] = 1;
+      }
     }
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(&sm.qempty[seg % QB]);
   }
 }
 
@@ -720,28 +666,28 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(SplitParams P, in
   }
 }
 
-template <int D, int WQ, int DS, int KG>
+template <int D, int WQ, int DS, int OCC, int QB>
 cudaError_t launch_cfg(const AttnLaunch& a, cudaStream_t s) {
-  using C = Cfg<D, WQ, DS, KG>;
+  using C = Cfg<D, WQ, DS, OCC, QB>;
   static std::atomic<uint64_t> done{0};
-  const int smem = (int)(C::kRing + C::kMerge + 2 * C::kQ + 1024);
+  const int smem = (int)(C::kRing + QB * C::kQ + sizeof(Small<C, QB>));
   cudaError_t e = once_per_device(done, [&] {
-    return cudaFuncSetAttribute(split_kernel<D, WQ, DS, KG>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    return cudaFuncSetAttribute(split_kernel<D, WQ, DS, OCC, QB>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   });
   if (e != cudaSuccess) return e;
   CUtensorMap kmap, vmap;
-  if (!encode_pool_maps(a.cache, a.cache.page_size < C::kTN ? a.cache.page_size : C::kTN, &kmap, &vmap))
+  if (!encode_pool_maps(a.cache, a.cache.page_size < kTN ? a.cache.page_size : kTN, &kmap, &vmap))
     return cudaErrorInvalidValue;
   SplitParams P{};
   P.a = a;
   P.info = static_cast<int32_t*>(a.ws);
-  P.stats = reinterpret_cast<float*>(P.info + 8 * kSplitCtas);
-  P.part = P.stats + (size_t)4 * kSplitCtas * C::kNQ;
+  P.stats = reinterpret_cast<float*>(P.info + 8 * C::kCtas);
+  P.part = P.stats + (size_t)4 * C::kCtas * C::kNQ;
   P.wait_ns = kDefaultWaitNs;
-  split_kernel<D, WQ, DS, KG><<<kSplitCtas, C::kThreads, smem, s>>>(P, kmap, vmap);
+  split_kernel<D, WQ, DS, OCC, QB><<<C::kCtas, C::kThreads, smem, s>>>(P, kmap, vmap);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(kSplitCtas, a.rows.max_q * a.G);
+  cfg.gridDim = dim3(C::kCtas, a.rows.max_q * a.G);
   cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -761,25 +707,33 @@ bool attn_split_supported(const AttnLaunch& a, gdn_dtype dtype) {
   return dtype == GDN_BF16 && (d == 64 || d == 128 || d == 256) && (int64_t)a.rows.max_q * a.G <= 64;
 }
 
+namespace {
+
+// d = 256: two warps share a query group's output columns (16 x 256 accumulators do not fit one).
+// CTAs per SM: as many as leave a ring of 2 to 4 stages and the registers.
+template <typename F>
+auto pick(int d, int slots, F f) {
+  if (d == 64) return slots == 16 ? f(Cfg<64, 1, 1, 6, 2>{}) : slots == 32 ? f(Cfg<64, 2, 1, 4, 1>{}) : f(Cfg<64, 4, 1, 2, 1>{});
+  if (d == 128)
+    return slots == 16 ? f(Cfg<128, 1, 1, 4, 1>{}) : slots == 32 ? f(Cfg<128, 2, 1, 3, 1>{}) : f(Cfg<128, 4, 1, 2, 1>{});
+  return slots == 16 ? f(Cfg<256, 1, 2, 2, 1>{}) : slots == 32 ? f(Cfg<256, 2, 2, 2, 1>{}) : f(Cfg<256, 4, 2, 1, 1>{});
+}
+
+template <int D, int WQ, int DS, int OCC, int QB>
+cudaError_t launch_picked(Cfg<D, WQ, DS, OCC, QB>, const AttnLaunch& a, cudaStream_t s) {
+  return launch_cfg<D, WQ, DS, OCC, QB>(a, s);
+}
+
+}  // namespace
+
 size_t attn_split_workspace(const AttnLaunch& a) {
-  const size_t q = query_slots((int64_t)a.rows.max_q * a.G);
-  return (size_t)kSplitCtas * (8 + 4 * q + 2 * q * a.cache.d) * 4;
+  const int q = query_slots((int64_t)a.rows.max_q * a.G);
+  const size_t ctas = pick(a.cache.d, q, [](auto c) { return decltype(c)::kCtas; });
+  return ctas * (8 + 4 * (size_t)q + 2 * (size_t)q * a.cache.d) * 4;
 }
 
 cudaError_t launch_attn_split(const AttnLaunch& a, cudaStream_t s) {
-  // d = 256: two warps share a query group's output columns (16 x 256 accumulators do not fit one)
-  switch (a.cache.d + query_slots((int64_t)a.rows.max_q * a.G)) {
-    case 64 + 16: return launch_cfg<64, 1, 1, 8>(a, s);
-    case 64 + 32: return launch_cfg<64, 2, 1, 4>(a, s);
-    case 64 + 64: return launch_cfg<64, 4, 1, 2>(a, s);
-    case 128 + 16: return launch_cfg<128, 1, 1, 4>(a, s);
-    case 128 + 32: return launch_cfg<128, 2, 1, 4>(a, s);
-    case 128 + 64: return launch_cfg<128, 4, 1, 2>(a, s);
-    case 256 + 16: return launch_cfg<256, 1, 2, 2>(a, s);
-    case 256 + 32: return launch_cfg<256, 2, 2, 2>(a, s);
-    case 256 + 64: return launch_cfg<256, 4, 2, 1>(a, s);
-    default: return cudaErrorInvalidValue;
-  }
+  return pick(a.cache.d, query_slots((int64_t)a.rows.max_q * a.G), [&](auto c) { return launch_picked(c, a, s); });
 }
 
 }  // namespace gdn
