@@ -10,13 +10,16 @@
 // (m, l, o) in the workspace; the join kernel adds a unit's pieces in the order of the CTAs, so
 // results do not depend on timing.
 //
-// A CTA is small: one warp fetches pages by TMA into a short ring of stages (a NULL page is fetched
-// from past the pool and reads as zeros) and the queries of the next unit; one warp per 16 queries
+// A CTA (one per SM) holds 1 to 6 workers, each with a share of its own: one warp fetches pages by TMA
+// into a short ring of stages (a NULL page is fetched from past the pool and reads as zeros) and the
+// queries of the next unit; one warp per 16 queries
 // computes, 32 tokens a step, with mma.m16n8k16 and a running maximum and sum of its own.  No warp
-// waits for another, and the 2 to 6 CTAs of an SM cover one another's starts and ends of units
-// (with 8 warps sharing a tile and meeting at every unit's end a 64 x 4-token verify batch took
-// 159 us).  The weights enter the second product as a bf16 pair (hi + lo), so they keep 16 bits: the
+// waits for another, and an SM's workers cover one another's starts and ends of units (with 8 warps
+// sharing a tile and meeting at every unit's end, 64 decode rows took 96 us).  They are one CTA so that
+// their computing warps spread evenly over the SM's four schedulers.  The weights enter the second product as a bf16 pair (hi + lo), so they keep 16 bits: the
 // product is nearly free here, and one bf16 would cost as much accuracy as the output's own rounding.
+#include <algorithm>
+
 #include "gdn_tma.cuh"
 
 namespace gdn {
@@ -26,31 +29,36 @@ namespace {
 constexpr int kSms = 152;
 constexpr int kTN = 32;       // tokens of a tile
 constexpr int kJoinWarps = 8;
+constexpr int kJoinRows = 8;  // blocks that share the queries of a unit
 
-// WQ groups of 16 queries x DS slices of the values' columns, a warp each; OCC CTAs per SM; QB buffers
-// for queries.
-template <int D, int WQ, int DS, int OCC, int QB>
+// NW workers of WQ groups of 16 queries x DS slices of the values' columns, a computing warp each.
+template <int D, int WQ, int DS, int NW>
 struct Cfg {
-  static constexpr int kWarps = WQ * DS;
-  static constexpr int kThreads = 32 * (kWarps + 1);
-  static constexpr int kCtas = kSms * OCC;
+  static constexpr int kTeam = WQ * DS;                             // computing warps of a worker
+  static constexpr int kThreads = 32 * NW * (kTeam + 1);
+  static constexpr int kWorkers = NW;
   static constexpr int kNQ = 16 * WQ;                               // queries of a unit, at most
   static constexpr int kDV = D / DS;                                // value columns of a warp
   static constexpr uint32_t kHalf = (uint32_t)kTN * D * 2;          // K (or V) bytes of a stage
   static constexpr uint32_t kPitch = D * 2 + 16;                    // bytes of a query: rows 16 bytes apart mod 128
   static constexpr uint32_t kQ = kNQ * kPitch;
-  static constexpr uint32_t kRoom = 233472 / OCC - 1024;            // shared memory of a CTA
-  static constexpr uint32_t kSmall = D == 256 && WQ == 2 ? 384 : 1024;        // struct Small
-  static constexpr int kStages = (int)((kRoom - QB * kQ - kSmall) / (2 * kHalf));
-  static constexpr uint32_t kRing = (uint32_t)kStages * 2 * kHalf;
+  // what a CTA with rings of s stages takes (struct Small's sizes among it)
+  static constexpr uint32_t bytes(int s) { return NW * (s * 2 * kHalf + kQ + (17 * s + 16 + 4 * kNQ + 7) / 8 * 8 + 48) + 16; }
+  static constexpr int most() {
+    int s = 8;
+    while (bytes(s) > 232448) --s;
+    return s;
+  }
+  static constexpr int kStages = most();
+  static constexpr uint32_t kRing = (uint32_t)kStages * 2 * kHalf;  // of a worker
   static_assert(kStages >= 2, "ring too short");
 };
 
 struct SplitParams {
   AttnLaunch a;
-  float* part;     // [2 * CTAs][kNQ][D]
-  float* stats;    // [2 * CTAs][kNQ][2]: m (of the scores before their scale), l
-  int32_t* info;   // [CTAs][8]: the unit that begins in a CTA and ends in another
+  float* part;     // [2 * workers][kNQ][D]
+  float* stats;    // [2 * workers][kNQ][2]: m (of the scores before their scale), l
+  int32_t* info;   // [workers][8]: the unit that begins in a worker's share and ends in another's
   uint64_t wait_ns;
 };
 
@@ -59,16 +67,28 @@ struct Unit {
   int sink_tiles, first_tile, tiles;
 };
 
-// The tiles that row n's queries see; 0 for an empty or bad row.
-__device__ __forceinline__ Unit unit_of(const AttnLaunch& p, int n, uint32_t* st) {
+// A row's values as they lie in memory.
+struct RawRow {
+  int bos, eos, kv, trow;
+};
+__device__ __forceinline__ RawRow raw_row(const AttnLaunch& p, int n) {
+  return RawRow{__ldg(p.rows.qsl + n), __ldg(p.rows.qsl + n + 1), __ldg(p.rows.kv_lens + n),
+                p.rows.table_rows ? __ldg(p.rows.table_rows + n) : n};
+}
+
+// The tiles that the row's queries see; 0 for an empty or bad row.
+__device__ __forceinline__ Unit unit_of(const AttnLaunch& p, const RawRow& r, uint32_t* st) {
   Unit u;
   u.tiles = u.sink_tiles = u.first_tile = 0;
-  if (!load_kv_row(p.rows, p.cache, n, u.r, st) || u.r.len == 0) return u;
+  if (!check_kv_row(p.rows, p.cache, r.bos, r.eos, r.kv, r.trow, u.r, st) || u.r.len == 0) return u;
   const int low = p.window > 0 ? max(0, u.r.kv - u.r.len - p.window + 1) : 0;
   u.sink_tiles = (min(p.sinks, low) + kTN - 1) / kTN;
   u.first_tile = max(low / kTN, u.sink_tiles);
   u.tiles = u.sink_tiles + (u.r.kv + kTN - 1) / kTN - u.first_tile;
   return u;
+}
+__device__ __forceinline__ Unit unit_of(const AttnLaunch& p, int n, uint32_t* st) {
+  return unit_of(p, raw_row(p, n), st);
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -103,11 +123,11 @@ __device__ __forceinline__ float bf_hi(uint32_t x) { return __uint_as_float(x & 
 __device__ __forceinline__ bool not_finite2(uint32_t x) {
   return (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u;
 }
-// The tiles dealt to the CTAs: the first `more` CTAs get each + 1, the others each.
+// The tiles dealt to the workers: the first `more` get each + 1, the others each.
 struct Deal {
   int64_t each;
   int more;
-  __device__ int64_t first(int cta) const { return each * cta + min(cta, more); }
+  __device__ int64_t first(int worker) const { return each * worker + min(worker, more); }
   __device__ int owner(int64_t tile) const;
 };
 
@@ -120,21 +140,22 @@ __device__ __forceinline__ int Deal::owner(int64_t tile) const {
   return (int)(tile < head ? quotient(tile, each + 1) : more + quotient(tile - head, each));
 }
 
-// A CTA's share of the tiles, and where it begins.
+// A worker's share of the tiles, and where it begins.
 struct Share {
-  Deal deal;
   int64_t first, last;
-  int row;
   int64_t into;  // tiles of row `row` before the share
+  int row;
+  RawRow raw;    // that row
 };
 
-template <int THREADS>
-__device__ void find_share(const AttnLaunch& p, int ctas, int cta, int64_t* s_part, Share& share) {
+// The shares of the CTA's workers; part: one value per warp.  All threads call.
+template <int NW, int THREADS>
+__device__ void find_shares(const AttnLaunch& p, int64_t* part, Deal& deal, Share* shares) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (p.rows.num_seqs + THREADS - 1) / THREADS;
   const int n0 = min(tid * per, p.rows.num_seqs), n1 = min(n0 + per, p.rows.num_seqs);
   int64_t mine = 0;
-  for (int n = n0; n < n1; ++n) mine += unit_of(p, n, cta == 0 ? p.status : nullptr).tiles;
+  for (int n = n0; n < n1; ++n) mine += unit_of(p, n, blockIdx.x == 0 ? p.status : nullptr).tiles;
   mine *= p.cache.Hkv;
   int64_t inc = mine;
 #pragma unroll
@@ -142,42 +163,51 @@ __device__ void find_share(const AttnLaunch& p, int ctas, int cta, int64_t* s_pa
     const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += v;
   }
-  if (lane == 31) s_part[warp] = inc;
+  if (lane == 31) part[warp] = inc;
   __syncthreads();
   int64_t before = inc - mine, total = 0;
 #pragma unroll
   for (int i = 0; i < THREADS / 32; ++i) {
-    if (i < warp) before += s_part[i];
-    total += s_part[i];
+    if (i < warp) before += part[i];
+    total += part[i];
   }
-  Share mine_of;
-  mine_of.deal.each = quotient(total, ctas);
-  mine_of.deal.more = (int)(total - mine_of.deal.each * ctas);
-  mine_of.first = mine_of.deal.first(cta);
-  mine_of.last = mine_of.deal.first(cta + 1);
-  mine_of.row = 0;
-  mine_of.into = 0;
-  const int64_t first = mine_of.first;
-  if (first == mine_of.last) {  // no tile: any thread's copy will do
-    if (tid == 0) share = mine_of;
-  } else if (first >= before && first < before + mine) {  // one thread
-    int n = n0;
-    if (per > 1) {
-      for (; n < n1; ++n) {
-        const int64_t t = (int64_t)unit_of(p, n, nullptr).tiles * p.cache.Hkv;
-        if (first < before + t) break;
-        before += t;
+  Deal d;
+  d.each = quotient(total, kSms * NW);
+  d.more = (int)(total - d.each * (kSms * NW));
+  if (tid == 0) deal = d;
+#pragma unroll 1
+  for (int w = 0; w < NW; ++w) {
+    Share s;
+    s.first = d.first(blockIdx.x * NW + w);
+    s.last = d.first(blockIdx.x * NW + w + 1);
+    s.row = 0;
+    s.into = 0;
+    s.raw = RawRow{0, 0, 0, 0};
+    if (s.first == s.last) {
+      if (tid == 0) shares[w] = s;
+    } else if (s.first >= before && s.first < before + mine) {  // one thread
+      int64_t at = before;
+      int n = n0;
+      if (per > 1) {
+        for (; n < n1; ++n) {
+          const int64_t t = (int64_t)unit_of(p, n, nullptr).tiles * p.cache.Hkv;
+          if (s.first < at + t) break;
+          at += t;
+        }
       }
+      s.row = n;
+      s.into = s.first - at;
+      s.raw = raw_row(p, n);
+      shares[w] = s;
     }
-    mine_of.row = n;
-    mine_of.into = first - before;
-    share = mine_of;
   }
+  tc::fence_async_smem();  // `part` is memory that copies write next
   __syncthreads();
 }
 
-// Walks the units of a share: (row, head, tiles [j0, j0 + len) of the unit).  A warp holds 32 rows,
-// one per lane, so that going on to the next row waits for no memory.  All lanes call together.
+// Walks the units of a share: (row, head, tiles [j0, j0 + len) of the unit).  A warp holds the raw
+// values of the next 32 rows, one per lane, so that going on to the next row waits for no memory.
+// All lanes call together.
 struct Walk {
   const AttnLaunch& p;
   int64_t left;
@@ -185,8 +215,8 @@ struct Walk {
   Unit u;
   __device__ Walk(const AttnLaunch& launch, const Share& s) : p(launch), left(s.last - s.first), n(s.row), len(0) {
     if (left <= 0) return;
-    fill();
-    pick();
+    fill(n + 1);
+    u = unit_of(p, s.raw, nullptr);
     h = (int)quotient(s.into, u.tiles);
     j0 = (int)(s.into - (int64_t)h * u.tiles);
     len = (int)min((int64_t)(u.tiles - j0), left);
@@ -203,8 +233,11 @@ struct Walk {
           left = 0;
           return;
         }
-        if (n == base + 32) fill();
-        pick();
+        if (n == base + 32) fill(n);
+        const int src = n - base;
+        const RawRow r{__shfl_sync(0xffffffffu, ahead.bos, src), __shfl_sync(0xffffffffu, ahead.eos, src),
+                       __shfl_sync(0xffffffffu, ahead.kv, src), __shfl_sync(0xffffffffu, ahead.trow, src)};
+        u = unit_of(p, r, nullptr);
       } while (u.tiles == 0);
     }
     len = (int)min((int64_t)u.tiles, left);
@@ -213,22 +246,10 @@ struct Walk {
 
  private:
   int base;
-  Unit mine;
-  __device__ void fill() {
-    base = n;
-    mine.tiles = 0;
-    const int row = n + (threadIdx.x & 31);
-    if (row < p.rows.num_seqs) mine = unit_of(p, row, nullptr);
-  }
-  __device__ void pick() {
-    const int src = n - base;
-    u.r.bos = __shfl_sync(0xffffffffu, mine.r.bos, src);
-    u.r.len = __shfl_sync(0xffffffffu, mine.r.len, src);
-    u.r.kv = __shfl_sync(0xffffffffu, mine.r.kv, src);
-    u.r.trow = __shfl_sync(0xffffffffu, mine.r.trow, src);
-    u.sink_tiles = __shfl_sync(0xffffffffu, mine.sink_tiles, src);
-    u.first_tile = __shfl_sync(0xffffffffu, mine.first_tile, src);
-    u.tiles = __shfl_sync(0xffffffffu, mine.tiles, src);
+  RawRow ahead;
+  __device__ void fill(int from) {
+    base = from;
+    ahead = raw_row(p, min(from + (int)(threadIdx.x & 31), p.rows.num_seqs - 1));
   }
 };
 
@@ -298,57 +319,60 @@ __device__ __forceinline__ void values_step(float (&o)[DV / 8][4], const uint32_
   }
 }
 
-// What a CTA keeps in shared memory behind its ring and queries.
-template <typename C, int QB>
+// What a CTA keeps in shared memory behind its rings and queries.
+template <typename C>
 struct Small {
-  uint64_t full[C::kStages], empty[C::kStages], qfull[QB], qempty[QB];
-  int64_t part[C::kThreads / 32];
-  Share share;
-  uint32_t held[C::kStages];  // per stage: which halves of the tile lie in pages that hold tokens
-  int qtok[QB][C::kNQ];       // the queries' global tokens, -1 for none
-  int dead;
+  struct Worker {
+    uint64_t full[C::kStages], empty[C::kStages], qfull, qempty;
+    int qtok[C::kNQ];          // the queries' global tokens, -1 for none
+    uint8_t held[C::kStages];  // per stage: which halves of the tile lie in pages that hold tokens
+  } worker[C::kWorkers];
+  Deal deal;
+  Share shares[C::kWorkers];
 };
 
-template <int D, int WQ, int DS, int OCC, int QB>
-__global__ void __launch_bounds__(Cfg<D, WQ, DS, OCC, QB>::kThreads, OCC)
+template <int D, int WQ, int DS, int NW>
+__global__ void __launch_bounds__(Cfg<D, WQ, DS, NW>::kThreads, 1)
     split_kernel(SplitParams P, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
-  using C = Cfg<D, WQ, DS, OCC, QB>;
+  using C = Cfg<D, WQ, DS, NW>;
   constexpr int S = C::kStages, DV = C::kDV;
-  static_assert(sizeof(Small<C, QB>) <= C::kSmall, "shared memory");
-  extern __shared__ __align__(1024) uint8_t ring[];
-  uint8_t* qbuf = ring + C::kRing;
-  Small<C, QB>& sm = *reinterpret_cast<Small<C, QB>*>(qbuf + QB * C::kQ);
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Small<C>& small = *reinterpret_cast<Small<C>*>(smem + NW * (C::kRing + C::kQ));
   const AttnLaunch& p = P.a;
   const KvDev& kv = p.cache;
   // The warp's number comes from a shuffle, so that the compiler takes it as one value of the warp.
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (tid == 0) {
+  if (tid < NW) {
     for (int i = 0; i < S; ++i) {
-      tc::mbar_init(&sm.full[i], 1);
-      tc::mbar_init(&sm.empty[i], C::kWarps);
+      tc::mbar_init(&small.worker[tid].full[i], 1);
+      tc::mbar_init(&small.worker[tid].empty[i], C::kTeam);
     }
-    for (int i = 0; i < QB; ++i) {
-      tc::mbar_init(&sm.qfull[i], 1);
-      tc::mbar_init(&sm.qempty[i], C::kWarps);
-    }
+    tc::mbar_init(&small.worker[tid].qfull, 1);
+    tc::mbar_init(&small.worker[tid].qempty, C::kTeam);
     tc::mbar_init_fence();
-    sm.dead = 0;
-    P.info[blockIdx.x * 8] = 0;
   }
-  if (tid == 32 * C::kWarps) {
+  if (tid == 32) {
     tc::prefetch_map(&kmap);
     tc::prefetch_map(&vmap);
   }
-  find_share<C::kThreads>(p, C::kCtas, blockIdx.x, sm.part, sm.share);
-  const Share& share = sm.share;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // what lies before this overlaps the kernel before this one
+  if (tid < NW) P.info[(blockIdx.x * NW + tid) * 8] = 0;
+  // (the sums of find_shares lie where the first worker's ring will be)
+  find_shares<NW, C::kThreads>(p, reinterpret_cast<int64_t*>(smem), small.deal, small.shares);
+  const bool fetches = warp >= NW * C::kTeam;
+  const int wk = fetches ? warp - NW * C::kTeam : warp / C::kTeam;  // the warp's worker
+  auto& sm = small.worker[wk];
+  const Share& share = small.shares[wk];
+  uint8_t* ring = smem + wk * C::kRing;
+  uint8_t* qbuf = smem + NW * C::kRing + wk * C::kQ;
   const int ps = kv.page_size;
   const int box = min(ps, kTN);      // tokens of one copy
   const int boxes = kTN / box;       // pages of a tile
   const int shift = __ffs(ps) - 1;
 
-  if (warp == C::kWarps) {
+  if (fetches) {
     // ---- the fetching warp: lane = (page of the tile, 64-column block, K or V) ----
     constexpr int CB = D / 64;
     const int bi = lane / (2 * CB), cb = (lane >> 1) % CB, is_v = lane & 1;
@@ -363,7 +387,7 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, OCC, QB>::kThreads, OCC)
       int ids = eb + lane < entries ? __ldg(row + eb + lane) : 0;
       int ahead = eb + 32 + lane < entries ? __ldg(row + eb + 32 + lane) : 0;
       // the unit's queries
-      const int nq = w.u.r.len * p.G, qb = seg % QB;
+      const int nq = w.u.r.len * p.G;
       int g[2];
       int rows = 0;
 #pragma unroll
@@ -373,23 +397,23 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, OCC, QB>::kThreads, OCC)
         if (qi < nq) g[u] = global_token(RowsDev{nullptr, p.rows.tok}, w.u.r.bos + qi / p.G, p.num_global, p.status);
         rows += __popc(__ballot_sync(0xffffffffu, g[u] >= 0));
       }
-      ok = seg < QB || tc::mbar_wait(&sm.qempty[qb], ((seg / QB) - 1) & 1, P.wait_ns);
+      ok = seg == 0 || tc::mbar_wait(&sm.qempty, (seg - 1) & 1, P.wait_ns);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
 #pragma unroll
       for (int u = 0; u < 2; ++u)
-        if (lane + 32 * u < C::kNQ) sm.qtok[qb][lane + 32 * u] = g[u];
+        if (lane + 32 * u < C::kNQ) sm.qtok[lane + 32 * u] = g[u];
       __syncwarp();
-      if (lane == 0) tc::expect_tx(&sm.qfull[qb], (uint32_t)rows * D * 2);
+      if (lane == 0) tc::expect_tx(&sm.qfull, (uint32_t)rows * D * 2);
       __syncwarp();
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int qi = lane + 32 * u;
         if (g[u] >= 0)
-          tc::bulk_g2s(qbuf + qb * C::kQ + qi * C::kPitch,
+          tc::bulk_g2s(qbuf + qi * C::kPitch,
                        static_cast<const __nv_bfloat16*>(p.q) + (int64_t)g[u] * p.q_stride +
                            (int64_t)(w.h * p.G + qi % p.G) * D,
-                       D * 2, &sm.qfull[qb]);
+                       D * 2, &sm.qfull);
       }
       for (int j = w.j0; j < w.j0 + w.len; ++j, ++it) {
         const int pos = w.tile_at(j) + bi * box;
@@ -414,7 +438,7 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, OCC, QB>::kThreads, OCC)
         uint32_t mask = 0;
         for (int i = 0; i < boxes; ++i) mask |= (have >> (i * 2 * CB) & 1u) << i;
         if (lane == 0) {
-          sm.held[s] = mask;
+          sm.held[s] = (uint8_t)mask;
           tc::expect_tx(&sm.full[s], 2 * C::kHalf);
         }
         __syncwarp();
@@ -428,16 +452,13 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, OCC, QB>::kThreads, OCC)
     // No copy may be in flight when the CTA ends.  Computing warps wait for every stage they use, so
     // this passes at once unless a wait gave up.
     for (int i = max(0, it - S); i < it; ++i) ok &= tc::mbar_wait(&sm.full[i % S], (i / S) & 1, P.wait_ns);
-    for (int i = max(0, seg - QB); i < seg; ++i) ok &= tc::mbar_wait(&sm.qfull[i % QB], (i / QB) & 1, P.wait_ns);
-    if (!ok && lane == 0) {
-      sm.dead = 1;
-      set_status(p.status, GDN_STATUS_WAIT_TIMEOUT);
-    }
+    if (seg > 0) ok &= tc::mbar_wait(&sm.qfull, (seg - 1) & 1, P.wait_ns);
+    if (!ok) set_status(p.status, GDN_STATUS_WAIT_TIMEOUT);
     return;
   }
 
   // ---- computing warps ----
-  const int ds = warp % DS, wq = warp / DS;
+  const int ds = warp % DS, wq = (warp - wk * C::kTeam) / DS;
   const int r8 = lane >> 2, c2 = (lane & 3) * 2;
   const int bshift = __ffs(box) - 1;
   const float sl2 = p.scale * 1.4426950408889634f;
@@ -457,9 +478,9 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, OCC, QB>::kThreads, OCC)
       l[e] = 0.f;
       pos[e] = min(pmin + (wq * 16 + r8 + 8 * e) / p.G, pmax);
     }
-    ok = __all_sync(0xffffffffu, ok && tc::mbar_wait(&sm.qfull[seg % QB], (seg / QB) & 1, P.wait_ns));
+    ok = __all_sync(0xffffffffu, ok && tc::mbar_wait(&sm.qfull, seg & 1, P.wait_ns));
     const uint32_t qbase =
-        tc::smem_addr(qbuf + (seg % QB) * C::kQ) + (wq * 16 + (lane & 15)) * C::kPitch + (lane >> 4) * 16;
+        tc::smem_addr(qbuf) + (wq * 16 + (lane & 15)) * C::kPitch + (lane >> 4) * 16;
 
     for (int j = w.j0; j < w.j0 + w.len; ++j, ++it) {
       const int s = it % S;
@@ -566,17 +587,15 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, OCC, QB>::kThreads, OCC)
       l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
       l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
     }
-    if (!ok && lane == 0) {
-      sm.dead = 1;
+    if (!ok) {
       set_status(p.status, GDN_STATUS_WAIT_TIMEOUT);
-    }
-    if (ok) {
+    } else {
       const bool whole = w.j0 == 0 && w.len == w.u.tiles;
-      const int slot = 2 * blockIdx.x + (w.j0 == 0 ? 1 : 0);
+      const int slot = 2 * (blockIdx.x * NW + wk) + (w.j0 == 0 ? 1 : 0);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int qi = wq * 16 + r8 + 8 * e;
-        const int g = sm.qtok[seg % QB][qi];
+        const int g = sm.qtok[qi];
         if (whole && g >= 0) {
           const float f = l[e] == 0.f ? 0.f : 1.f / l[e];
           __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + (int64_t)g * p.out_stride +
@@ -593,86 +612,101 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, OCC, QB>::kThreads, OCC)
             *reinterpret_cast<float2*>(P.stats + ((size_t)slot * C::kNQ + qi) * 2) = make_float2(m[e], l[e]);
         }
       }
-      if (!whole && w.j0 == 0 && tid == 0) {
-        int32_t* info = P.info + blockIdx.x * 8;
+      if (!whole && w.j0 == 0 && wq == 0 && ds == 0 && lane == 0) {
+        int32_t* info = P.info + (blockIdx.x * NW + wk) * 8;
         info[1] = row.bos;
         info[2] = nq;
         info[3] = w.h;
-        info[4] = share.deal.owner(share.last - w.left + w.u.tiles - 1);  // the CTA with the unit's last tile
+        info[4] = small.deal.owner(share.last - w.left + w.u.tiles - 1);  // the worker with the unit's last tile
         info[0] = 1;
       }
     }
     __syncwarp();
-    if (lane == 0) tc::mbar_arrive(&sm.qempty[seg % QB]);
+    if (lane == 0) tc::mbar_arrive(&sm.qempty);
   }
 }
 
-// Adds the pieces of the unit that begins in CTA blockIdx.x and ends in a later one; a block per
-// query, its warps over the pieces.
+// Adds the pieces of the units that begin in the shares of CTA blockIdx.x's workers and end in later
+// ones.  Block row y takes queries y, y + kJoinRows, ..; a team of warps shares a query's pieces.
 template <int D>
-__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(SplitParams P, int queries) {
-  const float sl2 = P.a.scale * 1.4426950408889634f;
+__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(SplitParams P, int queries, int workers) {
   __shared__ float so[kJoinWarps][D];
   __shared__ float sl[kJoinWarps], sm[kJoinWarps];
   const AttnLaunch& p = P.a;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int c0 = blockIdx.x, qi = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int32_t* info = P.info + c0 * 8;
-  if (!info[0] || qi >= info[2]) return;
-  const int bos = info[1], h = info[3], c1 = info[4];
+  const float sl2 = p.scale * 1.4426950408889634f;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int E = D / 32;
-  float m = -INFINITY, l = 0.f, o[E];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  for (int c0 = blockIdx.x * workers; c0 < (int)(blockIdx.x + 1) * workers; ++c0) {
+    const int32_t* info = P.info + c0 * 8;
+    if (!info[0]) continue;
+    const int bos = info[1], nq = info[2], h = info[3], c1 = info[4], pieces = c1 - c0 + 1;
+    const int team = pieces > 8 ? 8 : pieces > 4 ? 4 : pieces > 2 ? 2 : 1;  // warps of a query
+    for (int q0 = blockIdx.y; q0 < nq; q0 += kJoinRows * (kJoinWarps / team)) {
+      const int qi = q0 + kJoinRows * (warp / team);
+      float m = -INFINITY, l = 0.f, o[E];
 #pragma unroll
-  for (int i = 0; i < E; ++i) o[i] = 0.f;
-  for (int c = c0 + warp; c <= c1; c += kJoinWarps) {
-    const size_t at = (size_t)(2 * c + (c == c0 ? 1 : 0)) * queries + qi;
-    const float m2 = P.stats[at * 2], l2 = P.stats[at * 2 + 1];
-    float v[E];
+      for (int i = 0; i < E; ++i) o[i] = 0.f;
+      if (qi < nq) {
+#pragma unroll 4
+        for (int c = c0 + warp % team; c <= c1; c += team) {
+          const size_t at = (size_t)(2 * c + (c == c0 ? 1 : 0)) * queries + qi;
+          const float2 st = *reinterpret_cast<const float2*>(P.stats + at * 2);
+          float v[E];
 #pragma unroll
-    for (int i = 0; i < E; ++i) v[i] = P.part[at * D + lane + 32 * i];
-    const float mn = fmaxf(m, m2);
-    const float a = m == -INFINITY ? 0.f : ex2((m - mn) * sl2), b = m2 == -INFINITY ? 0.f : ex2((m2 - mn) * sl2);
-    l = l * a + l2 * b;
+          for (int i = 0; i < E; ++i) v[i] = P.part[at * D + lane + 32 * i];
+          const float mn = fmaxf(m, st.x);
+          const float a = m == -INFINITY ? 0.f : ex2((m - mn) * sl2);
+          const float b = st.x == -INFINITY ? 0.f : ex2((st.x - mn) * sl2);
+          l = l * a + st.y * b;
 #pragma unroll
-    for (int i = 0; i < E; ++i) o[i] = o[i] * a + v[i] * b;
-    m = mn;
-  }
+          for (int i = 0; i < E; ++i) o[i] = o[i] * a + v[i] * b;
+          m = mn;
+        }
+      }
+      if (team > 1) {
 #pragma unroll
-  for (int i = 0; i < E; ++i) so[warp][lane + 32 * i] = o[i];
-  if (lane == 0) {
-    sm[warp] = m;
-    sl[warp] = l;
-  }
-  __syncthreads();
-  float M = sm[0];
+        for (int i = 0; i < E; ++i) so[warp][lane + 32 * i] = o[i];
+        if (lane == 0) {
+          sm[warp] = m;
+          sl[warp] = l;
+        }
+        __syncthreads();
+        if (warp % team == 0) {
+          for (int w = warp + 1; w < warp + team; ++w) {
+            const float mn = fmaxf(m, sm[w]);
+            const float a = m == -INFINITY ? 0.f : ex2((m - mn) * sl2);
+            const float b = sm[w] == -INFINITY ? 0.f : ex2((sm[w] - mn) * sl2);
+            l = l * a + sl[w] * b;
 #pragma unroll
-  for (int i = 1; i < kJoinWarps; ++i) M = fmaxf(M, sm[i]);
-  float L = 0.f, f[kJoinWarps];
+            for (int i = 0; i < E; ++i) o[i] = o[i] * a + so[w][lane + 32 * i] * b;
+            m = mn;
+          }
+        }
+        __syncthreads();
+      }
+      if (qi >= nq || warp % team) continue;
+      const int t = qi / p.G;
+      const int g = p.rows.tok ? __ldg(p.rows.tok + bos + t) : bos + t;
+      if (g < 0 || g >= p.num_global) continue;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      __nv_bfloat16* out =
+          static_cast<__nv_bfloat16*>(p.out) + (int64_t)g * p.out_stride + (int64_t)(h * p.G + qi - t * p.G) * D;
 #pragma unroll
-  for (int i = 0; i < kJoinWarps; ++i) {
-    f[i] = sm[i] == -INFINITY ? 0.f : ex2((sm[i] - M) * sl2);
-    L += sl[i] * f[i];
-  }
-  const float inv = L == 0.f ? 0.f : 1.f / L;
-  const int t = qi / p.G;
-  const int g = p.rows.tok ? __ldg(p.rows.tok + bos + t) : bos + t;
-  if (g < 0 || g >= p.num_global) return;
-  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + (int64_t)g * p.out_stride + (int64_t)(h * p.G + qi - t * p.G) * D;
-  for (int d = threadIdx.x; d < D; d += 32 * kJoinWarps) {
-    float x = 0.f;
-#pragma unroll
-    for (int i = 0; i < kJoinWarps; ++i) x += so[i][d] * f[i];
-    out[d] = __float2bfloat16_rn(x * inv);
+      for (int i = 0; i < E; ++i) out[lane + 32 * i] = __float2bfloat16_rn(o[i] * inv);
+    }
   }
 }
 
-template <int D, int WQ, int DS, int OCC, int QB>
+template <int D, int WQ, int DS, int NW>
 cudaError_t launch_cfg(const AttnLaunch& a, cudaStream_t s) {
-  using C = Cfg<D, WQ, DS, OCC, QB>;
+  using C = Cfg<D, WQ, DS, NW>;
   static std::atomic<uint64_t> done{0};
-  const int smem = (int)(C::kRing + QB * C::kQ + sizeof(Small<C, QB>));
+  constexpr int smem = (int)(NW * (C::kRing + C::kQ) + sizeof(Small<C>));
+  static_assert(smem <= 232448 && C::kThreads / 32 * 8 <= (int)C::kRing, "shared memory");
   cudaError_t e = once_per_device(done, [&] {
-    return cudaFuncSetAttribute(split_kernel<D, WQ, DS, OCC, QB>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    return cudaFuncSetAttribute(split_kernel<D, WQ, DS, NW>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   });
   if (e != cudaSuccess) return e;
   CUtensorMap kmap, vmap;
@@ -681,21 +715,24 @@ cudaError_t launch_cfg(const AttnLaunch& a, cudaStream_t s) {
   SplitParams P{};
   P.a = a;
   P.info = static_cast<int32_t*>(a.ws);
-  P.stats = reinterpret_cast<float*>(P.info + 8 * C::kCtas);
-  P.part = P.stats + (size_t)4 * C::kCtas * C::kNQ;
+  P.stats = reinterpret_cast<float*>(P.info + 8 * kSms * NW);
+  P.part = P.stats + (size_t)4 * kSms * NW * C::kNQ;
   P.wait_ns = kDefaultWaitNs;
-  split_kernel<D, WQ, DS, OCC, QB><<<C::kCtas, C::kThreads, smem, s>>>(P, kmap, vmap);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(C::kCtas, a.rows.max_q * a.G);
-  cfg.blockDim = dim3(32 * kJoinWarps);
-  cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kSms);
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_kernel<D>, P, (int)C::kNQ);
+  if ((e = cudaLaunchKernelEx(&cfg, split_kernel<D, WQ, DS, NW>, P, kmap, vmap)) != cudaSuccess) return e;
+  cfg.gridDim = dim3(kSms, std::min(kJoinRows, a.rows.max_q * a.G));
+  cfg.blockDim = dim3(32 * kJoinWarps);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, join_kernel<D>, P, (int)C::kNQ, NW);
 }
 
 int query_slots(int64_t queries) { return queries <= 16 ? 16 : queries <= 32 ? 32 : 64; }
@@ -710,26 +747,25 @@ bool attn_split_supported(const AttnLaunch& a, gdn_dtype dtype) {
 namespace {
 
 // d = 256: two warps share a query group's output columns (16 x 256 accumulators do not fit one).
-// CTAs per SM: as many as leave a ring of 2 to 4 stages and the registers.
+// Workers: as many as leave each a ring of 3 stages or more and the registers (168 a thread).
 template <typename F>
 auto pick(int d, int slots, F f) {
-  if (d == 64) return slots == 16 ? f(Cfg<64, 1, 1, 6, 2>{}) : slots == 32 ? f(Cfg<64, 2, 1, 4, 1>{}) : f(Cfg<64, 4, 1, 2, 1>{});
-  if (d == 128)
-    return slots == 16 ? f(Cfg<128, 1, 1, 4, 1>{}) : slots == 32 ? f(Cfg<128, 2, 1, 3, 1>{}) : f(Cfg<128, 4, 1, 2, 1>{});
-  return slots == 16 ? f(Cfg<256, 1, 2, 2, 1>{}) : slots == 32 ? f(Cfg<256, 2, 2, 2, 1>{}) : f(Cfg<256, 4, 2, 1, 1>{});
+  if (d == 64) return slots == 16 ? f(Cfg<64, 1, 1, 6>{}) : slots == 32 ? f(Cfg<64, 2, 1, 4>{}) : f(Cfg<64, 4, 1, 2>{});
+  if (d == 128) return slots == 16 ? f(Cfg<128, 1, 1, 4>{}) : slots == 32 ? f(Cfg<128, 2, 1, 4>{}) : f(Cfg<128, 4, 1, 2>{});
+  return slots == 16 ? f(Cfg<256, 1, 2, 2>{}) : slots == 32 ? f(Cfg<256, 2, 2, 2>{}) : f(Cfg<256, 4, 2, 1>{});
 }
 
-template <int D, int WQ, int DS, int OCC, int QB>
-cudaError_t launch_picked(Cfg<D, WQ, DS, OCC, QB>, const AttnLaunch& a, cudaStream_t s) {
-  return launch_cfg<D, WQ, DS, OCC, QB>(a, s);
+template <int D, int WQ, int DS, int NW>
+cudaError_t launch_picked(Cfg<D, WQ, DS, NW>, const AttnLaunch& a, cudaStream_t s) {
+  return launch_cfg<D, WQ, DS, NW>(a, s);
 }
 
 }  // namespace
 
 size_t attn_split_workspace(const AttnLaunch& a) {
   const int q = query_slots((int64_t)a.rows.max_q * a.G);
-  const size_t ctas = pick(a.cache.d, q, [](auto c) { return decltype(c)::kCtas; });
-  return ctas * (8 + 4 * (size_t)q + 2 * (size_t)q * a.cache.d) * 4;
+  const size_t workers = (size_t)kSms * pick(a.cache.d, q, [](auto c) { return decltype(c)::kWorkers; });
+  return workers * (8 + 4 * (size_t)q + 2 * (size_t)q * a.cache.d) * 4;
 }
 
 cudaError_t launch_attn_split(const AttnLaunch& a, cudaStream_t s) {

@@ -30,24 +30,28 @@ struct KvRow {
   int32_t trow;      // row of the block table
 };
 
-// Row n, checked against the tensors it indexes; false (and the status bit) for a bad one.
-__device__ __forceinline__ bool load_kv_row(const KvRowsDev& R, const KvDev& C, int n, KvRow& r, uint32_t* st) {
-  r.bos = __ldg(R.qsl + n);
-  const int eos = __ldg(R.qsl + n + 1);
-  r.kv = __ldg(R.kv_lens + n);
-  r.trow = R.table_rows ? __ldg(R.table_rows + n) : n;
+// A row's values, checked against the tensors they index; false (and the status bit) for a bad one.
+__device__ __forceinline__ bool check_kv_row(const KvRowsDev& R, const KvDev& C, int bos, int eos, int kv, int trow,
+                                             KvRow& r, uint32_t* st) {
+  r.bos = bos;
+  r.kv = kv;
+  r.trow = trow;
   r.len = 0;
-  if (r.bos < 0 || eos < r.bos || eos > R.num_tokens || eos - r.bos > R.max_q || r.kv < eos - r.bos ||
-      (int64_t)r.kv > (int64_t)C.max_pages * C.page_size) {
+  if (bos < 0 || eos < bos || eos > R.num_tokens || eos - bos > R.max_q || kv < eos - bos ||
+      (int64_t)kv > (int64_t)C.max_pages * C.page_size) {
     set_status(st, GDN_STATUS_ROW_RANGE);
     return false;
   }
-  if (r.trow < 0 || r.trow >= C.num_table_rows) {
+  if (trow < 0 || trow >= C.num_table_rows) {
     set_status(st, GDN_STATUS_PAGE_RANGE);
     return false;
   }
-  r.len = eos - r.bos;
+  r.len = eos - bos;
   return true;
+}
+__device__ __forceinline__ bool load_kv_row(const KvRowsDev& R, const KvDev& C, int n, KvRow& r, uint32_t* st) {
+  return check_kv_row(R, C, __ldg(R.qsl + n), __ldg(R.qsl + n + 1), __ldg(R.kv_lens + n),
+                      R.table_rows ? __ldg(R.table_rows + n) : n, r, st);
 }
 
 // A table entry as a page to read: its id, or 0 (no tokens) for NULL and out-of-range entries.
