@@ -352,6 +352,16 @@ def _stream(stream) -> Optional[int]:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # 3 us less than a Stream object
+
+
+def _stream_of(t: torch.Tensor, stream) -> Optional[int]:
+    """``stream``, by default the current one of the tensor's device."""
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(t.get_device())
+    return _stream(stream)
+
+
 def _scratch(nbytes: int, device, stream) -> torch.Tensor:
     """A workspace that its allocator keeps until the work on ``stream`` is done with it."""
     ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
@@ -467,7 +477,7 @@ def gdn_kv_append(cache: KvCache, rows: KvRows, k: torch.Tensor, v: torch.Tensor
     if k.shape[0] != v.shape[0]:
         raise ValueError("k and v: expected one token count")
     _check(library().gdn_kv_append(cache._ref, rows._ref, kp, ks, vp, vs, k.shape[0],
-                                   _ptr(status, torch.int32, "status"), _stream(stream)))
+                                   _ptr(status, torch.int32, "status"), _stream_of(cache.k_pool, stream)))
 
 
 def gdn_attention_workspace_bytes(attn: Attention, cache: KvCache, rows: KvRows) -> int:
@@ -488,7 +498,7 @@ def gdn_paged_attention(attn: Attention, cache: KvCache, rows: KvRows, q: torch.
         workspace = _scratch(gdn_attention_workspace_bytes(attn, cache, rows), q.device, stream)
     _check(library().gdn_paged_attention(attn._ref, cache._ref, rows._ref, qp, qs, q.shape[0], op, os_,
                                          _ptr(workspace, torch.uint8, "workspace"), workspace.numel(),
-                                         _ptr(status, torch.int32, "status"), _stream(stream)))
+                                         _ptr(status, torch.int32, "status"), _stream_of(cache.k_pool, stream)))
 
 
 def gdn_kv_workspace_bytes(cache: KvCache, count: int) -> int:
@@ -508,7 +518,7 @@ def gdn_kv_reserve(cache: KvCache, table_rows: Optional[torch.Tensor], from_lens
     ws = _kv_workspace(cache, n, workspace, stream)
     _check(library().gdn_kv_reserve(cache._ref, n, _int32(table_rows, "table_rows", n), _int32(from_lens, "from_lens"),
                                     _int32(to_lens, "to_lens", n), _ptr(ws, torch.uint8, "workspace"), ws.numel(),
-                                    _ptr(status, torch.int32, "status"), _stream(stream)))
+                                    _ptr(status, torch.int32, "status"), _stream_of(cache.k_pool, stream)))
 
 
 def gdn_kv_release(cache: KvCache, table_rows: torch.Tensor, first_page: Optional[torch.Tensor] = None,
@@ -518,7 +528,7 @@ def gdn_kv_release(cache: KvCache, table_rows: torch.Tensor, first_page: Optiona
     n = table_rows.numel()
     _check(library().gdn_kv_release(cache._ref, n, _int32(table_rows, "table_rows"),
                                     _int32(first_page, "first_page", n), _int32(last_page, "last_page", n),
-                                    _ptr(status, torch.int32, "status"), _stream(stream)))
+                                    _ptr(status, torch.int32, "status"), _stream_of(cache.k_pool, stream)))
 
 
 def gdn_kv_fork(cache: KvCache, src_rows: torch.Tensor, dst_rows: torch.Tensor, lens: torch.Tensor,
@@ -528,7 +538,7 @@ def gdn_kv_fork(cache: KvCache, src_rows: torch.Tensor, dst_rows: torch.Tensor, 
     ws = _kv_workspace(cache, n, workspace, stream)
     _check(library().gdn_kv_fork(cache._ref, n, _int32(src_rows, "src_rows"), _int32(dst_rows, "dst_rows", n),
                                  _int32(lens, "lens", n), _ptr(ws, torch.uint8, "workspace"), ws.numel(),
-                                 _ptr(status, torch.int32, "status"), _stream(stream)))
+                                 _ptr(status, torch.int32, "status"), _stream_of(cache.k_pool, stream)))
 
 
 def gdn_kv_copy_pages(cache: KvCache, src_pages: torch.Tensor, dst_pages: torch.Tensor,
@@ -537,7 +547,7 @@ def gdn_kv_copy_pages(cache: KvCache, src_pages: torch.Tensor, dst_pages: torch.
     n = src_pages.numel()
     _check(library().gdn_kv_copy_pages(cache._ref, n, _int32(src_pages, "src_pages"),
                                        _int32(dst_pages, "dst_pages", n), _ptr(status, torch.int32, "status"),
-                                       _stream(stream)))
+                                       _stream_of(cache.k_pool, stream)))
 
 
 def gdn_kv_compact(cache: KvCache, num_live: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
@@ -545,7 +555,7 @@ def gdn_kv_compact(cache: KvCache, num_live: Optional[torch.Tensor] = None, work
     """Moves the live pages to ids 1..M; ``num_live`` (int32, one entry) receives M."""
     ws = _kv_workspace(cache, 0, workspace, stream)
     _check(library().gdn_kv_compact(cache._ref, _int32(num_live, "num_live", 1), _ptr(ws, torch.uint8, "workspace"),
-                                    ws.numel(), _ptr(status, torch.int32, "status"), _stream(stream)))
+                                    ws.numel(), _ptr(status, torch.int32, "status"), _stream_of(cache.k_pool, stream)))
 
 
 def gdn_copy_slots(layer: Layer, pools: Pools, src_slots: torch.Tensor, dst_slots: torch.Tensor,
@@ -555,7 +565,7 @@ def gdn_copy_slots(layer: Layer, pools: Pools, src_slots: torch.Tensor, dst_slot
     act = layer.act_dtype
     _check(library().gdn_copy_slots(ctypes.byref(layer.c()), ctypes.byref(pools.c(act)), n,
                                     _int32(src_slots, "src_slots"), _int32(dst_slots, "dst_slots", n),
-                                    _ptr(status, torch.int32, "status"), _stream(stream)))
+                                    _ptr(status, torch.int32, "status"), _stream_of(pools.ssm_pool, stream)))
 
 
 def gdn_testing_set_prefill_faults(wait_ns: int = 0, drop_copy_chunk: int = -1) -> None:

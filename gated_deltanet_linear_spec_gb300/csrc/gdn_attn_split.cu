@@ -638,10 +638,16 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(SplitParams P, in
   constexpr int E = D / 32;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  for (int c0 = blockIdx.x * workers; c0 < (int)(blockIdx.x + 1) * workers; ++c0) {
-    const int32_t* info = P.info + c0 * 8;
-    if (!info[0]) continue;
-    const int bos = info[1], nq = info[2], h = info[3], c1 = info[4], pieces = c1 - c0 + 1;
+  // lane: field lane % 8 of worker lane / 8's entry, and of the worker 4 behind it
+  const int first = blockIdx.x * workers;
+  const int f0 = lane < workers * 8 ? P.info[first * 8 + lane] : 0;
+  const int f1 = lane + 32 < workers * 8 ? P.info[first * 8 + lane + 32] : 0;
+  for (int w = 0; w < workers; ++w) {
+    const int from = (w & 3) * 8, f = w < 4 ? f0 : f1;
+    if (!__shfl_sync(0xffffffffu, f, from)) continue;
+    const int bos = __shfl_sync(0xffffffffu, f, from + 1), nq = __shfl_sync(0xffffffffu, f, from + 2);
+    const int h = __shfl_sync(0xffffffffu, f, from + 3), c1 = __shfl_sync(0xffffffffu, f, from + 4);
+    const int c0 = first + w, pieces = c1 - c0 + 1;
     const int team = pieces > 8 ? 8 : pieces > 4 ? 4 : pieces > 2 ? 2 : 1;  // warps of a query
     for (int q0 = blockIdx.y; q0 < nq; q0 += kJoinRows * (kJoinWarps / team)) {
       const int qi = q0 + kJoinRows * (warp / team);
@@ -674,13 +680,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(SplitParams P, in
         }
         __syncthreads();
         if (warp % team == 0) {
-          for (int w = warp + 1; w < warp + team; ++w) {
-            const float mn = fmaxf(m, sm[w]);
+          for (int v = warp + 1; v < warp + team; ++v) {
+            const float mn = fmaxf(m, sm[v]);
             const float a = m == -INFINITY ? 0.f : ex2((m - mn) * sl2);
-            const float b = sm[w] == -INFINITY ? 0.f : ex2((sm[w] - mn) * sl2);
-            l = l * a + sl[w] * b;
+            const float b = sm[v] == -INFINITY ? 0.f : ex2((sm[v] - mn) * sl2);
+            l = l * a + sl[v] * b;
 #pragma unroll
-            for (int i = 0; i < E; ++i) o[i] = o[i] * a + so[w][lane + 32 * i] * b;
+            for (int i = 0; i < E; ++i) o[i] = o[i] * a + so[v][lane + 32 * i] * b;
             m = mn;
           }
         }
