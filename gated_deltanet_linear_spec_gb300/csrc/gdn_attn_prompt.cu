@@ -1,0 +1,737 @@
+// gdn_attn_prompt.cu -- attention of prompt rows over the paged cache on tcgen05 (bf16, d = 64, 128, 256).
+//
+// A tile of M = 128 queries is 128 consecutive (new token, q-head of the kv-head) pairs of a row, so
+// the q-heads that share a kv-head share its keys and values in shared memory.  Per 128 cached tokens
+//   S = Q K^T (128 x 128, fp32 in TMEM),  P = 2^(scale log2e (S - m)) (bf16, over S in TMEM),
+//   O += P V (128 x d, fp32 in TMEM; A = P from TMEM, B = V read MN-major from its [token][d] tile).
+// 4 d flops per score against about 5 issue slots of softmax: the tensor core bounds it once both run
+// side by side.  So a CTA holds two query tiles (d <= 128; their S and O fill the 512 TMEM columns) and
+// the products of one run under the softmax of the other; at d = 256 one tile with two S buffers.
+//   warps 0-3 (and 4-7): softmax of tile 0 (1), a thread per query;
+//   then a warp that issues all products, one that fetches pages by TMA, two that look after V tiles
+//   of which some query must not see some token (below).
+// The maximum that P refers to follows the running maximum only when that has grown by 2^8 or more
+// (weights up to 256 lose nothing in bf16 or fp32): O is rescaled in TMEM a few times per row at most.
+// P is rounded to bf16, half a step of 2^-8 relative per weight, as the product takes one 16-bit type;
+// the sum of the weights is kept in fp32.
+//
+// What a query does not see must not reach it whatever it holds, and 0 times NaN is NaN.  In a tile
+// that some query sees only in part, values past the row's end are zeroed, and a token whose values hold an
+// infinity or NaN is zeroed and listed; queries that do see it add its share to O by hand.
+//
+// Work items (row, 256 or 128 queries, kv-head), the longest of a row first, go round the CTAs.  When
+// there are too few to fill the GPU, the cache of each is cut into up to 16 pieces whose (m, l, o) meet
+// in a second launch, in order.
+#include <algorithm>
+
+#include "gdn_tma.cuh"
+
+namespace gdn {
+
+namespace {
+
+constexpr int kSms = 152;
+constexpr int kTN = 128;        // cached tokens of a tile
+constexpr int kMaxPieces = 16;
+constexpr float kGrow = 8.f;    // log2 of how far weights may outgrow their reference
+
+template <int D>
+struct Cfg {
+  static constexpr int kTiles = D <= 128 ? 2 : 1;                    // query tiles of a CTA
+  static constexpr int kRows = 128 * kTiles;
+  static constexpr int kThreads = 128 * (kTiles + 1);
+  static constexpr uint32_t kQ = 128 * D * 2;                        // bytes of a query tile
+  static constexpr uint32_t kKv = kTN * D * 2;                       // bytes of a K or V tile
+  static constexpr int kFit = (int)((232448 - 2048 - kTiles * kQ) / kKv);
+  static constexpr int kRing = kFit < 8 ? kFit : 8;                  // K and V tiles in turn
+  static constexpr uint32_t kSmem = kTiles * kQ + kRing * kKv;
+  static constexpr int kO = 256;                                     // first O column of TMEM; S at 0 and 128
+  static_assert(kRing >= 2, "ring too short");
+};
+
+struct PromptParams {
+  AttnLaunch a;
+  int max_pieces;  // of an item
+  float* part;     // [kSms][kRows][D]
+  float* stats;    // [kSms][kRows][2]
+  uint64_t wait_ns;
+};
+
+struct Item {
+  KvRow r;
+  int q0;      // first (token, q-head) pair
+  int h;
+  int sink_tiles, first_tile, tiles;  // of its cached tokens, all pieces
+  int j0, j1;  // this piece
+  int low;     // first position that some query sees behind the sinks
+  int last;    // position of its last query
+};
+
+__device__ __forceinline__ int tile_at(const Item& w, int j) {
+  return (j < w.sink_tiles ? j : w.first_tile + j - w.sink_tiles) * kTN;
+}
+
+// Items of row n: its query tiles times kv-heads.
+template <int ROWS>
+__device__ __forceinline__ int64_t items_of(const AttnLaunch& p, int n, uint32_t* st, KvRow& r) {
+  if (n >= p.rows.num_seqs || !load_kv_row(p.rows, p.cache, n, r, st)) return 0;
+  return ((int64_t)r.len * p.G + ROWS - 1) / ROWS * p.cache.Hkv;
+}
+
+// Finds items in increasing order; a warp holds 32 rows, one per lane.  All lanes call together.
+template <int ROWS>
+struct Finder {
+  const AttnLaunch& p;
+  int base = 0;
+  int64_t before = 0;  // items of the rows before base
+  int64_t mine = 0;    // items of row base + lane
+  KvRow row;
+  __device__ explicit Finder(const AttnLaunch& launch) : p(launch) { load(); }
+  __device__ void load() { mine = items_of<ROWS>(p, base + (int)(threadIdx.x & 31), nullptr, row); }
+  __device__ bool find(int64_t idx, int pieces, Item& w) {
+    const int lane = threadIdx.x & 31;
+    const int64_t item = idx / pieces;
+    const int piece = (int)(idx - item * pieces);
+    while (true) {
+      int64_t inc = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += v;
+      }
+      const unsigned hit = __ballot_sync(0xffffffffu, item >= before + inc - mine && item < before + inc);
+      if (hit) {
+        const int src = __ffs(hit) - 1;
+        const int64_t at = item - before - __shfl_sync(0xffffffffu, inc - mine, src);
+        w.r.bos = __shfl_sync(0xffffffffu, row.bos, src);
+        w.r.len = __shfl_sync(0xffffffffu, row.len, src);
+        w.r.kv = __shfl_sync(0xffffffffu, row.kv, src);
+        w.r.trow = __shfl_sync(0xffffffffu, row.trow, src);
+        const int blocks = (int)(((int64_t)w.r.len * p.G + ROWS - 1) / ROWS);
+        w.h = (int)(at % p.cache.Hkv);
+        w.q0 = (blocks - 1 - (int)(at / p.cache.Hkv)) * ROWS;  // the longest first
+        const int pmin = w.r.kv - w.r.len + w.q0 / p.G;
+        w.last = min(w.r.kv - w.r.len + (w.q0 + ROWS - 1) / p.G, w.r.kv - 1);
+        w.low = p.window > 0 ? max(0, pmin - p.window + 1) : 0;
+        w.sink_tiles = (min(p.sinks, w.low) + kTN - 1) / kTN;
+        w.first_tile = max(w.low / kTN, w.sink_tiles);
+        w.tiles = w.sink_tiles + w.last / kTN + 1 - w.first_tile;
+        w.j0 = (int)((int64_t)w.tiles * piece / pieces);
+        w.j1 = (int)((int64_t)w.tiles * (piece + 1) / pieces);
+        return true;
+      }
+      before += __shfl_sync(0xffffffffu, inc, 31);
+      base += 32;
+      if (base >= p.rows.num_seqs) return false;
+      load();
+    }
+  }
+};
+
+// Some of queries [pmin, pmax] does not see some token of [b, b + kTN).
+__device__ __forceinline__ bool in_part(const AttnLaunch& p, int b, int pmin, int pmax) {
+  return b + kTN - 1 > pmin || (p.window > 0 && b <= pmax - p.window && b + kTN - 1 >= p.sinks);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float pack2f(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return __uint_as_float(r);
+}
+__device__ __forceinline__ bool not_finite2(uint32_t x) {
+  return (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u;
+}
+// D (TMEM) += A (TMEM) B: A's row m is lane m, two bf16 of K per column.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate));
+}
+
+// Items of all rows; sum: one value per warp.  All threads call.
+template <int ROWS, int THREADS>
+__device__ int64_t count_items(const AttnLaunch& p, int64_t* sum) {
+  int64_t mine = 0;
+  for (int n = threadIdx.x; n < p.rows.num_seqs; n += THREADS) {
+    KvRow r;
+    mine += items_of<ROWS>(p, n, blockIdx.x == 0 ? p.status : nullptr, r);
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+  if ((threadIdx.x & 31) == 0) sum[threadIdx.x >> 5] = mine;
+  tc::fence_before();  // (orders the TMEM allocation too)
+  __syncthreads();
+  tc::fence_after();
+  int64_t items = 0;
+#pragma unroll
+  for (int i = 0; i < THREADS / 32; ++i) items += sum[i];
+  return items;
+}
+__device__ __forceinline__ int pieces_of(int64_t items, int most) {
+  return items == 0 ? 1 : (int)min((int64_t)most, max((int64_t)1, (int64_t)kSms / items));
+}
+
+// Adds the listed tokens' share to O where the query sees them: their weights from S, their values from the
+// cache.  O is complete; the warp's lanes go together, as TMEM loads and stores need them all.
+template <int D, typename Sees>
+__device__ __forceinline__ void add_listed(const PromptParams& P, const Item& w, const uint32_t* bad, int b, uint32_t s_col,
+                                        uint32_t o_col, float sl2, float ms, Sees sees) {
+  const KvDev& kv = P.a.cache;
+#pragma unroll 1
+  for (int t = 0; t < kTN; ++t) {
+    if (!(bad[t >> 5] >> (t & 31) & 1u)) continue;
+    float x[8], s = 0.f;
+    tc::tmem_ld8(s_col + (t & ~7), x);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if ((t & 7) == i) s = x[i];
+    const bool seen = sees(t);
+    const float weight = ex2(fmaf(s, sl2, ms));
+    const int tok = b + t;  // below the row's end, in a page that is not NULL
+    const int page = kv.table[(int64_t)w.r.trow * kv.max_pages + tok / kv.page_size];
+    const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(kv.v) + (int64_t)page * kv.page_stride +
+                             ((int64_t)w.h * kv.page_size + tok % kv.page_size) * D;
+#pragma unroll 1
+    for (int c = 0; c < D; c += 32) {
+      float o[32];
+      tc::tmem_ld32(o_col + c, o);
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (seen) o[i] += weight * __bfloat162float(v[c + i]);
+      tc::tmem_st32(o_col + c, o);
+    }
+    tc::tmem_st_wait();
+  }
+}
+
+template <int D>
+struct Small {
+  uint64_t full[Cfg<D>::kRing], empty[Cfg<D>::kRing], checked[Cfg<D>::kRing];
+  uint64_t q_ready, s_ready[2], p_ready[2], pv_done[2], drain;
+  int64_t sum[Cfg<D>::kThreads / 32];
+  uint32_t bad[Cfg<D>::kRing][4];  // listed tokens of a V tile
+  uint32_t held[16];               // per tile, counted over all items, % 16: which of its pages hold tokens
+  uint32_t tmem;
+};
+
+template <int D>
+__global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
+    prompt_kernel(PromptParams P, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+  using C = Cfg<D>;
+  constexpr int NT = C::kTiles, R = C::kRing, CB = D / 64;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t* ring = smem + NT * C::kQ;
+  Small<D>& sm = *reinterpret_cast<Small<D>*>(ring + R * C::kKv);
+  const AttnLaunch& p = P.a;
+  const KvDev& kv = p.cache;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (tid == 0) {
+    for (int i = 0; i < R; ++i) {
+      tc::mbar_init(&sm.full[i], 1);
+      tc::mbar_init(&sm.empty[i], 3);  // the products and both warps that look after V tiles
+      tc::mbar_init(&sm.checked[i], 2);
+    }
+    tc::mbar_init(&sm.q_ready, 128 * NT);
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&sm.s_ready[i], 1);
+      tc::mbar_init(&sm.p_ready[i], 128);
+      tc::mbar_init(&sm.pv_done[i], 1);
+    }
+    tc::mbar_init(&sm.drain, 1);
+    tc::mbar_init_fence();
+    tc::prefetch_map(&kmap);
+    tc::prefetch_map(&vmap);
+  }
+  if (warp == 4 * NT) tc::tmem_alloc(&sm.tmem, 512);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // how many items there are, and into how many pieces each is cut
+  int64_t items = count_items<C::kRows, C::kThreads>(p, sm.sum);
+  const int pieces = pieces_of(items, P.max_pieces);
+  items *= pieces;
+  const uint32_t tmem = sm.tmem;
+  const int ps = kv.page_size, shift = __ffs(ps) - 1, box = min(ps, kTN), boxes = kTN / box;
+  const int bshift = __ffs(box) - 1;
+
+  Finder<C::kRows> finder(p);
+  Item w;
+  bool ok = true;
+  uint32_t at = 0;     // K and V tiles gone by; a K tile is entry at % R of the ring, its V tile the next
+  uint32_t tiles = 0;  // cached tiles gone by
+  const int role = warp - 4 * NT;  // < 0: softmax
+
+  if (role < 0) {
+    // ---- softmax: a thread per query ----
+    const int tile = warp >> 2, row = tid & 127;
+    const float sl2 = p.scale * 1.4426950408889634f;
+    uint8_t* qt = smem + tile * C::kQ;
+    const uint32_t lane_base = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+    const uint32_t o_col = lane_base + C::kO + tile * D;
+    uint32_t s_n[2] = {0, 0};  // score tiles of a slot gone by
+    uint32_t pv_n = 0;         // products of the query tile gone by
+    uint32_t chk = 0;          // parity of checked[entry]
+    for (int64_t idx = blockIdx.x; idx < items && ok; idx += kSms) {
+      if (!finder.find(idx, pieces, w)) break;
+      const int qi = w.q0 + tile * 128 + row, nq = w.r.len * p.G;
+      int g = -1;
+      if (qi < nq) g = global_token(RowsDev{nullptr, p.rows.tok}, w.r.bos + qi / p.G, p.num_global, p.status);
+      const int64_t head = (int64_t)(w.h * p.G + (qi < nq ? qi % p.G : 0)) * D;
+      {
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
+                                                          (int64_t)max(g, 0) * p.q_stride + head);
+#pragma unroll 8
+        for (int c = 0; c < D / 8; ++c) {
+          const uint4 v = g >= 0 ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(qt + (c >> 3) * 16384 + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = v;
+        }
+      }
+      tc::fence_async_smem();
+      tc::fence_before();  // (the O of the item before has been read)
+      tc::mbar_arrive(&sm.q_ready);
+      const int first = w.r.kv - w.r.len;  // position of the first new token
+      const int pos = min(first + qi / p.G, w.r.kv - 1);
+      const int tmin = first + min(w.q0 + tile * 128, nq - 1) / p.G, cmin = first + w.q0 / p.G;
+      const int tmax = min(first + (w.q0 + tile * 128 + 127) / p.G, w.r.kv - 1);
+      float m = -INFINITY, l = 0.f;  // the maximum that the weights refer to (of scores before their scale); their sum
+      bool wrote = false;            // O holds something
+      for (int j = w.j0; j < w.j1; ++j, at += 2, ++tiles) {
+        const int slot = NT == 2 ? tile : (j - w.j0) & 1;
+        const uint32_t s_col = lane_base + slot * 128, v_entry = (at + 1) % R;
+        const int b = tile_at(w, j);
+        ok = __all_sync(0xffffffffu, ok && tc::mbar_wait(&sm.s_ready[slot], s_n[slot] & 1, P.wait_ns));
+        ++s_n[slot];
+        if (!ok) break;
+        tc::fence_after();
+        const uint32_t have = sm.held[tiles & 15];
+        const bool all_pages = have == (1u << boxes) - 1u;
+        const bool part = !all_pages || in_part(p, b, tmin, tmax);
+        auto sees = [&](int c) {
+          const int tok = b + c;
+          return tok <= pos && (p.window <= 0 || tok > pos - p.window || tok < p.sinks) &&
+                 (all_pages || (have >> (c >> bshift) & 1u));
+        };
+        float mx = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 128; c += 64) {
+          float x[32], y[32];
+          tc::tmem_ld32x2(s_col + c, x, s_col + c + 32, y);
+          if (part) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              if (!sees(c + i)) x[i] = -INFINITY;
+              if (!sees(c + 32 + i)) y[i] = -INFINITY;
+            }
+          }
+          float m4[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int i = 0; i < 32; i += 4)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) m4[e] = fmaxf(m4[e], fmaxf(x[i + e], y[i + e]));
+          mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+        }
+        bool any_bad = false;  // the tile lists tokens
+        if (in_part(p, b, cmin, w.last)) {
+          ok = __all_sync(0xffffffffu, ok && tc::mbar_wait(&sm.checked[v_entry], (chk >> v_entry) & 1, P.wait_ns));
+          chk ^= 1u << v_entry;
+          if (!ok) break;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) any_bad |= sm.bad[v_entry][i] != 0;
+        }
+        const bool grow = mx > m && (m == -INFINITY || (mx - m) * sl2 > kGrow);
+        const bool rescale = wrote && __any_sync(0xffffffffu, grow);
+        const float f = grow && m != -INFINITY ? ex2((m - mx) * sl2) : 1.f;
+        if (grow) m = mx;
+        l *= f;
+        const float ms = m == -INFINITY ? 0.f : -m * sl2;
+        if (rescale || any_bad) {
+          if (wrote) {  // O is complete when the product of the tile before is
+            ok = __all_sync(0xffffffffu,
+                            ok && tc::mbar_wait(&sm.pv_done[tile], (pv_n - 1) & 1, P.wait_ns));
+            if (!ok) break;
+            tc::fence_after();
+          }
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            float o[32];
+            if (wrote) tc::tmem_ld32(o_col + c, o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = wrote ? o[i] * f : 0.f;
+            tc::tmem_st32(o_col + c, o);
+          }
+          tc::tmem_st_wait();
+          if (any_bad) add_listed<D>(P, w, sm.bad[v_entry], b, s_col, o_col, sl2, ms, sees);
+        }
+        // P over S, 64 tokens at a time: their 32 columns have been read
+        float l4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < 128; c += 64) {
+          float x[32], y[32];
+          tc::tmem_ld32x2(s_col + c, x, s_col + c + 32, y);
+          if (part) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              if (!sees(c + i)) x[i] = -INFINITY;
+              if (!sees(c + 32 + i)) y[i] = -INFINITY;
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            x[i] = ex2(fmaf(x[i], sl2, ms));
+            y[i] = ex2(fmaf(y[i], sl2, ms));
+          }
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            l4[0] += x[i];
+            l4[1] += x[i + 1];
+            l4[2] += y[i];
+            l4[3] += y[i + 1];
+          }
+          float u[32];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            u[i] = pack2f(x[2 * i], x[2 * i + 1]);
+            u[16 + i] = pack2f(y[2 * i], y[2 * i + 1]);
+          }
+          tc::tmem_st32(s_col + c / 2, u);
+        }
+        l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+        tc::tmem_st_wait();
+        if (NT == 1 && wrote) {
+          // The product of the tile before: the next one begins only after this, so that no phase of
+          // pv_done is taken for another.  (With two query tiles these scores came behind it.)
+          ok = __all_sync(0xffffffffu, ok && tc::mbar_wait(&sm.pv_done[tile], (pv_n - 1) & 1, P.wait_ns));
+          if (!ok) break;
+        }
+        tc::fence_before();
+        tc::mbar_arrive(&sm.p_ready[slot]);
+        ++pv_n;
+        wrote = true;
+      }
+      if (!ok) break;
+      if (wrote) {
+        ok = __all_sync(0xffffffffu, ok && tc::mbar_wait(&sm.pv_done[tile], (pv_n - 1) & 1, P.wait_ns));
+        if (!ok) break;
+        tc::fence_after();
+      }
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const int64_t part_row = (int64_t)blockIdx.x * C::kRows + tile * 128 + row;
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + (int64_t)max(g, 0) * p.out_stride + head;
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        float o[32];
+        if (wrote) {
+          tc::tmem_ld32(o_col + c, o);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = 0.f;
+        }
+        if (pieces > 1) {
+          float4* dst = reinterpret_cast<float4*>(P.part + part_row * D + c);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        } else if (g >= 0) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] *= inv;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(out + c + 8 * i) = tc::pack8(o + 8 * i);
+        }
+      }
+      if (pieces > 1) *reinterpret_cast<float2*>(P.stats + part_row * 2) = make_float2(m, l);
+    }
+    if (!ok) set_status(p.status, GDN_STATUS_WAIT_TIMEOUT);
+  } else if (role == 0) {
+    // ---- products: one lane issues them all ----
+    constexpr uint32_t kS = tc::idesc_bf16(128, kTN), kPv = tc::idesc_bf16_bmn(128, D);
+    uint32_t p_n[2] = {0, 0}, chk = 0, items_n = 0;
+    auto issue_s = [&](int tile, int slot, uint32_t k_at) {
+      const uint32_t q = tc::smem_addr(smem + tile * C::kQ), k = tc::smem_addr(ring + (k_at % R) * C::kKv);
+      if (lane == 0) {
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s) {
+          const uint32_t off = (s >> 2) * 16384 + (s & 3) * 32;
+          tc::mma(tmem + slot * 128, tc::sdesc(q + off, 1024), tc::sdesc(k + off, 1024), kS, s > 0);
+        }
+        tc::commit(&sm.s_ready[slot]);
+      }
+      __syncwarp();
+    };
+    auto issue_pv = [&](int tile, int slot, uint32_t v_at, bool onto) {
+      const uint32_t v = tc::smem_addr(ring + (v_at % R) * C::kKv);
+      if (lane == 0) {
+#pragma unroll
+        for (int s = 0; s < kTN / 16; ++s)
+          mma_ts(tmem + C::kO + tile * D, tmem + slot * 128 + s * 8, tc::sdesc_lbo(v + s * 2048, 16384, 1024), kPv,
+                 onto || s > 0);
+        tc::commit(&sm.pv_done[tile]);
+      }
+      __syncwarp();
+    };
+    auto release = [&](uint32_t which) {
+      if (lane == 0) tc::commit(&sm.empty[which % R]);
+      __syncwarp();
+    };
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      ok = __all_sync(0xffffffffu, ok && tc::mbar_wait(bar, parity & 1, P.wait_ns));
+      if (ok) tc::fence_after();
+      return ok;
+    };
+    for (int64_t idx = blockIdx.x; idx < items && ok; idx += kSms, ++items_n) {
+      if (!finder.find(idx, pieces, w)) break;
+      if (!wait(&sm.q_ready, items_n)) break;
+      const int n = w.j1 - w.j0;
+      if (n == 0) continue;
+      const int cmin = w.r.kv - w.r.len + w.q0 / p.G;
+      if (!wait(&sm.full[at % R], at / R)) break;
+      for (int i = 0; i < NT; ++i) issue_s(i, i, at);
+      release(at);
+      for (int j = 0; j < n && ok; ++j, at += 2) {
+        const uint32_t v_at = at + 1, k_next = at + 2;
+        const bool checked = in_part(p, tile_at(w, w.j0 + j), cmin, w.last);
+        if (NT == 1 && j + 1 < n) {  // the next scores run under this tile's softmax
+          if (!wait(&sm.full[k_next % R], k_next / R)) break;
+          issue_s(0, (j + 1) & 1, k_next);
+          release(k_next);
+        }
+        bool onto = j > 0;
+        for (int i = 0; i < NT && ok; ++i) {
+          const int slot = NT == 2 ? i : j & 1;
+          if (!wait(&sm.p_ready[slot], p_n[slot]++)) break;
+          if (i == 0) {
+            if (!wait(&sm.full[v_at % R], v_at / R)) break;
+            if (checked) {
+              if (!wait(&sm.checked[v_at % R], chk >> (v_at % R))) break;
+              chk ^= 1u << (v_at % R);
+              for (int e = 0; e < 4; ++e) onto |= sm.bad[v_at % R][e] != 0;  // the softmax has begun O
+            }
+          }
+          issue_pv(i, slot, v_at, onto);
+          if (i == NT - 1) release(v_at);
+          if (NT == 2 && j + 1 < n) {
+            if (i == 0 && !wait(&sm.full[k_next % R], k_next / R)) break;
+            issue_s(i, i, k_next);
+            if (i == NT - 1) release(k_next);
+          }
+        }
+      }
+    }
+    if (lane == 0) tc::commit(&sm.drain);
+    __syncwarp();
+    if (!tc::mbar_wait(&sm.drain, 0, P.wait_ns)) ok = false;
+    if (!ok) set_status(p.status, GDN_STATUS_WAIT_TIMEOUT);
+  } else if (role == 1) {
+    // ---- fetches: lane = (page of the tile, 64-column block) ----
+    const int bi = lane / CB, cb = lane % CB;
+    const bool active = bi < boxes;
+    for (int64_t idx = blockIdx.x; idx < items && ok; idx += kSms) {
+      if (!finder.find(idx, pieces, w)) break;
+      const int32_t* row = kv.table + (int64_t)w.r.trow * kv.max_pages;
+      const int entries = (w.r.kv + ps - 1) >> shift;
+      int eb = -64, ids = 0, ahead = 0;  // 32 table entries are held, one per lane, and the 32 behind them
+      for (int j = w.j0; j < w.j1 && ok; ++j, at += 2, ++tiles) {
+        const int pos = tile_at(w, j) + bi * box, e = tile_at(w, j) >> shift;
+        if (e >= eb + 32) {
+          if (e < eb + 64) {
+            ids = ahead;
+            eb += 32;
+          } else {
+            eb = e;
+            ids = eb + lane < entries ? __ldg(row + eb + lane) : 0;
+          }
+          ahead = eb + 32 + lane < entries ? __ldg(row + eb + 32 + lane) : 0;
+        }
+        int page = __shfl_sync(0xffffffffu, ids, active ? (pos >> shift) - eb : 0);
+        page = active && pos < w.r.kv ? page_or_null(page, kv, p.status) : 0;
+        const uint32_t have = __ballot_sync(0xffffffffu, page > 0 && cb == 0);
+        uint32_t mask = 0;
+        for (int i = 0; i < boxes; ++i) mask |= (have >> (i * CB) & 1u) << i;
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          const uint32_t a = at + v, en = a % R;
+          ok = __all_sync(0xffffffffu, a < R || tc::mbar_wait(&sm.empty[en], (a / R - 1) & 1, P.wait_ns));
+          if (!ok) break;
+          if (lane == 0) {
+            if (v == 0) sm.held[tiles & 15] = mask;
+            tc::expect_tx(&sm.full[en], C::kKv);
+          }
+          __syncwarp();
+          if (active)
+            tc::tma_page(ring + en * C::kKv + cb * 16384 + bi * box * 128, v ? &vmap : &kmap, cb * 64, pos & (ps - 1), w.h,
+                         page > 0 ? page : kv.num_pages, &sm.full[en]);
+        }
+        if (!ok) break;
+      }
+    }
+    // No copy may be in flight when the CTA ends (the products wait for every tile, so this passes at
+    // once unless a wait gave up).
+    for (uint32_t a = at > (uint32_t)R ? at - R : 0; a < at; ++a) ok &= tc::mbar_wait(&sm.full[a % R], (a / R) & 1, P.wait_ns);
+    if (!ok) set_status(p.status, GDN_STATUS_WAIT_TIMEOUT);
+  } else {
+    // ---- V tiles that some query sees in part: 64 tokens of each ----
+    // (these warps go through every phase of the ring, so that none is taken for another)
+    for (int64_t idx = blockIdx.x; idx < items && ok; idx += kSms) {
+      if (!finder.find(idx, pieces, w)) break;
+      const int cmin = w.r.kv - w.r.len + w.q0 / p.G;
+      for (int j = w.j0; j < w.j1; ++j, at += 2) {
+        const int b = tile_at(w, j);
+        const uint32_t en = (at + 1) % R;
+        ok = __all_sync(0xffffffffu, ok && tc::mbar_wait(&sm.full[at % R], (at / R) & 1, P.wait_ns));
+        if (!ok) break;
+        if (lane == 0) tc::mbar_arrive(&sm.empty[at % R]);
+        ok = __all_sync(0xffffffffu, ok && tc::mbar_wait(&sm.full[en], ((at + 1) / R) & 1, P.wait_ns));
+        if (!ok) break;
+        if (!in_part(p, b, cmin, w.last)) {
+          if (lane == 0) tc::mbar_arrive(&sm.empty[en]);
+          continue;
+        }
+#pragma unroll 1
+        for (int u = 0; u < 2; ++u) {
+          const int t = (role - 2) * 64 + u * 32 + lane;
+          uint8_t* v = ring + en * C::kKv + t * 128;
+          bool odd = false;
+          const bool past = b + t >= w.r.kv;
+#pragma unroll 8
+          for (int c = 0; c < D / 8; ++c) {
+            const uint4 x = *reinterpret_cast<const uint4*>(v + (c >> 3) * 16384 + (((c & 7) ^ (t & 7)) << 4));
+            odd |= not_finite2(x.x) || not_finite2(x.y) || not_finite2(x.z) || not_finite2(x.w);
+          }
+          if (past || odd)
+            for (int c = 0; c < D / 8; ++c)
+              *reinterpret_cast<uint4*>(v + (c >> 3) * 16384 + (((c & 7) ^ (t & 7)) << 4)) = make_uint4(0, 0, 0, 0);
+          const uint32_t list = __ballot_sync(0xffffffffu, odd && !past);
+          if (lane == 0) sm.bad[en][(role - 2) * 2 + u] = list;
+        }
+        tc::fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tc::mbar_arrive(&sm.checked[en]);
+          tc::mbar_arrive(&sm.empty[en]);
+        }
+      }
+    }
+    if (!ok) set_status(p.status, GDN_STATUS_WAIT_TIMEOUT);
+  }
+  tc::fence_before();
+  __syncthreads();
+  if (role == 0) {
+    tc::fence_after();
+    tc::tmem_dealloc(tmem, 512);
+  }
+}
+
+// Adds the pieces of an item's queries in order: a warp per query, kJoinRows queries per block.
+constexpr int kJoinRows = 32;
+template <int D>
+__global__ void __launch_bounds__(256) prompt_join_kernel(PromptParams P) {
+  constexpr int kRows = Cfg<D>::kRows, E = D / 32;
+  __shared__ int64_t sum[8];
+  const AttnLaunch& p = P.a;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int64_t items = count_items<kRows, 256>(p, sum);
+  const int pieces = pieces_of(items, P.max_pieces);
+  if (pieces == 1 || (int64_t)blockIdx.x >= items) return;
+  Finder<kRows> finder(p);
+  Item w;
+  if (!finder.find((int64_t)blockIdx.x * pieces, pieces, w)) return;
+  const float sl2 = p.scale * 1.4426950408889634f;
+  const int lane = threadIdx.x & 31;
+  for (int r = blockIdx.y * kJoinRows + (threadIdx.x >> 5); r < (int)(blockIdx.y + 1) * kJoinRows; r += 8) {
+    const int qi = w.q0 + r;
+    if (qi >= w.r.len * p.G) break;
+    float m = -INFINITY, l = 0.f, o[E];
+#pragma unroll
+    for (int i = 0; i < E; ++i) o[i] = 0.f;
+    // lane s holds piece s's (m, l)
+    const int64_t row0 = (int64_t)blockIdx.x * pieces * kRows + r;
+    const float2 st = lane < pieces ? *reinterpret_cast<const float2*>(P.stats + (row0 + (int64_t)lane * kRows) * 2)
+                                    : make_float2(-INFINITY, 0.f);
+    m = st.x;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    const float f = st.x == -INFINITY ? 0.f : ex2((st.x - m) * sl2);
+    for (int s = 0; s < pieces; ++s) {
+      const float fs = __shfl_sync(0xffffffffu, f, s), ls = __shfl_sync(0xffffffffu, st.y, s);
+      const float ms = __shfl_sync(0xffffffffu, st.x, s);
+      l += ls * fs;
+      if (ms == -INFINITY) continue;
+#pragma unroll
+      for (int i = 0; i < E; ++i) o[i] += P.part[(row0 + (int64_t)s * kRows) * D + lane + 32 * i] * fs;
+    }
+    const int t = qi / p.G;
+    const int g = p.rows.tok ? __ldg(p.rows.tok + w.r.bos + t) : w.r.bos + t;
+    if (g < 0 || g >= p.num_global) continue;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    __nv_bfloat16* out =
+        static_cast<__nv_bfloat16*>(p.out) + (int64_t)g * p.out_stride + (int64_t)(w.h * p.G + qi - t * p.G) * D;
+#pragma unroll
+    for (int i = 0; i < E; ++i) out[lane + 32 * i] = __float2bfloat16_rn(o[i] * inv);
+  }
+}
+
+// At least how many items there are when every row is good.
+int64_t least_items(const AttnLaunch& a, int rows) {
+  return ((int64_t)a.rows.num_tokens * a.G + rows - 1) / rows * a.cache.Hkv;
+}
+int max_pieces(const AttnLaunch& a, int rows) {
+  return (int)std::max<int64_t>(1, std::min<int64_t>(kMaxPieces, kSms / std::max<int64_t>(1, least_items(a, rows))));
+}
+
+template <int D>
+cudaError_t launch_d(const AttnLaunch& a, cudaStream_t s) {
+  using C = Cfg<D>;
+  static std::atomic<uint64_t> done{0};
+  constexpr int smem = (int)(C::kSmem + sizeof(Small<D>));
+  static_assert(smem <= 232448, "shared memory");
+  cudaError_t e = once_per_device(done, [&] {
+    return cudaFuncSetAttribute(prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  });
+  if (e != cudaSuccess) return e;
+  CUtensorMap kmap, vmap;
+  if (!encode_pool_maps(a.cache, a.cache.page_size < kTN ? a.cache.page_size : kTN, &kmap, &vmap))
+    return cudaErrorInvalidValue;
+  PromptParams P{};
+  P.a = a;
+  P.max_pieces = max_pieces(a, C::kRows);
+  P.stats = static_cast<float*>(a.ws);
+  P.part = P.stats + (size_t)2 * kSms * C::kRows;
+  P.wait_ns = kDefaultWaitNs;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kSms);
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if ((e = cudaLaunchKernelEx(&cfg, prompt_kernel<D>, P, kmap, vmap)) != cudaSuccess || P.max_pieces == 1) return e;
+  cfg.gridDim = dim3(kSms / 2, C::kRows / kJoinRows);
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, prompt_join_kernel<D>, P);
+}
+
+}  // namespace
+
+bool attn_prompt_supported(const AttnLaunch& a, gdn_dtype dtype) {
+  const int d = a.cache.d;
+  return dtype == GDN_BF16 && (d == 64 || d == 128 || d == 256);
+}
+
+size_t attn_prompt_workspace(const AttnLaunch& a) {
+  const int d = a.cache.d, rows = d <= 128 ? 256 : 128;
+  return max_pieces(a, rows) == 1 ? 0 : (size_t)kSms * rows * (d + 2) * 4;
+}
+
+cudaError_t launch_attn_prompt(const AttnLaunch& a, cudaStream_t s) {
+  return a.cache.d == 64 ? launch_d<64>(a, s) : a.cache.d == 128 ? launch_d<128>(a, s) : launch_d<256>(a, s);
+}
+
+}  // namespace gdn

@@ -133,6 +133,10 @@ cudaError_t launch_copy_items(const CopyLaunch& p, cudaStream_t s);
 bool attn_split_supported(const AttnLaunch& p, gdn_dtype dtype);
 size_t attn_split_workspace(const AttnLaunch& p);
 cudaError_t launch_attn_split(const AttnLaunch& p, cudaStream_t s);
+// Longer rows of the same layouts: prompts, on tcgen05.
+bool attn_prompt_supported(const AttnLaunch& p, gdn_dtype dtype);
+size_t attn_prompt_workspace(const AttnLaunch& p);
+cudaError_t launch_attn_prompt(const AttnLaunch& p, cudaStream_t s);
 // Every other layout.
 cudaError_t launch_attn_scalar(const AttnLaunch& p, gdn_dtype dtype, cudaStream_t s);
 

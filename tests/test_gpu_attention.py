@@ -258,6 +258,14 @@ def test_prompt_windows(window, sinks, dim):
          seed=window + dim).check()
 
 
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("window", [0, 333])
+def test_prompts_that_fill_the_gpu(dim, window):
+    # 88 work items or more: none is cut into pieces, CTAs take several
+    Step([(700, 700), (1, 9), (641, 1100), (130, 130)], heads=16, kv_heads=16, dim=dim, page=64, window=window, sinks=2,
+         seed=dim).check()
+
+
 def test_prompt_in_32_bits():
     Step([(200, 230), (90, 90)], heads=4, kv_heads=2, dim=64, dtype=F32, seed=20).check()
     Step([(200, 230), (90, 90)], heads=4, kv_heads=2, dim=48, seed=21).check()
