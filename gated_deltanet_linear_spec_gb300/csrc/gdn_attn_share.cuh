@@ -1,0 +1,281 @@
+// gdn_attn_share.cuh -- rows split over the cache's length: who works on what, and how pieces meet.
+//
+// A unit is one (row, kv-head), or one group of a row's queries of a kv-head: the 32-token tiles that
+// its queries see, window and first tokens included.  All units' tiles laid end to end are dealt out
+// evenly to the workers.  A share's piece of a unit that is not the whole unit leaves (m, l, o) in the
+// workspace; join_kernel adds a unit's pieces in the order of the workers.
+#pragma once
+
+#include "gdn_kv.cuh"
+#include "gdn_tc.cuh"
+
+namespace gdn {
+namespace split {
+
+constexpr int kSms = 152;
+constexpr int kTN = 32;       // tokens of a tile
+constexpr int kJoinWarps = 8;
+constexpr int kJoinRows = 8;  // blocks that share the queries of a unit
+
+struct SplitParams {
+  AttnLaunch a;
+  float* part;     // [2 * workers][queries of a unit][D]
+  float* stats;    // [2 * workers][queries of a unit][2]: m (of the scores before their scale), l
+  int32_t* info;   // [workers][8]: the unit that begins in a worker's share and ends in another's
+  uint64_t wait_ns;
+};
+
+struct Unit {
+  KvRow r;
+  int sink_tiles, first_tile, tiles;
+  int per;  // units of the row
+};
+
+// A row's values as they lie in memory.
+struct RawRow {
+  int bos, eos, kv, trow;
+};
+__device__ __forceinline__ RawRow raw_row(const AttnLaunch& p, int n) {
+  return RawRow{__ldg(p.rows.qsl + n), __ldg(p.rows.qsl + n + 1), __ldg(p.rows.kv_lens + n),
+                p.rows.table_rows ? __ldg(p.rows.table_rows + n) : n};
+}
+
+// The tiles that the row's queries see; 0 for an empty or bad row.  QG: queries of a unit, 0 for all
+// of a row and kv-head.
+template <int QG>
+__device__ __forceinline__ Unit unit_of(const AttnLaunch& p, const RawRow& r, uint32_t* st) {
+  Unit u;
+  u.tiles = u.sink_tiles = u.first_tile = 0;
+  u.per = p.cache.Hkv;
+  if (!check_kv_row(p.rows, p.cache, r.bos, r.eos, r.kv, r.trow, u.r, st) || u.r.len == 0) return u;
+  const int low = p.window > 0 ? max(0, u.r.kv - u.r.len - p.window + 1) : 0;
+  u.sink_tiles = (min(p.sinks, low) + kTN - 1) / kTN;
+  u.first_tile = max(low / kTN, u.sink_tiles);
+  u.tiles = u.sink_tiles + (u.r.kv + kTN - 1) / kTN - u.first_tile;
+  if (QG > 0) u.per *= (u.r.len * p.G + QG - 1) / (QG > 0 ? QG : 1);
+  return u;
+}
+// Tiles of all units of row n.
+template <int QG>
+__device__ __forceinline__ int64_t row_tiles(const AttnLaunch& p, int n, uint32_t* st) {
+  const Unit u = unit_of<QG>(p, raw_row(p, n), st);
+  return (int64_t)u.tiles * u.per;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// The tiles dealt to the workers: the first `more` get each + 1, the others each.
+struct Deal {
+  int64_t each;
+  int more;
+  __device__ int64_t first(int worker) const { return each * worker + min(worker, more); }
+  __device__ int owner(int64_t tile) const;
+};
+
+// 64-bit quotient; in 32 bits where that does.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+__device__ __forceinline__ int Deal::owner(int64_t tile) const {
+  const int64_t head = (each + 1) * more;
+  return (int)(tile < head ? quotient(tile, each + 1) : more + quotient(tile - head, each));
+}
+
+// A worker's share of the tiles, and where it begins.
+struct Share {
+  int64_t first, last;
+  int64_t into;  // tiles of row `row` before the share
+  int row;
+  RawRow raw;    // that row
+};
+
+// The shares of the CTA's workers; part: one value per warp.  All threads call.
+template <int QG, int NW, int THREADS>
+__device__ void find_shares(const AttnLaunch& p, int64_t* part, Deal& deal, Share* shares) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (p.rows.num_seqs + THREADS - 1) / THREADS;
+  const int n0 = min(tid * per, p.rows.num_seqs), n1 = min(n0 + per, p.rows.num_seqs);
+  int64_t mine = 0;
+  for (int n = n0; n < n1; ++n) mine += row_tiles<QG>(p, n, blockIdx.x == 0 ? p.status : nullptr);
+  int64_t inc = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += v;
+  }
+  if (lane == 31) part[warp] = inc;
+  __syncthreads();
+  int64_t before = inc - mine, total = 0;
+#pragma unroll
+  for (int i = 0; i < THREADS / 32; ++i) {
+    if (i < warp) before += part[i];
+    total += part[i];
+  }
+  Deal d;
+  const int workers = gridDim.x * NW;
+  d.each = quotient(total, workers);
+  d.more = (int)(total - d.each * workers);
+  if (tid == 0) deal = d;
+#pragma unroll 1
+  for (int w = 0; w < NW; ++w) {
+    Share s;
+    s.first = d.first(blockIdx.x * NW + w);
+    s.last = d.first(blockIdx.x * NW + w + 1);
+    s.row = 0;
+    s.into = 0;
+    s.raw = RawRow{0, 0, 0, 0};
+    if (s.first == s.last) {
+      if (tid == 0) shares[w] = s;
+    } else if (s.first >= before && s.first < before + mine) {  // one thread
+      int64_t at = before;
+      int n = n0;
+      if (per > 1) {
+        for (; n < n1; ++n) {
+          const int64_t t = row_tiles<QG>(p, n, nullptr);
+          if (s.first < at + t) break;
+          at += t;
+        }
+      }
+      s.row = n;
+      s.into = s.first - at;
+      s.raw = raw_row(p, n);
+      shares[w] = s;
+    }
+  }
+  tc::fence_async_smem();  // `part` is memory that copies write next
+  __syncthreads();
+}
+
+// Walks the units of a share: (row, unit of the row, tiles [j0, j0 + len) of the unit).  A warp holds the raw
+// values of the next 32 rows, one per lane, so that going on to the next row waits for no memory.
+// All lanes call together.
+template <int QG>
+struct Walk {
+  const AttnLaunch& p;
+  int64_t left;
+  int n, h, j0, len;  // h: unit of the row
+  Unit u;
+  __device__ Walk(const AttnLaunch& launch, const Share& s) : p(launch), left(s.last - s.first), n(s.row), len(0) {
+    if (left <= 0) return;
+    fill(n + 1);
+    u = unit_of<QG>(p, s.raw, nullptr);
+    h = (int)quotient(s.into, u.tiles);
+    j0 = (int)(s.into - (int64_t)h * u.tiles);
+    len = (int)min((int64_t)(u.tiles - j0), left);
+  }
+  __device__ bool valid() const { return left > 0; }
+  __device__ void next() {
+    left -= len;
+    if (left <= 0) return;
+    j0 = 0;
+    if (++h == u.per) {
+      h = 0;
+      do {
+        if (++n >= p.rows.num_seqs) {
+          left = 0;
+          return;
+        }
+        if (n == base + 32) fill(n);
+        const int src = n - base;
+        const RawRow r{__shfl_sync(0xffffffffu, ahead.bos, src), __shfl_sync(0xffffffffu, ahead.eos, src),
+                       __shfl_sync(0xffffffffu, ahead.kv, src), __shfl_sync(0xffffffffu, ahead.trow, src)};
+        u = unit_of<QG>(p, r, nullptr);
+      } while (u.tiles == 0);
+    }
+    len = (int)min((int64_t)u.tiles, left);
+  }
+  __device__ int tile_at(int j) const { return (j < u.sink_tiles ? j : u.first_tile + j - u.sink_tiles) * kTN; }
+
+ private:
+  int base;
+  RawRow ahead;
+  __device__ void fill(int from) {
+    base = from;
+    ahead = raw_row(p, min(from + (int)(threadIdx.x & 31), p.rows.num_seqs - 1));
+  }
+};
+
+// Adds the pieces of the units that begin in the shares of CTA blockIdx.x's workers and end in later
+// ones.  Block row y takes queries y, y + kJoinRows, ..; a team of warps shares a query's pieces.
+template <int D, typename T>
+__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(SplitParams P, int queries, int workers) {
+  __shared__ float so[kJoinWarps][D];
+  __shared__ float sl[kJoinWarps], sm[kJoinWarps];
+  const AttnLaunch& p = P.a;
+  const float sl2 = p.scale * 1.4426950408889634f;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int E = D / 32;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // lane: field lane % 8 of worker lane / 8's entry, and of the worker 4 behind it
+  const int first = blockIdx.x * workers;
+  const int f0 = lane < workers * 8 ? P.info[first * 8 + lane] : 0;
+  const int f1 = lane + 32 < workers * 8 ? P.info[first * 8 + lane + 32] : 0;
+  for (int w = 0; w < workers; ++w) {
+    const int from = (w & 3) * 8, f = w < 4 ? f0 : f1;
+    if (!__shfl_sync(0xffffffffu, f, from)) continue;
+    const int bos = __shfl_sync(0xffffffffu, f, from + 1), nq = __shfl_sync(0xffffffffu, f, from + 2);
+    const int h = __shfl_sync(0xffffffffu, f, from + 3), c1 = __shfl_sync(0xffffffffu, f, from + 4);
+    const int qi0 = __shfl_sync(0xffffffffu, f, from + 5);  // the unit's first query
+    const int c0 = first + w, pieces = c1 - c0 + 1;
+    const int team = pieces > 8 ? 8 : pieces > 4 ? 4 : pieces > 2 ? 2 : 1;  // warps of a query
+    for (int q0 = blockIdx.y; q0 < nq; q0 += kJoinRows * (kJoinWarps / team)) {
+      const int qi = q0 + kJoinRows * (warp / team);
+      float m = -INFINITY, l = 0.f, o[E];
+#pragma unroll
+      for (int i = 0; i < E; ++i) o[i] = 0.f;
+      if (qi < nq) {
+#pragma unroll 4
+        for (int c = c0 + warp % team; c <= c1; c += team) {
+          const size_t at = (size_t)(2 * c + (c == c0 ? 1 : 0)) * queries + qi;
+          const float2 st = *reinterpret_cast<const float2*>(P.stats + at * 2);
+          float v[E];
+#pragma unroll
+          for (int i = 0; i < E; ++i) v[i] = P.part[at * D + lane + 32 * i];
+          const float mn = fmaxf(m, st.x);
+          const float a = m == -INFINITY ? 0.f : ex2((m - mn) * sl2);
+          const float b = st.x == -INFINITY ? 0.f : ex2((st.x - mn) * sl2);
+          l = l * a + st.y * b;
+#pragma unroll
+          for (int i = 0; i < E; ++i) o[i] = o[i] * a + v[i] * b;
+          m = mn;
+        }
+      }
+      if (team > 1) {
+#pragma unroll
+        for (int i = 0; i < E; ++i) so[warp][lane + 32 * i] = o[i];
+        if (lane == 0) {
+          sm[warp] = m;
+          sl[warp] = l;
+        }
+        __syncthreads();
+        if (warp % team == 0) {
+          for (int v = warp + 1; v < warp + team; ++v) {
+            const float mn = fmaxf(m, sm[v]);
+            const float a = m == -INFINITY ? 0.f : ex2((m - mn) * sl2);
+            const float b = sm[v] == -INFINITY ? 0.f : ex2((sm[v] - mn) * sl2);
+            l = l * a + sl[v] * b;
+#pragma unroll
+            for (int i = 0; i < E; ++i) o[i] = o[i] * a + so[v][lane + 32 * i] * b;
+            m = mn;
+          }
+        }
+        __syncthreads();
+      }
+      if (qi >= nq || warp % team) continue;
+      const int t = (qi0 + qi) / p.G;
+      const int g = p.rows.tok ? __ldg(p.rows.tok + bos + t) : bos + t;
+      if (g < 0 || g >= p.num_global) continue;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      T* out = static_cast<T*>(p.out) + (int64_t)g * p.out_stride + (int64_t)(h * p.G + qi0 + qi - t * p.G) * D;
+#pragma unroll
+      for (int i = 0; i < E; ++i) out[lane + 32 * i] = from_f32<T>(o[i] * inv);
+    }
+  }
+}
+
+}  // namespace split
+}  // namespace gdn

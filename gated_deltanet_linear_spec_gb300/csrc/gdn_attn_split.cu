@@ -20,16 +20,14 @@
 // product is nearly free here, and one bf16 would cost as much accuracy as the output's own rounding.
 #include <algorithm>
 
+#include "gdn_attn_share.cuh"
 #include "gdn_tma.cuh"
 
 namespace gdn {
 
 namespace {
 
-constexpr int kSms = 152;
-constexpr int kTN = 32;       // tokens of a tile
-constexpr int kJoinWarps = 8;
-constexpr int kJoinRows = 8;  // blocks that share the queries of a unit
+using namespace split;
 
 // NW workers of WQ groups of 16 queries x DS slices of the values' columns, a computing warp each.
 template <int D, int WQ, int DS, int NW>
@@ -54,48 +52,6 @@ struct Cfg {
   static_assert(kStages >= 2, "ring too short");
 };
 
-struct SplitParams {
-  AttnLaunch a;
-  float* part;     // [2 * workers][kNQ][D]
-  float* stats;    // [2 * workers][kNQ][2]: m (of the scores before their scale), l
-  int32_t* info;   // [workers][8]: the unit that begins in a worker's share and ends in another's
-  uint64_t wait_ns;
-};
-
-struct Unit {
-  KvRow r;
-  int sink_tiles, first_tile, tiles;
-};
-
-// A row's values as they lie in memory.
-struct RawRow {
-  int bos, eos, kv, trow;
-};
-__device__ __forceinline__ RawRow raw_row(const AttnLaunch& p, int n) {
-  return RawRow{__ldg(p.rows.qsl + n), __ldg(p.rows.qsl + n + 1), __ldg(p.rows.kv_lens + n),
-                p.rows.table_rows ? __ldg(p.rows.table_rows + n) : n};
-}
-
-// The tiles that the row's queries see; 0 for an empty or bad row.
-__device__ __forceinline__ Unit unit_of(const AttnLaunch& p, const RawRow& r, uint32_t* st) {
-  Unit u;
-  u.tiles = u.sink_tiles = u.first_tile = 0;
-  if (!check_kv_row(p.rows, p.cache, r.bos, r.eos, r.kv, r.trow, u.r, st) || u.r.len == 0) return u;
-  const int low = p.window > 0 ? max(0, u.r.kv - u.r.len - p.window + 1) : 0;
-  u.sink_tiles = (min(p.sinks, low) + kTN - 1) / kTN;
-  u.first_tile = max(low / kTN, u.sink_tiles);
-  u.tiles = u.sink_tiles + (u.r.kv + kTN - 1) / kTN - u.first_tile;
-  return u;
-}
-__device__ __forceinline__ Unit unit_of(const AttnLaunch& p, int n, uint32_t* st) {
-  return unit_of(p, raw_row(p, n), st);
-}
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -123,136 +79,6 @@ __device__ __forceinline__ float bf_hi(uint32_t x) { return __uint_as_float(x & 
 __device__ __forceinline__ bool not_finite2(uint32_t x) {
   return (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u;
 }
-// The tiles dealt to the workers: the first `more` get each + 1, the others each.
-struct Deal {
-  int64_t each;
-  int more;
-  __device__ int64_t first(int worker) const { return each * worker + min(worker, more); }
-  __device__ int owner(int64_t tile) const;
-};
-
-// 64-bit quotient; in 32 bits where that does.
-__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
-  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
-}
-__device__ __forceinline__ int Deal::owner(int64_t tile) const {
-  const int64_t head = (each + 1) * more;
-  return (int)(tile < head ? quotient(tile, each + 1) : more + quotient(tile - head, each));
-}
-
-// A worker's share of the tiles, and where it begins.
-struct Share {
-  int64_t first, last;
-  int64_t into;  // tiles of row `row` before the share
-  int row;
-  RawRow raw;    // that row
-};
-
-// The shares of the CTA's workers; part: one value per warp.  All threads call.
-template <int NW, int THREADS>
-__device__ void find_shares(const AttnLaunch& p, int64_t* part, Deal& deal, Share* shares) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per = (p.rows.num_seqs + THREADS - 1) / THREADS;
-  const int n0 = min(tid * per, p.rows.num_seqs), n1 = min(n0 + per, p.rows.num_seqs);
-  int64_t mine = 0;
-  for (int n = n0; n < n1; ++n) mine += unit_of(p, n, blockIdx.x == 0 ? p.status : nullptr).tiles;
-  mine *= p.cache.Hkv;
-  int64_t inc = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += v;
-  }
-  if (lane == 31) part[warp] = inc;
-  __syncthreads();
-  int64_t before = inc - mine, total = 0;
-#pragma unroll
-  for (int i = 0; i < THREADS / 32; ++i) {
-    if (i < warp) before += part[i];
-    total += part[i];
-  }
-  Deal d;
-  d.each = quotient(total, kSms * NW);
-  d.more = (int)(total - d.each * (kSms * NW));
-  if (tid == 0) deal = d;
-#pragma unroll 1
-  for (int w = 0; w < NW; ++w) {
-    Share s;
-    s.first = d.first(blockIdx.x * NW + w);
-    s.last = d.first(blockIdx.x * NW + w + 1);
-    s.row = 0;
-    s.into = 0;
-    s.raw = RawRow{0, 0, 0, 0};
-    if (s.first == s.last) {
-      if (tid == 0) shares[w] = s;
-    } else if (s.first >= before && s.first < before + mine) {  // one thread
-      int64_t at = before;
-      int n = n0;
-      if (per > 1) {
-        for (; n < n1; ++n) {
-          const int64_t t = (int64_t)unit_of(p, n, nullptr).tiles * p.cache.Hkv;
-          if (s.first < at + t) break;
-          at += t;
-        }
-      }
-      s.row = n;
-      s.into = s.first - at;
-      s.raw = raw_row(p, n);
-      shares[w] = s;
-    }
-  }
-  tc::fence_async_smem();  // `part` is memory that copies write next
-  __syncthreads();
-}
-
-// Walks the units of a share: (row, head, tiles [j0, j0 + len) of the unit).  A warp holds the raw
-// values of the next 32 rows, one per lane, so that going on to the next row waits for no memory.
-// All lanes call together.
-struct Walk {
-  const AttnLaunch& p;
-  int64_t left;
-  int n, h, j0, len;
-  Unit u;
-  __device__ Walk(const AttnLaunch& launch, const Share& s) : p(launch), left(s.last - s.first), n(s.row), len(0) {
-    if (left <= 0) return;
-    fill(n + 1);
-    u = unit_of(p, s.raw, nullptr);
-    h = (int)quotient(s.into, u.tiles);
-    j0 = (int)(s.into - (int64_t)h * u.tiles);
-    len = (int)min((int64_t)(u.tiles - j0), left);
-  }
-  __device__ bool valid() const { return left > 0; }
-  __device__ void next() {
-    left -= len;
-    if (left <= 0) return;
-    j0 = 0;
-    if (++h == p.cache.Hkv) {
-      h = 0;
-      do {
-        if (++n >= p.rows.num_seqs) {
-          left = 0;
-          return;
-        }
-        if (n == base + 32) fill(n);
-        const int src = n - base;
-        const RawRow r{__shfl_sync(0xffffffffu, ahead.bos, src), __shfl_sync(0xffffffffu, ahead.eos, src),
-                       __shfl_sync(0xffffffffu, ahead.kv, src), __shfl_sync(0xffffffffu, ahead.trow, src)};
-        u = unit_of(p, r, nullptr);
-      } while (u.tiles == 0);
-    }
-    len = (int)min((int64_t)u.tiles, left);
-  }
-  __device__ int tile_at(int j) const { return (j < u.sink_tiles ? j : u.first_tile + j - u.sink_tiles) * kTN; }
-
- private:
-  int base;
-  RawRow ahead;
-  __device__ void fill(int from) {
-    base = from;
-    ahead = raw_row(p, min(from + (int)(threadIdx.x & 31), p.rows.num_seqs - 1));
-  }
-};
-
 // One 32-token step's second product, O += P V.  PART: some query does not see some token, so the
 // values must not reach it whatever they hold.
 template <bool PART, int DV>
@@ -360,7 +186,7 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, NW>::kThreads, 1)
   asm volatile("griddepcontrol.wait;" ::: "memory");  // what lies before this overlaps the kernel before this one
   if (tid < NW) P.info[(blockIdx.x * NW + tid) * 8] = 0;
   // (the sums of find_shares lie where the first worker's ring will be)
-  find_shares<NW, C::kThreads>(p, reinterpret_cast<int64_t*>(smem), small.deal, small.shares);
+  find_shares<0, NW, C::kThreads>(p, reinterpret_cast<int64_t*>(smem), small.deal, small.shares);
   const bool fetches = warp >= NW * C::kTeam;
   const int wk = fetches ? warp - NW * C::kTeam : warp / C::kTeam;  // the warp's worker
   auto& sm = small.worker[wk];
@@ -379,7 +205,7 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, NW>::kThreads, 1)
     const bool active = bi < boxes;
     int it = 0, seg = 0;
     bool ok = true;
-    for (Walk w(p, share); w.valid() && ok; w.next(), ++seg) {
+    for (Walk<0> w(p, share); w.valid() && ok; w.next(), ++seg) {
       // 32 table entries are held, one per lane, and the 32 behind them are on their way
       const int32_t* row = kv.table + (int64_t)w.u.r.trow * kv.max_pages;
       const int entries = (w.u.r.kv + ps - 1) >> shift;
@@ -464,7 +290,7 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, NW>::kThreads, 1)
   const float sl2 = p.scale * 1.4426950408889634f;
   int it = 0, seg = 0;
   bool ok = true;
-  for (Walk w(p, share); w.valid(); w.next(), ++seg) {
+  for (Walk<0> w(p, share); w.valid(); w.next(), ++seg) {
     const KvRow row = w.u.r;
     const int nq = row.len * p.G;
     const int pmin = row.kv - row.len, pmax = row.kv - 1;
@@ -617,91 +443,13 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, NW>::kThreads, 1)
         info[1] = row.bos;
         info[2] = nq;
         info[3] = w.h;
-        info[4] = small.deal.owner(share.last - w.left + w.u.tiles - 1);  // the worker with the unit's last tile
+        info[5] = 0;
+      info[4] = small.deal.owner(share.last - w.left + w.u.tiles - 1);  // the worker with the unit's last tile
         info[0] = 1;
       }
     }
     __syncwarp();
     if (lane == 0) tc::mbar_arrive(&sm.qempty);
-  }
-}
-
-// Adds the pieces of the units that begin in the shares of CTA blockIdx.x's workers and end in later
-// ones.  Block row y takes queries y, y + kJoinRows, ..; a team of warps shares a query's pieces.
-template <int D>
-__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(SplitParams P, int queries, int workers) {
-  __shared__ float so[kJoinWarps][D];
-  __shared__ float sl[kJoinWarps], sm[kJoinWarps];
-  const AttnLaunch& p = P.a;
-  const float sl2 = p.scale * 1.4426950408889634f;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr int E = D / 32;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  // lane: field lane % 8 of worker lane / 8's entry, and of the worker 4 behind it
-  const int first = blockIdx.x * workers;
-  const int f0 = lane < workers * 8 ? P.info[first * 8 + lane] : 0;
-  const int f1 = lane + 32 < workers * 8 ? P.info[first * 8 + lane + 32] : 0;
-  for (int w = 0; w < workers; ++w) {
-    const int from = (w & 3) * 8, f = w < 4 ? f0 : f1;
-    if (!__shfl_sync(0xffffffffu, f, from)) continue;
-    const int bos = __shfl_sync(0xffffffffu, f, from + 1), nq = __shfl_sync(0xffffffffu, f, from + 2);
-    const int h = __shfl_sync(0xffffffffu, f, from + 3), c1 = __shfl_sync(0xffffffffu, f, from + 4);
-    const int c0 = first + w, pieces = c1 - c0 + 1;
-    const int team = pieces > 8 ? 8 : pieces > 4 ? 4 : pieces > 2 ? 2 : 1;  // warps of a query
-    for (int q0 = blockIdx.y; q0 < nq; q0 += kJoinRows * (kJoinWarps / team)) {
-      const int qi = q0 + kJoinRows * (warp / team);
-      float m = -INFINITY, l = 0.f, o[E];
-#pragma unroll
-      for (int i = 0; i < E; ++i) o[i] = 0.f;
-      if (qi < nq) {
-#pragma unroll 4
-        for (int c = c0 + warp % team; c <= c1; c += team) {
-          const size_t at = (size_t)(2 * c + (c == c0 ? 1 : 0)) * queries + qi;
-          const float2 st = *reinterpret_cast<const float2*>(P.stats + at * 2);
-          float v[E];
-#pragma unroll
-          for (int i = 0; i < E; ++i) v[i] = P.part[at * D + lane + 32 * i];
-          const float mn = fmaxf(m, st.x);
-          const float a = m == -INFINITY ? 0.f : ex2((m - mn) * sl2);
-          const float b = st.x == -INFINITY ? 0.f : ex2((st.x - mn) * sl2);
-          l = l * a + st.y * b;
-#pragma unroll
-          for (int i = 0; i < E; ++i) o[i] = o[i] * a + v[i] * b;
-          m = mn;
-        }
-      }
-      if (team > 1) {
-#pragma unroll
-        for (int i = 0; i < E; ++i) so[warp][lane + 32 * i] = o[i];
-        if (lane == 0) {
-          sm[warp] = m;
-          sl[warp] = l;
-        }
-        __syncthreads();
-        if (warp % team == 0) {
-          for (int v = warp + 1; v < warp + team; ++v) {
-            const float mn = fmaxf(m, sm[v]);
-            const float a = m == -INFINITY ? 0.f : ex2((m - mn) * sl2);
-            const float b = sm[v] == -INFINITY ? 0.f : ex2((sm[v] - mn) * sl2);
-            l = l * a + sl[v] * b;
-#pragma unroll
-            for (int i = 0; i < E; ++i) o[i] = o[i] * a + so[v][lane + 32 * i] * b;
-            m = mn;
-          }
-        }
-        __syncthreads();
-      }
-      if (qi >= nq || warp % team) continue;
-      const int t = qi / p.G;
-      const int g = p.rows.tok ? __ldg(p.rows.tok + bos + t) : bos + t;
-      if (g < 0 || g >= p.num_global) continue;
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-      __nv_bfloat16* out =
-          static_cast<__nv_bfloat16*>(p.out) + (int64_t)g * p.out_stride + (int64_t)(h * p.G + qi - t * p.G) * D;
-#pragma unroll
-      for (int i = 0; i < E; ++i) out[lane + 32 * i] = __float2bfloat16_rn(o[i] * inv);
-    }
   }
 }
 
@@ -738,7 +486,7 @@ cudaError_t launch_cfg(const AttnLaunch& a, cudaStream_t s) {
   cfg.gridDim = dim3(kSms, std::min(kJoinRows, a.rows.max_q * a.G));
   cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, join_kernel<D>, P, (int)C::kNQ, NW);
+  return cudaLaunchKernelEx(&cfg, join_kernel<D, __nv_bfloat16>, P, (int)C::kNQ, NW);
 }
 
 int query_slots(int64_t queries) { return queries <= 16 ? 16 : queries <= 32 ? 32 : 64; }

@@ -133,7 +133,11 @@ cudaError_t launch_copy_items(const CopyLaunch& p, cudaStream_t s);
 bool attn_split_supported(const AttnLaunch& p, gdn_dtype dtype);
 size_t attn_split_workspace(const AttnLaunch& p);
 cudaError_t launch_attn_split(const AttnLaunch& p, cudaStream_t s);
-// Longer rows of the same layouts: prompts, on tcgen05.
+// The same over a 32-bit cache (d = 32, 64, 128, 256).
+bool attn_split_f32_supported(const AttnLaunch& p, gdn_dtype dtype);
+size_t attn_split_f32_workspace(const AttnLaunch& p);
+cudaError_t launch_attn_split_f32(const AttnLaunch& p, cudaStream_t s);
+// Longer bf16 rows (d = 64, 128, 256): prompts, on tcgen05.
 bool attn_prompt_supported(const AttnLaunch& p, gdn_dtype dtype);
 size_t attn_prompt_workspace(const AttnLaunch& p);
 cudaError_t launch_attn_prompt(const AttnLaunch& p, cudaStream_t s);

@@ -144,6 +144,15 @@ def test_up_to_64_queries_of_a_kv_head(dim, heads):
          null=[(0, 9, 0), (1, 4, -1)]).check()
 
 
+@pytest.mark.parametrize("heads", [1, 3, 8])
+@pytest.mark.parametrize("dim", [32, 64, 128, 256])
+def test_up_to_64_queries_of_a_kv_head_in_32_bits(dim, heads):
+    Step([(8, 100), (3, 77), (1, 2000), (8, 8), (0, 3), (7, 515)], heads=2 * heads, kv_heads=2, dim=dim, page=32,
+         dtype=F32, seed=heads).check()
+    Step([(8, 250), (5, 90)], heads=heads, kv_heads=1, dim=dim, window=37, sinks=5, seed=heads + 1, dtype=F32,
+         null=[(0, 9, 0), (1, 4, -1)], interleaved=True).check()
+
+
 @pytest.mark.parametrize("page", [16, 32, 64, 128, 256])
 @pytest.mark.parametrize("dim", [64, 128, 256])
 def test_page_sizes(page, dim):
