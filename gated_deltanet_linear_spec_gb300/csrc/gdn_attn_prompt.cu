@@ -23,6 +23,7 @@
 // there are too few to fill the GPU, the cache of each is cut into up to 16 pieces whose (m, l, o) meet
 // in a second launch, in order.
 #include <algorithm>
+#include <type_traits>
 
 #include "gdn_tma.cuh"
 
@@ -42,11 +43,11 @@ struct Cfg {
   static constexpr int kThreads = 128 * (kTiles + 1);
   static constexpr uint32_t kQ = 128 * D * 2;                        // bytes of a query tile
   static constexpr uint32_t kKv = kTN * D * 2;                       // bytes of a K or V tile
-  static constexpr int kFit = (int)((232448 - 2048 - kTiles * kQ) / kKv);
-  static constexpr int kRing = kFit < 8 ? kFit : 8;                  // K and V tiles in turn
+  static constexpr int kPhases = D <= 128 ? 2 : 1;                   // K and V pairs in the ring
+  static constexpr int kRing = 2 * kPhases;                          // K and V tiles in turn
   static constexpr uint32_t kSmem = kTiles * kQ + kRing * kKv;
   static constexpr int kO = 256;                                     // first O column of TMEM; S at 0 and 128
-  static_assert(kRing >= 2, "ring too short");
+  static_assert(kSmem + 2048 <= 232448, "shared memory");
 };
 
 struct PromptParams {
@@ -146,11 +147,58 @@ __device__ __forceinline__ float pack2f(float lo, float hi) {
 __device__ __forceinline__ bool not_finite2(uint32_t x) {
   return (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u;
 }
-// D (TMEM) += A (TMEM) B: A's row m is lane m, two bf16 of K per column.
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// Products, issued by the one lane whose `leader` is set while the warp goes together: in a branch of one
+// lane the compiler moves every descriptor to uniform registers anew, which takes longer than a product.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate,
+                                       uint32_t leader) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate));
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(leader));
+}
+// D (TMEM) += A (TMEM) B: A's row m is lane m, two bf16 of K per column.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate,
+                                       uint32_t leader) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(leader));
+}
+__device__ __forceinline__ void commit_by(uint64_t* bar, uint32_t leader) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(tc::smem_addr(bar)),
+      "r"(leader)
+      : "memory");
+}
+
+// The products of query tile TILE with the K (V) tile of ring phase PHASE.  All addresses are constants, TMEM's
+// as well (all 512 columns are this CTA's, from 0 on), so that a product costs an instruction and not the
+// moves that bring its operands together (85 cycles each that way, 64 of them the product's own).
+template <int D, int TILE, int SLOT, int PHASE, typename S>
+__device__ __forceinline__ void s_products(uint8_t* smem, S& sm, uint32_t leader) {
+  using C = Cfg<D>;
+  const uint32_t base = tc::smem_addr(smem);
+  const uint64_t q = tc::sdesc(base + TILE * C::kQ, 1024);
+  const uint64_t k = tc::sdesc(base + C::kTiles * C::kQ + 2 * PHASE * C::kKv, D / 64 * 1024);
+#pragma unroll
+  for (int s = 0; s < D / 16; ++s)
+    mma_ss(SLOT * 128, q + ((s >> 2) * 16384 + (s & 3) * 32) / 16, k + ((s >> 2) * 1024 + (s & 3) * 32) / 16,
+           tc::idesc_bf16(128, kTN), s > 0, leader);
+  commit_by(&sm.s_ready[SLOT], leader);
+  if (TILE == C::kTiles - 1) commit_by(&sm.empty[2 * PHASE], leader);
+}
+template <int D, int TILE, int SLOT, int PHASE, typename S>
+__device__ __forceinline__ void pv_products(uint8_t* smem, S& sm, bool onto, uint32_t leader) {
+  using C = Cfg<D>;
+  const uint32_t base = tc::smem_addr(smem);
+  const uint64_t v = tc::sdesc_lbo(base + C::kTiles * C::kQ + (2 * PHASE + 1) * C::kKv, 1024, D / 64 * 1024);
+#pragma unroll
+  for (int s = 0; s < kTN / 16; ++s)
+    mma_ts(C::kO + TILE * D, SLOT * 128 + s * 8, v + s * 2 * (D / 64) * 1024 / 16, tc::idesc_bf16_bmn(128, D),
+           s == 0 ? (uint32_t)onto : 1u, leader);
+  commit_by(&sm.pv_done[TILE], leader);
+  if (TILE == C::kTiles - 1) commit_by(&sm.empty[2 * PHASE + 1], leader);
 }
 
 // Items of all rows; sum: one value per warp.  All threads call.
@@ -176,11 +224,144 @@ __device__ __forceinline__ int pieces_of(int64_t items, int most) {
   return items == 0 ? 1 : (int)min((int64_t)most, max((int64_t)1, (int64_t)kSms / items));
 }
 
+// 32 columns of this thread's TMEM lane: the load is on its way until ld_wait, which the values pass through.
+__device__ __forceinline__ void ld_begin(uint32_t a, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(a));
+}
+__device__ __forceinline__ void ld_wait(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// Two 32-bit floats at once.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t x, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// Bits [0, n) of four words.
+__device__ __forceinline__ uint32_t low_bits(int n, int word) {
+  const int k = min(max(n - 32 * word, 0), 32);
+  return k == 32 ? 0xffffffffu : (1u << k) - 1u;
+}
+
+// The tokens of tile [b, b + 128) that a query at `pos` sees, a bit each.
+__device__ __forceinline__ void visible(const AttnLaunch& p, int b, int pos, uint32_t have, bool all_pages, int bshift,
+                                        uint32_t (&vis)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t x = low_bits(pos + 1 - b, i);
+    if (p.window > 0) x &= ~low_bits(pos - p.window + 1 - b, i) | low_bits(p.sinks - b, i);
+    if (!all_pages) {
+      uint32_t pages = 0;
+      for (int c = 0; c < 32; c += 16)
+        if (have >> ((32 * i + c) >> bshift) & 1u) pages |= 0xffffu << c;
+      x &= pages;
+    }
+    vis[i] = x;
+  }
+}
+
+// Hides the scores of tokens that the query does not see.
+__device__ __forceinline__ void hide(uint32_t (&r)[32], uint32_t vis) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) r[i] = vis >> i & 1u ? r[i] : 0xff800000u;
+}
+
+// (Both walks over a tile are loops of 64 scores: unrolled over the tile they are more code than the
+// instruction cache holds beside the other warps', and the warp that issues the products starves.)
+// The largest of a query's scores in a tile.
+__device__ __forceinline__ float tile_max(uint32_t s_col, bool part, const uint32_t (&vis)[4]) {
+  float mx[2] = {-INFINITY, -INFINITY};
+  uint32_t r[2][32];
+  ld_begin(s_col, r[0]);
+#pragma unroll 1
+  for (int c = 0; c < 2; ++c) {
+    const uint32_t v[2] = {c ? vis[2] : vis[0], c ? vis[3] : vis[1]};
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      ld_wait(r[e]);
+      if (e == 0) ld_begin(s_col + 64 * c + 32, r[1]);
+      else if (c == 0) ld_begin(s_col + 64, r[0]);
+      if (part) hide(r[e], v[e]);
+#pragma unroll
+      for (int i = 0; i < 32; i += 2)
+        mx[i / 2 & 1] = max3(mx[i / 2 & 1], __uint_as_float(r[e][i]), __uint_as_float(r[e][i + 1]));
+    }
+  }
+  return fmaxf(mx[0], mx[1]);
+}
+
+// The tile's weights 2^(sl2 s + ms) as bf16 pairs over the scores (32 columns once 64 have been read);
+// returns their sum.
+__device__ __forceinline__ float weights(uint32_t s_col, bool part, const uint32_t (&vis)[4], float sl2, float ms) {
+  const uint64_t scale = pair(sl2, sl2), shift = pair(ms, ms);
+  uint64_t sum[2] = {0, 0};
+  uint32_t r[2][32];
+  ld_begin(s_col, r[0]);
+#pragma unroll 1
+  for (int c = 0; c < 2; ++c) {
+    const uint32_t v[2] = {c ? vis[2] : vis[0], c ? vis[3] : vis[1]};
+    float u[32];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      ld_wait(r[e]);
+      if (e == 0) ld_begin(s_col + 64 * c + 32, r[1]);
+      else if (c == 0) ld_begin(s_col + 64, r[0]);
+      if (part) hide(r[e], v[e]);
+#pragma unroll
+      for (int i = 0; i < 32; i += 2) {
+        float a, b;
+        unpair(fma2(pair(__uint_as_float(r[e][i]), __uint_as_float(r[e][i + 1])), scale, shift), a, b);
+        a = ex2(a);
+        b = ex2(b);
+        sum[i / 2 & 1] = add2(sum[i / 2 & 1], pair(a, b));
+        u[16 * e + i / 2] = pack2f(a, b);
+      }
+    }
+    tc::tmem_st32(s_col + 32 * c, u);
+  }
+  float a, b;
+  unpair(add2(sum[0], sum[1]), a, b);
+  return a + b;
+}
+
 // Adds the listed tokens' share to O where the query sees them: their weights from S, their values from the
 // cache.  O is complete; the warp's lanes go together, as TMEM loads and stores need them all.
-template <int D, typename Sees>
-__device__ __forceinline__ void add_listed(const PromptParams& P, const Item& w, const uint32_t* bad, int b, uint32_t s_col,
-                                        uint32_t o_col, float sl2, float ms, Sees sees) {
+template <int D>
+__device__ __forceinline__ void add_listed(const PromptParams& P, const Item& w, const uint32_t* bad, int b,
+                                           uint32_t s_col, uint32_t o_col, float sl2, float ms,
+                                           const uint32_t (&vis)[4]) {
   const KvDev& kv = P.a.cache;
 #pragma unroll 1
   for (int t = 0; t < kTN; ++t) {
@@ -190,7 +371,8 @@ __device__ __forceinline__ void add_listed(const PromptParams& P, const Item& w,
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       if ((t & 7) == i) s = x[i];
-    const bool seen = sees(t);
+    const uint32_t word = t < 64 ? (t < 32 ? vis[0] : vis[1]) : (t < 96 ? vis[2] : vis[3]);
+    const bool seen = word >> (t & 31) & 1u;
     const float weight = ex2(fmaf(s, sl2, ms));
     const int tok = b + t;  // below the row's end, in a page that is not NULL
     const int page = kv.table[(int64_t)w.r.trow * kv.max_pages + tok / kv.page_size];
@@ -211,7 +393,8 @@ __device__ __forceinline__ void add_listed(const PromptParams& P, const Item& w,
 
 template <int D>
 struct Small {
-  uint64_t full[Cfg<D>::kRing], empty[Cfg<D>::kRing], checked[Cfg<D>::kRing];
+  uint64_t full[Cfg<D>::kRing], empty[Cfg<D>::kRing];
+  uint64_t checked[Cfg<D>::kRing];  // of a V tile, by its entry
   uint64_t q_ready, s_ready[2], p_ready[2], pv_done[2], drain;
   int64_t sum[Cfg<D>::kThreads / 32];
   uint32_t bad[Cfg<D>::kRing][4];  // listed tokens of a V tile
@@ -311,30 +494,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         const uint32_t have = sm.held[tiles & 15];
         const bool all_pages = have == (1u << boxes) - 1u;
         const bool part = !all_pages || in_part(p, b, tmin, tmax);
-        auto sees = [&](int c) {
-          const int tok = b + c;
-          return tok <= pos && (p.window <= 0 || tok > pos - p.window || tok < p.sinks) &&
-                 (all_pages || (have >> (c >> bshift) & 1u));
-        };
-        float mx = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < 128; c += 64) {
-          float x[32], y[32];
-          tc::tmem_ld32x2(s_col + c, x, s_col + c + 32, y);
-          if (part) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              if (!sees(c + i)) x[i] = -INFINITY;
-              if (!sees(c + 32 + i)) y[i] = -INFINITY;
-            }
-          }
-          float m4[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int i = 0; i < 32; i += 4)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) m4[e] = fmaxf(m4[e], fmaxf(x[i + e], y[i + e]));
-          mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-        }
+        uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u};  // the tile's tokens that this query sees
+        if (part) visible(p, b, pos, have, all_pages, bshift, vis);
         bool any_bad = false;  // the tile lists tokens
         if (in_part(p, b, cmin, w.last)) {
           ok = __all_sync(0xffffffffu, ok && tc::mbar_wait(&sm.checked[v_entry], (chk >> v_entry) & 1, P.wait_ns));
@@ -343,16 +504,15 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 4; ++i) any_bad |= sm.bad[v_entry][i] != 0;
         }
+        const float mx = tile_max(s_col, part, vis);
         const bool grow = mx > m && (m == -INFINITY || (mx - m) * sl2 > kGrow);
-        const bool rescale = wrote && __any_sync(0xffffffffu, grow);
+        const bool rewrite = any_bad || (wrote && __any_sync(0xffffffffu, grow));
         const float f = grow && m != -INFINITY ? ex2((m - mx) * sl2) : 1.f;
         if (grow) m = mx;
-        l *= f;
         const float ms = m == -INFINITY ? 0.f : -m * sl2;
-        if (rescale || any_bad) {
+        if (rewrite) {
           if (wrote) {  // O is complete when the product of the tile before is
-            ok = __all_sync(0xffffffffu,
-                            ok && tc::mbar_wait(&sm.pv_done[tile], (pv_n - 1) & 1, P.wait_ns));
+            ok = __all_sync(0xffffffffu, ok && tc::mbar_wait(&sm.pv_done[tile], (pv_n - 1) & 1, P.wait_ns));
             if (!ok) break;
             tc::fence_after();
           }
@@ -365,42 +525,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             tc::tmem_st32(o_col + c, o);
           }
           tc::tmem_st_wait();
-          if (any_bad) add_listed<D>(P, w, sm.bad[v_entry], b, s_col, o_col, sl2, ms, sees);
+          if (any_bad) add_listed<D>(P, w, sm.bad[v_entry], b, s_col, o_col, sl2, ms, vis);
         }
-        // P over S, 64 tokens at a time: their 32 columns have been read
-        float l4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int c = 0; c < 128; c += 64) {
-          float x[32], y[32];
-          tc::tmem_ld32x2(s_col + c, x, s_col + c + 32, y);
-          if (part) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              if (!sees(c + i)) x[i] = -INFINITY;
-              if (!sees(c + 32 + i)) y[i] = -INFINITY;
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            x[i] = ex2(fmaf(x[i], sl2, ms));
-            y[i] = ex2(fmaf(y[i], sl2, ms));
-          }
-#pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            l4[0] += x[i];
-            l4[1] += x[i + 1];
-            l4[2] += y[i];
-            l4[3] += y[i + 1];
-          }
-          float u[32];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            u[i] = pack2f(x[2 * i], x[2 * i + 1]);
-            u[16 + i] = pack2f(y[2 * i], y[2 * i + 1]);
-          }
-          tc::tmem_st32(s_col + c / 2, u);
-        }
-        l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+        l = l * f + weights(s_col, part, vis, sl2, ms);
         tc::tmem_st_wait();
         if (NT == 1 && wrote) {
           // The product of the tile before: the next one begins only after this, so that no phase of
@@ -447,86 +574,74 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     if (!ok) set_status(p.status, GDN_STATUS_WAIT_TIMEOUT);
   } else if (role == 0) {
     // ---- products: one lane issues them all ----
-    constexpr uint32_t kS = tc::idesc_bf16(128, kTN), kPv = tc::idesc_bf16_bmn(128, D);
     uint32_t p_n[2] = {0, 0}, chk = 0, items_n = 0;
-    auto issue_s = [&](int tile, int slot, uint32_t k_at) {
-      const uint32_t q = tc::smem_addr(smem + tile * C::kQ), k = tc::smem_addr(ring + (k_at % R) * C::kKv);
-      if (lane == 0) {
-#pragma unroll
-        for (int s = 0; s < D / 16; ++s) {
-          const uint32_t off = (s >> 2) * 16384 + (s & 3) * 32;
-          tc::mma(tmem + slot * 128, tc::sdesc(q + off, 1024), tc::sdesc(k + off, 1024), kS, s > 0);
-        }
-        tc::commit(&sm.s_ready[slot]);
-      }
-      __syncwarp();
-    };
-    auto issue_pv = [&](int tile, int slot, uint32_t v_at, bool onto) {
-      const uint32_t v = tc::smem_addr(ring + (v_at % R) * C::kKv);
-      if (lane == 0) {
-#pragma unroll
-        for (int s = 0; s < kTN / 16; ++s)
-          mma_ts(tmem + C::kO + tile * D, tmem + slot * 128 + s * 8, tc::sdesc_lbo(v + s * 2048, 16384, 1024), kPv,
-                 onto || s > 0);
-        tc::commit(&sm.pv_done[tile]);
-      }
-      __syncwarp();
-    };
-    auto release = [&](uint32_t which) {
-      if (lane == 0) tc::commit(&sm.empty[which % R]);
-      __syncwarp();
-    };
+    // (a phase of a barrier; false once a wait has given up)
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       ok = __all_sync(0xffffffffu, ok && tc::mbar_wait(bar, parity & 1, P.wait_ns));
       if (ok) tc::fence_after();
       return ok;
     };
+    const uint32_t leader = lane == 0;
+    auto issue_s = [&](auto tile, auto slot, uint32_t k_at) {
+      if (tile() == 0 && !wait(&sm.full[k_at % R], k_at / R)) return;
+      if (C::kPhases == 1 || k_at % R == 0)
+        s_products<D, tile(), slot(), 0>(smem, sm, leader);
+      else
+        s_products<D, tile(), slot(), C::kPhases - 1>(smem, sm, leader);
+    };
+    auto issue_pv = [&](auto tile, auto slot, uint32_t v_at, bool onto) {
+      if (C::kPhases == 1 || v_at % R == 1)
+        pv_products<D, tile(), slot(), 0>(smem, sm, onto, leader);
+      else
+        pv_products<D, tile(), slot(), C::kPhases - 1>(smem, sm, onto, leader);
+    };
+    constexpr std::integral_constant<int, 0> zero{};
+    constexpr std::integral_constant<int, 1> one{};
     for (int64_t idx = blockIdx.x; idx < items && ok; idx += kSms, ++items_n) {
       if (!finder.find(idx, pieces, w)) break;
       if (!wait(&sm.q_ready, items_n)) break;
       const int n = w.j1 - w.j0;
       if (n == 0) continue;
       const int cmin = w.r.kv - w.r.len + w.q0 / p.G;
-      if (!wait(&sm.full[at % R], at / R)) break;
-      for (int i = 0; i < NT; ++i) issue_s(i, i, at);
-      release(at);
+      issue_s(zero, zero, at);
+      if constexpr (NT == 2) {
+        if (ok) issue_s(one, one, at);
+      }
       for (int j = 0; j < n && ok; ++j, at += 2) {
-        const uint32_t v_at = at + 1, k_next = at + 2;
-        const bool checked = in_part(p, tile_at(w, w.j0 + j), cmin, w.last);
-        if (NT == 1 && j + 1 < n) {  // the next scores run under this tile's softmax
-          if (!wait(&sm.full[k_next % R], k_next / R)) break;
-          issue_s(0, (j + 1) & 1, k_next);
-          release(k_next);
+        const uint32_t v_at = at + 1, k_next = at + 2, odd = j & 1;
+        const bool checked = in_part(p, tile_at(w, w.j0 + j), cmin, w.last), more = j + 1 < n;
+        if constexpr (NT == 1) {
+          if (more) {  // the next scores run under this tile's softmax
+            if (odd) issue_s(zero, zero, k_next); else issue_s(zero, one, k_next);
+            if (!ok) break;
+          }
         }
+        const uint32_t first = NT == 2 ? 0 : odd;  // the slot of query tile 0
+        if (!wait(&sm.p_ready[first], p_n[first]++) || !wait(&sm.full[v_at % R], v_at / R)) break;
         bool onto = j > 0;
-        for (int i = 0; i < NT && ok; ++i) {
-          const int slot = NT == 2 ? i : j & 1;
-          if (!wait(&sm.p_ready[slot], p_n[slot]++)) break;
-          if (i == 0) {
-            if (!wait(&sm.full[v_at % R], v_at / R)) break;
-            if (checked) {
-              if (!wait(&sm.checked[v_at % R], chk >> (v_at % R))) break;
-              chk ^= 1u << (v_at % R);
-              for (int e = 0; e < 4; ++e) onto |= sm.bad[v_at % R][e] != 0;  // the softmax has begun O
-            }
-          }
-          issue_pv(i, slot, v_at, onto);
-          if (i == NT - 1) release(v_at);
-          if (NT == 2 && j + 1 < n) {
-            if (i == 0 && !wait(&sm.full[k_next % R], k_next / R)) break;
-            issue_s(i, i, k_next);
-            if (i == NT - 1) release(k_next);
-          }
+        if (checked) {
+          if (!wait(&sm.checked[v_at % R], chk >> (v_at % R))) break;
+          chk ^= 1u << (v_at % R);
+          for (int e = 0; e < 4; ++e) onto |= sm.bad[v_at % R][e] != 0;  // the softmax has begun O
+        }
+        if constexpr (NT == 1) {
+          if (odd) issue_pv(zero, one, v_at, onto); else issue_pv(zero, zero, v_at, onto);
+        } else {
+          issue_pv(zero, zero, v_at, onto);
+          if (more) issue_s(zero, zero, k_next);
+          if (!ok || !wait(&sm.p_ready[1], p_n[1]++)) break;
+          issue_pv(one, one, v_at, onto);
+          if (more) issue_s(one, one, k_next);
         }
       }
     }
-    if (lane == 0) tc::commit(&sm.drain);
-    __syncwarp();
+    commit_by(&sm.drain, leader);
     if (!tc::mbar_wait(&sm.drain, 0, P.wait_ns)) ok = false;
     if (!ok) set_status(p.status, GDN_STATUS_WAIT_TIMEOUT);
   } else if (role == 1) {
-    // ---- fetches: lane = (page of the tile, 64-column block) ----
-    const int bi = lane / CB, cb = lane % CB;
+    // ---- fetches: a lane per page of the tile ----
+    const int bi = lane, spp = slabs_per_page(kv);
+    const int none = (kv.num_pages - 1) * spp + kv.Hkv;  // a slab past the pool
     const bool active = bi < boxes;
     for (int64_t idx = blockIdx.x; idx < items && ok; idx += kSms) {
       if (!finder.find(idx, pieces, w)) break;
@@ -547,10 +662,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         }
         int page = __shfl_sync(0xffffffffu, ids, active ? (pos >> shift) - eb : 0);
         page = active && pos < w.r.kv ? page_or_null(page, kv, p.status) : 0;
-        const uint32_t have = __ballot_sync(0xffffffffu, page > 0 && cb == 0);
-        uint32_t mask = 0;
-        for (int i = 0; i < boxes; ++i) mask |= (have >> (i * CB) & 1u) << i;
-#pragma unroll
+        const uint32_t mask = __ballot_sync(0xffffffffu, page > 0);
         for (int v = 0; v < 2; ++v) {
           const uint32_t a = at + v, en = a % R;
           ok = __all_sync(0xffffffffu, a < R || tc::mbar_wait(&sm.empty[en], (a / R - 1) & 1, P.wait_ns));
@@ -561,8 +673,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
           }
           __syncwarp();
           if (active)
-            tc::tma_page(ring + en * C::kKv + cb * 16384 + bi * box * 128, v ? &vmap : &kmap, cb * 64, pos & (ps - 1), w.h,
-                         page > 0 ? page : kv.num_pages, &sm.full[en]);
+            tc::tma_page(ring + en * C::kKv + bi * box * D * 2, v ? &vmap : &kmap, pos & (ps - 1),
+                         page > 0 ? page * spp + w.h : none, &sm.full[en]);
         }
         if (!ok) break;
       }
@@ -577,32 +689,31 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     for (int64_t idx = blockIdx.x; idx < items && ok; idx += kSms) {
       if (!finder.find(idx, pieces, w)) break;
       const int cmin = w.r.kv - w.r.len + w.q0 / p.G;
-      for (int j = w.j0; j < w.j1; ++j, at += 2) {
+      for (int j = w.j0; j < w.j1 && ok; ++j, at += 2) {
         const int b = tile_at(w, j);
         const uint32_t en = (at + 1) % R;
-        ok = __all_sync(0xffffffffu, ok && tc::mbar_wait(&sm.full[at % R], (at / R) & 1, P.wait_ns));
-        if (!ok) break;
-        if (lane == 0) tc::mbar_arrive(&sm.empty[at % R]);
-        ok = __all_sync(0xffffffffu, ok && tc::mbar_wait(&sm.full[en], ((at + 1) / R) & 1, P.wait_ns));
-        if (!ok) break;
-        if (!in_part(p, b, cmin, w.last)) {
-          if (lane == 0) tc::mbar_arrive(&sm.empty[en]);
-          continue;
+        const bool look = in_part(p, b, cmin, w.last);
+        for (int v = 0; v < 2; ++v) {
+          const uint32_t a = at + v;
+          ok = __all_sync(0xffffffffu, ok && tc::mbar_wait(&sm.full[a % R], (a / R) & 1, P.wait_ns));
+          if (!ok) break;
+          if (lane == 0 && (v == 0 || !look)) tc::mbar_arrive(&sm.empty[a % R]);
         }
+        if (!ok || !look) continue;
 #pragma unroll 1
         for (int u = 0; u < 2; ++u) {
           const int t = (role - 2) * 64 + u * 32 + lane;
-          uint8_t* v = ring + en * C::kKv + t * 128;
+          uint8_t* v = ring + en * C::kKv + (t >> 3) * CB * 1024 + (t & 7) * 128;
           bool odd = false;
           const bool past = b + t >= w.r.kv;
 #pragma unroll 8
           for (int c = 0; c < D / 8; ++c) {
-            const uint4 x = *reinterpret_cast<const uint4*>(v + (c >> 3) * 16384 + (((c & 7) ^ (t & 7)) << 4));
+            const uint4 x = *reinterpret_cast<const uint4*>(v + (c >> 3) * 1024 + (((c & 7) ^ (t & 7)) << 4));
             odd |= not_finite2(x.x) || not_finite2(x.y) || not_finite2(x.z) || not_finite2(x.w);
           }
           if (past || odd)
             for (int c = 0; c < D / 8; ++c)
-              *reinterpret_cast<uint4*>(v + (c >> 3) * 16384 + (((c & 7) ^ (t & 7)) << 4)) = make_uint4(0, 0, 0, 0);
+              *reinterpret_cast<uint4*>(v + (c >> 3) * 1024 + (((c & 7) ^ (t & 7)) << 4)) = make_uint4(0, 0, 0, 0);
           const uint32_t list = __ballot_sync(0xffffffffu, odd && !past);
           if (lane == 0) sm.bad[en][(role - 2) * 2 + u] = list;
         }

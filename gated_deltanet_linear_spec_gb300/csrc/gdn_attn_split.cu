@@ -81,7 +81,7 @@ __device__ __forceinline__ bool not_finite2(uint32_t x) {
 }
 // One 32-token step's second product, O += P V.  PART: some query does not see some token, so the
 // values must not reach it whatever they hold.
-template <bool PART, int DV>
+template <bool PART, int DV, int CB>
 __device__ __forceinline__ void values_step(float (&o)[DV / 8][4], const uint32_t (&ph)[2][4], const uint32_t (&pl)[2][4],
                                             uint32_t vbase, int col0, int b, const int (&pos)[2], int pmax, int window,
                                             int sinks) {
@@ -91,7 +91,7 @@ __device__ __forceinline__ void values_step(float (&o)[DV / 8][4], const uint32_
     // lanes 0-7, 8-15, 16-23, 24-31 point at (tokens 0-7, left 8 columns), (8-15, left), (0-7, right),
     // (8-15, right); the transposing load puts two tokens of a column into a register
     const int r = (lane & 7) + (((lane >> 3) & 1) << 3);
-    const uint32_t base = vbase + (half * 16 + r) * 128;
+    const uint32_t base = vbase + (half * 2 + (r >> 3)) * CB * 1024 + (r & 7) * 128;
     const int t0 = b + half * 16;
     uint32_t m0 = 0xffffffffu, m1 = 0xffffffffu;
     if (PART) {  // tokens past the row's end hold anything
@@ -107,7 +107,7 @@ __device__ __forceinline__ void values_step(float (&o)[DV / 8][4], const uint32_
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int chunk = col0 / 8 + (i + u) * 2 + (lane >> 4);
-        ldsm4t(v[u], base + (chunk >> 3) * kTN * 128 + (((chunk & 7) ^ (r & 7)) << 4));
+        ldsm4t(v[u], base + (chunk >> 3) * 1024 + (((chunk & 7) ^ (r & 7)) << 4));
         if (PART) {
           v[u][0] &= m0;
           v[u][1] &= m1;
@@ -199,9 +199,9 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, NW>::kThreads, 1)
   const int shift = __ffs(ps) - 1;
 
   if (fetches) {
-    // ---- the fetching warp: lane = (page of the tile, 64-column block, K or V) ----
-    constexpr int CB = D / 64;
-    const int bi = lane / (2 * CB), cb = (lane >> 1) % CB, is_v = lane & 1;
+    // ---- the fetching warp: lane = (page of the tile, K or V) ----
+    const int bi = lane >> 1, is_v = lane & 1, spp = slabs_per_page(kv);
+    const int none = (kv.num_pages - 1) * spp + kv.Hkv;  // a slab past the pool
     const bool active = bi < boxes;
     int it = 0, seg = 0;
     bool ok = true;
@@ -260,18 +260,16 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, NW>::kThreads, 1)
         ok = it < S || tc::mbar_wait(&sm.empty[s], ((it / S) - 1) & 1, P.wait_ns);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        const uint32_t have = __ballot_sync(0xffffffffu, page > 0 && cb == 0 && is_v == 0);
-        uint32_t mask = 0;
-        for (int i = 0; i < boxes; ++i) mask |= (have >> (i * 2 * CB) & 1u) << i;
+        const uint32_t have = __ballot_sync(0xffffffffu, page > 0);
+        const uint32_t mask = (have & 1u) | (have >> 1 & 2u);  // (lanes 0 and 2: the tile's one or two pages)
         if (lane == 0) {
           sm.held[s] = (uint8_t)mask;
           tc::expect_tx(&sm.full[s], 2 * C::kHalf);
         }
         __syncwarp();
         if (active) {
-          uint8_t* dst = ring + (size_t)s * 2 * C::kHalf + is_v * C::kHalf + (size_t)(cb * kTN + bi * box) * 128;
-          tc::tma_page(dst, is_v ? &vmap : &kmap, cb * 64, pos & (ps - 1), w.h, page > 0 ? page : kv.num_pages,
-                       &sm.full[s]);
+          uint8_t* dst = ring + (size_t)s * 2 * C::kHalf + is_v * C::kHalf + (size_t)bi * box * D * 2;
+          tc::tma_page(dst, is_v ? &vmap : &kmap, pos & (ps - 1), page > 0 ? page * spp + w.h : none, &sm.full[s]);
         }
       }
     }
@@ -325,15 +323,15 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, NW>::kThreads, 1)
         for (int n = 0; n < 4; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.f;
         {
           const int r = (lane & 7) + ((lane >> 4) << 3);
-          const uint32_t base = kbase + r * 128;
+          const uint32_t base = kbase + (r >> 3) * (D / 64) * 1024 + (r & 7) * 128;
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
             uint32_t a[4], k0[4], k1[4];
             const uint32_t at =
-                base + (k >> 2) * kTN * 128 + ((((k & 3) * 2 + ((lane >> 3) & 1)) ^ (r & 7)) << 4);
+                base + (k >> 2) * 1024 + ((((k & 3) * 2 + ((lane >> 3) & 1)) ^ (r & 7)) << 4);
             ldsm4(a, qbase + k * 32);
             ldsm4(k0, at);
-            ldsm4(k1, at + 16 * 128);
+            ldsm4(k1, at + 2 * (D / 64) * 1024);
             mma16816(sc[0], a, k0[0], k0[1]);
             mma16816(sc[1], a, k0[2], k0[3]);
             mma16816(sc[2], a, k1[0], k1[1]);
@@ -400,9 +398,9 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, NW>::kThreads, 1)
           }
         }
         if (part)
-          values_step<true, DV>(o, ph, pl, vbase, ds * DV, b, pos, pmax, p.window, p.sinks);
+          values_step<true, DV, D / 64>(o, ph, pl, vbase, ds * DV, b, pos, pmax, p.window, p.sinks);
         else
-          values_step<false, DV>(o, ph, pl, vbase, ds * DV, b, pos, pmax, p.window, p.sinks);
+          values_step<false, DV, D / 64>(o, ph, pl, vbase, ds * DV, b, pos, pmax, p.window, p.sinks);
       }
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&sm.empty[s]);

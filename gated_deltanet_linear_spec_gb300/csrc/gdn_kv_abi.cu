@@ -37,6 +37,9 @@ int check_shape(const gdn_kv_cache* c) {
   const int64_t dense = (int64_t)c->num_kv_heads * c->page_size * c->head_dim;
   if (c->page_stride != 0 && (c->page_stride < dense || c->page_stride >= ((int64_t)1 << 38))) return GDN_ERR_SHAPE;
   if (c->page_stride * es_of(c->dtype) % 16) return GDN_ERR_ALIGN;
+  // pages are whole slabs of page_size x head_dim apart, and slabs are numbered in 32 bits
+  const int64_t slab = (int64_t)c->page_size * c->head_dim, stride = c->page_stride ? c->page_stride : dense;
+  if (stride % slab || (c->num_pages - 1) * (stride / slab) + c->num_kv_heads > INT32_MAX) return GDN_ERR_SHAPE;
   return GDN_OK;
 }
 

@@ -307,9 +307,9 @@ int gdn_mixed_batch_static_workspace(const gdn_layer_desc* layer, const gdn_laye
 typedef struct {
   void* k_pool;          /* [num_pages, num_kv_heads, page_size, head_dim] dtype                    */
   void* v_pool;          /* the same shape                                                          */
-  int64_t page_stride;   /* elements from one page to the next in both pools; 0 = dense; its bytes a
-                            multiple of 16, below 2^38 (a larger stride lets K and V share one
-                            allocation)                                                              */
+  int64_t page_stride;   /* elements from one page to the next in both pools; 0 = dense; else a multiple
+                            of page_size * head_dim, below 2^38 (a larger stride lets K and V share
+                            one allocation)                                                          */
   int32_t* block_table;  /* [num_table_rows, max_pages] page id of each page_size tokens of a row   */
   int32_t* refcount;     /* [num_pages]; NULL where a call says that it may be                      */
   int32_t num_pages;     /* 2..2^28 (page 0 is NULL)                                                */

@@ -56,6 +56,8 @@ BAD_CACHE = [
     (dict(num_kv_heads=0), SHAPE), (dict(num_kv_heads=1025), SHAPE), (dict(head_dim=8), SHAPE),
     (dict(head_dim=72), SHAPE), (dict(head_dim=272), SHAPE), (dict(page_stride=2 * 16 * 64 - 16), SHAPE),
     (dict(page_stride=-16), SHAPE), (dict(page_stride=2 * 16 * 64 + 4), ALIGN),
+    (dict(page_stride=2 * 16 * 64 + 64), SHAPE), (dict(page_stride=1 << 38), SHAPE),
+    (dict(page_stride=1 << 33, num_pages=1 << 20), SHAPE),
 ]
 BAD_TABLE = [(dict(block_table=None), NULL_ARG), (dict(num_table_rows=0), SHAPE), (dict(max_pages=0), SHAPE),
              (dict(max_pages=(1 << 20) + 1), SHAPE)]
