@@ -10,8 +10,9 @@
 //   warps 0-3 (and 4-7): softmax of tile 0 (1), a thread per query;
 //   then a warp that issues all products, one that fetches pages by TMA, two that look after V tiles
 //   of which some query must not see some token (below).
-// The maximum that P refers to follows the running maximum only when that has grown by 2^8 or more
-// (weights up to 256 lose nothing in bf16 or fp32): O is rescaled in TMEM a few times per row at most.
+// P refers to a maximum that follows the running one only when that has grown by 2^64 or more: scaled by
+// a power of two, weights lose nothing in bf16 or fp32 before they overflow.  So S is read once, and O is
+// rescaled in TMEM next to never.
 // P is rounded to bf16, half a step of 2^-8 relative per weight, as the product takes one 16-bit type;
 // the sum of the weights is kept in fp32.
 //
@@ -34,7 +35,7 @@ namespace {
 constexpr int kSms = 152;
 constexpr int kTN = 128;        // cached tokens of a tile
 constexpr int kMaxPieces = 16;
-constexpr float kGrow = 8.f;    // log2 of how far weights may outgrow their reference
+constexpr float kGrow = 64.f;   // log2 of how far weights may outgrow their reference
 
 template <int D>
 struct Cfg {
@@ -268,6 +269,11 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 
 // Bits [0, n) of four words.
 __device__ __forceinline__ uint32_t low_bits(int n, int word) {
@@ -298,62 +304,45 @@ __device__ __forceinline__ void hide(uint32_t (&r)[32], uint32_t vis) {
   for (int i = 0; i < 32; ++i) r[i] = vis >> i & 1u ? r[i] : 0xff800000u;
 }
 
-// (Both walks over a tile are loops of 64 scores: unrolled over the tile they are more code than the
-// instruction cache holds beside the other warps', and the warp that issues the products starves.)
-// The largest of a query's scores in a tile.
-__device__ __forceinline__ float tile_max(uint32_t s_col, bool part, const uint32_t (&vis)[4]) {
-  float mx[2] = {-INFINITY, -INFINITY};
-  uint32_t r[2][32];
-  ld_begin(s_col, r[0]);
-#pragma unroll 1
-  for (int c = 0; c < 2; ++c) {
-    const uint32_t v[2] = {c ? vis[2] : vis[0], c ? vis[3] : vis[1]};
+// The weights 2^(sl2 s + ms) of 32 scores as 16 bf16 pairs; added to sum.
+__device__ __forceinline__ void weights32(const uint32_t (&r)[32], uint64_t scale, uint64_t shift, uint64_t (&sum)[2],
+                                          float* u) {
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      ld_wait(r[e]);
-      if (e == 0) ld_begin(s_col + 64 * c + 32, r[1]);
-      else if (c == 0) ld_begin(s_col + 64, r[0]);
-      if (part) hide(r[e], v[e]);
-#pragma unroll
-      for (int i = 0; i < 32; i += 2)
-        mx[i / 2 & 1] = max3(mx[i / 2 & 1], __uint_as_float(r[e][i]), __uint_as_float(r[e][i + 1]));
-    }
+  for (int i = 0; i < 32; i += 2) {
+    float a, b;
+    unpair(fma2(pair(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), scale, shift), a, b);
+    a = ex2(a);
+    b = ex2(b);
+    sum[i / 2 & 1] = add2(sum[i / 2 & 1], pair(a, b));
+    u[i / 2] = pack2f(a, b);
   }
-  return fmaxf(mx[0], mx[1]);
 }
 
-// The tile's weights 2^(sl2 s + ms) as bf16 pairs over the scores (32 columns once 64 have been read);
-// returns their sum.
-__device__ __forceinline__ float weights(uint32_t s_col, bool part, const uint32_t (&vis)[4], float sl2, float ms) {
-  const uint64_t scale = pair(sl2, sl2), shift = pair(ms, ms);
-  uint64_t sum[2] = {0, 0};
-  uint32_t r[2][32];
-  ld_begin(s_col, r[0]);
+// O (D columns from o_col on) times f; zeros where it holds nothing yet.
+template <int D>
+__device__ __forceinline__ void scale_o(uint32_t o_col, bool wrote, float f) {
 #pragma unroll 1
-  for (int c = 0; c < 2; ++c) {
-    const uint32_t v[2] = {c ? vis[2] : vis[0], c ? vis[3] : vis[1]};
-    float u[32];
+  for (int c = 0; c < D; c += 32) {
+    float o[32];
+    if (wrote) tc::tmem_ld32(o_col + c, o);
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      ld_wait(r[e]);
-      if (e == 0) ld_begin(s_col + 64 * c + 32, r[1]);
-      else if (c == 0) ld_begin(s_col + 64, r[0]);
-      if (part) hide(r[e], v[e]);
-#pragma unroll
-      for (int i = 0; i < 32; i += 2) {
-        float a, b;
-        unpair(fma2(pair(__uint_as_float(r[e][i]), __uint_as_float(r[e][i + 1])), scale, shift), a, b);
-        a = ex2(a);
-        b = ex2(b);
-        sum[i / 2 & 1] = add2(sum[i / 2 & 1], pair(a, b));
-        u[16 * e + i / 2] = pack2f(a, b);
-      }
-    }
-    tc::tmem_st32(s_col + 32 * c, u);
+    for (int i = 0; i < 32; ++i) o[i] = wrote ? o[i] * f : 0.f;
+    tc::tmem_st32(o_col + c, o);
   }
-  float a, b;
-  unpair(add2(sum[0], sum[1]), a, b);
-  return a + b;
+  tc::tmem_st_wait();
+}
+
+// 64 tokens' weights (32 columns of bf16 pairs) times f.
+__device__ __forceinline__ void scale_p(uint32_t col, float f) {
+  float u[32];
+  tc::tmem_ld32(col, u);
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    const uint32_t x = __float_as_uint(u[i]);
+    u[i] = pack2f(__uint_as_float(x << 16) * f, __uint_as_float(x & 0xffff0000u) * f);
+  }
+  tc::tmem_st32(col, u);
+  tc::tmem_st_wait();
 }
 
 // Adds the listed tokens' share to O where the query sees them: their weights from S, their values from the
@@ -504,30 +493,89 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 4; ++i) any_bad |= sm.bad[v_entry][i] != 0;
         }
-        const float mx = tile_max(s_col, part, vis);
-        const bool grow = mx > m && (m == -INFINITY || (mx - m) * sl2 > kGrow);
-        const bool rewrite = any_bad || (wrote && __any_sync(0xffffffffu, grow));
-        const float f = grow && m != -INFINITY ? ex2((m - mx) * sl2) : 1.f;
-        if (grow) m = mx;
-        const float ms = m == -INFINITY ? 0.f : -m * sl2;
-        if (rewrite) {
-          if (wrote) {  // O is complete when the product of the tile before is
+        if (any_bad) {
+          // O by hand: complete when the product of the tile before is; the scores must not be overwritten yet,
+          // nor refer to another maximum afterwards
+          if (wrote) {
             ok = __all_sync(0xffffffffu, ok && tc::mbar_wait(&sm.pv_done[tile], (pv_n - 1) & 1, P.wait_ns));
             if (!ok) break;
             tc::fence_after();
           }
+          float mx = -INFINITY;
 #pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            float o[32];
-            if (wrote) tc::tmem_ld32(o_col + c, o);
+          for (int c = 0; c < 4; ++c) {
+            uint32_t r[32];
+            ld_begin(s_col + 32 * c, r);
+            ld_wait(r);
+            hide(r, c < 2 ? (c ? vis[1] : vis[0]) : (c == 3 ? vis[3] : vis[2]));
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = wrote ? o[i] * f : 0.f;
-            tc::tmem_st32(o_col + c, o);
+            for (int i = 0; i < 32; i += 2) mx = max3(mx, __uint_as_float(r[i]), __uint_as_float(r[i + 1]));
           }
-          tc::tmem_st_wait();
-          if (any_bad) add_listed<D>(P, w, sm.bad[v_entry], b, s_col, o_col, sl2, ms, vis);
+          float f = 1.f;
+          if (mx > m) {
+            f = m == -INFINITY ? 1.f : ex2((m - mx) * sl2);
+            m = mx;
+          }
+          l *= f;
+          scale_o<D>(o_col, wrote, f);
+          add_listed<D>(P, w, sm.bad[v_entry], b, s_col, o_col, sl2, m == -INFINITY ? 0.f : -m * sl2, vis);
         }
-        l = l * f + weights(s_col, part, vis, sl2, ms);
+        // 64 scores at a time; their 32 columns of weights go over scores that have been read.  (A loop: unrolled
+        // over the tile it is more code than the instruction cache holds beside the other warps', and the
+        // warp that issues the products starves.)
+        const uint64_t scale = pair(sl2, sl2);
+        uint64_t sum[2] = {0, 0};
+        uint32_t r[2][32];
+        ld_begin(s_col, r[0]);
+        ld_begin(s_col + 32, r[1]);
+#pragma unroll 1
+        for (int c = 0; c < 2; ++c) {
+          ld_wait(r[0]);
+          ld_wait(r[1]);
+          if (part) {
+            hide(r[0], c ? vis[2] : vis[0]);
+            hide(r[1], c ? vis[3] : vis[1]);
+          }
+          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int i = 0; i < 32; i += 4)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) m4[e] = max3(m4[e], __uint_as_float(r[0][i + e]), __uint_as_float(r[1][i + e]));
+          const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+          const bool grow = mx > m && (m == -INFINITY || (mx - m) * sl2 > kGrow);
+          if (__any_sync(0xffffffffu, grow)) {
+            const bool from = m != -INFINITY;
+            const float f = grow && from ? ex2((m - mx) * sl2) : 1.f;
+            if (grow) m = mx;
+            if (__any_sync(0xffffffffu, grow && from)) {
+              // what refers to the old maximum: O, the sums, and this tile's first weights
+              if (wrote) {
+                ok = __all_sync(0xffffffffu, ok && tc::mbar_wait(&sm.pv_done[tile], (pv_n - 1) & 1, P.wait_ns));
+                if (!ok) break;
+                tc::fence_after();
+              }
+              if (wrote || any_bad) scale_o<D>(o_col, true, f);
+              if (c) scale_p(s_col, f);
+              l *= f;
+              sum[0] = mul2(sum[0], pair(f, f));
+              sum[1] = mul2(sum[1], pair(f, f));
+            }
+          }
+          const float ms = m == -INFINITY ? 0.f : -m * sl2;
+          const uint64_t shift = pair(ms, ms);
+          float u[32];
+          weights32(r[0], scale, shift, sum, u);
+          if (c == 0) ld_begin(s_col + 64, r[0]);
+          weights32(r[1], scale, shift, sum, u + 16);
+          if (c == 0) ld_begin(s_col + 96, r[1]);
+          tc::tmem_st32(s_col + 32 * c, u);
+        }
+        if (!ok) break;
+        {
+          float a, b2;
+          unpair(add2(sum[0], sum[1]), a, b2);
+          l += a + b2;
+        }
         tc::tmem_st_wait();
         if (NT == 1 && wrote) {
           // The product of the tile before: the next one begins only after this, so that no phase of
