@@ -1,12 +1,13 @@
 // gdn_attn_prompt.cu -- attention of prompt rows over the paged cache on tcgen05 (bf16, d = 64, 128, 256).
 //
 // A tile of M = 128 queries is 128 consecutive (new token, q-head of the kv-head) pairs of a row, so
-// the q-heads that share a kv-head share its keys and values in shared memory.  Per 128 cached tokens
-//   S = Q K^T (128 x 128, fp32 in TMEM),  P = 2^(scale log2e (S - m)) (bf16, over S in TMEM),
+// the q-heads that share a kv-head share its keys and values in shared memory.  Per 64 cached tokens
+//   S = Q K^T (128 x 64, fp32 in TMEM),  P = 2^(scale log2e (S - m)) (bf16, over S in TMEM),
 //   O += P V (128 x d, fp32 in TMEM; A = P from TMEM, B = V read MN-major from its [token][d] tile).
-// 4 d flops per score against about 5 issue slots of softmax: the tensor core bounds it once both run
-// side by side.  So a CTA holds two query tiles (d <= 128; their S and O fill the 512 TMEM columns) and
-// the products of one run under the softmax of the other; at d = 256 one tile with two S buffers.
+// 4 d flops per score against about 4 issue slots of softmax: the tensor core bounds it once both run
+// side by side.  So a CTA holds two query tiles (d <= 128; one at d = 256) with two score buffers each, and the
+// products of the next scores run under the softmax of these.  (With 128 tokens a step there is room for one
+// buffer per tile: a tile's products and softmax then take turns, and the tensor core idled half the time.)
 //   warps 0-3 (and 4-7): softmax of tile 0 (1), a thread per query;
 //   then a warp that issues all products, one that fetches pages by TMA, two that look after V tiles
 //   of which some query must not see some token (below).
@@ -33,7 +34,7 @@ namespace gdn {
 namespace {
 
 constexpr int kSms = 152;
-constexpr int kTN = 128;        // cached tokens of a tile
+constexpr int kTN = 64;         // cached tokens of a tile
 constexpr int kMaxPieces = 16;
 constexpr float kGrow = 64.f;   // log2 of how far weights may outgrow their reference
 
@@ -44,11 +45,11 @@ struct Cfg {
   static constexpr int kThreads = 128 * (kTiles + 1);
   static constexpr uint32_t kQ = 128 * D * 2;                        // bytes of a query tile
   static constexpr uint32_t kKv = kTN * D * 2;                       // bytes of a K or V tile
-  static constexpr int kPhases = D <= 128 ? 2 : 1;                   // K and V pairs in the ring
+  static constexpr int kPhases = D <= 128 ? 4 : 2;                   // K and V pairs in the ring
   static constexpr int kRing = 2 * kPhases;                          // K and V tiles in turn
   static constexpr uint32_t kSmem = kTiles * kQ + kRing * kKv;
-  static constexpr int kO = 256;                                     // first O column of TMEM; S at 0 and 128
-  static_assert(kSmem + 2048 <= 232448, "shared memory");
+  static constexpr int kO = 256;                                     // first O column of TMEM; S of tile i at 128 i
+  static_assert(kSmem + 4096 <= 232448, "shared memory");
 };
 
 struct PromptParams {
@@ -148,58 +149,41 @@ __device__ __forceinline__ float pack2f(float lo, float hi) {
 __device__ __forceinline__ bool not_finite2(uint32_t x) {
   return (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u;
 }
-// Products, issued by the one lane whose `leader` is set while the warp goes together: in a branch of one
-// lane the compiler moves every descriptor to uniform registers anew, which takes longer than a product.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate,
-                                       uint32_t leader) {
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(leader));
-}
 // D (TMEM) += A (TMEM) B: A's row m is lane m, two bf16 of K per column.
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate,
-                                       uint32_t leader) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(leader));
-}
-__device__ __forceinline__ void commit_by(uint64_t* bar, uint32_t leader) {
-  asm volatile(
-      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
-      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(tc::smem_addr(bar)),
-      "r"(leader)
-      : "memory");
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate));
 }
 
-// The products of query tile TILE with the K (V) tile of ring phase PHASE.  All addresses are constants, TMEM's
-// as well (all 512 columns are this CTA's, from 0 on), so that a product costs an instruction and not the
-// moves that bring its operands together (85 cycles each that way, 64 of them the product's own).
-template <int D, int TILE, int SLOT, int PHASE, typename S>
-__device__ __forceinline__ void s_products(uint8_t* smem, S& sm, uint32_t leader) {
+// The products of query tile TILE with the K (V) tile of a ring phase, whose parity is the score buffer.
+template <int D, int TILE, typename S>
+__device__ __forceinline__ void s_products(uint8_t* smem, S& sm, uint32_t phase) {
   using C = Cfg<D>;
   const uint32_t base = tc::smem_addr(smem);
   const uint64_t q = tc::sdesc(base + TILE * C::kQ, 1024);
-  const uint64_t k = tc::sdesc(base + C::kTiles * C::kQ + 2 * PHASE * C::kKv, D / 64 * 1024);
+  const uint64_t k = tc::sdesc(base + C::kTiles * C::kQ + 2 * phase * C::kKv, D / 64 * 1024);
+  const uint32_t to = TILE * 128 + (phase & 1) * 64;
 #pragma unroll
   for (int s = 0; s < D / 16; ++s)
-    mma_ss(SLOT * 128, q + ((s >> 2) * 16384 + (s & 3) * 32) / 16, k + ((s >> 2) * 1024 + (s & 3) * 32) / 16,
-           tc::idesc_bf16(128, kTN), s > 0, leader);
-  commit_by(&sm.s_ready[SLOT], leader);
-  if (TILE == C::kTiles - 1) commit_by(&sm.empty[2 * PHASE], leader);
+    tc::mma(to, q + ((s >> 2) * 16384 + (s & 3) * 32) / 16, k + ((s >> 2) * 1024 + (s & 3) * 32) / 16,
+            tc::idesc_bf16(128, kTN), s > 0);
+  tc::commit(&sm.s_ready[TILE][phase & 1]);
+  if (TILE == C::kTiles - 1) tc::commit(&sm.empty[2 * phase]);
 }
-template <int D, int TILE, int SLOT, int PHASE, typename S>
-__device__ __forceinline__ void pv_products(uint8_t* smem, S& sm, bool onto, uint32_t leader) {
+template <int D, int TILE, typename S>
+__device__ __forceinline__ void pv_products(uint8_t* smem, S& sm, bool onto, uint32_t phase) {
   using C = Cfg<D>;
   const uint32_t base = tc::smem_addr(smem);
-  const uint64_t v = tc::sdesc_lbo(base + C::kTiles * C::kQ + (2 * PHASE + 1) * C::kKv, 1024, D / 64 * 1024);
+  const uint64_t v = tc::sdesc_lbo(base + C::kTiles * C::kQ + (2 * phase + 1) * C::kKv, 1024, D / 64 * 1024);
+  const uint32_t from = TILE * 128 + (phase & 1) * 64;
 #pragma unroll
   for (int s = 0; s < kTN / 16; ++s)
-    mma_ts(C::kO + TILE * D, SLOT * 128 + s * 8, v + s * 2 * (D / 64) * 1024 / 16, tc::idesc_bf16_bmn(128, D),
-           s == 0 ? (uint32_t)onto : 1u, leader);
-  commit_by(&sm.pv_done[TILE], leader);
-  if (TILE == C::kTiles - 1) commit_by(&sm.empty[2 * PHASE + 1], leader);
+    mma_ts(C::kO + TILE * D, from + s * 8, v + s * 2 * (D / 64) * 1024 / 16, tc::idesc_bf16_bmn(128, D),
+           s == 0 ? (uint32_t)onto : 1u);
+  tc::commit(&sm.pv_done[TILE][phase & 1]);
+  if (TILE == C::kTiles - 1) tc::commit(&sm.empty[2 * phase + 1]);
 }
 
 // Items of all rows; sum: one value per warp.  All threads call.
@@ -269,23 +253,17 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-
-// Bits [0, n) of four words.
+// Bits [0, n) of a run of words.
 __device__ __forceinline__ uint32_t low_bits(int n, int word) {
   const int k = min(max(n - 32 * word, 0), 32);
   return k == 32 ? 0xffffffffu : (1u << k) - 1u;
 }
 
-// The tokens of tile [b, b + 128) that a query at `pos` sees, a bit each.
+// The tokens of tile [b, b + 64) that a query at `pos` sees, a bit each.
 __device__ __forceinline__ void visible(const AttnLaunch& p, int b, int pos, uint32_t have, bool all_pages, int bshift,
-                                        uint32_t (&vis)[4]) {
+                                        uint32_t (&vis)[2]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 2; ++i) {
     uint32_t x = low_bits(pos + 1 - b, i);
     if (p.window > 0) x &= ~low_bits(pos - p.window + 1 - b, i) | low_bits(p.sinks - b, i);
     if (!all_pages) {
@@ -318,52 +296,48 @@ __device__ __forceinline__ void weights32(const uint32_t (&r)[32], uint64_t scal
   }
 }
 
-// O (D columns from o_col on) times f; zeros where it holds nothing yet.
+// O times f.
 template <int D>
-__device__ __forceinline__ void scale_o(uint32_t o_col, bool wrote, float f) {
+__device__ __forceinline__ void scale_o(uint32_t o_col, float f) {
 #pragma unroll 1
   for (int c = 0; c < D; c += 32) {
     float o[32];
-    if (wrote) tc::tmem_ld32(o_col + c, o);
+    tc::tmem_ld32(o_col + c, o);
 #pragma unroll
-    for (int i = 0; i < 32; ++i) o[i] = wrote ? o[i] * f : 0.f;
+    for (int i = 0; i < 32; ++i) o[i] *= f;
     tc::tmem_st32(o_col + c, o);
   }
   tc::tmem_st_wait();
 }
 
-// 64 tokens' weights (32 columns of bf16 pairs) times f.
-__device__ __forceinline__ void scale_p(uint32_t col, float f) {
-  float u[32];
-  tc::tmem_ld32(col, u);
+template <int D>
+__device__ __forceinline__ void clear_o(uint32_t o_col) {
+  float o[32];
 #pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    const uint32_t x = __float_as_uint(u[i]);
-    u[i] = pack2f(__uint_as_float(x << 16) * f, __uint_as_float(x & 0xffff0000u) * f);
-  }
-  tc::tmem_st32(col, u);
+  for (int i = 0; i < 32; ++i) o[i] = 0.f;
+#pragma unroll 1
+  for (int c = 0; c < D; c += 32) tc::tmem_st32(o_col + c, o);
   tc::tmem_st_wait();
 }
 
-// Adds the listed tokens' share to O where the query sees them: their weights from S, their values from the
-// cache.  O is complete; the warp's lanes go together, as TMEM loads and stores need them all.
+// Adds the listed tokens' share to O where the query, at `pos`, sees them: their weights from P, their values from
+// the cache.  O is complete up to the tile before; the warp's lanes go together, as TMEM loads and stores need them all.
 template <int D>
-__device__ __forceinline__ void add_listed(const PromptParams& P, const Item& w, const uint32_t* bad, int b,
-                                           uint32_t s_col, uint32_t o_col, float sl2, float ms,
-                                           const uint32_t (&vis)[4]) {
-  const KvDev& kv = P.a.cache;
+__device__ __forceinline__ void add_listed(const AttnLaunch& p, const Item& w, const uint32_t (&bad)[2], int b, int pos,
+                                           uint32_t p_col, uint32_t o_col) {
+  const KvDev& kv = p.cache;
 #pragma unroll 1
   for (int t = 0; t < kTN; ++t) {
-    if (!(bad[t >> 5] >> (t & 31) & 1u)) continue;
-    float x[8], s = 0.f;
-    tc::tmem_ld8(s_col + (t & ~7), x);
+    if (!((t < 32 ? bad[0] : bad[1]) >> (t & 31) & 1u)) continue;
+    float x[8];
+    uint32_t u = 0;
+    tc::tmem_ld8(p_col + (t >> 1 & ~7), x);
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if ((t & 7) == i) s = x[i];
-    const uint32_t word = t < 64 ? (t < 32 ? vis[0] : vis[1]) : (t < 96 ? vis[2] : vis[3]);
-    const bool seen = word >> (t & 31) & 1u;
-    const float weight = ex2(fmaf(s, sl2, ms));
+      if ((t >> 1 & 7) == i) u = __float_as_uint(x[i]);
+    const float weight = __uint_as_float(t & 1 ? u & 0xffff0000u : u << 16);
     const int tok = b + t;  // below the row's end, in a page that is not NULL
+    const bool seen = tok <= pos && (p.window <= 0 || tok > pos - p.window || tok < p.sinks);
     const int page = kv.table[(int64_t)w.r.trow * kv.max_pages + tok / kv.page_size];
     const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(kv.v) + (int64_t)page * kv.page_stride +
                              ((int64_t)w.h * kv.page_size + tok % kv.page_size) * D;
@@ -384,9 +358,9 @@ template <int D>
 struct Small {
   uint64_t full[Cfg<D>::kRing], empty[Cfg<D>::kRing];
   uint64_t checked[Cfg<D>::kRing];  // of a V tile, by its entry
-  uint64_t q_ready, s_ready[2], p_ready[2], pv_done[2], drain;
+  uint64_t q_ready, s_ready[2][2], p_ready[2][2], pv_done[2][2], drain[2];  // [query tile][score buffer]
   int64_t sum[Cfg<D>::kThreads / 32];
-  uint32_t bad[Cfg<D>::kRing][4];  // listed tokens of a V tile
+  uint32_t bad[Cfg<D>::kRing][2];  // listed tokens of a V tile
   uint32_t held[16];               // per tile, counted over all items, % 16: which of its pages hold tokens
   uint32_t tmem;
 };
@@ -407,16 +381,16 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < R; ++i) {
       tc::mbar_init(&sm.full[i], 1);
-      tc::mbar_init(&sm.empty[i], 3);  // the products and both warps that look after V tiles
-      tc::mbar_init(&sm.checked[i], 2);
+      tc::mbar_init(&sm.empty[i], 2);  // the products and the warp that looks after V tiles
+      tc::mbar_init(&sm.checked[i], 1);
     }
     tc::mbar_init(&sm.q_ready, 128 * NT);
-    for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(&sm.s_ready[i], 1);
-      tc::mbar_init(&sm.p_ready[i], 128);
-      tc::mbar_init(&sm.pv_done[i], 1);
+    for (int i = 0; i < 4; ++i) {
+      tc::mbar_init(&sm.s_ready[i >> 1][i & 1], 1);
+      tc::mbar_init(&sm.p_ready[i >> 1][i & 1], 128);
+      tc::mbar_init(&sm.pv_done[i >> 1][i & 1], 1);
     }
-    tc::mbar_init(&sm.drain, 1);
+    for (int i = 0; i < 2; ++i) tc::mbar_init(&sm.drain[i], 1);
     tc::mbar_init_fence();
     tc::prefetch_map(&kmap);
     tc::prefetch_map(&vmap);
@@ -445,9 +419,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     uint8_t* qt = smem + tile * C::kQ;
     const uint32_t lane_base = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const uint32_t o_col = lane_base + C::kO + tile * D;
-    uint32_t s_n[2] = {0, 0};  // score tiles of a slot gone by
-    uint32_t pv_n = 0;         // products of the query tile gone by
-    uint32_t chk = 0;          // parity of checked[entry]
+    uint32_t chk = 0;  // parity of checked[entry]
     for (int64_t idx = blockIdx.x; idx < items && ok; idx += kSms) {
       if (!finder.find(idx, pieces, w)) break;
       const int qi = w.q0 + tile * 128 + row, nq = w.r.len * p.G;
@@ -471,126 +443,85 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       const int tmin = first + min(w.q0 + tile * 128, nq - 1) / p.G, cmin = first + w.q0 / p.G;
       const int tmax = min(first + (w.q0 + tile * 128 + 127) / p.G, w.r.kv - 1);
       float m = -INFINITY, l = 0.f;  // the maximum that the weights refer to (of scores before their scale); their sum
-      bool wrote = false;            // O holds something
+      bool wrote = false;            // O holds something, or will
       for (int j = w.j0; j < w.j1; ++j, at += 2, ++tiles) {
-        const int slot = NT == 2 ? tile : (j - w.j0) & 1;
-        const uint32_t s_col = lane_base + slot * 128, v_entry = (at + 1) % R;
+        // The buffer's use is number tiles / 2, that of the tile before (tiles - 1) / 2.  (These scores came
+        // behind the product two tiles before, so no phase of pv_done can be taken for another.)
+        const uint32_t buf = tiles & 1, v_entry = (at + 1) % R;
+        const uint32_t s_col = lane_base + tile * 128 + buf * 64;
         const int b = tile_at(w, j);
-        ok = __all_sync(0xffffffffu, ok && tc::mbar_wait(&sm.s_ready[slot], s_n[slot] & 1, P.wait_ns));
-        ++s_n[slot];
+        ok = __all_sync(0xffffffffu, ok && tc::mbar_wait(&sm.s_ready[tile][buf], (tiles >> 1) & 1, P.wait_ns));
         if (!ok) break;
         tc::fence_after();
+        uint32_t r[2][32];
+        ld_begin(s_col, r[0]);
+        ld_begin(s_col + 32, r[1]);
         const uint32_t have = sm.held[tiles & 15];
         const bool all_pages = have == (1u << boxes) - 1u;
         const bool part = !all_pages || in_part(p, b, tmin, tmax);
-        uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u};  // the tile's tokens that this query sees
-        if (part) visible(p, b, pos, have, all_pages, bshift, vis);
-        bool any_bad = false;  // the tile lists tokens
+        ld_wait(r[0]);
+        ld_wait(r[1]);
+        if (part) {
+          uint32_t vis[2];
+          visible(p, b, pos, have, all_pages, bshift, vis);
+          hide(r[0], vis[0]);
+          hide(r[1], vis[1]);
+        }
+        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int i = 0; i < 32; i += 4)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) m4[e] = max3(m4[e], __uint_as_float(r[0][i + e]), __uint_as_float(r[1][i + e]));
+        const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+        const bool grow = mx > m && (m == -INFINITY || (mx - m) * sl2 > kGrow);
+        if (__any_sync(0xffffffffu, grow)) {
+          const bool from = grow && m != -INFINITY;
+          const float f = from ? ex2((m - mx) * sl2) : 1.f;
+          if (grow) m = mx;
+          l *= f;
+          if (wrote && __any_sync(0xffffffffu, from)) {
+            // O is complete when the product of the tile before is
+            ok = __all_sync(0xffffffffu, ok && tc::mbar_wait(&sm.pv_done[tile][buf ^ 1], ((tiles - 1) >> 1) & 1, P.wait_ns));
+            if (!ok) break;
+            tc::fence_after();
+            scale_o<D>(o_col, f);
+          }
+        }
+        const float ms = m == -INFINITY ? 0.f : -m * sl2;
+        const uint64_t scale = pair(sl2, sl2), shift = pair(ms, ms);
+        uint64_t sum[2] = {0, 0};
+        float u[32];
+        weights32(r[0], scale, shift, sum, u);
+        weights32(r[1], scale, shift, sum, u + 16);
+        tc::tmem_st32(s_col, u);
+        {
+          float a0, a1;
+          unpair(add2(sum[0], sum[1]), a0, a1);
+          l += a0 + a1;
+        }
+        tc::tmem_st_wait();
         if (in_part(p, b, cmin, w.last)) {
           ok = __all_sync(0xffffffffu, ok && tc::mbar_wait(&sm.checked[v_entry], (chk >> v_entry) & 1, P.wait_ns));
           chk ^= 1u << v_entry;
           if (!ok) break;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) any_bad |= sm.bad[v_entry][i] != 0;
-        }
-        if (any_bad) {
-          // O by hand: complete when the product of the tile before is; the scores must not be overwritten yet,
-          // nor refer to another maximum afterwards
-          if (wrote) {
-            ok = __all_sync(0xffffffffu, ok && tc::mbar_wait(&sm.pv_done[tile], (pv_n - 1) & 1, P.wait_ns));
+          const uint32_t bad[2] = {sm.bad[v_entry][0], sm.bad[v_entry][1]};
+          if ((bad[0] | bad[1]) != 0) {
+            if (wrote)
+              ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.pv_done[tile][buf ^ 1], ((tiles - 1) >> 1) & 1, P.wait_ns));
             if (!ok) break;
             tc::fence_after();
+            if (!wrote) clear_o<D>(o_col);
+            add_listed<D>(p, w, bad, b, pos, s_col, o_col);
           }
-          float mx = -INFINITY;
-#pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            uint32_t r[32];
-            ld_begin(s_col + 32 * c, r);
-            ld_wait(r);
-            hide(r, c < 2 ? (c ? vis[1] : vis[0]) : (c == 3 ? vis[3] : vis[2]));
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) mx = max3(mx, __uint_as_float(r[i]), __uint_as_float(r[i + 1]));
-          }
-          float f = 1.f;
-          if (mx > m) {
-            f = m == -INFINITY ? 1.f : ex2((m - mx) * sl2);
-            m = mx;
-          }
-          l *= f;
-          scale_o<D>(o_col, wrote, f);
-          add_listed<D>(P, w, sm.bad[v_entry], b, s_col, o_col, sl2, m == -INFINITY ? 0.f : -m * sl2, vis);
-        }
-        // 64 scores at a time; their 32 columns of weights go over scores that have been read.  (A loop: unrolled
-        // over the tile it is more code than the instruction cache holds beside the other warps', and the
-        // warp that issues the products starves.)
-        const uint64_t scale = pair(sl2, sl2);
-        uint64_t sum[2] = {0, 0};
-        uint32_t r[2][32];
-        ld_begin(s_col, r[0]);
-        ld_begin(s_col + 32, r[1]);
-#pragma unroll 1
-        for (int c = 0; c < 2; ++c) {
-          ld_wait(r[0]);
-          ld_wait(r[1]);
-          if (part) {
-            hide(r[0], c ? vis[2] : vis[0]);
-            hide(r[1], c ? vis[3] : vis[1]);
-          }
-          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int i = 0; i < 32; i += 4)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) m4[e] = max3(m4[e], __uint_as_float(r[0][i + e]), __uint_as_float(r[1][i + e]));
-          const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-          const bool grow = mx > m && (m == -INFINITY || (mx - m) * sl2 > kGrow);
-          if (__any_sync(0xffffffffu, grow)) {
-            const bool from = m != -INFINITY;
-            const float f = grow && from ? ex2((m - mx) * sl2) : 1.f;
-            if (grow) m = mx;
-            if (__any_sync(0xffffffffu, grow && from)) {
-              // what refers to the old maximum: O, the sums, and this tile's first weights
-              if (wrote) {
-                ok = __all_sync(0xffffffffu, ok && tc::mbar_wait(&sm.pv_done[tile], (pv_n - 1) & 1, P.wait_ns));
-                if (!ok) break;
-                tc::fence_after();
-              }
-              if (wrote || any_bad) scale_o<D>(o_col, true, f);
-              if (c) scale_p(s_col, f);
-              l *= f;
-              sum[0] = mul2(sum[0], pair(f, f));
-              sum[1] = mul2(sum[1], pair(f, f));
-            }
-          }
-          const float ms = m == -INFINITY ? 0.f : -m * sl2;
-          const uint64_t shift = pair(ms, ms);
-          float u[32];
-          weights32(r[0], scale, shift, sum, u);
-          if (c == 0) ld_begin(s_col + 64, r[0]);
-          weights32(r[1], scale, shift, sum, u + 16);
-          if (c == 0) ld_begin(s_col + 96, r[1]);
-          tc::tmem_st32(s_col + 32 * c, u);
-        }
-        if (!ok) break;
-        {
-          float a, b2;
-          unpair(add2(sum[0], sum[1]), a, b2);
-          l += a + b2;
-        }
-        tc::tmem_st_wait();
-        if (NT == 1 && wrote) {
-          // The product of the tile before: the next one begins only after this, so that no phase of
-          // pv_done is taken for another.  (With two query tiles these scores came behind it.)
-          ok = __all_sync(0xffffffffu, ok && tc::mbar_wait(&sm.pv_done[tile], (pv_n - 1) & 1, P.wait_ns));
-          if (!ok) break;
         }
         tc::fence_before();
-        tc::mbar_arrive(&sm.p_ready[slot]);
-        ++pv_n;
+        tc::mbar_arrive(&sm.p_ready[tile][buf]);
         wrote = true;
       }
       if (!ok) break;
       if (wrote) {
-        ok = __all_sync(0xffffffffu, ok && tc::mbar_wait(&sm.pv_done[tile], (pv_n - 1) & 1, P.wait_ns));
+        ok = __all_sync(0xffffffffu,
+                        ok && tc::mbar_wait(&sm.pv_done[tile][(tiles - 1) & 1], ((tiles - 1) >> 1) & 1, P.wait_ns));
         if (!ok) break;
         tc::fence_after();
       }
@@ -620,77 +551,65 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       if (pieces > 1) *reinterpret_cast<float2*>(P.stats + part_row * 2) = make_float2(m, l);
     }
     if (!ok) set_status(p.status, GDN_STATUS_WAIT_TIMEOUT);
-  } else if (role == 0) {
-    // ---- products: one lane issues them all ----
-    uint32_t p_n[2] = {0, 0}, chk = 0, items_n = 0;
+  } else if (role <= 1) {
+    // ---- products: one lane of warp 0 issues all S = Q K^T, one of warp 1 all O += P V ----
+    uint32_t items_n = 0;
+    uint32_t chk = 0;  // parity of checked, a bit per ring phase
     // (a phase of a barrier; false once a wait has given up)
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-      ok = __all_sync(0xffffffffu, ok && tc::mbar_wait(bar, parity & 1, P.wait_ns));
+      ok = ok && tc::mbar_wait(bar, parity & 1, P.wait_ns);
       if (ok) tc::fence_after();
       return ok;
     };
-    const uint32_t leader = lane == 0;
-    auto issue_s = [&](auto tile, auto slot, uint32_t k_at) {
-      if (tile() == 0 && !wait(&sm.full[k_at % R], k_at / R)) return;
-      if (C::kPhases == 1 || k_at % R == 0)
-        s_products<D, tile(), slot(), 0>(smem, sm, leader);
-      else
-        s_products<D, tile(), slot(), C::kPhases - 1>(smem, sm, leader);
-    };
-    auto issue_pv = [&](auto tile, auto slot, uint32_t v_at, bool onto) {
-      if (C::kPhases == 1 || v_at % R == 1)
-        pv_products<D, tile(), slot(), 0>(smem, sm, onto, leader);
-      else
-        pv_products<D, tile(), slot(), C::kPhases - 1>(smem, sm, onto, leader);
-    };
-    constexpr std::integral_constant<int, 0> zero{};
-    constexpr std::integral_constant<int, 1> one{};
     for (int64_t idx = blockIdx.x; idx < items && ok; idx += kSms, ++items_n) {
       if (!finder.find(idx, pieces, w)) break;
-      if (!wait(&sm.q_ready, items_n)) break;
-      const int n = w.j1 - w.j0;
-      if (n == 0) continue;
-      const int cmin = w.r.kv - w.r.len + w.q0 / p.G;
-      issue_s(zero, zero, at);
-      if constexpr (NT == 2) {
-        if (ok) issue_s(one, one, at);
-      }
-      for (int j = 0; j < n && ok; ++j, at += 2) {
-        const uint32_t v_at = at + 1, k_next = at + 2, odd = j & 1;
-        const bool checked = in_part(p, tile_at(w, w.j0 + j), cmin, w.last), more = j + 1 < n;
-        if constexpr (NT == 1) {
-          if (more) {  // the next scores run under this tile's softmax
-            if (odd) issue_s(zero, zero, k_next); else issue_s(zero, one, k_next);
-            if (!ok) break;
+      const int n = w.j1 - w.j0, cmin = w.r.kv - w.r.len + w.q0 / p.G;
+      if (lane == 0 && role == 0 && wait(&sm.q_ready, items_n)) {
+        for (int j = 0; j < n && ok; ++j) {
+          const uint32_t t = tiles + j, buf = t & 1, phase = t % C::kPhases;
+          if (!wait(&sm.full[2 * phase], t / C::kPhases)) break;
+          // the buffer is free once the product two tiles before is done
+          if (t >= 2 && !wait(&sm.pv_done[0][buf], (t >> 1) - 1)) break;
+          s_products<D, 0>(smem, sm, phase);
+          if constexpr (NT == 2) {
+            if (t >= 2 && !wait(&sm.pv_done[1][buf], (t >> 1) - 1)) break;
+            s_products<D, 1>(smem, sm, phase);
           }
         }
-        const uint32_t first = NT == 2 ? 0 : odd;  // the slot of query tile 0
-        if (!wait(&sm.p_ready[first], p_n[first]++) || !wait(&sm.full[v_at % R], v_at / R)) break;
-        bool onto = j > 0;
-        if (checked) {
-          if (!wait(&sm.checked[v_at % R], chk >> (v_at % R))) break;
-          chk ^= 1u << (v_at % R);
-          for (int e = 0; e < 4; ++e) onto |= sm.bad[v_at % R][e] != 0;  // the softmax has begun O
-        }
-        if constexpr (NT == 1) {
-          if (odd) issue_pv(zero, one, v_at, onto); else issue_pv(zero, zero, v_at, onto);
-        } else {
-          issue_pv(zero, zero, v_at, onto);
-          if (more) issue_s(zero, zero, k_next);
-          if (!ok || !wait(&sm.p_ready[1], p_n[1]++)) break;
-          issue_pv(one, one, v_at, onto);
-          if (more) issue_s(one, one, k_next);
+      }
+      if (lane == 0 && role == 1) {
+        for (int j = 0; j < n && ok; ++j) {
+          const uint32_t t = tiles + j, buf = t & 1, phase = t % C::kPhases;
+          bool onto = j > 0;
+          if (!wait(&sm.full[2 * phase + 1], t / C::kPhases)) break;
+          if (in_part(p, tile_at(w, w.j0 + j), cmin, w.last)) {
+            if (!wait(&sm.checked[2 * phase + 1], chk >> phase)) break;
+            chk ^= 1u << phase;
+            onto |= (sm.bad[2 * phase + 1][0] | sm.bad[2 * phase + 1][1]) != 0;  // O holds these tokens' share by then
+          }
+          if (!wait(&sm.p_ready[0][buf], t >> 1)) break;
+          pv_products<D, 0>(smem, sm, onto, phase);
+          if constexpr (NT == 2) {
+            if (!wait(&sm.p_ready[1][buf], t >> 1)) break;
+            pv_products<D, 1>(smem, sm, onto, phase);
+          }
         }
       }
+      ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+      tiles += n;
     }
-    commit_by(&sm.drain, leader);
-    if (!tc::mbar_wait(&sm.drain, 0, P.wait_ns)) ok = false;
-    if (!ok) set_status(p.status, GDN_STATUS_WAIT_TIMEOUT);
-  } else if (role == 1) {
+    if (lane == 0) {
+      tc::commit(&sm.drain[role]);
+      if (!tc::mbar_wait(&sm.drain[role], 0, P.wait_ns)) ok = false;
+      if (!ok) set_status(p.status, GDN_STATUS_WAIT_TIMEOUT);
+    }
+    __syncwarp();
+  } else if (role == 2) {
     // ---- fetches: a lane per page of the tile ----
     const int bi = lane, spp = slabs_per_page(kv);
     const int none = (kv.num_pages - 1) * spp + kv.Hkv;  // a slab past the pool
     const bool active = bi < boxes;
+    uint32_t fetched = 0;  // tiles fetched, K and V
     for (int64_t idx = blockIdx.x; idx < items && ok; idx += kSms) {
       if (!finder.find(idx, pieces, w)) break;
       const int32_t* row = kv.table + (int64_t)w.r.trow * kv.max_pages;
@@ -723,17 +642,19 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
           if (active)
             tc::tma_page(ring + en * C::kKv + bi * box * D * 2, v ? &vmap : &kmap, pos & (ps - 1),
                          page > 0 ? page * spp + w.h : none, &sm.full[en]);
+          fetched = a + 1;
         }
         if (!ok) break;
       }
     }
     // No copy may be in flight when the CTA ends (the products wait for every tile, so this passes at
     // once unless a wait gave up).
-    for (uint32_t a = at > (uint32_t)R ? at - R : 0; a < at; ++a) ok &= tc::mbar_wait(&sm.full[a % R], (a / R) & 1, P.wait_ns);
+    for (uint32_t a = fetched > (uint32_t)R ? fetched - R : 0; a < fetched; ++a)
+      ok &= tc::mbar_wait(&sm.full[a % R], (a / R) & 1, P.wait_ns);
     if (!ok) set_status(p.status, GDN_STATUS_WAIT_TIMEOUT);
   } else {
-    // ---- V tiles that some query sees in part: 64 tokens of each ----
-    // (these warps go through every phase of the ring, so that none is taken for another)
+    // ---- V tiles that some query sees in part ----
+    // (this warp goes through every phase of the ring, so that none is taken for another)
     for (int64_t idx = blockIdx.x; idx < items && ok; idx += kSms) {
       if (!finder.find(idx, pieces, w)) break;
       const int cmin = w.r.kv - w.r.len + w.q0 / p.G;
@@ -750,7 +671,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         if (!ok || !look) continue;
 #pragma unroll 1
         for (int u = 0; u < 2; ++u) {
-          const int t = (role - 2) * 64 + u * 32 + lane;
+          const int t = u * 32 + lane;
           uint8_t* v = ring + en * C::kKv + (t >> 3) * CB * 1024 + (t & 7) * 128;
           bool odd = false;
           const bool past = b + t >= w.r.kv;
@@ -763,7 +684,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             for (int c = 0; c < D / 8; ++c)
               *reinterpret_cast<uint4*>(v + (c >> 3) * 1024 + (((c & 7) ^ (t & 7)) << 4)) = make_uint4(0, 0, 0, 0);
           const uint32_t list = __ballot_sync(0xffffffffu, odd && !past);
-          if (lane == 0) sm.bad[en][(role - 2) * 2 + u] = list;
+          if (lane == 0) sm.bad[en][u] = list;
         }
         tc::fence_async_smem();
         __syncwarp();
