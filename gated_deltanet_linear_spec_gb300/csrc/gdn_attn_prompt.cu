@@ -21,9 +21,11 @@
 // that some query sees only in part, values past the row's end are zeroed, and a token whose values hold an
 // infinity or NaN is zeroed and listed; queries that do see it add its share to O by hand.
 //
-// Work items (row, 256 or 128 queries, kv-head), the longest of a row first, go round the CTAs.  When
-// there are too few to fill the GPU, the cache of each is cut into up to 16 pieces whose (m, l, o) meet
-// in a second launch, in order.
+// Work items (row, 256 or 128 queries, kv-head), the longest of a row first, go to the CTAs in rounds, every
+// other round in reverse order, so that who had the longest of one has the shortest of the next (1024 items of
+// 1 to 128 steps: 443 steps at most, 434.5 on average; 497 without).  The items that are left for a last round
+// are too few to fill the GPU: the cache of each is cut into up to 16 pieces, whose (m, l, o) meet in a second
+// launch, in order.
 #include <algorithm>
 #include <type_traits>
 
@@ -54,7 +56,7 @@ struct Cfg {
 
 struct PromptParams {
   AttnLaunch a;
-  int max_pieces;  // of an item
+  int max_pieces;  // of an item of the last round
   float* part;     // [kSms][kRows][D]
   float* stats;    // [kSms][kRows][2]
   uint64_t wait_ns;
@@ -65,7 +67,8 @@ struct Item {
   int q0;      // first (token, q-head) pair
   int h;
   int sink_tiles, first_tile, tiles;  // of its cached tokens, all pieces
-  int j0, j1;  // this piece
+  int pieces;  // > 1: this is one of several
+  int j0, j1;  // its tiles
   int low;     // first position that some query sees behind the sinks
   int last;    // position of its last query
 };
@@ -81,7 +84,17 @@ __device__ __forceinline__ int64_t items_of(const AttnLaunch& p, int n, uint32_t
   return ((int64_t)r.len * p.G + ROWS - 1) / ROWS * p.cache.Hkv;
 }
 
-// Finds items in increasing order; a warp holds 32 rows, one per lane.  All lanes call together.
+// How the items are dealt: `full` rounds of one per CTA, and a last one of the items left, cut into pieces.
+struct Plan {
+  int full, left, pieces;
+};
+__host__ __device__ inline Plan plan_of(int64_t items, int most) {
+  Plan plan{(int)(items / kSms), (int)(items % kSms), 1};
+  if (plan.left > 0) plan.pieces = most < kSms / plan.left ? most : kSms / plan.left;
+  return plan;
+}
+
+// Finds items in increasing order of rounds; a warp holds 32 rows, one per lane.  All lanes call together.
 template <int ROWS>
 struct Finder {
   const AttnLaunch& p;
@@ -91,10 +104,18 @@ struct Finder {
   KvRow row;
   __device__ explicit Finder(const AttnLaunch& launch) : p(launch) { load(); }
   __device__ void load() { mine = items_of<ROWS>(p, base + (int)(threadIdx.x & 31), nullptr, row); }
-  __device__ bool find(int64_t idx, int pieces, Item& w) {
+  // CTA cta's item of a round; false: it has none
+  __device__ bool find(const Plan& plan, int round, int cta, Item& w) {
     const int lane = threadIdx.x & 31;
-    const int64_t item = idx / pieces;
-    const int piece = (int)(idx - item * pieces);
+    int64_t item = (int64_t)round * kSms + (round & 1 ? kSms - 1 - cta : cta);
+    int piece = 0;
+    w.pieces = 1;
+    if (round == plan.full) {
+      if (cta >= plan.left * plan.pieces) return false;
+      w.pieces = plan.pieces;
+      item = (int64_t)round * kSms + cta / plan.pieces;
+      piece = cta % plan.pieces;
+    }
     while (true) {
       int64_t inc = mine;
 #pragma unroll
@@ -119,8 +140,8 @@ struct Finder {
         w.sink_tiles = (min(p.sinks, w.low) + kTN - 1) / kTN;
         w.first_tile = max(w.low / kTN, w.sink_tiles);
         w.tiles = w.sink_tiles + w.last / kTN + 1 - w.first_tile;
-        w.j0 = (int)((int64_t)w.tiles * piece / pieces);
-        w.j1 = (int)((int64_t)w.tiles * (piece + 1) / pieces);
+        w.j0 = (int)((int64_t)w.tiles * piece / w.pieces);
+        w.j1 = (int)((int64_t)w.tiles * (piece + 1) / w.pieces);
         return true;
       }
       before += __shfl_sync(0xffffffffu, inc, 31);
@@ -205,10 +226,6 @@ __device__ int64_t count_items(const AttnLaunch& p, int64_t* sum) {
   for (int i = 0; i < THREADS / 32; ++i) items += sum[i];
   return items;
 }
-__device__ __forceinline__ int pieces_of(int64_t items, int most) {
-  return items == 0 ? 1 : (int)min((int64_t)most, max((int64_t)1, (int64_t)kSms / items));
-}
-
 // 32 columns of this thread's TMEM lane: the load is on its way until ld_wait, which the values pass through.
 __device__ __forceinline__ void ld_begin(uint32_t a, uint32_t (&r)[32]) {
   asm volatile(
@@ -397,10 +414,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
   }
   if (warp == 4 * NT) tc::tmem_alloc(&sm.tmem, 512);
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  // how many items there are, and into how many pieces each is cut
-  int64_t items = count_items<C::kRows, C::kThreads>(p, sm.sum);
-  const int pieces = pieces_of(items, P.max_pieces);
-  items *= pieces;
+  const Plan plan = plan_of(count_items<C::kRows, C::kThreads>(p, sm.sum), P.max_pieces);
   const uint32_t tmem = sm.tmem;
   const int ps = kv.page_size, shift = __ffs(ps) - 1, box = min(ps, kTN), boxes = kTN / box;
   const int bshift = __ffs(box) - 1;
@@ -420,8 +434,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     const uint32_t lane_base = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const uint32_t o_col = lane_base + C::kO + tile * D;
     uint32_t chk = 0;  // parity of checked[entry]
-    for (int64_t idx = blockIdx.x; idx < items && ok; idx += kSms) {
-      if (!finder.find(idx, pieces, w)) break;
+    for (int round = 0; round <= plan.full && ok; ++round) {
+      if (!finder.find(plan, round, blockIdx.x, w)) break;
       const int qi = w.q0 + tile * 128 + row, nq = w.r.len * p.G;
       int g = -1;
       if (qi < nq) g = global_token(RowsDev{nullptr, p.rows.tok}, w.r.bos + qi / p.G, p.num_global, p.status);
@@ -537,7 +551,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] = 0.f;
         }
-        if (pieces > 1) {
+        if (w.pieces > 1) {
           float4* dst = reinterpret_cast<float4*>(P.part + part_row * D + c);
 #pragma unroll
           for (int i = 0; i < 8; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
@@ -548,12 +562,11 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
           for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(out + c + 8 * i) = tc::pack8(o + 8 * i);
         }
       }
-      if (pieces > 1) *reinterpret_cast<float2*>(P.stats + part_row * 2) = make_float2(m, l);
+      if (w.pieces > 1) *reinterpret_cast<float2*>(P.stats + part_row * 2) = make_float2(m, l);
     }
     if (!ok) set_status(p.status, GDN_STATUS_WAIT_TIMEOUT);
   } else if (role <= 1) {
     // ---- products: one lane of warp 0 issues all S = Q K^T, one of warp 1 all O += P V ----
-    uint32_t items_n = 0;
     uint32_t chk = 0;  // parity of checked, a bit per ring phase
     // (a phase of a barrier; false once a wait has given up)
     auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -561,10 +574,10 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       if (ok) tc::fence_after();
       return ok;
     };
-    for (int64_t idx = blockIdx.x; idx < items && ok; idx += kSms, ++items_n) {
-      if (!finder.find(idx, pieces, w)) break;
+    for (int round = 0; round <= plan.full && ok; ++round) {
+      if (!finder.find(plan, round, blockIdx.x, w)) break;
       const int n = w.j1 - w.j0, cmin = w.r.kv - w.r.len + w.q0 / p.G;
-      if (lane == 0 && role == 0 && wait(&sm.q_ready, items_n)) {
+      if (lane == 0 && role == 0 && wait(&sm.q_ready, round)) {
         for (int j = 0; j < n && ok; ++j) {
           const uint32_t t = tiles + j, buf = t & 1, phase = t % C::kPhases;
           if (!wait(&sm.full[2 * phase], t / C::kPhases)) break;
@@ -610,8 +623,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     const int none = (kv.num_pages - 1) * spp + kv.Hkv;  // a slab past the pool
     const bool active = bi < boxes;
     uint32_t fetched = 0;  // tiles fetched, K and V
-    for (int64_t idx = blockIdx.x; idx < items && ok; idx += kSms) {
-      if (!finder.find(idx, pieces, w)) break;
+    for (int round = 0; round <= plan.full && ok; ++round) {
+      if (!finder.find(plan, round, blockIdx.x, w)) break;
       const int32_t* row = kv.table + (int64_t)w.r.trow * kv.max_pages;
       const int entries = (w.r.kv + ps - 1) >> shift;
       int eb = -64, ids = 0, ahead = 0;  // 32 table entries are held, one per lane, and the 32 behind them
@@ -655,8 +668,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
   } else {
     // ---- V tiles that some query sees in part ----
     // (this warp goes through every phase of the ring, so that none is taken for another)
-    for (int64_t idx = blockIdx.x; idx < items && ok; idx += kSms) {
-      if (!finder.find(idx, pieces, w)) break;
+    for (int round = 0; round <= plan.full && ok; ++round) {
+      if (!finder.find(plan, round, blockIdx.x, w)) break;
       const int cmin = w.r.kv - w.r.len + w.q0 / p.G;
       for (int j = w.j0; j < w.j1 && ok; ++j, at += 2) {
         const int b = tile_at(w, j);
@@ -713,12 +726,12 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(PromptParams P) {
   const AttnLaunch& p = P.a;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int64_t items = count_items<kRows, 256>(p, sum);
-  const int pieces = pieces_of(items, P.max_pieces);
-  if (pieces == 1 || (int64_t)blockIdx.x >= items) return;
+  const Plan plan = plan_of(count_items<kRows, 256>(p, sum), P.max_pieces);
+  const int pieces = plan.pieces;
+  if (pieces == 1 || (int)blockIdx.x >= plan.left) return;
   Finder<kRows> finder(p);
   Item w;
-  if (!finder.find((int64_t)blockIdx.x * pieces, pieces, w)) return;
+  if (!finder.find(plan, plan.full, blockIdx.x * pieces, w)) return;
   const float sl2 = p.scale * 1.4426950408889634f;
   const int lane = threadIdx.x & 31;
   for (int r = blockIdx.y * kJoinRows + (threadIdx.x >> 5); r < (int)(blockIdx.y + 1) * kJoinRows; r += 8) {
@@ -754,12 +767,11 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(PromptParams P) {
   }
 }
 
-// At least how many items there are when every row is good.
-int64_t least_items(const AttnLaunch& a, int rows) {
-  return ((int64_t)a.rows.num_tokens * a.G + rows - 1) / rows * a.cache.Hkv;
-}
+// The pieces that an item of the last round may be cut into: as the items of a single row say, any number when
+// there are several rows, whose lengths the host does not know.
 int max_pieces(const AttnLaunch& a, int rows) {
-  return (int)std::max<int64_t>(1, std::min<int64_t>(kMaxPieces, kSms / std::max<int64_t>(1, least_items(a, rows))));
+  if (a.rows.num_seqs > 1) return kMaxPieces;
+  return plan_of(((int64_t)a.rows.num_tokens * a.G + rows - 1) / rows * a.cache.Hkv, kMaxPieces).pieces;
 }
 
 template <int D>
