@@ -6,11 +6,16 @@
 //   O += P V (128 x d, fp32 in TMEM; A = P from TMEM, B = V read MN-major from its [token][d] tile).
 // 4 d flops per score against about 4 issue slots of softmax: the tensor core bounds it once both run
 // side by side.  So a CTA holds two query tiles (d <= 128; one at d = 256) with two score buffers each, and the
-// products of the next scores run under the softmax of these.  (With 128 tokens a step there is room for one
-// buffer per tile: a tile's products and softmax then take turns, and the tensor core idled half the time.)
+// next scores come up under the softmax of these.
 //   warps 0-3 (and 4-7): softmax of tile 0 (1), a thread per query;
-//   then a warp that issues all products, one that fetches pages by TMA, two that look after V tiles
-//   of which some query must not see some token (below).
+//   then a warp that issues all Q K^T, one that issues all P V, one that fetches pages by TMA, one that looks
+//   after V tiles of which some query must not see some token (below).
+// Measured on 8192 x 8192 (32 q-heads, 8 kv-heads, d = 128) on the way here: one warp for both products, which
+// waits and issues in turn while the tensor core idles, 591 us; a warp for each, 533; rounds dealt back and
+// forth (below), 471; the next item's queries fetched under the last output, 453 (1210 TFLOP/s).  128 tokens a
+// step with one score buffer per tile and a thread holding all 128 scores took 488: a tile's products and softmax
+// then follow one another, and what overlaps is the other tile's alone.  Of a step's 2000 cycles the products take
+// 1650: Q K^T with N = 64 reads 6 KB of shared memory per instruction, 52 cycles instead of 32.
 // P refers to a maximum that follows the running one only when that has grown by 2^64 or more: scaled by
 // a power of two, weights lose nothing in bf16 or fp32 before they overflow.  So S is read once, and O is
 // rescaled in TMEM next to never.
@@ -36,7 +41,7 @@ namespace gdn {
 namespace {
 
 constexpr int kSms = 152;
-constexpr int kTN = 64;         // cached tokens of a tile
+constexpr int kTN = 64;         // cached tokens of a step
 constexpr int kMaxPieces = 16;
 constexpr float kGrow = 64.f;   // log2 of how far weights may outgrow their reference
 
@@ -50,7 +55,7 @@ struct Cfg {
   static constexpr int kPhases = D <= 128 ? 4 : 2;                   // K and V pairs in the ring
   static constexpr int kRing = 2 * kPhases;                          // K and V tiles in turn
   static constexpr uint32_t kSmem = kTiles * kQ + kRing * kKv;
-  static constexpr int kO = 256;                                     // first O column of TMEM; S of tile i at 128 i
+  static constexpr int kO = 256;  // first O column of TMEM; scores of tile i (buffer i) from 128 i (64 i) on
   static_assert(kSmem + 4096 <= 232448, "shared memory");
 };
 
@@ -95,8 +100,9 @@ __host__ __device__ inline Plan plan_of(int64_t items, int most) {
 }
 
 // Finds items in increasing order of rounds; a warp holds 32 rows, one per lane.  All lanes call together.
-template <int ROWS>
+template <int D>
 struct Finder {
+  static constexpr int ROWS = Cfg<D>::kRows;
   const AttnLaunch& p;
   int base = 0;
   int64_t before = 0;  // items of the rows before base
@@ -167,8 +173,11 @@ __device__ __forceinline__ float pack2f(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return __uint_as_float(r);
 }
-__device__ __forceinline__ bool not_finite2(uint32_t x) {
-  return (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u;
+// acc + 0 x, a bf16 pair: stays zero, of either sign, while all x are finite, and is NaN from then on.
+__device__ __forceinline__ uint32_t note2(uint32_t x, uint32_t acc) {
+  uint32_t r;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(0u), "r"(acc));
+  return r;
 }
 // D (TMEM) += A (TMEM) B: A's row m is lane m, two bf16 of K per column.
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
@@ -178,33 +187,26 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
       "r"(a), "l"(b), "r"(idesc), "r"(accumulate));
 }
 
-// The products of query tile TILE with the K (V) tile of a ring phase, whose parity is the score buffer.
-template <int D, int TILE, typename S>
-__device__ __forceinline__ void s_products(uint8_t* smem, S& sm, uint32_t phase) {
+// S = Q K^T of a query tile with the K tile of a ring phase, into TMEM column `to`.
+template <int D>
+__device__ __forceinline__ void s_products(uint32_t smem, uint32_t tile, uint32_t phase, uint32_t to) {
   using C = Cfg<D>;
-  const uint32_t base = tc::smem_addr(smem);
-  const uint64_t q = tc::sdesc(base + TILE * C::kQ, 1024);
-  const uint64_t k = tc::sdesc(base + C::kTiles * C::kQ + 2 * phase * C::kKv, D / 64 * 1024);
-  const uint32_t to = TILE * 128 + (phase & 1) * 64;
+  const uint64_t q = tc::sdesc(smem + tile * C::kQ, 1024);
+  const uint64_t k = tc::sdesc(smem + C::kTiles * C::kQ + 2 * phase * C::kKv, D / 64 * 1024);
 #pragma unroll
   for (int s = 0; s < D / 16; ++s)
     tc::mma(to, q + ((s >> 2) * 16384 + (s & 3) * 32) / 16, k + ((s >> 2) * 1024 + (s & 3) * 32) / 16,
             tc::idesc_bf16(128, kTN), s > 0);
-  tc::commit(&sm.s_ready[TILE][phase & 1]);
-  if (TILE == C::kTiles - 1) tc::commit(&sm.empty[2 * phase]);
 }
-template <int D, int TILE, typename S>
-__device__ __forceinline__ void pv_products(uint8_t* smem, S& sm, bool onto, uint32_t phase) {
+// O += P V of a query tile with the V tile of a ring phase; the weights stand from TMEM column `from` on.
+template <int D>
+__device__ __forceinline__ void pv_products(uint32_t smem, uint32_t tile, uint32_t phase, uint32_t from, bool onto) {
   using C = Cfg<D>;
-  const uint32_t base = tc::smem_addr(smem);
-  const uint64_t v = tc::sdesc_lbo(base + C::kTiles * C::kQ + (2 * phase + 1) * C::kKv, 1024, D / 64 * 1024);
-  const uint32_t from = TILE * 128 + (phase & 1) * 64;
+  const uint64_t v = tc::sdesc_lbo(smem + C::kTiles * C::kQ + (2 * phase + 1) * C::kKv, 1024, D / 64 * 1024);
 #pragma unroll
   for (int s = 0; s < kTN / 16; ++s)
-    mma_ts(C::kO + TILE * D, from + s * 8, v + s * 2 * (D / 64) * 1024 / 16, tc::idesc_bf16_bmn(128, D),
+    mma_ts(C::kO + tile * D, from + s * 8, v + s * 2 * (D / 64) * 1024 / 16, tc::idesc_bf16_bmn(128, D),
            s == 0 ? (uint32_t)onto : 1u);
-  tc::commit(&sm.pv_done[TILE][phase & 1]);
-  if (TILE == C::kTiles - 1) tc::commit(&sm.empty[2 * phase + 1]);
 }
 
 // Items of all rows; sum: one value per warp.  All threads call.
@@ -276,7 +278,7 @@ __device__ __forceinline__ uint32_t low_bits(int n, int word) {
   return k == 32 ? 0xffffffffu : (1u << k) - 1u;
 }
 
-// The tokens of tile [b, b + 64) that a query at `pos` sees, a bit each.
+// The tokens of [b, b + 64) that a query at `pos` sees, a bit each.
 __device__ __forceinline__ void visible(const AttnLaunch& p, int b, int pos, uint32_t have, bool all_pages, int bshift,
                                         uint32_t (&vis)[2]) {
 #pragma unroll
@@ -338,14 +340,15 @@ __device__ __forceinline__ void clear_o(uint32_t o_col) {
 }
 
 // Adds the listed tokens' share to O where the query, at `pos`, sees them: their weights from P, their values from
-// the cache.  O is complete up to the tile before; the warp's lanes go together, as TMEM loads and stores need them all.
+// the cache.  O is complete up to the tile before; the warp's lanes go together, as TMEM loads and stores need
+// them all.
 template <int D>
-__device__ __forceinline__ void add_listed(const AttnLaunch& p, const Item& w, const uint32_t (&bad)[2], int b, int pos,
+__device__ __forceinline__ void add_listed(const AttnLaunch& p, int trow, int h, const uint32_t* bad, int b, int pos,
                                            uint32_t p_col, uint32_t o_col) {
   const KvDev& kv = p.cache;
 #pragma unroll 1
   for (int t = 0; t < kTN; ++t) {
-    if (!((t < 32 ? bad[0] : bad[1]) >> (t & 31) & 1u)) continue;
+    if (!(bad[t >> 5] >> (t & 31) & 1u)) continue;
     float x[8];
     uint32_t u = 0;
     tc::tmem_ld8(p_col + (t >> 1 & ~7), x);
@@ -355,9 +358,9 @@ __device__ __forceinline__ void add_listed(const AttnLaunch& p, const Item& w, c
     const float weight = __uint_as_float(t & 1 ? u & 0xffff0000u : u << 16);
     const int tok = b + t;  // below the row's end, in a page that is not NULL
     const bool seen = tok <= pos && (p.window <= 0 || tok > pos - p.window || tok < p.sinks);
-    const int page = kv.table[(int64_t)w.r.trow * kv.max_pages + tok / kv.page_size];
+    const int page = kv.table[(int64_t)trow * kv.max_pages + tok / kv.page_size];
     const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(kv.v) + (int64_t)page * kv.page_stride +
-                             ((int64_t)w.h * kv.page_size + tok % kv.page_size) * D;
+                             ((int64_t)h * kv.page_size + tok % kv.page_size) * D;
 #pragma unroll 1
     for (int c = 0; c < D; c += 32) {
       float o[32];
@@ -371,13 +374,29 @@ __device__ __forceinline__ void add_listed(const AttnLaunch& p, const Item& w, c
   }
 }
 
+// A warp's 32 queries, from number row0 of the tile on; at: a lane's query's first element, -1 for zeros.
+template <int D>
+__device__ __forceinline__ void load_queries(const AttnLaunch& p, uint8_t* qt, int row0, int64_t at) {
+  constexpr int L = D / 8;  // lanes per row
+  const int lane = threadIdx.x & 31, c = lane % L;
+#pragma unroll 8
+  for (int i = 0; i < L; ++i) {
+    const int r = i * (32 / L) + lane / L, row = row0 + r;
+    const int64_t from = __shfl_sync(0xffffffffu, at, r);
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (from >= 0) v = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + from) + c);
+    *reinterpret_cast<uint4*>(qt + (c >> 3) * 16384 + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = v;
+  }
+}
+
 template <int D>
 struct Small {
   uint64_t full[Cfg<D>::kRing], empty[Cfg<D>::kRing];
-  uint64_t checked[Cfg<D>::kRing];  // of a V tile, by its entry
-  uint64_t q_ready, s_ready[2][2], p_ready[2][2], pv_done[2][2], drain[2];  // [query tile][score buffer]
+  uint64_t checked[Cfg<D>::kPhases];  // of a V tile
+  uint64_t q_ready[2], drain[2];
+  uint64_t s_ready[2][2], p_ready[2][2], pv_done[2][2];  // [query tile][score buffer]
   int64_t sum[Cfg<D>::kThreads / 32];
-  uint32_t bad[Cfg<D>::kRing][2];  // listed tokens of a V tile
+  uint32_t bad[Cfg<D>::kPhases][2];  // listed tokens of a V tile
   uint32_t held[16];               // per tile, counted over all items, % 16: which of its pages hold tokens
   uint32_t tmem;
 };
@@ -386,7 +405,7 @@ template <int D>
 __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     prompt_kernel(PromptParams P, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
   using C = Cfg<D>;
-  constexpr int NT = C::kTiles, R = C::kRing, CB = D / 64;
+  constexpr int NT = C::kTiles, R = C::kRing, CB = D / 64, kPh = C::kPhases;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* ring = smem + NT * C::kQ;
   Small<D>& sm = *reinterpret_cast<Small<D>*>(ring + R * C::kKv);
@@ -399,15 +418,17 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     for (int i = 0; i < R; ++i) {
       tc::mbar_init(&sm.full[i], 1);
       tc::mbar_init(&sm.empty[i], 2);  // the products and the warp that looks after V tiles
-      tc::mbar_init(&sm.checked[i], 1);
     }
-    tc::mbar_init(&sm.q_ready, 128 * NT);
+    for (int i = 0; i < kPh; ++i) tc::mbar_init(&sm.checked[i], 1);
     for (int i = 0; i < 4; ++i) {
       tc::mbar_init(&sm.s_ready[i >> 1][i & 1], 1);
       tc::mbar_init(&sm.p_ready[i >> 1][i & 1], 128);
       tc::mbar_init(&sm.pv_done[i >> 1][i & 1], 1);
     }
-    for (int i = 0; i < 2; ++i) tc::mbar_init(&sm.drain[i], 1);
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&sm.q_ready[i], 128);
+      tc::mbar_init(&sm.drain[i], 1);
+    }
     tc::mbar_init_fence();
     tc::prefetch_map(&kmap);
     tc::prefetch_map(&vmap);
@@ -419,13 +440,15 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
   const int ps = kv.page_size, shift = __ffs(ps) - 1, box = min(ps, kTN), boxes = kTN / box;
   const int bshift = __ffs(box) - 1;
 
-  Finder<C::kRows> finder(p);
+  Finder<D> finder(p);
   Item w;
   bool ok = true;
   uint32_t at = 0;     // K and V tiles gone by; a K tile is entry at % R of the ring, its V tile the next
   uint32_t tiles = 0;  // cached tiles gone by
   const int role = warp - 4 * NT;  // < 0: softmax
 
+  // Registers of two query tiles' CTA: 12 warps of 168 at launch; the softmax holds a row of scores and takes
+  // 200, the other four warps keep 104 (8 x 200 + 4 x 104 = 12 x 168).
   if (role < 0) {
     // ---- softmax: a thread per query ----
     const int tile = warp >> 2, row = tid & 127;
@@ -433,37 +456,44 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     uint8_t* qt = smem + tile * C::kQ;
     const uint32_t lane_base = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const uint32_t o_col = lane_base + C::kO + tile * D;
-    uint32_t chk = 0;  // parity of checked[entry]
-    for (int round = 0; round <= plan.full && ok; ++round) {
-      if (!finder.find(plan, round, blockIdx.x, w)) break;
-      const int qi = w.q0 + tile * 128 + row, nq = w.r.len * p.G;
+    uint32_t chk = 0;      // parity of checked, a bit per ring phase
+    int64_t out_at = -1;   // of this thread's query; -1: none
+    // Finds the item of a round and brings its queries to shared memory.  (No product reads those of the item
+    // before any more once its last scores are ready.)
+    auto begin = [&](int round) {
+      if (!finder.find(plan, round, blockIdx.x, w)) return false;
+      const int qi = w.q0 + tile * 128 + row;
+      const bool mine = qi < w.r.len * p.G;
       int g = -1;
-      if (qi < nq) g = global_token(RowsDev{nullptr, p.rows.tok}, w.r.bos + qi / p.G, p.num_global, p.status);
-      const int64_t head = (int64_t)(w.h * p.G + (qi < nq ? qi % p.G : 0)) * D;
-      {
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
-                                                          (int64_t)max(g, 0) * p.q_stride + head);
-#pragma unroll 8
-        for (int c = 0; c < D / 8; ++c) {
-          const uint4 v = g >= 0 ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-          *reinterpret_cast<uint4*>(qt + (c >> 3) * 16384 + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = v;
-        }
-      }
+      if (mine) g = global_token(RowsDev{nullptr, p.rows.tok}, w.r.bos + qi / p.G, p.num_global, p.status);
+      const int64_t head = (int64_t)(w.h * p.G + (mine ? qi % p.G : 0)) * D;
+      out_at = g >= 0 ? (int64_t)g * p.out_stride + head : -1;
+      load_queries<D>(p, qt, 32 * (warp & 3), g >= 0 ? (int64_t)g * p.q_stride + head : -1);
       tc::fence_async_smem();
-      tc::fence_before();  // (the O of the item before has been read)
-      tc::mbar_arrive(&sm.q_ready);
+      tc::mbar_arrive(&sm.q_ready[tile]);
+      return true;
+    };
+    bool more = begin(0);
+    for (int round = 0; more && ok; ++round) {
+      const int qi = w.q0 + tile * 128 + row, nq = w.r.len * p.G;
       const int first = w.r.kv - w.r.len;  // position of the first new token
       const int pos = min(first + qi / p.G, w.r.kv - 1);
       const int tmin = first + min(w.q0 + tile * 128, nq - 1) / p.G, cmin = first + w.q0 / p.G;
       const int tmax = min(first + (w.q0 + tile * 128 + 127) / p.G, w.r.kv - 1);
       float m = -INFINITY, l = 0.f;  // the maximum that the weights refer to (of scores before their scale); their sum
       bool wrote = false;            // O holds something, or will
-      for (int j = w.j0; j < w.j1; ++j, at += 2, ++tiles) {
-        // The buffer's use is number tiles / 2, that of the tile before (tiles - 1) / 2.  (These scores came
-        // behind the product two tiles before, so no phase of pv_done can be taken for another.)
-        const uint32_t buf = tiles & 1, v_entry = (at + 1) % R;
+      for (int j = w.j0; j < w.j1; ++j, ++tiles) {
+        const uint32_t buf = tiles & 1, phase = tiles % kPh;
         const uint32_t s_col = lane_base + tile * 128 + buf * 64;
         const int b = tile_at(w, j);
+        // O is complete when the product of the tile before is.  (The product two tiles before came before these
+        // scores, so no phase can be taken for another.)
+        auto o_complete = [&]() {
+          const uint32_t last = tiles - 1;
+          ok = __all_sync(0xffffffffu, ok && tc::mbar_wait(&sm.pv_done[tile][buf ^ 1], (last >> 1) & 1, P.wait_ns));
+          tc::fence_after();
+          return ok;
+        };
         ok = __all_sync(0xffffffffu, ok && tc::mbar_wait(&sm.s_ready[tile][buf], (tiles >> 1) & 1, P.wait_ns));
         if (!ok) break;
         tc::fence_after();
@@ -473,6 +503,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         const uint32_t have = sm.held[tiles & 15];
         const bool all_pages = have == (1u << boxes) - 1u;
         const bool part = !all_pages || in_part(p, b, tmin, tmax);
+        const bool look = in_part(p, b, cmin, w.last);
         ld_wait(r[0]);
         ld_wait(r[1]);
         if (part) {
@@ -483,9 +514,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         }
         float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int i = 0; i < 32; i += 4)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) m4[e] = max3(m4[e], __uint_as_float(r[0][i + e]), __uint_as_float(r[1][i + e]));
+        for (int i = 0; i < 32; ++i) m4[i & 3] = max3(m4[i & 3], __uint_as_float(r[0][i]), __uint_as_float(r[1][i]));
         const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
         const bool grow = mx > m && (m == -INFINITY || (mx - m) * sl2 > kGrow);
         if (__any_sync(0xffffffffu, grow)) {
@@ -494,10 +523,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
           if (grow) m = mx;
           l *= f;
           if (wrote && __any_sync(0xffffffffu, from)) {
-            // O is complete when the product of the tile before is
-            ok = __all_sync(0xffffffffu, ok && tc::mbar_wait(&sm.pv_done[tile][buf ^ 1], ((tiles - 1) >> 1) & 1, P.wait_ns));
-            if (!ok) break;
-            tc::fence_after();
+            if (!o_complete()) break;
             scale_o<D>(o_col, f);
           }
         }
@@ -514,18 +540,17 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
           l += a0 + a1;
         }
         tc::tmem_st_wait();
-        if (in_part(p, b, cmin, w.last)) {
-          ok = __all_sync(0xffffffffu, ok && tc::mbar_wait(&sm.checked[v_entry], (chk >> v_entry) & 1, P.wait_ns));
-          chk ^= 1u << v_entry;
+        if (look) {
+          ok = __all_sync(0xffffffffu, ok && tc::mbar_wait(&sm.checked[phase], (chk >> phase) & 1, P.wait_ns));
+          chk ^= 1u << phase;
           if (!ok) break;
-          const uint32_t bad[2] = {sm.bad[v_entry][0], sm.bad[v_entry][1]};
-          if ((bad[0] | bad[1]) != 0) {
-            if (wrote)
-              ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.pv_done[tile][buf ^ 1], ((tiles - 1) >> 1) & 1, P.wait_ns));
-            if (!ok) break;
-            tc::fence_after();
-            if (!wrote) clear_o<D>(o_col);
-            add_listed<D>(p, w, bad, b, pos, s_col, o_col);
+          if ((sm.bad[phase][0] | sm.bad[phase][1]) != 0) {
+            if (wrote) {
+              if (!o_complete()) break;
+            } else {
+              clear_o<D>(o_col);
+            }
+            add_listed<D>(p, w.r.trow, w.h, sm.bad[phase], b, pos, s_col, o_col);
           }
         }
         tc::fence_before();
@@ -533,15 +558,18 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         wrote = true;
       }
       if (!ok) break;
+      const bool cut = w.pieces > 1;
+      const int64_t at = out_at;
+      more = begin(round + 1);  // its first scores come up while O goes out
       if (wrote) {
-        ok = __all_sync(0xffffffffu,
-                        ok && tc::mbar_wait(&sm.pv_done[tile][(tiles - 1) & 1], ((tiles - 1) >> 1) & 1, P.wait_ns));
+        const uint32_t last = tiles - 1;
+        ok = __all_sync(0xffffffffu, ok && tc::mbar_wait(&sm.pv_done[tile][last & 1], (last >> 1) & 1, P.wait_ns));
         if (!ok) break;
         tc::fence_after();
       }
       const float inv = l == 0.f ? 0.f : 1.f / l;
       const int64_t part_row = (int64_t)blockIdx.x * C::kRows + tile * 128 + row;
-      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + (int64_t)max(g, 0) * p.out_stride + head;
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + max(at, (int64_t)0);
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
         float o[32];
@@ -551,22 +579,23 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] = 0.f;
         }
-        if (w.pieces > 1) {
+        if (cut) {
           float4* dst = reinterpret_cast<float4*>(P.part + part_row * D + c);
 #pragma unroll
           for (int i = 0; i < 8; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-        } else if (g >= 0) {
+        } else if (at >= 0) {
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] *= inv;
 #pragma unroll
           for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(out + c + 8 * i) = tc::pack8(o + 8 * i);
         }
       }
-      if (w.pieces > 1) *reinterpret_cast<float2*>(P.stats + part_row * 2) = make_float2(m, l);
+      if (cut) *reinterpret_cast<float2*>(P.stats + part_row * 2) = make_float2(m, l);
     }
     if (!ok) set_status(p.status, GDN_STATUS_WAIT_TIMEOUT);
   } else if (role <= 1) {
-    // ---- products: one lane of warp 0 issues all S = Q K^T, one of warp 1 all O += P V ----
+    // ---- products: a lane of warp 0 issues all S = Q K^T, one of warp 1 all O += P V ----
+    const uint32_t base = tc::smem_addr(smem);
     uint32_t chk = 0;  // parity of checked, a bit per ring phase
     // (a phase of a barrier; false once a wait has given up)
     auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -574,38 +603,45 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       if (ok) tc::fence_after();
       return ok;
     };
+    // V of tile t, of this item's number j, is there; onto: O holds listed tokens' share by then
+    auto v_ready = [&](uint32_t t, int j, int cmin, bool& onto) {
+      const uint32_t phase = t % kPh;
+      if (!wait(&sm.full[2 * phase + 1], t / kPh)) return false;
+      if (!in_part(p, tile_at(w, j), cmin, w.last)) return true;
+      if (!wait(&sm.checked[phase], chk >> phase)) return false;
+      chk ^= 1u << phase;
+      onto |= (sm.bad[phase][0] | sm.bad[phase][1]) != 0;
+      return true;
+    };
     for (int round = 0; round <= plan.full && ok; ++round) {
       if (!finder.find(plan, round, blockIdx.x, w)) break;
       const int n = w.j1 - w.j0, cmin = w.r.kv - w.r.len + w.q0 / p.G;
-      if (lane == 0 && role == 0 && wait(&sm.q_ready, round)) {
+      if (lane == 0 && role == 0) {
         for (int j = 0; j < n && ok; ++j) {
-          const uint32_t t = tiles + j, buf = t & 1, phase = t % C::kPhases;
-          if (!wait(&sm.full[2 * phase], t / C::kPhases)) break;
-          // the buffer is free once the product two tiles before is done
-          if (t >= 2 && !wait(&sm.pv_done[0][buf], (t >> 1) - 1)) break;
-          s_products<D, 0>(smem, sm, phase);
-          if constexpr (NT == 2) {
-            if (t >= 2 && !wait(&sm.pv_done[1][buf], (t >> 1) - 1)) break;
-            s_products<D, 1>(smem, sm, phase);
+          const uint32_t t = tiles + j, buf = t & 1, phase = t % kPh;
+          if (!wait(&sm.full[2 * phase], t / kPh)) break;
+#pragma unroll
+          for (uint32_t i = 0; i < NT; ++i) {
+            if (j == 0 && !wait(&sm.q_ready[i], round)) break;
+            // the buffer is free once the product two tiles before is done
+            if (t >= 2 && !wait(&sm.pv_done[i][buf], (t >> 1) - 1)) break;
+            s_products<D>(base, i, phase, i * 128 + buf * 64);
+            tc::commit(&sm.s_ready[i][buf]);
           }
+          tc::commit(&sm.empty[2 * phase]);
         }
-      }
-      if (lane == 0 && role == 1) {
+      } else if (lane == 0) {
         for (int j = 0; j < n && ok; ++j) {
-          const uint32_t t = tiles + j, buf = t & 1, phase = t % C::kPhases;
+          const uint32_t t = tiles + j, buf = t & 1, phase = t % kPh;
           bool onto = j > 0;
-          if (!wait(&sm.full[2 * phase + 1], t / C::kPhases)) break;
-          if (in_part(p, tile_at(w, w.j0 + j), cmin, w.last)) {
-            if (!wait(&sm.checked[2 * phase + 1], chk >> phase)) break;
-            chk ^= 1u << phase;
-            onto |= (sm.bad[2 * phase + 1][0] | sm.bad[2 * phase + 1][1]) != 0;  // O holds these tokens' share by then
+          if (!v_ready(t, w.j0 + j, cmin, onto)) break;
+#pragma unroll
+          for (uint32_t i = 0; i < NT; ++i) {
+            if (!wait(&sm.p_ready[i][buf], t >> 1)) break;
+            pv_products<D>(base, i, phase, i * 128 + buf * 64, onto);
+            tc::commit(&sm.pv_done[i][buf]);
           }
-          if (!wait(&sm.p_ready[0][buf], t >> 1)) break;
-          pv_products<D, 0>(smem, sm, onto, phase);
-          if constexpr (NT == 2) {
-            if (!wait(&sm.p_ready[1][buf], t >> 1)) break;
-            pv_products<D, 1>(smem, sm, onto, phase);
-          }
+          tc::commit(&sm.empty[2 * phase + 1]);
         }
       }
       ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
@@ -667,7 +703,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     if (!ok) set_status(p.status, GDN_STATUS_WAIT_TIMEOUT);
   } else {
     // ---- V tiles that some query sees in part ----
-    // (this warp goes through every phase of the ring, so that none is taken for another)
+    // (this warp goes through every V tile, so that no phase is taken for another)
     for (int round = 0; round <= plan.full && ok; ++round) {
       if (!finder.find(plan, round, blockIdx.x, w)) break;
       const int cmin = w.r.kv - w.r.len + w.q0 / p.G;
@@ -683,26 +719,30 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         }
         if (!ok || !look) continue;
 #pragma unroll 1
-        for (int u = 0; u < 2; ++u) {
+        for (int u = 0; u < kTN / 32; ++u) {
           const int t = u * 32 + lane;
           uint8_t* v = ring + en * C::kKv + (t >> 3) * CB * 1024 + (t & 7) * 128;
-          bool odd = false;
+          uint32_t acc[4] = {0, 0, 0, 0};
           const bool past = b + t >= w.r.kv;
 #pragma unroll 8
           for (int c = 0; c < D / 8; ++c) {
             const uint4 x = *reinterpret_cast<const uint4*>(v + (c >> 3) * 1024 + (((c & 7) ^ (t & 7)) << 4));
-            odd |= not_finite2(x.x) || not_finite2(x.y) || not_finite2(x.z) || not_finite2(x.w);
+            acc[0] = note2(x.x, acc[0]);
+            acc[1] = note2(x.y, acc[1]);
+            acc[2] = note2(x.z, acc[2]);
+            acc[3] = note2(x.w, acc[3]);
           }
+          const bool odd = ((acc[0] | acc[1] | acc[2] | acc[3]) & 0x7fff7fffu) != 0;
           if (past || odd)
             for (int c = 0; c < D / 8; ++c)
               *reinterpret_cast<uint4*>(v + (c >> 3) * 1024 + (((c & 7) ^ (t & 7)) << 4)) = make_uint4(0, 0, 0, 0);
           const uint32_t list = __ballot_sync(0xffffffffu, odd && !past);
-          if (lane == 0) sm.bad[en][u] = list;
+          if (lane == 0) sm.bad[en >> 1][u] = list;
         }
         tc::fence_async_smem();
         __syncwarp();
         if (lane == 0) {
-          tc::mbar_arrive(&sm.checked[en]);
+          tc::mbar_arrive(&sm.checked[en >> 1]);
           tc::mbar_arrive(&sm.empty[en]);
         }
       }
@@ -729,7 +769,7 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(PromptParams P) {
   const Plan plan = plan_of(count_items<kRows, 256>(p, sum), P.max_pieces);
   const int pieces = plan.pieces;
   if (pieces == 1 || (int)blockIdx.x >= plan.left) return;
-  Finder<kRows> finder(p);
+  Finder<D> finder(p);
   Item w;
   if (!finder.find(plan, plan.full, blockIdx.x * pieces, w)) return;
   const float sl2 = p.scale * 1.4426950408889634f;
