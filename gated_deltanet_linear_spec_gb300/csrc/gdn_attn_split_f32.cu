@@ -20,9 +20,31 @@ constexpr int kWarps = 4;   // workers of a CTA
 constexpr int kPerSm = 2;   // CTAs
 constexpr int kNQ = 8;      // queries of a unit
 
+// E floats of a row, aligned to their size; zeros unless `there`.
+template <int E>
+__device__ __forceinline__ void load_row(const float* v, bool there, float (&x)[E]) {
+  if constexpr (E == 1) {
+    x[0] = there ? __ldg(v) : 0.f;
+  } else if constexpr (E == 2) {
+    const float2 y = there ? __ldg(reinterpret_cast<const float2*>(v)) : make_float2(0.f, 0.f);
+    x[0] = y.x;
+    x[1] = y.y;
+  } else {
+#pragma unroll
+    for (int e = 0; e < E; e += 4) {
+      const float4 y = there ? __ldg(reinterpret_cast<const float4*>(v + e)) : make_float4(0.f, 0.f, 0.f, 0.f);
+      x[e] = y.x;
+      x[e + 1] = y.y;
+      x[e + 2] = y.z;
+      x[e + 3] = y.w;
+    }
+  }
+}
+
 template <int D>
 __global__ void __launch_bounds__(32 * kWarps, kPerSm) split_f32_kernel(SplitParams P) {
-  constexpr int E = D / 32;  // output columns of a lane
+  constexpr int E = D / 32;                          // output columns of a lane
+  constexpr int kU = E <= 2 ? 16 : E == 4 ? 8 : 2;   // tokens whose values a lane holds at a time
   __shared__ __align__(16) float sq[kWarps][kNQ][D];
   __shared__ __align__(16) float sp[kWarps][32][kNQ];
   __shared__ int64_t part[kWarps];
@@ -38,6 +60,7 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) split_f32_kernel(SplitPar
   find_shares<kNQ, kWarps, 32 * kWarps>(p, part, deal, shares);
   const Share& share = shares[warp];
   const float sl2 = p.scale * 1.4426950408889634f;
+  const int shift = __ffs(kv.page_size) - 1;
 
   for (Walk<kNQ> w(p, share); w.valid(); w.next()) {
     const KvRow row = w.u.r;
@@ -64,26 +87,41 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) split_f32_kernel(SplitPar
       for (int e = 0; e < E; ++e) o[i][e] = 0.f;
     }
     const int32_t* table = kv.table + (int64_t)row.trow * kv.max_pages;
+    auto entry = [&](int j) {  // the table's entry of this lane's token of tile j
+      const int tok = w.tile_at(j) + lane;
+      return j < w.j0 + w.len && tok <= pos1 ? __ldg(table + (tok >> shift)) : 0;
+    };
+    int ahead = entry(w.j0);
     for (int j = w.j0; j < w.j0 + w.len; ++j) {
       const int b = w.tile_at(j), tok = b + lane;
-      int page = 0;
-      if (tok <= pos1) page = page_or_null(__ldg(table + tok / kv.page_size), kv, p.status);
+      const int page = page_or_null(ahead, kv, p.status);
+      ahead = entry(j + 1);
       // some query sees this lane's token
       const bool some = page > 0 && (p.window <= 0 || tok > pos0 - p.window || tok < p.sinks);
       const unsigned seen = __ballot_sync(0xffffffffu, some);
       if (seen == 0) continue;
-      const int64_t at = (int64_t)page * kv.page_stride + ((int64_t)h * kv.page_size + tok % kv.page_size) * D;
+      const int64_t at = (int64_t)page * kv.page_stride + ((int64_t)h * kv.page_size + (tok & (kv.page_size - 1))) * D;
+      // the values of kU tokens, a lane per E columns, on their way while those before are worked on; a page holds
+      // 16 tokens or more
+      float x[2][kU][E];
+      auto fetch = [&](int c) {
+        const float* v = static_cast<const float*>(kv.v) + __shfl_sync(0xffffffffu, at, c * kU & 16) + lane * E;
+#pragma unroll
+        for (int u = 0; u < kU; ++u)
+          load_row<E>(v + (int64_t)(c * kU % 16 + u) * D, seen >> (c * kU + u) & 1u, x[c & 1][u]);
+      };
+      fetch(0);
       float s[kNQ];
 #pragma unroll
       for (int i = 0; i < kNQ; ++i) s[i] = 0.f;
       const float4* k = reinterpret_cast<const float4*>(static_cast<const float*>(kv.k) + at);
 #pragma unroll 16
       for (int c = 0; c < D / 4; ++c) {
-        const float4 x = some ? __ldg(k + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+        const float4 y = some ? __ldg(k + c) : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < kNQ; ++i) {
           const float4 q = *reinterpret_cast<const float4*>(&sq[warp][i][4 * c]);
-          s[i] = fmaf(q.x, x.x, fmaf(q.y, x.y, fmaf(q.z, x.z, fmaf(q.w, x.w, s[i]))));
+          s[i] = fmaf(q.x, y.x, fmaf(q.y, y.y, fmaf(q.z, y.z, fmaf(q.w, y.w, s[i]))));
         }
       }
       float f[kNQ];
@@ -109,21 +147,18 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) split_f32_kernel(SplitPar
       for (int i = 0; i < kNQ; ++i)
 #pragma unroll
         for (int e = 0; e < E; ++e) t[i][e] = 0.f;
-      for (int half = 0; half < 32; half += 16) {  // a page holds 16 tokens or more
-        const float* v = static_cast<const float*>(kv.v) + __shfl_sync(0xffffffffu, at, half) + lane * E;
-#pragma unroll 4
-        for (int u = 0; u < 16; ++u) {
-          if (!(seen >> (half + u) & 1u)) continue;
-          float x[E];
 #pragma unroll
-          for (int e = 0; e < E; ++e) x[e] = __ldg(v + (int64_t)u * D + e);
+      for (int c = 0; c < 32 / kU; ++c) {
+        if (c + 1 < 32 / kU) fetch(c + 1);
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
           float pw[kNQ];
-          *reinterpret_cast<float4*>(pw) = *reinterpret_cast<const float4*>(&sp[warp][half + u][0]);
-          *reinterpret_cast<float4*>(pw + 4) = *reinterpret_cast<const float4*>(&sp[warp][half + u][4]);
+          *reinterpret_cast<float4*>(pw) = *reinterpret_cast<const float4*>(&sp[warp][c * kU + u][0]);
+          *reinterpret_cast<float4*>(pw + 4) = *reinterpret_cast<const float4*>(&sp[warp][c * kU + u][4]);
 #pragma unroll
           for (int i = 0; i < kNQ; ++i)
 #pragma unroll
-            for (int e = 0; e < E; ++e) t[i][e] = pw[i] == 0.f ? t[i][e] : fmaf(pw[i], x[e], t[i][e]);
+            for (int e = 0; e < E; ++e) t[i][e] = pw[i] == 0.f ? t[i][e] : fmaf(pw[i], x[c & 1][u][e], t[i][e]);
         }
       }
       __syncwarp();
