@@ -90,12 +90,31 @@ __device__ __forceinline__ bool live_page(const KvDev& C, int p) { return p > 0 
 
 // ---- append -----------------------------------------------------------------------------------
 
-// A warp per (token, K or V, kv head group): 16-byte vectors over the token's Hkv x d elements.
+constexpr int kHeld = 4;  // 16-byte vectors of K and of V that a lane holds
+
+// A warp per token: 16-byte vectors over the token's Hkv x d elements.  The token's values are on their way before
+// its page is looked up, which takes four loads one after another.
 __global__ void __launch_bounds__(kThreads) append_kernel(AppendLaunch p) {
   const KvDev& C = p.cache;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int local = blockIdx.x * (kThreads / 32) + warp;
   if (local >= p.rows.num_tokens) return;
+  const int32_t g = p.rows.tok ? __ldg(p.rows.tok + local) : local;
+  const bool there = g >= 0 && g < p.num_global;
+  const int vec = C.d * p.es / 16;  // 16-byte vectors of one head
+  const int all = C.Hkv * vec;
+  const uint4* ks = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.k) + (int64_t)g * p.k_stride * p.es);
+  const uint4* vs = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.v) + (int64_t)g * p.v_stride * p.es);
+  uint4 kx[kHeld], vx[kHeld];
+  auto fetch = [&](int from) {
+#pragma unroll
+    for (int u = 0; u < kHeld; ++u) {
+      const int i = from + 32 * u + lane;
+      kx[u] = there && i < all ? __ldg(ks + i) : make_uint4(0, 0, 0, 0);
+      vx[u] = there && i < all ? __ldg(vs + i) : make_uint4(0, 0, 0, 0);
+    }
+  };
+  fetch(0);
   // the row of the token: the last one that begins at or before it
   int lo = 0, hi = p.rows.num_seqs - 1;
   while (lo < hi) {
@@ -112,23 +131,26 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendLaunch p) {
     set_status(p.status, GDN_STATUS_PAGE_SHARED);
     return;
   }
-  const int32_t g = p.rows.tok ? __ldg(p.rows.tok + local) : local;
-  if (g < 0 || g >= p.num_global) {
+  if (!there) {
     set_status(p.status, GDN_STATUS_TOKEN_RANGE);
     return;
   }
-  const int vec = C.d * p.es / 16;  // 16-byte vectors of one head
-  const int slot = pos % C.page_size;
-  const uint4* ks = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.k) + (int64_t)g * p.k_stride * p.es);
-  const uint4* vs = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.v) + (int64_t)g * p.v_stride * p.es);
+  const int slot = pos % C.page_size, by = __ffs(vec) - 1;
   const int64_t page_off = (int64_t)page * C.page_stride * p.es;
   uint4* kd = reinterpret_cast<uint4*>(static_cast<uint8_t*>(C.k) + page_off);
   uint4* vd = reinterpret_cast<uint4*>(static_cast<uint8_t*>(C.v) + page_off);
-  for (int i = lane; i < C.Hkv * vec; i += 32) {
-    const int h = i / vec, c = i - h * vec;
-    const int64_t o = ((int64_t)h * C.page_size + slot) * vec + c;
-    kd[o] = ks[i];
-    vd[o] = vs[i];
+  const bool shift = (vec & (vec - 1)) == 0;
+  for (int from = 0; from < all; from += 32 * kHeld) {
+    if (from > 0) fetch(from);
+#pragma unroll
+    for (int u = 0; u < kHeld; ++u) {
+      const int i = from + 32 * u + lane;
+      if (i >= all) break;
+      const int h = shift ? i >> by : i / vec, c = i - h * vec;
+      const int64_t o = ((int64_t)h * C.page_size + slot) * vec + c;
+      kd[o] = kx[u];
+      vd[o] = vx[u];
+    }
   }
 }
 
