@@ -3,11 +3,12 @@
 // State on the device: the block table and refcount[p], the number of table entries that hold
 // page p.  There is no free list to keep in step with them: a page is free when its count is 0,
 // and pages are handed out lowest id first, so every call is a function of the table and the
-// counts alone.  Handing out is three dependent launches:
-//   count:  per row the pages it needs; per block of kPageBlock pages how many are free;
-//   list:   the free pages, lowest first, up to the total need (blocks behind it stop at once),
-//           and the rows' exclusive sums;
+// counts alone.  Handing out is three steps:
+//   count:  per row the pages it needs; per block of pages how many are free;
+//   list:   the free pages, lowest first, up to the total need, and the rows' exclusive sums;
 //   assign: row i takes free[offset_i ..] when offset_i + need_i is covered.
+// Pools of up to 131072 pages (kHandPages) go through them in one launch of a cluster, with barriers in
+// between; larger ones in three dependent launches.
 // Counters change by integer adds only, so their order does not matter.
 #include "gdn_kv.cuh"
 
@@ -15,14 +16,16 @@ namespace gdn {
 
 namespace {
 
-constexpr int kPageBlock = 4096;  // pages counted by one block
+constexpr int kPageBlock = 1024;  // pages counted by one block
 constexpr int kThreads = 256;
 constexpr int kPer = kPageBlock / kThreads;
 
 __host__ __device__ inline int page_blocks(int32_t num_pages) { return (num_pages + kPageBlock - 1) / kPageBlock; }
 
+__host__ __device__ inline int max_of(int a, int b) { return a > b ? a : b; }
+
 // Workspace, in ints: need[count] | off[count] | old[count] | fresh[count] | used[count] |
-// blocks[page_blocks] | total[4] | list_a[num_pages] | list_b[num_pages].
+// blocks[page_blocks, at least 8] | total[4] | list_a[num_pages] | list_b[num_pages].
 struct Ws {
   int32_t *need, *off, *old_page, *new_page, *used, *blocks, *total, *list_a, *list_b;
 };
@@ -34,7 +37,7 @@ __host__ __device__ inline Ws carve(int32_t* w, int32_t num_pages, int32_t count
   s.new_page = s.old_page + count;
   s.used = s.new_page + count;
   s.blocks = s.used + count;
-  s.total = s.blocks + page_blocks(num_pages);
+  s.total = s.blocks + max_of(page_blocks(num_pages), 8);
   s.list_a = s.total + 4;
   s.list_b = s.list_a + num_pages;
   return s;
@@ -96,6 +99,8 @@ constexpr int kHeld = 4;  // 16-byte vectors of K and of V that a lane holds
 // its page is looked up, which takes four loads one after another.
 __global__ void __launch_bounds__(kThreads) append_kernel(AppendLaunch p) {
   const KvDev& C = p.cache;
+  let_next();
+  wait_prior();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int local = blockIdx.x * (kThreads / 32) + warp;
   if (local >= p.rows.num_tokens) return;
@@ -197,6 +202,7 @@ __global__ void __launch_bounds__(kThreads) need_kernel(PageRowsLaunch p) {
   const Ws w = carve(p.ws, C.num_pages, p.count);
   const int nb = page_blocks(C.num_pages);
   let_next();
+  wait_prior();
   if ((int)blockIdx.x < nb) {
     const int p0 = blockIdx.x * kPageBlock;
     int n = 0;
@@ -298,6 +304,7 @@ __device__ __forceinline__ bool granted(const Ws& w, int i, uint32_t* st) {
 __global__ void __launch_bounds__(kThreads) reserve_kernel(PageRowsLaunch p) {
   const KvDev& C = p.cache;
   const Ws w = carve(p.ws, C.num_pages, p.count);
+  let_next();
   wait_prior();
   const int i = blockIdx.x;
   RowNeed r;
@@ -315,6 +322,161 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(PageRowsLaunch p) {
       C.refcount[page] = 1;
     }
     base += total;
+  }
+}
+
+__device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+constexpr int kHandCtas = 8, kHandThreads = 1024;
+constexpr int kHandPer = 16;  // pages of a thread
+constexpr int kHandPages = kHandCtas * kHandThreads * kHandPer;
+
+// Exclusive sum over the threads of a CTA of the cluster.
+__device__ int hand_scan(int v, int& total, int* part) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int inc = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += u;
+  }
+  __syncthreads();
+  if (lane == 31) part[warp] = inc;
+  __syncthreads();
+  int w = part[lane];
+  const int mine = w;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, w, o);
+    if (lane >= o) w += u;
+  }
+  total = __shfl_sync(0xffffffffu, w, 31);
+  return __shfl_sync(0xffffffffu, w - mine, warp) + inc - v;
+}
+
+// Reserve, or fork but for the copies, in one launch of a cluster: a warp per row, a thread per kHandPer pages.
+// The three launches that it stands for take their time in starts and ends; what is computed is a few microseconds'
+// reads.  Release, fork and reserve of 64 rows took 26.8 us in eight launches and take 21.1 in four.
+template <bool kFork>
+__global__ void __cluster_dims__(kHandCtas) __launch_bounds__(kHandThreads, 1) hand_out_kernel(PageRowsLaunch p) {
+  __shared__ int part[32];
+  const KvDev& C = p.cache;
+  const Ws w = carve(p.ws, C.num_pages, p.count);
+  const int cta = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
+  const int warp = cta * (kHandThreads / 32) + (tid >> 5);
+  constexpr int kWarps = kHandCtas * kHandThreads / 32;
+  let_next();
+  wait_prior();
+  // count: a row's need (-1: the row is left out), and the thread's free pages
+  const int per = (C.num_pages + kHandCtas * kHandThreads - 1) / (kHandCtas * kHandThreads);
+  const int p0 = (cta * kHandThreads + tid) * per;
+  uint32_t mask = 0;
+  for (int j = 0; j < per; ++j) mask |= (free_page(C, p0 + j) ? 1u : 0u) << j;
+  for (int i = warp; i < p.count; i += kWarps) {
+    bool ok;
+    int n = 0, held = 0, last = 0, used = 0;
+    if constexpr (kFork) {
+      ForkItem f;
+      ok = fork_item(p, i, f);
+      if (ok) {
+        const int32_t* from = C.table + (int64_t)f.src * C.max_pages;
+        const int32_t* to = C.table + (int64_t)f.dst * C.max_pages;
+#pragma unroll 4
+        for (int e = lane; e < f.full + (f.part ? 1 : 0); e += 32) held |= to[e] > 0 || from[e] >= C.num_pages;
+        if (f.part) last = from[f.full];
+        used = f.part;
+      }
+      ok = ok && !__any_sync(0xffffffffu, held);
+      n = last > 0 ? 1 : 0;
+    } else {
+      RowNeed r;
+      ok = reserve_range(p, i, r);
+      if (ok) {
+        const int32_t* row = C.table + (int64_t)r.trow * C.max_pages;
+#pragma unroll 4
+        for (int e = r.lo + lane; e < r.hi; e += 32) n += row[e] <= 0 ? 1 : 0;
+        n = __reduce_add_sync(0xffffffffu, n);
+      }
+    }
+    if (lane == 0) {
+      if (!ok) set_status(p.status, GDN_STATUS_PAGE_RANGE);
+      w.need[i] = ok ? n : -1;
+      if (kFork) {
+        w.old_page[i] = ok && last > 0 ? last : 0;
+        w.used[i] = ok ? used : 0;
+      }
+    }
+  }
+  int total;
+  const int before = hand_scan(__popc(mask), total, part);
+  if (tid == 0) w.blocks[cta] = total;
+  cluster_sync();
+  // list: as many pages as are needed; every CTA sums the needs, the first writes the rows' offsets
+  int first = 0, have = 0;
+#pragma unroll
+  for (int i = 0; i < kHandCtas; ++i) {
+    const int n = __ldcg(w.blocks + i);
+    first += i < cta ? n : 0;
+    have += n;
+  }
+  int base = 0;
+  for (int i0 = 0; i0 < p.count; i0 += kHandThreads) {
+    const int i = i0 + tid;
+    int sum;
+    const int at = hand_scan(i < p.count ? max(__ldcg(w.need + i), 0) : 0, sum, part);
+    if (cta == 0 && i < p.count) w.off[i] = base + at;
+    base = min(base + sum, 1 << 30);  // needs past every pool stay past it
+  }
+  if (cta == 0 && tid == 0) w.total[0] = have;
+  for (int at = first + before; mask && at < base; mask &= mask - 1) w.list_a[at++] = p0 + __ffs(mask) - 1;
+  cluster_sync();
+  // assign
+  for (int i = warp; i < p.count; i += kWarps) {
+    const int need = __ldcg(w.need + i), off = __ldcg(w.off + i);
+    const bool enough = off + need <= have;
+    if (need >= 0 && !enough && lane == 0) set_status(p.status, GDN_STATUS_NO_PAGES);
+    const bool ok = need >= 0 && enough;
+    if constexpr (kFork) {
+      const int page = ok && need > 0 ? __ldcg(w.list_a + off) : 0;
+      if (lane == 0) w.new_page[i] = page;
+      ForkItem f;
+      if (!ok || !fork_item(p, i, f)) continue;
+      const int32_t* from = C.table + (int64_t)f.src * C.max_pages;
+      int32_t* to = C.table + (int64_t)f.dst * C.max_pages;
+      for (int e0 = lane; e0 < f.full; e0 += 128) {
+        int id[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) id[u] = e0 + 32 * u < f.full ? max(from[e0 + 32 * u], 0) : 0;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          if (e0 + 32 * u < f.full) to[e0 + 32 * u] = id[u];
+          if (id[u] > 0) atomicAdd(C.refcount + id[u], 1);
+        }
+      }
+      if (f.part && lane == 0) {
+        to[f.full] = page;
+        if (page > 0) C.refcount[page] = 1;
+      }
+    } else {
+      RowNeed r;
+      if (!ok || need == 0 || !reserve_range(p, i, r)) continue;
+      int32_t* row = C.table + (int64_t)r.trow * C.max_pages;
+      int next = off;
+      for (int e0 = r.lo; e0 < r.hi; e0 += 32) {
+        const int e = e0 + lane;
+        const bool empty = e < r.hi && row[e] <= 0;
+        const uint32_t set = __ballot_sync(0xffffffffu, empty);
+        if (empty) {
+          const int page = __ldcg(w.list_a + next + __popc(set & ((1u << lane) - 1u)));
+          row[e] = page;
+          C.refcount[page] = 1;
+        }
+        next += __popc(set);
+      }
+    }
   }
 }
 
@@ -346,6 +508,7 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(PageRowsLaunch p) {
 __global__ void __launch_bounds__(kThreads) fork_copy_kernel(PageRowsLaunch p) {
   const KvDev& C = p.cache;
   const Ws w = carve(p.ws, C.num_pages, p.count);
+  let_next();
   wait_prior();
   const int i = blockIdx.x;
   const int dst = w.new_page[i], src = w.old_page[i];
@@ -362,6 +525,8 @@ __global__ void __launch_bounds__(kThreads) fork_copy_kernel(PageRowsLaunch p) {
 
 __global__ void __launch_bounds__(kThreads) release_kernel(PageRowsLaunch p) {
   const KvDev& C = p.cache;
+  let_next();
+  wait_prior();
   for (int i = blockIdx.y; i < p.count; i += gridDim.y) {
     const int trow = p.rows ? __ldg(p.rows + i) : i;
     const int lo = p.a ? __ldg(p.a + i) : 0, hi = p.b ? __ldg(p.b + i) : C.max_pages;
@@ -391,6 +556,7 @@ __global__ void __launch_bounds__(kThreads) live_kernel(PageRowsLaunch p) {
   const KvDev& C = p.cache;
   const Ws w = carve(p.ws, C.num_pages, 0);
   let_next();
+  wait_prior();
   const int p0 = blockIdx.x * kPageBlock;
   int n = 0;
 #pragma unroll
@@ -420,7 +586,11 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(PageRowsLaunch p, int32_
   const int mb = M / kPageBlock;  // the block that holds page M
   int upto = 0;
   for (int i = threadIdx.x; i < mb; i += kThreads) upto += w.blocks[i];
-  for (int q = mb * kPageBlock + threadIdx.x; q <= M; q += kThreads) upto += live_page(C, q) ? 1 : 0;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const int q = mb * kPageBlock + j * kThreads + threadIdx.x;
+    upto += q <= M && live_page(C, q) ? 1 : 0;
+  }
   upto = block_sum(upto);
   if (blockIdx.x == 0 && threadIdx.x == 0) {
     w.total[0] = M;
@@ -464,6 +634,7 @@ __device__ __forceinline__ void copy_vecs(uint4* d, const uint4* s, int64_t firs
 __global__ void __launch_bounds__(kThreads) move_kernel(PageRowsLaunch p) {
   const KvDev& C = p.cache;
   const Ws w = carve(p.ws, C.num_pages, 0);
+  let_next();
   wait_prior();
   const int moved = w.total[1];
   const int32_t* holes = w.list_a + C.num_pages / 2;
@@ -501,6 +672,8 @@ __global__ void __launch_bounds__(kThreads) move_kernel(PageRowsLaunch p) {
 // ---- copies of whole items ------------------------------------------------------------------------
 
 __global__ void __launch_bounds__(kThreads) copy_items_kernel(CopyLaunch p, int pieces0, int pieces) {
+  let_next();
+  wait_prior();
   const int64_t units = (int64_t)p.count * pieces;
   for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
     const int i = (int)(u / pieces);
@@ -525,10 +698,10 @@ __global__ void __launch_bounds__(kThreads) copy_items_kernel(CopyLaunch p, int 
 
 // Launch as a programmatic dependent of the kernel just before it on the stream.
 template <typename... P, typename... A>
-cudaError_t launch_after(void (*kernel)(P...), dim3 grid, cudaStream_t s, A... args) {
+cudaError_t launch_of(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t s, A... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(threads);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -537,24 +710,30 @@ cudaError_t launch_after(void (*kernel)(P...), dim3 grid, cudaStream_t s, A... a
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, cudaStream_t s, A... args) {
+  return launch_of(kernel, grid, kThreads, s, args...);
+}
+cudaError_t launch_hand_out(void (*kernel)(PageRowsLaunch), cudaStream_t s, const PageRowsLaunch& p) {
+  return launch_of(kernel, dim3(kHandCtas), kHandThreads, s, p);
+}
 
 constexpr int kCopyBlocks = 152 * 8;  // two thousand threads per SM
 
 }  // namespace
 
 size_t kv_workspace_ints(int32_t num_pages, int32_t count) {
-  return (size_t)5 * count + page_blocks(num_pages) + 4 + 2 * (size_t)num_pages;
+  return (size_t)5 * count + max_of(page_blocks(num_pages), 8) + 4 + 2 * (size_t)num_pages;
 }
 
 cudaError_t launch_kv_append(const AppendLaunch& p, cudaStream_t s) {
-  append_kernel<<<(p.rows.num_tokens + kThreads / 32 - 1) / (kThreads / 32), kThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  return launch_after(append_kernel, dim3((p.rows.num_tokens + kThreads / 32 - 1) / (kThreads / 32)), s, p);
 }
 
 cudaError_t launch_kv_reserve(const PageRowsLaunch& p, cudaStream_t s) {
   const int nb = page_blocks(p.cache.num_pages);
-  need_kernel<false><<<nb + p.count, kThreads, 0, s>>>(p);
-  cudaError_t e = cudaGetLastError();
+  if (p.cache.num_pages <= kHandPages) return launch_hand_out(hand_out_kernel<false>, s, p);
+  cudaError_t e = launch_after(need_kernel<false>, dim3(nb + p.count), s, p);
   if (e == cudaSuccess) e = launch_after(free_list_kernel, dim3(nb + 1), s, p);
   if (e == cudaSuccess) e = launch_after(reserve_kernel, dim3(p.count), s, p);
   return e;
@@ -562,24 +741,26 @@ cudaError_t launch_kv_reserve(const PageRowsLaunch& p, cudaStream_t s) {
 
 cudaError_t launch_kv_release(const PageRowsLaunch& p, cudaStream_t s) {
   const int per_row = (p.cache.max_pages + kThreads - 1) / kThreads;
-  release_kernel<<<dim3(per_row < 64 ? per_row : 64, p.count < 65535 ? p.count : 65535), kThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  return launch_after(release_kernel, dim3(per_row < 64 ? per_row : 64, p.count < 65535 ? p.count : 65535), s, p);
 }
 
 cudaError_t launch_kv_fork(const PageRowsLaunch& p, cudaStream_t s) {
   const int nb = page_blocks(p.cache.num_pages);
-  need_kernel<true><<<nb + p.count, kThreads, 0, s>>>(p);
-  cudaError_t e = cudaGetLastError();
-  if (e == cudaSuccess) e = launch_after(free_list_kernel, dim3(nb + 1), s, p);
-  if (e == cudaSuccess) e = launch_after(fork_kernel, dim3(p.count), s, p);
+  cudaError_t e;
+  if (p.cache.num_pages <= kHandPages) {
+    e = launch_hand_out(hand_out_kernel<true>, s, p);
+  } else {
+    e = launch_after(need_kernel<true>, dim3(nb + p.count), s, p);
+    if (e == cudaSuccess) e = launch_after(free_list_kernel, dim3(nb + 1), s, p);
+    if (e == cudaSuccess) e = launch_after(fork_kernel, dim3(p.count), s, p);
+  }
   if (e == cudaSuccess) e = launch_after(fork_copy_kernel, dim3(p.count, p.cache.Hkv, 2), s, p);
   return e;
 }
 
 cudaError_t launch_kv_compact(const PageRowsLaunch& p, int32_t* num_live, cudaStream_t s) {
   const int nb = page_blocks(p.cache.num_pages);
-  live_kernel<<<nb, kThreads, 0, s>>>(p);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = launch_after(live_kernel, dim3(nb), s, p);
   if (e == cudaSuccess) e = launch_after(plan_kernel, dim3(nb), s, p, num_live);
   if (e == cudaSuccess) e = launch_after(move_kernel, dim3(kCopyBlocks), s, p);
   return e;
@@ -589,8 +770,7 @@ cudaError_t launch_copy_items(const CopyLaunch& p, cudaStream_t s) {
   const int pieces0 = (int)((p.bytes[0] / 16 + 1023) / 1024);
   const int pieces = pieces0 + (int)((p.bytes[1] / 16 + 1023) / 1024);
   const int64_t units = (int64_t)p.count * pieces;
-  copy_items_kernel<<<(int)(units < kCopyBlocks ? units : kCopyBlocks), kThreads, 0, s>>>(p, pieces0, pieces);
-  return cudaGetLastError();
+  return launch_after(copy_items_kernel, dim3((int)(units < kCopyBlocks ? units : kCopyBlocks)), s, p, pieces0, pieces);
 }
 
 }  // namespace gdn

@@ -249,3 +249,23 @@ def test_pages_in_a_graph():
     for got, w in zip((P.table, P.count, P.k, P.v), want):
         assert torch.equal(got, w)
     assert int(P.status) == 0
+
+
+@pytest.mark.parametrize("pages", [131072, 131073, 135000])
+def test_pools_on_both_sides_of_one_launch(pages):
+    """Up to 131072 pages are handed out in one launch, more in three; here only far pages are free."""
+    P = Pool(pages, 40, 24, page=16, dim=16)
+    free = {1, 5000, 70000} | set(range(pages - 120, pages))
+    P.ref.count = [0 if i in free or i == 0 else 1 for i in range(pages)]
+    P.load()
+    rng = random.Random(pages)
+    lens = [rng.randint(0, 60) for _ in range(30)]
+    P.reserve(list(range(30)), [0] * 30, lens)
+    P.same()
+    src = [r for r in range(30) if lens[r]][:10]
+    P.fork(src, list(range(30, 40)), [lens[r] for r in src])
+    P.same()
+    P.release(src)
+    P.reserve(src + [35], [0] * 11, [24 * 16] * 11)  # more than is left
+    P.same()
+    assert P.ref.status == ref.NO_PAGES
