@@ -7,17 +7,17 @@
 // Work.  A unit is one (row, kv-head): the 32-token tiles that its queries see, window and first
 // tokens included.  All units' tiles laid end to end are dealt out evenly, so ragged lengths and a
 // single long row load the SMs alike.  A share's piece of a unit that is not the whole unit leaves
-// (m, l, o) in the workspace; the join kernel adds a unit's pieces in the order of the CTAs, so
+// (m, l, o) in the workspace; the join kernel adds a unit's pieces in the order of the workers, so
 // results do not depend on timing.
 //
 // A CTA (one per SM) holds 1 to 6 workers, each with a share of its own: one warp fetches pages by TMA
 // into a short ring of stages (a NULL page is fetched from past the pool and reads as zeros) and the
-// queries of the next unit; one warp per 16 queries
-// computes, 32 tokens a step, with mma.m16n8k16 and a running maximum and sum of its own.  No warp
-// waits for another, and an SM's workers cover one another's starts and ends of units (with 8 warps
-// sharing a tile and meeting at every unit's end, 64 decode rows took 96 us).  They are one CTA so that
-// their computing warps spread evenly over the SM's four schedulers.  The weights enter the second product as a bf16 pair (hi + lo), so they keep 16 bits: the
-// product is nearly free here, and one bf16 would cost as much accuracy as the output's own rounding.
+// queries of the next unit; one warp per 16 queries computes, 32 tokens a step, with mma.m16n8k16 and a
+// running maximum and sum of its own.  No warp waits for another, and an SM's workers cover one another's starts
+// and ends of units (with 8 warps sharing a tile and meeting at every unit's end, 64 decode rows took 96 us).
+// They are one CTA so that their computing warps spread evenly over the SM's four schedulers.  The weights enter
+// the second product as a bf16 pair (hi + lo), so they keep 16 bits: the product is nearly free here, and one
+// bf16 would cost as much accuracy as the output's own rounding.
 #include <algorithm>
 
 #include "gdn_attn_share.cuh"
@@ -442,7 +442,7 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, NW>::kThreads, 1)
         info[2] = nq;
         info[3] = w.h;
         info[5] = 0;
-      info[4] = small.deal.owner(share.last - w.left + w.u.tiles - 1);  // the worker with the unit's last tile
+        info[4] = small.deal.owner(share.last - w.left + w.u.tiles - 1);  // the worker with the unit's last tile
         info[0] = 1;
       }
     }
