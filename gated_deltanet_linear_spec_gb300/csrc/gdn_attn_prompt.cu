@@ -374,19 +374,22 @@ __device__ __forceinline__ void add_listed(const AttnLaunch& p, int trow, int h,
   }
 }
 
-// A warp's 32 queries, from number row0 of the tile on; at: a lane's query's first element, -1 for zeros.
+// A warp's 32 queries, from number row0 of the tile on; at: a lane's query's first element, -1 for zeros.  All loads
+// are on their way at once.
 template <int D>
 __device__ __forceinline__ void load_queries(const AttnLaunch& p, uint8_t* qt, int row0, int64_t at) {
   constexpr int L = D / 8;  // lanes per row
   const int lane = threadIdx.x & 31, c = lane % L;
-#pragma unroll 8
+  const uint32_t base = tc::smem_addr(qt) + (c >> 3) * 16384;
+#pragma unroll 4
   for (int i = 0; i < L; ++i) {
     const int r = i * (32 / L) + lane / L, row = row0 + r;
     const int64_t from = __shfl_sync(0xffffffffu, at, r);
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (from >= 0) v = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + from) + c);
-    *reinterpret_cast<uint4*>(qt + (c >> 3) * 16384 + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = v;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(base + row * 128 + (((c & 7) ^ (row & 7)) << 4)),
+                 "l"(static_cast<const __nv_bfloat16*>(p.q) + max(from, (int64_t)0) + 8 * c), "r"(from >= 0 ? 16 : 0)
+                 : "memory");
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 template <int D>
