@@ -1,8 +1,8 @@
 // gdn_attn_share.cuh -- rows split over the cache's length: who works on what, and how pieces meet.
 //
 // A unit is one (row, kv-head), or one group of a row's queries of a kv-head: the 32-token tiles that
-// its queries see, window and first tokens included.  All units' tiles laid end to end are dealt out
-// evenly to the workers.  A share's piece of a unit that is not the whole unit leaves (m, l, o) in the
+// its queries see, window and first tokens included, and kStart tiles in front that stand for what beginning a
+// unit takes.  All units' tiles laid end to end are dealt out evenly to the workers.  A share's piece of a unit that is not the whole unit leaves (m, l, o) in the
 // workspace; join_kernel adds a unit's pieces in the order of the workers.
 #pragma once
 
@@ -14,6 +14,9 @@ namespace split {
 
 constexpr int kSms = 152;
 constexpr int kTN = 32;       // tokens of a tile
+// Beginning a unit takes about as long as 2 to 3 tiles: without them in the deal, of 64 decode rows' workers those
+// with pieces of one unit took 107 thousand cycles, of three 121 and of four 133.
+constexpr int kStart = 2;
 constexpr int kJoinWarps = 8;
 constexpr int kJoinRows = 8;  // blocks that share the queries of a unit
 
@@ -29,6 +32,7 @@ struct Unit {
   KvRow r;
   int sink_tiles, first_tile, tiles;
   int per;  // units of the row
+  __device__ int cost() const { return tiles > 0 ? tiles + kStart : 0; }
 };
 
 // A row's values as they lie in memory.
@@ -55,11 +59,11 @@ __device__ __forceinline__ Unit unit_of(const AttnLaunch& p, const RawRow& r, ui
   if (QG > 0) u.per *= (u.r.len * p.G + QG - 1) / (QG > 0 ? QG : 1);
   return u;
 }
-// Tiles of all units of row n.
+// The cost in tiles of all units of row n.
 template <int QG>
-__device__ __forceinline__ int64_t row_tiles(const AttnLaunch& p, int n, uint32_t* st) {
+__device__ __forceinline__ int64_t row_cost(const AttnLaunch& p, int n, uint32_t* st) {
   const Unit u = unit_of<QG>(p, raw_row(p, n), st);
-  return (int64_t)u.tiles * u.per;
+  return (int64_t)u.cost() * u.per;
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -99,7 +103,7 @@ __device__ void find_shares(const AttnLaunch& p, int64_t* part, Deal& deal, Shar
   const int per = (p.rows.num_seqs + THREADS - 1) / THREADS;
   const int n0 = min(tid * per, p.rows.num_seqs), n1 = min(n0 + per, p.rows.num_seqs);
   int64_t mine = 0;
-  for (int n = n0; n < n1; ++n) mine += row_tiles<QG>(p, n, blockIdx.x == 0 ? p.status : nullptr);
+  for (int n = n0; n < n1; ++n) mine += row_cost<QG>(p, n, blockIdx.x == 0 ? p.status : nullptr);
   int64_t inc = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -134,7 +138,7 @@ __device__ void find_shares(const AttnLaunch& p, int64_t* part, Deal& deal, Shar
       int n = n0;
       if (per > 1) {
         for (; n < n1; ++n) {
-          const int64_t t = row_tiles<QG>(p, n, nullptr);
+          const int64_t t = row_cost<QG>(p, n, nullptr);
           if (s.first < at + t) break;
           at += t;
         }
@@ -162,15 +166,13 @@ struct Walk {
     if (left <= 0) return;
     fill(n + 1);
     u = unit_of<QG>(p, s.raw, nullptr);
-    h = (int)quotient(s.into, u.tiles);
-    j0 = (int)(s.into - (int64_t)h * u.tiles);
-    len = (int)min((int64_t)(u.tiles - j0), left);
+    h = (int)quotient(s.into, u.cost());
+    piece((int)(s.into - (int64_t)h * u.cost()));
   }
   __device__ bool valid() const { return left > 0; }
   __device__ void next() {
-    left -= len;
+    left -= span;
     if (left <= 0) return;
-    j0 = 0;
     if (++h == u.per) {
       h = 0;
       do {
@@ -185,11 +187,21 @@ struct Walk {
         u = unit_of<QG>(p, r, nullptr);
       } while (u.tiles == 0);
     }
-    len = (int)min((int64_t)u.tiles, left);
+    piece(0);
   }
   __device__ int tile_at(int j) const { return (j < u.sink_tiles ? j : u.first_tile + j - u.sink_tiles) * kTN; }
+  // Where the unit ends in the deal.
+  __device__ int64_t unit_last(const Share& s) const { return s.last - left - from + u.cost() - 1; }
 
  private:
+  int from, span;  // the piece in the unit's tiles with those that stand for its beginning
+  __device__ void piece(int at) {
+    from = at;
+    span = (int)min((int64_t)(u.cost() - at), left);
+    j0 = max(at - kStart, 0);
+    len = at + span - kStart - j0;
+    if (len <= 0) left = 0;  // the share ends before the unit's first tile
+  }
   int base;
   RawRow ahead;
   __device__ void fill(int from) {

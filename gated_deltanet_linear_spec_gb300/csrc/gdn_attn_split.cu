@@ -442,7 +442,7 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, NW>::kThreads, 1)
         info[2] = nq;
         info[3] = w.h;
         info[5] = 0;
-        info[4] = small.deal.owner(share.last - w.left + w.u.tiles - 1);  // the worker with the unit's last tile
+        info[4] = small.deal.owner(w.unit_last(share));  // the worker with the unit's last tile
         info[0] = 1;
       }
     }

@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) split_f32_kernel(SplitPar
       info[1] = row.bos;
       info[2] = nq;
       info[3] = h;
-      info[4] = deal.owner(share.last - w.left + w.u.tiles - 1);  // the worker with the unit's last tile
+      info[4] = deal.owner(w.unit_last(share));  // the worker with the unit's last tile
       info[5] = q0;
       info[0] = 1;
     }
