@@ -760,8 +760,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
   }
 }
 
-// Adds the pieces of an item's queries in order: a warp per query, kJoinRows queries per block.
-constexpr int kJoinRows = 32;
+// Adds the pieces of an item's queries in order: a warp per query, kJoinRows queries per block, four pieces' values on
+// their way at a time.
+constexpr int kJoinRows = 8;
 template <int D>
 __global__ void __launch_bounds__(256) prompt_join_kernel(PromptParams P) {
   constexpr int kRows = Cfg<D>::kRows, E = D / 32;
@@ -777,37 +778,45 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(PromptParams P) {
   if (!finder.find(plan, plan.full, blockIdx.x * pieces, w)) return;
   const float sl2 = p.scale * 1.4426950408889634f;
   const int lane = threadIdx.x & 31;
-  for (int r = blockIdx.y * kJoinRows + (threadIdx.x >> 5); r < (int)(blockIdx.y + 1) * kJoinRows; r += 8) {
-    const int qi = w.q0 + r;
-    if (qi >= w.r.len * p.G) break;
-    float m = -INFINITY, l = 0.f, o[E];
+  const int r = blockIdx.y * kJoinRows + (threadIdx.x >> 5);
+  const int qi = w.q0 + r;
+  if (qi >= w.r.len * p.G) return;
+  float m = -INFINITY, l = 0.f, o[E];
 #pragma unroll
-    for (int i = 0; i < E; ++i) o[i] = 0.f;
-    // lane s holds piece s's (m, l)
-    const int64_t row0 = (int64_t)blockIdx.x * pieces * kRows + r;
-    const float2 st = lane < pieces ? *reinterpret_cast<const float2*>(P.stats + (row0 + (int64_t)lane * kRows) * 2)
-                                    : make_float2(-INFINITY, 0.f);
-    m = st.x;
+  for (int i = 0; i < E; ++i) o[i] = 0.f;
+  // lane s holds piece s's (m, l)
+  const int64_t row0 = (int64_t)blockIdx.x * pieces * kRows + r;
+  const float2 st = lane < pieces ? *reinterpret_cast<const float2*>(P.stats + (row0 + (int64_t)lane * kRows) * 2)
+                                  : make_float2(-INFINITY, 0.f);
+  m = st.x;
 #pragma unroll
-    for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    const float f = st.x == -INFINITY ? 0.f : ex2((st.x - m) * sl2);
-    for (int s = 0; s < pieces; ++s) {
-      const float fs = __shfl_sync(0xffffffffu, f, s), ls = __shfl_sync(0xffffffffu, st.y, s);
-      const float ms = __shfl_sync(0xffffffffu, st.x, s);
-      l += ls * fs;
-      if (ms == -INFINITY) continue;
+  for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+  const float f = st.x == -INFINITY ? 0.f : ex2((st.x - m) * sl2);
+  for (int s0 = 0; s0 < pieces; s0 += 4) {
+    float x[4][E];
 #pragma unroll
-      for (int i = 0; i < E; ++i) o[i] += P.part[(row0 + (int64_t)s * kRows) * D + lane + 32 * i] * fs;
+    for (int u = 0; u < 4; ++u) {
+      const bool there = __shfl_sync(0xffffffffu, st.x, s0 + u) != -INFINITY;  // (lanes past the pieces hold none)
+#pragma unroll
+      for (int i = 0; i < E; ++i)
+        x[u][i] = there ? P.part[(row0 + (int64_t)(s0 + u) * kRows) * D + lane + 32 * i] : 0.f;
     }
-    const int t = qi / p.G;
-    const int g = p.rows.tok ? __ldg(p.rows.tok + w.r.bos + t) : w.r.bos + t;
-    if (g < 0 || g >= p.num_global) continue;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    __nv_bfloat16* out =
-        static_cast<__nv_bfloat16*>(p.out) + (int64_t)g * p.out_stride + (int64_t)(w.h * p.G + qi - t * p.G) * D;
 #pragma unroll
-    for (int i = 0; i < E; ++i) out[lane + 32 * i] = __float2bfloat16_rn(o[i] * inv);
+    for (int u = 0; u < 4; ++u) {
+      const float fs = __shfl_sync(0xffffffffu, f, s0 + u);
+      l += __shfl_sync(0xffffffffu, st.y, s0 + u) * fs;
+#pragma unroll
+      for (int i = 0; i < E; ++i) o[i] += x[u][i] * fs;
+    }
   }
+  const int t = qi / p.G;
+  const int g = p.rows.tok ? __ldg(p.rows.tok + w.r.bos + t) : w.r.bos + t;
+  if (g < 0 || g >= p.num_global) return;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  __nv_bfloat16* out =
+      static_cast<__nv_bfloat16*>(p.out) + (int64_t)g * p.out_stride + (int64_t)(w.h * p.G + qi - t * p.G) * D;
+#pragma unroll
+  for (int i = 0; i < E; ++i) out[lane + 32 * i] = __float2bfloat16_rn(o[i] * inv);
 }
 
 // The pieces that an item of the last round may be cut into: as the items of a single row say, any number when

@@ -6,6 +6,8 @@
 // workspace; join_kernel adds a unit's pieces in the order of the workers.
 #pragma once
 
+#include <algorithm>
+
 #include "gdn_kv.cuh"
 #include "gdn_tc.cuh"
 
@@ -18,7 +20,7 @@ constexpr int kTN = 32;       // tokens of a tile
 // with pieces of one unit took 107 thousand cycles, of three 121 and of four 133.
 constexpr int kStart = 2;
 constexpr int kJoinWarps = 8;
-constexpr int kJoinRows = 8;  // blocks that share the queries of a unit
+constexpr int kJoinBlocks = 16 * kSms;  // of a launch, more only where the queries need them
 
 struct SplitParams {
   AttnLaunch a;
@@ -210,50 +212,72 @@ struct Walk {
   }
 };
 
-// Adds the pieces of the units that begin in the shares of CTA blockIdx.x's workers and end in later
-// ones.  Block row y takes queries y, y + kJoinRows, ..; a team of warps shares a query's pieces.
+// Adds the pieces of the unit that begins in worker blockIdx.x's share and ends in a later one's.  A warp per query, or
+// a team of them; a lane per piece for the statistics, then eight pieces' values on their way at a time; the blocks
+// of a column share the queries.  (A block per CTA of the attention, which took its workers' units and their
+// pieces in turn, took 16 us under 128 windowed verify rows; that call went from 59.6 us to 52.7.)
+inline int join_rows(int workers, int queries) {
+  return std::max((queries + kJoinWarps - 1) / kJoinWarps, std::min(queries, std::min(kJoinWarps, kJoinBlocks / workers)));
+}
 template <int D, typename T>
-__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(SplitParams P, int queries, int workers) {
+__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(SplitParams P, int queries) {
   __shared__ float so[kJoinWarps][D];
   __shared__ float sl[kJoinWarps], sm[kJoinWarps];
   const AttnLaunch& p = P.a;
   const float sl2 = p.scale * 1.4426950408889634f;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr int E = D / 32;
+  constexpr int E = D / 32, kAtOnce = 8;  // pieces whose values are on their way
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  // lane: field lane % 8 of worker lane / 8's entry, and of the worker 4 behind it
-  const int first = blockIdx.x * workers;
-  const int f0 = lane < workers * 8 ? P.info[first * 8 + lane] : 0;
-  const int f1 = lane + 32 < workers * 8 ? P.info[first * 8 + lane + 32] : 0;
-  for (int w = 0; w < workers; ++w) {
-    const int from = (w & 3) * 8, f = w < 4 ? f0 : f1;
-    if (!__shfl_sync(0xffffffffu, f, from)) continue;
-    const int bos = __shfl_sync(0xffffffffu, f, from + 1), nq = __shfl_sync(0xffffffffu, f, from + 2);
-    const int h = __shfl_sync(0xffffffffu, f, from + 3), c1 = __shfl_sync(0xffffffffu, f, from + 4);
-    const int qi0 = __shfl_sync(0xffffffffu, f, from + 5);  // the unit's first query
-    const int c0 = first + w, pieces = c1 - c0 + 1;
-    const int team = pieces > 8 ? 8 : pieces > 4 ? 4 : pieces > 2 ? 2 : 1;  // warps of a query
-    for (int q0 = blockIdx.y; q0 < nq; q0 += kJoinRows * (kJoinWarps / team)) {
-      const int qi = q0 + kJoinRows * (warp / team);
+  const int c0 = blockIdx.x, f = lane < 8 ? P.info[c0 * 8 + lane] : 0;
+  if (__shfl_sync(0xffffffffu, f, 0)) {
+    const int bos = __shfl_sync(0xffffffffu, f, 1), nq = __shfl_sync(0xffffffffu, f, 2);
+    const int h = __shfl_sync(0xffffffffu, f, 3), c1 = __shfl_sync(0xffffffffu, f, 4);
+    const int qi0 = __shfl_sync(0xffffffffu, f, 5);  // the unit's first query
+    const int pieces = c1 - c0 + 1;
+    const int team = pieces > 64 ? 8 : pieces > 32 ? 4 : pieces > 16 ? 2 : 1;  // warps of a query
+    for (int q0 = blockIdx.y * (kJoinWarps / team); q0 < nq; q0 += gridDim.y * (kJoinWarps / team)) {
+      const int qi = q0 + warp / team;
       float m = -INFINITY, l = 0.f, o[E];
 #pragma unroll
       for (int i = 0; i < E; ++i) o[i] = 0.f;
       if (qi < nq) {
-#pragma unroll 4
-        for (int c = c0 + warp % team; c <= c1; c += team) {
-          const size_t at = (size_t)(2 * c + (c == c0 ? 1 : 0)) * queries + qi;
-          const float2 st = *reinterpret_cast<const float2*>(P.stats + at * 2);
-          float v[E];
+        const int mine = (pieces - warp % team + team - 1) / team;  // this warp's pieces: every team-th
+        for (int s0 = 0; s0 < mine; s0 += 32) {
+          // a lane per piece for the statistics
+          auto place = [&](int i) {
+            const int c = c0 + warp % team + team * (s0 + i);
+            return (size_t)(2 * c + (c == c0 ? 1 : 0)) * queries + qi;
+          };
+          const float2 st = s0 + lane < mine ? *reinterpret_cast<const float2*>(P.stats + place(lane) * 2)
+                                             : make_float2(-INFINITY, 0.f);
+          float mn = st.x;
 #pragma unroll
-          for (int i = 0; i < E; ++i) v[i] = P.part[at * D + lane + 32 * i];
-          const float mn = fmaxf(m, st.x);
+          for (int d = 16; d; d >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, d));
+          mn = fmaxf(mn, m);
           const float a = m == -INFINITY ? 0.f : ex2((m - mn) * sl2);
-          const float b = st.x == -INFINITY ? 0.f : ex2((st.x - mn) * sl2);
-          l = l * a + st.y * b;
+          const float f = st.x == -INFINITY ? 0.f : ex2((st.x - mn) * sl2);
+          float sum = st.y * f;
 #pragma unroll
-          for (int i = 0; i < E; ++i) o[i] = o[i] * a + v[i] * b;
+          for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+          l = l * a + sum;
           m = mn;
+#pragma unroll
+          for (int i = 0; i < E; ++i) o[i] *= a;
+          for (int u0 = 0; u0 < 32 && s0 + u0 < mine; u0 += kAtOnce) {
+            float v[kAtOnce][E];
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u)
+#pragma unroll
+              for (int i = 0; i < E; ++i)
+                v[u][i] = s0 + u0 + u < mine ? P.part[place(u0 + u) * D + lane + 32 * i] : 0.f;
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u) {
+              const float b = __shfl_sync(0xffffffffu, f, u0 + u);
+#pragma unroll
+              for (int i = 0; i < E; ++i) o[i] = fmaf(v[u][i], b, o[i]);
+            }
+          }
         }
       }
       if (team > 1) {

@@ -221,9 +221,9 @@ cudaError_t launch_d(const AttnLaunch& a, cudaStream_t s) {
   cfg.numAttrs = 1;
   cudaError_t e = cudaLaunchKernelEx(&cfg, split_f32_kernel<D>, P);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3(ctas, std::min(kNQ, a.rows.max_q * a.G));
+  cfg.gridDim = dim3(ctas * kWarps, join_rows(ctas * kWarps, std::min(kNQ, a.rows.max_q * a.G)));
   cfg.blockDim = dim3(32 * kJoinWarps);
-  return cudaLaunchKernelEx(&cfg, join_kernel<D, float>, P, kNQ, kWarps);
+  return cudaLaunchKernelEx(&cfg, join_kernel<D, float>, P, kNQ);
 }
 
 }  // namespace
