@@ -12,7 +12,7 @@
 //   after V tiles of which some query must not see some token (below).
 // Measured on 8192 x 8192 (32 q-heads, 8 kv-heads, d = 128) on the way here: one warp for both products, which
 // waits and issues in turn while the tensor core idles, 591 us; a warp for each, 533; rounds dealt back and
-// forth (below), 471; the next item's queries fetched under the last output, 453 (1210 TFLOP/s).  128 tokens a
+// forth (below), 471; the next item's queries fetched under the last output, 449 (1230 TFLOP/s).  128 tokens a
 // step with one score buffer per tile and a thread holding all 128 scores took 488: a tile's products and softmax
 // then follow one another, and what overlaps is the other tile's alone.  Of a step's 2000 cycles the products take
 // 1650: Q K^T with N = 64 reads 6 KB of shared memory per instruction, 52 cycles instead of 32.

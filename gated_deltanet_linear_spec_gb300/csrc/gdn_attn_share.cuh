@@ -2,8 +2,9 @@
 //
 // A unit is one (row, kv-head), or one group of a row's queries of a kv-head: the 32-token tiles that
 // its queries see, window and first tokens included, and kStart tiles in front that stand for what beginning a
-// unit takes.  All units' tiles laid end to end are dealt out evenly to the workers.  A share's piece of a unit that is not the whole unit leaves (m, l, o) in the
-// workspace; join_kernel adds a unit's pieces in the order of the workers.
+// unit takes.  All units' tiles laid end to end are dealt out evenly to the workers.  A share's piece of a unit that
+// is not the whole unit leaves (m, l, o) in the workspace; join_kernel adds a unit's pieces in the order of the
+// workers.
 #pragma once
 
 #include <algorithm>

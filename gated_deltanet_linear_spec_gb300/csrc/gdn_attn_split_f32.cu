@@ -3,8 +3,11 @@
 // The work is dealt out as in gdn_attn_split.cu; a worker is a warp, a unit 8 queries of a (row, kv-head).
 // Products are 32-bit FMAs (the tensor cores have no such type): per 32 cached tokens a lane scores one token
 // against the 8 queries, then the lanes turn to the output's columns and walk the tokens.  2 x 8 FMAs
-// per pair of cached floats is about what the SMs do in the time that HBM takes to bring them, so
-// neither is far ahead; short caches are bound by the latency of their loads.
+// per pair of cached floats are little, but every broadcast of a query's or weight's 16 bytes to a warp fills its
+// registers in four cycles, and that bounds long caches; short ones are bound by the tiles' latency.  The values of a
+// tile are fetched in batches before they are wanted (one token at a time: 67 us instead of 29 for 24
+// verify rows of 3 tokens, 8 q-heads, 2 kv-heads, d = 64, contexts of 64 to 4096).  Tried and slower there: packed
+// pairs of FMAs (34 us), 8 warps a CTA at 128 registers (spills), keys staged in shared memory (32 us).
 // A tile's outputs are summed on their own and added once, which keeps long sums exact to a few steps.
 #include <algorithm>
 
