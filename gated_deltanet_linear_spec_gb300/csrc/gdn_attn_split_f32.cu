@@ -1,4 +1,4 @@
-// gdn_attn_split_f32.cu -- attention of decode and verify rows over a 32-bit cache (d = 32, 64, 128, 256).
+// gdn_attn_split_f32.cu -- attention over a 32-bit cache (d = 32, 64, 128, 256).
 //
 // The work is dealt out as in gdn_attn_split.cu; a worker is a warp, a unit 8 queries of a (row, kv-head).
 // Products are 32-bit FMAs (the tensor cores have no such type): per 32 cached tokens a lane scores one token
@@ -8,6 +8,8 @@
 // tile are fetched in batches before they are wanted (one token at a time: 67 us instead of 29 for 24
 // verify rows of 3 tokens, 8 q-heads, 2 kv-heads, d = 64, contexts of 64 to 4096).  Tried and slower there: packed
 // pairs of FMAs (34 us), 8 warps a CTA at 128 registers (spills), keys staged in shared memory (32 us).
+// Rows of any length come here: eight queries share every key and value (1024 new tokens at 4096, 8 q-heads, d = 64:
+// 545 us; a warp per query, as in gdn_attn_scalar.cu, 4190).
 // A tile's outputs are summed on their own and added once, which keeps long sums exact to a few steps.
 #include <algorithm>
 
@@ -233,7 +235,7 @@ cudaError_t launch_d(const AttnLaunch& a, cudaStream_t s) {
 
 bool attn_split_f32_supported(const AttnLaunch& a, gdn_dtype dtype) {
   const int d = a.cache.d;
-  return dtype == GDN_F32 && (d == 32 || d == 64 || d == 128 || d == 256) && (int64_t)a.rows.max_q * a.G <= 64;
+  return dtype == GDN_F32 && (d == 32 || d == 64 || d == 128 || d == 256);
 }
 
 size_t attn_split_f32_workspace(const AttnLaunch& a) {
