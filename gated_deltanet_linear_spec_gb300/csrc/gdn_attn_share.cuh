@@ -220,14 +220,16 @@ struct Walk {
 inline int join_rows(int workers, int queries) {
   return std::max((queries + kJoinWarps - 1) / kJoinWarps, std::min(queries, std::min(kJoinWarps, kJoinBlocks / workers)));
 }
-template <int D, typename T>
+// E: 32 E columns or fewer are worked on; DC: head_dim, 0 for that of the cache.
+template <typename T, int E, int DC>
 __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(SplitParams P, int queries) {
-  __shared__ float so[kJoinWarps][D];
+  __shared__ float so[kJoinWarps][32 * E];
   __shared__ float sl[kJoinWarps], sm[kJoinWarps];
   const AttnLaunch& p = P.a;
   const float sl2 = p.scale * 1.4426950408889634f;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr int E = D / 32, kAtOnce = 8;  // pieces whose values are on their way
+  constexpr int kAtOnce = 8;  // pieces whose values are on their way
+  const int D = DC > 0 ? DC : p.cache.d;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int c0 = blockIdx.x, f = lane < 8 ? P.info[c0 * 8 + lane] : 0;
@@ -271,7 +273,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(SplitParams P, in
             for (int u = 0; u < kAtOnce; ++u)
 #pragma unroll
               for (int i = 0; i < E; ++i)
-                v[u][i] = s0 + u0 + u < mine ? P.part[place(u0 + u) * D + lane + 32 * i] : 0.f;
+                v[u][i] = s0 + u0 + u < mine && (DC > 0 || lane + 32 * i < D) ? P.part[place(u0 + u) * D + lane + 32 * i] : 0.f;
 #pragma unroll
             for (int u = 0; u < kAtOnce; ++u) {
               const float b = __shfl_sync(0xffffffffu, f, u0 + u);
@@ -309,7 +311,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(SplitParams P, in
       const float inv = l == 0.f ? 0.f : 1.f / l;
       T* out = static_cast<T*>(p.out) + (int64_t)g * p.out_stride + (int64_t)(h * p.G + qi0 + qi - t * p.G) * D;
 #pragma unroll
-      for (int i = 0; i < E; ++i) out[lane + 32 * i] = from_f32<T>(o[i] * inv);
+      for (int i = 0; i < E; ++i)
+        if (DC > 0 || lane + 32 * i < D) out[lane + 32 * i] = from_f32<T>(o[i] * inv);
     }
   }
 }

@@ -489,7 +489,7 @@ cudaError_t launch_cfg(const AttnLaunch& a, cudaStream_t s) {
   cfg.gridDim = dim3(kSms * NW, join_rows(kSms * NW, a.rows.max_q * a.G));
   cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, join_kernel<D, __nv_bfloat16>, P, (int)C::kNQ);
+  return cudaLaunchKernelEx(&cfg, join_kernel<__nv_bfloat16, D / 32, D>, P, (int)C::kNQ);
 }
 
 int query_slots(int64_t queries) { return queries <= 16 ? 16 : queries <= 32 ? 32 : 64; }

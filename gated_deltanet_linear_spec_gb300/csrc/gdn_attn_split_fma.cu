@@ -1,15 +1,15 @@
-// gdn_attn_split_f32.cu -- attention over a 32-bit cache (d = 32, 64, 128, 256).
+// gdn_attn_split_fma.cu -- attention on the CUDA cores: 32-bit caches, and the head dimensions that the tensor core
+// kernels do not take (bf16 with d other than 64, 128 and 256).
 //
-// The work is dealt out as in gdn_attn_split.cu; a worker is a warp, a unit 8 queries of a (row, kv-head).
-// Products are 32-bit FMAs (the tensor cores have no such type): per 32 cached tokens a lane scores one token
-// against the 8 queries, then the lanes turn to the output's columns and walk the tokens.  2 x 8 FMAs
-// per pair of cached floats are little, but every broadcast of a query's or weight's 16 bytes to a warp fills its
-// registers in four cycles, and that bounds long caches; short ones are bound by the tiles' latency.  The values of a
-// tile are fetched in batches before they are wanted (one token at a time: 67 us instead of 29 for 24
-// verify rows of 3 tokens, 8 q-heads, 2 kv-heads, d = 64, contexts of 64 to 4096).  Tried and slower there: packed
-// pairs of FMAs (34 us), 8 warps a CTA at 128 registers (spills), keys staged in shared memory (32 us).
-// Rows of any length come here: eight queries share every key and value (1024 new tokens at 4096, 8 q-heads, d = 64:
-// 545 us; a warp per query, as in gdn_attn_scalar.cu, 4190).
+// The work is dealt out as in gdn_attn_split.cu; a worker is a warp, a unit 8 queries of a (row, kv-head), rows
+// have any length.  Per 32 cached tokens a lane scores one token against the 8 queries in 32-bit FMAs, then the lanes turn
+// to the output's columns, E neighbours each, and walk the tokens.  2 x 8 FMAs per pair of cached values are
+// little, but every broadcast of a query's or weight's 16 bytes to a warp fills its registers in four cycles, and that
+// bounds long caches; short ones are bound by the tiles' latency.  The values of a tile are fetched in batches
+// before they are wanted (one token at a time: 67 us instead of 29 for 24 verify rows of 3 tokens, 8 q-heads, 2
+// kv-heads, d = 64, 32 bits, contexts of 64 to 4096).  Tried and slower there: packed pairs of FMAs (34 us), 8 warps a
+// CTA at 128 registers (spills), keys staged in shared memory (32 us).  1024 new tokens at 4096 take 545 us;
+// with a warp per query, which shares nothing, 4190.
 // A tile's outputs are summed on their own and added once, which keeps long sums exact to a few steps.
 #include <algorithm>
 
@@ -25,7 +25,30 @@ constexpr int kWarps = 4;   // workers of a CTA
 constexpr int kPerSm = 2;   // CTAs
 constexpr int kNQ = 8;      // queries of a unit
 
-// E floats of a row, aligned to their size; zeros unless `there`.
+template <typename T>
+struct Vec {  // 16 bytes
+  static constexpr int kN = 16 / sizeof(T);
+};
+// 16 bytes' values.
+__device__ __forceinline__ void load16(const float* v, bool there, float (&x)[4]) {
+  const float4 y = there ? __ldg(reinterpret_cast<const float4*>(v)) : make_float4(0.f, 0.f, 0.f, 0.f);
+  x[0] = y.x;
+  x[1] = y.y;
+  x[2] = y.z;
+  x[3] = y.w;
+}
+__device__ __forceinline__ void open2(uint32_t u, float& lo, float& hi) {
+  lo = __uint_as_float(u << 16);
+  hi = __uint_as_float(u & 0xffff0000u);
+}
+__device__ __forceinline__ void load16(const __nv_bfloat16* v, bool there, float (&x)[8]) {
+  const uint4 y = there ? __ldg(reinterpret_cast<const uint4*>(v)) : make_uint4(0, 0, 0, 0);
+  open2(y.x, x[0], x[1]);
+  open2(y.y, x[2], x[3]);
+  open2(y.z, x[4], x[5]);
+  open2(y.w, x[6], x[7]);
+}
+// E neighbouring values of a row, aligned to their size; zeros unless `there`.
 template <int E>
 __device__ __forceinline__ void load_row(const float* v, bool there, float (&x)[E]) {
   if constexpr (E == 1) {
@@ -37,28 +60,42 @@ __device__ __forceinline__ void load_row(const float* v, bool there, float (&x)[
   } else {
 #pragma unroll
     for (int e = 0; e < E; e += 4) {
-      const float4 y = there ? __ldg(reinterpret_cast<const float4*>(v + e)) : make_float4(0.f, 0.f, 0.f, 0.f);
-      x[e] = y.x;
-      x[e + 1] = y.y;
-      x[e + 2] = y.z;
-      x[e + 3] = y.w;
+      float y[4];
+      load16(v + e, there, y);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[e + i] = y[i];
     }
   }
 }
+template <int E>
+__device__ __forceinline__ void load_row(const __nv_bfloat16* v, bool there, float (&x)[E]) {
+  if constexpr (E == 2) {
+    open2(there ? __ldg(reinterpret_cast<const uint32_t*>(v)) : 0u, x[0], x[1]);
+  } else if constexpr (E == 4) {
+    const uint2 y = there ? __ldg(reinterpret_cast<const uint2*>(v)) : make_uint2(0, 0);
+    open2(y.x, x[0], x[1]);
+    open2(y.y, x[2], x[3]);
+  } else {
+    load16(v, there, x);
+  }
+}
 
-template <int D>
-__global__ void __launch_bounds__(32 * kWarps, kPerSm) split_f32_kernel(SplitParams P) {
-  constexpr int E = D / 32;                          // output columns of a lane
-  constexpr int kU = E <= 2 ? 16 : E == 4 ? 8 : 2;   // tokens whose values a lane holds at a time
-  __shared__ __align__(16) float sq[kWarps][kNQ][D];
+// E: columns of a lane, 32 E are head_dim or more; DC: head_dim where it is 32 E, else 0.
+template <typename T, int E, int DC>
+__global__ void __launch_bounds__(32 * kWarps, kPerSm) split_fma_kernel(SplitParams P) {
+  constexpr int kU = E <= 2 ? 16 : E == 4 ? 8 : 2;  // tokens whose values a lane holds at a time
+  constexpr int kV = Vec<T>::kN;
+  __shared__ __align__(16) float sq[kWarps][kNQ][32 * E];
   __shared__ __align__(16) float sp[kWarps][32][kNQ];
   __shared__ int64_t part[kWarps];
   __shared__ Deal deal;
   __shared__ Share shares[kWarps];
   const AttnLaunch& p = P.a;
   const KvDev& kv = p.cache;
+  const int D = DC > 0 ? DC : kv.d;  // a multiple of 16, so of E
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int worker = blockIdx.x * kWarps + warp;
+  const bool columns = DC > 0 || lane * E < D;  // this lane has some
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (lane == 0) P.info[worker * 8] = 0;
@@ -77,9 +114,13 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) split_f32_kernel(SplitPar
 #pragma unroll
     for (int i = 0; i < kNQ; ++i) {
       const int gi = __shfl_sync(0xffffffffu, g, i);
-      const float* q = static_cast<const float*>(p.q) + (int64_t)max(gi, 0) * p.q_stride + (int64_t)(h * p.G + (q0 + i) % p.G) * D;
+      const T* q =
+          static_cast<const T*>(p.q) + (int64_t)max(gi, 0) * p.q_stride + (int64_t)(h * p.G + (q0 + i) % p.G) * D;
 #pragma unroll
-      for (int e = 0; e < E; ++e) sq[warp][i][lane + 32 * e] = gi >= 0 ? __ldg(q + lane + 32 * e) : 0.f;
+      for (int e = 0; e < E; ++e) {
+        const int c = lane + 32 * e;
+        sq[warp][i][c] = gi >= 0 && (DC > 0 || c < D) ? to_f32(q[c]) : 0.f;
+      }
     }
     __syncwarp();
     const int pos0 = first + q0 / p.G, pos1 = first + (q0 + nq - 1) / p.G;  // of the first and last query
@@ -110,24 +151,27 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) split_f32_kernel(SplitPar
       // 16 tokens or more
       float x[2][kU][E];
       auto fetch = [&](int c) {
-        const float* v = static_cast<const float*>(kv.v) + __shfl_sync(0xffffffffu, at, c * kU & 16) + lane * E;
+        const T* v = static_cast<const T*>(kv.v) + __shfl_sync(0xffffffffu, at, c * kU & 16) + lane * E;
 #pragma unroll
         for (int u = 0; u < kU; ++u)
-          load_row<E>(v + (int64_t)(c * kU % 16 + u) * D, seen >> (c * kU + u) & 1u, x[c & 1][u]);
+          load_row<E>(v + (int64_t)(c * kU % 16 + u) * D, columns && (seen >> (c * kU + u) & 1u), x[c & 1][u]);
       };
       fetch(0);
       float s[kNQ];
 #pragma unroll
       for (int i = 0; i < kNQ; ++i) s[i] = 0.f;
-      const float4* k = reinterpret_cast<const float4*>(static_cast<const float*>(kv.k) + at);
-#pragma unroll 16
-      for (int c = 0; c < D / 4; ++c) {
-        const float4 y = some ? __ldg(k + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+      const T* k = static_cast<const T*>(kv.k) + at;
+#pragma unroll(DC > 0 ? 16 : 4)
+      for (int c = 0; c < D; c += kV) {
+        float y[kV];
+        load16(k + c, some, y);
 #pragma unroll
-        for (int i = 0; i < kNQ; ++i) {
-          const float4 q = *reinterpret_cast<const float4*>(&sq[warp][i][4 * c]);
-          s[i] = fmaf(q.x, y.x, fmaf(q.y, y.y, fmaf(q.z, y.z, fmaf(q.w, y.w, s[i]))));
-        }
+        for (int i = 0; i < kNQ; ++i)
+#pragma unroll
+          for (int e = 0; e < kV; e += 4) {
+            const float4 q = *reinterpret_cast<const float4*>(&sq[warp][i][c + e]);
+            s[i] = fmaf(q.x, y[e], fmaf(q.y, y[e + 1], fmaf(q.z, y[e + 2], fmaf(q.w, y[e + 3], s[i]))));
+          }
       }
       float f[kNQ];
 #pragma unroll
@@ -184,13 +228,15 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) split_f32_kernel(SplitPar
       if (whole) {
         if (gi < 0) continue;
         const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
-        float* out = static_cast<float*>(p.out) + (int64_t)gi * p.out_stride + (int64_t)(h * p.G + (q0 + i) % p.G) * D;
+        T* out = static_cast<T*>(p.out) + (int64_t)gi * p.out_stride + (int64_t)(h * p.G + (q0 + i) % p.G) * D;
 #pragma unroll
-        for (int e = 0; e < E; ++e) out[lane * E + e] = o[i][e] * inv;
+        for (int e = 0; e < E; ++e)
+          if (columns) out[lane * E + e] = from_f32<T>(o[i][e] * inv);
       } else {
         float* dst = P.part + ((size_t)slot * kNQ + i) * D + lane * E;
 #pragma unroll
-        for (int e = 0; e < E; ++e) dst[e] = o[i][e];
+        for (int e = 0; e < E; ++e)
+          if (columns) dst[e] = o[i][e];
         if (lane == 0)
           *reinterpret_cast<float2*>(P.stats + ((size_t)slot * kNQ + i) * 2) = make_float2(m[i], l[i]);
       }
@@ -207,8 +253,8 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) split_f32_kernel(SplitPar
   }
 }
 
-template <int D>
-cudaError_t launch_d(const AttnLaunch& a, cudaStream_t s) {
+template <typename T, int E, int DC>
+cudaError_t launch_as(const AttnLaunch& a, cudaStream_t s) {
   constexpr int ctas = kSms * kPerSm;
   SplitParams P{};
   P.a = a;
@@ -224,31 +270,33 @@ cudaError_t launch_d(const AttnLaunch& a, cudaStream_t s) {
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, split_f32_kernel<D>, P);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, split_fma_kernel<T, E, DC>, P);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3(ctas * kWarps, join_rows(ctas * kWarps, std::min(kNQ, a.rows.max_q * a.G)));
+  const int queries = (int)std::min<int64_t>(kNQ, (int64_t)a.rows.max_q * a.G);
+  cfg.gridDim = dim3(ctas * kWarps, join_rows(ctas * kWarps, queries));
   cfg.blockDim = dim3(32 * kJoinWarps);
-  return cudaLaunchKernelEx(&cfg, join_kernel<D, float>, P, kNQ);
+  return cudaLaunchKernelEx(&cfg, join_kernel<T, E, DC>, P, kNQ);
+}
+template <typename T>
+cudaError_t launch_any(const AttnLaunch& a, cudaStream_t s) {
+  const int d = a.cache.d;
+  return d <= 64 ? launch_as<T, 2, 0>(a, s) : d <= 128 ? launch_as<T, 4, 0>(a, s) : launch_as<T, 8, 0>(a, s);
 }
 
 }  // namespace
 
-bool attn_split_f32_supported(const AttnLaunch& a, gdn_dtype dtype) {
-  const int d = a.cache.d;
-  return dtype == GDN_F32 && (d == 32 || d == 64 || d == 128 || d == 256);
-}
-
-size_t attn_split_f32_workspace(const AttnLaunch& a) {
+size_t attn_split_fma_workspace(const AttnLaunch& a) {
   return (size_t)kSms * kPerSm * kWarps * (8 + 4 * kNQ + 2 * kNQ * a.cache.d) * 4;
 }
 
-cudaError_t launch_attn_split_f32(const AttnLaunch& a, cudaStream_t s) {
+cudaError_t launch_attn_split_fma(const AttnLaunch& a, gdn_dtype dtype, cudaStream_t s) {
+  if (dtype == GDN_BF16) return launch_any<__nv_bfloat16>(a, s);
   switch (a.cache.d) {
-    case 32: return launch_d<32>(a, s);
-    case 64: return launch_d<64>(a, s);
-    case 128: return launch_d<128>(a, s);
-    case 256: return launch_d<256>(a, s);
-    default: return cudaErrorInvalidValue;
+    case 32: return launch_as<float, 1, 32>(a, s);
+    case 64: return launch_as<float, 2, 64>(a, s);
+    case 128: return launch_as<float, 4, 128>(a, s);
+    case 256: return launch_as<float, 8, 256>(a, s);
+    default: return launch_any<float>(a, s);
   }
 }
 

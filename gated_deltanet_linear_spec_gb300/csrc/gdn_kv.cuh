@@ -133,15 +133,12 @@ cudaError_t launch_copy_items(const CopyLaunch& p, cudaStream_t s);
 bool attn_split_supported(const AttnLaunch& p, gdn_dtype dtype);
 size_t attn_split_workspace(const AttnLaunch& p);
 cudaError_t launch_attn_split(const AttnLaunch& p, cudaStream_t s);
-// The same over a 32-bit cache (d = 32, 64, 128, 256).
-bool attn_split_f32_supported(const AttnLaunch& p, gdn_dtype dtype);
-size_t attn_split_f32_workspace(const AttnLaunch& p);
-cudaError_t launch_attn_split_f32(const AttnLaunch& p, cudaStream_t s);
 // Longer bf16 rows (d = 64, 128, 256): prompts, on tcgen05.
 bool attn_prompt_supported(const AttnLaunch& p, gdn_dtype dtype);
 size_t attn_prompt_workspace(const AttnLaunch& p);
 cudaError_t launch_attn_prompt(const AttnLaunch& p, cudaStream_t s);
-// Every other layout.
-cudaError_t launch_attn_scalar(const AttnLaunch& p, gdn_dtype dtype, cudaStream_t s);
+// Every other layout, rows of any length: split over the cache's length, on the CUDA cores.
+size_t attn_split_fma_workspace(const AttnLaunch& p);
+cudaError_t launch_attn_split_fma(const AttnLaunch& p, gdn_dtype dtype, cudaStream_t s);
 
 }  // namespace gdn

@@ -409,3 +409,28 @@ def test_append_refuses_what_it_must_not_write():
     want = s.k.clone()
     want[int(s.table[s.table_rows[1]][2]), :, 38 % 16] = 1
     assert torch.equal(s.kv[0].cpu().view(torch.int16), want.view(torch.int16))
+
+
+@pytest.mark.parametrize("dim", [16, 48, 80, 96, 112, 160, 192, 240])
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+def test_every_head_dim(dim, dtype):
+    Step([(1, 700), (4, 130), (0, 9), (90, 300), (1, 1)], heads=6, kv_heads=2, dim=dim, dtype=dtype, seed=dim).check()
+    Step([(3, 257), (40, 600)], heads=4, kv_heads=4, dim=dim, page=32, window=70, sinks=5, dtype=dtype,
+         seed=dim + 1).check()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_a_last_token_reaches_itself_alone_at_other_head_dims(value, dtype):
+    s = Step([(4, 70), (40, 64)], dim=96, dtype=dtype, seed=3, gather=False)
+    clean, _ = s.run()
+    clean = clean.clone()
+    for n in range(2):
+        pos = s.rows[n][1] - 1
+        page, slot = int(s.table[s.table_rows[n]][pos // s.page]), pos % s.page
+        s.kv[0][page, :, slot] = value
+        s.kv[1][page, :, slot] = value
+    got, _ = s.run()
+    others = [t for t in range(44) if t not in (3, 43)]
+    assert torch.equal(got[others], clean[others])
+    assert not torch.isfinite(got[[3, 43]].float()).all()
