@@ -2,16 +2,18 @@
 // kernels do not take (bf16 with d other than 64, 128 and 256).
 //
 // The work is dealt out as in gdn_attn_split.cu; a worker is a warp, a unit 8 queries of a (row, kv-head), rows
-// have any length.  Per 32 cached tokens a lane scores one token against the 8 queries in 32-bit FMAs, then the lanes
-// turn to the output's columns, E neighbours each, and walk the tokens.  2 x 8 FMAs per pair of cached values are
-// little, but every broadcast of a query's or weight's 16 bytes to a warp fills its registers in four cycles, and that
-// bounds long caches; short ones are bound by the tiles' latency.  The values of a tile are fetched in batches
-// before they are wanted (one token at a time: 67 us instead of 29 for 24 verify rows of 3 tokens, 8 q-heads, 2
-// kv-heads, d = 64, 32 bits, contexts of 64 to 4096).  Tried and slower there: packed pairs of FMAs (34 us), 8 warps a
-// CTA at 128 registers (spills), keys staged in shared memory (32 us).  1024 new tokens at 4096 take 545 us;
-// with a warp per query, which shares nothing, 4190; 64 decode rows over 512 to 8192 tokens (bf16, d = 96, 32 q-heads,
-// 4 kv-heads) 180 us against 5731.
-// A tile's outputs are summed on their own and added once, which keeps long sums exact to a few steps.
+// have any length.  A lane holds E neighbouring columns of the 8 queries and of their outputs in registers and walks
+// the keys, then the values, of 32 tokens a step: 2 x 8 32-bit FMAs per pair of cached values.  The parts of 8 x 4
+// scores meet by exchanges that halve what a lane keeps, so a lane ends up with one query's scores of every fourth
+// token, and the softmax takes two exchanges.  (Scores by lane = token, queries broadcast from shared memory, are
+// bound by those broadcasts, four cycles each: 64 rows of 3 tokens, 64 to 4096 cached, 8 q-heads, 2 kv-heads, 32 bits,
+// d = 256: 187 us instead of 138.)  Keys and values are fetched a chunk ahead; one token at a time, 24 such rows
+// with d = 64 took 67 us instead of 25.  Loops of two chunks a turn, as unrolled ones fall out of the instruction
+// cache (d = 96: 1467 us instead of 739 for 1024 new tokens at 2048, 16 q-heads, 4 kv-heads).
+// Per token of a step, a unit of 8 queries takes about 16 E FMAs and 8 exchanges: that bounds long caches, the
+// steps' latency short ones.  1024 new tokens at 4096 (d = 64) take 443 us, with a warp per query, which shares
+// nothing, 4190; 64 decode rows over 512 to 8192 tokens (bf16, d = 96, 32 q-heads, 4 kv-heads) 219 us against 5731.
+// Up to d = 128 a step's outputs are summed on their own and added once, which keeps long sums exact to a few steps.
 #include <algorithm>
 
 #include "gdn_attn_share.cuh"
@@ -26,10 +28,6 @@ constexpr int kWarps = 4;   // workers of a CTA
 constexpr int kPerSm = 2;   // CTAs
 constexpr int kNQ = 8;      // queries of a unit
 
-template <typename T>
-struct Vec {  // 16 bytes
-  static constexpr int kN = 16 / sizeof(T);
-};
 // 16 bytes' values.
 __device__ __forceinline__ void load16(const float* v, bool there, float (&x)[4]) {
   const float4 y = there ? __ldg(reinterpret_cast<const float4*>(v)) : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -84,9 +82,8 @@ __device__ __forceinline__ void load_row(const __nv_bfloat16* v, bool there, flo
 // E: columns of a lane, 32 E are head_dim or more; DC: head_dim where it is 32 E, else 0.
 template <typename T, int E, int DC>
 __global__ void __launch_bounds__(32 * kWarps, kPerSm) split_fma_kernel(SplitParams P) {
-  constexpr int kU = E <= 2 ? 16 : E == 4 ? 8 : 2;  // tokens whose values a lane holds at a time
-  constexpr int kV = Vec<T>::kN;
-  __shared__ __align__(16) float sq[kWarps][kNQ][32 * E];
+  constexpr int kU = E <= 4 ? 8 : 4;  // tokens whose keys or values a lane holds at a time
+  constexpr int kC = 32 / kU;         // as many chunks of keys, then as many of values
   __shared__ __align__(16) float sp[kWarps][32][kNQ];
   __shared__ int64_t part[kWarps];
   __shared__ Deal deal;
@@ -111,28 +108,21 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) split_fma_kernel(SplitPar
     const int first = row.kv - row.len;  // position of the first new token
     int g = -1;                          // lane i < nq: the query's global token
     if (lane < nq) g = global_token(RowsDev{nullptr, p.rows.tok}, row.bos + (q0 + lane) / p.G, p.num_global, p.status);
-    __syncwarp();
+    float q[kNQ][E];
 #pragma unroll
     for (int i = 0; i < kNQ; ++i) {
       const int gi = __shfl_sync(0xffffffffu, g, i);
-      const T* q =
-          static_cast<const T*>(p.q) + (int64_t)max(gi, 0) * p.q_stride + (int64_t)(h * p.G + (q0 + i) % p.G) * D;
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const int c = lane + 32 * e;
-        sq[warp][i][c] = gi >= 0 && (DC > 0 || c < D) ? to_f32(q[c]) : 0.f;
-      }
+      const T* from = static_cast<const T*>(p.q) + (int64_t)max(gi, 0) * p.q_stride;
+      load_row<E>(from + (int64_t)(h * p.G + (q0 + i) % p.G) * D + lane * E, columns && gi >= 0, q[i]);
     }
-    __syncwarp();
     const int pos0 = first + q0 / p.G, pos1 = first + (q0 + nq - 1) / p.G;  // of the first and last query
-    float o[kNQ][E], m[kNQ], l[kNQ];
+    const int mine = lane >> 2;  // the query whose scores, maximum and sum this lane has, those of every 4th token
+    const int pos = min(first + (q0 + mine) / p.G, pos1);
+    float o[kNQ][E], m = -INFINITY, l = 0.f;
 #pragma unroll
-    for (int i = 0; i < kNQ; ++i) {
-      m[i] = -INFINITY;
-      l[i] = 0.f;
+    for (int i = 0; i < kNQ; ++i)
 #pragma unroll
       for (int e = 0; e < E; ++e) o[i][e] = 0.f;
-    }
     const int32_t* table = kv.table + (int64_t)row.trow * kv.max_pages;
     auto entry = [&](int j) {  // the table's entry of this lane's token of tile j
       const int tok = w.tile_at(j) + lane;
@@ -148,87 +138,124 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) split_fma_kernel(SplitPar
       const unsigned seen = __ballot_sync(0xffffffffu, some);
       if (seen == 0) continue;
       const int64_t at = (int64_t)page * kv.page_stride + ((int64_t)h * kv.page_size + (tok & (kv.page_size - 1))) * D;
-      // the values of kU tokens, a lane per E columns, on their way while those before are worked on; a page holds
-      // 16 tokens or more
+      // chunk c of the keys, then of the values, on its way while the one before is worked on; a page holds 16 tokens
+      // or more
       float x[2][kU][E];
-      auto fetch = [&](int c) {
-        const T* v = static_cast<const T*>(kv.v) + __shfl_sync(0xffffffffu, at, c * kU & 16) + lane * E;
+      auto fetch = [&](int c, float (&to)[kU][E]) {
+        const int from = c % kC * kU;
+        const T* v = static_cast<const T*>(c < kC ? kv.k : kv.v) + __shfl_sync(0xffffffffu, at, from & 16) +
+                     from % 16 * D + lane * E;
 #pragma unroll
-        for (int u = 0; u < kU; ++u)
-          load_row<E>(v + (int64_t)(c * kU % 16 + u) * D, columns && (seen >> (c * kU + u) & 1u), x[c & 1][u]);
+        for (int u = 0; u < kU; ++u) load_row<E>(v + u * D, columns && (seen >> (from + u) & 1u), to[u]);
       };
-      fetch(0);
-      float s[kNQ];
+      fetch(0, x[0]);
+      // (rolled, two chunks a turn: in one piece these loops are too long for the instruction cache)
+#pragma unroll 1
+      for (int c0 = 0; c0 < kC; c0 += 2) {
 #pragma unroll
-      for (int i = 0; i < kNQ; ++i) s[i] = 0.f;
-      const T* k = static_cast<const T*>(kv.k) + at;
-#pragma unroll(DC > 0 ? 16 : 4)
-      for (int c = 0; c < D; c += kV) {
-        float y[kV];
-        load16(k + c, some, y);
+        for (int d = 0; d < 2; ++d) {
+          const int c = c0 + d;
+          fetch(c + 1, x[d ^ 1]);
 #pragma unroll
-        for (int i = 0; i < kNQ; ++i)
+          for (int n = 0; n < kU / 4; ++n) {
+            // A lane's part of 8 queries x 4 tokens; halving what a lane keeps with every exchange, 31 of them leave it
+            // the sum of one.
+            float r[32];
 #pragma unroll
-          for (int e = 0; e < kV; e += 4) {
-            const float4 q = *reinterpret_cast<const float4*>(&sq[warp][i][c + e]);
-            s[i] = fmaf(q.x, y[e], fmaf(q.y, y[e + 1], fmaf(q.z, y[e + 2], fmaf(q.w, y[e + 3], s[i]))));
+            for (int i = 0; i < kNQ; ++i)
+#pragma unroll
+              for (int u = 0; u < 4; ++u) {
+                float t = 0.f;
+#pragma unroll
+                for (int e = 0; e < E; ++e) t = fmaf(q[i][e], x[d][4 * n + u][e], t);
+                r[4 * i + u] = t;
+              }
+#pragma unroll
+            for (int half = 16; half; half >>= 1)
+#pragma unroll
+              for (int i = 0; i < half; ++i) {
+                const float keep = lane & half ? r[i + half] : r[i], give = lane & half ? r[i] : r[i + half];
+                r[i] = keep + __shfl_xor_sync(0xffffffffu, give, half);
+              }
+            sp[warp][c * kU + 4 * n + (lane & 3)][mine] = r[0];
           }
+        }
       }
-      float f[kNQ];
+      float s[8];  // of tokens (lane & 3) + 4 n, which this lane wrote
 #pragma unroll
-      for (int i = 0; i < kNQ; ++i) {
-        const int pos = min(first + (q0 + i) / p.G, pos1);
-        const bool sees = some && tok <= pos && (p.window <= 0 || tok > pos - p.window || tok < p.sinks);
-        if (!sees) s[i] = -INFINITY;
-        float x = s[i];
+      for (int n = 0; n < 8; ++n) s[n] = sp[warp][4 * n + (lane & 3)][mine];
+      float x_max = -INFINITY;
 #pragma unroll
-        for (int d = 16; d; d >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-        const float mn = fmaxf(m[i], x);
-        f[i] = m[i] == -INFINITY ? 0.f : ex2((m[i] - mn) * sl2);
-        m[i] = mn;
-        const float e = ex2(fmaf(s[i], sl2, mn == -INFINITY ? 0.f : -mn * sl2));
-        l[i] = l[i] * f[i] + e;
-        sp[warp][lane][i] = e;
+      for (int n = 0; n < 8; ++n) {
+        const int t = 4 * n + (lane & 3), tk = b + t;
+        const bool sees = (seen >> t & 1u) && tk <= pos && (p.window <= 0 || tk > pos - p.window || tk < p.sinks);
+        if (!sees) s[n] = -INFINITY;
+        x_max = fmaxf(x_max, s[n]);
+      }
+      x_max = fmaxf(x_max, __shfl_xor_sync(0xffffffffu, x_max, 1));
+      x_max = fmaxf(x_max, __shfl_xor_sync(0xffffffffu, x_max, 2));
+      const float mn = fmaxf(m, x_max);
+      const float f = m == -INFINITY ? 0.f : ex2((m - mn) * sl2);
+      const float ms = mn == -INFINITY ? 0.f : -mn * sl2;
+      m = mn;
+      l *= f;
+#pragma unroll
+      for (int n = 0; n < 8; ++n) {
+        const float e = ex2(fmaf(s[n], sl2, ms));
+        l += e;
+        sp[warp][4 * n + (lane & 3)][mine] = e;
       }
       __syncwarp();
-      // the tile's own sums, a lane per E columns; a weight of 0 takes no value in, whatever that holds
+      // The tile's own sums (with 8 columns a lane there are no registers for them); a weight of 0 takes no value in,
+      // whatever that holds.
+      constexpr bool kOwn = E <= 4;
       float t[kNQ][E];
 #pragma unroll
-      for (int i = 0; i < kNQ; ++i)
+      for (int i = 0; i < kNQ; ++i) {
+        const float fi = __shfl_sync(0xffffffffu, f, 4 * i);
 #pragma unroll
-        for (int e = 0; e < E; ++e) t[i][e] = 0.f;
+        for (int e = 0; e < E; ++e) {
+          t[i][e] = kOwn ? 0.f : o[i][e] * fi;
+          if (kOwn) o[i][e] *= fi;
+        }
+      }
+#pragma unroll 1
+      for (int c0 = 0; c0 < kC; c0 += 2) {
 #pragma unroll
-      for (int c = 0; c < 32 / kU; ++c) {
-        if (c + 1 < 32 / kU) fetch(c + 1);
+        for (int d = 0; d < 2; ++d) {
+          const int c = c0 + d;
+          if (c + 1 < kC) fetch(kC + c + 1, x[d ^ 1]);
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
-          float pw[kNQ];
-          *reinterpret_cast<float4*>(pw) = *reinterpret_cast<const float4*>(&sp[warp][c * kU + u][0]);
-          *reinterpret_cast<float4*>(pw + 4) = *reinterpret_cast<const float4*>(&sp[warp][c * kU + u][4]);
+          for (int u = 0; u < kU; ++u) {
+            float pw[kNQ];
+            *reinterpret_cast<float4*>(pw) = *reinterpret_cast<const float4*>(&sp[warp][c * kU + u][0]);
+            *reinterpret_cast<float4*>(pw + 4) = *reinterpret_cast<const float4*>(&sp[warp][c * kU + u][4]);
 #pragma unroll
-          for (int i = 0; i < kNQ; ++i)
+            for (int i = 0; i < kNQ; ++i)
 #pragma unroll
-            for (int e = 0; e < E; ++e) t[i][e] = pw[i] == 0.f ? t[i][e] : fmaf(pw[i], x[c & 1][u][e], t[i][e]);
+              for (int e = 0; e < E; ++e) t[i][e] = pw[i] == 0.f ? t[i][e] : fmaf(pw[i], x[d][u][e], t[i][e]);
+          }
         }
       }
       __syncwarp();
 #pragma unroll
       for (int i = 0; i < kNQ; ++i)
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[i][e] = fmaf(o[i][e], f[i], t[i][e]);
+        for (int e = 0; e < E; ++e) o[i][e] = kOwn ? o[i][e] + t[i][e] : t[i][e];
     }
 
+    l += __shfl_xor_sync(0xffffffffu, l, 1);
+    l += __shfl_xor_sync(0xffffffffu, l, 2);
     const bool whole = w.j0 == 0 && w.len == w.u.tiles;
     const int slot = 2 * worker + (w.j0 == 0 ? 1 : 0);
 #pragma unroll
     for (int i = 0; i < kNQ; ++i) {
-#pragma unroll
-      for (int d = 16; d; d >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], d);
+      const float li = __shfl_sync(0xffffffffu, l, 4 * i), mi = __shfl_sync(0xffffffffu, m, 4 * i);
       const int gi = __shfl_sync(0xffffffffu, g, i);
       if (i >= nq) continue;
       if (whole) {
         if (gi < 0) continue;
-        const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
+        const float inv = li == 0.f ? 0.f : 1.f / li;
         T* out = static_cast<T*>(p.out) + (int64_t)gi * p.out_stride + (int64_t)(h * p.G + (q0 + i) % p.G) * D;
 #pragma unroll
         for (int e = 0; e < E; ++e)
@@ -239,7 +266,7 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) split_fma_kernel(SplitPar
         for (int e = 0; e < E; ++e)
           if (columns) dst[e] = o[i][e];
         if (lane == 0)
-          *reinterpret_cast<float2*>(P.stats + ((size_t)slot * kNQ + i) * 2) = make_float2(m[i], l[i]);
+          *reinterpret_cast<float2*>(P.stats + ((size_t)slot * kNQ + i) * 2) = make_float2(mi, li);
       }
     }
     if (!whole && w.j0 == 0 && lane == 0) {
