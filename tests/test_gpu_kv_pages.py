@@ -269,3 +269,17 @@ def test_pools_on_both_sides_of_one_launch(pages):
     P.reserve(src + [35], [0] * 11, [24 * 16] * 11)  # more than is left
     P.same()
     assert P.ref.status == ref.NO_PAGES
+
+
+@pytest.mark.parametrize("pages", [131072, 131073])
+def test_compaction_of_large_pools(pages):
+    P = Pool(pages, 30, 24, page=16, dim=16)
+    held = {1, 2, 77, 5000, 70000, 131071} | set(range(pages - 90, pages))
+    P.ref.count = [0 if i in held or i == 0 else 1 for i in range(pages)]
+    P.load()
+    P.reserve(list(range(30)), [0] * 30, [40] * 30)  # every row holds some of the free pages, low and far ones
+    P.ref.count = [n if i in held else 0 for i, n in enumerate(P.ref.count)]
+    P.load()
+    P.same()
+    P.compact()
+    P.same()
