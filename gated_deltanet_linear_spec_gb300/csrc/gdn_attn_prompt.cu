@@ -85,7 +85,7 @@ __device__ __forceinline__ int tile_at(const Item& w, int j) {
 // Items of row n: its query tiles times kv-heads.
 template <int ROWS>
 __device__ __forceinline__ int64_t items_of(const AttnLaunch& p, int n, uint32_t* st, KvRow& r) {
-  if (n >= p.rows.num_seqs || !load_kv_row(p.rows, p.cache, n, r, st)) return 0;
+  if (n >= p.rows.num_seqs || !load_kv_row(p.rows, p.cache, n, r, st) || r.len * p.G <= p.few) return 0;
   return ((int64_t)r.len * p.G + ROWS - 1) / ROWS * p.cache.Hkv;
 }
 

@@ -54,7 +54,9 @@ __device__ __forceinline__ Unit unit_of(const AttnLaunch& p, const RawRow& r, ui
   Unit u;
   u.tiles = u.sink_tiles = u.first_tile = 0;
   u.per = p.cache.Hkv;
-  if (!check_kv_row(p.rows, p.cache, r.bos, r.eos, r.kv, r.trow, u.r, st) || u.r.len == 0) return u;
+  if (!check_kv_row(p.rows, p.cache, r.bos, r.eos, r.kv, r.trow, u.r, st) || u.r.len == 0 ||
+      (p.few > 0 && u.r.len * p.G > p.few))
+    return u;
   const int low = p.window > 0 ? max(0, u.r.kv - u.r.len - p.window + 1) : 0;
   u.sink_tiles = (min(p.sinks, low) + kTN - 1) / kTN;
   u.first_tile = max(low / kTN, u.sink_tiles);

@@ -456,6 +456,9 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, NW>::kThreads, 1)
   }
 }
 
+// Queries of a unit, at most.
+int64_t queries_of(const AttnLaunch& a) { return a.few > 0 ? a.few : (int64_t)a.rows.max_q * a.G; }
+
 template <int D, int WQ, int DS, int NW>
 cudaError_t launch_cfg(const AttnLaunch& a, cudaStream_t s) {
   using C = Cfg<D, WQ, DS, NW>;
@@ -486,7 +489,7 @@ cudaError_t launch_cfg(const AttnLaunch& a, cudaStream_t s) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if ((e = cudaLaunchKernelEx(&cfg, split_kernel<D, WQ, DS, NW>, P, kmap, vmap)) != cudaSuccess) return e;
-  cfg.gridDim = dim3(kSms * NW, join_rows(kSms * NW, a.rows.max_q * a.G));
+  cfg.gridDim = dim3(kSms * NW, join_rows(kSms * NW, (int)queries_of(a)));
   cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, join_kernel<__nv_bfloat16, D / 32, D>, P, (int)C::kNQ);
@@ -495,6 +498,18 @@ cudaError_t launch_cfg(const AttnLaunch& a, cudaStream_t s) {
 int query_slots(int64_t queries) { return queries <= 16 ? 16 : queries <= 32 ? 32 : 64; }
 
 }  // namespace
+
+// A call of long rows may hold one-token rows too (a GDN batch's decode rows come with its prompts).  As prompts they
+// take a CTA per row and kv-head, 128 or 256 queries wide: with 64 decode rows over 512 to 8192 tokens beside a
+// 1024-token prompt (32 q-heads, 4 kv-heads, d = 128) the call took 226 us, with the short rows split it takes 137
+// (16 such rows beside two prompts: 220 and 211).  The two more launches cost 9 us where no row is short (12 ragged
+// prompts: 115 and 125), so fewer than 16 rows, or rows that must all be of one length, go one way.
+int32_t attn_few(const AttnLaunch& a, gdn_dtype dtype) {
+  const bool ragged = (int64_t)a.rows.num_tokens < (int64_t)a.rows.num_seqs * a.rows.max_q;
+  if (!attn_prompt_supported(a, dtype) || attn_split_supported(a, dtype) || a.G > 64 || a.rows.num_seqs < 16 || !ragged)
+    return 0;
+  return query_slots(a.G);
+}
 
 bool attn_split_supported(const AttnLaunch& a, gdn_dtype dtype) {
   const int d = a.cache.d;
@@ -520,13 +535,13 @@ cudaError_t launch_picked(Cfg<D, WQ, DS, NW>, const AttnLaunch& a, cudaStream_t 
 }  // namespace
 
 size_t attn_split_workspace(const AttnLaunch& a) {
-  const int q = query_slots((int64_t)a.rows.max_q * a.G);
+  const int q = query_slots(queries_of(a));
   const size_t workers = (size_t)kSms * pick(a.cache.d, q, [](auto c) { return decltype(c)::kWorkers; });
   return workers * (8 + 4 * (size_t)q + 2 * (size_t)q * a.cache.d) * 4;
 }
 
 cudaError_t launch_attn_split(const AttnLaunch& a, cudaStream_t s) {
-  return pick(a.cache.d, query_slots((int64_t)a.rows.max_q * a.G), [&](auto c) { return launch_picked(c, a, s); });
+  return pick(a.cache.d, query_slots(queries_of(a)), [&](auto c) { return launch_picked(c, a, s); });
 }
 
 }  // namespace gdn

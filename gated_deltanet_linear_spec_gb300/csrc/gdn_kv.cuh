@@ -85,6 +85,7 @@ struct AttnLaunch {
   float scale;
   int32_t window;  // 0 = none
   int32_t sinks;
+  int32_t few;     // > 0: rows of up to so many queries per kv-head are the split kernel's, others the prompt one's
   void* ws;
   uint32_t* status;
 };
@@ -134,6 +135,8 @@ bool attn_split_supported(const AttnLaunch& p, gdn_dtype dtype);
 size_t attn_split_workspace(const AttnLaunch& p);
 cudaError_t launch_attn_split(const AttnLaunch& p, cudaStream_t s);
 // Longer bf16 rows (d = 64, 128, 256): prompts, on tcgen05.
+// What `few` of a call with both kinds of rows is; 0: all rows go one way.
+int32_t attn_few(const AttnLaunch& p, gdn_dtype dtype);
 bool attn_prompt_supported(const AttnLaunch& p, gdn_dtype dtype);
 size_t attn_prompt_workspace(const AttnLaunch& p);
 cudaError_t launch_attn_prompt(const AttnLaunch& p, cudaStream_t s);

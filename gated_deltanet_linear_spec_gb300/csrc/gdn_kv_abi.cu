@@ -168,10 +168,12 @@ int gdn_kv_append(const gdn_kv_cache* cache, const gdn_kv_rows* rows, const void
 size_t gdn_attention_workspace_bytes(const gdn_attn_desc* attn, const gdn_kv_cache* cache, const gdn_kv_rows* rows) {
   if (check_shape(cache) || check_table(cache) || check_attn(attn, cache) || check_kv_rows(rows)) return 0;
   if (rows->num_seqs == 0 || rows->max_query_len == 0) return 0;
-  const AttnLaunch p = attn_args(attn, cache, rows);
+  AttnLaunch p = attn_args(attn, cache, rows);
   if (attn_split_supported(p, cache->dtype)) return round256(attn_split_workspace(p));
-  if (attn_prompt_supported(p, cache->dtype)) return round256(attn_prompt_workspace(p));
-  return round256(attn_split_fma_workspace(p));
+  if (!attn_prompt_supported(p, cache->dtype)) return round256(attn_split_fma_workspace(p));
+  p.few = attn_few(p, cache->dtype);
+  const size_t need = attn_prompt_workspace(p), split = p.few ? attn_split_workspace(p) : 0;
+  return round256(need > split ? need : split);  // one after the other in one workspace
 }
 
 int gdn_paged_attention(const gdn_attn_desc* attn, const gdn_kv_cache* cache, const gdn_kv_rows* rows, const void* q,
@@ -202,8 +204,11 @@ int gdn_paged_attention(const gdn_attn_desc* attn, const gdn_kv_cache* cache, co
   p.ws = workspace;
   p.status = d_status;
   if (attn_split_supported(p, cache->dtype)) return cuda_rc(launch_attn_split(p, (cudaStream_t)stream));
-  if (attn_prompt_supported(p, cache->dtype)) return cuda_rc(launch_attn_prompt(p, (cudaStream_t)stream));
-  return cuda_rc(launch_attn_split_fma(p, cache->dtype, (cudaStream_t)stream));
+  if (!attn_prompt_supported(p, cache->dtype))
+    return cuda_rc(launch_attn_split_fma(p, cache->dtype, (cudaStream_t)stream));
+  p.few = attn_few(p, cache->dtype);
+  if (p.few && (rc = cuda_rc(launch_attn_split(p, (cudaStream_t)stream)))) return rc;
+  return cuda_rc(launch_attn_prompt(p, (cudaStream_t)stream));
 }
 
 int gdn_kv_reserve(const gdn_kv_cache* cache, int32_t count, const int32_t* table_rows, const int32_t* from_lens,

@@ -434,3 +434,12 @@ def test_a_last_token_reaches_itself_alone_at_other_head_dims(value, dtype):
     others = [t for t in range(44) if t not in (3, 43)]
     assert torch.equal(got[others], clean[others])
     assert not torch.isfinite(got[[3, 43]].float()).all()
+
+
+@pytest.mark.parametrize("heads,kv_heads", [(8, 2), (16, 1), (4, 4), (24, 1)])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_decode_rows_beside_prompts(dim, heads, kv_heads):
+    rows = [(1, 300), (1, 1), (140, 200), (1, 64), (4, 90), (0, 7), (1, 513), (70, 70), (1, 33), (3, 40), (1, 128), (17, 99),
+            (1, 2), (5, 5), (1, 700), (33, 33), (0, 0)]
+    Step(rows, heads=heads, kv_heads=kv_heads, dim=dim, page=32, seed=dim + heads).check()
+    Step(rows, heads=heads, kv_heads=kv_heads, dim=dim, window=50, sinks=3, seed=dim + heads + 1, fused=True).check()
