@@ -255,6 +255,8 @@ def _token_rows(t: torch.Tensor, dtype: torch.dtype, heads: int, dim: int, name:
     st = t.stride()
     if (dim > 1 and st[2] != 1) or (heads > 1 and st[1] != dim):
         raise TypeError(f"{name}: the heads of a token must be contiguous")
+    if t.shape[0] > 1 and st[0] < heads * dim:  # (0, an expanded tensor's stride, means dense in the C descriptors)
+        raise TypeError(f"{name}: tokens share memory (an expanded tensor needs a copy)")
     return t.data_ptr(), (st[0] if t.shape[0] > 1 else 0)
 
 
@@ -278,6 +280,8 @@ class KvCache:
         for t, name in ((k, "k_pool"), (v, "v_pool")):
             if not t[:1].is_contiguous():
                 raise TypeError(f"{name}: a page must be contiguous")
+            if t.shape[0] > 1 and t.stride(0) < t[0].numel():
+                raise TypeError(f"{name}: pages share memory")
         if k.shape[0] > 1 and k.stride(0) != v.stride(0):
             raise ValueError("k_pool and v_pool: expected one page stride")
         if self.block_table.dim() != 2:

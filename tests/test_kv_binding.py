@@ -1,0 +1,71 @@
+"""What the paged cache's binding refuses or arranges before it calls the library, on the host: tensors of the
+CPU stand in for those of a GPU, and every call here ends before a launch."""
+import pytest
+import torch
+
+import gated_deltanet_linear_spec_gb300 as gdn
+
+
+class OnDevice(torch.Tensor):
+    """A CPU tensor that says it is one of cuda:0."""
+    is_cuda = True
+
+    def get_device(self):
+        return 0
+
+
+def dev(*shape, dtype=torch.bfloat16):
+    return torch.zeros(*shape, dtype=dtype).as_subclass(OnDevice)
+
+
+def i32(values):
+    return torch.tensor(values, dtype=torch.int32).as_subclass(OnDevice)
+
+
+def cache(**kw):
+    d = dict(k_pool=dev(8, 2, 16, 64), v_pool=dev(8, 2, 16, 64), block_table=i32([[1, 2], [3, 4]]), refcount=i32([0] * 8))
+    d.update(kw)
+    return gdn.KvCache(**d)
+
+
+def rows(**kw):
+    d = dict(query_start_loc=i32([0, 2, 4]), num_tokens=4, kv_lens=i32([5, 9]), max_query_len=2)
+    d.update(kw)
+    return gdn.KvRows(**d)
+
+
+# ------------------------------------------------------------------------------------------
+# tensors whose tokens or pages share memory
+
+def test_expanded_tokens_are_refused():
+    one, four = dev(1, 2, 64).expand(4, 2, 64), dev(4, 2, 64)
+    assert one.stride(0) == 0
+    for k, v in ((one, four), (four, one)):
+        with pytest.raises(TypeError, match="share memory"):
+            gdn.gdn_kv_append(cache(), rows(), k, v)
+    wide, out = dev(1, 8, 64).expand(4, 8, 64), dev(4, 8, 64)
+    ws = torch.zeros(1 << 20, dtype=torch.uint8).as_subclass(OnDevice)
+    for q, o in ((wide, out), (out, wide)):
+        with pytest.raises(TypeError, match="share memory"):
+            gdn.gdn_paged_attention(gdn.Attention(8), cache(), rows(), q, o, workspace=ws)
+
+
+def test_overlapping_tokens_are_refused():
+    long = dev(4 * 2 * 64 + 64)
+    with pytest.raises(TypeError, match="share memory"):
+        gdn._token_rows(long.as_strided((4, 2, 64), (64, 64, 1)), torch.bfloat16, 2, 64, "k")
+
+
+def test_expanded_pools_are_refused():
+    one, all_ = dev(1, 2, 16, 64).expand(8, 2, 16, 64), dev(8, 2, 16, 64)
+    for k, v in ((one, one), (one, all_), (all_, one)):
+        with pytest.raises((TypeError, ValueError)):
+            cache(k_pool=k, v_pool=v)
+
+
+def test_one_token_and_strided_tokens_are_taken():
+    assert gdn._token_rows(dev(1, 2, 64).expand(1, 2, 64), torch.bfloat16, 2, 64, "k")[1] == 0
+    assert gdn._token_rows(dev(4, 6, 64)[:, 2:4], torch.bfloat16, 2, 64, "k")[1] == 6 * 64
+    assert gdn._token_rows(dev(0, 2, 64), torch.bfloat16, 2, 64, "k")[1] == 0
+    both = dev(8, 2, 2, 16, 64)
+    assert cache(k_pool=both[:, 0], v_pool=both[:, 1])._desc.page_stride == 2 * 2 * 16 * 64
