@@ -16,9 +16,10 @@
 // step with one score buffer per tile and a thread holding all 128 scores took 488: a tile's products and softmax
 // then follow one another, and what overlaps is the other tile's alone.  Of a step's 2000 cycles the products take
 // 1650: Q K^T with N = 64 reads 6 KB of shared memory per instruction, 52 cycles instead of 32.
-// P refers to a maximum that follows the running one only when that has grown by 2^64 or more: scaled by
-// a power of two, weights lose nothing in bf16 or fp32 before they overflow.  So S is read once, and O is
-// rescaled in TMEM next to never.
+// P refers to a maximum that follows the running one only when that has grown by 2^16 or more, and lies 2^16 above
+// it: no weight passes 1, so O overflows only where a sum of values does, and scaled by a power of two weights lose
+// nothing until they are below 2^-110 of the largest, where fp32 ends.  So S is read once, and O is rescaled in TMEM
+// next to never.
 // P is rounded to bf16, half a step of 2^-8 relative per weight, as the product takes one 16-bit type;
 // the sum of the weights is kept in fp32.
 //
@@ -43,7 +44,7 @@ namespace {
 constexpr int kSms = 152;
 constexpr int kTN = 64;         // cached tokens of a step
 constexpr int kMaxPieces = 16;
-constexpr float kGrow = 64.f;   // log2 of how far weights may outgrow their reference
+constexpr float kGrow = 16.f;   // log2 of how far scores may outgrow the maximum that weights refer to
 
 template <int D>
 struct Cfg {
@@ -483,7 +484,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       const int pos = min(first + qi / p.G, w.r.kv - 1);
       const int tmin = first + min(w.q0 + tile * 128, nq - 1) / p.G, cmin = first + w.q0 / p.G;
       const int tmax = min(first + (w.q0 + tile * 128 + 127) / p.G, w.r.kv - 1);
-      float m = -INFINITY, l = 0.f;  // the maximum that the weights refer to (of scores before their scale); their sum
+      float m = -INFINITY, l = 0.f;  // the maximum that the weights refer to (of scores before their scale); their
+                                     // sum, both pieces' and O's 2^-kGrow of e^(s - m)'s, which the join takes as it is
       bool wrote = false;            // O holds something, or will
       for (int j = w.j0; j < w.j1; ++j, ++tiles) {
         const uint32_t buf = tiles & 1, phase = tiles % kPh;
@@ -530,7 +532,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             scale_o<D>(o_col, f);
           }
         }
-        const float ms = m == -INFINITY ? 0.f : -m * sl2;
+        const float ms = m == -INFINITY ? 0.f : fmaf(-m, sl2, -kGrow);  // so that the largest weight is 1
         const uint64_t scale = pair(sl2, sl2), shift = pair(ms, ms);
         uint64_t sum[2] = {0, 0};
         float u[32];
