@@ -469,7 +469,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       const int qi = w.q0 + tile * 128 + row;
       const bool mine = qi < w.r.len * p.G;
       int g = -1;
-      if (mine) g = global_token(RowsDev{nullptr, p.rows.tok}, w.r.bos + qi / p.G, p.num_global, p.status);
+      if (mine) g = kv_token(p.rows, w.r.bos + qi / p.G, p.num_global, p.status);
       const int64_t head = (int64_t)(w.h * p.G + (mine ? qi % p.G : 0)) * D;
       out_at = g >= 0 ? (int64_t)g * p.out_stride + head : -1;
       load_queries<D>(p, qt, 32 * (warp & 3), g >= 0 ? (int64_t)g * p.q_stride + head : -1);
@@ -677,9 +677,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             eb += 32;
           } else {
             eb = e;
-            ids = eb + lane < entries ? __ldg(row + eb + lane) : 0;
+            ids = eb + lane < entries ? load(row + eb + lane) : 0;
           }
-          ahead = eb + 32 + lane < entries ? __ldg(row + eb + 32 + lane) : 0;
+          ahead = eb + 32 + lane < entries ? load(row + eb + 32 + lane) : 0;
         }
         int page = __shfl_sync(0xffffffffu, ids, active ? (pos >> shift) - eb : 0);
         page = active && pos < w.r.kv ? page_or_null(page, kv, p.status) : 0;
@@ -812,7 +812,7 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(PromptParams P) {
     }
   }
   const int t = qi / p.G;
-  const int g = p.rows.tok ? __ldg(p.rows.tok + w.r.bos + t) : w.r.bos + t;
+  const int g = p.rows.tok ? load(p.rows.tok + w.r.bos + t) : w.r.bos + t;
   if (g < 0 || g >= p.num_global) return;
   const float inv = l == 0.f ? 0.f : 1.f / l;
   __nv_bfloat16* out =

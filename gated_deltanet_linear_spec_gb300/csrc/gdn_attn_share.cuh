@@ -43,8 +43,8 @@ struct RawRow {
   int bos, eos, kv, trow;
 };
 __device__ __forceinline__ RawRow raw_row(const AttnLaunch& p, int n) {
-  return RawRow{__ldg(p.rows.qsl + n), __ldg(p.rows.qsl + n + 1), __ldg(p.rows.kv_lens + n),
-                p.rows.table_rows ? __ldg(p.rows.table_rows + n) : n};
+  return RawRow{load(p.rows.qsl + n), load(p.rows.qsl + n + 1), load(p.rows.kv_lens + n),
+                p.rows.table_rows ? load(p.rows.table_rows + n) : n};
 }
 
 // The tiles that the row's queries see; 0 for an empty or bad row.  QG: queries of a unit, 0 for all
@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(SplitParams P, in
       }
       if (qi >= nq || warp % team) continue;
       const int t = (qi0 + qi) / p.G;
-      const int g = p.rows.tok ? __ldg(p.rows.tok + bos + t) : bos + t;
+      const int g = p.rows.tok ? load(p.rows.tok + bos + t) : bos + t;
       if (g < 0 || g >= p.num_global) continue;
       const float inv = l == 0.f ? 0.f : 1.f / l;
       T* out = static_cast<T*>(p.out) + (int64_t)g * p.out_stride + (int64_t)(h * p.G + qi0 + qi - t * p.G) * D;

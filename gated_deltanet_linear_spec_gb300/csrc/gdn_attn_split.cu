@@ -215,8 +215,8 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, NW>::kThreads, 1)
       const int32_t* row = kv.table + (int64_t)w.u.r.trow * kv.max_pages;
       const int entries = (w.u.r.kv + ps - 1) >> shift;
       int eb = w.tile_at(w.j0) >> shift;
-      int ids = eb + lane < entries ? __ldg(row + eb + lane) : 0;
-      int ahead = eb + 32 + lane < entries ? __ldg(row + eb + 32 + lane) : 0;
+      int ids = eb + lane < entries ? load(row + eb + lane) : 0;
+      int ahead = eb + 32 + lane < entries ? load(row + eb + 32 + lane) : 0;
       // the unit's queries
       const int nq = w.u.r.len * p.G;
       int g[2];
@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, NW>::kThreads, 1)
       for (int u = 0; u < 2; ++u) {
         const int qi = lane + 32 * u;
         g[u] = -1;
-        if (qi < nq) g[u] = global_token(RowsDev{nullptr, p.rows.tok}, w.u.r.bos + qi / p.G, p.num_global, p.status);
+        if (qi < nq) g[u] = kv_token(p.rows, w.u.r.bos + qi / p.G, p.num_global, p.status);
         rows += __popc(__ballot_sync(0xffffffffu, g[u] >= 0));
       }
       ok = seg == 0 || tc::mbar_wait(&sm.qempty, (seg - 1) & 1, P.wait_ns);
@@ -255,9 +255,9 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, NW>::kThreads, 1)
             eb += 32;
           } else {
             eb = e;
-            ids = eb + lane < entries ? __ldg(row + eb + lane) : 0;
+            ids = eb + lane < entries ? load(row + eb + lane) : 0;
           }
-          ahead = eb + 32 + lane < entries ? __ldg(row + eb + 32 + lane) : 0;
+          ahead = eb + 32 + lane < entries ? load(row + eb + 32 + lane) : 0;
         }
         int page = __shfl_sync(0xffffffffu, ids, active ? (pos >> shift) - eb : 0);
         page = active && pos < w.u.r.kv ? page_or_null(page, kv, p.status) : 0;

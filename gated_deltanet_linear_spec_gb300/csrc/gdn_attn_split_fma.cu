@@ -30,7 +30,7 @@ constexpr int kNQ = 8;      // queries of a unit
 
 // 16 bytes' values.
 __device__ __forceinline__ void load16(const float* v, bool there, float (&x)[4]) {
-  const float4 y = there ? __ldg(reinterpret_cast<const float4*>(v)) : make_float4(0.f, 0.f, 0.f, 0.f);
+  const float4 y = there ? load(reinterpret_cast<const float4*>(v)) : make_float4(0.f, 0.f, 0.f, 0.f);
   x[0] = y.x;
   x[1] = y.y;
   x[2] = y.z;
@@ -41,7 +41,7 @@ __device__ __forceinline__ void open2(uint32_t u, float& lo, float& hi) {
   hi = __uint_as_float(u & 0xffff0000u);
 }
 __device__ __forceinline__ void load16(const __nv_bfloat16* v, bool there, float (&x)[8]) {
-  const uint4 y = there ? __ldg(reinterpret_cast<const uint4*>(v)) : make_uint4(0, 0, 0, 0);
+  const uint4 y = there ? load(reinterpret_cast<const uint4*>(v)) : make_uint4(0, 0, 0, 0);
   open2(y.x, x[0], x[1]);
   open2(y.y, x[2], x[3]);
   open2(y.z, x[4], x[5]);
@@ -51,9 +51,9 @@ __device__ __forceinline__ void load16(const __nv_bfloat16* v, bool there, float
 template <int E>
 __device__ __forceinline__ void load_row(const float* v, bool there, float (&x)[E]) {
   if constexpr (E == 1) {
-    x[0] = there ? __ldg(v) : 0.f;
+    x[0] = there ? load(v) : 0.f;
   } else if constexpr (E == 2) {
-    const float2 y = there ? __ldg(reinterpret_cast<const float2*>(v)) : make_float2(0.f, 0.f);
+    const float2 y = there ? load(reinterpret_cast<const float2*>(v)) : make_float2(0.f, 0.f);
     x[0] = y.x;
     x[1] = y.y;
   } else {
@@ -69,9 +69,9 @@ __device__ __forceinline__ void load_row(const float* v, bool there, float (&x)[
 template <int E>
 __device__ __forceinline__ void load_row(const __nv_bfloat16* v, bool there, float (&x)[E]) {
   if constexpr (E == 2) {
-    open2(there ? __ldg(reinterpret_cast<const uint32_t*>(v)) : 0u, x[0], x[1]);
+    open2(there ? load(reinterpret_cast<const uint32_t*>(v)) : 0u, x[0], x[1]);
   } else if constexpr (E == 4) {
-    const uint2 y = there ? __ldg(reinterpret_cast<const uint2*>(v)) : make_uint2(0, 0);
+    const uint2 y = there ? load(reinterpret_cast<const uint2*>(v)) : make_uint2(0, 0);
     open2(y.x, x[0], x[1]);
     open2(y.y, x[2], x[3]);
   } else {
@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) split_fma_kernel(SplitPar
     const int h = w.h % kv.Hkv, q0 = w.h / kv.Hkv * kNQ, nq = min(kNQ, row.len * p.G - q0);
     const int first = row.kv - row.len;  // position of the first new token
     int g = -1;                          // lane i < nq: the query's global token
-    if (lane < nq) g = global_token(RowsDev{nullptr, p.rows.tok}, row.bos + (q0 + lane) / p.G, p.num_global, p.status);
+    if (lane < nq) g = kv_token(p.rows, row.bos + (q0 + lane) / p.G, p.num_global, p.status);
     float q[kNQ][E];
 #pragma unroll
     for (int i = 0; i < kNQ; ++i) {
@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) split_fma_kernel(SplitPar
     const int32_t* table = kv.table + (int64_t)row.trow * kv.max_pages;
     auto entry = [&](int j) {  // the table's entry of this lane's token of tile j
       const int tok = w.tile_at(j) + lane;
-      return j < w.j0 + w.len && tok <= pos1 ? __ldg(table + (tok >> shift)) : 0;
+      return j < w.j0 + w.len && tok <= pos1 ? load(table + (tok >> shift)) : 0;
     };
     int ahead = entry(w.j0);
     for (int j = w.j0; j < w.j0 + w.len; ++j) {

@@ -24,6 +24,15 @@ struct KvRowsDev {
   int32_t num_seqs, num_tokens, max_q;
 };
 
+// What the calls read, by coherent loads: a kernel here starts while the one before it still runs, so lines of the
+// table, the pages and the rows may change between its start and its griddepcontrol.wait, which rules out the
+// read-only path (ld.global.nc, __ldg).
+template <typename T>
+__device__ __forceinline__ T load(const T* p) {
+  __builtin_assume(__isGlobal(p));  // (else a generic load, which waits for stores to shared memory)
+  return *p;
+}
+
 struct KvRow {
   int32_t bos, len;  // local tokens
   int32_t kv;        // cache length with them
@@ -50,8 +59,16 @@ __device__ __forceinline__ bool check_kv_row(const KvRowsDev& R, const KvDev& C,
   return true;
 }
 __device__ __forceinline__ bool load_kv_row(const KvRowsDev& R, const KvDev& C, int n, KvRow& r, uint32_t* st) {
-  return check_kv_row(R, C, __ldg(R.qsl + n), __ldg(R.qsl + n + 1), __ldg(R.kv_lens + n),
-                      R.table_rows ? __ldg(R.table_rows + n) : n, r, st);
+  return check_kv_row(R, C, load(R.qsl + n), load(R.qsl + n + 1), load(R.kv_lens + n),
+                      R.table_rows ? load(R.table_rows + n) : n, r, st);
+}
+
+// Global token of local token i (identity when there is no token_indx), or -1 if out of range.
+__device__ __forceinline__ int32_t kv_token(const KvRowsDev& R, int32_t i, int32_t num_global, uint32_t* st) {
+  const int32_t g = R.tok ? load(R.tok + i) : i;
+  if (g >= 0 && g < num_global) return g;
+  set_status(st, GDN_STATUS_TOKEN_RANGE);
+  return -1;
 }
 
 // A table entry as a page to read: its id, or 0 (no tokens) for NULL and out-of-range entries.

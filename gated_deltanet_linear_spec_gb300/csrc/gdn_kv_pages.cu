@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendLaunch p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int local = blockIdx.x * (kThreads / 32) + warp;
   if (local >= p.rows.num_tokens) return;
-  const int32_t g = p.rows.tok ? __ldg(p.rows.tok + local) : local;
+  const int32_t g = p.rows.tok ? load(p.rows.tok + local) : local;
   const bool there = g >= 0 && g < p.num_global;
   const int vec = C.d * p.es / 16;  // 16-byte vectors of one head
   const int all = C.Hkv * vec;
@@ -116,8 +116,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendLaunch p) {
 #pragma unroll
     for (int u = 0; u < kHeld; ++u) {
       const int i = from + 32 * u + lane;
-      kx[u] = there && i < all ? __ldg(ks + i) : make_uint4(0, 0, 0, 0);
-      vx[u] = there && i < all ? __ldg(vs + i) : make_uint4(0, 0, 0, 0);
+      kx[u] = there && i < all ? load(ks + i) : make_uint4(0, 0, 0, 0);
+      vx[u] = there && i < all ? load(vs + i) : make_uint4(0, 0, 0, 0);
     }
   };
   fetch(0);
@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendLaunch p) {
   int lo = 0, hi = p.rows.num_seqs - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (__ldg(p.rows.qsl + mid) <= local) lo = mid; else hi = mid - 1;
+    if (load(p.rows.qsl + mid) <= local) lo = mid; else hi = mid - 1;
   }
   KvRow r;
   if (!load_kv_row(p.rows, C, lo, r, p.status) || local < r.bos || local >= r.bos + r.len) return;
@@ -168,8 +168,8 @@ struct RowNeed {
 
 __device__ bool reserve_range(const PageRowsLaunch& p, int i, RowNeed& r) {
   const KvDev& C = p.cache;
-  r.trow = p.rows ? __ldg(p.rows + i) : i;
-  const int from = __ldg(p.a + i), to = __ldg(p.b + i);
+  r.trow = p.rows ? load(p.rows + i) : i;
+  const int from = load(p.a + i), to = load(p.b + i);
   if (r.trow < 0 || r.trow >= C.num_table_rows || from < 0 || to < 0 ||
       (int64_t)to > (int64_t)C.max_pages * C.page_size)
     return false;
@@ -184,9 +184,9 @@ struct ForkItem {
 };
 __device__ bool fork_item(const PageRowsLaunch& p, int i, ForkItem& f) {
   const KvDev& C = p.cache;
-  f.src = __ldg(p.src_rows + i);
-  f.dst = __ldg(p.rows + i);
-  const int len = __ldg(p.a + i);
+  f.src = load(p.src_rows + i);
+  f.dst = load(p.rows + i);
+  const int len = load(p.a + i);
   if (f.src < 0 || f.src >= C.num_table_rows || f.dst < 0 || f.dst >= C.num_table_rows || len < 0 ||
       (int64_t)len > (int64_t)C.max_pages * C.page_size)
     return false;
@@ -529,8 +529,8 @@ __global__ void __launch_bounds__(kThreads) release_kernel(PageRowsLaunch p) {
   let_next();
   wait_prior();
   for (int i = blockIdx.y; i < p.count; i += gridDim.y) {
-    const int trow = p.rows ? __ldg(p.rows + i) : i;
-    const int lo = p.a ? __ldg(p.a + i) : 0, hi = p.b ? __ldg(p.b + i) : C.max_pages;
+    const int trow = p.rows ? load(p.rows + i) : i;
+    const int lo = p.a ? load(p.a + i) : 0, hi = p.b ? load(p.b + i) : C.max_pages;
     if (trow < 0 || trow >= C.num_table_rows || lo < 0 || hi > C.max_pages) {
       if (blockIdx.x == 0 && threadIdx.x == 0) set_status(p.status, GDN_STATUS_PAGE_RANGE);
       continue;
@@ -680,7 +680,7 @@ __global__ void __launch_bounds__(kThreads) copy_items_kernel(CopyLaunch p, int 
   for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
     const int i = (int)(u / pieces);
     int piece = (int)(u - (int64_t)i * pieces);
-    const int src = __ldg(p.src + i), dst = __ldg(p.dst + i);
+    const int src = load(p.src + i), dst = load(p.dst + i);
     if (src >= p.limit || dst >= p.limit) {
       if (threadIdx.x == 0) set_status(p.status, p.range_bit);
       continue;
