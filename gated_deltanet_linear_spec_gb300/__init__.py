@@ -367,11 +367,15 @@ def _stream_of(t: torch.Tensor, stream) -> Optional[int]:
 
 
 def _scratch(nbytes: int, device, stream) -> torch.Tensor:
-    """A workspace that its allocator keeps until the work on ``stream`` is done with it."""
-    ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
-    if stream is not None:
-        ws.record_stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
-    return ws
+    """A workspace, allocated on the stream that works on it: a block of another stream's could still be in use by
+    work queued there, and would be free for more of it as soon as the call returns."""
+    if stream is None:
+        return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream(stream)
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
 
 
 def _check(rc: int) -> None:

@@ -60,3 +60,43 @@ def test_pages_handed_out_again(dtype):
                     torch.cuda.synchronize()
         outs.append(out)
     assert torch.equal(*outs)
+
+
+def test_a_workspace_is_a_block_of_the_stream_that_uses_it():
+    """Nothing may run here: a block that the current stream has just given back is not another stream's."""
+    side, size = torch.cuda.Stream(), 3 << 20
+    held = torch.empty(size, dtype=torch.uint8, device="cuda")
+    at = held.data_ptr()
+    del held
+    ws = gdn._scratch(size, "cuda", side)
+    mine = ws.data_ptr()
+    assert mine != at
+    del ws
+    assert torch.empty(size, dtype=torch.uint8, device="cuda").data_ptr() != mine
+    for same in (side, side.cuda_stream):
+        assert gdn._scratch(size, "cuda", same).data_ptr() == mine
+    assert gdn._scratch(size, "cuda", None).data_ptr() == at
+    assert gdn._scratch(size, "cuda", 0).data_ptr() == at
+
+
+@pytest.mark.parametrize("rows", [[(1, 900), (1, 65)] * 8, [(200, 300), (70, 70)]], ids=["decode", "prompt"])
+@pytest.mark.parametrize("dim,dtype", [(128, BF16), (96, BF16), (64, F32)])
+def test_other_streams_and_graphs(rows, dim, dtype):
+    s = Step(rows, heads=8, kv_heads=2, dim=dim, dtype=dtype, seed=dim)
+    want, _ = s.run()
+    side = torch.cuda.Stream()
+    for given in (side, side.cuda_stream):
+        s.out.fill_(0)
+        side.wait_stream(torch.cuda.current_stream())
+        gdn.gdn_paged_attention(s.attn, s.cache, s.kv_rows, s.qd, s.out, stream=given)
+        side.synchronize()
+        assert torch.equal(s.out.cpu()[s.token], want[s.token])
+    ws = torch.empty(max(gdn.gdn_attention_workspace_bytes(s.attn, s.cache, s.kv_rows), 1), dtype=torch.uint8, device="cuda")
+    for kept in (ws, None):  # (a workspace made under capture belongs to the graph)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            gdn.gdn_paged_attention(s.attn, s.cache, s.kv_rows, s.qd, s.out, workspace=kept)
+        s.out.fill_(0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(s.out.cpu()[s.token], want[s.token])

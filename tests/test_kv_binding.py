@@ -69,3 +69,42 @@ def test_one_token_and_strided_tokens_are_taken():
     assert gdn._token_rows(dev(0, 2, 64), torch.bfloat16, 2, 64, "k")[1] == 0
     both = dev(8, 2, 2, 16, 64)
     assert cache(k_pool=both[:, 0], v_pool=both[:, 1])._desc.page_stride == 2 * 2 * 16 * 64
+
+
+# ------------------------------------------------------------------------------------------
+# workspaces that a call makes
+
+class Stream:
+    """A stream as far as the binding looks at it."""
+
+    def __init__(self, handle):
+        self.handle = self.cuda_stream = handle
+
+
+@pytest.mark.parametrize("given,want", [(None, None), (Stream(77), 77), (88, 88), (0, "default")])
+def test_a_workspace_is_allocated_on_the_stream_that_uses_it(monkeypatch, given, want):
+    active, seen = [], []
+
+    class Under:
+        def __init__(self, stream):
+            self.stream = stream
+
+        def __enter__(self):
+            active.append(self.stream.handle)
+
+        def __exit__(self, *_):
+            active.pop()
+
+    empty = torch.empty
+
+    def allocate(*size, device=None, **kw):
+        seen.append(active[-1] if active else None)
+        return empty(*size, **kw)
+
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    monkeypatch.setattr(torch.cuda, "stream", Under)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device=None: Stream(handle))
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: Stream("default"))
+    monkeypatch.setattr(torch, "empty", allocate)
+    assert gdn._scratch(100, "cuda:0", given).numel() == 100
+    assert seen == [want] and not active
