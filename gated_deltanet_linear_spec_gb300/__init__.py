@@ -426,7 +426,7 @@ def gdn_chunk_prefill(layer: Layer, params: Params, pools: Pools, qkv: torch.Ten
     act = layer.act_dtype
     need = gdn_prefill_workspace_bytes(layer, rows, rows.num_seqs)
     if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=qkv.device)
+        workspace = _scratch(need, qkv.device, stream)
     ws_ptr = _ptr(workspace, torch.uint8, "workspace")
     ws_bytes = 0 if workspace is None else workspace.numel()
     rc = library().gdn_chunk_prefill(ctypes.byref(layer.c()), ctypes.byref(params.c(act)), ctypes.byref(pools.c(act)),
@@ -449,7 +449,7 @@ def gdn_mixed_batch(layer: Layer, params: Params, pools: Pools, x: torch.Tensor,
         num_actual_tokens = int(x.shape[0])
     if workspace is None:
         need = mixed_batch_workspace_bytes(layer, non_spec, num_prefills, spec)
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=x.device)
+        workspace = _scratch(need, x.device, stream)
     rc = library().gdn_mixed_batch(ctypes.byref(layer.c()), ctypes.byref(params.c(act)), ctypes.byref(pools.c(act)),
                                    _ptr(x, act, "x"), _ptr(a, act, "a"), _ptr(b, act, "b"), int(num_actual_tokens),
                                    _rows_ref(non_spec), int(num_decodes), int(num_prefills), _rows_ref(spec),

@@ -108,3 +108,27 @@ def test_a_workspace_is_allocated_on_the_stream_that_uses_it(monkeypatch, given,
     monkeypatch.setattr(torch, "empty", allocate)
     assert gdn._scratch(100, "cuda:0", given).numel() == 100
     assert seen == [want] and not active
+
+
+def test_the_gdn_calls_make_their_workspace_the_same_way(monkeypatch):
+    class Made(Exception):
+        pass
+
+    def scratch(nbytes, device, stream):
+        assert nbytes >= 1
+        raise Made(stream)
+
+    monkeypatch.setattr(gdn, "_scratch", scratch)
+    layer = gdn.Layer(1, 2, 128, 128, 4, 6)
+    f32 = torch.float32
+    params = gdn.Params(dev(layer.channels, 4), dev(2, dtype=f32), dev(2, dtype=f32))
+    pools = gdn.Pools(dev(3, 6, layer.channels), dev(3, 2, 128, 128, dtype=f32))
+    some = gdn.Rows(i32([0, 70]), 70, state_indices=i32([1]))
+    x, a, out = dev(70, layer.channels), dev(70, 2), dev(70, 2, 128)
+    for stream in (None, 77):
+        with pytest.raises(Made) as e:
+            gdn.gdn_chunk_prefill(layer, params, pools, x, a, a, some, out, stream=stream)
+        assert e.value.args == (stream,)
+        with pytest.raises(Made) as e:
+            gdn.gdn_mixed_batch(layer, params, pools, x, a, a, some, 0, 1, None, out, stream=stream)
+        assert e.value.args == (stream,)
