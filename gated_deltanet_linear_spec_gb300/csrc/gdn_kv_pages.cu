@@ -404,7 +404,8 @@ __global__ void __cluster_dims__(kHandCtas) __launch_bounds__(kHandThreads, 1) h
     }
     if (lane == 0) {
       if (!ok) set_status(p.status, GDN_STATUS_PAGE_RANGE);
-      w.need[i] = ok ? n : -1;
+      // (as many as the pool has are never free: the sums of 1024 rows stay below 2^27)
+      w.need[i] = ok ? min(n, C.num_pages) : -1;
       if (kFork) {
         w.old_page[i] = ok && last > 0 ? last : 0;
         w.used[i] = ok ? used : 0;
@@ -429,7 +430,7 @@ __global__ void __cluster_dims__(kHandCtas) __launch_bounds__(kHandThreads, 1) h
     int sum;
     const int at = hand_scan(i < p.count ? max(__ldcg(w.need + i), 0) : 0, sum, part);
     if (cta == 0 && i < p.count) w.off[i] = base + at;
-    base = min(base + sum, 1 << 30);  // needs past every pool stay past it
+    base = min(base + sum, 1 << 30);  // needs past every pool stay past it (here a pool has 2^17 pages at most)
   }
   if (cta == 0 && tid == 0) w.total[0] = have;
   for (int at = first + before; mask && at < base; mask &= mask - 1) w.list_a[at++] = p0 + __ffs(mask) - 1;
