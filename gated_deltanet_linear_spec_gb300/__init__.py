@@ -260,6 +260,19 @@ def _token_rows(t: torch.Tensor, dtype: torch.dtype, heads: int, dim: int, name:
     return t.data_ptr(), (st[0] if t.shape[0] > 1 else 0)
 
 
+def _one_device(device: int, *tensors: Optional[torch.Tensor]) -> None:
+    for t in tensors:
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"tensors on cuda:{device} and cuda:{t.get_device()} in one call")
+
+
+def _on_current(device: int, *tensors: Optional[torch.Tensor]) -> None:
+    """The library launches on the current device: every tensor of a call has to be there."""
+    if torch.cuda.current_device() != device:
+        raise ValueError(f"the call's tensors are on cuda:{device}, the current device is cuda:{torch.cuda.current_device()}")
+    _one_device(device, *tensors)
+
+
 @dataclass(frozen=True)
 class KvCache:
     """The paged key-value cache of an attention layer (``gdn_kv_cache``): pools
@@ -292,8 +305,10 @@ class KvCache:
         desc = _KvCache(k.data_ptr(), v.data_ptr(), k.stride(0) if pages > 1 else 0,
                         _int32(self.block_table, "block_table"), _int32(self.refcount, "refcount", pages), pages,
                         self.block_table.shape[0], self.block_table.shape[1], size, heads, dim, _dtype_code(k.dtype))
+        _one_device(k.get_device(), v, self.block_table, self.refcount)
         object.__setattr__(self, "_desc", desc)
         object.__setattr__(self, "_ref", ctypes.byref(desc))
+        object.__setattr__(self, "_device", k.get_device())
 
     @property
     def dtype(self) -> torch.dtype:
@@ -318,6 +333,7 @@ class KvRows:
                        _int32(self.token_indx, "token_indx", int(self.num_tokens)),
                        _int32(self.table_rows, "table_rows", n), _int32(self.kv_lens, "kv_lens", n),
                        int(self.max_query_len))
+        _one_device(self.query_start_loc.get_device(), self.token_indx, self.table_rows, self.kv_lens)
         object.__setattr__(self, "_desc", desc)
         object.__setattr__(self, "_ref", ctypes.byref(desc))
 
@@ -484,6 +500,7 @@ def gdn_kv_append(cache: KvCache, rows: KvRows, k: torch.Tensor, v: torch.Tensor
     vp, vs = _token_rows(v, cache.dtype, heads, dim, "v")
     if k.shape[0] != v.shape[0]:
         raise ValueError("k and v: expected one token count")
+    _on_current(cache._device, rows.query_start_loc, k, v, status)
     _check(library().gdn_kv_append(cache._ref, rows._ref, kp, ks, vp, vs, k.shape[0],
                                    _ptr(status, torch.int32, "status"), _stream_of(cache.k_pool, stream)))
 
@@ -502,6 +519,7 @@ def gdn_paged_attention(attn: Attention, cache: KvCache, rows: KvRows, q: torch.
     op, os_ = _token_rows(out, cache.dtype, attn.num_q_heads, dim, "out")
     if q.shape[0] != out.shape[0]:
         raise ValueError("q and out: expected one token count")
+    _on_current(cache._device, rows.query_start_loc, q, out, workspace, status)
     if workspace is None:
         workspace = _scratch(gdn_attention_workspace_bytes(attn, cache, rows), q.device, stream)
     _check(library().gdn_paged_attention(attn._ref, cache._ref, rows._ref, qp, qs, q.shape[0], op, os_,
@@ -523,6 +541,7 @@ def gdn_kv_reserve(cache: KvCache, table_rows: Optional[torch.Tensor], from_lens
                    stream=None) -> None:
     """Gives each listed table row free pages for its tokens [from_lens, to_lens)."""
     n = from_lens.numel()
+    _on_current(cache._device, table_rows, from_lens, to_lens, workspace, status)
     ws = _kv_workspace(cache, n, workspace, stream)
     _check(library().gdn_kv_reserve(cache._ref, n, _int32(table_rows, "table_rows", n), _int32(from_lens, "from_lens"),
                                     _int32(to_lens, "to_lens", n), _ptr(ws, torch.uint8, "workspace"), ws.numel(),
@@ -534,6 +553,7 @@ def gdn_kv_release(cache: KvCache, table_rows: torch.Tensor, first_page: Optiona
                    stream=None) -> None:
     """Gives back the pages of entries [first_page, last_page) of each listed table row."""
     n = table_rows.numel()
+    _on_current(cache._device, table_rows, first_page, last_page, status)
     _check(library().gdn_kv_release(cache._ref, n, _int32(table_rows, "table_rows"),
                                     _int32(first_page, "first_page", n), _int32(last_page, "last_page", n),
                                     _ptr(status, torch.int32, "status"), _stream_of(cache.k_pool, stream)))
@@ -543,6 +563,7 @@ def gdn_kv_fork(cache: KvCache, src_rows: torch.Tensor, dst_rows: torch.Tensor, 
                 workspace: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None, stream=None) -> None:
     """Table row dst_rows[i] becomes a holder of the first lens[i] tokens of src_rows[i]."""
     n = src_rows.numel()
+    _on_current(cache._device, src_rows, dst_rows, lens, workspace, status)
     ws = _kv_workspace(cache, n, workspace, stream)
     _check(library().gdn_kv_fork(cache._ref, n, _int32(src_rows, "src_rows"), _int32(dst_rows, "dst_rows", n),
                                  _int32(lens, "lens", n), _ptr(ws, torch.uint8, "workspace"), ws.numel(),
@@ -553,6 +574,7 @@ def gdn_kv_copy_pages(cache: KvCache, src_pages: torch.Tensor, dst_pages: torch.
                       status: Optional[torch.Tensor] = None, stream=None) -> None:
     """Copies page src_pages[i] onto dst_pages[i] in both pools."""
     n = src_pages.numel()
+    _on_current(cache._device, src_pages, dst_pages, status)
     _check(library().gdn_kv_copy_pages(cache._ref, n, _int32(src_pages, "src_pages"),
                                        _int32(dst_pages, "dst_pages", n), _ptr(status, torch.int32, "status"),
                                        _stream_of(cache.k_pool, stream)))
@@ -561,6 +583,7 @@ def gdn_kv_copy_pages(cache: KvCache, src_pages: torch.Tensor, dst_pages: torch.
 def gdn_kv_compact(cache: KvCache, num_live: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
                    status: Optional[torch.Tensor] = None, stream=None) -> None:
     """Moves the live pages to ids 1..M; ``num_live`` (int32, one entry) receives M."""
+    _on_current(cache._device, num_live, workspace, status)
     ws = _kv_workspace(cache, 0, workspace, stream)
     _check(library().gdn_kv_compact(cache._ref, _int32(num_live, "num_live", 1), _ptr(ws, torch.uint8, "workspace"),
                                     ws.numel(), _ptr(status, torch.int32, "status"), _stream_of(cache.k_pool, stream)))
@@ -571,6 +594,7 @@ def gdn_copy_slots(layer: Layer, pools: Pools, src_slots: torch.Tensor, dst_slot
     """Copies GDN state: slot src_slots[i] of both pools onto dst_slots[i] (a NULL source reads as zeros)."""
     n = src_slots.numel()
     act = layer.act_dtype
+    _on_current(pools.ssm_pool.get_device(), pools.conv_pool, src_slots, dst_slots, status)
     _check(library().gdn_copy_slots(ctypes.byref(layer.c()), ctypes.byref(pools.c(act)), n,
                                     _int32(src_slots, "src_slots"), _int32(dst_slots, "dst_slots", n),
                                     _ptr(status, torch.int32, "status"), _stream_of(pools.ssm_pool, stream)))

@@ -132,3 +132,80 @@ def test_the_gdn_calls_make_their_workspace_the_same_way(monkeypatch):
         with pytest.raises(Made) as e:
             gdn.gdn_mixed_batch(layer, params, pools, x, a, a, some, 0, 1, None, out, stream=stream)
         assert e.value.args == (stream,)
+
+
+# ------------------------------------------------------------------------------------------
+# tensors of several devices, and of one that is not the current one
+
+class OnAnother(OnDevice):
+    def get_device(self):
+        return 1
+
+
+def other(t):
+    return t.as_subclass(OnAnother)
+
+
+def test_descriptors_over_two_devices_are_refused():
+    for name, t in (("v_pool", dev(8, 2, 16, 64)), ("block_table", i32([[1]])), ("refcount", i32([0] * 8))):
+        with pytest.raises(ValueError, match="cuda:0 and cuda:1"):
+            cache(**{name: other(t)})
+    for name, t in (("kv_lens", i32([5, 9])), ("table_rows", i32([0, 1])), ("token_indx", i32([0, 1, 2, 3]))):
+        with pytest.raises(ValueError, match="cuda:0 and cuda:1"):
+            rows(**{name: other(t)})
+
+
+def calls(c, r, move=lambda t: t):
+    """Every call of the cache, its tensors taken through ``move``."""
+    k, q, n, ws = move(dev(4, 2, 64)), move(dev(4, 8, 64)), move(i32([1, 2])), move(torch.zeros(1 << 20, dtype=torch.uint8).as_subclass(OnDevice))
+    layer, pools = gdn.Layer(2, 4, 16, 32, 4, 5), gdn.Pools(None, move(dev(4, 4, 32, 16, dtype=torch.float32)))
+    return [lambda **kw: gdn.gdn_kv_append(c, r, k, k, **kw),
+            lambda **kw: gdn.gdn_paged_attention(gdn.Attention(8), c, r, q, q, workspace=ws, **kw),
+            lambda **kw: gdn.gdn_kv_reserve(c, n, n, n, workspace=ws, **kw),
+            lambda **kw: gdn.gdn_kv_release(c, n, n, n, **kw),
+            lambda **kw: gdn.gdn_kv_fork(c, n, n, n, workspace=ws, **kw),
+            lambda **kw: gdn.gdn_kv_copy_pages(c, n, n, **kw),
+            lambda **kw: gdn.gdn_kv_compact(c, n[:1], workspace=ws, **kw),
+            lambda **kw: gdn.gdn_copy_slots(layer, pools, n, n, **kw)]
+
+
+@pytest.fixture
+def no_launch(monkeypatch):
+    """The library's calls do nothing, and say so."""
+    ran = []
+
+    class Library:
+        def __getattr__(self, name):
+            return lambda *a: ran.append(name) or 0
+
+    monkeypatch.setattr(gdn, "library", lambda: Library())
+    monkeypatch.setattr(gdn, "_stream_of", lambda t, stream: None)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    return ran
+
+
+def test_calls_go_through_on_the_current_device(no_launch):
+    for call in calls(cache(), rows()):
+        call(status=i32([0]))
+    assert len(no_launch) == 8
+
+
+def test_calls_over_two_devices_are_refused(no_launch):
+    c, r = cache(), rows()
+    for call in calls(c, r, other)[:-1]:  # (the last one's tensors are all on the other device)
+        with pytest.raises(ValueError, match="cuda:0 and cuda:1"):
+            call()
+    for call in calls(c, r):
+        with pytest.raises(ValueError, match="cuda:0 and cuda:1"):
+            call(status=other(i32([0])))
+    with pytest.raises(ValueError, match="cuda:0 and cuda:1"):
+        calls(c, rows(**{k: other(v) for k, v in dict(query_start_loc=i32([0, 2, 4]), kv_lens=i32([5, 9])).items()}))[0]()
+    assert not no_launch
+
+
+def test_calls_off_the_current_device_are_refused(no_launch, monkeypatch):
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    for call in calls(cache(), rows()):
+        with pytest.raises(ValueError, match="current device"):
+            call()
+    assert not no_launch
