@@ -456,8 +456,10 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, NW>::kThreads, 1)
   }
 }
 
-// Queries of a unit, at most.
-int64_t queries_of(const AttnLaunch& a) { return a.few > 0 ? a.few : (int64_t)a.rows.max_q * a.G; }
+// Queries of a unit, at most (with max_q = 0 every row is a bad one, and reported).
+int64_t queries_of(const AttnLaunch& a) {
+  return a.few > 0 ? a.few : std::max<int64_t>(1, (int64_t)a.rows.max_q * a.G);
+}
 
 template <int D, int WQ, int DS, int NW>
 cudaError_t launch_cfg(const AttnLaunch& a, cudaStream_t s) {

@@ -300,7 +300,7 @@ cudaError_t launch_as(const AttnLaunch& a, cudaStream_t s) {
   cfg.numAttrs = 1;
   cudaError_t e = cudaLaunchKernelEx(&cfg, split_fma_kernel<T, E, DC>, P);
   if (e != cudaSuccess) return e;
-  const int queries = (int)std::min<int64_t>(kNQ, (int64_t)a.rows.max_q * a.G);
+  const int queries = (int)std::min<int64_t>(kNQ, std::max<int64_t>(1, (int64_t)a.rows.max_q * a.G));
   cfg.gridDim = dim3(ctas * kWarps, join_rows(ctas * kWarps, queries));
   cfg.blockDim = dim3(32 * kJoinWarps);
   return cudaLaunchKernelEx(&cfg, join_kernel<T, E, DC>, P, kNQ);

@@ -167,7 +167,7 @@ int gdn_kv_append(const gdn_kv_cache* cache, const gdn_kv_rows* rows, const void
 
 size_t gdn_attention_workspace_bytes(const gdn_attn_desc* attn, const gdn_kv_cache* cache, const gdn_kv_rows* rows) {
   if (check_shape(cache) || check_table(cache) || check_attn(attn, cache) || check_kv_rows(rows)) return 0;
-  if (rows->num_seqs == 0 || rows->max_query_len == 0) return 0;
+  if (rows->num_seqs == 0) return 0;
   AttnLaunch p = attn_args(attn, cache, rows);
   if (attn_split_supported(p, cache->dtype)) return round256(attn_split_workspace(p));
   if (!attn_prompt_supported(p, cache->dtype)) return round256(attn_split_fma_workspace(p));
@@ -185,7 +185,7 @@ int gdn_paged_attention(const gdn_attn_desc* attn, const gdn_kv_cache* cache, co
       (rc = check_attn(attn, cache)) || (rc = check_kv_rows(rows)))
     return rc;
   if (num_global_tokens < 0) return GDN_ERR_SHAPE;
-  if (rows->num_tokens == 0 || rows->max_query_len == 0) return GDN_OK;
+  if (rows->num_tokens == 0) return GDN_OK;
   if (!q || !out) return GDN_ERR_NULL_ARG;
   if (!aligned16(q) || !aligned16(out)) return GDN_ERR_ALIGN;
   if (!rows->token_indx && rows->num_tokens > num_global_tokens) return GDN_ERR_SHAPE;

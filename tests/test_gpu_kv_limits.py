@@ -4,6 +4,7 @@ import torch
 
 import gated_deltanet_linear_spec_gb300 as gdn
 from tests import kv_reference as ref
+from tests.test_gpu_attention import BF16, F32, Step
 
 pytestmark = pytest.mark.gpu
 
@@ -27,3 +28,18 @@ def test_needs_whose_sum_passes_32_bits(pages):
     assert int(table[0].count_nonzero()) == 3
     assert all(int(table[i:i + 256].count_nonzero()) == 0 for i in range(1, rows, 256))
     assert count[:5].tolist() == [0, 1, 1, 1, 0] and int(count.sum()) == 3
+
+
+@pytest.mark.parametrize("dim,dtype", [(64, BF16), (128, BF16), (256, BF16), (96, BF16), (64, F32)])
+def test_rows_longer_than_a_length_of_zero_are_reported(dim, dtype):
+    s = Step([(1, 20), (0, 7), (3, 40)], dim=dim, dtype=dtype, gather=False)
+    s.kv_rows = gdn.KvRows(s.kv_rows.query_start_loc, 4, s.kv_rows.kv_lens, 0, s.kv_rows.table_rows)
+    got, status = s.run()
+    assert status == ref.ROW_RANGE and torch.all(got.float() == 7.0)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    k = torch.ones(4, 2, dim, dtype=dtype, device="cuda")
+    before = [t.clone() for t in s.kv]
+    gdn.gdn_kv_append(s.cache, s.kv_rows, k, k, status=status)
+    assert int(status) == ref.ROW_RANGE
+    view = torch.int16 if dtype == BF16 else torch.int32
+    assert all(torch.equal(a.view(view), b.view(view)) for a, b in zip(s.kv, before))
