@@ -244,6 +244,13 @@ def _int32(t: Optional[torch.Tensor], name: str, count: Optional[int] = None) ->
     return _ptr(t, torch.int32, name)
 
 
+def _fits32(value: int, name: str) -> int:
+    """ctypes cuts what a 32-bit field does not hold."""
+    if not -(1 << 31) <= int(value) < 1 << 31:
+        raise ValueError(f"{name}: {value} does not fit 32 bits")
+    return int(value)
+
+
 def _token_rows(t: torch.Tensor, dtype: torch.dtype, heads: int, dim: int, name: str):
     """Pointer and token stride of a [tokens, heads, dim] tensor; the token dimension may be strided."""
     if not t.is_cuda:
@@ -252,6 +259,7 @@ def _token_rows(t: torch.Tensor, dtype: torch.dtype, heads: int, dim: int, name:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
         raise ValueError(f"{name}: expected [tokens, {heads}, {dim}], got {tuple(t.shape)}")
+    _fits32(t.shape[0], f"{name}'s tokens")
     st = t.stride()
     if (dim > 1 and st[2] != 1) or (heads > 1 and st[1] != dim):
         raise TypeError(f"{name}: the heads of a token must be contiguous")
@@ -329,10 +337,10 @@ class KvRows:
 
     def __post_init__(self):
         n = self.query_start_loc.numel() - 1
-        desc = _KvRows(n, int(self.num_tokens), _int32(self.query_start_loc, "query_start_loc"),
+        desc = _KvRows(n, _fits32(self.num_tokens, "num_tokens"), _int32(self.query_start_loc, "query_start_loc"),
                        _int32(self.token_indx, "token_indx", int(self.num_tokens)),
                        _int32(self.table_rows, "table_rows", n), _int32(self.kv_lens, "kv_lens", n),
-                       int(self.max_query_len))
+                       _fits32(self.max_query_len, "max_query_len"))
         _one_device(self.query_start_loc.get_device(), self.token_indx, self.table_rows, self.kv_lens)
         object.__setattr__(self, "_desc", desc)
         object.__setattr__(self, "_ref", ctypes.byref(desc))
@@ -357,7 +365,8 @@ class Attention:
     num_sinks: int = 0
 
     def __post_init__(self):
-        desc = _AttnDesc(self.num_q_heads, float(self.scale), self.window, self.num_sinks)
+        desc = _AttnDesc(_fits32(self.num_q_heads, "num_q_heads"), float(self.scale), _fits32(self.window, "window"),
+                         _fits32(self.num_sinks, "num_sinks"))
         object.__setattr__(self, "_desc", desc)
         object.__setattr__(self, "_ref", ctypes.byref(desc))
 

@@ -209,3 +209,19 @@ def test_calls_off_the_current_device_are_refused(no_launch, monkeypatch):
         with pytest.raises(ValueError, match="current device"):
             call()
     assert not no_launch
+
+
+# ------------------------------------------------------------------------------------------
+# values that a 32-bit field does not hold
+
+@pytest.mark.parametrize("value", [1 << 31, (1 << 32) + 1, -(1 << 31) - 1])
+def test_values_past_32_bits_are_refused(value):
+    for field in ("num_q_heads", "window", "num_sinks"):
+        with pytest.raises(ValueError, match=field):
+            gdn.Attention(**{"num_q_heads": 8, field: value})
+    for field in ("num_tokens", "max_query_len"):
+        with pytest.raises(ValueError, match=field):
+            rows(**{field: value})
+    with pytest.raises(ValueError, match="32 bits"):
+        gdn._token_rows(dev(1, 2, 64).expand(1 << 32, 2, 64), torch.bfloat16, 2, 64, "k")
+    assert gdn.Attention(8, window=(1 << 31) - 1)._desc.window == (1 << 31) - 1
