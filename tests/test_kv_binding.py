@@ -1,5 +1,7 @@
 """What the paged cache's binding refuses or arranges before it calls the library, on the host: tensors of the
 CPU stand in for those of a GPU, and every call here ends before a launch."""
+import ctypes
+
 import pytest
 import torch
 
@@ -225,3 +227,10 @@ def test_values_past_32_bits_are_refused(value):
     with pytest.raises(ValueError, match="32 bits"):
         gdn._token_rows(dev(1, 2, 64).expand(1 << 32, 2, 64), torch.bfloat16, 2, 64, "k")
     assert gdn.Attention(8, window=(1 << 31) - 1)._desc.window == (1 << 31) - 1
+
+
+@pytest.mark.parametrize("pages,count", [(2, 0), (60, 0), (60, 3), (9000, 17), (131072, 64), (300000, 1)])
+def test_workspace_of_the_page_calls(pages, count):
+    desc = gdn._KvCache(0x100000, 0x100000, 0, 0x100000, 0x100000, pages, 8, 16, 16, 2, 64, gdn.GDN_BF16)
+    ints = 5 * count + max(-(-pages // 1024), 8) + 4 + 2 * pages  # rows' values, block counts, totals, two lists
+    assert gdn.library().gdn_kv_workspace_bytes(ctypes.byref(desc), count) == (4 * ints + 255) // 256 * 256
