@@ -8,7 +8,7 @@
 //   list:   the free pages, lowest first, up to the total need, and the rows' exclusive sums;
 //   assign: row i takes free[offset_i ..] when offset_i + need_i is covered.
 // Pools of up to 131072 pages (kHandPages) go through them in one launch of a cluster, with barriers in
-// between; larger ones in three dependent launches.
+// between; larger ones, and forks in tables of long rows (kHandEntries), in three dependent launches.
 // Counters change by integer adds only, so their order does not matter.
 #include "gdn_kv.cuh"
 
@@ -334,6 +334,11 @@ __device__ __forceinline__ void cluster_sync() {
 constexpr int kHandCtas = 8, kHandThreads = 1024;
 constexpr int kHandPer = 16;  // pages of a thread
 constexpr int kHandPages = kHandCtas * kHandThreads * kHandPer;
+// Entries of a table row up to which forks go in one launch.  There a warp walks a row's entries and a cluster has 256
+// warps, in three launches a block on any SM does.  64 forks of full rows (pages of 16, time on the GPU): of 62 entries
+// 17 us in one launch, 14 in three, of 500 27 and 14, of 1000 38 and 14, of 8000 224 and 32; three more launches cost a
+// step that is bound by its launches 3 us a call (release, fork and reserve of 64 rows: 20 us, 26).
+constexpr int kHandEntries = 1024;
 
 // Exclusive sum over the threads of a CTA of the cluster.
 __device__ int hand_scan(int v, int& total, int* part) {
@@ -360,7 +365,7 @@ __device__ int hand_scan(int v, int& total, int* part) {
 
 // Reserve, or fork but for the copies, in one launch of a cluster: a warp per row, a thread per kHandPer pages.
 // The three launches that it stands for take their time in starts and ends; what is computed is a few microseconds'
-// reads.  Release, fork and reserve of 64 rows took 26.8 us in eight launches and take 20.1 in four.
+// reads.  Release, fork and reserve of 64 rows take 26 to 29 us in eight launches and 20 in four.
 template <bool kFork>
 __global__ void __cluster_dims__(kHandCtas) __launch_bounds__(kHandThreads, 1) hand_out_kernel(PageRowsLaunch p) {
   __shared__ int part[32];
@@ -750,7 +755,7 @@ cudaError_t launch_kv_release(const PageRowsLaunch& p, cudaStream_t s) {
 cudaError_t launch_kv_fork(const PageRowsLaunch& p, cudaStream_t s) {
   const int nb = page_blocks(p.cache.num_pages);
   cudaError_t e;
-  if (p.cache.num_pages <= kHandPages) {
+  if (p.cache.num_pages <= kHandPages && p.cache.max_pages <= kHandEntries) {
     e = launch_hand_out(hand_out_kernel<true>, s, p);
   } else {
     e = launch_after(need_kernel<true>, dim3(nb + p.count), s, p);

@@ -5,6 +5,7 @@ import torch
 import gated_deltanet_linear_spec_gb300 as gdn
 from tests import kv_reference as ref
 from tests.test_gpu_attention import BF16, F32, Step
+from tests.test_gpu_kv_pages import Pool
 
 pytestmark = pytest.mark.gpu
 
@@ -43,3 +44,21 @@ def test_rows_longer_than_a_length_of_zero_are_reported(dim, dtype):
     assert int(status) == ref.ROW_RANGE
     view = torch.int16 if dtype == BF16 else torch.int32
     assert all(torch.equal(a.view(view), b.view(view)) for a, b in zip(s.kv, before))
+
+
+@pytest.mark.parametrize("width", [1023, 1024, 1025, 2500])
+@pytest.mark.parametrize("pages", [9000, 131073])
+def test_forks_in_tables_of_long_rows(width, pages):
+    """Tables of up to 1024 entries a row and of more: other launches, the same pages."""
+    P = Pool(pages, 12, width, page=16, heads=2, dim=16)
+    full = 16 * width
+    P.reserve([3, 8, 0], [0, 0, 0], [full, full - 5, 100])
+    P.fork([3, 8, 3, 8, 0, 3], [1, 2, 4, 5, 6, 7], [full, full - 5, 33, full - 16, 100, full - 1])
+    P.same()
+    assert P.ref.status == 0
+    P.fork([1, 2], [9, 10], [full - 7, 500])
+    P.same()
+    P.release([3, 8, 1], [0, 5, 0], [width, width, 7])
+    P.fork([2, 9, 5], [3, 8, 11], [full - 5, full - 7, 0])
+    P.same()
+    assert P.ref.status == ref.PAGE_RANGE  # row 8 still holds its first pages
