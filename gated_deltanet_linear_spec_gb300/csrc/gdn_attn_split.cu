@@ -502,13 +502,16 @@ int query_slots(int64_t queries) { return queries <= 16 ? 16 : queries <= 32 ? 3
 }  // namespace
 
 // A call of long rows may hold one-token rows too (a GDN batch's decode rows come with its prompts).  As prompts they
-// take a CTA per row and kv-head, 128 or 256 queries wide: with 64 decode rows over 512 to 8192 tokens beside a
-// 1024-token prompt (32 q-heads, 4 kv-heads, d = 128) the call took 226 us, with the short rows split it takes 137
-// (16 such rows beside two prompts: 220 and 211).  The two more launches cost 9 us where no row is short (12 ragged
-// prompts: 115 and 125), so fewer than 16 rows, or rows that must all be of one length, go one way.
+// take a CTA per row and kv-head, 128 or 256 queries wide.  The host knows the rows' count, their tokens and the longest:
+// from 5 rows on that have less than half the longest's tokens on average, some are short and the call is split.  Decode
+// rows over 512 to 8192 tokens (32 q-heads, 4 kv-heads, d = 128), all as prompts and split: beside a 1024-token prompt 2
+// rows 76 and 55 us, 4 101 and 59, 16 140 and 73, 64 164 and 123; beside one of 4096 2 rows 158 and 178, 4 185 and 182,
+// 16 212 and 195; 300 new tokens at 2000 2 rows 48 and 59, 4 70 and 63, 16 125 and 78.  Where no row is short the two more
+// launches lose 9 to 11 us (3 ragged prompts: 48 and 57; 12 of 100 to 1200 tokens, which this rule does not split: 113 and
+// 125).
 int32_t attn_few(const AttnLaunch& a, gdn_dtype dtype) {
-  const bool ragged = (int64_t)a.rows.num_tokens < (int64_t)a.rows.num_seqs * a.rows.max_q;
-  if (!attn_prompt_supported(a, dtype) || attn_split_supported(a, dtype) || a.G > 64 || a.rows.num_seqs < 16 || !ragged)
+  const bool short_ones = 2 * (int64_t)a.rows.num_tokens < (int64_t)a.rows.num_seqs * a.rows.max_q;
+  if (!attn_prompt_supported(a, dtype) || attn_split_supported(a, dtype) || a.G > 64 || a.rows.num_seqs < 5 || !short_ones)
     return 0;
   return query_slots(a.G);
 }

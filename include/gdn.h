@@ -371,9 +371,9 @@ int gdn_kv_append(const gdn_kv_cache* cache, const gdn_kv_rows* rows, const void
  *   out_stride: elements from one token to the next (0 = dense), their bytes a multiple of 16.
  * The cache's refcount is not used and may be NULL.
  * max_query_len and the sizes pick the kernel on the host: rows of few new tokens share the cache's length out to
- * all SMs, long ones take the tensor cores 128 queries at a time.  A call of 16 rows or more that are not all of one
- * length goes both ways, a row by its own length; decode rows beside prompts in a smaller call go the prompts' way
- * and are faster in one of their own (another gdn_kv_rows over the same tokens).
+ * all SMs, long ones take the tensor cores 128 queries at a time.  A bf16 call of 5 rows or more whose num_tokens are
+ * less than half of num_seqs * max_query_len goes both ways, a row by its own length; decode rows beside prompts in
+ * other calls go the prompts' way and are faster in one of their own (another gdn_kv_rows over the same tokens).
  * workspace: at least gdn_attention_workspace_bytes(attn, cache, rows) bytes, 256-byte aligned
  * (may be NULL when that is 0); it holds the partial results of rows whose cache is split.
  */

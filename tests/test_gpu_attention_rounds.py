@@ -111,3 +111,13 @@ def test_many_verify_rows(dim, dtype, monkeypatch):
 @pytest.mark.parametrize("dim,dtype", [(96, BF16), (64, F32), (128, F32)])
 def test_long_rows_on_the_cuda_cores(dim, dtype, monkeypatch):
     check(Step([(700, 900), (1, 3000), (33, 33)], heads=8, kv_heads=2, dim=dim, page=32, dtype=dtype, seed=dim), monkeypatch)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("rows", [[(1, 300), (1, 1), (140, 200), (1, 64)], [(1, 300), (1, 1), (140, 200), (1, 64), (1, 513)],
+                                  [(1, 300), (1, 1), (140, 200), (140, 141), (65, 64 + 65)],
+                                  [(n, n + 7 * n % 90) for n in range(40, 160, 7)]], ids=["4", "5", "half", "long"])
+def test_short_rows_beside_long_ones(dim, rows, monkeypatch):
+    """Calls on both sides of the rule that sends short rows another way."""
+    check(Step(rows, heads=8, kv_heads=2, dim=dim, page=32, seed=dim, fused=True), monkeypatch)
+    check(Step(rows, heads=3, kv_heads=3, dim=dim, page=16, window=60, sinks=2, seed=dim + 1), monkeypatch)
