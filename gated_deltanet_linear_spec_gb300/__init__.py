@@ -156,11 +156,14 @@ def _dtype_code(dt: torch.dtype) -> int:
     raise TypeError(f"unsupported dtype {dt}")
 
 
-def _ptr(t: Optional[torch.Tensor], dtype: Optional[torch.dtype] = None, name: str = "") -> Optional[int]:
+def _ptr(t: Optional[torch.Tensor], dtype: Optional[torch.dtype] = None, name: str = "",
+         device: Optional[int] = None) -> Optional[int]:
     if t is None:
         return None
     if not t.is_cuda:
         raise TypeError(f"{name}: expected a CUDA tensor")
+    if device is not None and t.get_device() != device:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, other tensors of the call on cuda:{device}")
     if not t.is_contiguous():
         raise TypeError(f"{name}: expected a contiguous tensor")
     if dtype is not None and t.dtype != dtype:
@@ -238,10 +241,11 @@ class Rows:
                      _ptr(self.num_accepted_tokens, i32, "num_accepted_tokens"), cols)
 
 
-def _int32(t: Optional[torch.Tensor], name: str, count: Optional[int] = None) -> Optional[int]:
+def _int32(t: Optional[torch.Tensor], name: str, count: Optional[int] = None,
+           device: Optional[int] = None) -> Optional[int]:
     if t is not None and count is not None and t.numel() != count:
         raise ValueError(f"{name}: expected {count} entries, got {t.numel()}")
-    return _ptr(t, torch.int32, name)
+    return _ptr(t, torch.int32, name, device)
 
 
 def _fits32(value: int, name: str) -> int:
@@ -251,34 +255,40 @@ def _fits32(value: int, name: str) -> int:
     return int(value)
 
 
-def _token_rows(t: torch.Tensor, dtype: torch.dtype, heads: int, dim: int, name: str):
-    """Pointer and token stride of a [tokens, heads, dim] tensor; the token dimension may be strided."""
-    if not t.is_cuda:
+def _token_rows(t: torch.Tensor, dtype: torch.dtype, heads: int, dim: int, name: str, device: int):
+    """Pointer, token stride and tokens of a [tokens, heads, dim] tensor; the token dimension may be strided."""
+    at = t.get_device()
+    if at < 0:
         raise TypeError(f"{name}: expected a CUDA tensor")
+    if at != device:
+        raise ValueError(f"{name} is on cuda:{at}, other tensors of the call on cuda:{device}")
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
-        raise ValueError(f"{name}: expected [tokens, {heads}, {dim}], got {tuple(t.shape)}")
-    _fits32(t.shape[0], f"{name}'s tokens")
-    st = t.stride()
+    shape, st = t.shape, t.stride()
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
+        raise ValueError(f"{name}: expected [tokens, {heads}, {dim}], got {tuple(shape)}")
+    tokens = shape[0]
     if (dim > 1 and st[2] != 1) or (heads > 1 and st[1] != dim):
         raise TypeError(f"{name}: the heads of a token must be contiguous")
-    if t.shape[0] > 1 and st[0] < heads * dim:  # (0, an expanded tensor's stride, means dense in the C descriptors)
+    if tokens <= 1:
+        return t.data_ptr(), 0, tokens
+    if tokens >= 1 << 31:
+        raise ValueError(f"{name}: {tokens} tokens do not fit 32 bits")
+    if st[0] < heads * dim:  # (0, an expanded tensor's stride, means dense in the C descriptors)
         raise TypeError(f"{name}: tokens share memory (an expanded tensor needs a copy)")
-    return t.data_ptr(), (st[0] if t.shape[0] > 1 else 0)
+    return t.data_ptr(), st[0], tokens
 
 
-def _one_device(device: int, *tensors: Optional[torch.Tensor]) -> None:
-    for t in tensors:
-        if t is not None and t.get_device() != device:
-            raise ValueError(f"tensors on cuda:{device} and cuda:{t.get_device()} in one call")
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)  # 1 us less than the public call
 
 
-def _on_current(device: int, *tensors: Optional[torch.Tensor]) -> None:
+def _on_current(device: int, rows: Optional["KvRows"] = None) -> int:
     """The library launches on the current device: every tensor of a call has to be there."""
-    if torch.cuda.current_device() != device:
-        raise ValueError(f"the call's tensors are on cuda:{device}, the current device is cuda:{torch.cuda.current_device()}")
-    _one_device(device, *tensors)
+    if _current_device() != device:
+        raise ValueError(f"the call's tensors are on cuda:{device}, the current device is cuda:{_current_device()}")
+    if rows is not None and rows._device != device:
+        raise ValueError(f"the rows are on cuda:{rows._device}, other tensors of the call on cuda:{device}")
+    return device
 
 
 @dataclass(frozen=True)
@@ -310,13 +320,16 @@ class KvCache:
         pages, heads, size, dim = k.shape
         if max(pages, heads, size, dim, *self.block_table.shape) >= 1 << 31:
             raise ValueError("a dimension does not fit 32 bits")
+        device = k.get_device()
+        if v.get_device() != device:
+            raise ValueError(f"v_pool is on cuda:{v.get_device()}, k_pool on cuda:{device}")
         desc = _KvCache(k.data_ptr(), v.data_ptr(), k.stride(0) if pages > 1 else 0,
-                        _int32(self.block_table, "block_table"), _int32(self.refcount, "refcount", pages), pages,
+                        _int32(self.block_table, "block_table", None, device),
+                        _int32(self.refcount, "refcount", pages, device), pages,
                         self.block_table.shape[0], self.block_table.shape[1], size, heads, dim, _dtype_code(k.dtype))
-        _one_device(k.get_device(), v, self.block_table, self.refcount)
         object.__setattr__(self, "_desc", desc)
         object.__setattr__(self, "_ref", ctypes.byref(desc))
-        object.__setattr__(self, "_device", k.get_device())
+        object.__setattr__(self, "_device", device)
 
     @property
     def dtype(self) -> torch.dtype:
@@ -337,11 +350,12 @@ class KvRows:
 
     def __post_init__(self):
         n = self.query_start_loc.numel() - 1
+        device = self.query_start_loc.get_device()
         desc = _KvRows(n, _fits32(self.num_tokens, "num_tokens"), _int32(self.query_start_loc, "query_start_loc"),
-                       _int32(self.token_indx, "token_indx", int(self.num_tokens)),
-                       _int32(self.table_rows, "table_rows", n), _int32(self.kv_lens, "kv_lens", n),
+                       _int32(self.token_indx, "token_indx", int(self.num_tokens), device),
+                       _int32(self.table_rows, "table_rows", n, device), _int32(self.kv_lens, "kv_lens", n, device),
                        _fits32(self.max_query_len, "max_query_len"))
-        _one_device(self.query_start_loc.get_device(), self.token_indx, self.table_rows, self.kv_lens)
+        object.__setattr__(self, "_device", device)
         object.__setattr__(self, "_desc", desc)
         object.__setattr__(self, "_ref", ctypes.byref(desc))
 
@@ -505,13 +519,13 @@ def gdn_kv_append(cache: KvCache, rows: KvRows, k: torch.Tensor, v: torch.Tensor
                   status: Optional[torch.Tensor] = None, stream=None) -> None:
     """Writes the new tokens' k, v [num_global_tokens, num_kv_heads, head_dim] into the rows' pages."""
     _, heads, _, dim = cache.k_pool.shape
-    kp, ks = _token_rows(k, cache.dtype, heads, dim, "k")
-    vp, vs = _token_rows(v, cache.dtype, heads, dim, "v")
-    if k.shape[0] != v.shape[0]:
+    kp, ks, tokens = _token_rows(k, cache.dtype, heads, dim, "k", cache._device)
+    vp, vs, of_v = _token_rows(v, cache.dtype, heads, dim, "v", cache._device)
+    if tokens != of_v:
         raise ValueError("k and v: expected one token count")
-    _on_current(cache._device, rows.query_start_loc, k, v, status)
-    _check(library().gdn_kv_append(cache._ref, rows._ref, kp, ks, vp, vs, k.shape[0],
-                                   _ptr(status, torch.int32, "status"), _stream_of(cache.k_pool, stream)))
+    device = _on_current(cache._device, rows)
+    _check(library().gdn_kv_append(cache._ref, rows._ref, kp, ks, vp, vs, tokens,
+                                   _ptr(status, torch.int32, "status", device), _stream_of(cache.k_pool, stream)))
 
 
 def gdn_attention_workspace_bytes(attn: Attention, cache: KvCache, rows: KvRows) -> int:
@@ -524,16 +538,16 @@ def gdn_paged_attention(attn: Attention, cache: KvCache, rows: KvRows, q: torch.
     """Causal attention of the rows' new tokens over their pages (which already hold them);
     q, out [num_global_tokens, num_q_heads, head_dim]."""
     dim = cache.k_pool.shape[3]
-    qp, qs = _token_rows(q, cache.dtype, attn.num_q_heads, dim, "q")
-    op, os_ = _token_rows(out, cache.dtype, attn.num_q_heads, dim, "out")
-    if q.shape[0] != out.shape[0]:
+    qp, qs, tokens = _token_rows(q, cache.dtype, attn.num_q_heads, dim, "q", cache._device)
+    op, os_, of_out = _token_rows(out, cache.dtype, attn.num_q_heads, dim, "out", cache._device)
+    if tokens != of_out:
         raise ValueError("q and out: expected one token count")
-    _on_current(cache._device, rows.query_start_loc, q, out, workspace, status)
+    device = _on_current(cache._device, rows)
     if workspace is None:
         workspace = _scratch(gdn_attention_workspace_bytes(attn, cache, rows), q.device, stream)
-    _check(library().gdn_paged_attention(attn._ref, cache._ref, rows._ref, qp, qs, q.shape[0], op, os_,
-                                         _ptr(workspace, torch.uint8, "workspace"), workspace.numel(),
-                                         _ptr(status, torch.int32, "status"), _stream_of(cache.k_pool, stream)))
+    _check(library().gdn_paged_attention(attn._ref, cache._ref, rows._ref, qp, qs, tokens, op, os_,
+                                         _ptr(workspace, torch.uint8, "workspace", device), workspace.numel(),
+                                         _ptr(status, torch.int32, "status", device), _stream_of(cache.k_pool, stream)))
 
 
 def gdn_kv_workspace_bytes(cache: KvCache, count: int) -> int:
@@ -550,11 +564,12 @@ def gdn_kv_reserve(cache: KvCache, table_rows: Optional[torch.Tensor], from_lens
                    stream=None) -> None:
     """Gives each listed table row free pages for its tokens [from_lens, to_lens)."""
     n = from_lens.numel()
-    _on_current(cache._device, table_rows, from_lens, to_lens, workspace, status)
+    device = _on_current(cache._device)
     ws = _kv_workspace(cache, n, workspace, stream)
-    _check(library().gdn_kv_reserve(cache._ref, n, _int32(table_rows, "table_rows", n), _int32(from_lens, "from_lens"),
-                                    _int32(to_lens, "to_lens", n), _ptr(ws, torch.uint8, "workspace"), ws.numel(),
-                                    _ptr(status, torch.int32, "status"), _stream_of(cache.k_pool, stream)))
+    _check(library().gdn_kv_reserve(cache._ref, n, _int32(table_rows, "table_rows", n, device),
+                                    _int32(from_lens, "from_lens", None, device), _int32(to_lens, "to_lens", n, device),
+                                    _ptr(ws, torch.uint8, "workspace", device), ws.numel(),
+                                    _ptr(status, torch.int32, "status", device), _stream_of(cache.k_pool, stream)))
 
 
 def gdn_kv_release(cache: KvCache, table_rows: torch.Tensor, first_page: Optional[torch.Tensor] = None,
@@ -562,40 +577,42 @@ def gdn_kv_release(cache: KvCache, table_rows: torch.Tensor, first_page: Optiona
                    stream=None) -> None:
     """Gives back the pages of entries [first_page, last_page) of each listed table row."""
     n = table_rows.numel()
-    _on_current(cache._device, table_rows, first_page, last_page, status)
-    _check(library().gdn_kv_release(cache._ref, n, _int32(table_rows, "table_rows"),
-                                    _int32(first_page, "first_page", n), _int32(last_page, "last_page", n),
-                                    _ptr(status, torch.int32, "status"), _stream_of(cache.k_pool, stream)))
+    device = _on_current(cache._device)
+    _check(library().gdn_kv_release(cache._ref, n, _int32(table_rows, "table_rows", None, device),
+                                    _int32(first_page, "first_page", n, device), _int32(last_page, "last_page", n, device),
+                                    _ptr(status, torch.int32, "status", device), _stream_of(cache.k_pool, stream)))
 
 
 def gdn_kv_fork(cache: KvCache, src_rows: torch.Tensor, dst_rows: torch.Tensor, lens: torch.Tensor,
                 workspace: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None, stream=None) -> None:
     """Table row dst_rows[i] becomes a holder of the first lens[i] tokens of src_rows[i]."""
     n = src_rows.numel()
-    _on_current(cache._device, src_rows, dst_rows, lens, workspace, status)
+    device = _on_current(cache._device)
     ws = _kv_workspace(cache, n, workspace, stream)
-    _check(library().gdn_kv_fork(cache._ref, n, _int32(src_rows, "src_rows"), _int32(dst_rows, "dst_rows", n),
-                                 _int32(lens, "lens", n), _ptr(ws, torch.uint8, "workspace"), ws.numel(),
-                                 _ptr(status, torch.int32, "status"), _stream_of(cache.k_pool, stream)))
+    _check(library().gdn_kv_fork(cache._ref, n, _int32(src_rows, "src_rows", None, device),
+                                 _int32(dst_rows, "dst_rows", n, device), _int32(lens, "lens", n, device),
+                                 _ptr(ws, torch.uint8, "workspace", device), ws.numel(),
+                                 _ptr(status, torch.int32, "status", device), _stream_of(cache.k_pool, stream)))
 
 
 def gdn_kv_copy_pages(cache: KvCache, src_pages: torch.Tensor, dst_pages: torch.Tensor,
                       status: Optional[torch.Tensor] = None, stream=None) -> None:
     """Copies page src_pages[i] onto dst_pages[i] in both pools."""
     n = src_pages.numel()
-    _on_current(cache._device, src_pages, dst_pages, status)
-    _check(library().gdn_kv_copy_pages(cache._ref, n, _int32(src_pages, "src_pages"),
-                                       _int32(dst_pages, "dst_pages", n), _ptr(status, torch.int32, "status"),
-                                       _stream_of(cache.k_pool, stream)))
+    device = _on_current(cache._device)
+    _check(library().gdn_kv_copy_pages(cache._ref, n, _int32(src_pages, "src_pages", None, device),
+                                       _int32(dst_pages, "dst_pages", n, device),
+                                       _ptr(status, torch.int32, "status", device), _stream_of(cache.k_pool, stream)))
 
 
 def gdn_kv_compact(cache: KvCache, num_live: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
                    status: Optional[torch.Tensor] = None, stream=None) -> None:
     """Moves the live pages to ids 1..M; ``num_live`` (int32, one entry) receives M."""
-    _on_current(cache._device, num_live, workspace, status)
+    device = _on_current(cache._device)
     ws = _kv_workspace(cache, 0, workspace, stream)
-    _check(library().gdn_kv_compact(cache._ref, _int32(num_live, "num_live", 1), _ptr(ws, torch.uint8, "workspace"),
-                                    ws.numel(), _ptr(status, torch.int32, "status"), _stream_of(cache.k_pool, stream)))
+    _check(library().gdn_kv_compact(cache._ref, _int32(num_live, "num_live", 1, device),
+                                    _ptr(ws, torch.uint8, "workspace", device), ws.numel(),
+                                    _ptr(status, torch.int32, "status", device), _stream_of(cache.k_pool, stream)))
 
 
 def gdn_copy_slots(layer: Layer, pools: Pools, src_slots: torch.Tensor, dst_slots: torch.Tensor,
@@ -603,10 +620,11 @@ def gdn_copy_slots(layer: Layer, pools: Pools, src_slots: torch.Tensor, dst_slot
     """Copies GDN state: slot src_slots[i] of both pools onto dst_slots[i] (a NULL source reads as zeros)."""
     n = src_slots.numel()
     act = layer.act_dtype
-    _on_current(pools.ssm_pool.get_device(), pools.conv_pool, src_slots, dst_slots, status)
+    device = _on_current(pools.ssm_pool.get_device())
+    _ptr(pools.conv_pool, act, "conv_pool", device)
     _check(library().gdn_copy_slots(ctypes.byref(layer.c()), ctypes.byref(pools.c(act)), n,
-                                    _int32(src_slots, "src_slots"), _int32(dst_slots, "dst_slots", n),
-                                    _ptr(status, torch.int32, "status"), _stream_of(pools.ssm_pool, stream)))
+                                    _int32(src_slots, "src_slots", None, device), _int32(dst_slots, "dst_slots", n, device),
+                                    _ptr(status, torch.int32, "status", device), _stream_of(pools.ssm_pool, stream)))
 
 
 def gdn_testing_set_prefill_faults(wait_ns: int = 0, drop_copy_chunk: int = -1) -> None:

@@ -55,7 +55,7 @@ def test_expanded_tokens_are_refused():
 def test_overlapping_tokens_are_refused():
     long = dev(4 * 2 * 64 + 64)
     with pytest.raises(TypeError, match="share memory"):
-        gdn._token_rows(long.as_strided((4, 2, 64), (64, 64, 1)), torch.bfloat16, 2, 64, "k")
+        gdn._token_rows(long.as_strided((4, 2, 64), (64, 64, 1)), torch.bfloat16, 2, 64, "k", 0)
 
 
 def test_expanded_pools_are_refused():
@@ -66,9 +66,9 @@ def test_expanded_pools_are_refused():
 
 
 def test_one_token_and_strided_tokens_are_taken():
-    assert gdn._token_rows(dev(1, 2, 64).expand(1, 2, 64), torch.bfloat16, 2, 64, "k")[1] == 0
-    assert gdn._token_rows(dev(4, 6, 64)[:, 2:4], torch.bfloat16, 2, 64, "k")[1] == 6 * 64
-    assert gdn._token_rows(dev(0, 2, 64), torch.bfloat16, 2, 64, "k")[1] == 0
+    assert gdn._token_rows(dev(1, 2, 64).expand(1, 2, 64), torch.bfloat16, 2, 64, "k", 0)[1] == 0
+    assert gdn._token_rows(dev(4, 6, 64)[:, 2:4], torch.bfloat16, 2, 64, "k", 0)[1] == 6 * 64
+    assert gdn._token_rows(dev(0, 2, 64), torch.bfloat16, 2, 64, "k", 0)[1] == 0
     both = dev(8, 2, 2, 16, 64)
     assert cache(k_pool=both[:, 0], v_pool=both[:, 1])._desc.page_stride == 2 * 2 * 16 * 64
 
@@ -150,10 +150,10 @@ def other(t):
 
 def test_descriptors_over_two_devices_are_refused():
     for name, t in (("v_pool", dev(8, 2, 16, 64)), ("block_table", i32([[1]])), ("refcount", i32([0] * 8))):
-        with pytest.raises(ValueError, match="cuda:0 and cuda:1"):
+        with pytest.raises(ValueError, match="cuda:1"):
             cache(**{name: other(t)})
     for name, t in (("kv_lens", i32([5, 9])), ("table_rows", i32([0, 1])), ("token_indx", i32([0, 1, 2, 3]))):
-        with pytest.raises(ValueError, match="cuda:0 and cuda:1"):
+        with pytest.raises(ValueError, match="cuda:1"):
             rows(**{name: other(t)})
 
 
@@ -182,7 +182,7 @@ def no_launch(monkeypatch):
 
     monkeypatch.setattr(gdn, "library", lambda: Library())
     monkeypatch.setattr(gdn, "_stream_of", lambda t, stream: None)
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(gdn, "_current_device", lambda: 0)
     return ran
 
 
@@ -195,18 +195,21 @@ def test_calls_go_through_on_the_current_device(no_launch):
 def test_calls_over_two_devices_are_refused(no_launch):
     c, r = cache(), rows()
     for call in calls(c, r, other)[:-1]:  # (the last one's tensors are all on the other device)
-        with pytest.raises(ValueError, match="cuda:0 and cuda:1"):
+        with pytest.raises(ValueError, match="cuda:1"):
             call()
     for call in calls(c, r):
-        with pytest.raises(ValueError, match="cuda:0 and cuda:1"):
+        with pytest.raises(ValueError, match="cuda:1"):
             call(status=other(i32([0])))
-    with pytest.raises(ValueError, match="cuda:0 and cuda:1"):
+    layer, ssm = gdn.Layer(2, 4, 16, 32, 4, 5), dev(4, 4, 32, 16, dtype=torch.float32)
+    with pytest.raises(ValueError, match="cuda:1"):
+        gdn.gdn_copy_slots(layer, gdn.Pools(other(dev(4, 5, layer.channels)), ssm), i32([1]), i32([2]))
+    with pytest.raises(ValueError, match="cuda:1"):
         calls(c, rows(**{k: other(v) for k, v in dict(query_start_loc=i32([0, 2, 4]), kv_lens=i32([5, 9])).items()}))[0]()
     assert not no_launch
 
 
 def test_calls_off_the_current_device_are_refused(no_launch, monkeypatch):
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    monkeypatch.setattr(gdn, "_current_device", lambda: 1)
     for call in calls(cache(), rows()):
         with pytest.raises(ValueError, match="current device"):
             call()
@@ -225,7 +228,7 @@ def test_values_past_32_bits_are_refused(value):
         with pytest.raises(ValueError, match=field):
             rows(**{field: value})
     with pytest.raises(ValueError, match="32 bits"):
-        gdn._token_rows(dev(1, 2, 64).expand(1 << 32, 2, 64), torch.bfloat16, 2, 64, "k")
+        gdn._token_rows(dev(1, 2, 64).expand(1 << 32, 2, 64), torch.bfloat16, 2, 64, "k", 0)
     assert gdn.Attention(8, window=(1 << 31) - 1)._desc.window == (1 << 31) - 1
 
 
