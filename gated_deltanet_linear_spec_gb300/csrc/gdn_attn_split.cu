@@ -171,7 +171,9 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, NW>::kThreads, 1)
   Small<C>& small = *reinterpret_cast<Small<C>*>(smem + NW * (C::kRing + C::kQ));
   const AttnLaunch& p = P.a;
   const KvDev& kv = p.cache;
-  // The warp's number comes from a shuffle, so that the compiler takes it as one value of the warp.
+  // The warp's number comes from a shuffle, so that the compiler takes it as one value of the warp.  (In an early form
+  // that took it as threadIdx.x / 32, nvcc 13.0 got the range of an index into shared memory wrong under nested
+  // conditions, and the index left its array.)
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

@@ -7,12 +7,12 @@
 // scores meet by exchanges that halve what a lane keeps, so a lane ends up with one query's scores of every fourth
 // token, and the softmax takes two exchanges.  (Scores by lane = token, queries broadcast from shared memory, are
 // bound by those broadcasts, four cycles each: 64 rows of 3 tokens, 64 to 4096 cached, 8 q-heads, 2 kv-heads, 32 bits,
-// d = 256: 187 us instead of 138.)  Keys and values are fetched a chunk ahead; one token at a time, 24 such rows
-// with d = 64 took 67 us instead of 25.  Loops of two chunks a turn, as unrolled ones fall out of the instruction
-// cache (d = 96: 1467 us instead of 739 for 1024 new tokens at 2048, 16 q-heads, 4 kv-heads).
+// d = 256: 187 us instead of 126.)  Keys and values are fetched a chunk ahead; one token at a time, 24 such rows
+// with d = 64 took 67 us instead of 26.  Loops of two chunks a turn, as unrolled ones fall out of the instruction
+// cache (d = 96: 1467 us instead of 714 for 1024 new tokens at 2048, 16 q-heads, 4 kv-heads).
 // Per token of a step, a unit of 8 queries takes about 16 E FMAs and 8 exchanges: that bounds long caches, the
-// steps' latency short ones.  1024 new tokens at 4096 (d = 64) take 443 us, with a warp per query, which shares
-// nothing, 4190; 64 decode rows over 512 to 8192 tokens (bf16, d = 96, 32 q-heads, 4 kv-heads) 219 us against 5731.
+// steps' latency short ones.  1024 new tokens at 4096 (d = 64) take 432 us, with a warp per query, which shares
+// nothing, 4190; 64 decode rows over 512 to 8192 tokens (bf16, d = 96, 32 q-heads, 4 kv-heads) 198 us against 5731.
 // Up to d = 128 a step's outputs are summed on their own and added once, which keeps long sums exact to a few steps.
 #include <algorithm>
 

@@ -365,8 +365,11 @@ int gdn_kv_append(const gdn_kv_cache* cache, const gdn_kv_rows* rows, const void
  * query of q-head h at position p of row n sees the row's key j when j <= p, and (window <= 0 or
  * j > p - window or j < num_sinks), and the page of j is not NULL:
  *   out = sum_j e^(s_j - m) v_j / sum_j e^(s_j - m),  s_j = scale q.k_j,  m = max_j s_j,
- * in fp32, rounded once to dtype; a query that sees no key gives 0.  What a query does not see
- * never reaches its result, whatever it holds (infinities and NaN included).
+ * scores, maximum and sums in fp32, rounded once to dtype; a query that sees no key gives 0.  The weights
+ * e^(s_j - m) <= 1 go into the second sum in fp32 (GDN_F32, and head dimensions other than 64, 128 and 256), as a
+ * pair of bf16 that keeps 16 bits (bf16 rows of up to 64 queries per kv-head), or as one bf16, 2^-8 relative at most
+ * (longer bf16 rows: the tensor core's operand): the same token may differ by that between a prompt and a verify row.
+ * What a query does not see never reaches its result, whatever it holds (infinities and NaN included).
  *   q, out [num_global_tokens, Hq, d] dtype, read and written at token_indx; q_stride,
  *   out_stride: elements from one token to the next (0 = dense), their bytes a multiple of 16.
  * The cache's refcount is not used and may be NULL.
