@@ -42,7 +42,6 @@ namespace gdn {
 
 namespace {
 
-constexpr int kSms = 152;
 constexpr int kTN = 64;         // cached tokens of a step
 constexpr int kMaxPieces = 16;
 constexpr float kGrow = 16.f;   // log2 of how far scores may outgrow the maximum that weights refer to

@@ -15,7 +15,6 @@
 namespace gdn {
 namespace split {
 
-constexpr int kSms = 152;
 constexpr int kTN = 32;       // tokens of a tile
 // Beginning a unit takes about as long as 2 to 3 tiles: without them in the deal, of 64 decode rows' workers those
 // with pieces of one unit took 107 thousand cycles, of three 121 and of four 133.

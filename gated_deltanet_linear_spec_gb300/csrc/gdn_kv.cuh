@@ -5,6 +5,8 @@
 
 namespace gdn {
 
+constexpr int kSms = 152;
+
 // The cache as the kernels see it (plain values copied from gdn_kv_cache).
 struct KvDev {
   void* k;

@@ -726,7 +726,7 @@ cudaError_t launch_hand_out(void (*kernel)(PageRowsLaunch), cudaStream_t s, cons
   return launch_of(kernel, dim3(kHandCtas), kHandThreads, s, p);
 }
 
-constexpr int kCopyBlocks = 152 * 8;  // two thousand threads per SM
+constexpr int kCopyBlocks = kSms * 8;  // two thousand threads per SM
 
 }  // namespace
 
