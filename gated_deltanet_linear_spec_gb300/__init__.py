@@ -4,7 +4,8 @@ The functions here mirror the C entry points in ``include/gdn.h`` one for one
 (``gdn_conv_update``, ``gdn_recurrent_step``, ``gdn_chunk_prefill``, ``gdn_mixed_batch``,
 ``gdn_workspace_bytes``, and the paged key-value cache's ``gdn_paged_attention``, ``gdn_kv_append``,
 ``gdn_kv_reserve``, ``gdn_kv_release``, ``gdn_kv_fork``, ``gdn_kv_copy_pages``, ``gdn_kv_compact``,
-``gdn_copy_slots``) and only marshal arguments: torch CUDA tensors become device
+``gdn_copy_slots``, ``gdn_shared_attention``, ``gdn_kv_common_prefix``, and rotary positions' ``gdn_rope``,
+``gdn_kv_append_rope``) and only marshal arguments: torch CUDA tensors become device
 pointers, the current torch stream becomes the ``cudaStream_t``, and a negative return code
 becomes a ``GdnError``.  Every step of the path runs in the library's CUDA kernels; there is
 no fallback, and a missing library raises at the first call.
@@ -25,6 +26,8 @@ LIB_PATH = os.path.join(_HERE, "libgdn.so")
 GDN_F32, GDN_BF16 = 0, 1
 GDN_QKV_PACKED, GDN_QKV_PER_KHEAD = 0, 1
 GDN_CONV_ROLLED, GDN_CONV_PER_SLOT = 0, 1
+GDN_ROPE_HALF, GDN_ROPE_INTERLEAVED = 0, 1
+GDN_ROPE_PLAIN, GDN_ROPE_LINEAR, GDN_ROPE_NTK, GDN_ROPE_BANDS, GDN_ROPE_RAMP = 0, 1, 2, 3, 4
 STATUS_SLOT_RANGE, STATUS_NUM_ACCEPTED, STATUS_TOKEN_RANGE, STATUS_ROW_RANGE = 0x1, 0x2, 0x4, 0x8
 STATUS_WAIT_TIMEOUT = 0x10
 STATUS_PAGE_RANGE, STATUS_PAGE_SHARED, STATUS_NO_PAGES = 0x20, 0x40, 0x80
@@ -82,10 +85,27 @@ class _AttnDesc(ctypes.Structure):
                 ("num_sinks", ctypes.c_int32)]
 
 
+class _KvGroups(ctypes.Structure):
+    _fields_ = [("num_groups", ctypes.c_int32), ("group_start_loc", ctypes.c_void_p), ("prefix_lens", ctypes.c_void_p)]
+
+
+class _RopeDesc(ctypes.Structure):
+    _fields_ = [("turns", ctypes.c_void_p), ("rotary_dim", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("magnitude", ctypes.c_float)]
+
+
+class _RopeFreq(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("scaling", ctypes.c_int32), ("base", ctypes.c_double),
+                ("factor", ctypes.c_double), ("original_len", ctypes.c_double), ("low", ctypes.c_double),
+                ("high", ctypes.c_double)]
+
+
 EXPORTS = ("gdn_workspace_bytes", "gdn_prefill_workspace_bytes", "gdn_conv_update", "gdn_recurrent_step", "gdn_chunk_prefill",
            "gdn_mixed_batch", "gdn_mixed_batch_static_workspace", "gdn_status_string", "gdn_kv_append", "gdn_paged_attention",
            "gdn_attention_workspace_bytes", "gdn_kv_reserve", "gdn_kv_release", "gdn_kv_fork", "gdn_kv_copy_pages",
-           "gdn_kv_compact", "gdn_kv_workspace_bytes", "gdn_copy_slots")
+           "gdn_kv_compact", "gdn_kv_workspace_bytes", "gdn_copy_slots", "gdn_shared_attention",
+           "gdn_shared_attention_workspace_bytes", "gdn_kv_common_prefix", "gdn_rope", "gdn_rope_turns", "gdn_rope_turns_of",
+           "gdn_kv_append_rope")
 # include/gdn_testing.h: hooks that let tests drive the kernels' failure paths
 TESTING_EXPORTS = ("gdn_testing_set_prefill_faults",)
 STATIC_WORKSPACE_BYTES = 16 << 20
@@ -136,7 +156,16 @@ def library() -> ctypes.CDLL:
                     ("gdn_kv_copy_pages", ctypes.c_int, [P(_KvCache), I32, VP, VP, VP, VP]),
                     ("gdn_kv_compact", ctypes.c_int, [P(_KvCache), VP, VP, SZ, VP, VP]),
                     ("gdn_kv_workspace_bytes", SZ, [P(_KvCache), I32]),
-                    ("gdn_copy_slots", ctypes.c_int, [P(_LayerDesc), P(_Pools), I32, VP, VP, VP, VP])):
+                    ("gdn_copy_slots", ctypes.c_int, [P(_LayerDesc), P(_Pools), I32, VP, VP, VP, VP]),
+                    ("gdn_shared_attention", ctypes.c_int, [P(_AttnDesc), P(_KvCache), P(_KvRows), P(_KvGroups), VP, I64, I32,
+                                                            VP, I64, VP, SZ, VP, VP]),
+                    ("gdn_shared_attention_workspace_bytes", SZ, [P(_AttnDesc), P(_KvCache), P(_KvRows), P(_KvGroups)]),
+                    ("gdn_kv_common_prefix", ctypes.c_int, [P(_KvCache), P(_KvRows), P(_KvGroups), VP, VP]),
+                    ("gdn_rope", ctypes.c_int, [P(_RopeDesc), I32, I32, I32, VP, I32, VP, I64, VP, I64, VP]),
+                    ("gdn_rope_turns", ctypes.c_int, [P(_RopeFreq), P(ctypes.c_uint64), P(ctypes.c_float)]),
+                    ("gdn_rope_turns_of", ctypes.c_int, [P(ctypes.c_double), I32, P(ctypes.c_uint64)]),
+                    ("gdn_kv_append_rope", ctypes.c_int, [P(_KvCache), P(_KvRows), P(_RopeDesc), VP, I64, VP, I64, I32, VP,
+                                                          I64, VP, I64, I32, VP, VP])):
                 fn = getattr(lib, name)
                 fn.restype, fn.argtypes = res, args
             lib.gdn_testing_set_prefill_faults.restype = ctypes.c_int
@@ -385,6 +414,69 @@ class Attention:
         object.__setattr__(self, "_ref", ctypes.byref(desc))
 
 
+@dataclass(frozen=True)
+class KvGroups:
+    """Groups of rows that share the beginning of their caches (``gdn_kv_groups``, int32 CUDA tensors): group g is
+    rows [group_start_loc[g], group_start_loc[g + 1]) of a call, which hold the same pages for their first prefix_lens[g]
+    tokens."""
+    group_start_loc: torch.Tensor
+    prefix_lens: torch.Tensor
+
+    def __post_init__(self):
+        n = self.prefix_lens.numel()
+        device = self.prefix_lens.get_device()
+        desc = _KvGroups(n, _int32(self.group_start_loc, "group_start_loc", n + 1, device),
+                         _int32(self.prefix_lens, "prefix_lens"))
+        object.__setattr__(self, "_device", device)
+        object.__setattr__(self, "_desc", desc)
+        object.__setattr__(self, "_ref", ctypes.byref(desc))
+
+    @property
+    def num_groups(self) -> int:
+        return self.prefix_lens.numel()
+
+
+@dataclass(frozen=True)
+class Rope:
+    """Rotary positions (``gdn_rope_desc``): the first ``rotary_dim`` values of a head turn, pairs as ``layout`` says
+    (GDN_ROPE_HALF or GDN_ROPE_INTERLEAVED).  The frequencies base^(-2i/rotary_dim) are scaled as ``scaling`` says
+    (GDN_ROPE_PLAIN, _LINEAR, _NTK, _BANDS, _RAMP: include/gdn.h), or given in radians a position as ``frequencies``.
+    ``magnitude`` 0 selects that of the scaling.  The table of frequencies is made once, here, on ``device`` (the current CUDA
+    device)."""
+    rotary_dim: int
+    base: float = 10000.0
+    layout: int = GDN_ROPE_HALF
+    scaling: int = GDN_ROPE_PLAIN
+    factor: float = 1.0
+    original_len: float = 0.0
+    low: float = 0.0
+    high: float = 0.0
+    magnitude: float = 0.0
+    frequencies: Optional[tuple] = None
+    device: Optional[torch.device] = None
+
+    def __post_init__(self):
+        r = _fits32(self.rotary_dim, "rotary_dim")
+        if r < 2 or r > 256 or r % 2:
+            raise ValueError(f"rotary_dim: {r} is not an even number of 2 to 256")
+        turns, size = (ctypes.c_uint64 * (r // 2))(), ctypes.c_float(1.0)
+        if self.frequencies is not None:
+            f = torch.as_tensor(self.frequencies, dtype=torch.float64).flatten().tolist()
+            if len(f) != r // 2:
+                raise ValueError(f"frequencies: expected {r // 2}, got {len(f)}")
+            _check(library().gdn_rope_turns_of((ctypes.c_double * len(f))(*f), len(f), turns))
+        else:
+            freq = _RopeFreq(r, _fits32(self.scaling, "scaling"), self.base, self.factor, self.original_len, self.low, self.high)
+            _check(library().gdn_rope_turns(ctypes.byref(freq), turns, ctypes.byref(size)))
+        table = torch.tensor([t - (1 << 64) if t >> 63 else t for t in turns], dtype=torch.int64)
+        table = table.to("cuda" if self.device is None else self.device)
+        desc = _RopeDesc(table.data_ptr(), r, _fits32(self.layout, "layout"), float(self.magnitude) or size.value)
+        object.__setattr__(self, "turns", table)
+        object.__setattr__(self, "_device", table.get_device())
+        object.__setattr__(self, "_desc", desc)
+        object.__setattr__(self, "_ref", ctypes.byref(desc))
+
+
 def _rows_ref(r: Optional[Rows]):
     return None if r is None else ctypes.byref(r.c())
 
@@ -550,6 +642,88 @@ def gdn_paged_attention(attn: Attention, cache: KvCache, rows: KvRows, q: torch.
                                          _ptr(status, torch.int32, "status", device), _stream_of(cache.k_pool, stream)))
 
 
+def gdn_shared_attention_workspace_bytes(attn: Attention, cache: KvCache, rows: KvRows, groups: KvGroups) -> int:
+    return int(library().gdn_shared_attention_workspace_bytes(attn._ref, cache._ref, rows._ref, groups._ref))
+
+
+def _of_device(part, device: int, name: str) -> None:
+    if part._device != device:
+        where = "the CPU" if part._device < 0 else f"cuda:{part._device}"
+        raise ValueError(f"the {name} is on {where}, other tensors of the call on cuda:{device}")
+
+
+def gdn_shared_attention(attn: Attention, cache: KvCache, rows: KvRows, groups: KvGroups, q: torch.Tensor,
+                         out: torch.Tensor, workspace: Optional[torch.Tensor] = None,
+                         status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """gdn_paged_attention with the pages that the rows of a group share read once for all of them."""
+    dim = cache.k_pool.shape[3]
+    qp, qs, tokens = _token_rows(q, cache.dtype, attn.num_q_heads, dim, "q", cache._device)
+    op, os_, of_out = _token_rows(out, cache.dtype, attn.num_q_heads, dim, "out", cache._device)
+    if tokens != of_out:
+        raise ValueError("q and out: expected one token count")
+    device = _on_current(cache._device, rows)
+    _of_device(groups, device, "groups' table")
+    if workspace is None:
+        workspace = _scratch(gdn_shared_attention_workspace_bytes(attn, cache, rows, groups), q.device, stream)
+    _check(library().gdn_shared_attention(attn._ref, cache._ref, rows._ref, groups._ref, qp, qs, tokens, op, os_,
+                                          _ptr(workspace, torch.uint8, "workspace", device), workspace.numel(),
+                                          _ptr(status, torch.int32, "status", device), _stream_of(cache.k_pool, stream)))
+
+
+def gdn_kv_common_prefix(cache: KvCache, rows: KvRows, groups: KvGroups, status: Optional[torch.Tensor] = None,
+                         stream=None) -> None:
+    """Writes to groups.prefix_lens how many leading tokens the rows of each group hold in the same pages."""
+    device = _on_current(cache._device, rows)
+    _of_device(groups, device, "groups' table")
+    _check(library().gdn_kv_common_prefix(cache._ref, rows._ref, groups._ref, _ptr(status, torch.int32, "status", device),
+                                          _stream_of(cache.k_pool, stream)))
+
+
+def gdn_rope(rope: Rope, positions: torch.Tensor, x: torch.Tensor, out: torch.Tensor, stream=None) -> None:
+    """Turns the heads of x [tokens, heads, head_dim] by ``positions`` (int32, one per token, or of the first tokens) into
+    ``out``, which may be x.  At negated positions it is the gradient with respect to x."""
+    if x.dim() != 3:
+        raise ValueError(f"x: expected [tokens, heads, head_dim], got {tuple(x.shape)}")
+    device = x.get_device()
+    heads, dim = x.shape[1:]
+    xp, xs, tokens = _token_rows(x, x.dtype, heads, dim, "x", device)
+    op, os_, of_out = _token_rows(out, x.dtype, heads, dim, "out", device)
+    n = positions.numel()
+    if tokens != of_out or n > tokens:
+        raise ValueError("positions, x and out: expected one token count, or fewer positions")
+    _on_current(device)
+    _of_device(rope, device, "frequencies' table")
+    _check(library().gdn_rope(rope._ref, heads, dim, _dtype_code(x.dtype), _int32(positions, "positions", None, device), n,
+                              xp, xs, op, os_, _stream_of(x, stream)))
+
+
+def gdn_kv_append_rope(cache: KvCache, rows: KvRows, rope: Rope, k: torch.Tensor, v: torch.Tensor,
+                       q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+                       status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """gdn_kv_append with the new tokens' keys turned by their positions on the way, and the queries q
+    [num_global_tokens, num_q_heads, head_dim] of the same tokens turned into ``q_out`` (None: in place)."""
+    _, heads, _, dim = cache.k_pool.shape
+    kp, ks, tokens = _token_rows(k, cache.dtype, heads, dim, "k", cache._device)
+    vp, vs, of_v = _token_rows(v, cache.dtype, heads, dim, "v", cache._device)
+    if tokens != of_v:
+        raise ValueError("k and v: expected one token count")
+    hq, qp, qs, op, os_ = 0, None, 0, None, 0
+    if q is not None:
+        if q.dim() != 3:
+            raise ValueError(f"q: expected [tokens, heads, head_dim], got {tuple(q.shape)}")
+        hq = q.shape[1]
+        qp, qs, of_q = _token_rows(q, cache.dtype, hq, dim, "q", cache._device)
+        op, os_, of_out = _token_rows(q if q_out is None else q_out, cache.dtype, hq, dim, "q_out", cache._device)
+        if tokens != of_q or tokens != of_out:
+            raise ValueError("k, v, q and q_out: expected one token count")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    device = _on_current(cache._device, rows)
+    _of_device(rope, device, "frequencies' table")
+    _check(library().gdn_kv_append_rope(cache._ref, rows._ref, rope._ref, kp, ks, vp, vs, hq, qp, qs, op, os_, tokens,
+                                        _ptr(status, torch.int32, "status", device), _stream_of(cache.k_pool, stream)))
+
+
 def gdn_kv_workspace_bytes(cache: KvCache, count: int) -> int:
     """Workspace of gdn_kv_reserve and gdn_kv_fork over ``count`` rows, and of gdn_kv_compact."""
     return int(library().gdn_kv_workspace_bytes(cache._ref, int(count)))
@@ -641,4 +815,7 @@ __all__ = ["Layer", "Params", "Pools", "Rows", "GdnError", "library", "LIB_PATH"
            "STATUS_TOKEN_RANGE", "STATUS_ROW_RANGE", "KvCache", "KvRows", "Attention", "gdn_kv_append",
            "gdn_paged_attention", "gdn_attention_workspace_bytes", "gdn_kv_reserve", "gdn_kv_release", "gdn_kv_fork",
            "gdn_kv_copy_pages", "gdn_kv_compact", "gdn_kv_workspace_bytes", "gdn_copy_slots", "STATUS_PAGE_RANGE",
-           "STATUS_PAGE_SHARED", "STATUS_NO_PAGES"]
+           "STATUS_PAGE_SHARED", "STATUS_NO_PAGES", "KvGroups", "gdn_shared_attention",
+           "gdn_shared_attention_workspace_bytes", "gdn_kv_common_prefix", "Rope", "gdn_rope", "gdn_kv_append_rope",
+           "GDN_ROPE_HALF", "GDN_ROPE_INTERLEAVED", "GDN_ROPE_PLAIN", "GDN_ROPE_LINEAR", "GDN_ROPE_NTK", "GDN_ROPE_BANDS",
+           "GDN_ROPE_RAMP"]

@@ -151,7 +151,7 @@ __device__ __forceinline__ void values_step(float (&o)[DV / 8][4], const uint32_
 }
 
 // What a CTA keeps in shared memory behind its rings and queries.
-template <typename C>
+template <typename C, Part PART>
 struct Small {
   struct Worker {
     uint64_t full[C::kStages], empty[C::kStages], qfull, qempty;
@@ -159,16 +159,18 @@ struct Small {
     uint8_t held[C::kStages];  // per stage: which halves of the tile lie in pages that hold tokens
   } worker[C::kWorkers];
   Deal deal;
-  Share shares[C::kWorkers];
+  Share<PART> shares[C::kWorkers];
 };
 
-template <int D, int WQ, int DS, int NW>
+// PART (see gdn_attn_share.cuh): kShared takes units of kNQ of a group's queries and leaves their states, kTail begins
+// from those.
+template <int D, int WQ, int DS, int NW, Part PART = kWhole>
 __global__ void __launch_bounds__(Cfg<D, WQ, DS, NW>::kThreads, 1)
     split_kernel(SplitParams P, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
   using C = Cfg<D, WQ, DS, NW>;
-  constexpr int S = C::kStages, DV = C::kDV;
+  constexpr int S = C::kStages, DV = C::kDV, QG = PART == kShared ? C::kNQ : 0;
   extern __shared__ __align__(1024) uint8_t smem[];
-  Small<C>& small = *reinterpret_cast<Small<C>*>(smem + NW * (C::kRing + C::kQ));
+  Small<C, PART>& small = *reinterpret_cast<Small<C, PART>*>(smem + NW * (C::kRing + C::kQ));
   const AttnLaunch& p = P.a;
   const KvDev& kv = p.cache;
   // The warp's number comes from a shuffle, so that the compiler takes it as one value of the warp.  (In an early form
@@ -193,11 +195,11 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, NW>::kThreads, 1)
   asm volatile("griddepcontrol.wait;" ::: "memory");  // what lies before this overlaps the kernel before this one
   if (tid < NW) P.info[(blockIdx.x * NW + tid) * 8] = 0;
   // (the sums of find_shares lie where the first worker's ring will be)
-  find_shares<0, NW, C::kThreads>(p, reinterpret_cast<int64_t*>(smem), small.deal, small.shares);
+  find_shares<QG, NW, C::kThreads, PART>(p, reinterpret_cast<int64_t*>(smem), small.deal, small.shares);
   const bool fetches = warp >= NW * C::kTeam;
   const int wk = fetches ? warp - NW * C::kTeam : warp / C::kTeam;  // the warp's worker
   auto& sm = small.worker[wk];
-  const Share& share = small.shares[wk];
+  const Share<PART>& share = small.shares[wk];
   uint8_t* ring = smem + wk * C::kRing;
   uint8_t* qbuf = smem + NW * C::kRing + wk * C::kQ;
   const int ps = kv.page_size;
@@ -212,7 +214,8 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, NW>::kThreads, 1)
     const bool active = bi < boxes;
     int it = 0, seg = 0;
     bool ok = true;
-    for (Walk<0> w(p, share); w.valid() && ok; w.next(), ++seg) {
+    for (Walk<QG, PART> w(p, share); w.valid() && ok; w.next(), ++seg) {
+      const int h = PART == kShared ? w.h % kv.Hkv : w.h, q0 = PART == kShared ? w.h / kv.Hkv * QG : 0;
       // 32 table entries are held, one per lane, and the 32 behind them are on their way
       const int32_t* row = kv.table + (int64_t)w.u.r.trow * kv.max_pages;
       const int entries = (w.u.r.kv + ps - 1) >> shift;
@@ -220,14 +223,14 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, NW>::kThreads, 1)
       int ids = eb + lane < entries ? load(row + eb + lane) : 0;
       int ahead = eb + 32 + lane < entries ? load(row + eb + 32 + lane) : 0;
       // the unit's queries
-      const int nq = w.u.r.len * p.G;
+      const int nq = PART == kShared ? min(QG, w.u.r.len * p.G - q0) : w.u.r.len * p.G;
       int g[2];
       int rows = 0;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int qi = lane + 32 * u;
         g[u] = -1;
-        if (qi < nq) g[u] = kv_token(p.rows, w.u.r.bos + qi / p.G, p.num_global, p.status);
+        if (qi < nq) g[u] = kv_token(p.rows, w.u.r.bos + (q0 + qi) / p.G, p.num_global, p.status);
         rows += __popc(__ballot_sync(0xffffffffu, g[u] >= 0));
       }
       ok = seg == 0 || tc::mbar_wait(&sm.qempty, (seg - 1) & 1, P.wait_ns);
@@ -245,7 +248,7 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, NW>::kThreads, 1)
         if (g[u] >= 0)
           tc::bulk_g2s(qbuf + qi * C::kPitch,
                        static_cast<const __nv_bfloat16*>(p.q) + (int64_t)g[u] * p.q_stride +
-                           (int64_t)(w.h * p.G + qi % p.G) * D,
+                           (int64_t)(h * p.G + (q0 + qi) % p.G) * D,
                        D * 2, &sm.qfull);
       }
       for (int j = w.j0; j < w.j0 + w.len; ++j, ++it) {
@@ -276,7 +279,7 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, NW>::kThreads, 1)
         __syncwarp();
         if (active) {
           uint8_t* dst = ring + (size_t)s * 2 * C::kHalf + is_v * C::kHalf + (size_t)bi * box * D * 2;
-          tc::tma_page(dst, is_v ? &vmap : &kmap, pos & (ps - 1), page > 0 ? page * spp + w.h : none, &sm.full[s]);
+          tc::tma_page(dst, is_v ? &vmap : &kmap, pos & (ps - 1), page > 0 ? page * spp + h : none, &sm.full[s]);
         }
       }
     }
@@ -295,10 +298,12 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, NW>::kThreads, 1)
   const float sl2 = p.scale * 1.4426950408889634f;
   int it = 0, seg = 0;
   bool ok = true;
-  for (Walk<0> w(p, share); w.valid(); w.next(), ++seg) {
+  for (Walk<QG, PART> w(p, share); w.valid(); w.next(), ++seg) {
     const KvRow row = w.u.r;
-    const int nq = row.len * p.G;
-    const int pmin = row.kv - row.len, pmax = row.kv - 1;
+    const int h = PART == kShared ? w.h % kv.Hkv : w.h, q0 = PART == kShared ? w.h / kv.Hkv * QG : 0;
+    const int nq = PART == kShared ? min(QG, row.len * p.G - q0) : row.len * p.G;
+    // tokens up to `seen` are seen by all queries, but for the window; up to `end` by some
+    const int seen = PART == kShared ? row.kv - 1 : row.kv - row.len, end = row.kv - 1;
     float o[DV / 8][4], m[2], l[2];
     int pos[2];  // the positions of this thread's two queries, r8 and r8 + 8 of the group's 16
 #pragma unroll
@@ -307,8 +312,29 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, NW>::kThreads, 1)
     for (int e = 0; e < 2; ++e) {
       m[e] = -INFINITY;
       l[e] = 0.f;
-      pos[e] = min(pmin + (wq * 16 + r8 + 8 * e) / p.G, pmax);
+      const int qi = wq * 16 + r8 + 8 * e;
+      if constexpr (PART == kShared) {
+        pos[e] = p.window > 0 && qi < nq ? load(p.sh.token_pos + row.bos + (q0 + qi) / p.G) : end;
+      } else {
+        pos[e] = min(seen + qi / p.G, end);
+      }
+      if constexpr (PART == kTail) {
+        if (w.j0 == 0 && (w.u.own & 1) && qi < nq) {  // the state over the shared tokens
+          const int64_t at = (int64_t)(row.bos + qi / p.G) * p.Hq + h * p.G + qi % p.G;
+          const float2 ml = load(reinterpret_cast<const float2*>(p.sh.state_ml) + at);
+          m[e] = ml.x;
+          l[e] = c2 == 0 ? ml.y : 0.f;  // (the four threads of a query add their sums up at the end)
+          const float* from = p.sh.state_o + at * D + ds * DV + c2;
+#pragma unroll
+          for (int i = 0; i < DV / 8; ++i) {
+            const float2 x = load(reinterpret_cast<const float2*>(from + i * 8));
+            o[i][2 * e] = x.x;
+            o[i][2 * e + 1] = x.y;
+          }
+        }
+      }
     }
+    const int pmax = PART == kShared ? __reduce_max_sync(0xffffffffu, max(pos[0], pos[1])) : end;
     ok = __all_sync(0xffffffffu, ok && tc::mbar_wait(&sm.qfull, seg & 1, P.wait_ns));
     const uint32_t qbase =
         tc::smem_addr(qbuf) + (wq * 16 + (lane & 15)) * C::kPitch + (lane >> 4) * 16;
@@ -346,7 +372,7 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, NW>::kThreads, 1)
           }
         }
         // not every query sees every token?
-        const bool part = b + 31 > pmin || !have0 || !have1 ||
+        const bool part = b + 31 > seen || !have0 || !have1 ||
                           (p.window > 0 && b <= pmax - p.window && b + 31 >= p.sinks);
         if (part) {
 #pragma unroll
@@ -354,8 +380,8 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, NW>::kThreads, 1)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const int tok = b + n * 8 + c2 + (e & 1), at = pos[e >> 1];
-              const bool sees = tok <= at && (p.window <= 0 || tok > at - p.window || tok < p.sinks) &&
-                                (n < 2 ? have0 : have1);
+              const bool sees = tok <= at && (PART != kShared || tok <= end) &&
+                                (p.window <= 0 || tok > at - p.window || tok < p.sinks) && (n < 2 ? have0 : have1);
               if (!sees) sc[n][e] = -INFINITY;
             }
         }
@@ -405,9 +431,9 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, NW>::kThreads, 1)
           }
         }
         if (part)
-          values_step<true, DV, D / 64>(o, ph, pl, vbase, ds * DV, b, pos, pmax, p.window, p.sinks);
+          values_step<true, DV, D / 64>(o, ph, pl, vbase, ds * DV, b, pos, end, p.window, p.sinks);
         else
-          values_step<false, DV, D / 64>(o, ph, pl, vbase, ds * DV, b, pos, pmax, p.window, p.sinks);
+          values_step<false, DV, D / 64>(o, ph, pl, vbase, ds * DV, b, pos, end, p.window, p.sinks);
       }
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&sm.empty[s]);
@@ -427,10 +453,18 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, NW>::kThreads, 1)
       for (int e = 0; e < 2; ++e) {
         const int qi = wq * 16 + r8 + 8 * e;
         const int g = sm.qtok[qi];
-        if (whole && g >= 0) {
+        if (PART == kShared && whole) {
+          if (qi >= nq) continue;
+          const int64_t at = (int64_t)(row.bos + (q0 + qi) / p.G) * p.Hq + h * p.G + (q0 + qi) % p.G;
+          float* to = p.sh.state_o + at * D + ds * DV + c2;
+#pragma unroll
+          for (int i = 0; i < DV / 8; ++i)
+            *reinterpret_cast<float2*>(to + i * 8) = make_float2(o[i][2 * e], o[i][2 * e + 1]);
+          if (ds == 0 && c2 == 0) *reinterpret_cast<float2*>(p.sh.state_ml + at * 2) = make_float2(m[e], l[e]);
+        } else if (whole && g >= 0) {
           const float f = l[e] == 0.f ? 0.f : 1.f / l[e];
           __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + (int64_t)g * p.out_stride +
-                               (int64_t)(w.h * p.G + qi % p.G) * D + ds * DV + c2;
+                               (int64_t)(h * p.G + qi % p.G) * D + ds * DV + c2;
 #pragma unroll
           for (int i = 0; i < DV / 8; ++i)
             *reinterpret_cast<uint32_t*>(out + i * 8) = pack2(o[i][2 * e] * f, o[i][2 * e + 1] * f);
@@ -447,8 +481,8 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, NW>::kThreads, 1)
         int32_t* info = P.info + (blockIdx.x * NW + wk) * 8;
         info[1] = row.bos;
         info[2] = nq;
-        info[3] = w.h;
-        info[5] = 0;
+        info[3] = h;
+        info[5] = q0;
         info[4] = small.deal.owner(w.unit_last(share));  // the worker with the unit's last tile
         info[0] = 1;
       }
@@ -459,18 +493,20 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, NW>::kThreads, 1)
 }
 
 // Queries of a unit, at most (with max_q = 0 every row is a bad one, and reported).
+template <Part PART = kWhole>
 int64_t queries_of(const AttnLaunch& a) {
+  if (PART == kShared) return std::min<int64_t>(64, (int64_t)a.rows.num_tokens * a.G);
   return a.few > 0 ? a.few : std::max<int64_t>(1, (int64_t)a.rows.max_q * a.G);
 }
 
-template <int D, int WQ, int DS, int NW>
+template <Part PART, int D, int WQ, int DS, int NW>
 cudaError_t launch_cfg(const AttnLaunch& a, cudaStream_t s) {
   using C = Cfg<D, WQ, DS, NW>;
   static std::atomic<uint64_t> done{0};
-  constexpr int smem = (int)(NW * (C::kRing + C::kQ) + sizeof(Small<C>));
+  constexpr int smem = (int)(NW * (C::kRing + C::kQ) + sizeof(Small<C, PART>));
   static_assert(smem <= 232448 && C::kThreads / 32 * 8 <= (int)C::kRing, "shared memory");
   cudaError_t e = once_per_device(done, [&] {
-    return cudaFuncSetAttribute(split_kernel<D, WQ, DS, NW>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    return cudaFuncSetAttribute(split_kernel<D, WQ, DS, NW, PART>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   });
   if (e != cudaSuccess) return e;
   CUtensorMap kmap, vmap;
@@ -492,11 +528,11 @@ cudaError_t launch_cfg(const AttnLaunch& a, cudaStream_t s) {
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if ((e = cudaLaunchKernelEx(&cfg, split_kernel<D, WQ, DS, NW>, P, kmap, vmap)) != cudaSuccess) return e;
-  cfg.gridDim = dim3(kSms * NW, join_rows(kSms * NW, (int)queries_of(a)));
+  if ((e = cudaLaunchKernelEx(&cfg, split_kernel<D, WQ, DS, NW, PART>, P, kmap, vmap)) != cudaSuccess) return e;
+  cfg.gridDim = dim3(kSms * NW, join_rows(kSms * NW, (int)queries_of<PART>(a)));
   cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, join_kernel<__nv_bfloat16, D / 32, D>, P, (int)C::kNQ);
+  return cudaLaunchKernelEx(&cfg, join_kernel<__nv_bfloat16, D / 32, D, PART == kShared>, P, (int)C::kNQ);
 }
 
 int query_slots(int64_t queries) { return queries <= 16 ? 16 : queries <= 32 ? 32 : 64; }
@@ -534,21 +570,28 @@ auto pick(int d, int slots, F f) {
   return slots == 16 ? f(Cfg<256, 1, 2, 2>{}) : slots == 32 ? f(Cfg<256, 2, 2, 2>{}) : f(Cfg<256, 4, 2, 1>{});
 }
 
-template <int D, int WQ, int DS, int NW>
+template <Part PART, int D, int WQ, int DS, int NW>
 cudaError_t launch_picked(Cfg<D, WQ, DS, NW>, const AttnLaunch& a, cudaStream_t s) {
-  return launch_cfg<D, WQ, DS, NW>(a, s);
+  return launch_cfg<PART, D, WQ, DS, NW>(a, s);
 }
-
-}  // namespace
-
-size_t attn_split_workspace(const AttnLaunch& a) {
-  const int q = query_slots(queries_of(a));
+template <Part PART>
+cudaError_t launch_part(const AttnLaunch& a, cudaStream_t s) {
+  return pick(a.cache.d, query_slots(queries_of<PART>(a)), [&](auto c) { return launch_picked<PART>(c, a, s); });
+}
+template <Part PART>
+size_t workspace_of(const AttnLaunch& a) {
+  const int q = query_slots(queries_of<PART>(a));
   const size_t workers = (size_t)kSms * pick(a.cache.d, q, [](auto c) { return decltype(c)::kWorkers; });
   return workers * (8 + 4 * (size_t)q + 2 * (size_t)q * a.cache.d) * 4;
 }
 
-cudaError_t launch_attn_split(const AttnLaunch& a, cudaStream_t s) {
-  return pick(a.cache.d, query_slots(queries_of(a)), [&](auto c) { return launch_picked(c, a, s); });
-}
+}  // namespace
+
+size_t attn_split_workspace(const AttnLaunch& a) { return workspace_of<kWhole>(a); }
+size_t attn_split_shared_workspace(const AttnLaunch& a) { return workspace_of<kShared>(a); }
+
+cudaError_t launch_attn_split(const AttnLaunch& a, cudaStream_t s) { return launch_part<kWhole>(a, s); }
+cudaError_t launch_attn_split_shared(const AttnLaunch& a, cudaStream_t s) { return launch_part<kShared>(a, s); }
+cudaError_t launch_attn_split_own(const AttnLaunch& a, cudaStream_t s) { return launch_part<kTail>(a, s); }
 
 }  // namespace gdn

@@ -83,14 +83,15 @@ __device__ __forceinline__ void load_row(const __nv_bfloat16* v, bool there, flo
 }
 
 // E: columns of a lane, 32 E are head_dim or more; DC: head_dim where it is 32 E, else 0.
-template <typename T, int E, int DC>
+// PART: see gdn_attn_share.cuh.
+template <typename T, int E, int DC, Part PART = kWhole>
 __global__ void __launch_bounds__(32 * kWarps, kPerSm) split_fma_kernel(SplitParams P) {
   constexpr int kU = E <= 4 ? 8 : 4;  // tokens whose keys or values a lane holds at a time
   constexpr int kC = 32 / kU;         // as many chunks of keys, then as many of values
   __shared__ __align__(16) float sp[kWarps][32][kNQ];
   __shared__ int64_t part[kWarps];
   __shared__ Deal deal;
-  __shared__ Share shares[kWarps];
+  __shared__ Share<PART> shares[kWarps];
   const AttnLaunch& p = P.a;
   const KvDev& kv = p.cache;
   const int D = DC > 0 ? DC : kv.d;  // a multiple of 16, so of E
@@ -100,12 +101,12 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) split_fma_kernel(SplitPar
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (lane == 0) P.info[worker * 8] = 0;
-  find_shares<kNQ, kWarps, 32 * kWarps>(p, part, deal, shares);
-  const Share& share = shares[warp];
+  find_shares<kNQ, kWarps, 32 * kWarps, PART>(p, part, deal, shares);
+  const Share<PART>& share = shares[warp];
   const float sl2 = p.scale * 1.4426950408889634f;
   const int shift = __ffs(kv.page_size) - 1;
 
-  for (Walk<kNQ> w(p, share); w.valid(); w.next()) {
+  for (Walk<kNQ, PART> w(p, share); w.valid(); w.next()) {
     const KvRow row = w.u.r;
     const int h = w.h % kv.Hkv, q0 = w.h / kv.Hkv * kNQ, nq = min(kNQ, row.len * p.G - q0);
     const int first = row.kv - row.len;  // position of the first new token
@@ -118,14 +119,33 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) split_fma_kernel(SplitPar
       const T* from = static_cast<const T*>(p.q) + (int64_t)max(gi, 0) * p.q_stride;
       load_row<E>(from + (int64_t)(h * p.G + (q0 + i) % p.G) * D + lane * E, columns && gi >= 0, q[i]);
     }
-    const int pos0 = first + q0 / p.G, pos1 = first + (q0 + nq - 1) / p.G;  // of the first and last query
+    // the lowest position of a query, and the last token that some query sees
+    const int pos0 = PART == kShared ? w.u.own : first + q0 / p.G;
+    const int pos1 = PART == kShared ? row.kv - 1 : first + (q0 + nq - 1) / p.G;
     const int mine = lane >> 2;  // the query whose scores, maximum and sum this lane has, those of every 4th token
-    const int pos = min(first + (q0 + mine) / p.G, pos1);
+    int pos = min(first + (q0 + mine) / p.G, pos1);
+    if constexpr (PART == kShared)
+      pos = p.window > 0 && mine < nq ? load(p.sh.token_pos + row.bos + (q0 + mine) / p.G) : pos1;
     float o[kNQ][E], m = -INFINITY, l = 0.f;
+    const auto state_of = [&](int i) {  // of query i
+      return (int64_t)(row.bos + (q0 + i) / p.G) * p.Hq + h * p.G + (q0 + i) % p.G;
+    };
 #pragma unroll
     for (int i = 0; i < kNQ; ++i)
 #pragma unroll
       for (int e = 0; e < E; ++e) o[i][e] = 0.f;
+    if constexpr (PART == kTail) {
+      if (w.j0 == 0 && (w.u.own & 1)) {  // the states over the shared tokens
+        if (mine < nq) {
+          const float2 ml = load(reinterpret_cast<const float2*>(p.sh.state_ml) + state_of(mine));
+          m = ml.x;
+          l = (lane & 3) == 0 ? ml.y : 0.f;  // (the four lanes of a query add their sums up at the end)
+        }
+#pragma unroll
+        for (int i = 0; i < kNQ; ++i)
+          if (columns && i < nq) load_row<E>(p.sh.state_o + state_of(i) * D + lane * E, true, o[i]);
+      }
+    }
     const int32_t* table = kv.table + (int64_t)row.trow * kv.max_pages;
     auto entry = [&](int j) {  // the table's entry of this lane's token of tile j
       const int tok = w.tile_at(j) + lane;
@@ -191,7 +211,7 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) split_fma_kernel(SplitPar
 #pragma unroll
       for (int n = 0; n < 8; ++n) {
         const int t = 4 * n + (lane & 3), tk = b + t;
-        const bool sees = (seen >> t & 1u) && tk <= pos && (p.window <= 0 || tk > pos - p.window || tk < p.sinks);
+        const bool sees = (seen >> t & 1u) && tk <= pos && (PART != kShared || tk <= pos1) && (p.window <= 0 || tk > pos - p.window || tk < p.sinks);
         if (!sees) s[n] = -INFINITY;
         x_max = fmaxf(x_max, s[n]);
       }
@@ -256,7 +276,13 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) split_fma_kernel(SplitPar
       const float li = __shfl_sync(0xffffffffu, l, 4 * i), mi = __shfl_sync(0xffffffffu, m, 4 * i);
       const int gi = __shfl_sync(0xffffffffu, g, i);
       if (i >= nq) continue;
-      if (whole) {
+      if (PART == kShared && whole) {
+        float* dst = p.sh.state_o + state_of(i) * D + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          if (columns) dst[e] = o[i][e];
+        if (lane == 0) *reinterpret_cast<float2*>(p.sh.state_ml + state_of(i) * 2) = make_float2(mi, li);
+      } else if (whole) {
         if (gi < 0) continue;
         const float inv = li == 0.f ? 0.f : 1.f / li;
         T* out = static_cast<T*>(p.out) + (int64_t)gi * p.out_stride + (int64_t)(h * p.G + (q0 + i) % p.G) * D;
@@ -284,7 +310,7 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) split_fma_kernel(SplitPar
   }
 }
 
-template <typename T, int E, int DC>
+template <Part PART, typename T, int E, int DC>
 cudaError_t launch_as(const AttnLaunch& a, cudaStream_t s) {
   constexpr int ctas = kSms * kPerSm;
   SplitParams P{};
@@ -301,17 +327,31 @@ cudaError_t launch_as(const AttnLaunch& a, cudaStream_t s) {
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, split_fma_kernel<T, E, DC>, P);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, split_fma_kernel<T, E, DC, PART>, P);
   if (e != cudaSuccess) return e;
-  const int queries = (int)std::min<int64_t>(kNQ, std::max<int64_t>(1, (int64_t)a.rows.max_q * a.G));
+  const int most = PART == kShared ? a.rows.num_tokens : a.rows.max_q;
+  const int queries = (int)std::min<int64_t>(kNQ, std::max<int64_t>(1, (int64_t)most * a.G));
   cfg.gridDim = dim3(ctas * kWarps, join_rows(ctas * kWarps, queries));
   cfg.blockDim = dim3(32 * kJoinWarps);
-  return cudaLaunchKernelEx(&cfg, join_kernel<T, E, DC>, P, kNQ);
+  return cudaLaunchKernelEx(&cfg, join_kernel<T, E, DC, PART == kShared>, P, kNQ);
 }
-template <typename T>
+template <Part PART, typename T>
 cudaError_t launch_any(const AttnLaunch& a, cudaStream_t s) {
   const int d = a.cache.d;
-  return d <= 64 ? launch_as<T, 2, 0>(a, s) : d <= 128 ? launch_as<T, 4, 0>(a, s) : launch_as<T, 8, 0>(a, s);
+  return d <= 64    ? launch_as<PART, T, 2, 0>(a, s)
+         : d <= 128 ? launch_as<PART, T, 4, 0>(a, s)
+                    : launch_as<PART, T, 8, 0>(a, s);
+}
+template <Part PART>
+cudaError_t launch_part(const AttnLaunch& a, gdn_dtype dtype, cudaStream_t s) {
+  if (dtype == GDN_BF16) return launch_any<PART, __nv_bfloat16>(a, s);
+  switch (a.cache.d) {
+    case 32: return launch_as<PART, float, 1, 32>(a, s);
+    case 64: return launch_as<PART, float, 2, 64>(a, s);
+    case 128: return launch_as<PART, float, 4, 128>(a, s);
+    case 256: return launch_as<PART, float, 8, 256>(a, s);
+    default: return launch_any<PART, float>(a, s);
+  }
 }
 
 }  // namespace
@@ -321,14 +361,13 @@ size_t attn_split_fma_workspace(const AttnLaunch& a) {
 }
 
 cudaError_t launch_attn_split_fma(const AttnLaunch& a, gdn_dtype dtype, cudaStream_t s) {
-  if (dtype == GDN_BF16) return launch_any<__nv_bfloat16>(a, s);
-  switch (a.cache.d) {
-    case 32: return launch_as<float, 1, 32>(a, s);
-    case 64: return launch_as<float, 2, 64>(a, s);
-    case 128: return launch_as<float, 4, 128>(a, s);
-    case 256: return launch_as<float, 8, 256>(a, s);
-    default: return launch_any<float>(a, s);
-  }
+  return launch_part<kWhole>(a, dtype, s);
+}
+cudaError_t launch_attn_split_fma_shared(const AttnLaunch& a, gdn_dtype dtype, cudaStream_t s) {
+  return launch_part<kShared>(a, dtype, s);
+}
+cudaError_t launch_attn_split_fma_own(const AttnLaunch& a, gdn_dtype dtype, cudaStream_t s) {
+  return launch_part<kTail>(a, dtype, s);
 }
 
 }  // namespace gdn

@@ -93,6 +93,29 @@ struct AppendLaunch {
   uint32_t* status;
 };
 
+// Which part of a row's cache a pass of attention goes over: all of it; what the rows of a group share, for the queries of
+// all of them; or a row's own, beginning from what the pass over the shared part has left.
+enum Part { kWhole, kShared, kTail };
+
+// A group of rows that share a prefix, as the passes see it (written on the device).
+struct GroupRec {
+  int32_t bos, eos;        // its rows' local tokens
+  int32_t shared;          // tokens of the prefix, whole pages
+  int32_t trow;            // the row of the block table that they are read by
+  int32_t pos_min;         // the lowest position of a query
+  int32_t pad[3];
+};
+
+// What the passes over shared prefixes and own tokens hand on.
+struct SharedDev {
+  GroupRec* groups;    // [num_groups]
+  int32_t* row_own;    // [num_seqs] first own token of a row (a multiple of 16); + 1: its queries have a state
+  int32_t* token_pos;  // [num_tokens] position of a local token, written under a window only
+  float* state_ml;     // [num_tokens][Hq][2]: m (of the scores before their scale), l
+  float* state_o;      // [num_tokens][Hq][d]
+  int32_t num_groups;
+};
+
 struct AttnLaunch {
   KvDev cache;
   KvRowsDev rows;
@@ -106,6 +129,39 @@ struct AttnLaunch {
   int32_t sinks;
   int32_t few;     // > 0: rows of up to so many queries per kv-head are the split kernel's, others the prompt one's
   void* ws;
+  uint32_t* status;
+  SharedDev sh;    // of the passes over shared and own parts
+};
+
+// Heads turned by their tokens' positions, alone or on their way into the cache.
+struct TurnLaunch {
+  const uint64_t* turns;  // [rotary / 2]
+  int32_t rotary, layout;
+  float magnitude;
+  int32_t d, Hq, num_tokens;
+  const int32_t* positions;  // alone: [num_tokens]
+  const void* q;
+  void* q_out;
+  int64_t q_stride, q_out_stride;  // elements
+  // into the cache
+  KvDev cache;
+  KvRowsDev rows;
+  const void* k;
+  const void* v;
+  int64_t k_stride, v_stride;
+  int32_t num_global;
+  uint32_t* status;
+};
+
+// Groups of rows: group g is rows [start[g], start[g + 1]).
+struct GroupsLaunch {
+  KvDev cache;
+  KvRowsDev rows;
+  const int32_t* start;
+  int32_t* prefix;  // [num_groups] shared tokens, read or written
+  int32_t num_groups;
+  int32_t window, sinks;
+  SharedDev sh;
   uint32_t* status;
 };
 
@@ -143,6 +199,8 @@ int check_layer_pools(const gdn_layer_desc* layer, const gdn_pools* pools);
 size_t kv_workspace_ints(int32_t num_pages, int32_t count);
 
 cudaError_t launch_kv_append(const AppendLaunch& p, cudaStream_t s);
+cudaError_t launch_rope(const TurnLaunch& p, gdn_dtype dtype, cudaStream_t s);
+cudaError_t launch_kv_append_rope(const TurnLaunch& p, gdn_dtype dtype, cudaStream_t s);
 cudaError_t launch_kv_reserve(const PageRowsLaunch& p, cudaStream_t s);
 cudaError_t launch_kv_release(const PageRowsLaunch& p, cudaStream_t s);
 cudaError_t launch_kv_fork(const PageRowsLaunch& p, cudaStream_t s);
@@ -162,5 +220,14 @@ cudaError_t launch_attn_prompt(const AttnLaunch& p, cudaStream_t s);
 // Every other layout, rows of any length: split over the cache's length, on the CUDA cores.
 size_t attn_split_fma_workspace(const AttnLaunch& p);
 cudaError_t launch_attn_split_fma(const AttnLaunch& p, gdn_dtype dtype, cudaStream_t s);
+
+// Groups of rows over shared prefixes: the plan, and the passes over the shared and the own parts.
+cudaError_t launch_kv_common_prefix(const GroupsLaunch& p, cudaStream_t s);
+cudaError_t launch_group_plan(const GroupsLaunch& p, cudaStream_t s);
+size_t attn_split_shared_workspace(const AttnLaunch& p);
+cudaError_t launch_attn_split_shared(const AttnLaunch& p, cudaStream_t s);
+cudaError_t launch_attn_split_own(const AttnLaunch& p, cudaStream_t s);
+cudaError_t launch_attn_split_fma_shared(const AttnLaunch& p, gdn_dtype dtype, cudaStream_t s);
+cudaError_t launch_attn_split_fma_own(const AttnLaunch& p, gdn_dtype dtype, cudaStream_t s);
 
 }  // namespace gdn

@@ -15,6 +15,7 @@ namespace {
 
 constexpr int32_t kMaxTableEntries = 1 << 20;  // of one row: the sums of needs stay in 32 bits
 constexpr int32_t kMaxPages = 1 << 28;
+constexpr int32_t kMaxPairs = 128;  // of a head
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 size_t round256(size_t b) { return (b + 255) & ~size_t(255); }
@@ -76,6 +77,88 @@ int check_attn(const gdn_attn_desc* a, const gdn_kv_cache* c) {
   return a->scale == a->scale && fabsf(a->scale) < INFINITY ? GDN_OK : GDN_ERR_SHAPE;
 }
 
+int check_rope(const gdn_rope_desc* r, int32_t head_dim) {
+  if (!r || !r->turns) return GDN_ERR_NULL_ARG;
+  if (r->rotary_dim < 2 || r->rotary_dim % 2 || r->rotary_dim > head_dim) return GDN_ERR_SHAPE;
+  if (r->layout != GDN_ROPE_HALF && r->layout != GDN_ROPE_INTERLEAVED) return GDN_ERR_SHAPE;
+  if (!(fabsf(r->magnitude) < INFINITY)) return GDN_ERR_SHAPE;
+  return (reinterpret_cast<uintptr_t>(r->turns) & 7u) ? GDN_ERR_ALIGN : GDN_OK;
+}
+
+// Whether tokens written to `out` may be read from `x` by another thread, all of one type; strides and widths in elements.
+// What a call writes has to be memory that it does not read (other columns of one wider tensor included) or, in place,
+// what the same thread reads.
+bool entangled(const void* x, int64_t x_stride, int64_t x_width, const void* out, int64_t out_stride, int64_t out_width,
+               int64_t tokens, int es, bool in_place) {
+  if (tokens < 1) return false;
+  const int64_t a = (int64_t)reinterpret_cast<uintptr_t>(x), b = (int64_t)reinterpret_cast<uintptr_t>(out);
+  const int64_t aw = x_width * es, bw = out_width * es, stride = x_stride * es;
+  const int64_t a_end = a + (tokens - 1) * stride + aw, b_end = b + (tokens - 1) * out_stride * es + bw;
+  if (a_end <= b || b_end <= a || (in_place && a == b && (tokens == 1 || x_stride == out_stride))) return false;
+  if (tokens == 1 || x_stride != out_stride) return true;
+  const int64_t between = ((b - a) % stride + stride) % stride;
+  return between < aw || stride - between < bw;
+}
+
+// A frequency as a 64-bit fraction of a turn; false for one that is none.
+bool turn_fraction(double radians, uint64_t& fraction) {
+  const double turns = radians / 6.283185307179586476925;
+  if (!(fabs(turns) < 0x1p52)) return false;
+  const double scaled = floor(ldexp(turns - floor(turns), 64) + 0.5);
+  fraction = scaled < 0x1p64 ? (uint64_t)scaled : 0;  // (a whole turn)
+  return true;
+}
+
+// The frequencies of gdn_rope_turns; false for values that make none.
+bool rope_turns(const gdn_rope_freq& f, uint64_t* turns, float* magnitude) {
+  const int r = f.rotary_dim;
+  const bool scaled = f.scaling != GDN_ROPE_PLAIN;
+  if (r < 2 || r > 2 * kMaxPairs || r % 2 || f.scaling < GDN_ROPE_PLAIN || f.scaling > GDN_ROPE_RAMP) return false;
+  if (!(f.base > 1.0 && f.base < INFINITY) || (scaled && !(f.factor > 0.0 && f.factor < INFINITY))) return false;
+  const bool parts = f.scaling == GDN_ROPE_BANDS || f.scaling == GDN_ROPE_RAMP;
+  if (parts && !(f.original_len > 0.0 && f.original_len < INFINITY)) return false;
+  const double low = f.low != 0.0 ? f.low : 1.0;
+  const double high = f.high != 0.0 ? f.high : f.scaling == GDN_ROPE_RAMP ? 32.0 : 4.0;
+  if (parts && !(low > 0.0 && low < high && high < INFINITY)) return false;
+  const double two_pi = 6.283185307179586476925;
+  const double base = f.scaling == GDN_ROPE_NTK && r > 2 ? f.base * pow(f.factor, (double)r / (r - 2)) : f.base;
+  if (!(base > 0.0 && base < INFINITY)) return false;
+  // the pair that turns so often over the original length
+  auto pair_of = [&](double times) { return r * log(f.original_len / (two_pi * times)) / (2.0 * log(f.base)); };
+  double from = 0.0, to = 0.0;
+  if (f.scaling == GDN_ROPE_RAMP) {
+    from = fmax(floor(pair_of(high)), 0.0);
+    to = fmin(ceil(pair_of(low)), r - 1.0);
+  }
+  for (int i = 0; i < r / 2; ++i) {
+    double w = pow(base, -2.0 * i / r);
+    if (f.scaling == GDN_ROPE_LINEAR) w /= f.factor;
+    if (parts) {
+      const double keep = f.scaling == GDN_ROPE_BANDS ? (f.original_len * w / two_pi - low) / (high - low)
+                                                      : 1.0 - (i - from) / fmax(to - from, 0.001);
+      const double k = fmin(fmax(keep, 0.0), 1.0);
+      w = k * w + (1.0 - k) * w / f.factor;
+    }
+    if (!turn_fraction(w, turns[i])) return false;
+  }
+  if (magnitude) *magnitude = f.scaling == GDN_ROPE_RAMP ? (float)(0.1 * log(f.factor) + 1.0) : 1.f;
+  return true;
+}
+
+void rope_args(const gdn_rope_desc* r, TurnLaunch& p) {
+  p.turns = r->turns;
+  p.rotary = r->rotary_dim;
+  p.layout = r->layout;
+  p.magnitude = r->magnitude == 0.f ? 1.f : r->magnitude;
+}
+
+int check_groups(const gdn_kv_groups* g) {
+  if (!g) return GDN_ERR_NULL_ARG;
+  if (g->num_groups < 0 || g->num_groups > 65535) return GDN_ERR_SHAPE;
+  if (g->num_groups > 0 && (!g->group_start_loc || !g->prefix_lens)) return GDN_ERR_NULL_ARG;
+  return GDN_OK;
+}
+
 KvDev kv_dev(const gdn_kv_cache* c) {
   KvDev d{};
   d.k = c->k_pool;
@@ -106,6 +189,85 @@ AttnLaunch attn_args(const gdn_attn_desc* a, const gdn_kv_cache* c, const gdn_kv
   p.scale = a->scale > 0.f ? a->scale : 1.0f / sqrtf((float)c->head_dim);
   p.window = a->window > 0 ? a->window : 0;
   p.sinks = a->window > 0 ? a->num_sinks : 0;
+  return p;
+}
+
+// What the attention calls refuse before their workspace is looked at; GDN_OK with no tokens: there is nothing to do.
+int attention_checks(const gdn_attn_desc* attn, const gdn_kv_cache* cache, const gdn_kv_rows* rows, const void* q,
+                     int32_t num_global_tokens, const void* out) {
+  int rc;
+  if ((rc = check_shape(cache)) || (rc = check_table(cache)) || (rc = check_pools(cache)) ||
+      (rc = check_attn(attn, cache)) || (rc = check_kv_rows(rows)))
+    return rc;
+  if (num_global_tokens < 0) return GDN_ERR_SHAPE;
+  if (rows->num_tokens == 0) return GDN_OK;
+  if (!q || !out) return GDN_ERR_NULL_ARG;
+  if (!aligned16(q) || !aligned16(out)) return GDN_ERR_ALIGN;
+  if (!rows->token_indx && rows->num_tokens > num_global_tokens) return GDN_ERR_SHAPE;
+  return (int64_t)rows->num_tokens * attn->num_q_heads > INT32_MAX ? GDN_ERR_SHAPE : GDN_OK;
+}
+
+int attention_args(const gdn_attn_desc* attn, const gdn_kv_cache* cache, const gdn_kv_rows* rows, const void* q,
+                   int64_t q_stride, int32_t num_global_tokens, void* out, int64_t out_stride, void* workspace,
+                   size_t workspace_bytes, size_t need, uint32_t* d_status, AttnLaunch& p) {
+  if (need && (!workspace || workspace_bytes < need)) return GDN_ERR_WORKSPACE;
+  if (need && (reinterpret_cast<uintptr_t>(workspace) & 255u)) return GDN_ERR_ALIGN;
+  p = attn_args(attn, cache, rows);
+  const int64_t dense = (int64_t)attn->num_q_heads * cache->head_dim;
+  p.q = q;
+  p.out = out;
+  p.q_stride = token_stride(q_stride, dense, es_of(cache->dtype));
+  p.out_stride = token_stride(out_stride, dense, es_of(cache->dtype));
+  if (!p.q_stride || !p.out_stride) return GDN_ERR_SHAPE;
+  p.num_global = num_global_tokens;
+  p.ws = workspace;
+  p.status = d_status;
+  return GDN_OK;
+}
+
+int attend_whole(AttnLaunch& p, gdn_dtype dtype, cudaStream_t s) {
+  if (attn_split_supported(p, dtype)) return cuda_rc(launch_attn_split(p, s));
+  if (!attn_prompt_supported(p, dtype)) return cuda_rc(launch_attn_split_fma(p, dtype, s));
+  p.few = attn_few(p, dtype);
+  int rc;
+  if (p.few && (rc = cuda_rc(launch_attn_split(p, s)))) return rc;
+  return cuda_rc(launch_attn_prompt(p, s));
+}
+
+// Whether rows of these sizes share their groups' prefixes: all that one pass over own tokens takes.  Rows of more than 64
+// queries per kv-head on the tensor cores fill a tile of their own, and go over the whole of their caches.
+bool shares(const AttnLaunch& p, gdn_dtype dtype) {
+  return attn_split_supported(p, dtype) || !attn_prompt_supported(p, dtype);
+}
+
+// The workspace of attention over groups: the plan, the queries' states, and what the larger of the two passes takes.
+struct SharedWs {
+  size_t groups, row_own, token_pos, ml, o, pass, end;
+};
+SharedWs shared_ws(const AttnLaunch& p, int32_t num_groups, gdn_dtype dtype) {
+  SharedWs w{};
+  const size_t tokens = p.rows.num_tokens, queries = tokens * p.Hq;
+  w.groups = 0;
+  w.row_own = round256(w.groups + (size_t)num_groups * sizeof(GroupRec));
+  w.token_pos = round256(w.row_own + (size_t)p.rows.num_seqs * 4);
+  w.ml = round256(w.token_pos + (p.window > 0 ? tokens * 4 : 0));
+  w.o = round256(w.ml + queries * 8);
+  w.pass = round256(w.o + queries * p.cache.d * 4);
+  const bool split = attn_split_supported(p, dtype);
+  const size_t shared = split ? attn_split_shared_workspace(p) : attn_split_fma_workspace(p);
+  const size_t own = split ? attn_split_workspace(p) : attn_split_fma_workspace(p);
+  w.end = w.pass + round256(shared > own ? shared : own);
+  return w;
+}
+
+GroupsLaunch groups_args(const gdn_kv_cache* c, const gdn_kv_rows* r, const gdn_kv_groups* g, uint32_t* status) {
+  GroupsLaunch p{};
+  p.cache = kv_dev(c);
+  p.rows = kv_rows_dev(r);
+  p.start = g->group_start_loc;
+  p.prefix = g->prefix_lens;
+  p.num_groups = g->num_groups;
+  p.status = status;
   return p;
 }
 
@@ -165,6 +327,94 @@ int gdn_kv_append(const gdn_kv_cache* cache, const gdn_kv_rows* rows, const void
   return cuda_rc(launch_kv_append(p, (cudaStream_t)stream));
 }
 
+int gdn_rope_turns(const gdn_rope_freq* freq, uint64_t* turns, float* magnitude) {
+  if (!freq || !turns) return GDN_ERR_NULL_ARG;
+  return rope_turns(*freq, turns, magnitude) ? GDN_OK : GDN_ERR_SHAPE;
+}
+
+int gdn_rope_turns_of(const double* radians, int32_t count, uint64_t* turns) {
+  if (!radians || !turns) return GDN_ERR_NULL_ARG;
+  if (count < 1 || count > kMaxPairs) return GDN_ERR_SHAPE;
+  for (int32_t i = 0; i < count; ++i)
+    if (!turn_fraction(radians[i], turns[i])) return GDN_ERR_SHAPE;
+  return GDN_OK;
+}
+
+int gdn_rope(const gdn_rope_desc* rope, int32_t num_heads, int32_t head_dim, gdn_dtype dtype, const int32_t* positions,
+             int32_t num_tokens, const void* x, int64_t x_stride, void* out, int64_t out_stride, void* stream) {
+  Range range("gdn_rope");
+  if (dtype != GDN_BF16 && dtype != GDN_F32) return GDN_ERR_DTYPE;
+  if (head_dim < 16 || head_dim > 256 || head_dim % 16 || num_heads < 1 || num_heads > 65535) return GDN_ERR_SHAPE;
+  int rc = check_rope(rope, head_dim);
+  if (rc) return rc;
+  if (num_tokens < 0) return GDN_ERR_SHAPE;
+  if (num_tokens == 0) return GDN_OK;
+  if (!positions || !x || !out) return GDN_ERR_NULL_ARG;
+  if (!aligned16(x) || !aligned16(out)) return GDN_ERR_ALIGN;
+  TurnLaunch p{};
+  rope_args(rope, p);
+  const int64_t dense = (int64_t)num_heads * head_dim;
+  const int es = es_of(dtype);
+  p.q_stride = token_stride(x_stride, dense, es);
+  p.q_out_stride = token_stride(out_stride, dense, es);
+  if (!p.q_stride || !p.q_out_stride || entangled(x, p.q_stride, dense, out, p.q_out_stride, dense, num_tokens, es, true))
+    return GDN_ERR_SHAPE;
+  p.d = head_dim;
+  p.Hq = num_heads;
+  p.num_tokens = num_tokens;
+  p.positions = positions;
+  p.q = x;
+  p.q_out = out;
+  return cuda_rc(launch_rope(p, dtype, (cudaStream_t)stream));
+}
+
+int gdn_kv_append_rope(const gdn_kv_cache* cache, const gdn_kv_rows* rows, const gdn_rope_desc* rope, const void* k,
+                       int64_t k_stride, const void* v, int64_t v_stride, int32_t num_q_heads, const void* q,
+                       int64_t q_stride, void* q_out, int64_t q_out_stride, int32_t num_global_tokens, uint32_t* d_status,
+                       void* stream) {
+  Range range("gdn_kv_append_rope");
+  int rc;
+  if ((rc = check_shape(cache)) || (rc = check_table(cache)) || (rc = check_pools(cache)) ||
+      (rc = check_kv_rows(rows)) || (rc = check_rope(rope, cache->head_dim)))
+    return rc;
+  if (num_global_tokens < 0 || num_q_heads < 0 || num_q_heads > 65535) return GDN_ERR_SHAPE;
+  if (rows->num_tokens == 0) return GDN_OK;
+  if (!k || !v || (num_q_heads > 0 && (!q || !q_out))) return GDN_ERR_NULL_ARG;
+  if (!aligned16(k) || !aligned16(v)) return GDN_ERR_ALIGN;
+  if (num_q_heads > 0 && (!aligned16(q) || !aligned16(q_out))) return GDN_ERR_ALIGN;
+  if (!rows->token_indx && rows->num_tokens > num_global_tokens) return GDN_ERR_SHAPE;
+  TurnLaunch p{};
+  rope_args(rope, p);
+  p.cache = kv_dev(cache);
+  p.rows = kv_rows_dev(rows);
+  const int es = es_of(cache->dtype);
+  const int64_t dense = (int64_t)cache->num_kv_heads * cache->head_dim;
+  p.k = k;
+  p.v = v;
+  p.k_stride = token_stride(k_stride, dense, es);
+  p.v_stride = token_stride(v_stride, dense, es);
+  if (!p.k_stride || !p.v_stride) return GDN_ERR_SHAPE;
+  p.num_global = num_global_tokens;
+  if (num_q_heads > 0) {
+    const int64_t width = (int64_t)num_q_heads * cache->head_dim;
+    p.q = q;
+    p.q_out = q_out;
+    p.q_stride = token_stride(q_stride, width, es);
+    p.q_out_stride = token_stride(q_out_stride, width, es);
+    if (!p.q_stride || !p.q_out_stride) return GDN_ERR_SHAPE;
+    const int n = num_global_tokens;
+    if (entangled(q, p.q_stride, width, q_out, p.q_out_stride, width, n, es, true) ||
+        entangled(k, p.k_stride, dense, q_out, p.q_out_stride, width, n, es, false) ||
+        entangled(v, p.v_stride, dense, q_out, p.q_out_stride, width, n, es, false))
+      return GDN_ERR_SHAPE;
+  }
+  p.Hq = num_q_heads;
+  p.d = cache->head_dim;
+  p.num_tokens = rows->num_tokens;
+  p.status = d_status;
+  return cuda_rc(launch_kv_append_rope(p, cache->dtype, (cudaStream_t)stream));
+}
+
 size_t gdn_attention_workspace_bytes(const gdn_attn_desc* attn, const gdn_kv_cache* cache, const gdn_kv_rows* rows) {
   if (check_shape(cache) || check_table(cache) || check_attn(attn, cache) || check_kv_rows(rows)) return 0;
   if (rows->num_seqs == 0) return 0;
@@ -180,35 +430,68 @@ int gdn_paged_attention(const gdn_attn_desc* attn, const gdn_kv_cache* cache, co
                         int64_t q_stride, int32_t num_global_tokens, void* out, int64_t out_stride, void* workspace,
                         size_t workspace_bytes, uint32_t* d_status, void* stream) {
   Range range("gdn_paged_attention");
-  int rc;
-  if ((rc = check_shape(cache)) || (rc = check_table(cache)) || (rc = check_pools(cache)) ||
-      (rc = check_attn(attn, cache)) || (rc = check_kv_rows(rows)))
+  int rc = attention_checks(attn, cache, rows, q, num_global_tokens, out);
+  if (rc || rows->num_tokens == 0) return rc;
+  AttnLaunch p;
+  if ((rc = attention_args(attn, cache, rows, q, q_stride, num_global_tokens, out, out_stride, workspace, workspace_bytes,
+                           gdn_attention_workspace_bytes(attn, cache, rows), d_status, p)))
     return rc;
-  if (num_global_tokens < 0) return GDN_ERR_SHAPE;
-  if (rows->num_tokens == 0) return GDN_OK;
-  if (!q || !out) return GDN_ERR_NULL_ARG;
-  if (!aligned16(q) || !aligned16(out)) return GDN_ERR_ALIGN;
-  if (!rows->token_indx && rows->num_tokens > num_global_tokens) return GDN_ERR_SHAPE;
-  if ((int64_t)rows->num_tokens * attn->num_q_heads > INT32_MAX) return GDN_ERR_SHAPE;
-  const size_t need = gdn_attention_workspace_bytes(attn, cache, rows);
-  if (need && (!workspace || workspace_bytes < need)) return GDN_ERR_WORKSPACE;
-  if (need && (reinterpret_cast<uintptr_t>(workspace) & 255u)) return GDN_ERR_ALIGN;
-  AttnLaunch p = attn_args(attn, cache, rows);
-  const int64_t dense = (int64_t)attn->num_q_heads * cache->head_dim;
-  p.q = q;
-  p.out = out;
-  p.q_stride = token_stride(q_stride, dense, es_of(cache->dtype));
-  p.out_stride = token_stride(out_stride, dense, es_of(cache->dtype));
-  if (!p.q_stride || !p.out_stride) return GDN_ERR_SHAPE;
-  p.num_global = num_global_tokens;
-  p.ws = workspace;
-  p.status = d_status;
-  if (attn_split_supported(p, cache->dtype)) return cuda_rc(launch_attn_split(p, (cudaStream_t)stream));
-  if (!attn_prompt_supported(p, cache->dtype))
-    return cuda_rc(launch_attn_split_fma(p, cache->dtype, (cudaStream_t)stream));
-  p.few = attn_few(p, cache->dtype);
-  if (p.few && (rc = cuda_rc(launch_attn_split(p, (cudaStream_t)stream)))) return rc;
-  return cuda_rc(launch_attn_prompt(p, (cudaStream_t)stream));
+  return attend_whole(p, cache->dtype, (cudaStream_t)stream);
+}
+
+size_t gdn_shared_attention_workspace_bytes(const gdn_attn_desc* attn, const gdn_kv_cache* cache, const gdn_kv_rows* rows,
+                                            const gdn_kv_groups* groups) {
+  if (check_groups(groups)) return 0;
+  const size_t whole = gdn_attention_workspace_bytes(attn, cache, rows);
+  if (check_shape(cache) || check_table(cache) || check_attn(attn, cache) || check_kv_rows(rows)) return 0;
+  const AttnLaunch p = attn_args(attn, cache, rows);
+  if (rows->num_tokens == 0 || groups->num_groups == 0 || !shares(p, cache->dtype)) return whole;
+  return shared_ws(p, groups->num_groups, cache->dtype).end;
+}
+
+int gdn_shared_attention(const gdn_attn_desc* attn, const gdn_kv_cache* cache, const gdn_kv_rows* rows,
+                         const gdn_kv_groups* groups, const void* q, int64_t q_stride, int32_t num_global_tokens, void* out,
+                         int64_t out_stride, void* workspace, size_t workspace_bytes, uint32_t* d_status, void* stream) {
+  Range range("gdn_shared_attention");
+  int rc = attention_checks(attn, cache, rows, q, num_global_tokens, out);
+  if (rc || (rc = check_groups(groups)) || rows->num_tokens == 0) return rc;
+  const size_t need = gdn_shared_attention_workspace_bytes(attn, cache, rows, groups);
+  AttnLaunch p;
+  if ((rc = attention_args(attn, cache, rows, q, q_stride, num_global_tokens, out, out_stride, workspace, workspace_bytes,
+                           need, d_status, p)))
+    return rc;
+  if (groups->num_groups == 0 || !shares(p, cache->dtype)) return attend_whole(p, cache->dtype, (cudaStream_t)stream);
+  const SharedWs w = shared_ws(p, groups->num_groups, cache->dtype);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.sh.groups = reinterpret_cast<GroupRec*>(ws + w.groups);
+  p.sh.row_own = reinterpret_cast<int32_t*>(ws + w.row_own);
+  p.sh.token_pos = reinterpret_cast<int32_t*>(ws + w.token_pos);
+  p.sh.state_ml = reinterpret_cast<float*>(ws + w.ml);
+  p.sh.state_o = reinterpret_cast<float*>(ws + w.o);
+  p.sh.num_groups = groups->num_groups;
+  p.ws = ws + w.pass;
+  GroupsLaunch plan = groups_args(cache, rows, groups, d_status);
+  plan.window = p.window;
+  plan.sinks = p.sinks;
+  plan.sh = p.sh;
+  const cudaStream_t s = (cudaStream_t)stream;
+  if ((rc = cuda_rc(launch_group_plan(plan, s)))) return rc;
+  if (attn_split_supported(p, cache->dtype)) {
+    if ((rc = cuda_rc(launch_attn_split_shared(p, s)))) return rc;
+    return cuda_rc(launch_attn_split_own(p, s));
+  }
+  if ((rc = cuda_rc(launch_attn_split_fma_shared(p, cache->dtype, s)))) return rc;
+  return cuda_rc(launch_attn_split_fma_own(p, cache->dtype, s));
+}
+
+int gdn_kv_common_prefix(const gdn_kv_cache* cache, const gdn_kv_rows* rows, const gdn_kv_groups* groups,
+                         uint32_t* d_status, void* stream) {
+  Range range("gdn_kv_common_prefix");
+  int rc;
+  if ((rc = check_shape(cache)) || (rc = check_table(cache)) || (rc = check_kv_rows(rows)) || (rc = check_groups(groups)))
+    return rc;
+  if (groups->num_groups == 0) return GDN_OK;
+  return cuda_rc(launch_kv_common_prefix(groups_args(cache, rows, groups, d_status), (cudaStream_t)stream));
 }
 
 int gdn_kv_reserve(const gdn_kv_cache* cache, int32_t count, const int32_t* table_rows, const int32_t* from_lens,

@@ -1,0 +1,203 @@
+// gdn_kv_groups.cu -- groups of rows that hold the same pages: how far they agree, and the plan of attention over them.
+//
+// Both read a few integers per row and entry, 4 bytes an entry and row: what takes time is the launch and the loads that
+// depend on one another (bounds, rows, table).
+#include "gdn_kv.cuh"
+
+namespace gdn {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kCluster = 8;
+
+__device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ int cluster_rank() {
+  int r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// The value that CTA `rank` of the cluster holds at `mine` of its shared memory.
+__device__ __forceinline__ int from_rank(const int* mine, int rank) {
+  uint32_t a;
+  int v;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"((uint32_t)__cvta_generic_to_shared(mine)), "r"(rank));
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+
+// The group's rows [a, b); false (and the status bit) for bounds that are none.
+__device__ __forceinline__ bool group_rows(const GroupsLaunch& p, int g, int& a, int& b, uint32_t* st) {
+  a = load(p.start + g);
+  b = load(p.start + g + 1);
+  if (a >= 0 && b >= a && b <= p.rows.num_seqs) return true;
+  set_status(st, GDN_STATUS_ROW_RANGE);
+  return false;
+}
+
+// What a group's rows say together: those with new tokens that are well formed.
+struct Rows {
+  int count;
+  int first;           // the first of them
+  int least;           // tokens before the new ones, of the row that has fewest
+  int bos, eos;        // their local tokens
+};
+__device__ __forceinline__ void add_row(const GroupsLaunch& p, int n, Rows& s, uint32_t* st) {
+  KvRow r;
+  if (!load_kv_row(p.rows, p.cache, n, r, st) || r.len == 0) return;
+  ++s.count;
+  s.first = min(s.first, n);
+  s.least = min(s.least, r.kv - r.len);
+  s.bos = min(s.bos, r.bos);
+  s.eos = max(s.eos, r.bos + r.len);
+}
+__device__ __forceinline__ Rows none() { return Rows{0, INT32_MAX, INT32_MAX, INT32_MAX, 0}; }
+__device__ __forceinline__ void warp_meet(Rows& s) {
+  s.count = __reduce_add_sync(0xffffffffu, s.count);
+  s.first = __reduce_min_sync(0xffffffffu, s.first);
+  s.least = __reduce_min_sync(0xffffffffu, s.least);
+  s.bos = __reduce_min_sync(0xffffffffu, s.bos);
+  s.eos = __reduce_max_sync(0xffffffffu, s.eos);
+}
+
+// ---- common prefix ----------------------------------------------------------------------------
+
+__device__ __forceinline__ int table_row_of(const GroupsLaunch& p, int n) {
+  return p.rows.table_rows ? load(p.rows.table_rows + n) : n;
+}
+__device__ __forceinline__ const int32_t* entries_of(const GroupsLaunch& p, int n) {
+  return p.cache.table + (int64_t)table_row_of(p, n) * p.cache.max_pages;
+}
+
+// A cluster per group; a warp per row, which goes along its entries and those of the group's first row until they differ.
+__global__ void __cluster_dims__(kCluster) __launch_bounds__(kThreads) common_kernel(GroupsLaunch p) {
+  __shared__ int least[kThreads / 32], first[kThreads / 32];
+  __shared__ int agree;
+  const int g = blockIdx.x / kCluster, rank = cluster_rank();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  int a, b;
+  if (!group_rows(p, g, a, b, rank == 0 ? p.status : nullptr)) a = b = 0;
+  Rows s = none();
+  for (int n = a + (int)threadIdx.x; n < b; n += kThreads) add_row(p, n, s, rank == 0 ? p.status : nullptr);
+  warp_meet(s);
+  if (lane == 0) {
+    least[warp] = s.least;
+    first[warp] = s.first;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kThreads / 32; ++i) {
+    s.least = min(s.least, least[i]);
+    s.first = min(s.first, first[i]);
+  }
+  const bool any = s.first != INT32_MAX;
+  int whole = any ? s.least / p.cache.page_size : 0;
+  if (threadIdx.x == 0) agree = whole;
+  __syncthreads();
+  if (whole > 0) {
+    const int32_t* of_first = entries_of(p, s.first);
+    for (int n = a + rank * (kThreads / 32) + warp; n < b; n += kCluster * (kThreads / 32)) {
+      KvRow r;
+      if (n == s.first || !load_kv_row(p.rows, p.cache, n, r, nullptr) || r.len == 0) continue;
+      const int32_t* mine = entries_of(p, n);
+      constexpr int kAhead = 4;
+      for (int e0 = 0; e0 < whole; e0 += 32 * kAhead) {
+        bool differs[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+          const int e = e0 + 32 * u + lane;
+          differs[u] = e < whole && page_or_null(load(of_first + e), p.cache, p.status) !=
+                                        page_or_null(load(mine + e), p.cache, p.status);
+        }
+        int at = whole;
+#pragma unroll
+        for (int u = kAhead - 1; u >= 0; --u) {
+          const unsigned m = __ballot_sync(0xffffffffu, differs[u]);
+          if (m) at = e0 + 32 * u + __ffs(m) - 1;
+        }
+        if (at < whole) {
+          if (lane == 0) atomicMin(&agree, at);
+          whole = at;
+        }
+      }
+    }
+  }
+  __syncthreads();
+  cluster_sync();
+  if (rank == 0 && warp == 0) {
+    int v = lane < kCluster ? from_rank(&agree, lane) : INT32_MAX;
+    v = __reduce_min_sync(0xffffffffu, v);
+    if (lane == 0) p.prefix[g] = v * p.cache.page_size;
+  }
+  cluster_sync();  // (no CTA ends while another reads its shared memory)
+}
+
+// ---- the plan ---------------------------------------------------------------------------------
+
+// One cluster, a warp per group: its record, and its rows' and queries' places.  A row of no group has nothing shared.
+__global__ void __cluster_dims__(kCluster) __launch_bounds__(kThreads) group_plan_kernel(GroupsLaunch p) {
+  const int lane = threadIdx.x & 31;
+  const int me = blockIdx.x * kThreads + threadIdx.x;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  for (int n = me; n < p.rows.num_seqs; n += kCluster * kThreads) p.sh.row_own[n] = 0;
+  cluster_sync();
+  for (int g = me >> 5; g < p.num_groups; g += kCluster * kThreads / 32) {
+    int a, b;
+    if (!group_rows(p, g, a, b, lane == 0 ? p.status : nullptr)) a = b = 0;
+    Rows s = none();
+    for (int n = a + lane; n < b; n += 32) add_row(p, n, s, nullptr);  // (the passes report bad rows)
+    warp_meet(s);
+    int shared = s.count >= 2 ? min(max(load(p.prefix + g), 0), s.least) : 0;
+    shared -= shared % p.cache.page_size;
+    // behind all windows with nothing in front of them: no query sees any of it
+    const int low = p.window > 0 ? max(0, s.least - p.window + 1) : 0;
+    const bool seen = shared > low || (shared > 0 && min(p.sinks, low) > 0);
+    for (int n = a + lane; n < b; n += 32) {
+      KvRow r;
+      if (shared == 0 || !load_kv_row(p.rows, p.cache, n, r, nullptr) || r.len == 0) continue;
+      p.sh.row_own[n] = shared + (seen ? 1 : 0);
+      if (p.window > 0 && seen)
+        for (int t = 0; t < r.len; ++t) p.sh.token_pos[r.bos + t] = r.kv - r.len + t;
+    }
+    if (lane == 0) {
+      GroupRec rec{};
+      if (seen) {
+        rec.bos = s.bos;
+        rec.eos = s.eos;
+        rec.shared = shared;
+        rec.trow = table_row_of(p, s.first);
+        rec.pos_min = s.least;
+      }
+      p.sh.groups[g] = rec;
+    }
+  }
+}
+
+cudaError_t launch_cluster(void (*kernel)(GroupsLaunch), int clusters, const GroupsLaunch& p, cudaStream_t s) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(clusters * kCluster);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+}  // namespace
+
+cudaError_t launch_kv_common_prefix(const GroupsLaunch& p, cudaStream_t s) {
+  return launch_cluster(common_kernel, p.num_groups, p, s);
+}
+
+cudaError_t launch_group_plan(const GroupsLaunch& p, cudaStream_t s) { return launch_cluster(group_plan_kernel, 1, p, s); }
+
+}  // namespace gdn

@@ -1,0 +1,286 @@
+// gdn_kv_rope.cu -- rotary positions: heads turned by their tokens' positions, alone or on their way into the cache.
+//
+// Pair i of a head's first r = rotary_dim values is (x_i, x_{i+r/2}) or (x_2i, x_2i+1); at position p it turns by the
+// angle p f_i.  Frequencies are 64-bit fractions of a turn, so p f_i mod 1 is a product of whole numbers that wraps
+// around: exact to 2^-33 of a turn for every 32-bit position, where a 32-bit product of position and frequency is off by
+// 0.06 at 10^6.  The turn's quarter comes from the top bits, and what is left, at most an eighth of a turn, goes
+// through sincospi in 32 bits: cosine and sine are off by 2^-23 at most.
+//
+// Every value is read and written once, so HBM bounds long calls and the launch short ones.  A block takes a few tokens
+// with all their heads: its threads' values are on their way while it looks up the tokens' rows and pages and works
+// out the tokens' cosines and sines, which all heads share, in shared memory.  A thread reads and writes both values of a
+// pair, so a call may work in place.
+#include <algorithm>
+
+#include "gdn_kv.cuh"
+
+namespace gdn {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kHeld = 4;      // items of a thread whose values are on their way
+constexpr int kTokens = 8;    // of a block, at most: a warp looks up each
+constexpr int kPairs = 136;   // of a head, with those that fill up the last vector
+
+enum Pairs { kHalf, kHalfAny, kInterleaved };  // kHalfAny: halves that 16-byte vectors do not fit
+
+struct TurnParams {
+  TurnLaunch a;
+  int tb;                  // tokens of a block
+  int heads;               // of a token, all kinds
+  int items;               // of a head
+  uint32_t per_token;      // items of a token
+  uint32_t item_magic, token_magic;
+};
+
+// n / by, where magic = 2^32 / by + 1; rest: n % by.
+__device__ __forceinline__ uint32_t divide(uint32_t n, uint32_t by, uint32_t magic, uint32_t& rest) {
+  uint32_t q = by == 1 ? n : __umulhi(n, magic);
+  rest = n - q * by;
+  if ((int32_t)rest < 0) {  // the quotient is one too large at most
+    --q;
+    rest += by;
+  }
+  return q;
+}
+
+// Cosine and sine of pair i at a position, times the magnitude.
+__device__ __forceinline__ float2 turn_of(const TurnLaunch& p, int pair, int pos) {
+  const uint64_t t = load(p.turns + pair) * (uint64_t)(int64_t)pos + 0x80000000u;
+  const uint32_t h = (uint32_t)(t >> 32);  // 2^-32 turns
+  const uint32_t quarter = (h + 0x20000000u) >> 30;
+  float c, s;
+  sincospif((float)(int32_t)(h - (quarter << 30)) * 0x1p-31f, &s, &c);
+  if (quarter & 1) {
+    const float x = c;
+    c = -s;
+    s = x;
+  }
+  if (quarter & 2) {
+    c = -c;
+    s = -s;
+  }
+  return make_float2(c * p.magnitude, s * p.magnitude);
+}
+
+// Where a token's values come from and go to.
+struct Place {
+  int32_t g;     // global token, -1: nothing of it is written
+  int32_t pos;
+  int32_t page;  // 0: its keys and values are not written
+  int32_t slot;
+};
+
+// The row of a local token: the last one that begins at or before it.  32 rows a step; all lanes call together.
+__device__ __forceinline__ int row_of(const KvRowsDev& R, int local) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = R.num_seqs;  // among rows [lo, lo + n), the first of which begins at or before the token
+  while (n > 1) {
+    const int step = (n + 31) / 32, at = lo + lane * step;
+    const bool before = lane == 0 || (lane * step < n && load(R.qsl + at) <= local);
+    const int last = 31 - __clz(__ballot_sync(0xffffffffu, before));
+    lo += last * step;
+    n = min(step, n - last * step);
+  }
+  return lo;
+}
+
+__device__ __forceinline__ Place place_of(const TurnLaunch& p, int local, int32_t g) {
+  const KvDev& C = p.cache;
+  Place w{-1, 0, 0, 0};
+  KvRow r;
+  if (!load_kv_row(p.rows, C, row_of(p.rows, local), r, p.status) || local < r.bos || local >= r.bos + r.len) return w;
+  w.pos = r.kv - r.len + (local - r.bos);
+  w.slot = w.pos & (C.page_size - 1);
+  w.page = page_or_null(load(C.table + (int64_t)r.trow * C.max_pages + w.pos / C.page_size), C, p.status);
+  if (w.page > 0 && C.refcount && load(C.refcount + w.page) > 1) {
+    set_status(p.status, GDN_STATUS_PAGE_SHARED);
+    w.page = 0;
+  }
+  if (g < 0 || g >= p.num_global) {
+    set_status(p.status, GDN_STATUS_TOKEN_RANGE);
+    return w;
+  }
+  w.g = g;
+  return w;
+}
+
+template <typename T>
+struct Vec {
+  static constexpr int kN = 16 / (int)sizeof(T);
+  union {
+    uint4 raw;
+    T v[16 / sizeof(T)];
+  };
+  __device__ Vec() : raw(make_uint4(0, 0, 0, 0)) {}
+};
+
+template <typename T, int PAIRS, bool APPEND>
+__global__ void __launch_bounds__(kThreads, 4) turn_kernel(TurnParams P) {
+  constexpr int VE = 16 / (int)sizeof(T);
+  __shared__ float2 cs[kTokens][kPairs];
+  __shared__ Place places[kTokens];
+  const TurnLaunch& p = P.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int first = blockIdx.x * P.tb, tokens = min(P.tb, p.num_tokens - first);
+  const uint32_t all = tokens * P.per_token;
+  const int half = p.rotary / 2, n = PAIRS == kHalfAny ? half : (half + VE - 1) / VE;
+
+  // An item is two vectors of a head (two values where vectors do not fit): the two of some pairs, or two that stay.
+  struct Item {
+    int t, head, i;
+    bool turns;
+    int a, b;  // first elements
+  };
+  auto item_at = [&](uint32_t at) {
+    Item w;
+    uint32_t rest, i;
+    w.t = (int)divide(at, P.per_token, P.token_magic, rest);
+    w.head = (int)divide(rest, P.items, P.item_magic, i);
+    w.i = (int)i;
+    if (PAIRS == kInterleaved) {
+      w.turns = w.i < n;
+      w.a = w.i * 2 * VE;
+      w.b = w.a + VE;
+    } else {
+      constexpr int E = PAIRS == kHalf ? VE : 1;
+      w.turns = w.i < n;
+      w.a = w.turns ? w.i * E : PAIRS == kHalf ? 2 * half + (w.i - n) * 2 * E : 2 * half + (w.i - n);
+      w.b = w.turns ? w.a + half : w.a + E;
+    }
+    return w;
+  };
+  auto source = [&](const Item& w) {
+    const int local = first + w.t;
+    const int64_t g = APPEND && p.rows.tok ? load(p.rows.tok + local) : local;
+    if (APPEND && (g < 0 || g >= p.num_global)) return static_cast<const T*>(nullptr);
+    if (!APPEND || w.head < p.Hq) return static_cast<const T*>(p.q) + g * p.q_stride + w.head * p.d;
+    const int h = w.head - p.Hq;
+    return h < p.cache.Hkv ? static_cast<const T*>(p.k) + g * p.k_stride + h * p.d
+                           : static_cast<const T*>(p.v) + g * p.v_stride + (h - p.cache.Hkv) * p.d;
+  };
+  auto target = [&](const Item& w, const Place& at) {
+    if (at.g < 0) return static_cast<T*>(nullptr);
+    if (!APPEND || w.head < p.Hq) return static_cast<T*>(p.q_out) + at.g * p.q_out_stride + w.head * p.d;
+    if (at.page == 0) return static_cast<T*>(nullptr);
+    const KvDev& C = p.cache;
+    const int h = w.head - p.Hq;
+    T* pool = static_cast<T*>(h < C.Hkv ? C.k : C.v);
+    return pool + at.page * C.page_stride + ((int64_t)(h < C.Hkv ? h : h - C.Hkv) * C.page_size + at.slot) * p.d;
+  };
+
+  for (uint32_t from = 0; from < all; from += kHeld * kThreads) {
+    Vec<T> a[kHeld], b[kHeld];
+#pragma unroll
+    for (int u = 0; u < kHeld; ++u) {
+      const uint32_t at = from + u * kThreads + tid;
+      if (at >= all) break;
+      const Item w = item_at(at);
+      const T* x = source(w);
+      if (!x) continue;
+      if (PAIRS == kHalfAny) {
+        a[u].v[0] = load(x + w.a);
+        if (w.turns) b[u].v[0] = load(x + w.b);
+      } else {
+        a[u].raw = load(reinterpret_cast<const uint4*>(x + w.a));
+        b[u].raw = load(reinterpret_cast<const uint4*>(x + w.b));
+      }
+    }
+    if (from == 0) {
+      if (APPEND) {
+        if (warp < tokens) {
+          const int local = first + warp;
+          const Place w = place_of(p, local, p.rows.tok ? load(p.rows.tok + local) : local);
+          if (lane == 0) places[warp] = w;
+        }
+      } else if (tid < tokens) {
+        places[tid] = Place{first + tid, load(p.positions + first + tid), 0, 0};
+      }
+      __syncthreads();
+      // pair e of item i stands at [e n + i]: neighbouring items' pairs are neighbours
+      for (int t = 0; t < tokens; ++t)
+        for (int pair = tid; pair < half; pair += kThreads)
+          cs[t][PAIRS == kHalfAny ? pair : pair % VE * n + pair / VE] = turn_of(p, pair, places[t].pos);
+      __syncthreads();
+    }
+#pragma unroll
+    for (int u = 0; u < kHeld; ++u) {
+      const uint32_t at = from + u * kThreads + tid;
+      if (at >= all) break;
+      const Item w = item_at(at);
+      T* out = target(w, places[w.t]);
+      if (!out) continue;
+      const bool turns = w.turns && (!APPEND || w.head < p.Hq + p.cache.Hkv);
+      auto turn = [&](T& x, T& y, float2 f) {
+        const float xf = to_f32(x), yf = to_f32(y);
+        x = from_f32<T>(fmaf(xf, f.x, -yf * f.y));
+        y = from_f32<T>(fmaf(yf, f.x, xf * f.y));
+      };
+      if (PAIRS == kHalfAny) {
+        if (turns) turn(a[u].v[0], b[u].v[0], cs[w.t][w.i]);
+        out[w.a] = a[u].v[0];
+        if (w.turns) out[w.b] = b[u].v[0];
+        continue;
+      }
+      if (turns) {
+#pragma unroll
+        for (int e = 0; e < VE; ++e) {
+          const float2 f = cs[w.t][e * n + w.i];
+          if (PAIRS == kHalf) {
+            turn(a[u].v[e], b[u].v[e], f);
+          } else if (w.i * VE + e < half) {
+            Vec<T>& x = e < VE / 2 ? a[u] : b[u];
+            turn(x.v[2 * (e % (VE / 2))], x.v[2 * (e % (VE / 2)) + 1], f);
+          }
+        }
+      }
+      *reinterpret_cast<uint4*>(out + w.a) = a[u].raw;
+      *reinterpret_cast<uint4*>(out + w.b) = b[u].raw;
+    }
+  }
+}
+
+template <typename T, int PAIRS, bool APPEND>
+cudaError_t launch_pairs(const TurnLaunch& a, cudaStream_t s) {
+  TurnParams P{};
+  P.a = a;
+  P.heads = a.Hq + (APPEND ? 2 * a.cache.Hkv : 0);
+  P.items = PAIRS == kHalfAny ? a.d - a.rotary / 2 : a.d * (int)sizeof(T) / 32;
+  P.per_token = (uint32_t)P.heads * P.items;
+  P.item_magic = (uint32_t)((1ull << 32) / P.items) + 1;
+  P.token_magic = (uint32_t)((1ull << 32) / P.per_token) + 1;
+  // as many tokens as a block holds at once, fewer where that leaves SMs without a block
+  P.tb = std::max(1, std::min(kTokens, kHeld * kThreads / (int)P.per_token));
+  P.tb = std::max(1, std::min(P.tb, a.num_tokens / (2 * kSms)));
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((a.num_tokens + P.tb - 1) / P.tb);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, turn_kernel<T, PAIRS, APPEND>, P);
+}
+
+template <typename T, bool APPEND>
+cudaError_t launch_type(const TurnLaunch& a, cudaStream_t s) {
+  if (a.layout == GDN_ROPE_INTERLEAVED) return launch_pairs<T, kInterleaved, APPEND>(a, s);
+  return a.rotary / 2 * sizeof(T) % 16 == 0 ? launch_pairs<T, kHalf, APPEND>(a, s) : launch_pairs<T, kHalfAny, APPEND>(a, s);
+}
+
+}  // namespace
+
+cudaError_t launch_rope(const TurnLaunch& p, gdn_dtype dtype, cudaStream_t s) {
+  return dtype == GDN_BF16 ? launch_type<__nv_bfloat16, false>(p, s) : launch_type<float, false>(p, s);
+}
+
+cudaError_t launch_kv_append_rope(const TurnLaunch& p, gdn_dtype dtype, cudaStream_t s) {
+  return dtype == GDN_BF16 ? launch_type<__nv_bfloat16, true>(p, s) : launch_type<float, true>(p, s);
+}
+
+}  // namespace gdn

@@ -388,6 +388,122 @@ int gdn_paged_attention(const gdn_attn_desc* attn, const gdn_kv_cache* cache, co
 size_t gdn_attention_workspace_bytes(const gdn_attn_desc* attn, const gdn_kv_cache* cache, const gdn_kv_rows* rows);
 
 /*
+ * Groups of rows that share the beginning of their caches: group g is rows [group_start_loc[g], group_start_loc[g+1]) of
+ * the call.  Its rows hold the same pages in the entries of its first prefix_lens[g] tokens, as gdn_kv_fork leaves them
+ * (lens may be passed on as they are: of a partly filled last page every row has its own copy, and only whole pages
+ * count).  Rows of no group share nothing.
+ */
+typedef struct {
+  int32_t num_groups;             /* 0..65535                                                  */
+  const int32_t* group_start_loc; /* [num_groups+1], ascending, within [0, num_seqs]           */
+  int32_t* prefix_lens;           /* [num_groups] tokens; read, and by gdn_kv_common_prefix written */
+} gdn_kv_groups;
+
+/*
+ * gdn_paged_attention over groups of rows, with every group's shared pages read once for all of its rows.  The result is
+ * gdn_paged_attention's: the same keys are seen, in the same positions, by the same formula; (m, l, sum) over the
+ * shared and over the row's own tokens meet as those of a split row do.
+ * Shared are min(prefix_lens[g], kv_lens[n] - L of the rows with new tokens) tokens, down to whole pages, where at least
+ * two rows of the group have new tokens; prefix_lens <= 0 shares nothing.  They are read by the table row of the
+ * first such row: where the rows' entries differ after all, its pages count.  Rows of one call are in one group at most
+ * (group bounds that do not ascend or leave the rows: GDN_STATUS_ROW_RANGE, that group shares nothing).
+ * bf16 rows of more than 64 queries per kv-head (d = 64, 128, 256; max_query_len decides) go over their whole caches each,
+ * as in gdn_paged_attention: they fill the tensor cores by themselves.
+ * workspace: at least gdn_shared_attention_workspace_bytes(attn, cache, rows, groups) bytes, 256-byte aligned; it holds
+ * the plan, (2 + d) fp32 per query and head, and partial results.
+ */
+int gdn_shared_attention(const gdn_attn_desc* attn, const gdn_kv_cache* cache, const gdn_kv_rows* rows,
+                         const gdn_kv_groups* groups, const void* q, int64_t q_stride, int32_t num_global_tokens, void* out,
+                         int64_t out_stride, void* workspace, size_t workspace_bytes, uint32_t* d_status, void* stream);
+
+/* Depends only on the host-side values of the descriptors and on the device; 0 for invalid descriptors. */
+size_t gdn_shared_attention_workspace_bytes(const gdn_attn_desc* attn, const gdn_kv_cache* cache, const gdn_kv_rows* rows,
+                                            const gdn_kv_groups* groups);
+
+/*
+ * Finds what groups share: prefix_lens[g] = page_size x the largest E for which the rows of group g that have new
+ * tokens agree in their table entries [0, E) (NULL entries agree with one another) and E whole pages lie before the new
+ * tokens of each.  0 for a group without such rows.  Rows that gdn_paged_attention would skip do not count.
+ * The cache's pools are not read, its refcount is not used and may be NULL.
+ */
+int gdn_kv_common_prefix(const gdn_kv_cache* cache, const gdn_kv_rows* rows, const gdn_kv_groups* groups,
+                         uint32_t* d_status, void* stream);
+
+/* ------------------------------------------------------------------------------------------
+ * Rotary positions.
+ *
+ * Pair i < rotary_dim / 2 of a head is (x[i], x[i + rotary_dim/2]) in the half layout and (x[2i], x[2i+1]) in the
+ * interleaved one; at position p it becomes
+ *   (x cos a - y sin a, y cos a + x sin a) * magnitude,   a = p * f_i,
+ * in fp32, rounded once to the dtype; values from rotary_dim on are copied.  A negative position turns back, so the same
+ * call at -p is the transposed map: the gradient of the inputs, and (magnitude 1) the inverse.
+ * Frequencies are 64-bit binary fractions of a turn, so p * f_i is exact to 2^-33 of a turn at every 32-bit position.
+ */
+typedef enum { GDN_ROPE_HALF = 0, GDN_ROPE_INTERLEAVED = 1 } gdn_rope_layout;
+
+typedef struct {
+  const uint64_t* turns; /* device, [rotary_dim/2]: f_i / (2 pi) in units of 2^-64, modulo 1        */
+  int32_t rotary_dim;    /* even, 2..head_dim                                                       */
+  int32_t layout;        /* gdn_rope_layout                                                         */
+  float magnitude;       /* multiplies cosine and sine; 0 selects 1                                 */
+} gdn_rope_desc;
+
+/*
+ * How the frequencies f_i = base^(-2i/rotary_dim) are scaled for contexts longer than the one that was trained on:
+ *   PLAIN   not at all;
+ *   LINEAR  f_i / factor;
+ *   NTK     base * factor^(r/(r-2)) in base's place, r = rotary_dim > 2: the slowest pair as LINEAR, the fastest as PLAIN;
+ *   BANDS   pairs that turn `high` times or more over original_len are kept, those of `low` or fewer are divided by factor,
+ *           and between them w f_i + (1-w) f_i / factor with w linear in the number of turns (0: low 1, high 4);
+ *   RAMP    as BANDS, with w linear in the pair's number between the pair that turns `high` times (rounded down, at least
+ *           0) and the one that turns `low` times (rounded up, at most r-1) (0: low 1, high 32); magnitude 0.1 ln factor + 1.
+ */
+typedef enum {
+  GDN_ROPE_PLAIN = 0,
+  GDN_ROPE_LINEAR = 1,
+  GDN_ROPE_NTK = 2,
+  GDN_ROPE_BANDS = 3,
+  GDN_ROPE_RAMP = 4
+} gdn_rope_scaling;
+
+typedef struct {
+  int32_t rotary_dim;  /* even, 2..256                                 */
+  int32_t scaling;     /* gdn_rope_scaling                             */
+  double base;         /* > 1                                          */
+  double factor;       /* > 0; not used by PLAIN                       */
+  double original_len; /* BANDS, RAMP: > 0                             */
+  double low, high;    /* BANDS, RAMP: 0 < low < high; 0 selects the default */
+} gdn_rope_freq;
+
+/* Host only: writes the rotary_dim/2 fractions for gdn_rope_desc to `turns` (host) and, where not NULL, the magnitude.
+ * gdn_rope_turns_of takes `count` (1..128) frequencies in radians a position instead. */
+int gdn_rope_turns(const gdn_rope_freq* freq, uint64_t* turns, float* magnitude);
+int gdn_rope_turns_of(const double* radians, int32_t count, uint64_t* turns);
+
+/*
+ * Turns the heads of x [num_tokens, num_heads, head_dim] by positions[token] into out (the same shape).  Tokens behind
+ * num_tokens are neither read nor written.  out may be x (with one stride), or other columns of the same wider
+ * tensor; any other overlap is refused (GDN_ERR_SHAPE).
+ *   num_heads 1..65535, head_dim a multiple of 16, <= 256; x_stride, out_stride: elements from one token to the next
+ *   (0 = dense), their bytes a multiple of 16.
+ */
+int gdn_rope(const gdn_rope_desc* rope, int32_t num_heads, int32_t head_dim, gdn_dtype dtype, const int32_t* positions,
+             int32_t num_tokens, const void* x, int64_t x_stride, void* out, int64_t out_stride, void* stream);
+
+/*
+ * gdn_kv_append with the rotation on the way, at the positions that the rows' kv_lens give: the new tokens' keys are
+ * turned into their pages, their values copied, and the q heads of the same tokens turned from q to q_out (which may be q).
+ * Everything that gdn_kv_append says holds; q_out is written for every token of a well-formed row, wherever its page
+ * is.  num_q_heads = 0: keys and values only.
+ *   q, q_out [num_global_tokens, num_q_heads, d], read and written at token_indx; q_out overlaps neither k nor v, and q
+ *   only as in gdn_rope.
+ */
+int gdn_kv_append_rope(const gdn_kv_cache* cache, const gdn_kv_rows* rows, const gdn_rope_desc* rope, const void* k,
+                       int64_t k_stride, const void* v, int64_t v_stride, int32_t num_q_heads, const void* q,
+                       int64_t q_stride, void* q_out, int64_t q_out_stride, int32_t num_global_tokens, uint32_t* d_status,
+                       void* stream);
+
+/*
  * Makes room: for each of the `count` table rows listed, the entries of tokens
  * [from_lens[i], to_lens[i]) that begin a page -- entries ceil(from/page_size) ..
  * ceil(to/page_size)-1 -- and hold no page get a free one (refcount 1).  A row gets all of them
