@@ -1,0 +1,178 @@
+// gdn_attn_parts.cu -- joins what passes over parts of the rows' caches have left of every query.
+//
+// A query's result over one part is whole, or in pieces by the workers that shared its unit; over its group's shared tokens
+// and its row's own ones together: m = max m_i, l = sum l_i e^(m_i - m), out = sum o_i e^(m_i - m) / l, the pieces in a fixed
+// order.  A warp per query, or a team of them where queries are few and their pieces many: a lane per piece for the
+// statistics, then eight pieces' values on their way at a time.
+#include <algorithm>
+
+#include "gdn_attn_share.cuh"
+
+namespace gdn {
+
+namespace {
+
+constexpr int kWarps = 8;
+
+struct JoinParams {
+  AttnLaunch a;
+  PartPieces from[2];  // the pieces of groups' parts and of rows' own
+  int team;            // warps of a query
+};
+
+template <int E>
+__device__ __forceinline__ void load_row(const float* v, bool there, float (&x)[E]) {
+  if constexpr (E == 1) {
+    x[0] = there ? load(v) : 0.f;
+  } else if constexpr (E == 2) {
+    const float2 y = there ? load(reinterpret_cast<const float2*>(v)) : make_float2(0.f, 0.f);
+    x[0] = y.x;
+    x[1] = y.y;
+  } else {
+#pragma unroll
+    for (int e = 0; e < E; e += 4) {
+      const float4 y = there ? load(reinterpret_cast<const float4*>(v + e)) : make_float4(0.f, 0.f, 0.f, 0.f);
+      x[e] = y.x;
+      x[e + 1] = y.y;
+      x[e + 2] = y.z;
+      x[e + 3] = y.w;
+    }
+  }
+}
+
+// E columns of a lane; DC: head_dim where it is 32 E, else 0.
+template <typename T, int E, int DC>
+__global__ void __launch_bounds__(32 * kWarps) join_parts_kernel(JoinParams J) {
+  constexpr int kAtOnce = E <= 4 ? 8 : 4;
+  __shared__ float so[kWarps][32 * E], sl[kWarps], sm[kWarps];
+  const AttnLaunch& p = J.a;
+  const PartDev& part = p.part;
+  const int D = DC > 0 ? DC : p.cache.d;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool columns = DC > 0 || lane * E < D;
+  const float sl2 = p.scale * 1.4426950408889634f;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int64_t all = (int64_t)part.tokens * p.Hq, q = (int64_t)blockIdx.x * (kWarps / J.team) + warp / J.team;
+  const int token = q < all ? (int)(q / p.Hq) : 0;
+  int2 rec = make_int2(-1, 0);
+  PieceRange r[2] = {};
+  int g = -1;
+  if (q < all) {
+    rec = load(part.token + token);
+    g = p.rows.tok ? load(p.rows.tok + token) : token;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const int4 x = load(reinterpret_cast<const int4*>(part.range + s * all + q));
+      r[s] = {x.x, x.y, x.z, 0};
+    }
+  }
+  const bool there = rec.x >= 0 && g >= 0 && g < p.num_global;
+  const int n0 = !there || !rec.y ? 0 : r[0].c0 < 0 ? 1 : r[0].c1 - r[0].c0 + 1;
+  const int n = !there ? 0 : n0 + (r[1].c0 < 0 ? 1 : r[1].c1 - r[1].c0 + 1);
+  float m = -INFINITY, l = 0.f, o[E];
+#pragma unroll
+  for (int i = 0; i < E; ++i) o[i] = 0.f;
+  for (int s0 = warp % J.team; s0 < n; s0 += 32 * J.team) {
+    // a lane per piece: every team-th from s0 on
+    const int i = s0 + lane * J.team, s = i < n0 ? 0 : 1;
+    float2 st = make_float2(-INFINITY, 0.f);
+    const float* values = nullptr;
+    if (i < n) {
+      const PieceRange x = s ? r[1] : r[0];
+      const PartPieces from = s ? J.from[1] : J.from[0];
+      const int c = x.c0 + i - (s ? n0 : 0);
+      const int64_t at = x.c0 < 0 ? s * all + q : (int64_t)(2 * c + (c == x.c0 ? 1 : 0)) * from.queries + x.qi;
+      st = load(reinterpret_cast<const float2*>(x.c0 < 0 ? part.ml : from.stats) + at);
+      values = (x.c0 < 0 ? part.o : from.o) + at * D;
+    }
+    float mn = st.x;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, d));
+    mn = fmaxf(mn, m);
+    const float a = m == -INFINITY ? 0.f : split::ex2((m - mn) * sl2);
+    const float f = st.x == -INFINITY ? 0.f : split::ex2((st.x - mn) * sl2);
+    float sum = st.y * f;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    l = l * a + sum;
+    m = mn;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] *= a;
+    const int mine = min(32, (n - s0 + J.team - 1) / J.team);
+    for (int u0 = 0; u0 < mine; u0 += kAtOnce) {
+      float v[kAtOnce][E];
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) {
+        const uint64_t from = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(values), (u0 + u) & 31);
+        load_row<E>(reinterpret_cast<const float*>(from) + lane * E, u0 + u < mine && columns, v[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) {
+        const float b = __shfl_sync(0xffffffffu, f, (u0 + u) & 31);
+        if (u0 + u < mine) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) o[e] = fmaf(v[u][e], b, o[e]);
+        }
+      }
+    }
+  }
+  if (J.team > 1) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) so[warp][lane + 32 * e] = o[e];
+    if (lane == 0) {
+      sm[warp] = m;
+      sl[warp] = l;
+    }
+    __syncthreads();
+    if (warp % J.team) return;
+    for (int v = warp + 1; v < warp + J.team; ++v) {
+      const float mn = fmaxf(m, sm[v]);
+      const float a = m == -INFINITY ? 0.f : split::ex2((m - mn) * sl2);
+      const float b = sm[v] == -INFINITY ? 0.f : split::ex2((sm[v] - mn) * sl2);
+      l = l * a + sl[v] * b;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = o[e] * a + so[v][lane + 32 * e] * b;
+      m = mn;
+    }
+  }
+  if (!there || !columns) return;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  T* out = static_cast<T*>(p.out) + (int64_t)g * p.out_stride + (q - (int64_t)token * p.Hq) * D + lane * E;
+#pragma unroll
+  for (int e = 0; e < E; ++e) out[e] = from_f32<T>(o[e] * inv);
+}
+
+template <typename T, int E, int DC>
+cudaError_t launch_as(JoinParams& J, cudaStream_t s) {
+  const int64_t queries = (int64_t)J.a.part.tokens * J.a.Hq;
+  J.team = queries <= 2 * kSms * kWarps ? 8 : 1;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  const int per = kWarps / J.team;
+  cfg.gridDim = dim3((unsigned)((queries + per - 1) / per));
+  cfg.blockDim = dim3(32 * kWarps);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, join_parts_kernel<T, E, DC>, J);
+}
+template <typename T>
+cudaError_t launch_type(JoinParams& J, cudaStream_t s) {
+  const int d = J.a.cache.d;
+  if (d == 64) return launch_as<T, 2, 64>(J, s);
+  if (d == 128) return launch_as<T, 4, 128>(J, s);
+  if (d == 256) return launch_as<T, 8, 256>(J, s);
+  return d < 64 ? launch_as<T, 2, 0>(J, s) : d < 128 ? launch_as<T, 4, 0>(J, s) : launch_as<T, 8, 0>(J, s);
+}
+
+}  // namespace
+
+cudaError_t launch_join_parts(const AttnLaunch& p, gdn_dtype dtype, PartPieces groups, PartPieces rows, cudaStream_t s) {
+  JoinParams J{p, {groups, rows}, 1};
+  return dtype == GDN_BF16 ? launch_type<__nv_bfloat16>(J, s) : launch_type<float>(J, s);
+}
+
+}  // namespace gdn

@@ -6,9 +6,9 @@
 // is not the whole unit leaves (m, l, o) in the workspace; join_kernel adds a unit's pieces in the order of the
 // workers.
 //
-// The same goes for the passes over a part of the rows' caches: in that over shared prefixes a group of rows takes a
-// row's place, with its queries one after the other, and what comes out is every query's (m, l, o); in that over the
-// rows' own tokens, tiles begin at the first of them and a unit's first piece begins from that state.
+// PART: a pass over parts of the rows' caches, listed as PartRec: a group's queries over what its rows share, a row's over
+// its own tokens.  Every query's (m, l, o) over its part comes out, whole or in pieces, and where they are; the join of
+// parts (gdn_attn_parts.cu) makes the outputs.
 #pragma once
 
 #include <algorithm>
@@ -37,83 +37,81 @@ struct SplitParams {
 struct Unit {
   KvRow r;
   int sink_tiles, first_tile, tiles;
-  int per;  // units of the row
-  int own;  // kTail: the row's first own token, + 1 with a state; kShared: the lowest position of the group's queries
-  __device__ int cost() const { return tiles > 0 ? tiles + kStart : 0; }
+  int per;       // units of the row
+  int from, lo;  // PART: the part's first token, the lowest position of a query
+  __device__ int cost(int start) const { return tiles > 0 ? tiles + start : 0; }
 };
 
-// A row's values as they lie in memory.
-template <Part PART>
+// A row's values as they lie in memory; with PART, a part's.
+template <bool PART>
 struct RawRow {
   int bos, eos, kv, trow;
-  int own;  // as in Unit
 };
 template <>
-struct RawRow<kWhole> {
-  int bos, eos, kv, trow;
+struct RawRow<true> {
+  int bos, len, from, end, trow, lo;
 };
-template <Part PART>
+template <bool PART>
 __device__ __forceinline__ int rows_of(const AttnLaunch& p) {
-  return PART == kShared ? p.sh.num_groups : p.rows.num_seqs;
+  return PART ? p.part.count : p.rows.num_seqs;
 }
-template <Part PART>
+template <bool PART>
 __device__ __forceinline__ RawRow<PART> raw_row(const AttnLaunch& p, int n) {
-  if constexpr (PART == kShared) {
-    const GroupRec* g = p.sh.groups + n;
-    return {load(&g->bos), load(&g->eos), load(&g->shared), load(&g->trow), load(&g->pos_min)};
+  if constexpr (PART) {
+    const int4* rec = reinterpret_cast<const int4*>(p.part.recs + n);
+    const int4 a = load(rec), b = load(rec + 1);
+    return {a.x, a.y, a.z, a.w, b.x, b.y};
   } else {
-    RawRow<PART> r;
-    r.bos = load(p.rows.qsl + n);
-    r.eos = load(p.rows.qsl + n + 1);
-    r.kv = load(p.rows.kv_lens + n);
-    r.trow = p.rows.table_rows ? load(p.rows.table_rows + n) : n;
-    if constexpr (PART == kTail) r.own = load(p.sh.row_own + n);
-    return r;
+    return {load(p.rows.qsl + n), load(p.rows.qsl + n + 1), load(p.rows.kv_lens + n),
+            p.rows.table_rows ? load(p.rows.table_rows + n) : n};
   }
+}
+template <bool PART>
+__device__ __forceinline__ RawRow<PART> raw_of_lane(const RawRow<PART>& r, int src) {
+  RawRow<PART> x;
+  int* to = reinterpret_cast<int*>(&x);
+  const int* from = reinterpret_cast<const int*>(&r);
+#pragma unroll
+  for (int i = 0; i < (int)(sizeof(x) / 4); ++i) to[i] = __shfl_sync(0xffffffffu, from[i], src);
+  return x;
 }
 
 // The tiles that the row's queries see; 0 for an empty or bad row.  QG: queries of a unit, 0 for all
 // of a row and kv-head.
-template <int QG, Part PART>
+template <int QG, bool PART, int TN>
 __device__ __forceinline__ Unit unit_of(const AttnLaunch& p, const RawRow<PART>& r, uint32_t* st) {
   Unit u;
   u.tiles = u.sink_tiles = u.first_tile = 0;
   u.per = p.cache.Hkv;
-  if constexpr (PART == kShared) {
-    u.r = KvRow{r.bos, r.eos - r.bos, r.kv, r.trow};  // (of no tokens where nothing is shared)
-    u.own = r.own;
-    if (u.r.len == 0) return u;
-    const int low = p.window > 0 ? min(max(0, r.own - p.window + 1), r.kv) : 0;
-    u.sink_tiles = (min(p.sinks, low) + kTN - 1) / kTN;
-    u.first_tile = max(low / kTN, u.sink_tiles);
-    u.tiles = u.sink_tiles + max((r.kv + kTN - 1) / kTN - u.first_tile, 0);
-    u.per *= (int)(((int64_t)u.r.len * p.G + QG - 1) / (QG > 0 ? QG : 1));
+  if constexpr (PART) {
+    u.r = KvRow{r.bos, r.len, r.end, r.trow};
+    u.from = r.from;
+    u.lo = r.lo;
+    if (r.len == 0) return u;
+    const int tokens = r.end - r.from;
+    const int low = p.window > 0 ? min(max(max(0, r.lo - p.window + 1) - r.from, 0), tokens) : 0;
+    u.sink_tiles = (min(max(p.sinks - r.from, 0), low) + TN - 1) / TN;
+    u.first_tile = max(low / TN, u.sink_tiles);
+    u.tiles = u.sink_tiles + max((tokens + TN - 1) / TN - u.first_tile, 0);
+    u.per *= (int)(((int64_t)r.len * p.G + QG - 1) / QG);
     return u;
-  }
-  if (!check_kv_row(p.rows, p.cache, r.bos, r.eos, r.kv, r.trow, u.r, st) || u.r.len == 0 ||
-      (p.few > 0 && u.r.len * p.G > p.few))
-    return u;
-  if constexpr (PART == kTail) {
-    u.own = r.own;
-    const int from = r.own & ~1;  // (the plan leaves it at or below the row's first new token)
-    const int low = p.window > 0 ? max(0, u.r.kv - u.r.len - p.window + 1 - from) : 0;
-    u.sink_tiles = (min(max(p.sinks - from, 0), low) + kTN - 1) / kTN;
-    u.first_tile = max(low / kTN, u.sink_tiles);
-    u.tiles = u.sink_tiles + (u.r.kv - from + kTN - 1) / kTN - u.first_tile;
   } else {
+    if (!check_kv_row(p.rows, p.cache, r.bos, r.eos, r.kv, r.trow, u.r, st) || u.r.len == 0 ||
+        (p.few > 0 && u.r.len * p.G > p.few))
+      return u;
     const int low = p.window > 0 ? max(0, u.r.kv - u.r.len - p.window + 1) : 0;
     u.sink_tiles = (min(p.sinks, low) + kTN - 1) / kTN;
     u.first_tile = max(low / kTN, u.sink_tiles);
     u.tiles = u.sink_tiles + (u.r.kv + kTN - 1) / kTN - u.first_tile;
+    if (QG > 0) u.per *= (u.r.len * p.G + QG - 1) / (QG > 0 ? QG : 1);
+    return u;
   }
-  if (QG > 0) u.per *= (u.r.len * p.G + QG - 1) / (QG > 0 ? QG : 1);
-  return u;
 }
 // The cost in tiles of all units of row n.
-template <int QG, Part PART>
+template <int QG, bool PART, int TN, int START>
 __device__ __forceinline__ int64_t row_cost(const AttnLaunch& p, int n, uint32_t* st) {
-  const Unit u = unit_of<QG, PART>(p, raw_row<PART>(p, n), st);
-  return (int64_t)u.cost() * u.per;
+  const Unit u = unit_of<QG, PART, TN>(p, raw_row<PART>(p, n), st);
+  return (int64_t)u.cost(START) * u.per;
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -139,22 +137,23 @@ __device__ __forceinline__ int Deal::owner(int64_t tile) const {
 }
 
 // A worker's share of the tiles, and where it begins.
-template <Part PART>
+template <bool PART>
 struct Share {
-  int64_t first, last;
+  int64_t first;
   int64_t into;  // tiles of row `row` before the share
   int row;
+  int span;      // tiles
   RawRow<PART> raw;  // that row
 };
 
 // The shares of the CTA's workers; part: one value per warp.  All threads call.
-template <int QG, int NW, int THREADS, Part PART = kWhole>
+template <int QG, int NW, int THREADS, bool PART = false, int TN = kTN, int START = kStart>
 __device__ void find_shares(const AttnLaunch& p, int64_t* part, Deal& deal, Share<PART>* shares) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rows = rows_of<PART>(p), per = (rows + THREADS - 1) / THREADS;
   const int n0 = min(tid * per, rows), n1 = min(n0 + per, rows);
   int64_t mine = 0;
-  for (int n = n0; n < n1; ++n) mine += row_cost<QG, PART>(p, n, blockIdx.x == 0 ? p.status : nullptr);
+  for (int n = n0; n < n1; ++n) mine += row_cost<QG, PART, TN, START>(p, n, blockIdx.x == 0 ? p.status : nullptr);
   int64_t inc = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -178,18 +177,18 @@ __device__ void find_shares(const AttnLaunch& p, int64_t* part, Deal& deal, Shar
   for (int w = 0; w < NW; ++w) {
     Share<PART> s;
     s.first = d.first(blockIdx.x * NW + w);
-    s.last = d.first(blockIdx.x * NW + w + 1);
+    s.span = (int)(d.first(blockIdx.x * NW + w + 1) - s.first);
     s.row = 0;
     s.into = 0;
     s.raw = RawRow<PART>{};
-    if (s.first == s.last) {
+    if (s.span == 0) {
       if (tid == 0) shares[w] = s;
     } else if (s.first >= before && s.first < before + mine) {  // one thread
       int64_t at = before;
       int n = n0;
       if (per > 1) {
         for (; n < n1; ++n) {
-          const int64_t t = row_cost<QG, PART>(p, n, nullptr);
+          const int64_t t = row_cost<QG, PART, TN, START>(p, n, nullptr);
           if (s.first < at + t) break;
           at += t;
         }
@@ -207,18 +206,18 @@ __device__ void find_shares(const AttnLaunch& p, int64_t* part, Deal& deal, Shar
 // Walks the units of a share: (row, unit of the row, tiles [j0, j0 + len) of the unit).  A warp holds the raw
 // values of the next 32 rows, one per lane, so that going on to the next row waits for no memory.
 // All lanes call together.
-template <int QG, Part PART = kWhole>
+template <int QG, bool PART = false, int TN = kTN, int START = kStart>
 struct Walk {
   const AttnLaunch& p;
-  int64_t left;
+  int left;
   int n, h, j0, len;  // h: unit of the row
   Unit u;
-  __device__ Walk(const AttnLaunch& launch, const Share<PART>& s) : p(launch), left(s.last - s.first), n(s.row), len(0) {
+  __device__ Walk(const AttnLaunch& launch, const Share<PART>& s) : p(launch), left(s.span), n(s.row), len(0) {
     if (left <= 0) return;
     fill(n + 1);
-    u = unit_of<QG, PART>(p, s.raw, nullptr);
-    h = (int)quotient(s.into, u.cost());
-    piece((int)(s.into - (int64_t)h * u.cost()));
+    u = unit_of<QG, PART, TN>(p, s.raw, nullptr);
+    h = (int)quotient(s.into, u.cost(START));
+    piece((int)(s.into - (int64_t)h * u.cost(START)));
   }
   __device__ bool valid() const { return left > 0; }
   __device__ void next() {
@@ -232,32 +231,25 @@ struct Walk {
           return;
         }
         if (n == base + 32) fill(n);
-        const int src = n - base;
-        RawRow<PART> r;
-        r.bos = __shfl_sync(0xffffffffu, ahead.bos, src);
-        r.eos = __shfl_sync(0xffffffffu, ahead.eos, src);
-        r.kv = __shfl_sync(0xffffffffu, ahead.kv, src);
-        r.trow = __shfl_sync(0xffffffffu, ahead.trow, src);
-        if constexpr (PART != kWhole) r.own = __shfl_sync(0xffffffffu, ahead.own, src);
-        u = unit_of<QG, PART>(p, r, nullptr);
+        u = unit_of<QG, PART, TN>(p, raw_of_lane<PART>(ahead, n - base), nullptr);
       } while (u.tiles == 0);
     }
     piece(0);
   }
   __device__ int tile_at(int j) const {
-    const int at = (j < u.sink_tiles ? j : u.first_tile + j - u.sink_tiles) * kTN;
-    return PART == kTail ? (u.own & ~1) + at : at;
+    const int at = (j < u.sink_tiles ? j : u.first_tile + j - u.sink_tiles) * TN;
+    return PART ? u.from + at : at;
   }
   // Where the unit ends in the deal.
-  __device__ int64_t unit_last(const Share<PART>& s) const { return s.last - left - from + u.cost() - 1; }
+  __device__ int64_t unit_last(const Share<PART>& s) const { return s.first + s.span - left - from + u.cost(START) - 1; }
 
  private:
   int from, span;  // the piece in the unit's tiles with those that stand for its beginning
   __device__ void piece(int at) {
     from = at;
-    span = (int)min((int64_t)(u.cost() - at), left);
-    j0 = max(at - kStart, 0);
-    len = at + span - kStart - j0;
+    span = min(u.cost(START) - at, left);
+    j0 = max(at - START, 0);
+    len = at + span - START - j0;
     if (len <= 0) left = 0;  // the share ends before the unit's first tile
   }
   int base;
@@ -275,8 +267,8 @@ struct Walk {
 inline int join_rows(int workers, int queries) {
   return std::max((queries + kJoinWarps - 1) / kJoinWarps, std::min(queries, std::min(kJoinWarps, kJoinBlocks / workers)));
 }
-// E: 32 E columns or fewer are worked on; DC: head_dim, 0 for that of the cache; STATE: the queries' (m, l, o) come out.
-template <typename T, int E, int DC, bool STATE = false>
+// E: 32 E columns or fewer are worked on; DC: head_dim, 0 for that of the cache.
+template <typename T, int E, int DC>
 __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(SplitParams P, int queries) {
   __shared__ float so[kJoinWarps][32 * E];
   __shared__ float sl[kJoinWarps], sm[kJoinWarps];
@@ -361,14 +353,6 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(SplitParams P, in
       }
       if (qi >= nq || warp % team) continue;
       const int t = (qi0 + qi) / p.G;
-      if constexpr (STATE) {
-        const int64_t at = (int64_t)(bos + t) * p.Hq + h * p.G + qi0 + qi - t * p.G;
-        if (lane == 0) *reinterpret_cast<float2*>(p.sh.state_ml + at * 2) = make_float2(m, l);
-#pragma unroll
-        for (int i = 0; i < E; ++i)
-          if (DC > 0 || lane + 32 * i < D) p.sh.state_o[at * D + lane + 32 * i] = o[i];
-        continue;
-      }
       const int g = p.rows.tok ? load(p.rows.tok + bos + t) : bos + t;
       if (g < 0 || g >= p.num_global) continue;
       const float inv = l == 0.f ? 0.f : 1.f / l;

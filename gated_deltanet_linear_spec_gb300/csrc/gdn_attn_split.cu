@@ -151,7 +151,7 @@ __device__ __forceinline__ void values_step(float (&o)[DV / 8][4], const uint32_
 }
 
 // What a CTA keeps in shared memory behind its rings and queries.
-template <typename C, Part PART>
+template <typename C, bool PART>
 struct Small {
   struct Worker {
     uint64_t full[C::kStages], empty[C::kStages], qfull, qempty;
@@ -162,13 +162,12 @@ struct Small {
   Share<PART> shares[C::kWorkers];
 };
 
-// PART (see gdn_attn_share.cuh): kShared takes units of kNQ of a group's queries and leaves their states, kTail begins
-// from those.
-template <int D, int WQ, int DS, int NW, Part PART = kWhole>
+// PART: a pass over parts (see gdn_attn_share.cuh), in units of up to kNQ queries.
+template <int D, int WQ, int DS, int NW, bool PART = false>
 __global__ void __launch_bounds__(Cfg<D, WQ, DS, NW>::kThreads, 1)
     split_kernel(SplitParams P, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
   using C = Cfg<D, WQ, DS, NW>;
-  constexpr int S = C::kStages, DV = C::kDV, QG = PART == kShared ? C::kNQ : 0;
+  constexpr int S = C::kStages, DV = C::kDV, QG = PART ? C::kNQ : 0;
   extern __shared__ __align__(1024) uint8_t smem[];
   Small<C, PART>& small = *reinterpret_cast<Small<C, PART>*>(smem + NW * (C::kRing + C::kQ));
   const AttnLaunch& p = P.a;
@@ -193,7 +192,7 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, NW>::kThreads, 1)
     tc::prefetch_map(&vmap);
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");  // what lies before this overlaps the kernel before this one
-  if (tid < NW) P.info[(blockIdx.x * NW + tid) * 8] = 0;
+  if (!PART && tid < NW) P.info[(blockIdx.x * NW + tid) * 8] = 0;
   // (the sums of find_shares lie where the first worker's ring will be)
   find_shares<QG, NW, C::kThreads, PART>(p, reinterpret_cast<int64_t*>(smem), small.deal, small.shares);
   const bool fetches = warp >= NW * C::kTeam;
@@ -215,7 +214,7 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, NW>::kThreads, 1)
     int it = 0, seg = 0;
     bool ok = true;
     for (Walk<QG, PART> w(p, share); w.valid() && ok; w.next(), ++seg) {
-      const int h = PART == kShared ? w.h % kv.Hkv : w.h, q0 = PART == kShared ? w.h / kv.Hkv * QG : 0;
+      const int h = PART ? w.h % kv.Hkv : w.h, q0 = PART ? w.h / kv.Hkv * QG : 0;
       // 32 table entries are held, one per lane, and the 32 behind them are on their way
       const int32_t* row = kv.table + (int64_t)w.u.r.trow * kv.max_pages;
       const int entries = (w.u.r.kv + ps - 1) >> shift;
@@ -223,7 +222,7 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, NW>::kThreads, 1)
       int ids = eb + lane < entries ? load(row + eb + lane) : 0;
       int ahead = eb + 32 + lane < entries ? load(row + eb + 32 + lane) : 0;
       // the unit's queries
-      const int nq = PART == kShared ? min(QG, w.u.r.len * p.G - q0) : w.u.r.len * p.G;
+      const int nq = PART ? min(QG, w.u.r.len * p.G - q0) : w.u.r.len * p.G;
       int g[2];
       int rows = 0;
 #pragma unroll
@@ -300,10 +299,10 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, NW>::kThreads, 1)
   bool ok = true;
   for (Walk<QG, PART> w(p, share); w.valid(); w.next(), ++seg) {
     const KvRow row = w.u.r;
-    const int h = PART == kShared ? w.h % kv.Hkv : w.h, q0 = PART == kShared ? w.h / kv.Hkv * QG : 0;
-    const int nq = PART == kShared ? min(QG, row.len * p.G - q0) : row.len * p.G;
+    const int h = PART ? w.h % kv.Hkv : w.h, q0 = PART ? w.h / kv.Hkv * QG : 0;
+    const int nq = PART ? min(QG, row.len * p.G - q0) : row.len * p.G;
     // tokens up to `seen` are seen by all queries, but for the window; up to `end` by some
-    const int seen = PART == kShared ? row.kv - 1 : row.kv - row.len, end = row.kv - 1;
+    const int end = row.kv - 1, seen = PART ? min(w.u.lo, end) : row.kv - row.len;
     float o[DV / 8][4], m[2], l[2];
     int pos[2];  // the positions of this thread's two queries, r8 and r8 + 8 of the group's 16
 #pragma unroll
@@ -313,28 +312,11 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, NW>::kThreads, 1)
       m[e] = -INFINITY;
       l[e] = 0.f;
       const int qi = wq * 16 + r8 + 8 * e;
-      if constexpr (PART == kShared) {
-        pos[e] = p.window > 0 && qi < nq ? load(p.sh.token_pos + row.bos + (q0 + qi) / p.G) : end;
-      } else {
-        pos[e] = min(seen + qi / p.G, end);
-      }
-      if constexpr (PART == kTail) {
-        if (w.j0 == 0 && (w.u.own & 1) && qi < nq) {  // the state over the shared tokens
-          const int64_t at = (int64_t)(row.bos + qi / p.G) * p.Hq + h * p.G + qi % p.G;
-          const float2 ml = load(reinterpret_cast<const float2*>(p.sh.state_ml) + at);
-          m[e] = ml.x;
-          l[e] = c2 == 0 ? ml.y : 0.f;  // (the four threads of a query add their sums up at the end)
-          const float* from = p.sh.state_o + at * D + ds * DV + c2;
-#pragma unroll
-          for (int i = 0; i < DV / 8; ++i) {
-            const float2 x = load(reinterpret_cast<const float2*>(from + i * 8));
-            o[i][2 * e] = x.x;
-            o[i][2 * e + 1] = x.y;
-          }
-        }
-      }
+      pos[e] = min(PART ? w.u.lo + (q0 + qi) / p.G : seen + qi / p.G, end);
+      // (without a window it does not matter how far behind a group's part its queries stand)
+      if (PART && p.window > 0 && qi < nq) pos[e] = load(&p.part.token[row.bos + (q0 + qi) / p.G].x);
     }
-    const int pmax = PART == kShared ? __reduce_max_sync(0xffffffffu, max(pos[0], pos[1])) : end;
+    const int pmax = PART ? __reduce_max_sync(0xffffffffu, max(pos[0], pos[1])) : end;
     ok = __all_sync(0xffffffffu, ok && tc::mbar_wait(&sm.qfull, seg & 1, P.wait_ns));
     const uint32_t qbase =
         tc::smem_addr(qbuf) + (wq * 16 + (lane & 15)) * C::kPitch + (lane >> 4) * 16;
@@ -380,7 +362,7 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, NW>::kThreads, 1)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const int tok = b + n * 8 + c2 + (e & 1), at = pos[e >> 1];
-              const bool sees = tok <= at && (PART != kShared || tok <= end) &&
+              const bool sees = tok <= at && (!PART || tok <= end) &&
                                 (p.window <= 0 || tok > at - p.window || tok < p.sinks) && (n < 2 ? have0 : have1);
               if (!sees) sc[n][e] = -INFINITY;
             }
@@ -452,16 +434,24 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, NW>::kThreads, 1)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int qi = wq * 16 + r8 + 8 * e;
-        const int g = sm.qtok[qi];
-        if (PART == kShared && whole) {
+        if constexpr (PART) {
           if (qi >= nq) continue;
-          const int64_t at = (int64_t)(row.bos + (q0 + qi) / p.G) * p.Hq + h * p.G + (q0 + qi) % p.G;
-          float* to = p.sh.state_o + at * D + ds * DV + c2;
+          const int64_t place = ((int64_t)(w.n < p.part.groups ? 0 : p.part.tokens) + row.bos + (q0 + qi) / p.G) * p.Hq +
+                                h * p.G + (q0 + qi) % p.G;
+          const int64_t at = whole ? place : (int64_t)slot * C::kNQ + qi;
+          float* to = (whole ? p.part.o : P.part) + at * D + ds * DV + c2;
 #pragma unroll
           for (int i = 0; i < DV / 8; ++i)
             *reinterpret_cast<float2*>(to + i * 8) = make_float2(o[i][2 * e], o[i][2 * e + 1]);
-          if (ds == 0 && c2 == 0) *reinterpret_cast<float2*>(p.sh.state_ml + at * 2) = make_float2(m[e], l[e]);
-        } else if (whole && g >= 0) {
+          if (ds == 0 && c2 == 0) {
+            *reinterpret_cast<float2*>((whole ? p.part.ml : P.stats) + at * 2) = make_float2(m[e], l[e]);
+            if (w.j0 == 0)
+              p.part.range[place] = {whole ? -1 : (int)blockIdx.x * NW + wk, small.deal.owner(w.unit_last(share)), qi, 0};
+          }
+          continue;
+        }
+        const int g = sm.qtok[qi];
+        if (whole && g >= 0) {
           const float f = l[e] == 0.f ? 0.f : 1.f / l[e];
           __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + (int64_t)g * p.out_stride +
                                (int64_t)(h * p.G + qi % p.G) * D + ds * DV + c2;
@@ -477,12 +467,12 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, NW>::kThreads, 1)
             *reinterpret_cast<float2*>(P.stats + ((size_t)slot * C::kNQ + qi) * 2) = make_float2(m[e], l[e]);
         }
       }
-      if (!whole && w.j0 == 0 && wq == 0 && ds == 0 && lane == 0) {
+      if (!PART && !whole && w.j0 == 0 && wq == 0 && ds == 0 && lane == 0) {
         int32_t* info = P.info + (blockIdx.x * NW + wk) * 8;
         info[1] = row.bos;
         info[2] = nq;
         info[3] = h;
-        info[5] = q0;
+        info[5] = 0;
         info[4] = small.deal.owner(w.unit_last(share));  // the worker with the unit's last tile
         info[0] = 1;
       }
@@ -493,13 +483,11 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, NW>::kThreads, 1)
 }
 
 // Queries of a unit, at most (with max_q = 0 every row is a bad one, and reported).
-template <Part PART = kWhole>
 int64_t queries_of(const AttnLaunch& a) {
-  if (PART == kShared) return std::min<int64_t>(64, (int64_t)a.rows.num_tokens * a.G);
   return a.few > 0 ? a.few : std::max<int64_t>(1, (int64_t)a.rows.max_q * a.G);
 }
 
-template <Part PART, int D, int WQ, int DS, int NW>
+template <bool PART, int D, int WQ, int DS, int NW>
 cudaError_t launch_cfg(const AttnLaunch& a, cudaStream_t s) {
   using C = Cfg<D, WQ, DS, NW>;
   static std::atomic<uint64_t> done{0};
@@ -528,11 +516,11 @@ cudaError_t launch_cfg(const AttnLaunch& a, cudaStream_t s) {
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if ((e = cudaLaunchKernelEx(&cfg, split_kernel<D, WQ, DS, NW, PART>, P, kmap, vmap)) != cudaSuccess) return e;
-  cfg.gridDim = dim3(kSms * NW, join_rows(kSms * NW, (int)queries_of<PART>(a)));
+  if ((e = cudaLaunchKernelEx(&cfg, split_kernel<D, WQ, DS, NW, PART>, P, kmap, vmap)) != cudaSuccess || PART) return e;
+  cfg.gridDim = dim3(kSms * NW, join_rows(kSms * NW, (int)queries_of(a)));
   cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, join_kernel<__nv_bfloat16, D / 32, D, PART == kShared>, P, (int)C::kNQ);
+  return cudaLaunchKernelEx(&cfg, join_kernel<__nv_bfloat16, D / 32, D>, P, (int)C::kNQ);
 }
 
 int query_slots(int64_t queries) { return queries <= 16 ? 16 : queries <= 32 ? 32 : 64; }
@@ -570,28 +558,40 @@ auto pick(int d, int slots, F f) {
   return slots == 16 ? f(Cfg<256, 1, 2, 2>{}) : slots == 32 ? f(Cfg<256, 2, 2, 2>{}) : f(Cfg<256, 4, 2, 1>{});
 }
 
-template <Part PART, int D, int WQ, int DS, int NW>
+template <bool PART, int D, int WQ, int DS, int NW>
 cudaError_t launch_picked(Cfg<D, WQ, DS, NW>, const AttnLaunch& a, cudaStream_t s) {
   return launch_cfg<PART, D, WQ, DS, NW>(a, s);
 }
-template <Part PART>
-cudaError_t launch_part(const AttnLaunch& a, cudaStream_t s) {
-  return pick(a.cache.d, query_slots(queries_of<PART>(a)), [&](auto c) { return launch_picked<PART>(c, a, s); });
-}
-template <Part PART>
-size_t workspace_of(const AttnLaunch& a) {
-  const int q = query_slots(queries_of<PART>(a));
+
+size_t workspace_of(const AttnLaunch& a, int q) {
   const size_t workers = (size_t)kSms * pick(a.cache.d, q, [](auto c) { return decltype(c)::kWorkers; });
   return workers * (8 + 4 * (size_t)q + 2 * (size_t)q * a.cache.d) * 4;
 }
 
+// Queries of a unit of a pass over parts: those of a group may be those of all rows.
+int part_slots(const AttnLaunch& a) {
+  const int64_t most = (int64_t)(a.part.groups > 0 ? a.rows.num_tokens : a.rows.max_q) * a.G;
+  return query_slots(std::max<int64_t>(most, 1));
+}
+
 }  // namespace
 
-size_t attn_split_workspace(const AttnLaunch& a) { return workspace_of<kWhole>(a); }
-size_t attn_split_shared_workspace(const AttnLaunch& a) { return workspace_of<kShared>(a); }
+size_t attn_split_workspace(const AttnLaunch& a) { return workspace_of(a, query_slots(queries_of(a))); }
 
-cudaError_t launch_attn_split(const AttnLaunch& a, cudaStream_t s) { return launch_part<kWhole>(a, s); }
-cudaError_t launch_attn_split_shared(const AttnLaunch& a, cudaStream_t s) { return launch_part<kShared>(a, s); }
-cudaError_t launch_attn_split_own(const AttnLaunch& a, cudaStream_t s) { return launch_part<kTail>(a, s); }
+cudaError_t launch_attn_split(const AttnLaunch& a, cudaStream_t s) {
+  return pick(a.cache.d, query_slots(queries_of(a)), [&](auto c) { return launch_picked<false>(c, a, s); });
+}
+
+size_t attn_split_parts_workspace(const AttnLaunch& a) { return workspace_of(a, part_slots(a)); }
+
+PartPieces attn_split_parts_pieces(const AttnLaunch& a, void* ws) {
+  const int q = part_slots(a), workers = kSms * pick(a.cache.d, q, [](auto c) { return decltype(c)::kWorkers; });
+  float* stats = static_cast<float*>(ws) + 8 * workers;
+  return {stats, stats + (size_t)4 * workers * q, q};
+}
+
+cudaError_t launch_attn_split_parts(const AttnLaunch& a, cudaStream_t s) {
+  return pick(a.cache.d, part_slots(a), [&](auto c) { return launch_picked<true>(c, a, s); });
+}
 
 }  // namespace gdn

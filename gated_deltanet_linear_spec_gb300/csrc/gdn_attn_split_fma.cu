@@ -83,8 +83,8 @@ __device__ __forceinline__ void load_row(const __nv_bfloat16* v, bool there, flo
 }
 
 // E: columns of a lane, 32 E are head_dim or more; DC: head_dim where it is 32 E, else 0.
-// PART: see gdn_attn_share.cuh.
-template <typename T, int E, int DC, Part PART = kWhole>
+// PART: a pass over parts (see gdn_attn_share.cuh).
+template <typename T, int E, int DC, bool PART = false>
 __global__ void __launch_bounds__(32 * kWarps, kPerSm) split_fma_kernel(SplitParams P) {
   constexpr int kU = E <= 4 ? 8 : 4;  // tokens whose keys or values a lane holds at a time
   constexpr int kC = 32 / kU;         // as many chunks of keys, then as many of values
@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) split_fma_kernel(SplitPar
   const bool columns = DC > 0 || lane * E < D;  // this lane has some
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (lane == 0) P.info[worker * 8] = 0;
+  if (!PART && lane == 0) P.info[worker * 8] = 0;
   find_shares<kNQ, kWarps, 32 * kWarps, PART>(p, part, deal, shares);
   const Share<PART>& share = shares[warp];
   const float sl2 = p.scale * 1.4426950408889634f;
@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) split_fma_kernel(SplitPar
   for (Walk<kNQ, PART> w(p, share); w.valid(); w.next()) {
     const KvRow row = w.u.r;
     const int h = w.h % kv.Hkv, q0 = w.h / kv.Hkv * kNQ, nq = min(kNQ, row.len * p.G - q0);
-    const int first = row.kv - row.len;  // position of the first new token
+    const int first = PART ? w.u.lo : row.kv - row.len;  // position of the first new token, or the lowest of a query
     int g = -1;                          // lane i < nq: the query's global token
     if (lane < nq) g = kv_token(p.rows, row.bos + (q0 + lane) / p.G, p.num_global, p.status);
     float q[kNQ][E];
@@ -119,33 +119,18 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) split_fma_kernel(SplitPar
       const T* from = static_cast<const T*>(p.q) + (int64_t)max(gi, 0) * p.q_stride;
       load_row<E>(from + (int64_t)(h * p.G + (q0 + i) % p.G) * D + lane * E, columns && gi >= 0, q[i]);
     }
-    // the lowest position of a query, and the last token that some query sees
-    const int pos0 = PART == kShared ? w.u.own : first + q0 / p.G;
-    const int pos1 = PART == kShared ? row.kv - 1 : first + (q0 + nq - 1) / p.G;
+    // the lowest position of a query of the unit, and the last token that one sees
+    const int pos0 = PART && p.window > 0 ? first : first + q0 / p.G;
+    const int pos1 = PART ? min(p.window > 0 ? INT32_MAX : first + (q0 + nq - 1) / p.G, row.kv - 1) : first + (q0 + nq - 1) / p.G;
     const int mine = lane >> 2;  // the query whose scores, maximum and sum this lane has, those of every 4th token
     int pos = min(first + (q0 + mine) / p.G, pos1);
-    if constexpr (PART == kShared)
-      pos = p.window > 0 && mine < nq ? load(p.sh.token_pos + row.bos + (q0 + mine) / p.G) : pos1;
+    // (without a window it does not matter how far behind a group's part its queries stand)
+    if (PART && p.window > 0 && mine < nq) pos = load(&p.part.token[row.bos + (q0 + mine) / p.G].x);
     float o[kNQ][E], m = -INFINITY, l = 0.f;
-    const auto state_of = [&](int i) {  // of query i
-      return (int64_t)(row.bos + (q0 + i) / p.G) * p.Hq + h * p.G + (q0 + i) % p.G;
-    };
 #pragma unroll
     for (int i = 0; i < kNQ; ++i)
 #pragma unroll
       for (int e = 0; e < E; ++e) o[i][e] = 0.f;
-    if constexpr (PART == kTail) {
-      if (w.j0 == 0 && (w.u.own & 1)) {  // the states over the shared tokens
-        if (mine < nq) {
-          const float2 ml = load(reinterpret_cast<const float2*>(p.sh.state_ml) + state_of(mine));
-          m = ml.x;
-          l = (lane & 3) == 0 ? ml.y : 0.f;  // (the four lanes of a query add their sums up at the end)
-        }
-#pragma unroll
-        for (int i = 0; i < kNQ; ++i)
-          if (columns && i < nq) load_row<E>(p.sh.state_o + state_of(i) * D + lane * E, true, o[i]);
-      }
-    }
     const int32_t* table = kv.table + (int64_t)row.trow * kv.max_pages;
     auto entry = [&](int j) {  // the table's entry of this lane's token of tile j
       const int tok = w.tile_at(j) + lane;
@@ -211,7 +196,7 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) split_fma_kernel(SplitPar
 #pragma unroll
       for (int n = 0; n < 8; ++n) {
         const int t = 4 * n + (lane & 3), tk = b + t;
-        const bool sees = (seen >> t & 1u) && tk <= pos && (PART != kShared || tk <= pos1) && (p.window <= 0 || tk > pos - p.window || tk < p.sinks);
+        const bool sees = (seen >> t & 1u) && tk <= pos && (!PART || tk <= pos1) && (p.window <= 0 || tk > pos - p.window || tk < p.sinks);
         if (!sees) s[n] = -INFINITY;
         x_max = fmaxf(x_max, s[n]);
       }
@@ -271,18 +256,32 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) split_fma_kernel(SplitPar
     l += __shfl_xor_sync(0xffffffffu, l, 2);
     const bool whole = w.j0 == 0 && w.len == w.u.tiles;
     const int slot = 2 * worker + (w.j0 == 0 ? 1 : 0);
+    if constexpr (PART) {
+      const int last = deal.owner(w.unit_last(share));
+#pragma unroll
+      for (int i = 0; i < kNQ; ++i) {
+        const float li = __shfl_sync(0xffffffffu, l, 4 * i), mi = __shfl_sync(0xffffffffu, m, 4 * i);
+        if (i >= nq) continue;
+        const int64_t place = ((int64_t)(w.n < p.part.groups ? 0 : p.part.tokens) + row.bos + (q0 + i) / p.G) * p.Hq + h * p.G +
+                              (q0 + i) % p.G;
+        const int64_t at = whole ? place : (int64_t)slot * kNQ + i;
+        float* dst = (whole ? p.part.o : P.part) + at * D + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          if (columns) dst[e] = o[i][e];
+        if (lane == 0) {
+          *reinterpret_cast<float2*>((whole ? p.part.ml : P.stats) + at * 2) = make_float2(mi, li);
+          if (w.j0 == 0) p.part.range[place] = {whole ? -1 : worker, last, i, 0};
+        }
+      }
+      continue;
+    }
 #pragma unroll
     for (int i = 0; i < kNQ; ++i) {
       const float li = __shfl_sync(0xffffffffu, l, 4 * i), mi = __shfl_sync(0xffffffffu, m, 4 * i);
       const int gi = __shfl_sync(0xffffffffu, g, i);
       if (i >= nq) continue;
-      if (PART == kShared && whole) {
-        float* dst = p.sh.state_o + state_of(i) * D + lane * E;
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-          if (columns) dst[e] = o[i][e];
-        if (lane == 0) *reinterpret_cast<float2*>(p.sh.state_ml + state_of(i) * 2) = make_float2(mi, li);
-      } else if (whole) {
+      if (whole) {
         if (gi < 0) continue;
         const float inv = li == 0.f ? 0.f : 1.f / li;
         T* out = static_cast<T*>(p.out) + (int64_t)gi * p.out_stride + (int64_t)(h * p.G + (q0 + i) % p.G) * D;
@@ -310,7 +309,7 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) split_fma_kernel(SplitPar
   }
 }
 
-template <Part PART, typename T, int E, int DC>
+template <bool PART, typename T, int E, int DC>
 cudaError_t launch_as(const AttnLaunch& a, cudaStream_t s) {
   constexpr int ctas = kSms * kPerSm;
   SplitParams P{};
@@ -328,22 +327,21 @@ cudaError_t launch_as(const AttnLaunch& a, cudaStream_t s) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cudaError_t e = cudaLaunchKernelEx(&cfg, split_fma_kernel<T, E, DC, PART>, P);
-  if (e != cudaSuccess) return e;
-  const int most = PART == kShared ? a.rows.num_tokens : a.rows.max_q;
-  const int queries = (int)std::min<int64_t>(kNQ, std::max<int64_t>(1, (int64_t)most * a.G));
+  if (e != cudaSuccess || PART) return e;
+  const int queries = (int)std::min<int64_t>(kNQ, std::max<int64_t>(1, (int64_t)a.rows.max_q * a.G));
   cfg.gridDim = dim3(ctas * kWarps, join_rows(ctas * kWarps, queries));
   cfg.blockDim = dim3(32 * kJoinWarps);
-  return cudaLaunchKernelEx(&cfg, join_kernel<T, E, DC, PART == kShared>, P, kNQ);
+  return cudaLaunchKernelEx(&cfg, join_kernel<T, E, DC>, P, kNQ);
 }
-template <Part PART, typename T>
+template <bool PART, typename T>
 cudaError_t launch_any(const AttnLaunch& a, cudaStream_t s) {
   const int d = a.cache.d;
   return d <= 64    ? launch_as<PART, T, 2, 0>(a, s)
          : d <= 128 ? launch_as<PART, T, 4, 0>(a, s)
                     : launch_as<PART, T, 8, 0>(a, s);
 }
-template <Part PART>
-cudaError_t launch_part(const AttnLaunch& a, gdn_dtype dtype, cudaStream_t s) {
+template <bool PART>
+cudaError_t launch_type(const AttnLaunch& a, gdn_dtype dtype, cudaStream_t s) {
   if (dtype == GDN_BF16) return launch_any<PART, __nv_bfloat16>(a, s);
   switch (a.cache.d) {
     case 32: return launch_as<PART, float, 1, 32>(a, s);
@@ -361,13 +359,19 @@ size_t attn_split_fma_workspace(const AttnLaunch& a) {
 }
 
 cudaError_t launch_attn_split_fma(const AttnLaunch& a, gdn_dtype dtype, cudaStream_t s) {
-  return launch_part<kWhole>(a, dtype, s);
+  return launch_type<false>(a, dtype, s);
 }
-cudaError_t launch_attn_split_fma_shared(const AttnLaunch& a, gdn_dtype dtype, cudaStream_t s) {
-  return launch_part<kShared>(a, dtype, s);
+
+size_t attn_split_fma_parts_workspace(const AttnLaunch& a) { return attn_split_fma_workspace(a); }
+
+PartPieces attn_split_fma_parts_pieces(const AttnLaunch& a, void* ws) {
+  constexpr int workers = kSms * kPerSm * kWarps;
+  float* stats = static_cast<float*>(ws) + 8 * workers;
+  return {stats, stats + (size_t)4 * workers * kNQ, kNQ};
 }
-cudaError_t launch_attn_split_fma_own(const AttnLaunch& a, gdn_dtype dtype, cudaStream_t s) {
-  return launch_part<kTail>(a, dtype, s);
+
+cudaError_t launch_attn_split_fma_parts(const AttnLaunch& a, gdn_dtype dtype, cudaStream_t s) {
+  return launch_type<true>(a, dtype, s);
 }
 
 }  // namespace gdn

@@ -93,27 +93,33 @@ struct AppendLaunch {
   uint32_t* status;
 };
 
-// Which part of a row's cache a pass of attention goes over: all of it; what the rows of a group share, for the queries of
-// all of them; or a row's own, beginning from what the pass over the shared part has left.
-enum Part { kWhole, kShared, kTail };
-
-// A group of rows that share a prefix, as the passes see it (written on the device).
-struct GroupRec {
-  int32_t bos, eos;        // its rows' local tokens
-  int32_t shared;          // tokens of the prefix, whole pages
-  int32_t trow;            // the row of the block table that they are read by
-  int32_t pos_min;         // the lowest position of a query
-  int32_t pad[3];
+// One entry of a pass over parts of the rows' caches: what a group's queries share, or what a row has of its own.  Written on
+// the device, groups first.
+struct PartRec {
+  int32_t bos, len;    // local tokens, whose queries of a kv-head go together; len 0: nothing to do
+  int32_t from, end;   // cached tokens; from is a multiple of the page size
+  int32_t trow;        // row of the block table
+  int32_t lo, hi;      // lowest and highest position of a query
+  int32_t pad;
 };
 
-// What the passes over shared prefixes and own tokens hand on.
-struct SharedDev {
-  GroupRec* groups;    // [num_groups]
-  int32_t* row_own;    // [num_seqs] first own token of a row (a multiple of 16); + 1: its queries have a state
-  int32_t* token_pos;  // [num_tokens] position of a local token, written under a window only
-  float* state_ml;     // [num_tokens][Hq][2]: m (of the scores before their scale), l
-  float* state_o;      // [num_tokens][Hq][d]
-  int32_t num_groups;
+// Where the pieces of a query's result over one part are: of the workers c0 to c1, the qi-th query of their unit; c0 < 0: one
+// piece, in the query's own place.
+struct PieceRange {
+  int32_t c0, c1, qi, pad;
+};
+
+// A pass over parts, and where it leaves (m, l, o) of its pieces.  Queries are numbered (local token, q-head), those of groups'
+// parts first, then those of rows' own.
+struct PartDev {
+  const PartRec* recs;
+  int32_t count;        // of this pass
+  int32_t groups;       // of them, those that are groups' (the first)
+  int32_t tokens;       // local tokens of the call
+  const int2* token;    // [tokens]: position (-1: of no well-formed row), whether its row shares a prefix
+  PieceRange* range;    // [2][tokens][Hq]
+  float* ml;            // [2][tokens][Hq][2]: m (of the scores before their scale), l of a query in one piece
+  float* o;             // [2][tokens][Hq][d]
 };
 
 struct AttnLaunch {
@@ -130,7 +136,7 @@ struct AttnLaunch {
   int32_t few;     // > 0: rows of up to so many queries per kv-head are the split kernel's, others the prompt one's
   void* ws;
   uint32_t* status;
-  SharedDev sh;    // of the passes over shared and own parts
+  PartDev part;    // of passes over parts
 };
 
 // Heads turned by their tokens' positions, alone or on their way into the cache.
@@ -161,7 +167,8 @@ struct GroupsLaunch {
   int32_t* prefix;  // [num_groups] shared tokens, read or written
   int32_t num_groups;
   int32_t window, sinks;
-  SharedDev sh;
+  PartRec* recs;    // the plan's: [num_groups + num_seqs]
+  int2* token;      // [num_tokens]
   uint32_t* status;
 };
 
@@ -221,13 +228,21 @@ cudaError_t launch_attn_prompt(const AttnLaunch& p, cudaStream_t s);
 size_t attn_split_fma_workspace(const AttnLaunch& p);
 cudaError_t launch_attn_split_fma(const AttnLaunch& p, gdn_dtype dtype, cudaStream_t s);
 
-// Groups of rows over shared prefixes: the plan, and the passes over the shared and the own parts.
+// Groups of rows over shared prefixes: the plan of their parts, passes over parts, and the join of what those leave.
 cudaError_t launch_kv_common_prefix(const GroupsLaunch& p, cudaStream_t s);
 cudaError_t launch_group_plan(const GroupsLaunch& p, cudaStream_t s);
-size_t attn_split_shared_workspace(const AttnLaunch& p);
-cudaError_t launch_attn_split_shared(const AttnLaunch& p, cudaStream_t s);
-cudaError_t launch_attn_split_own(const AttnLaunch& p, cudaStream_t s);
-cudaError_t launch_attn_split_fma_shared(const AttnLaunch& p, gdn_dtype dtype, cudaStream_t s);
-cudaError_t launch_attn_split_fma_own(const AttnLaunch& p, gdn_dtype dtype, cudaStream_t s);
+// Where a pass leaves its pieces: [2 * workers][queries of a unit], (m, l) and o.
+struct PartPieces {
+  float* stats;
+  float* o;
+  int32_t queries;
+};
+size_t attn_split_parts_workspace(const AttnLaunch& p);
+PartPieces attn_split_parts_pieces(const AttnLaunch& p, void* ws);
+cudaError_t launch_attn_split_parts(const AttnLaunch& p, cudaStream_t s);
+size_t attn_split_fma_parts_workspace(const AttnLaunch& p);
+PartPieces attn_split_fma_parts_pieces(const AttnLaunch& p, void* ws);
+cudaError_t launch_attn_split_fma_parts(const AttnLaunch& p, gdn_dtype dtype, cudaStream_t s);
+cudaError_t launch_join_parts(const AttnLaunch& p, gdn_dtype dtype, PartPieces groups, PartPieces rows, cudaStream_t s);
 
 }  // namespace gdn

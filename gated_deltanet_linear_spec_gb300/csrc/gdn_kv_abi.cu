@@ -240,24 +240,29 @@ bool shares(const AttnLaunch& p, gdn_dtype dtype) {
   return attn_split_supported(p, dtype) || !attn_prompt_supported(p, dtype);
 }
 
-// The workspace of attention over groups: the plan, the queries' states, and what the larger of the two passes takes.
+// The workspace of attention over groups: the plan's parts and tokens, where queries' pieces are, results in one piece, and the
+// pass's own.
 struct SharedWs {
-  size_t groups, row_own, token_pos, ml, o, pass, end;
+  size_t recs, token, range, ml, o, pass, end;
 };
-SharedWs shared_ws(const AttnLaunch& p, int32_t num_groups, gdn_dtype dtype) {
+SharedWs shared_ws(const AttnLaunch& p, gdn_dtype dtype) {
   SharedWs w{};
-  const size_t tokens = p.rows.num_tokens, queries = tokens * p.Hq;
-  w.groups = 0;
-  w.row_own = round256(w.groups + (size_t)num_groups * sizeof(GroupRec));
-  w.token_pos = round256(w.row_own + (size_t)p.rows.num_seqs * 4);
-  w.ml = round256(w.token_pos + (p.window > 0 ? tokens * 4 : 0));
+  const size_t tokens = p.rows.num_tokens, queries = 2 * tokens * p.Hq;
+  w.recs = 0;
+  w.token = round256(w.recs + (size_t)p.part.count * sizeof(PartRec));
+  w.range = round256(w.token + tokens * sizeof(int2));
+  w.ml = round256(w.range + queries * sizeof(PieceRange));
   w.o = round256(w.ml + queries * 8);
   w.pass = round256(w.o + queries * p.cache.d * 4);
   const bool split = attn_split_supported(p, dtype);
-  const size_t shared = split ? attn_split_shared_workspace(p) : attn_split_fma_workspace(p);
-  const size_t own = split ? attn_split_workspace(p) : attn_split_fma_workspace(p);
-  w.end = w.pass + round256(shared > own ? shared : own);
+  w.end = w.pass + round256(split ? attn_split_parts_workspace(p) : attn_split_fma_parts_workspace(p));
   return w;
+}
+// The parts of all groups and rows in one pass.
+void all_parts(AttnLaunch& p, int32_t num_groups) {
+  p.part.groups = num_groups;
+  p.part.count = num_groups + p.rows.num_seqs;
+  p.part.tokens = p.rows.num_tokens;
 }
 
 GroupsLaunch groups_args(const gdn_kv_cache* c, const gdn_kv_rows* r, const gdn_kv_groups* g, uint32_t* status) {
@@ -444,9 +449,10 @@ size_t gdn_shared_attention_workspace_bytes(const gdn_attn_desc* attn, const gdn
   if (check_groups(groups)) return 0;
   const size_t whole = gdn_attention_workspace_bytes(attn, cache, rows);
   if (check_shape(cache) || check_table(cache) || check_attn(attn, cache) || check_kv_rows(rows)) return 0;
-  const AttnLaunch p = attn_args(attn, cache, rows);
+  AttnLaunch p = attn_args(attn, cache, rows);
   if (rows->num_tokens == 0 || groups->num_groups == 0 || !shares(p, cache->dtype)) return whole;
-  return shared_ws(p, groups->num_groups, cache->dtype).end;
+  all_parts(p, groups->num_groups);
+  return shared_ws(p, cache->dtype).end;
 }
 
 int gdn_shared_attention(const gdn_attn_desc* attn, const gdn_kv_cache* cache, const gdn_kv_rows* rows,
@@ -461,27 +467,31 @@ int gdn_shared_attention(const gdn_attn_desc* attn, const gdn_kv_cache* cache, c
                            need, d_status, p)))
     return rc;
   if (groups->num_groups == 0 || !shares(p, cache->dtype)) return attend_whole(p, cache->dtype, (cudaStream_t)stream);
-  const SharedWs w = shared_ws(p, groups->num_groups, cache->dtype);
+  all_parts(p, groups->num_groups);
+  const SharedWs w = shared_ws(p, cache->dtype);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  p.sh.groups = reinterpret_cast<GroupRec*>(ws + w.groups);
-  p.sh.row_own = reinterpret_cast<int32_t*>(ws + w.row_own);
-  p.sh.token_pos = reinterpret_cast<int32_t*>(ws + w.token_pos);
-  p.sh.state_ml = reinterpret_cast<float*>(ws + w.ml);
-  p.sh.state_o = reinterpret_cast<float*>(ws + w.o);
-  p.sh.num_groups = groups->num_groups;
-  p.ws = ws + w.pass;
   GroupsLaunch plan = groups_args(cache, rows, groups, d_status);
   plan.window = p.window;
   plan.sinks = p.sinks;
-  plan.sh = p.sh;
+  plan.recs = reinterpret_cast<PartRec*>(ws + w.recs);
+  plan.token = reinterpret_cast<int2*>(ws + w.token);
+  p.part.recs = plan.recs;
+  p.part.token = plan.token;
+  p.part.range = reinterpret_cast<PieceRange*>(ws + w.range);
+  p.part.ml = reinterpret_cast<float*>(ws + w.ml);
+  p.part.o = reinterpret_cast<float*>(ws + w.o);
+  p.ws = ws + w.pass;
   const cudaStream_t s = (cudaStream_t)stream;
   if ((rc = cuda_rc(launch_group_plan(plan, s)))) return rc;
+  PartPieces pieces;
   if (attn_split_supported(p, cache->dtype)) {
-    if ((rc = cuda_rc(launch_attn_split_shared(p, s)))) return rc;
-    return cuda_rc(launch_attn_split_own(p, s));
+    pieces = attn_split_parts_pieces(p, p.ws);
+    rc = cuda_rc(launch_attn_split_parts(p, s));
+  } else {
+    pieces = attn_split_fma_parts_pieces(p, p.ws);
+    rc = cuda_rc(launch_attn_split_fma_parts(p, cache->dtype, s));
   }
-  if ((rc = cuda_rc(launch_attn_split_fma_shared(p, cache->dtype, s)))) return rc;
-  return cuda_rc(launch_attn_split_fma_own(p, cache->dtype, s));
+  return rc ? rc : cuda_rc(launch_join_parts(p, cache->dtype, pieces, pieces, s));
 }
 
 int gdn_kv_common_prefix(const gdn_kv_cache* cache, const gdn_kv_rows* rows, const gdn_kv_groups* groups,

@@ -44,6 +44,7 @@ struct Rows {
   int first;           // the first of them
   int least;           // tokens before the new ones, of the row that has fewest
   int bos, eos;        // their local tokens
+  int pos_max;         // the highest position of a query (the lowest is `least`)
 };
 __device__ __forceinline__ void add_row(const GroupsLaunch& p, int n, Rows& s, uint32_t* st) {
   KvRow r;
@@ -53,14 +54,16 @@ __device__ __forceinline__ void add_row(const GroupsLaunch& p, int n, Rows& s, u
   s.least = min(s.least, r.kv - r.len);
   s.bos = min(s.bos, r.bos);
   s.eos = max(s.eos, r.bos + r.len);
+  s.pos_max = max(s.pos_max, r.kv - 1);
 }
-__device__ __forceinline__ Rows none() { return Rows{0, INT32_MAX, INT32_MAX, INT32_MAX, 0}; }
+__device__ __forceinline__ Rows none() { return Rows{0, INT32_MAX, INT32_MAX, INT32_MAX, 0, 0}; }
 __device__ __forceinline__ void warp_meet(Rows& s) {
   s.count = __reduce_add_sync(0xffffffffu, s.count);
   s.first = __reduce_min_sync(0xffffffffu, s.first);
   s.least = __reduce_min_sync(0xffffffffu, s.least);
   s.bos = __reduce_min_sync(0xffffffffu, s.bos);
   s.eos = __reduce_max_sync(0xffffffffu, s.eos);
+  s.pos_max = __reduce_max_sync(0xffffffffu, s.pos_max);
 }
 
 // ---- common prefix ----------------------------------------------------------------------------
@@ -139,42 +142,55 @@ __global__ void __cluster_dims__(kCluster) __launch_bounds__(kThreads) common_ke
 
 // ---- the plan ---------------------------------------------------------------------------------
 
-// One cluster, a warp per group: its record, and its rows' and queries' places.  A row of no group has nothing shared.
+// A row's new tokens, each with its position: a lane per row takes them one by one, which does for verify rows; the
+// caller's lanes take long rows' together.
+__device__ __forceinline__ void place_tokens(int2* token, const KvRow& r, int from, int step, int shares) {
+  for (int t = from; t < r.len; t += step) token[r.bos + t] = make_int2(r.kv - r.len + t, shares);
+}
+
+// One cluster: the parts of rows, a thread (or, where rows may be long, a warp) each, then those of groups, a warp each, which
+// move the beginnings of their rows' own parts.
 __global__ void __cluster_dims__(kCluster) __launch_bounds__(kThreads) group_plan_kernel(GroupsLaunch p) {
+  constexpr int kAll = kCluster * kThreads;
   const int lane = threadIdx.x & 31;
   const int me = blockIdx.x * kThreads + threadIdx.x;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  for (int n = me; n < p.rows.num_seqs; n += kCluster * kThreads) p.sh.row_own[n] = 0;
+  for (int i = me; i < p.rows.num_tokens; i += kAll) p.token[i] = make_int2(-1, 0);
   cluster_sync();
-  for (int g = me >> 5; g < p.num_groups; g += kCluster * kThreads / 32) {
+  const bool lanes = p.rows.max_q > 64;  // a row's tokens go to a warp's lanes
+  for (int n = lanes ? me >> 5 : me; n < p.rows.num_seqs; n += lanes ? kAll / 32 : kAll) {
+    KvRow r;
+    PartRec rec{};
+    if (load_kv_row(p.rows, p.cache, n, r, p.status) && r.len > 0) {
+      rec = {r.bos, r.len, 0, r.kv, r.trow, r.kv - r.len, r.kv - 1, 0};
+      place_tokens(p.token, r, lanes ? lane : 0, lanes ? 32 : 1, 0);
+    }
+    if (!lanes || lane == 0) p.recs[p.num_groups + n] = rec;
+  }
+  cluster_sync();
+  for (int g = me >> 5; g < p.num_groups; g += kAll / 32) {
     int a, b;
     if (!group_rows(p, g, a, b, lane == 0 ? p.status : nullptr)) a = b = 0;
     Rows s = none();
-    for (int n = a + lane; n < b; n += 32) add_row(p, n, s, nullptr);  // (the passes report bad rows)
+    for (int n = a + lane; n < b; n += 32) add_row(p, n, s, nullptr);
     warp_meet(s);
     int shared = s.count >= 2 ? min(max(load(p.prefix + g), 0), s.least) : 0;
     shared -= shared % p.cache.page_size;
-    // behind all windows with nothing in front of them: no query sees any of it
+    // behind all windows, with nothing in front that stays visible, no query sees any of it
     const int low = p.window > 0 ? max(0, s.least - p.window + 1) : 0;
     const bool seen = shared > low || (shared > 0 && min(p.sinks, low) > 0);
-    for (int n = a + lane; n < b; n += 32) {
+    for (int i = a; shared > 0 && i < b; i += lanes ? 1 : 32) {
+      const int n = lanes ? i : i + lane;
       KvRow r;
-      if (shared == 0 || !load_kv_row(p.rows, p.cache, n, r, nullptr) || r.len == 0) continue;
-      p.sh.row_own[n] = shared + (seen ? 1 : 0);
-      if (p.window > 0 && seen)
-        for (int t = 0; t < r.len; ++t) p.sh.token_pos[r.bos + t] = r.kv - r.len + t;
+      if (n >= b || !load_kv_row(p.rows, p.cache, n, r, nullptr) || r.len == 0) continue;
+      if (!lanes || lane == 0) p.recs[p.num_groups + n].from = shared;
+      if (seen) place_tokens(p.token, r, lanes ? lane : 0, lanes ? 32 : 1, 1);
     }
     if (lane == 0) {
-      GroupRec rec{};
-      if (seen) {
-        rec.bos = s.bos;
-        rec.eos = s.eos;
-        rec.shared = shared;
-        rec.trow = table_row_of(p, s.first);
-        rec.pos_min = s.least;
-      }
-      p.sh.groups[g] = rec;
+      PartRec rec{};
+      if (seen) rec = {s.bos, s.eos - s.bos, 0, shared, table_row_of(p, s.first), s.least, s.pos_max, 0};
+      p.recs[g] = rec;
     }
   }
 }
