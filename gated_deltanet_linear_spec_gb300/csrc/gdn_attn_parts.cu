@@ -17,6 +17,7 @@ constexpr int kWarps = 8;
 struct JoinParams {
   AttnLaunch a;
   PartPieces from[2];  // the pieces of groups' parts and of rows' own
+  float down[2];       // log2 of what brings each to the lower scale of the two
   int team;            // warps of a query
 };
 
@@ -91,7 +92,7 @@ __global__ void __launch_bounds__(32 * kWarps) join_parts_kernel(JoinParams J) {
     for (int d = 16; d; d >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, d));
     mn = fmaxf(mn, m);
     const float a = m == -INFINITY ? 0.f : split::ex2((m - mn) * sl2);
-    const float f = st.x == -INFINITY ? 0.f : split::ex2((st.x - mn) * sl2);
+    const float f = st.x == -INFINITY ? 0.f : split::ex2(fmaf(st.x - mn, sl2, s ? J.down[1] : J.down[0]));
     float sum = st.y * f;
 #pragma unroll
     for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
@@ -171,7 +172,8 @@ cudaError_t launch_type(JoinParams& J, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_join_parts(const AttnLaunch& p, gdn_dtype dtype, PartPieces groups, PartPieces rows, cudaStream_t s) {
-  JoinParams J{p, {groups, rows}, 1};
+  const float low = std::min(groups.shift, rows.shift);
+  JoinParams J{p, {groups, rows}, {low - groups.shift, low - rows.shift}, 1};
   return dtype == GDN_BF16 ? launch_type<__nv_bfloat16>(J, s) : launch_type<float>(J, s);
 }
 

@@ -191,7 +191,9 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, NW>::kThreads, 1)
     tc::prefetch_map(&kmap);
     tc::prefetch_map(&vmap);
   }
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // what lies before this overlaps the kernel before this one
+  // What lies before this overlaps the kernel before this one.  (A pass over rows' own parts behind that over groups' takes
+  // nothing from it, and waits for it at its end.)
+  if (!PART || !p.part.behind) asm volatile("griddepcontrol.wait;" ::: "memory");
   if (!PART && tid < NW) P.info[(blockIdx.x * NW + tid) * 8] = 0;
   // (the sums of find_shares lie where the first worker's ring will be)
   find_shares<QG, NW, C::kThreads, PART>(p, reinterpret_cast<int64_t*>(smem), small.deal, small.shares);
@@ -287,6 +289,7 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, NW>::kThreads, 1)
     for (int i = max(0, it - S); i < it; ++i) ok &= tc::mbar_wait(&sm.full[i % S], (i / S) & 1, P.wait_ns);
     if (seg > 0) ok &= tc::mbar_wait(&sm.qfull, (seg - 1) & 1, P.wait_ns);
     if (!ok) set_status(p.status, GDN_STATUS_WAIT_TIMEOUT);
+    if (PART && p.part.behind) asm volatile("griddepcontrol.wait;" ::: "memory");
     return;
   }
 
@@ -587,7 +590,7 @@ size_t attn_split_parts_workspace(const AttnLaunch& a) { return workspace_of(a, 
 PartPieces attn_split_parts_pieces(const AttnLaunch& a, void* ws) {
   const int q = part_slots(a), workers = kSms * pick(a.cache.d, q, [](auto c) { return decltype(c)::kWorkers; });
   float* stats = static_cast<float*>(ws) + 8 * workers;
-  return {stats, stats + (size_t)4 * workers * q, q};
+  return {stats, stats + (size_t)4 * workers * q, q, 0.f};
 }
 
 cudaError_t launch_attn_split_parts(const AttnLaunch& a, cudaStream_t s) {

@@ -120,6 +120,7 @@ struct PartDev {
   PieceRange* range;    // [2][tokens][Hq]
   float* ml;            // [2][tokens][Hq][2]: m (of the scores before their scale), l of a query in one piece
   float* o;             // [2][tokens][Hq][d]
+  int32_t behind;       // this pass's inputs are complete when it may start, and the pass before it need not be
 };
 
 struct AttnLaunch {
@@ -236,7 +237,11 @@ struct PartPieces {
   float* stats;
   float* o;
   int32_t queries;
+  float shift;  // log2 of what weights are scaled by: (l, o) are sums of 2^shift e^(s - m)
 };
+size_t attn_shared_workspace(const AttnLaunch& p);  // groups' parts on tcgen05
+PartPieces attn_shared_pieces(const AttnLaunch& p, void* ws);
+cudaError_t launch_attn_shared(const AttnLaunch& p, cudaStream_t s);
 size_t attn_split_parts_workspace(const AttnLaunch& p);
 PartPieces attn_split_parts_pieces(const AttnLaunch& p, void* ws);
 cudaError_t launch_attn_split_parts(const AttnLaunch& p, cudaStream_t s);

@@ -243,8 +243,13 @@ bool shares(const AttnLaunch& p, gdn_dtype dtype) {
 // The workspace of attention over groups: the plan's parts and tokens, where queries' pieces are, results in one piece, and the
 // pass's own.
 struct SharedWs {
-  size_t recs, token, range, ml, o, pass, end;
+  size_t recs, token, range, ml, o, shared, pass, end;
 };
+// Whether groups' queries go over the shared tokens on the tensor cores, apart from the rows' own parts: more of them than the
+// split kernel's units hold.
+bool apart(const AttnLaunch& p, gdn_dtype dtype) {
+  return attn_split_supported(p, dtype) && (int64_t)p.rows.num_tokens * p.G > 64;
+}
 SharedWs shared_ws(const AttnLaunch& p, gdn_dtype dtype) {
   SharedWs w{};
   const size_t tokens = p.rows.num_tokens, queries = 2 * tokens * p.Hq;
@@ -253,9 +258,12 @@ SharedWs shared_ws(const AttnLaunch& p, gdn_dtype dtype) {
   w.range = round256(w.token + tokens * sizeof(int2));
   w.ml = round256(w.range + queries * sizeof(PieceRange));
   w.o = round256(w.ml + queries * 8);
-  w.pass = round256(w.o + queries * p.cache.d * 4);
+  w.shared = round256(w.o + queries * p.cache.d * 4);
+  w.pass = w.shared + (apart(p, dtype) ? round256(attn_shared_workspace(p)) : 0);
+  AttnLaunch last = p;  // the pass that is not apart
+  if (apart(p, dtype)) last.part.groups = 0;
   const bool split = attn_split_supported(p, dtype);
-  w.end = w.pass + round256(split ? attn_split_parts_workspace(p) : attn_split_fma_parts_workspace(p));
+  w.end = w.pass + round256(split ? attn_split_parts_workspace(last) : attn_split_fma_parts_workspace(last));
   return w;
 }
 // The parts of all groups and rows in one pass.
@@ -480,10 +488,20 @@ int gdn_shared_attention(const gdn_attn_desc* attn, const gdn_kv_cache* cache, c
   p.part.range = reinterpret_cast<PieceRange*>(ws + w.range);
   p.part.ml = reinterpret_cast<float*>(ws + w.ml);
   p.part.o = reinterpret_cast<float*>(ws + w.o);
-  p.ws = ws + w.pass;
   const cudaStream_t s = (cudaStream_t)stream;
   if ((rc = cuda_rc(launch_group_plan(plan, s)))) return rc;
-  PartPieces pieces;
+  PartPieces shared, pieces;
+  if (apart(p, cache->dtype)) {
+    p.part.count = groups->num_groups;
+    p.ws = ws + w.shared;
+    shared = attn_shared_pieces(p, p.ws);
+    if ((rc = cuda_rc(launch_attn_shared(p, s)))) return rc;
+    p.part.recs += groups->num_groups;
+    p.part.count = rows->num_seqs;
+    p.part.groups = 0;
+    p.part.behind = 1;
+  }
+  p.ws = ws + w.pass;
   if (attn_split_supported(p, cache->dtype)) {
     pieces = attn_split_parts_pieces(p, p.ws);
     rc = cuda_rc(launch_attn_split_parts(p, s));
@@ -491,7 +509,7 @@ int gdn_shared_attention(const gdn_attn_desc* attn, const gdn_kv_cache* cache, c
     pieces = attn_split_fma_parts_pieces(p, p.ws);
     rc = cuda_rc(launch_attn_split_fma_parts(p, cache->dtype, s));
   }
-  return rc ? rc : cuda_rc(launch_join_parts(p, cache->dtype, pieces, pieces, s));
+  return rc ? rc : cuda_rc(launch_join_parts(p, cache->dtype, p.part.behind ? shared : pieces, pieces, s));
 }
 
 int gdn_kv_common_prefix(const gdn_kv_cache* cache, const gdn_kv_rows* rows, const gdn_kv_groups* groups,
