@@ -18,32 +18,26 @@ namespace gdn {
 
 namespace {
 
-constexpr int kThreads = 256;
 constexpr int kHeld = 4;      // items of a thread whose values are on their way
-constexpr int kTokens = 8;    // of a block, at most: a warp looks up each
+constexpr int kTokens = 4;    // of a block, at most: a warp looks up each
 constexpr int kPairs = 136;   // of a head, with those that fill up the last vector
 
 enum Pairs { kHalf, kHalfAny, kInterleaved };  // kHalfAny: halves that 16-byte vectors do not fit
+// Threads of a block: more than items of a head, of which there are up to 32, or 255 where an item is two values.
+__host__ __device__ constexpr int threads_of(int pairs) { return pairs == kHalfAny ? 256 : 128; }
 
 struct TurnParams {
   TurnLaunch a;
-  int tb;                  // tokens of a block
-  int heads;               // of a token, all kinds
-  int items;               // of a head
-  uint32_t per_token;      // items of a token
-  uint32_t item_magic, token_magic;
+  int tb;        // tokens of a block
+  int heads;     // of a token, all kinds
+  int items;     // of a head
+  int turning;   // of them (interleaved: of a head's vectors), those that turn
+  int at_once;   // heads that a block goes through at a time
+  uint32_t head_magic, item_magic;  // 2^32 / heads + 1, 2^32 / items + 1
 };
 
-// n / by, where magic = 2^32 / by + 1; rest: n % by.
-__device__ __forceinline__ uint32_t divide(uint32_t n, uint32_t by, uint32_t magic, uint32_t& rest) {
-  uint32_t q = by == 1 ? n : __umulhi(n, magic);
-  rest = n - q * by;
-  if ((int32_t)rest < 0) {  // the quotient is one too large at most
-    --q;
-    rest += by;
-  }
-  return q;
-}
+// n / by where magic = 2^32 / by + 1 and n by < 2^32.
+__device__ __forceinline__ int divide(int n, int by, uint32_t magic) { return by == 1 ? n : (int)__umulhi((uint32_t)n, magic); }
 
 // Cosine and sine of pair i at a position, times the magnitude.
 __device__ __forceinline__ float2 turn_of(const TurnLaunch& p, int pair, int pos) {
@@ -116,9 +110,13 @@ struct Vec {
   __device__ Vec() : raw(make_uint4(0, 0, 0, 0)) {}
 };
 
+// An item is two vectors of a head: the two that some pairs lie in, or two of those that stay, or, interleaved, any two
+// with pairs of their own; or it is a pair or a value that stays, where vectors do not fit the halves.  A thread keeps to
+// one item of the heads that it takes, and its neighbours take the neighbouring vectors: an item of two vectors side by side
+// would leave every 32 bytes to two stores.
 template <typename T, int PAIRS, bool APPEND>
-__global__ void __launch_bounds__(kThreads, 4) turn_kernel(TurnParams P) {
-  constexpr int VE = 16 / (int)sizeof(T);
+__global__ void __launch_bounds__(threads_of(PAIRS), 1024 / threads_of(PAIRS)) turn_kernel(TurnParams P) {
+  constexpr int kThreads = threads_of(PAIRS), VE = 16 / (int)sizeof(T), E = PAIRS == kHalfAny ? 1 : PAIRS == kHalf ? VE : VE / 2;  // E: pairs of a vector
   __shared__ float2 cs[kTokens][kPairs];
   __shared__ Place places[kTokens];
   const TurnLaunch& p = P.a;
@@ -126,67 +124,54 @@ __global__ void __launch_bounds__(kThreads, 4) turn_kernel(TurnParams P) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int first = blockIdx.x * P.tb, tokens = min(P.tb, p.num_tokens - first);
-  const uint32_t all = tokens * P.per_token;
-  const int half = p.rotary / 2, n = PAIRS == kHalfAny ? half : (half + VE - 1) / VE;
+  const int half = p.rotary / 2, n = P.turning;
+  // (token, head) `row` of the block from `row0` on, `at_once` a step, this thread's item of them
+  const int row0 = divide(tid, P.items, P.item_magic), i = tid - row0 * P.items;
+  const int rows = row0 < P.at_once ? tokens * P.heads : 0;
+  const bool turns = i < n;
+  const int ia = PAIRS == kInterleaved || turns ? i * (PAIRS == kHalfAny ? 1 : VE) : 2 * half + (i - n) * E;
+  const int ib = PAIRS == kInterleaved ? (i + P.items) * VE : turns ? ia + half : ia + (P.items - n) * E;
 
-  // An item is two vectors of a head (two values where vectors do not fit): the two of some pairs, or two that stay.
-  struct Item {
-    int t, head, i;
-    bool turns;
-    int a, b;  // first elements
-  };
-  auto item_at = [&](uint32_t at) {
-    Item w;
-    uint32_t rest, i;
-    w.t = (int)divide(at, P.per_token, P.token_magic, rest);
-    w.head = (int)divide(rest, P.items, P.item_magic, i);
-    w.i = (int)i;
-    if (PAIRS == kInterleaved) {
-      w.turns = w.i < n;
-      w.a = w.i * 2 * VE;
-      w.b = w.a + VE;
-    } else {
-      constexpr int E = PAIRS == kHalf ? VE : 1;
-      w.turns = w.i < n;
-      w.a = w.turns ? w.i * E : PAIRS == kHalf ? 2 * half + (w.i - n) * 2 * E : 2 * half + (w.i - n);
-      w.b = w.turns ? w.a + half : w.a + E;
-    }
-    return w;
-  };
-  auto source = [&](const Item& w) {
-    const int local = first + w.t;
+  const auto source = [&](int t, int head) {
+    const int local = first + t;
     const int64_t g = APPEND && p.rows.tok ? load(p.rows.tok + local) : local;
     if (APPEND && (g < 0 || g >= p.num_global)) return static_cast<const T*>(nullptr);
-    if (!APPEND || w.head < p.Hq) return static_cast<const T*>(p.q) + g * p.q_stride + w.head * p.d;
-    const int h = w.head - p.Hq;
-    return h < p.cache.Hkv ? static_cast<const T*>(p.k) + g * p.k_stride + h * p.d
-                           : static_cast<const T*>(p.v) + g * p.v_stride + (h - p.cache.Hkv) * p.d;
+    if (!APPEND || head < p.Hq) return static_cast<const T*>(p.q) + g * p.q_stride + head * p.d;
+    head -= p.Hq;
+    return head < p.cache.Hkv ? static_cast<const T*>(p.k) + g * p.k_stride + head * p.d
+                              : static_cast<const T*>(p.v) + g * p.v_stride + (head - p.cache.Hkv) * p.d;
   };
-  auto target = [&](const Item& w, const Place& at) {
+  const auto target = [&](const Place& at, int head) {
     if (at.g < 0) return static_cast<T*>(nullptr);
-    if (!APPEND || w.head < p.Hq) return static_cast<T*>(p.q_out) + at.g * p.q_out_stride + w.head * p.d;
+    if (!APPEND || head < p.Hq) return static_cast<T*>(p.q_out) + at.g * p.q_out_stride + head * p.d;
     if (at.page == 0) return static_cast<T*>(nullptr);
     const KvDev& C = p.cache;
-    const int h = w.head - p.Hq;
-    T* pool = static_cast<T*>(h < C.Hkv ? C.k : C.v);
-    return pool + at.page * C.page_stride + ((int64_t)(h < C.Hkv ? h : h - C.Hkv) * C.page_size + at.slot) * p.d;
+    head -= p.Hq;
+    const bool key = head < C.Hkv;
+    T* pool = static_cast<T*>(key ? C.k : C.v) + at.page * C.page_stride;
+    return pool + ((key ? head : head - C.Hkv) * C.page_size + at.slot) * p.d;
+  };
+  const auto turn = [](T& x, T& y, float2 f) {
+    const float xf = to_f32(x), yf = to_f32(y);
+    x = from_f32<T>(fmaf(xf, f.x, -yf * f.y));
+    y = from_f32<T>(fmaf(yf, f.x, xf * f.y));
   };
 
-  for (uint32_t from = 0; from < all; from += kHeld * kThreads) {
+  for (int from = 0; from == 0 || from < rows; from += kHeld * P.at_once) {
     Vec<T> a[kHeld], b[kHeld];
 #pragma unroll
     for (int u = 0; u < kHeld; ++u) {
-      const uint32_t at = from + u * kThreads + tid;
-      if (at >= all) break;
-      const Item w = item_at(at);
-      const T* x = source(w);
+      const int row = from + u * P.at_once + row0;
+      if (row >= rows) break;
+      const int t = P.tb == 1 ? 0 : divide(row, P.heads, P.head_magic);
+      const T* x = source(t, row - t * P.heads);
       if (!x) continue;
       if (PAIRS == kHalfAny) {
-        a[u].v[0] = load(x + w.a);
-        if (w.turns) b[u].v[0] = load(x + w.b);
+        a[u].v[0] = load(x + ia);
+        if (turns) b[u].v[0] = load(x + ib);
       } else {
-        a[u].raw = load(reinterpret_cast<const uint4*>(x + w.a));
-        b[u].raw = load(reinterpret_cast<const uint4*>(x + w.b));
+        a[u].raw = load(reinterpret_cast<const uint4*>(x + ia));
+        b[u].raw = load(reinterpret_cast<const uint4*>(x + ib));
       }
     }
     if (from == 0) {
@@ -200,61 +185,61 @@ __global__ void __launch_bounds__(kThreads, 4) turn_kernel(TurnParams P) {
         places[tid] = Place{first + tid, load(p.positions + first + tid), 0, 0};
       }
       __syncthreads();
-      // pair e of item i stands at [e n + i]: neighbouring items' pairs are neighbours
+      // pair e of item (or vector) i stands at [e n + i]: neighbouring items' pairs are neighbours
       for (int t = 0; t < tokens; ++t)
-        for (int pair = tid; pair < half; pair += kThreads)
-          cs[t][PAIRS == kHalfAny ? pair : pair % VE * n + pair / VE] = turn_of(p, pair, places[t].pos);
+        for (int pair = tid; pair < half; pair += kThreads) cs[t][pair % E * n + pair / E] = turn_of(p, pair, places[t].pos);
       __syncthreads();
     }
 #pragma unroll
     for (int u = 0; u < kHeld; ++u) {
-      const uint32_t at = from + u * kThreads + tid;
-      if (at >= all) break;
-      const Item w = item_at(at);
-      T* out = target(w, places[w.t]);
+      const int row = from + u * P.at_once + row0;
+      if (row >= rows) break;
+      const int t = P.tb == 1 ? 0 : divide(row, P.heads, P.head_magic), head = row - t * P.heads;
+      T* out = target(places[t], head);
       if (!out) continue;
-      const bool turns = w.turns && (!APPEND || w.head < p.Hq + p.cache.Hkv);
-      auto turn = [&](T& x, T& y, float2 f) {
-        const float xf = to_f32(x), yf = to_f32(y);
-        x = from_f32<T>(fmaf(xf, f.x, -yf * f.y));
-        y = from_f32<T>(fmaf(yf, f.x, xf * f.y));
-      };
+      const bool turned = turns && (!APPEND || head < p.Hq + p.cache.Hkv);
       if (PAIRS == kHalfAny) {
-        if (turns) turn(a[u].v[0], b[u].v[0], cs[w.t][w.i]);
-        out[w.a] = a[u].v[0];
-        if (w.turns) out[w.b] = b[u].v[0];
+        if (turned) turn(a[u].v[0], b[u].v[0], cs[t][i]);
+        out[ia] = a[u].v[0];
+        if (turns) out[ib] = b[u].v[0];
         continue;
       }
-      if (turns) {
+      if (turned) {
 #pragma unroll
-        for (int e = 0; e < VE; ++e) {
-          const float2 f = cs[w.t][e * n + w.i];
+        for (int e = 0; e < E; ++e) {
           if (PAIRS == kHalf) {
-            turn(a[u].v[e], b[u].v[e], f);
-          } else if (w.i * VE + e < half) {
-            Vec<T>& x = e < VE / 2 ? a[u] : b[u];
-            turn(x.v[2 * (e % (VE / 2))], x.v[2 * (e % (VE / 2)) + 1], f);
+            turn(a[u].v[e], b[u].v[e], cs[t][e * n + i]);
+          } else {
+            if (i * E + e < half) turn(a[u].v[2 * e], a[u].v[2 * e + 1], cs[t][e * n + i]);
+            if ((i + P.items) * E + e < half) turn(b[u].v[2 * e], b[u].v[2 * e + 1], cs[t][e * n + i + P.items]);
           }
         }
       }
-      *reinterpret_cast<uint4*>(out + w.a) = a[u].raw;
-      *reinterpret_cast<uint4*>(out + w.b) = b[u].raw;
+      *reinterpret_cast<uint4*>(out + ia) = a[u].raw;
+      *reinterpret_cast<uint4*>(out + ib) = b[u].raw;
     }
   }
 }
 
 template <typename T, int PAIRS, bool APPEND>
 cudaError_t launch_pairs(const TurnLaunch& a, cudaStream_t s) {
+  constexpr int kThreads = threads_of(PAIRS);
   TurnParams P{};
   P.a = a;
   P.heads = a.Hq + (APPEND ? 2 * a.cache.Hkv : 0);
   P.items = PAIRS == kHalfAny ? a.d - a.rotary / 2 : a.d * (int)sizeof(T) / 32;
-  P.per_token = (uint32_t)P.heads * P.items;
+  const int pairs = PAIRS == kHalfAny ? 1 : (PAIRS == kHalf ? 16 : 8) / (int)sizeof(T);  // of a vector
+  P.turning = (a.rotary / 2 + pairs - 1) / pairs;
+  P.at_once = kThreads / P.items;
   P.item_magic = (uint32_t)((1ull << 32) / P.items) + 1;
-  P.token_magic = (uint32_t)((1ull << 32) / P.per_token) + 1;
-  // as many tokens as a block holds at once, fewer where that leaves SMs without a block
-  P.tb = std::max(1, std::min(kTokens, kHeld * kThreads / (int)P.per_token));
-  P.tb = std::max(1, std::min(P.tb, a.num_tokens / (2 * kSms)));
+  P.head_magic = (uint32_t)((1ull << 32) / P.heads) + 1;
+  // As many tokens as leave the fewest threads without an item, fewer where that leaves SMs without a block.
+  const int held = kHeld * P.at_once;
+  const auto rounds = [&](int tokens) { return (tokens * P.heads + held - 1) / held; };
+  P.tb = 1;
+  for (int t = 2; t <= kTokens; ++t)
+    if (rounds(t) * P.tb < rounds(P.tb) * t) P.tb = t;
+  P.tb = std::max(1, std::min(P.tb, a.num_tokens / (4 * kSms)));
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
