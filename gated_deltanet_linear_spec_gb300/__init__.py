@@ -117,6 +117,8 @@ _lock = threading.Lock()
 def library() -> ctypes.CDLL:
     """Loads ``libgdn.so`` (built by ``build.py``); raises if it is missing."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):

@@ -16,9 +16,8 @@ constexpr int kWarps = 8;
 
 struct JoinParams {
   AttnLaunch a;
-  PartPieces from[2];  // the pieces of groups' parts and of rows' own
-  float down[2];       // log2 of what brings each to the lower scale of the two
-  int team;            // warps of a query
+  PartPieces from;
+  int team;  // warps of a query
 };
 
 template <int E>
@@ -41,8 +40,8 @@ __device__ __forceinline__ void load_row(const float* v, bool there, float (&x)[
   }
 }
 
-// E columns of a lane; DC: head_dim where it is 32 E, else 0.
-template <typename T, int E, int DC>
+// E columns of a lane; DC: head_dim where it is 32 E, else 0; QUADS: see PartDev.
+template <typename T, int E, int DC, bool QUADS>
 __global__ void __launch_bounds__(32 * kWarps) join_parts_kernel(JoinParams J) {
   constexpr int kAtOnce = E <= 4 ? 8 : 4;
   __shared__ float so[kWarps][32 * E], sl[kWarps], sm[kWarps];
@@ -81,18 +80,21 @@ __global__ void __launch_bounds__(32 * kWarps) join_parts_kernel(JoinParams J) {
     const float* values = nullptr;
     if (i < n) {
       const PieceRange x = s ? r[1] : r[0];
-      const PartPieces from = s ? J.from[1] : J.from[0];
       const int c = x.c0 + i - (s ? n0 : 0);
-      const int64_t at = x.c0 < 0 ? s * all + q : (int64_t)(2 * c + (c == x.c0 ? 1 : 0)) * from.queries + x.qi;
-      st = load(reinterpret_cast<const float2*>(x.c0 < 0 ? part.ml : from.stats) + at);
-      values = (x.c0 < 0 ? part.o : from.o) + at * D;
+      const int64_t at = x.c0 < 0 ? s * all + q : (int64_t)(2 * c + (c == x.c0 ? 1 : 0)) * J.from.queries + x.qi;
+      st = load(reinterpret_cast<const float2*>(x.c0 < 0 ? part.ml : J.from.stats) + at);
+      if (QUADS)
+        values = x.c0 < 0 ? part.o + at * 4 : J.from.o + ((at - x.qi) * (D / 4) + x.qi) * 4;
+      else
+        values = (x.c0 < 0 ? part.o : J.from.o) + at * D;
     }
     float mn = st.x;
 #pragma unroll
     for (int d = 16; d; d >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, d));
     mn = fmaxf(mn, m);
     const float a = m == -INFINITY ? 0.f : split::ex2((m - mn) * sl2);
-    const float f = st.x == -INFINITY ? 0.f : split::ex2(fmaf(st.x - mn, sl2, s ? J.down[1] : J.down[0]));
+    const float f = st.x == -INFINITY ? 0.f : split::ex2((st.x - mn) * sl2);
+    const int step = i < n && (s ? r[1].c0 : r[0].c0) < 0 ? (int)(2 * all) : J.from.queries;  // QUADS: 16 bytes from one to the next
     float sum = st.y * f;
 #pragma unroll
     for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
@@ -106,7 +108,23 @@ __global__ void __launch_bounds__(32 * kWarps) join_parts_kernel(JoinParams J) {
 #pragma unroll
       for (int u = 0; u < kAtOnce; ++u) {
         const uint64_t from = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(values), (u0 + u) & 31);
-        load_row<E>(reinterpret_cast<const float*>(from) + lane * E, u0 + u < mine && columns, v[u]);
+        if constexpr (QUADS) {
+          const int64_t to = __shfl_sync(0xffffffffu, step, (u0 + u) & 31);
+          const float* x = reinterpret_cast<const float*>(from) + lane * E / 4 * to * 4 + lane * E % 4;
+          if constexpr (E <= 4) {
+            load_row<E>(x, u0 + u < mine, v[u]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < E; e += 4) {
+              float y[4];
+              load_row<4>(x + e * to, u0 + u < mine, y);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) v[u][e + k] = y[k];
+            }
+          }
+        } else {
+          load_row<E>(reinterpret_cast<const float*>(from) + lane * E, u0 + u < mine && columns, v[u]);
+        }
       }
 #pragma unroll
       for (int u = 0; u < kAtOnce; ++u) {
@@ -144,10 +162,11 @@ __global__ void __launch_bounds__(32 * kWarps) join_parts_kernel(JoinParams J) {
   for (int e = 0; e < E; ++e) out[e] = from_f32<T>(o[e] * inv);
 }
 
-template <typename T, int E, int DC>
+template <typename T, int E, int DC, bool QUADS>
 cudaError_t launch_as(JoinParams& J, cudaStream_t s) {
   const int64_t queries = (int64_t)J.a.part.tokens * J.a.Hq;
-  J.team = queries <= 2 * kSms * kWarps ? 8 : 1;
+  J.team = 8;
+  while (J.team > 1 && queries * J.team > kSms * 32) J.team /= 2;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -158,23 +177,26 @@ cudaError_t launch_as(JoinParams& J, cudaStream_t s) {
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_parts_kernel<T, E, DC>, J);
+  return cudaLaunchKernelEx(&cfg, join_parts_kernel<T, E, DC, QUADS>, J);
 }
 template <typename T>
-cudaError_t launch_type(JoinParams& J, cudaStream_t s) {
+cudaError_t launch_rows(JoinParams& J, cudaStream_t s) {
   const int d = J.a.cache.d;
-  if (d == 64) return launch_as<T, 2, 64>(J, s);
-  if (d == 128) return launch_as<T, 4, 128>(J, s);
-  if (d == 256) return launch_as<T, 8, 256>(J, s);
-  return d < 64 ? launch_as<T, 2, 0>(J, s) : d < 128 ? launch_as<T, 4, 0>(J, s) : launch_as<T, 8, 0>(J, s);
+  return d <= 64    ? launch_as<T, 2, 0, false>(J, s)
+         : d <= 128 ? launch_as<T, 4, 0, false>(J, s)
+                    : launch_as<T, 8, 0, false>(J, s);
 }
 
 }  // namespace
 
-cudaError_t launch_join_parts(const AttnLaunch& p, gdn_dtype dtype, PartPieces groups, PartPieces rows, cudaStream_t s) {
-  const float low = std::min(groups.shift, rows.shift);
-  JoinParams J{p, {groups, rows}, {low - groups.shift, low - rows.shift}, 1};
-  return dtype == GDN_BF16 ? launch_type<__nv_bfloat16>(J, s) : launch_type<float>(J, s);
+cudaError_t launch_join_parts(const AttnLaunch& p, gdn_dtype dtype, PartPieces pieces, cudaStream_t s) {
+  JoinParams J{p, pieces, 1};
+  if (dtype == GDN_F32) return launch_rows<float>(J, s);
+  if (!p.part.quads) return launch_rows<__nv_bfloat16>(J, s);
+  const int d = p.cache.d;
+  return d == 64    ? launch_as<__nv_bfloat16, 2, 64, true>(J, s)
+         : d == 128 ? launch_as<__nv_bfloat16, 4, 128, true>(J, s)
+                    : launch_as<__nv_bfloat16, 8, 256, true>(J, s);
 }
 
 }  // namespace gdn

@@ -1,13 +1,14 @@
-// gdn_attn_shared.cu -- the queries of groups of rows over what the rows of each share, on tcgen05 (bf16, d = 64, 128, 256).
+// gdn_attn_shared.cu -- groups' queries over what their rows share, and rows' over their own tokens, on tcgen05 (bf16, d = 64,
+// 128, 256).
 //
-// The queries of a group's rows stand one after the other, 256 (d = 256: 128) to a CTA, and every key and value is read once
-// for all of them: 4 d flops per score, so the tensor core bounds it as it does prompts, and tiles, products and softmax
-// are those of gdn_attn_prompt.cu.  Nothing is causal here: a query stands behind all shared tokens, and only a window
-// hides some.
+// The queries of a group's rows stand one after the other, 256 (d = 256: 128) to a CTA, and every shared key and value is read
+// once for all of them: 4 d flops per score, so the tensor core bounds it as it does prompts, and tiles, products and
+// softmax are those of gdn_attn_prompt.cu.  A query stands behind all shared tokens, so only a window hides some of them; a
+// row's own tokens are causal.
 //
-// Units (group, kv-head, 256 queries) are dealt out as in gdn_attn_share.cuh, 64-token tiles laid end to end, so that all SMs
+// Units (part, kv-head, 256 queries) are dealt out as in gdn_attn_share.cuh, 64-token tiles laid end to end, so that all SMs
 // end together whatever the groups' sizes are; a unit's pieces meet in the join of parts.  A tile of 128 queries that a unit
-// does not have (few queries, a group's last ones) takes no part in its steps.
+// does not have (few queries, a row's own part) takes no part in its steps.
 #include <algorithm>
 
 #include "gdn_attn_share.cuh"
@@ -56,6 +57,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
   const KvDev& kv = p.cache;
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (tid == 0) {
     for (int i = 0; i < R; ++i) {
       tc::mbar_init(&sm.full[i], 1);
@@ -77,8 +79,6 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
   }
   if (warp == 4 * NT) tc::tmem_alloc(&sm.tmem, 512);
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  // Only now: the pass over the rows' own parts, which may start from here on, reads the plan without waiting for it.
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   split::find_shares<C::kRows, 1, C::kThreads, true, kTN, kBegin>(p, sm.sum, sm.deal, &sm.share);
   tc::fence_before();
   __syncthreads();
@@ -99,8 +99,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
   const auto first_of = [&]() { return w.h / kv.Hkv * C::kRows; };
   const auto tiles_of = [&]() { return NT == 2 && w.u.r.len * p.G - first_of() > 128 ? 2 : 1; };
   const auto highest = [&]() { return p.window > 0 ? load(&p.part.recs[w.n].hi) : 0; };
-  // Some query does not see some token of [b, b + kTN) that a page holds.
-  const auto in_part_of = [&](int b, int hi) { return in_part(p, b, INT32_MAX, hi); };
+  // Some query may not see some token of [b, b + kTN).  (A row has one unit of a kv-head, so its first query is `lo`'s.)
+  const auto in_part_of = [&](int b, int hi) { return in_part(p, b, w.u.lo, hi); };
 
   if (role < 0) {
     // ---- softmax: a thread per query ----
@@ -136,7 +136,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       }
       const int qi = first_of() + tile * 128 + row;
       const bool there = qi < w.u.r.len * p.G;
-      const int pos = p.window > 0 && there ? load(&p.part.token[w.u.r.bos + qi / p.G].x) : w.u.r.kv;
+      // (without a window it does not matter how far behind a group's part its queries stand)
+      const int pos = p.window > 0 && there ? load(&p.part.token[w.u.r.bos + qi / p.G].x)
+                                            : min(w.u.lo + qi / p.G, w.u.r.kv - 1);
       float m = -INFINITY, l = 0.f;  // the maximum that the weights refer to (of scores before their scale); their
                                      // sum, both l's and O's 2^-kGrow of e^(s - m)'s
       bool wrote = false;            // O holds something, or will
@@ -216,8 +218,10 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       if (!ok) break;
       // where this piece goes
       const bool whole = w.j0 == 0 && w.len == w.u.tiles;
-      const int64_t place = (int64_t)(w.u.r.bos + qi / p.G) * p.Hq + head_of() * p.G + qi % p.G;
-      const int64_t to = whole ? place : (int64_t)(2 * blockIdx.x + (w.j0 == 0 ? 1 : 0)) * C::kRows + tile * 128 + row;
+      const int64_t place = ((int64_t)(w.n < p.part.groups ? 0 : p.part.tokens) + w.u.r.bos + qi / p.G) * p.Hq +
+                            head_of() * p.G + qi % p.G;
+      const int slot = 2 * blockIdx.x + (w.j0 == 0 ? 1 : 0), at_tile = tile * 128 + row;
+      const int64_t to = whole ? place : (int64_t)slot * C::kRows + at_tile;
       if (there && w.j0 == 0)
         p.part.range[place] = {whole ? -1 : (int)blockIdx.x, sm.deal.owner(w.unit_last(sm.share)), tile * 128 + row, 0};
       w.next();
@@ -227,7 +231,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       if (!ok) break;
       tc::fence_after();
       if (there) *reinterpret_cast<float2*>((whole ? p.part.ml : P.stats) + to * 2) = make_float2(m, l);
-      float* dst = (whole ? p.part.o : P.o) + to * D;
+      // four columns of all queries side by side: a warp's store goes to 512 bytes in a row, not to 32 places (3 us a unit)
+      const int64_t step = whole ? (int64_t)2 * p.part.tokens * p.Hq : C::kRows;
+      float4* dst = reinterpret_cast<float4*>(whole ? p.part.o : P.o) + (whole ? place : (int64_t)slot * (D / 4) * C::kRows + at_tile);
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
         float o[32];
@@ -235,7 +241,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         if (there) {
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            reinterpret_cast<float4*>(dst + c)[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            dst[(c / 4 + i) * step] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
         }
       }
       // The next unit's first product overwrites O; its p_ready, which this thread arrives at, comes after these loads.
@@ -374,6 +380,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
           const int t = u * 32 + lane;
           uint8_t* v = ring + en * C::kKv + (t >> 3) * CB * 1024 + (t & 7) * 128;
           uint32_t acc[4] = {0, 0, 0, 0};
+          const bool past = b + t >= w.u.r.kv;
 #pragma unroll 8
           for (int c = 0; c < D / 8; ++c) {
             const uint4 x = *reinterpret_cast<const uint4*>(v + (c >> 3) * 1024 + (((c & 7) ^ (t & 7)) << 4));
@@ -383,10 +390,10 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             acc[3] = note2(x.w, acc[3]);
           }
           const bool odd = ((acc[0] | acc[1] | acc[2] | acc[3]) & 0x7fff7fffu) != 0;
-          if (odd)
+          if (past || odd)
             for (int c = 0; c < D / 8; ++c)
               *reinterpret_cast<uint4*>(v + (c >> 3) * 1024 + (((c & 7) ^ (t & 7)) << 4)) = make_uint4(0, 0, 0, 0);
-          const uint32_t list = __ballot_sync(0xffffffffu, odd);
+          const uint32_t list = __ballot_sync(0xffffffffu, odd && !past);
           if (lane == 0) sm.bad[en >> 1][u] = list;
         }
         tc::fence_async_smem();
@@ -443,12 +450,16 @@ int rows_of_cta(const AttnLaunch& a) { return a.cache.d <= 128 ? Cfg<128>::kRows
 
 }  // namespace
 
+bool attn_shared_supported(const AttnLaunch& a, gdn_dtype dtype) {
+  return attn_prompt_supported(a, dtype) && (int64_t)a.rows.max_q * a.G <= rows_of_cta(a);
+}
+
 size_t attn_shared_workspace(const AttnLaunch& a) { return (size_t)2 * kSms * rows_of_cta(a) * (a.cache.d + 2) * 4; }
 
 PartPieces attn_shared_pieces(const AttnLaunch& a, void* ws) {
   const int rows = rows_of_cta(a);
   float* stats = static_cast<float*>(ws);
-  return {stats, stats + (size_t)4 * kSms * rows, rows, -kGrow};
+  return {stats, stats + (size_t)4 * kSms * rows, rows};
 }
 
 cudaError_t launch_attn_shared(const AttnLaunch& a, cudaStream_t s) {

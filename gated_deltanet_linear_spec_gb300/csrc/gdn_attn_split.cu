@@ -191,9 +191,7 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, NW>::kThreads, 1)
     tc::prefetch_map(&kmap);
     tc::prefetch_map(&vmap);
   }
-  // What lies before this overlaps the kernel before this one.  (A pass over rows' own parts behind that over groups' takes
-  // nothing from it, and waits for it at its end.)
-  if (!PART || !p.part.behind) asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // what lies before this overlaps the kernel before this one
   if (!PART && tid < NW) P.info[(blockIdx.x * NW + tid) * 8] = 0;
   // (the sums of find_shares lie where the first worker's ring will be)
   find_shares<QG, NW, C::kThreads, PART>(p, reinterpret_cast<int64_t*>(smem), small.deal, small.shares);
@@ -289,7 +287,6 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, NW>::kThreads, 1)
     for (int i = max(0, it - S); i < it; ++i) ok &= tc::mbar_wait(&sm.full[i % S], (i / S) & 1, P.wait_ns);
     if (seg > 0) ok &= tc::mbar_wait(&sm.qfull, (seg - 1) & 1, P.wait_ns);
     if (!ok) set_status(p.status, GDN_STATUS_WAIT_TIMEOUT);
-    if (PART && p.part.behind) asm volatile("griddepcontrol.wait;" ::: "memory");
     return;
   }
 
@@ -442,10 +439,13 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, NW>::kThreads, 1)
           const int64_t place = ((int64_t)(w.n < p.part.groups ? 0 : p.part.tokens) + row.bos + (q0 + qi) / p.G) * p.Hq +
                                 h * p.G + (q0 + qi) % p.G;
           const int64_t at = whole ? place : (int64_t)slot * C::kNQ + qi;
-          float* to = (whole ? p.part.o : P.part) + at * D + ds * DV + c2;
+          // four columns of all queries side by side (see PartDev::quads)
+          const int64_t step = whole ? (int64_t)2 * p.part.tokens * p.Hq * 4 : C::kNQ * 4;
+          float* to = (whole ? p.part.o + place * 4 : P.part + ((int64_t)slot * (D / 4) * C::kNQ + qi) * 4) +
+                      (ds * DV + c2) / 4 * step + c2 % 4;
 #pragma unroll
           for (int i = 0; i < DV / 8; ++i)
-            *reinterpret_cast<float2*>(to + i * 8) = make_float2(o[i][2 * e], o[i][2 * e + 1]);
+            *reinterpret_cast<float2*>(to + i * 2 * step) = make_float2(o[i][2 * e], o[i][2 * e + 1]);
           if (ds == 0 && c2 == 0) {
             *reinterpret_cast<float2*>((whole ? p.part.ml : P.stats) + at * 2) = make_float2(m[e], l[e]);
             if (w.j0 == 0)
@@ -573,8 +573,7 @@ size_t workspace_of(const AttnLaunch& a, int q) {
 
 // Queries of a unit of a pass over parts: those of a group may be those of all rows.
 int part_slots(const AttnLaunch& a) {
-  const int64_t most = (int64_t)(a.part.groups > 0 ? a.rows.num_tokens : a.rows.max_q) * a.G;
-  return query_slots(std::max<int64_t>(most, 1));
+  return query_slots(std::max<int64_t>((int64_t)a.rows.num_tokens * a.G, 1));
 }
 
 }  // namespace
@@ -590,7 +589,7 @@ size_t attn_split_parts_workspace(const AttnLaunch& a) { return workspace_of(a, 
 PartPieces attn_split_parts_pieces(const AttnLaunch& a, void* ws) {
   const int q = part_slots(a), workers = kSms * pick(a.cache.d, q, [](auto c) { return decltype(c)::kWorkers; });
   float* stats = static_cast<float*>(ws) + 8 * workers;
-  return {stats, stats + (size_t)4 * workers * q, q, 0.f};
+  return {stats, stats + (size_t)4 * workers * q, q};
 }
 
 cudaError_t launch_attn_split_parts(const AttnLaunch& a, cudaStream_t s) {

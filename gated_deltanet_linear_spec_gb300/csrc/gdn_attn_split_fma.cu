@@ -367,7 +367,7 @@ size_t attn_split_fma_parts_workspace(const AttnLaunch& a) { return attn_split_f
 PartPieces attn_split_fma_parts_pieces(const AttnLaunch& a, void* ws) {
   constexpr int workers = kSms * kPerSm * kWarps;
   float* stats = static_cast<float*>(ws) + 8 * workers;
-  return {stats, stats + (size_t)4 * workers * kNQ, kNQ, 0.f};
+  return {stats, stats + (size_t)4 * workers * kNQ, kNQ};
 }
 
 cudaError_t launch_attn_split_fma_parts(const AttnLaunch& a, gdn_dtype dtype, cudaStream_t s) {

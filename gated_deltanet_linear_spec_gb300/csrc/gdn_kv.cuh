@@ -119,8 +119,8 @@ struct PartDev {
   const int2* token;    // [tokens]: position (-1: of no well-formed row), whether its row shares a prefix
   PieceRange* range;    // [2][tokens][Hq]
   float* ml;            // [2][tokens][Hq][2]: m (of the scores before their scale), l of a query in one piece
-  float* o;             // [2][tokens][Hq][d]
-  int32_t behind;       // this pass's inputs are complete when it may start, and the pass before it need not be
+  float* o;             // [2][tokens][Hq][d], or with `quads` [2][d / 4][tokens][Hq][4]
+  int32_t quads;        // o, here and in pieces, by four columns: what neighbouring queries write is side by side
 };
 
 struct AttnLaunch {
@@ -232,14 +232,14 @@ cudaError_t launch_attn_split_fma(const AttnLaunch& p, gdn_dtype dtype, cudaStre
 // Groups of rows over shared prefixes: the plan of their parts, passes over parts, and the join of what those leave.
 cudaError_t launch_kv_common_prefix(const GroupsLaunch& p, cudaStream_t s);
 cudaError_t launch_group_plan(const GroupsLaunch& p, cudaStream_t s);
-// Where a pass leaves its pieces: [2 * workers][queries of a unit], (m, l) and o.
+// Where a pass leaves its pieces: [2 * workers][queries of a unit] (m, l), and o, with `quads` [2 * workers][d / 4][queries][4].
 struct PartPieces {
   float* stats;
   float* o;
   int32_t queries;
-  float shift;  // log2 of what weights are scaled by: (l, o) are sums of 2^shift e^(s - m)
 };
-size_t attn_shared_workspace(const AttnLaunch& p);  // groups' parts on tcgen05
+bool attn_shared_supported(const AttnLaunch& p, gdn_dtype dtype);  // on tcgen05: rows of up to a CTA's queries
+size_t attn_shared_workspace(const AttnLaunch& p);
 PartPieces attn_shared_pieces(const AttnLaunch& p, void* ws);
 cudaError_t launch_attn_shared(const AttnLaunch& p, cudaStream_t s);
 size_t attn_split_parts_workspace(const AttnLaunch& p);
@@ -248,6 +248,6 @@ cudaError_t launch_attn_split_parts(const AttnLaunch& p, cudaStream_t s);
 size_t attn_split_fma_parts_workspace(const AttnLaunch& p);
 PartPieces attn_split_fma_parts_pieces(const AttnLaunch& p, void* ws);
 cudaError_t launch_attn_split_fma_parts(const AttnLaunch& p, gdn_dtype dtype, cudaStream_t s);
-cudaError_t launch_join_parts(const AttnLaunch& p, gdn_dtype dtype, PartPieces groups, PartPieces rows, cudaStream_t s);
+cudaError_t launch_join_parts(const AttnLaunch& p, gdn_dtype dtype, PartPieces pieces, cudaStream_t s);
 
 }  // namespace gdn

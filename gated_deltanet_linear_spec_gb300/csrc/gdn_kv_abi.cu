@@ -234,22 +234,21 @@ int attend_whole(AttnLaunch& p, gdn_dtype dtype, cudaStream_t s) {
   return cuda_rc(launch_attn_prompt(p, s));
 }
 
-// Whether rows of these sizes share their groups' prefixes: all that one pass over own tokens takes.  Rows of more than 64
-// queries per kv-head on the tensor cores fill a tile of their own, and go over the whole of their caches.
-bool shares(const AttnLaunch& p, gdn_dtype dtype) {
-  return attn_split_supported(p, dtype) || !attn_prompt_supported(p, dtype);
+// The pass that goes over the parts of all groups and rows: the split kernel's where the queries of all rows fit a unit of
+// its, tcgen05's where those of a row fit a CTA, the CUDA cores' for types that take neither.  Longer rows on the tensor
+// cores fill tiles of their own, and share nothing.
+enum Pass { kNoPass, kSplitPass, kTilePass, kFmaPass };
+Pass pass_of(const AttnLaunch& p, gdn_dtype dtype) {
+  if (!attn_prompt_supported(p, dtype)) return kFmaPass;
+  if ((int64_t)p.rows.num_tokens * p.G <= 64 && attn_split_supported(p, dtype)) return kSplitPass;
+  return attn_shared_supported(p, dtype) ? kTilePass : kNoPass;
 }
 
 // The workspace of attention over groups: the plan's parts and tokens, where queries' pieces are, results in one piece, and the
 // pass's own.
 struct SharedWs {
-  size_t recs, token, range, ml, o, shared, pass, end;
+  size_t recs, token, range, ml, o, pass, end;
 };
-// Whether groups' queries go over the shared tokens on the tensor cores, apart from the rows' own parts: more of them than the
-// split kernel's units hold.
-bool apart(const AttnLaunch& p, gdn_dtype dtype) {
-  return attn_split_supported(p, dtype) && (int64_t)p.rows.num_tokens * p.G > 64;
-}
 SharedWs shared_ws(const AttnLaunch& p, gdn_dtype dtype) {
   SharedWs w{};
   const size_t tokens = p.rows.num_tokens, queries = 2 * tokens * p.Hq;
@@ -258,12 +257,11 @@ SharedWs shared_ws(const AttnLaunch& p, gdn_dtype dtype) {
   w.range = round256(w.token + tokens * sizeof(int2));
   w.ml = round256(w.range + queries * sizeof(PieceRange));
   w.o = round256(w.ml + queries * 8);
-  w.shared = round256(w.o + queries * p.cache.d * 4);
-  w.pass = w.shared + (apart(p, dtype) ? round256(attn_shared_workspace(p)) : 0);
-  AttnLaunch last = p;  // the pass that is not apart
-  if (apart(p, dtype)) last.part.groups = 0;
-  const bool split = attn_split_supported(p, dtype);
-  w.end = w.pass + round256(split ? attn_split_parts_workspace(last) : attn_split_fma_parts_workspace(last));
+  w.pass = round256(w.o + queries * p.cache.d * 4);
+  const Pass pass = pass_of(p, dtype);
+  w.end = w.pass + round256(pass == kSplitPass  ? attn_split_parts_workspace(p)
+                            : pass == kTilePass ? attn_shared_workspace(p)
+                                                : attn_split_fma_parts_workspace(p));
   return w;
 }
 // The parts of all groups and rows in one pass.
@@ -458,7 +456,7 @@ size_t gdn_shared_attention_workspace_bytes(const gdn_attn_desc* attn, const gdn
   const size_t whole = gdn_attention_workspace_bytes(attn, cache, rows);
   if (check_shape(cache) || check_table(cache) || check_attn(attn, cache) || check_kv_rows(rows)) return 0;
   AttnLaunch p = attn_args(attn, cache, rows);
-  if (rows->num_tokens == 0 || groups->num_groups == 0 || !shares(p, cache->dtype)) return whole;
+  if (rows->num_tokens == 0 || groups->num_groups == 0 || pass_of(p, cache->dtype) == kNoPass) return whole;
   all_parts(p, groups->num_groups);
   return shared_ws(p, cache->dtype).end;
 }
@@ -474,7 +472,7 @@ int gdn_shared_attention(const gdn_attn_desc* attn, const gdn_kv_cache* cache, c
   if ((rc = attention_args(attn, cache, rows, q, q_stride, num_global_tokens, out, out_stride, workspace, workspace_bytes,
                            need, d_status, p)))
     return rc;
-  if (groups->num_groups == 0 || !shares(p, cache->dtype)) return attend_whole(p, cache->dtype, (cudaStream_t)stream);
+  if (groups->num_groups == 0 || pass_of(p, cache->dtype) == kNoPass) return attend_whole(p, cache->dtype, (cudaStream_t)stream);
   all_parts(p, groups->num_groups);
   const SharedWs w = shared_ws(p, cache->dtype);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -488,28 +486,23 @@ int gdn_shared_attention(const gdn_attn_desc* attn, const gdn_kv_cache* cache, c
   p.part.range = reinterpret_cast<PieceRange*>(ws + w.range);
   p.part.ml = reinterpret_cast<float*>(ws + w.ml);
   p.part.o = reinterpret_cast<float*>(ws + w.o);
+  p.ws = ws + w.pass;
+  const Pass pass = pass_of(p, cache->dtype);
+  p.part.quads = pass != kFmaPass;
   const cudaStream_t s = (cudaStream_t)stream;
   if ((rc = cuda_rc(launch_group_plan(plan, s)))) return rc;
-  PartPieces shared, pieces;
-  if (apart(p, cache->dtype)) {
-    p.part.count = groups->num_groups;
-    p.ws = ws + w.shared;
-    shared = attn_shared_pieces(p, p.ws);
-    if ((rc = cuda_rc(launch_attn_shared(p, s)))) return rc;
-    p.part.recs += groups->num_groups;
-    p.part.count = rows->num_seqs;
-    p.part.groups = 0;
-    p.part.behind = 1;
-  }
-  p.ws = ws + w.pass;
-  if (attn_split_supported(p, cache->dtype)) {
+  PartPieces pieces;
+  if (pass == kSplitPass) {
     pieces = attn_split_parts_pieces(p, p.ws);
     rc = cuda_rc(launch_attn_split_parts(p, s));
+  } else if (pass == kTilePass) {
+    pieces = attn_shared_pieces(p, p.ws);
+    rc = cuda_rc(launch_attn_shared(p, s));
   } else {
     pieces = attn_split_fma_parts_pieces(p, p.ws);
     rc = cuda_rc(launch_attn_split_fma_parts(p, cache->dtype, s));
   }
-  return rc ? rc : cuda_rc(launch_join_parts(p, cache->dtype, p.part.behind ? shared : pieces, pieces, s));
+  return rc ? rc : cuda_rc(launch_join_parts(p, cache->dtype, pieces, s));
 }
 
 int gdn_kv_common_prefix(const gdn_kv_cache* cache, const gdn_kv_rows* rows, const gdn_kv_groups* groups,

@@ -407,8 +407,10 @@ typedef struct {
  * two rows of the group have new tokens; prefix_lens <= 0 shares nothing.  They are read by the table row of the
  * first such row: where the rows' entries differ after all, its pages count.  Rows of one call are in one group at most
  * (group bounds that do not ascend or leave the rows: GDN_STATUS_ROW_RANGE, that group shares nothing).
- * bf16 rows of more than 64 queries per kv-head (d = 64, 128, 256; max_query_len decides) go over their whole caches each,
- * as in gdn_paged_attention: they fill the tensor cores by themselves.
+ * bf16 rows of more than 256 queries per kv-head (d = 64, 128; 128 at d = 256; max_query_len decides) go over their whole
+ * caches each, as in gdn_paged_attention: they fill the tensor cores by themselves.
+ * Where the rows have more than 64 queries per kv-head in all, bf16 weights (d = 64, 128, 256) go into the second sum as one
+ * bf16, else as in gdn_paged_attention.
  * workspace: at least gdn_shared_attention_workspace_bytes(attn, cache, rows, groups) bytes, 256-byte aligned; it holds
  * the plan, (2 + d) fp32 per query and head, and partial results.
  */

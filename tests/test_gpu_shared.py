@@ -171,11 +171,13 @@ def test_many_groups():
     Groups(groups, heads=4, kv_heads=2, dim=64, seed=6).check()
 
 
-@pytest.mark.parametrize("dim,dtype", [(128, BF16), (96, BF16), (64, F32)])
-def test_long_rows(dim, dtype):
-    """More than 64 queries per kv-head."""
-    groups = [(300, [(40, 340), (1, 320), (70, 390)]), (64, [(33, 100), (2, 66)])]
-    Groups(groups, heads=4, kv_heads=2, dim=dim, dtype=dtype, seed=7).check()
+@pytest.mark.parametrize("dim,dtype", [(64, BF16), (128, BF16), (256, BF16), (96, BF16), (64, F32)])
+@pytest.mark.parametrize("longest", [33, 65, 129, 140])
+def test_long_rows(longest, dim, dtype):
+    """More than 64, 128 and 256 queries per kv-head; rows that end inside a page whose other places hold NaN."""
+    groups = [(300, [(40, 340), (1, 320), (longest, 300 + longest + 20)]), (64, [(33, 100), (2, 66)])]
+    Groups(groups, heads=4, kv_heads=2, dim=dim, dtype=dtype, seed=longest).check()
+    Groups(groups, heads=4, kv_heads=2, dim=dim, dtype=dtype, seed=longest, window=100, sinks=3).check()
 
 
 def test_rows_without_tokens_do_not_stand_for_their_group():
