@@ -21,7 +21,7 @@ namespace {
 using namespace tile;
 
 // Beginning a unit -- its queries, the first scores, its results -- takes about as long as so many 64-token steps.
-constexpr int kBegin = 4;
+constexpr int kBegin = 2;
 
 struct SharedParams {
   AttnLaunch a;
