@@ -13,7 +13,7 @@
 
 #include <algorithm>
 
-#include "gdn_kv.cuh"
+#include "gdn_attn_plan.cuh"
 #include "gdn_tc.cuh"
 
 namespace gdn {
@@ -58,7 +58,7 @@ __device__ __forceinline__ int rows_of(const AttnLaunch& p) {
 template <bool PART>
 __device__ __forceinline__ RawRow<PART> raw_row(const AttnLaunch& p, int n) {
   if constexpr (PART) {
-    const int4* rec = reinterpret_cast<const int4*>(p.part.recs + n);
+    const int4* rec = reinterpret_cast<const int4*>(part_recs(p.part) + n);
     const int4 a = load(rec), b = load(rec + 1);
     return {a.x, a.y, a.z, a.w, b.x, b.y};
   } else {

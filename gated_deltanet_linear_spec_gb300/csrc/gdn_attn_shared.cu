@@ -79,6 +79,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
   }
   if (warp == 4 * NT) tc::tmem_alloc(&sm.tmem, 512);
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (p.part.plan_here) plan_here<C::kThreads>(p, reinterpret_cast<int*>(ring));
   split::find_shares<C::kRows, 1, C::kThreads, true, kTN, kBegin>(p, sm.sum, sm.deal, &sm.share);
   tc::fence_before();
   __syncthreads();
@@ -98,7 +99,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
   const auto head_of = [&]() { return w.h % kv.Hkv; };
   const auto first_of = [&]() { return w.h / kv.Hkv * C::kRows; };
   const auto tiles_of = [&]() { return NT == 2 && w.u.r.len * p.G - first_of() > 128 ? 2 : 1; };
-  const auto highest = [&]() { return p.window > 0 ? load(&p.part.recs[w.n].hi) : 0; };
+  const auto highest = [&]() { return p.window > 0 ? load(&part_recs(p.part)[w.n].hi) : 0; };
   // Some query may not see some token of [b, b + kTN).  (A row has one unit of a kv-head, so its first query is `lo`'s.)
   const auto in_part_of = [&](int b, int hi) { return in_part(p, b, w.u.lo, hi); };
 
@@ -137,7 +138,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       const int qi = first_of() + tile * 128 + row;
       const bool there = qi < w.u.r.len * p.G;
       // (without a window it does not matter how far behind a group's part its queries stand)
-      const int pos = p.window > 0 && there ? load(&p.part.token[w.u.r.bos + qi / p.G].x)
+      const int pos = p.window > 0 && there ? load(&part_tokens(p.part)[w.u.r.bos + qi / p.G].x)
                                             : min(w.u.lo + qi / p.G, w.u.r.kv - 1);
       float m = -INFINITY, l = 0.f;  // the maximum that the weights refer to (of scores before their scale); their
                                      // sum, both l's and O's 2^-kGrow of e^(s - m)'s

@@ -193,6 +193,7 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, NW>::kThreads, 1)
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");  // what lies before this overlaps the kernel before this one
   if (!PART && tid < NW) P.info[(blockIdx.x * NW + tid) * 8] = 0;
+  if (PART && p.part.plan_here) plan_here<C::kThreads>(p, reinterpret_cast<int*>(smem));
   // (the sums of find_shares lie where the first worker's ring will be)
   find_shares<QG, NW, C::kThreads, PART>(p, reinterpret_cast<int64_t*>(smem), small.deal, small.shares);
   const bool fetches = warp >= NW * C::kTeam;
@@ -314,7 +315,7 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, NW>::kThreads, 1)
       const int qi = wq * 16 + r8 + 8 * e;
       pos[e] = min(PART ? w.u.lo + (q0 + qi) / p.G : seen + qi / p.G, end);
       // (without a window it does not matter how far behind a group's part its queries stand)
-      if (PART && p.window > 0 && qi < nq) pos[e] = load(&p.part.token[row.bos + (q0 + qi) / p.G].x);
+      if (PART && p.window > 0 && qi < nq) pos[e] = load(&part_tokens(p.part)[row.bos + (q0 + qi) / p.G].x);
     }
     const int pmax = PART ? __reduce_max_sync(0xffffffffu, max(pos[0], pos[1])) : end;
     ok = __all_sync(0xffffffffu, ok && tc::mbar_wait(&sm.qfull, seg & 1, P.wait_ns));
@@ -495,7 +496,7 @@ cudaError_t launch_cfg(const AttnLaunch& a, cudaStream_t s) {
   using C = Cfg<D, WQ, DS, NW>;
   static std::atomic<uint64_t> done{0};
   constexpr int smem = (int)(NW * (C::kRing + C::kQ) + sizeof(Small<C, PART>));
-  static_assert(smem <= 232448 && C::kThreads / 32 * 8 <= (int)C::kRing, "shared memory");
+  static_assert(smem <= 232448 && C::kThreads / 32 * 8 <= (int)C::kRing && kPlanInts * 4 <= (int)(NW * C::kRing), "shared memory");
   cudaError_t e = once_per_device(done, [&] {
     return cudaFuncSetAttribute(split_kernel<D, WQ, DS, NW, PART>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   });

@@ -27,6 +27,7 @@ using namespace split;
 constexpr int kWarps = 4;   // workers of a CTA
 constexpr int kPerSm = 2;   // CTAs
 constexpr int kNQ = 8;      // queries of a unit
+static_assert(kSms * kPerSm <= kMaxPassCtas, "copies of the plan");
 
 // 16 bytes' values.
 __device__ __forceinline__ void load16(const float* v, bool there, float (&x)[4]) {
@@ -89,6 +90,7 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) split_fma_kernel(SplitPar
   constexpr int kU = E <= 4 ? 8 : 4;  // tokens whose keys or values a lane holds at a time
   constexpr int kC = 32 / kU;         // as many chunks of keys, then as many of values
   __shared__ __align__(16) float sp[kWarps][32][kNQ];
+  __shared__ int scratch[PART ? kPlanInts : 1];
   __shared__ int64_t part[kWarps];
   __shared__ Deal deal;
   __shared__ Share<PART> shares[kWarps];
@@ -101,6 +103,7 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) split_fma_kernel(SplitPar
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (!PART && lane == 0) P.info[worker * 8] = 0;
+  if (PART && p.part.plan_here) plan_here<32 * kWarps>(p, scratch);
   find_shares<kNQ, kWarps, 32 * kWarps, PART>(p, part, deal, shares);
   const Share<PART>& share = shares[warp];
   const float sl2 = p.scale * 1.4426950408889634f;
@@ -125,7 +128,7 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) split_fma_kernel(SplitPar
     const int mine = lane >> 2;  // the query whose scores, maximum and sum this lane has, those of every 4th token
     int pos = min(first + (q0 + mine) / p.G, pos1);
     // (without a window it does not matter how far behind a group's part its queries stand)
-    if (PART && p.window > 0 && mine < nq) pos = load(&p.part.token[row.bos + (q0 + mine) / p.G].x);
+    if (PART && p.window > 0 && mine < nq) pos = load(&part_tokens(p.part)[row.bos + (q0 + mine) / p.G].x);
     float o[kNQ][E], m = -INFINITY, l = 0.f;
 #pragma unroll
     for (int i = 0; i < kNQ; ++i)

@@ -112,16 +112,27 @@ struct PieceRange {
 // A pass over parts, and where it leaves (m, l, o) of its pieces.  Queries are numbered (local token, q-head), those of groups'
 // parts first, then those of rows' own.
 struct PartDev {
-  const PartRec* recs;
-  int32_t count;        // of this pass
-  int32_t groups;       // of them, those that are groups' (the first)
+  PartRec* recs;        // [count], those of groups first
+  int32_t count;
+  int32_t groups;       // of them, those of groups
   int32_t tokens;       // local tokens of the call
-  const int2* token;    // [tokens]: position (-1: of no well-formed row), whether its row shares a prefix
+  int2* token;          // [tokens]: position (-1: of no well-formed row), whether its row shares a prefix
+  const int32_t* start;   // [groups + 1] first rows of groups
+  const int32_t* prefix;  // [groups] tokens that they may share
+  int32_t plan_here;    // the pass makes recs and token itself, a copy of them for each CTA
   PieceRange* range;    // [2][tokens][Hq]
   float* ml;            // [2][tokens][Hq][2]: m (of the scores before their scale), l of a query in one piece
   float* o;             // [2][tokens][Hq][d], or with `quads` [2][d / 4][tokens][Hq][4]
   int32_t quads;        // o, here and in pieces, by four columns: what neighbouring queries write is side by side
 };
+
+// The plan as this CTA of a pass sees it.  (Where all CTAs write one copy, their stores to one place queue up: 4 us.)
+__device__ __forceinline__ PartRec* part_recs(const PartDev& p) {
+  return p.recs + (p.plan_here ? (size_t)blockIdx.x * p.count : 0);
+}
+__device__ __forceinline__ int2* part_tokens(const PartDev& p) {
+  return p.token + (p.plan_here ? (size_t)blockIdx.x * p.tokens : 0);
+}
 
 struct AttnLaunch {
   KvDev cache;
@@ -231,6 +242,8 @@ cudaError_t launch_attn_split_fma(const AttnLaunch& p, gdn_dtype dtype, cudaStre
 
 // Groups of rows over shared prefixes: the plan of their parts, passes over parts, and the join of what those leave.
 cudaError_t launch_kv_common_prefix(const GroupsLaunch& p, cudaStream_t s);
+bool group_plan_here(const AttnLaunch& p);  // the pass makes its plan itself
+constexpr int kMaxPassCtas = 2 * kSms;      // of a pass over parts
 cudaError_t launch_group_plan(const GroupsLaunch& p, cudaStream_t s);
 // Where a pass leaves its pieces: [2 * workers][queries of a unit] (m, l), and o, with `quads` [2 * workers][d / 4][queries][4].
 struct PartPieces {

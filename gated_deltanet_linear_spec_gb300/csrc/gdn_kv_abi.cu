@@ -253,8 +253,9 @@ SharedWs shared_ws(const AttnLaunch& p, gdn_dtype dtype) {
   SharedWs w{};
   const size_t tokens = p.rows.num_tokens, queries = 2 * tokens * p.Hq;
   w.recs = 0;
-  w.token = round256(w.recs + (size_t)p.part.count * sizeof(PartRec));
-  w.range = round256(w.token + tokens * sizeof(int2));
+  const size_t copies = group_plan_here(p) ? kMaxPassCtas : 1;
+  w.token = round256(w.recs + copies * p.part.count * sizeof(PartRec));
+  w.range = round256(w.token + copies * tokens * sizeof(int2));
   w.ml = round256(w.range + queries * sizeof(PieceRange));
   w.o = round256(w.ml + queries * 8);
   w.pass = round256(w.o + queries * p.cache.d * 4);
@@ -483,6 +484,9 @@ int gdn_shared_attention(const gdn_attn_desc* attn, const gdn_kv_cache* cache, c
   plan.token = reinterpret_cast<int2*>(ws + w.token);
   p.part.recs = plan.recs;
   p.part.token = plan.token;
+  p.part.start = plan.start;
+  p.part.prefix = plan.prefix;
+  p.part.plan_here = group_plan_here(p) ? 1 : 0;
   p.part.range = reinterpret_cast<PieceRange*>(ws + w.range);
   p.part.ml = reinterpret_cast<float*>(ws + w.ml);
   p.part.o = reinterpret_cast<float*>(ws + w.o);
@@ -490,7 +494,7 @@ int gdn_shared_attention(const gdn_attn_desc* attn, const gdn_kv_cache* cache, c
   const Pass pass = pass_of(p, cache->dtype);
   p.part.quads = pass != kFmaPass;
   const cudaStream_t s = (cudaStream_t)stream;
-  if ((rc = cuda_rc(launch_group_plan(plan, s)))) return rc;
+  if (!p.part.plan_here && (rc = cuda_rc(launch_group_plan(plan, s)))) return rc;
   PartPieces pieces;
   if (pass == kSplitPass) {
     pieces = attn_split_parts_pieces(p, p.ws);

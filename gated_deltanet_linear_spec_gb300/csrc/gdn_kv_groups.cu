@@ -2,7 +2,7 @@
 //
 // Both read a few integers per row and entry, 4 bytes an entry and row: what takes time is the launch and the loads that
 // depend on one another (bounds, rows, table).
-#include "gdn_kv.cuh"
+#include "gdn_attn_plan.cuh"
 
 namespace gdn {
 
@@ -29,41 +29,14 @@ __device__ __forceinline__ int from_rank(const int* mine, int rank) {
   return v;
 }
 
-// The group's rows [a, b); false (and the status bit) for bounds that are none.
 __device__ __forceinline__ bool group_rows(const GroupsLaunch& p, int g, int& a, int& b, uint32_t* st) {
   a = load(p.start + g);
   b = load(p.start + g + 1);
-  if (a >= 0 && b >= a && b <= p.rows.num_seqs) return true;
-  set_status(st, GDN_STATUS_ROW_RANGE);
-  return false;
+  return group_bounds(a, b, p.rows.num_seqs, st);
 }
-
-// What a group's rows say together: those with new tokens that are well formed.
-struct Rows {
-  int count;
-  int first;           // the first of them
-  int least;           // tokens before the new ones, of the row that has fewest
-  int bos, eos;        // their local tokens
-  int pos_max;         // the highest position of a query (the lowest is `least`)
-};
-__device__ __forceinline__ void add_row(const GroupsLaunch& p, int n, Rows& s, uint32_t* st) {
+__device__ __forceinline__ void add_row(const GroupsLaunch& p, int n, GroupRows& s, uint32_t* st) {
   KvRow r;
-  if (!load_kv_row(p.rows, p.cache, n, r, st) || r.len == 0) return;
-  ++s.count;
-  s.first = min(s.first, n);
-  s.least = min(s.least, r.kv - r.len);
-  s.bos = min(s.bos, r.bos);
-  s.eos = max(s.eos, r.bos + r.len);
-  s.pos_max = max(s.pos_max, r.kv - 1);
-}
-__device__ __forceinline__ Rows none() { return Rows{0, INT32_MAX, INT32_MAX, INT32_MAX, 0, 0}; }
-__device__ __forceinline__ void warp_meet(Rows& s) {
-  s.count = __reduce_add_sync(0xffffffffu, s.count);
-  s.first = __reduce_min_sync(0xffffffffu, s.first);
-  s.least = __reduce_min_sync(0xffffffffu, s.least);
-  s.bos = __reduce_min_sync(0xffffffffu, s.bos);
-  s.eos = __reduce_max_sync(0xffffffffu, s.eos);
-  s.pos_max = __reduce_max_sync(0xffffffffu, s.pos_max);
+  if (load_kv_row(p.rows, p.cache, n, r, st) && r.len > 0) s.add(n, r.bos, r.len, r.kv);
 }
 
 // ---- common prefix ----------------------------------------------------------------------------
@@ -92,9 +65,9 @@ __global__ void __cluster_dims__(kCluster) __launch_bounds__(THREADS) common_ker
   asm volatile("griddepcontrol.wait;" ::: "memory");
   int a, b;
   if (!group_rows(p, g, a, b, rank == 0 ? p.status : nullptr)) a = b = 0;
-  Rows s = none();
+  GroupRows s;
   for (int n = a + (int)threadIdx.x; n < b; n += THREADS) add_row(p, n, s, rank == 0 ? p.status : nullptr);
-  warp_meet(s);
+  s.warp_meet();
   if (lane == 0) {
     least[warp] = s.least;
     first[warp] = s.first;
@@ -173,14 +146,11 @@ __global__ void __cluster_dims__(kCluster) __launch_bounds__(kThreads) group_pla
   for (int g = me >> 5; g < p.num_groups; g += kAll / 32) {
     int a, b;
     if (!group_rows(p, g, a, b, lane == 0 ? p.status : nullptr)) a = b = 0;
-    Rows s = none();
+    GroupRows s;
     for (int n = a + lane; n < b; n += 32) add_row(p, n, s, nullptr);
-    warp_meet(s);
-    int shared = s.count >= 2 ? min(max(load(p.prefix + g), 0), s.least) : 0;
-    shared -= shared % p.cache.page_size;
-    // behind all windows, with nothing in front that stays visible, no query sees any of it
-    const int low = p.window > 0 ? max(0, s.least - p.window + 1) : 0;
-    const bool seen = shared > low || (shared > 0 && min(p.sinks, low) > 0);
+    s.warp_meet();
+    bool seen;
+    const int shared = s.shared(load(p.prefix + g), p.cache.page_size, p.window, p.sinks, seen);
     for (int i = a; shared > 0 && i < b; i += lanes ? 1 : 32) {
       const int n = lanes ? i : i + lane;
       KvRow r;
@@ -189,8 +159,7 @@ __global__ void __cluster_dims__(kCluster) __launch_bounds__(kThreads) group_pla
       if (seen) place_tokens(p.token, r, lanes ? lane : 0, lanes ? 32 : 1, 1);
     }
     if (lane == 0) {
-      PartRec rec{};
-      if (seen) rec = {s.bos, s.eos - s.bos, 0, shared, table_row_of(p, s.first), s.least, s.pos_max, 0};
+      const PartRec rec = seen ? s.record(shared, table_row_of(p, s.first)) : PartRec{};
       p.recs[g] = rec;
     }
   }
@@ -216,6 +185,12 @@ cudaError_t launch_kv_common_prefix(const GroupsLaunch& p, cudaStream_t s) {
   const int64_t entries = (int64_t)p.cache.max_pages * p.rows.num_seqs / p.num_groups;
   return entries > kCluster * kThreads * kAhead ? launch_cluster(common_kernel<1024>, p.num_groups, 1024, p, s)
                                                 : launch_cluster(common_kernel<kThreads>, p.num_groups, kThreads, p, s);
+}
+
+// Every CTA goes over all rows, groups and tokens then, which takes it longer than the launch of a kernel would for more of
+// them.
+bool group_plan_here(const AttnLaunch& p) {
+  return p.rows.num_seqs <= kPlanRows && p.part.groups <= kPlanGroups && p.rows.num_tokens <= 4 * kPlanRows;
 }
 
 cudaError_t launch_group_plan(const GroupsLaunch& p, cudaStream_t s) {

@@ -180,6 +180,17 @@ def test_long_rows(longest, dim, dtype):
     Groups(groups, heads=4, kv_heads=2, dim=dim, dtype=dtype, seed=longest, window=100, sinks=3).check()
 
 
+def test_rows_of_many_tokens():
+    Groups([(300, [(700, 1000), (400, 700)]), (30, [(3, 40)])], heads=2, kv_heads=1, dim=32, dtype=F32, seed=2).check()
+
+
+@pytest.mark.parametrize("dim,dtype", [(64, BF16), (64, F32)])
+def test_more_rows_than_a_pass_plans_itself(dim, dtype):
+    groups = [(48, [(1 + i % 2, 50 + i % 7) for i in range(5)]) for _ in range(53)]
+    Groups(groups, lone=[(1, 20)], heads=2, kv_heads=1, dim=dim, dtype=dtype, seed=3).check()
+    Groups(groups, heads=2, kv_heads=1, dim=dim, dtype=dtype, window=30, sinks=2, seed=4).check()
+
+
 def test_rows_without_tokens_do_not_stand_for_their_group():
     s = Groups([(64, [(0, 64), (1, 80), (2, 90)]), (48, [(0, 48), (0, 50)]), (32, [(1, 40)])], dim=128)
     s.table[s.table_rows[0]] = 0  # a finished row, whose pages were given back
