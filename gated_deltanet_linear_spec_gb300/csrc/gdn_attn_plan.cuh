@@ -54,16 +54,18 @@ struct GroupRows {
 };
 
 // A plan of few rows is made by every CTA of the pass for itself, which saves the launch of a kernel for it.  (The join reads
-// the first one's.)  scratch: kPlanInts.  All threads call.
+// the first one's.)  scratch: kPlanInts, 16-byte aligned; returns the parts there.  All threads call.
 constexpr int kPlanRows = 256, kPlanGroups = 64;
-constexpr int kPlanInts = 5 * kPlanRows + 4 * kPlanGroups + 1;
+constexpr int kPlanRecs = (kPlanRows + kPlanGroups) * (int)(sizeof(PartRec) / 4);
+constexpr int kPlanInts = kPlanRecs + 5 * kPlanRows + 2 * kPlanGroups + 1;
 
 template <int THREADS>
-__device__ void plan_here(const AttnLaunch& p, int* scratch) {
+__device__ const PartRec* plan_here(const AttnLaunch& p, int* scratch) {
   const PartDev& part = p.part;
   const KvRowsDev& R = p.rows;
   const int tid = threadIdx.x, lane = tid & 31;
-  int* first = scratch;                // of a row: query_start_loc
+  PartRec* near = reinterpret_cast<PartRec*>(scratch);
+  int* first = scratch + kPlanRecs;    // of a row: query_start_loc
   int* len = first + kPlanRows;        // new tokens, 0 for a row that is none
   int* kv = len + kPlanRows;
   int* trow = kv + kPlanRows;
@@ -99,11 +101,11 @@ __device__ void plan_here(const AttnLaunch& p, int* scratch) {
       tokens = s.shared(prefix[g], p.cache.page_size, p.window, p.sinks, seen);
       for (int n = a + lane; n < b; n += 32) own[n] = tokens + (seen ? 1 : 0);
     }
-    if (lane == 0) recs[g] = seen ? s.record(tokens, trow[s.first]) : PartRec{};
+    if (lane == 0) recs[g] = near[g] = seen ? s.record(tokens, trow[s.first]) : PartRec{};
   }
   __syncthreads();
   for (int n = tid; n < R.num_seqs; n += THREADS)
-    recs[part.groups + n] =
+    recs[part.groups + n] = near[part.groups + n] =
         len[n] > 0 ? PartRec{first[n], len[n], own[n] & ~1, kv[n], trow[n], kv[n] - len[n], kv[n] - 1, 0} : PartRec{};
   // (the pass itself looks tokens up under a window; the join does in any case)
   if (p.window > 0 || blockIdx.x == 0) {
@@ -116,6 +118,7 @@ __device__ void plan_here(const AttnLaunch& p, int* scratch) {
     }
   }
   __syncthreads();
+  return near;
 }
 
 }  // namespace gdn

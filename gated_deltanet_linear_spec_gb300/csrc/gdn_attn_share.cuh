@@ -55,9 +55,11 @@ template <bool PART>
 __device__ __forceinline__ int rows_of(const AttnLaunch& p) {
   return PART ? p.part.count : p.rows.num_seqs;
 }
+// near: the parts in shared memory, if they are there.
 template <bool PART>
-__device__ __forceinline__ RawRow<PART> raw_row(const AttnLaunch& p, int n) {
+__device__ __forceinline__ RawRow<PART> raw_row(const AttnLaunch& p, int n, const PartRec* near = nullptr) {
   if constexpr (PART) {
+    if (near) return {near[n].bos, near[n].len, near[n].from, near[n].end, near[n].trow, near[n].lo};
     const int4* rec = reinterpret_cast<const int4*>(part_recs(p.part) + n);
     const int4 a = load(rec), b = load(rec + 1);
     return {a.x, a.y, a.z, a.w, b.x, b.y};
@@ -109,8 +111,8 @@ __device__ __forceinline__ Unit unit_of(const AttnLaunch& p, const RawRow<PART>&
 }
 // The cost in tiles of all units of row n.
 template <int QG, bool PART, int TN, int START>
-__device__ __forceinline__ int64_t row_cost(const AttnLaunch& p, int n, uint32_t* st) {
-  const Unit u = unit_of<QG, PART, TN>(p, raw_row<PART>(p, n), st);
+__device__ __forceinline__ int64_t row_cost(const AttnLaunch& p, int n, uint32_t* st, const PartRec* near) {
+  const Unit u = unit_of<QG, PART, TN>(p, raw_row<PART>(p, n, near), st);
   return (int64_t)u.cost(START) * u.per;
 }
 
@@ -146,14 +148,16 @@ struct Share {
   RawRow<PART> raw;  // that row
 };
 
-// The shares of the CTA's workers; part: one value per warp.  All threads call.
+// The shares of the CTA's workers; part: one value per warp; near: the parts in shared memory, if they are there.  All
+// threads call.
 template <int QG, int NW, int THREADS, bool PART = false, int TN = kTN, int START = kStart>
-__device__ void find_shares(const AttnLaunch& p, int64_t* part, Deal& deal, Share<PART>* shares) {
+__device__ void find_shares(const AttnLaunch& p, int64_t* part, Deal& deal, Share<PART>* shares,
+                            const PartRec* near = nullptr) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rows = rows_of<PART>(p), per = (rows + THREADS - 1) / THREADS;
   const int n0 = min(tid * per, rows), n1 = min(n0 + per, rows);
   int64_t mine = 0;
-  for (int n = n0; n < n1; ++n) mine += row_cost<QG, PART, TN, START>(p, n, blockIdx.x == 0 ? p.status : nullptr);
+  for (int n = n0; n < n1; ++n) mine += row_cost<QG, PART, TN, START>(p, n, blockIdx.x == 0 ? p.status : nullptr, near);
   int64_t inc = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -188,14 +192,14 @@ __device__ void find_shares(const AttnLaunch& p, int64_t* part, Deal& deal, Shar
       int n = n0;
       if (per > 1) {
         for (; n < n1; ++n) {
-          const int64_t t = row_cost<QG, PART, TN, START>(p, n, nullptr);
+          const int64_t t = row_cost<QG, PART, TN, START>(p, n, nullptr, near);
           if (s.first < at + t) break;
           at += t;
         }
       }
       s.row = n;
       s.into = s.first - at;
-      s.raw = raw_row<PART>(p, n);
+      s.raw = raw_row<PART>(p, n, near);
       shares[w] = s;
     }
   }

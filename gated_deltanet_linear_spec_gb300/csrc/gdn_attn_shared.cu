@@ -79,8 +79,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
   }
   if (warp == 4 * NT) tc::tmem_alloc(&sm.tmem, 512);
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (p.part.plan_here) plan_here<C::kThreads>(p, reinterpret_cast<int*>(ring));
-  split::find_shares<C::kRows, 1, C::kThreads, true, kTN, kBegin>(p, sm.sum, sm.deal, &sm.share);
+  const PartRec* near = p.part.plan_here ? plan_here<C::kThreads>(p, reinterpret_cast<int*>(ring)) : nullptr;
+  split::find_shares<C::kRows, 1, C::kThreads, true, kTN, kBegin>(p, sm.sum, sm.deal, &sm.share, near);
   tc::fence_before();
   __syncthreads();
   tc::fence_after();

@@ -193,9 +193,10 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, NW>::kThreads, 1)
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");  // what lies before this overlaps the kernel before this one
   if (!PART && tid < NW) P.info[(blockIdx.x * NW + tid) * 8] = 0;
-  if (PART && p.part.plan_here) plan_here<C::kThreads>(p, reinterpret_cast<int*>(smem));
+  const PartRec* near = nullptr;
+  if (PART && p.part.plan_here) near = plan_here<C::kThreads>(p, reinterpret_cast<int*>(smem + 1024));
   // (the sums of find_shares lie where the first worker's ring will be)
-  find_shares<QG, NW, C::kThreads, PART>(p, reinterpret_cast<int64_t*>(smem), small.deal, small.shares);
+  find_shares<QG, NW, C::kThreads, PART>(p, reinterpret_cast<int64_t*>(smem), small.deal, small.shares, near);
   const bool fetches = warp >= NW * C::kTeam;
   const int wk = fetches ? warp - NW * C::kTeam : warp / C::kTeam;  // the warp's worker
   auto& sm = small.worker[wk];
@@ -496,7 +497,7 @@ cudaError_t launch_cfg(const AttnLaunch& a, cudaStream_t s) {
   using C = Cfg<D, WQ, DS, NW>;
   static std::atomic<uint64_t> done{0};
   constexpr int smem = (int)(NW * (C::kRing + C::kQ) + sizeof(Small<C, PART>));
-  static_assert(smem <= 232448 && C::kThreads / 32 * 8 <= (int)C::kRing && kPlanInts * 4 <= (int)(NW * C::kRing), "shared memory");
+  static_assert(smem <= 232448 && C::kThreads / 32 * 8 <= (int)C::kRing && kPlanInts * 4 + 1024 <= (int)(NW * C::kRing), "shared memory");
   cudaError_t e = once_per_device(done, [&] {
     return cudaFuncSetAttribute(split_kernel<D, WQ, DS, NW, PART>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   });

@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) split_fma_kernel(SplitPar
   constexpr int kU = E <= 4 ? 8 : 4;  // tokens whose keys or values a lane holds at a time
   constexpr int kC = 32 / kU;         // as many chunks of keys, then as many of values
   __shared__ __align__(16) float sp[kWarps][32][kNQ];
-  __shared__ int scratch[PART ? kPlanInts : 1];
+  __shared__ __align__(16) int scratch[PART ? kPlanInts : 4];
   __shared__ int64_t part[kWarps];
   __shared__ Deal deal;
   __shared__ Share<PART> shares[kWarps];
@@ -103,8 +103,9 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) split_fma_kernel(SplitPar
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (!PART && lane == 0) P.info[worker * 8] = 0;
-  if (PART && p.part.plan_here) plan_here<32 * kWarps>(p, scratch);
-  find_shares<kNQ, kWarps, 32 * kWarps, PART>(p, part, deal, shares);
+  const PartRec* near = nullptr;
+  if (PART && p.part.plan_here) near = plan_here<32 * kWarps>(p, scratch);
+  find_shares<kNQ, kWarps, 32 * kWarps, PART>(p, part, deal, shares, near);
   const Share<PART>& share = shares[warp];
   const float sl2 = p.scale * 1.4426950408889634f;
   const int shift = __ffs(kv.page_size) - 1;
