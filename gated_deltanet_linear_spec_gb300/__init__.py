@@ -191,10 +191,11 @@ def _ptr(t: Optional[torch.Tensor], dtype: Optional[torch.dtype] = None, name: s
          device: Optional[int] = None) -> Optional[int]:
     if t is None:
         return None
-    if not t.is_cuda:
+    at = t.get_device()
+    if at < 0:
         raise TypeError(f"{name}: expected a CUDA tensor")
-    if device is not None and t.get_device() != device:
-        raise ValueError(f"{name} is on cuda:{t.get_device()}, other tensors of the call on cuda:{device}")
+    if device is not None and at != device:
+        raise ValueError(f"{name} is on cuda:{at}, other tensors of the call on cuda:{device}")
     if not t.is_contiguous():
         raise TypeError(f"{name}: expected a contiguous tensor")
     if dtype is not None and t.dtype != dtype:
@@ -684,18 +685,21 @@ def gdn_kv_common_prefix(cache: KvCache, rows: KvRows, groups: KvGroups, status:
 def gdn_rope(rope: Rope, positions: torch.Tensor, x: torch.Tensor, out: torch.Tensor, stream=None) -> None:
     """Turns the heads of x [tokens, heads, head_dim] by ``positions`` (int32, one per token, or of the first tokens) into
     ``out``, which may be x.  At negated positions it is the gradient with respect to x."""
-    if x.dim() != 3:
-        raise ValueError(f"x: expected [tokens, heads, head_dim], got {tuple(x.shape)}")
-    device = x.get_device()
-    heads, dim = x.shape[1:]
-    xp, xs, tokens = _token_rows(x, x.dtype, heads, dim, "x", device)
-    op, os_, of_out = _token_rows(out, x.dtype, heads, dim, "out", device)
+    shape = x.shape
+    if len(shape) != 3:
+        raise ValueError(f"x: expected [tokens, heads, head_dim], got {tuple(shape)}")
+    _, heads, dim = shape
+    device, dtype = x.get_device(), x.dtype
+    xp, xs, tokens = _token_rows(x, dtype, heads, dim, "x", device)
+    op, os_, of_out = (xp, xs, tokens) if out is x else _token_rows(out, dtype, heads, dim, "out", device)
     n = positions.numel()
     if tokens != of_out or n > tokens:
         raise ValueError("positions, x and out: expected one token count, or fewer positions")
-    _on_current(device)
-    _of_device(rope, device, "frequencies' table")
-    _check(library().gdn_rope(rope._ref, heads, dim, _dtype_code(x.dtype), _int32(positions, "positions", None, device), n,
+    if _current_device() != device:
+        _on_current(device)
+    if rope._device != device:
+        _of_device(rope, device, "frequencies' table")
+    _check(library().gdn_rope(rope._ref, heads, dim, _dtype_code(dtype), _int32(positions, "positions", None, device), n,
                               xp, xs, op, os_, _stream_of(x, stream)))
 
 
@@ -705,8 +709,9 @@ def gdn_kv_append_rope(cache: KvCache, rows: KvRows, rope: Rope, k: torch.Tensor
     """gdn_kv_append with the new tokens' keys turned by their positions on the way, and the queries q
     [num_global_tokens, num_q_heads, head_dim] of the same tokens turned into ``q_out`` (None: in place)."""
     _, heads, _, dim = cache.k_pool.shape
-    kp, ks, tokens = _token_rows(k, cache.dtype, heads, dim, "k", cache._device)
-    vp, vs, of_v = _token_rows(v, cache.dtype, heads, dim, "v", cache._device)
+    dtype, device = cache.dtype, cache._device
+    kp, ks, tokens = _token_rows(k, dtype, heads, dim, "k", device)
+    vp, vs, of_v = _token_rows(v, dtype, heads, dim, "v", device)
     if tokens != of_v:
         raise ValueError("k and v: expected one token count")
     hq, qp, qs, op, os_ = 0, None, 0, None, 0
@@ -714,14 +719,15 @@ def gdn_kv_append_rope(cache: KvCache, rows: KvRows, rope: Rope, k: torch.Tensor
         if q.dim() != 3:
             raise ValueError(f"q: expected [tokens, heads, head_dim], got {tuple(q.shape)}")
         hq = q.shape[1]
-        qp, qs, of_q = _token_rows(q, cache.dtype, hq, dim, "q", cache._device)
-        op, os_, of_out = _token_rows(q if q_out is None else q_out, cache.dtype, hq, dim, "q_out", cache._device)
+        qp, qs, of_q = _token_rows(q, dtype, hq, dim, "q", device)
+        op, os_, of_out = (qp, qs, of_q) if q_out is None else _token_rows(q_out, dtype, hq, dim, "q_out", device)
         if tokens != of_q or tokens != of_out:
             raise ValueError("k, v, q and q_out: expected one token count")
     elif q_out is not None:
         raise ValueError("q_out without q")
-    device = _on_current(cache._device, rows)
-    _of_device(rope, device, "frequencies' table")
+    _on_current(device, rows)
+    if rope._device != device:
+        _of_device(rope, device, "frequencies' table")
     _check(library().gdn_kv_append_rope(cache._ref, rows._ref, rope._ref, kp, ks, vp, vs, hq, qp, qs, op, os_, tokens,
                                         _ptr(status, torch.int32, "status", device), _stream_of(cache.k_pool, stream)))
 

@@ -27,7 +27,10 @@ using namespace split;
 constexpr int kWarps = 4;   // workers of a CTA
 constexpr int kPerSm = 2;   // CTAs
 constexpr int kNQ = 8;      // queries of a unit
-static_assert(kSms * kPerSm <= kMaxPassCtas, "copies of the plan");
+// CTAs of an SM in a pass over parts: with few columns a lane its registers leave room for more.
+constexpr int kPartsPerSm = 3;
+constexpr int per_sm(int d, bool part) { return part && d <= 64 ? kPartsPerSm : kPerSm; }
+static_assert(kSms * kPartsPerSm <= kMaxPassCtas, "copies of the plan");
 
 // 16 bytes' values.
 __device__ __forceinline__ void load16(const float* v, bool there, float (&x)[4]) {
@@ -86,7 +89,7 @@ __device__ __forceinline__ void load_row(const __nv_bfloat16* v, bool there, flo
 // E: columns of a lane, 32 E are head_dim or more; DC: head_dim where it is 32 E, else 0.
 // PART: a pass over parts (see gdn_attn_share.cuh).
 template <typename T, int E, int DC, bool PART = false>
-__global__ void __launch_bounds__(32 * kWarps, kPerSm) split_fma_kernel(SplitParams P) {
+__global__ void __launch_bounds__(32 * kWarps, per_sm(32 * E, PART)) split_fma_kernel(SplitParams P) {
   constexpr int kU = E <= 4 ? 8 : 4;  // tokens whose keys or values a lane holds at a time
   constexpr int kC = 32 / kU;         // as many chunks of keys, then as many of values
   __shared__ __align__(16) float sp[kWarps][32][kNQ];
@@ -315,7 +318,7 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) split_fma_kernel(SplitPar
 
 template <bool PART, typename T, int E, int DC>
 cudaError_t launch_as(const AttnLaunch& a, cudaStream_t s) {
-  constexpr int ctas = kSms * kPerSm;
+  constexpr int ctas = kSms * per_sm(32 * E, PART);
   SplitParams P{};
   P.a = a;
   P.info = static_cast<int32_t*>(a.ws);
@@ -366,10 +369,12 @@ cudaError_t launch_attn_split_fma(const AttnLaunch& a, gdn_dtype dtype, cudaStre
   return launch_type<false>(a, dtype, s);
 }
 
-size_t attn_split_fma_parts_workspace(const AttnLaunch& a) { return attn_split_fma_workspace(a); }
+size_t attn_split_fma_parts_workspace(const AttnLaunch& a) {
+  return (size_t)kSms * per_sm(a.cache.d, true) * kWarps * (8 + 4 * kNQ + 2 * kNQ * a.cache.d) * 4;
+}
 
 PartPieces attn_split_fma_parts_pieces(const AttnLaunch& a, void* ws) {
-  constexpr int workers = kSms * kPerSm * kWarps;
+  const int workers = kSms * per_sm(a.cache.d, true) * kWarps;
   float* stats = static_cast<float*>(ws) + 8 * workers;
   return {stats, stats + (size_t)4 * workers * kNQ, kNQ};
 }

@@ -243,7 +243,7 @@ cudaError_t launch_attn_split_fma(const AttnLaunch& p, gdn_dtype dtype, cudaStre
 // Groups of rows over shared prefixes: the plan of their parts, passes over parts, and the join of what those leave.
 cudaError_t launch_kv_common_prefix(const GroupsLaunch& p, cudaStream_t s);
 bool group_plan_here(const AttnLaunch& p);  // the pass makes its plan itself
-constexpr int kMaxPassCtas = 2 * kSms;      // of a pass over parts
+constexpr int kMaxPassCtas = 3 * kSms;      // of a pass over parts
 cudaError_t launch_group_plan(const GroupsLaunch& p, cudaStream_t s);
 // Where a pass leaves its pieces: [2 * workers][queries of a unit] (m, l), and o, with `quads` [2 * workers][d / 4][queries][4].
 struct PartPieces {
