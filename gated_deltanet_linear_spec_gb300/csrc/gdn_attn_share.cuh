@@ -70,12 +70,11 @@ __device__ __forceinline__ RawRow<PART> raw_row(const AttnLaunch& p, int n, cons
 }
 template <bool PART>
 __device__ __forceinline__ RawRow<PART> raw_of_lane(const RawRow<PART>& r, int src) {
-  RawRow<PART> x;
-  int* to = reinterpret_cast<int*>(&x);
-  const int* from = reinterpret_cast<const int*>(&r);
-#pragma unroll
-  for (int i = 0; i < (int)(sizeof(x) / 4); ++i) to[i] = __shfl_sync(0xffffffffu, from[i], src);
-  return x;
+  const auto of = [&](int v) { return __shfl_sync(0xffffffffu, v, src); };
+  if constexpr (PART)
+    return {of(r.bos), of(r.len), of(r.from), of(r.end), of(r.trow), of(r.lo)};
+  else
+    return {of(r.bos), of(r.eos), of(r.kv), of(r.trow)};
 }
 
 // The tiles that the row's queries see; 0 for an empty or bad row.  QG: queries of a unit, 0 for all

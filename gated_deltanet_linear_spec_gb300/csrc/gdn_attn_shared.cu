@@ -23,6 +23,9 @@ using namespace tile;
 // Beginning a unit -- its queries, the first scores, its results -- takes about as long as so many 64-token steps.
 constexpr int kBegin = 2;
 
+// K and V pairs in the ring: 128 KB, which keeps HBM busy under short steps too.
+__host__ __device__ constexpr int phases_of(int d) { return 512 / d; }
+
 struct SharedParams {
   AttnLaunch a;
   float* o;      // [2 * kSms][kRows][D]
@@ -32,15 +35,15 @@ struct SharedParams {
 
 template <int D>
 struct Small {
-  uint64_t full[Cfg<D>::kRing], empty[Cfg<D>::kRing];
-  uint64_t checked[Cfg<D>::kPhases];  // of a V tile
+  uint64_t full[2 * phases_of(D)], empty[2 * phases_of(D)];
+  uint64_t checked[phases_of(D)];  // of a V tile
   uint64_t q_ready[2], drain[2];
   uint64_t s_ready[2][2], p_ready[2][2], pv_done[2][2];  // [query tile][score buffer]
   int64_t sum[Cfg<D>::kThreads / 32];
   split::Deal deal;
   split::Share<true> share;
-  uint32_t bad[Cfg<D>::kPhases][2];  // listed tokens of a V tile
-  uint32_t held[16];                 // per tile, counted over all units, % 16: which of its pages hold tokens
+  uint32_t bad[phases_of(D)][2];  // listed tokens of a V tile
+  uint32_t held[16];              // per tile, counted over all units, % 16: which of its pages hold tokens
   uint32_t tmem;
 };
 
@@ -49,7 +52,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     shared_kernel(SharedParams P, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
   using C = Cfg<D>;
   using Units = split::Walk<C::kRows, true, kTN, kBegin>;
-  constexpr int NT = C::kTiles, R = C::kRing, CB = D / 64, kPh = C::kPhases;
+  constexpr int NT = C::kTiles, kPh = phases_of(D), R = 2 * kPh, CB = D / 64;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* ring = smem + NT * C::kQ;
   Small<D>& sm = *reinterpret_cast<Small<D>*>(ring + R * C::kKv);
@@ -315,7 +318,11 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     __syncwarp();
   } else if (role == 2) {
     // ---- fetches: a lane per page of the tile ----
-    const int bi = lane, spp = slabs_per_page(kv);
+    // With a long ring K's pages and V's go together, a half of the warp each, in half the time (a step of one query tile is
+    // short: 64 rows of 8000 own tokens, pages of 16, d = 64, 327 us one after the other, 283 together); with a short one K does
+    // not wait for V's place.
+    constexpr bool kTogether = kPh > 2;
+    const int bi = kTogether ? lane & 15 : lane, spp = slabs_per_page(kv);
     const int none = (kv.num_pages - 1) * spp + kv.Hkv;  // a slab past the pool
     const bool active = bi < boxes;
     uint32_t fetched = 0;  // tiles fetched, K and V
@@ -324,7 +331,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       const int entries = (w.u.r.kv + ps - 1) >> shift, h = head_of();
       int eb = -64, ids = 0, ahead = 0;  // 32 table entries are held, one per lane, and the 32 behind them
       for (int j = w.j0; j < w.j0 + w.len && ok; ++j, at += 2, ++tiles) {
-        const int pos = w.tile_at(j) + bi * box, e = w.tile_at(j) >> shift;
+        const int b = w.tile_at(j), pos = b + bi * box, e = b >> shift;
         if (e >= eb + 32) {
           if (e < eb + 64) {
             ids = ahead;
@@ -337,22 +344,18 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         }
         int page = __shfl_sync(0xffffffffu, ids, active ? (pos >> shift) - eb : 0);
         page = active && pos < w.u.r.kv ? page_or_null(page, kv, p.status) : 0;
-        const uint32_t mask = __ballot_sync(0xffffffffu, page > 0);
-        for (int v = 0; v < 2; ++v) {
+        const uint32_t mask = __ballot_sync(0xffffffffu, page > 0) & 0xffffu;
+        const int slot = pos & (ps - 1), slab = page > 0 ? page * spp + h : none;
+        for (int v = kTogether ? lane >> 4 : 0; v < 2; v += kTogether ? 2 : 1) {
           const uint32_t a = at + v, en = a % R;
           ok = __all_sync(0xffffffffu, a < R || tc::mbar_wait(&sm.empty[en], (a / R - 1) & 1, P.wait_ns));
           if (!ok) break;
-          if (lane == 0) {
-            if (v == 0) sm.held[tiles & 15] = mask;
-            tc::expect_tx(&sm.full[en], C::kKv);
-          }
+          if (bi == 0) tc::expect_tx(&sm.full[en], C::kKv);
+          if (lane == 0 && v == 0) sm.held[tiles & 15] = mask;
           __syncwarp();
-          if (active)
-            tc::tma_page(ring + en * C::kKv + bi * box * D * 2, v ? &vmap : &kmap, pos & (ps - 1),
-                         page > 0 ? page * spp + h : none, &sm.full[en]);
-          fetched = a + 1;
+          if (active) tc::tma_page(ring + en * C::kKv + bi * box * D * 2, v ? &vmap : &kmap, slot, slab, &sm.full[en]);
+          fetched = kTogether ? at + 2 : a + 1;
         }
-        if (!ok) break;
       }
     }
     // No copy may be in flight when the CTA ends (the products wait for every tile, so this passes at
@@ -419,7 +422,7 @@ template <int D>
 cudaError_t launch_d(const AttnLaunch& a, cudaStream_t s) {
   using C = Cfg<D>;
   static std::atomic<uint64_t> done{0};
-  constexpr int smem = (int)(C::kSmem + sizeof(Small<D>));
+  constexpr int smem = (int)(C::kTiles * C::kQ + 2 * phases_of(D) * C::kKv + sizeof(Small<D>));
   static_assert(smem <= 232448, "shared memory");
   cudaError_t e = once_per_device(done, [&] {
     return cudaFuncSetAttribute(shared_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
