@@ -151,7 +151,7 @@ __device__ __forceinline__ void values_step(float (&o)[DV / 8][4], const uint32_
 }
 
 // What a CTA keeps in shared memory behind its rings and queries.
-template <typename C, bool PART>
+template <typename C>
 struct Small {
   struct Worker {
     uint64_t full[C::kStages], empty[C::kStages], qfull, qempty;
@@ -159,17 +159,16 @@ struct Small {
     uint8_t held[C::kStages];  // per stage: which halves of the tile lie in pages that hold tokens
   } worker[C::kWorkers];
   Deal deal;
-  Share<PART> shares[C::kWorkers];
+  Share<false> shares[C::kWorkers];
 };
 
-// PART: a pass over parts (see gdn_attn_share.cuh), in units of up to kNQ queries.
-template <int D, int WQ, int DS, int NW, bool PART = false>
+template <int D, int WQ, int DS, int NW>
 __global__ void __launch_bounds__(Cfg<D, WQ, DS, NW>::kThreads, 1)
     split_kernel(SplitParams P, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
   using C = Cfg<D, WQ, DS, NW>;
-  constexpr int S = C::kStages, DV = C::kDV, QG = PART ? C::kNQ : 0;
+  constexpr int S = C::kStages, DV = C::kDV;
   extern __shared__ __align__(1024) uint8_t smem[];
-  Small<C, PART>& small = *reinterpret_cast<Small<C, PART>*>(smem + NW * (C::kRing + C::kQ));
+  Small<C>& small = *reinterpret_cast<Small<C>*>(smem + NW * (C::kRing + C::kQ));
   const AttnLaunch& p = P.a;
   const KvDev& kv = p.cache;
   // The warp's number comes from a shuffle, so that the compiler takes it as one value of the warp.  (In an early form
@@ -192,15 +191,13 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, NW>::kThreads, 1)
     tc::prefetch_map(&vmap);
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");  // what lies before this overlaps the kernel before this one
-  if (!PART && tid < NW) P.info[(blockIdx.x * NW + tid) * 8] = 0;
-  const PartRec* near = nullptr;
-  if (PART && p.part.plan_here) near = plan_here<C::kThreads>(p, reinterpret_cast<int*>(smem + 1024));
+  if (tid < NW) P.info[(blockIdx.x * NW + tid) * 8] = 0;
   // (the sums of find_shares lie where the first worker's ring will be)
-  find_shares<QG, NW, C::kThreads, PART>(p, reinterpret_cast<int64_t*>(smem), small.deal, small.shares, near);
+  find_shares<0, NW, C::kThreads>(p, reinterpret_cast<int64_t*>(smem), small.deal, small.shares);
   const bool fetches = warp >= NW * C::kTeam;
   const int wk = fetches ? warp - NW * C::kTeam : warp / C::kTeam;  // the warp's worker
   auto& sm = small.worker[wk];
-  const Share<PART>& share = small.shares[wk];
+  const Share<false>& share = small.shares[wk];
   uint8_t* ring = smem + wk * C::kRing;
   uint8_t* qbuf = smem + NW * C::kRing + wk * C::kQ;
   const int ps = kv.page_size;
@@ -215,8 +212,7 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, NW>::kThreads, 1)
     const bool active = bi < boxes;
     int it = 0, seg = 0;
     bool ok = true;
-    for (Walk<QG, PART> w(p, share); w.valid() && ok; w.next(), ++seg) {
-      const int h = PART ? w.h % kv.Hkv : w.h, q0 = PART ? w.h / kv.Hkv * QG : 0;
+    for (Walk<0> w(p, share); w.valid() && ok; w.next(), ++seg) {
       // 32 table entries are held, one per lane, and the 32 behind them are on their way
       const int32_t* row = kv.table + (int64_t)w.u.r.trow * kv.max_pages;
       const int entries = (w.u.r.kv + ps - 1) >> shift;
@@ -224,14 +220,14 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, NW>::kThreads, 1)
       int ids = eb + lane < entries ? load(row + eb + lane) : 0;
       int ahead = eb + 32 + lane < entries ? load(row + eb + 32 + lane) : 0;
       // the unit's queries
-      const int nq = PART ? min(QG, w.u.r.len * p.G - q0) : w.u.r.len * p.G;
+      const int nq = w.u.r.len * p.G;
       int g[2];
       int rows = 0;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int qi = lane + 32 * u;
         g[u] = -1;
-        if (qi < nq) g[u] = kv_token(p.rows, w.u.r.bos + (q0 + qi) / p.G, p.num_global, p.status);
+        if (qi < nq) g[u] = kv_token(p.rows, w.u.r.bos + qi / p.G, p.num_global, p.status);
         rows += __popc(__ballot_sync(0xffffffffu, g[u] >= 0));
       }
       ok = seg == 0 || tc::mbar_wait(&sm.qempty, (seg - 1) & 1, P.wait_ns);
@@ -249,7 +245,7 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, NW>::kThreads, 1)
         if (g[u] >= 0)
           tc::bulk_g2s(qbuf + qi * C::kPitch,
                        static_cast<const __nv_bfloat16*>(p.q) + (int64_t)g[u] * p.q_stride +
-                           (int64_t)(h * p.G + (q0 + qi) % p.G) * D,
+                           (int64_t)(w.h * p.G + qi % p.G) * D,
                        D * 2, &sm.qfull);
       }
       for (int j = w.j0; j < w.j0 + w.len; ++j, ++it) {
@@ -280,7 +276,7 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, NW>::kThreads, 1)
         __syncwarp();
         if (active) {
           uint8_t* dst = ring + (size_t)s * 2 * C::kHalf + is_v * C::kHalf + (size_t)bi * box * D * 2;
-          tc::tma_page(dst, is_v ? &vmap : &kmap, pos & (ps - 1), page > 0 ? page * spp + h : none, &sm.full[s]);
+          tc::tma_page(dst, is_v ? &vmap : &kmap, pos & (ps - 1), page > 0 ? page * spp + w.h : none, &sm.full[s]);
         }
       }
     }
@@ -299,12 +295,10 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, NW>::kThreads, 1)
   const float sl2 = p.scale * 1.4426950408889634f;
   int it = 0, seg = 0;
   bool ok = true;
-  for (Walk<QG, PART> w(p, share); w.valid(); w.next(), ++seg) {
+  for (Walk<0> w(p, share); w.valid(); w.next(), ++seg) {
     const KvRow row = w.u.r;
-    const int h = PART ? w.h % kv.Hkv : w.h, q0 = PART ? w.h / kv.Hkv * QG : 0;
-    const int nq = PART ? min(QG, row.len * p.G - q0) : row.len * p.G;
-    // tokens up to `seen` are seen by all queries, but for the window; up to `end` by some
-    const int end = row.kv - 1, seen = PART ? min(w.u.lo, end) : row.kv - row.len;
+    const int nq = row.len * p.G;
+    const int pmin = row.kv - row.len, pmax = row.kv - 1;
     float o[DV / 8][4], m[2], l[2];
     int pos[2];  // the positions of this thread's two queries, r8 and r8 + 8 of the group's 16
 #pragma unroll
@@ -313,12 +307,8 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, NW>::kThreads, 1)
     for (int e = 0; e < 2; ++e) {
       m[e] = -INFINITY;
       l[e] = 0.f;
-      const int qi = wq * 16 + r8 + 8 * e;
-      pos[e] = min(PART ? w.u.lo + (q0 + qi) / p.G : seen + qi / p.G, end);
-      // (without a window it does not matter how far behind a group's part its queries stand)
-      if (PART && p.window > 0 && qi < nq) pos[e] = load(&part_tokens(p.part)[row.bos + (q0 + qi) / p.G].x);
+      pos[e] = min(pmin + (wq * 16 + r8 + 8 * e) / p.G, pmax);
     }
-    const int pmax = PART ? __reduce_max_sync(0xffffffffu, max(pos[0], pos[1])) : end;
     ok = __all_sync(0xffffffffu, ok && tc::mbar_wait(&sm.qfull, seg & 1, P.wait_ns));
     const uint32_t qbase =
         tc::smem_addr(qbuf) + (wq * 16 + (lane & 15)) * C::kPitch + (lane >> 4) * 16;
@@ -356,7 +346,7 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, NW>::kThreads, 1)
           }
         }
         // not every query sees every token?
-        const bool part = b + 31 > seen || !have0 || !have1 ||
+        const bool part = b + 31 > pmin || !have0 || !have1 ||
                           (p.window > 0 && b <= pmax - p.window && b + 31 >= p.sinks);
         if (part) {
 #pragma unroll
@@ -364,8 +354,8 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, NW>::kThreads, 1)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const int tok = b + n * 8 + c2 + (e & 1), at = pos[e >> 1];
-              const bool sees = tok <= at && (!PART || tok <= end) &&
-                                (p.window <= 0 || tok > at - p.window || tok < p.sinks) && (n < 2 ? have0 : have1);
+              const bool sees = tok <= at && (p.window <= 0 || tok > at - p.window || tok < p.sinks) &&
+                                (n < 2 ? have0 : have1);
               if (!sees) sc[n][e] = -INFINITY;
             }
         }
@@ -415,9 +405,9 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, NW>::kThreads, 1)
           }
         }
         if (part)
-          values_step<true, DV, D / 64>(o, ph, pl, vbase, ds * DV, b, pos, end, p.window, p.sinks);
+          values_step<true, DV, D / 64>(o, ph, pl, vbase, ds * DV, b, pos, pmax, p.window, p.sinks);
         else
-          values_step<false, DV, D / 64>(o, ph, pl, vbase, ds * DV, b, pos, end, p.window, p.sinks);
+          values_step<false, DV, D / 64>(o, ph, pl, vbase, ds * DV, b, pos, pmax, p.window, p.sinks);
       }
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&sm.empty[s]);
@@ -436,30 +426,11 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, NW>::kThreads, 1)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int qi = wq * 16 + r8 + 8 * e;
-        if constexpr (PART) {
-          if (qi >= nq) continue;
-          const int64_t place = ((int64_t)(w.n < p.part.groups ? 0 : p.part.tokens) + row.bos + (q0 + qi) / p.G) * p.Hq +
-                                h * p.G + (q0 + qi) % p.G;
-          const int64_t at = whole ? place : (int64_t)slot * C::kNQ + qi;
-          // four columns of all queries side by side (see PartDev::quads)
-          const int64_t step = whole ? (int64_t)2 * p.part.tokens * p.Hq * 4 : C::kNQ * 4;
-          float* to = (whole ? p.part.o + place * 4 : P.part + ((int64_t)slot * (D / 4) * C::kNQ + qi) * 4) +
-                      (ds * DV + c2) / 4 * step + c2 % 4;
-#pragma unroll
-          for (int i = 0; i < DV / 8; ++i)
-            *reinterpret_cast<float2*>(to + i * 2 * step) = make_float2(o[i][2 * e], o[i][2 * e + 1]);
-          if (ds == 0 && c2 == 0) {
-            *reinterpret_cast<float2*>((whole ? p.part.ml : P.stats) + at * 2) = make_float2(m[e], l[e]);
-            if (w.j0 == 0)
-              p.part.range[place] = {whole ? -1 : (int)blockIdx.x * NW + wk, small.deal.owner(w.unit_last(share)), qi, 0};
-          }
-          continue;
-        }
         const int g = sm.qtok[qi];
         if (whole && g >= 0) {
           const float f = l[e] == 0.f ? 0.f : 1.f / l[e];
           __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + (int64_t)g * p.out_stride +
-                               (int64_t)(h * p.G + qi % p.G) * D + ds * DV + c2;
+                               (int64_t)(w.h * p.G + qi % p.G) * D + ds * DV + c2;
 #pragma unroll
           for (int i = 0; i < DV / 8; ++i)
             *reinterpret_cast<uint32_t*>(out + i * 8) = pack2(o[i][2 * e] * f, o[i][2 * e + 1] * f);
@@ -472,11 +443,11 @@ __global__ void __launch_bounds__(Cfg<D, WQ, DS, NW>::kThreads, 1)
             *reinterpret_cast<float2*>(P.stats + ((size_t)slot * C::kNQ + qi) * 2) = make_float2(m[e], l[e]);
         }
       }
-      if (!PART && !whole && w.j0 == 0 && wq == 0 && ds == 0 && lane == 0) {
+      if (!whole && w.j0 == 0 && wq == 0 && ds == 0 && lane == 0) {
         int32_t* info = P.info + (blockIdx.x * NW + wk) * 8;
         info[1] = row.bos;
         info[2] = nq;
-        info[3] = h;
+        info[3] = w.h;
         info[5] = 0;
         info[4] = small.deal.owner(w.unit_last(share));  // the worker with the unit's last tile
         info[0] = 1;
@@ -492,14 +463,14 @@ int64_t queries_of(const AttnLaunch& a) {
   return a.few > 0 ? a.few : std::max<int64_t>(1, (int64_t)a.rows.max_q * a.G);
 }
 
-template <bool PART, int D, int WQ, int DS, int NW>
+template <int D, int WQ, int DS, int NW>
 cudaError_t launch_cfg(const AttnLaunch& a, cudaStream_t s) {
   using C = Cfg<D, WQ, DS, NW>;
   static std::atomic<uint64_t> done{0};
-  constexpr int smem = (int)(NW * (C::kRing + C::kQ) + sizeof(Small<C, PART>));
-  static_assert(smem <= 232448 && C::kThreads / 32 * 8 <= (int)C::kRing && kPlanInts * 4 + 1024 <= (int)(NW * C::kRing), "shared memory");
+  constexpr int smem = (int)(NW * (C::kRing + C::kQ) + sizeof(Small<C>));
+  static_assert(smem <= 232448 && C::kThreads / 32 * 8 <= (int)C::kRing, "shared memory");
   cudaError_t e = once_per_device(done, [&] {
-    return cudaFuncSetAttribute(split_kernel<D, WQ, DS, NW, PART>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    return cudaFuncSetAttribute(split_kernel<D, WQ, DS, NW>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   });
   if (e != cudaSuccess) return e;
   CUtensorMap kmap, vmap;
@@ -521,7 +492,7 @@ cudaError_t launch_cfg(const AttnLaunch& a, cudaStream_t s) {
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if ((e = cudaLaunchKernelEx(&cfg, split_kernel<D, WQ, DS, NW, PART>, P, kmap, vmap)) != cudaSuccess || PART) return e;
+  if ((e = cudaLaunchKernelEx(&cfg, split_kernel<D, WQ, DS, NW>, P, kmap, vmap)) != cudaSuccess) return e;
   cfg.gridDim = dim3(kSms * NW, join_rows(kSms * NW, (int)queries_of(a)));
   cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.dynamicSmemBytes = 0;
@@ -563,39 +534,21 @@ auto pick(int d, int slots, F f) {
   return slots == 16 ? f(Cfg<256, 1, 2, 2>{}) : slots == 32 ? f(Cfg<256, 2, 2, 2>{}) : f(Cfg<256, 4, 2, 1>{});
 }
 
-template <bool PART, int D, int WQ, int DS, int NW>
+template <int D, int WQ, int DS, int NW>
 cudaError_t launch_picked(Cfg<D, WQ, DS, NW>, const AttnLaunch& a, cudaStream_t s) {
-  return launch_cfg<PART, D, WQ, DS, NW>(a, s);
-}
-
-size_t workspace_of(const AttnLaunch& a, int q) {
-  const size_t workers = (size_t)kSms * pick(a.cache.d, q, [](auto c) { return decltype(c)::kWorkers; });
-  return workers * (8 + 4 * (size_t)q + 2 * (size_t)q * a.cache.d) * 4;
-}
-
-// Queries of a unit of a pass over parts: those of a group may be those of all rows.
-int part_slots(const AttnLaunch& a) {
-  return query_slots(std::max<int64_t>((int64_t)a.rows.num_tokens * a.G, 1));
+  return launch_cfg<D, WQ, DS, NW>(a, s);
 }
 
 }  // namespace
 
-size_t attn_split_workspace(const AttnLaunch& a) { return workspace_of(a, query_slots(queries_of(a))); }
+size_t attn_split_workspace(const AttnLaunch& a) {
+  const int q = query_slots(queries_of(a));
+  const size_t workers = (size_t)kSms * pick(a.cache.d, q, [](auto c) { return decltype(c)::kWorkers; });
+  return workers * (8 + 4 * (size_t)q + 2 * (size_t)q * a.cache.d) * 4;
+}
 
 cudaError_t launch_attn_split(const AttnLaunch& a, cudaStream_t s) {
-  return pick(a.cache.d, query_slots(queries_of(a)), [&](auto c) { return launch_picked<false>(c, a, s); });
-}
-
-size_t attn_split_parts_workspace(const AttnLaunch& a) { return workspace_of(a, part_slots(a)); }
-
-PartPieces attn_split_parts_pieces(const AttnLaunch& a, void* ws) {
-  const int q = part_slots(a), workers = kSms * pick(a.cache.d, q, [](auto c) { return decltype(c)::kWorkers; });
-  float* stats = static_cast<float*>(ws) + 8 * workers;
-  return {stats, stats + (size_t)4 * workers * q, q};
-}
-
-cudaError_t launch_attn_split_parts(const AttnLaunch& a, cudaStream_t s) {
-  return pick(a.cache.d, part_slots(a), [&](auto c) { return launch_picked<true>(c, a, s); });
+  return pick(a.cache.d, query_slots(queries_of(a)), [&](auto c) { return launch_picked(c, a, s); });
 }
 
 }  // namespace gdn

@@ -255,9 +255,6 @@ bool attn_shared_supported(const AttnLaunch& p, gdn_dtype dtype);  // on tcgen05
 size_t attn_shared_workspace(const AttnLaunch& p);
 PartPieces attn_shared_pieces(const AttnLaunch& p, void* ws);
 cudaError_t launch_attn_shared(const AttnLaunch& p, cudaStream_t s);
-size_t attn_split_parts_workspace(const AttnLaunch& p);
-PartPieces attn_split_parts_pieces(const AttnLaunch& p, void* ws);
-cudaError_t launch_attn_split_parts(const AttnLaunch& p, cudaStream_t s);
 size_t attn_split_fma_parts_workspace(const AttnLaunch& p);
 PartPieces attn_split_fma_parts_pieces(const AttnLaunch& p, void* ws);
 cudaError_t launch_attn_split_fma_parts(const AttnLaunch& p, gdn_dtype dtype, cudaStream_t s);

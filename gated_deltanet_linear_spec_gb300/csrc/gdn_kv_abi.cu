@@ -234,13 +234,14 @@ int attend_whole(AttnLaunch& p, gdn_dtype dtype, cudaStream_t s) {
   return cuda_rc(launch_attn_prompt(p, s));
 }
 
-// The pass that goes over the parts of all groups and rows: the split kernel's where the queries of all rows fit a unit of
-// its, tcgen05's where those of a row fit a CTA, the CUDA cores' for types that take neither.  Longer rows on the tensor
+// The pass that goes over the parts of all groups and rows: tcgen05's, where the queries of a row fit a CTA (with few queries as
+// with many: 4 rows of one group behind 65536 tokens, 16 q-heads, 2 kv-heads, d = 128, take 29 us, 61 on mma.sync with
+// 16 queries a tile; 12 and 15 behind 777); the CUDA cores' for types that it does not take.  Longer rows on the tensor
 // cores fill tiles of their own, and share nothing.
-enum Pass { kNoPass, kSplitPass, kTilePass, kFmaPass };
-Pass pass_of(const AttnLaunch& p, gdn_dtype dtype) {
+enum Pass { kNoPass, kTilePass, kFmaPass };
+Pass pass_of(const AttnLaunch& p, int32_t num_groups, gdn_dtype dtype) {
+  if (p.rows.num_tokens == 0 || num_groups == 0) return kNoPass;
   if (!attn_prompt_supported(p, dtype)) return kFmaPass;
-  if ((int64_t)p.rows.num_tokens * p.G <= 64 && attn_split_supported(p, dtype)) return kSplitPass;
   return attn_shared_supported(p, dtype) ? kTilePass : kNoPass;
 }
 
@@ -259,10 +260,8 @@ SharedWs shared_ws(const AttnLaunch& p, gdn_dtype dtype) {
   w.ml = round256(w.range + queries * sizeof(PieceRange));
   w.o = round256(w.ml + queries * 8);
   w.pass = round256(w.o + queries * p.cache.d * 4);
-  const Pass pass = pass_of(p, dtype);
-  w.end = w.pass + round256(pass == kSplitPass  ? attn_split_parts_workspace(p)
-                            : pass == kTilePass ? attn_shared_workspace(p)
-                                                : attn_split_fma_parts_workspace(p));
+  const bool tiles = pass_of(p, p.part.groups, dtype) == kTilePass;
+  w.end = w.pass + round256(tiles ? attn_shared_workspace(p) : attn_split_fma_parts_workspace(p));
   return w;
 }
 // The parts of all groups and rows in one pass.
@@ -457,7 +456,7 @@ size_t gdn_shared_attention_workspace_bytes(const gdn_attn_desc* attn, const gdn
   const size_t whole = gdn_attention_workspace_bytes(attn, cache, rows);
   if (check_shape(cache) || check_table(cache) || check_attn(attn, cache) || check_kv_rows(rows)) return 0;
   AttnLaunch p = attn_args(attn, cache, rows);
-  if (rows->num_tokens == 0 || groups->num_groups == 0 || pass_of(p, cache->dtype) == kNoPass) return whole;
+  if (pass_of(p, groups->num_groups, cache->dtype) == kNoPass) return whole;
   all_parts(p, groups->num_groups);
   return shared_ws(p, cache->dtype).end;
 }
@@ -473,7 +472,8 @@ int gdn_shared_attention(const gdn_attn_desc* attn, const gdn_kv_cache* cache, c
   if ((rc = attention_args(attn, cache, rows, q, q_stride, num_global_tokens, out, out_stride, workspace, workspace_bytes,
                            need, d_status, p)))
     return rc;
-  if (groups->num_groups == 0 || pass_of(p, cache->dtype) == kNoPass) return attend_whole(p, cache->dtype, (cudaStream_t)stream);
+  const Pass pass = pass_of(p, groups->num_groups, cache->dtype);
+  if (pass == kNoPass) return attend_whole(p, cache->dtype, (cudaStream_t)stream);
   all_parts(p, groups->num_groups);
   const SharedWs w = shared_ws(p, cache->dtype);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -491,15 +491,11 @@ int gdn_shared_attention(const gdn_attn_desc* attn, const gdn_kv_cache* cache, c
   p.part.ml = reinterpret_cast<float*>(ws + w.ml);
   p.part.o = reinterpret_cast<float*>(ws + w.o);
   p.ws = ws + w.pass;
-  const Pass pass = pass_of(p, cache->dtype);
   p.part.quads = pass != kFmaPass;
   const cudaStream_t s = (cudaStream_t)stream;
   if (!p.part.plan_here && (rc = cuda_rc(launch_group_plan(plan, s)))) return rc;
   PartPieces pieces;
-  if (pass == kSplitPass) {
-    pieces = attn_split_parts_pieces(p, p.ws);
-    rc = cuda_rc(launch_attn_split_parts(p, s));
-  } else if (pass == kTilePass) {
+  if (pass == kTilePass) {
     pieces = attn_shared_pieces(p, p.ws);
     rc = cuda_rc(launch_attn_shared(p, s));
   } else {

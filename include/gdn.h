@@ -408,11 +408,11 @@ typedef struct {
  * first such row: where the rows' entries differ after all, its pages count.  Rows of one call are in one group at most
  * (group bounds that do not ascend or leave the rows: GDN_STATUS_ROW_RANGE, that group shares nothing).
  * bf16 rows of more than 256 queries per kv-head (d = 64, 128; 128 at d = 256; max_query_len decides) go over their whole
- * caches each, as in gdn_paged_attention: they fill the tensor cores by themselves.
- * Where the rows have more than 64 queries per kv-head in all, bf16 weights (d = 64, 128, 256) go into the second sum as one
- * bf16, else as in gdn_paged_attention.
+ * caches as in gdn_paged_attention: they fill the tensor cores by themselves.  Else bf16 weights (d = 64, 128, 256) go into the
+ * second sum as one bf16.  Groups pay from three or four rows on; pairs that share a few thousand tokens take up to a half
+ * longer here than in gdn_paged_attention, which finds the second row's pages in the L2.
  * workspace: at least gdn_shared_attention_workspace_bytes(attn, cache, rows, groups) bytes, 256-byte aligned; it holds
- * the plan, (2 + d) fp32 per query and head, and partial results.
+ * the plan (a copy for each CTA that makes its own), two states of (2 + d) fp32 per query and head, and partial results.
  */
 int gdn_shared_attention(const gdn_attn_desc* attn, const gdn_kv_cache* cache, const gdn_kv_rows* rows,
                          const gdn_kv_groups* groups, const void* q, int64_t q_stride, int32_t num_global_tokens, void* out,

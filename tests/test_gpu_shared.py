@@ -10,6 +10,11 @@ from tests.test_gpu_attention import BF16, F32, Step, i32
 pytestmark = pytest.mark.gpu
 
 
+def weight_bits(dim, dtype):
+    """The tensor cores take the weights as bf16; the CUDA cores keep 32 bits of them."""
+    return 8 if dtype == BF16 and dim in (64, 128, 256) else 24
+
+
 class Groups(Step):
     """Groups (prefix tokens, rows of (new tokens, cache length)); the rows of a group hold the pages of its first row for
     the whole pages of the prefix.  ``lone`` rows in front and behind belong to no group."""
@@ -44,10 +49,7 @@ class Groups(Step):
         used[self.token] = True
         assert torch.all(got[~used].float() == 7.0), "a token of no row was written"
         keys = max([kv for _, kv in self.rows] + [1])
-        group = self.heads // self.kv_heads
-        # the tensor cores take the weights of many queries as bf16; otherwise they keep 16 bits or more
-        many = self.max_q * group > 64 or self.starts[-1] * group > 64
-        bits = 24 if self.dtype == F32 else 8 if many else 16
+        bits = weight_bits(self.dim, self.dtype)
         tol = ref.attention_tolerance(out, spread, logits, keys, self.dim, self.dtype, bits)
         err = (got.double() - out).abs()
         bad = ~(err <= tol) & used[:, None, None]
@@ -71,7 +73,7 @@ def test_head_layouts(heads, kv_heads, dim, dtype):
     Groups(TREE, heads=heads, kv_heads=kv_heads, dim=dim, dtype=dtype, seed=heads, fused=True, interleaved=True).check()
 
 
-# heads and types: few queries in all, and more than a unit of the split kernel holds
+# heads and types: few queries in all, and many
 FEW_AND_MANY = [(4, 64, BF16), (4, 128, BF16), (4, 256, BF16), (4, 96, BF16), (4, 64, F32), (32, 64, BF16), (32, 128, BF16),
                 (32, 256, BF16), (32, 96, BF16)]
 
@@ -125,7 +127,7 @@ def test_values_that_windows_hide(heads, dim, dtype):
     s.cache = gdn.KvCache(k.cuda(), v.cuda(), s.table.cuda())
     got, status = s.run()
     assert status == 0
-    tol = ref.attention_tolerance(want, spread, logits, 260, dim, dtype, 24 if dtype == F32 else 16 if heads == 4 else 8)
+    tol = ref.attention_tolerance(want, spread, logits, 260, dim, dtype, weight_bits(dim, dtype))
     for i, (new, kv) in enumerate(s.rows):
         for t in range(new):
             low = kv - new + t - 90  # positions up to here are hidden
@@ -203,7 +205,7 @@ def test_bad_rows_and_groups(dtype):
     s = Groups([(64, [(1, 80), (2, 90), (1, 70)])], dtype=dtype, gather=False)
     s.check()
     want, spread, logits = s.expected()
-    tol = ref.attention_tolerance(want, spread, logits, 90, 64, dtype, 24 if dtype == F32 else 16)
+    tol = ref.attention_tolerance(want, spread, logits, 90, 64, dtype, weight_bits(64, dtype))
     lens = i32([80, 1, 70])  # row 1: fewer tokens than new ones
     s.kv_rows = gdn.KvRows(s.kv_rows.query_start_loc, 4, lens, 2, s.kv_rows.table_rows)
     s.out.fill_(7.0)
@@ -356,7 +358,7 @@ def test_branches_decode_in_a_graph(dtype, dim):
         want, spread, logits = ref.attention(turned.cpu(), pool[:, 0].cpu(), pool[:, 1].cpu(), cache.block_table.cpu(),
                                              [(i, 1) for i in range(branches)], list(range(branches)), list(range(branches)),
                                              lens.tolist(), 0.0, 0, 0)
-        tol = ref.attention_tolerance(want, spread, logits, prompt + 9, dim, dtype, 24 if dtype == F32 else 16)
+        tol = ref.attention_tolerance(want, spread, logits, prompt + 9, dim, dtype, weight_bits(dim, dtype))
         assert torch.all((out.cpu().double() - want).abs() <= tol), t
         old += 1
         lens += 1
