@@ -8,7 +8,7 @@
 
 namespace gdn {
 
-// The group's rows [a, b); false (and the status bit) for bounds that are none.
+// The group's rows [a, b); false (and the status bit) for bounds that are none.  (Where all groups' are some, no row is in two.)
 __device__ __forceinline__ bool group_bounds(int a, int b, int num_seqs, uint32_t* st) {
   if (a >= 0 && b >= a && b <= num_seqs) return true;
   set_status(st, GDN_STATUS_ROW_RANGE);
@@ -55,7 +55,7 @@ struct GroupRows {
 
 // A plan of few rows is made by every CTA of the pass for itself, which saves the launch of a kernel for it.  (The join reads
 // the first one's.)  scratch: kPlanInts, 16-byte aligned; returns the parts there.  All threads call.
-constexpr int kPlanRows = 256, kPlanGroups = 64;
+constexpr int kPlanRows = 256, kPlanGroups = 32;
 constexpr int kPlanRecs = (kPlanRows + kPlanGroups) * (int)(sizeof(PartRec) / 4);
 constexpr int kPlanInts = kPlanRecs + 5 * kPlanRows + 2 * kPlanGroups + 1;
 
@@ -82,11 +82,14 @@ __device__ const PartRec* plan_here(const AttnLaunch& p, int* scratch) {
     trow[n] = r.trow;
     own[n] = 0;
   }
+  bool none = false;  // nothing is shared
   for (int g = tid; g <= part.groups; g += THREADS) {
     start[g] = load(part.start + g);
-    if (g < part.groups) prefix[g] = load(part.prefix + g);
+    if (g == part.groups) break;
+    prefix[g] = load(part.prefix + g);
+    none |= !group_bounds(start[g], load(part.start + g + 1), R.num_seqs, st);
   }
-  __syncthreads();
+  none = __syncthreads_or(none);
   PartRec* recs = part_recs(part);
   int2* token = part_tokens(part);
   for (int g = tid >> 5; g < part.groups; g += THREADS / 32) {
@@ -94,7 +97,7 @@ __device__ const PartRec* plan_here(const AttnLaunch& p, int* scratch) {
     GroupRows s;
     bool seen = false;
     int tokens = 0;
-    if (group_bounds(a, b, R.num_seqs, lane == 0 ? st : nullptr)) {
+    if (!none) {
       for (int n = a + lane; n < b; n += 32)
         if (len[n] > 0) s.add(n, first[n], len[n], kv[n]);
       s.warp_meet();

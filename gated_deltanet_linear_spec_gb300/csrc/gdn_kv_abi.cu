@@ -250,25 +250,26 @@ Pass pass_of(const AttnLaunch& p, int32_t num_groups, gdn_dtype dtype) {
 struct SharedWs {
   size_t recs, token, range, ml, o, pass, end;
 };
-SharedWs shared_ws(const AttnLaunch& p, gdn_dtype dtype) {
+SharedWs shared_ws(const AttnLaunch& p) {
   SharedWs w{};
   const size_t tokens = p.rows.num_tokens, queries = 2 * tokens * p.Hq;
   w.recs = 0;
-  const size_t copies = group_plan_here(p) ? kMaxPassCtas : 1;
+  const size_t copies = p.part.plan_here ? kMaxPassCtas : 1;
   w.token = round256(w.recs + copies * p.part.count * sizeof(PartRec));
   w.range = round256(w.token + copies * tokens * sizeof(int2));
   w.ml = round256(w.range + queries * sizeof(PieceRange));
   w.o = round256(w.ml + queries * 8);
   w.pass = round256(w.o + queries * p.cache.d * 4);
-  const bool tiles = pass_of(p, p.part.groups, dtype) == kTilePass;
-  w.end = w.pass + round256(tiles ? attn_shared_workspace(p) : attn_split_fma_parts_workspace(p));
+  w.end = w.pass + round256(p.part.quads ? attn_shared_workspace(p) : attn_split_fma_parts_workspace(p));
   return w;
 }
 // The parts of all groups and rows in one pass.
-void all_parts(AttnLaunch& p, int32_t num_groups) {
+void all_parts(AttnLaunch& p, int32_t num_groups, Pass pass) {
   p.part.groups = num_groups;
   p.part.count = num_groups + p.rows.num_seqs;
   p.part.tokens = p.rows.num_tokens;
+  p.part.quads = pass == kTilePass;
+  p.part.plan_here = group_plan_here(p);
 }
 
 GroupsLaunch groups_args(const gdn_kv_cache* c, const gdn_kv_rows* r, const gdn_kv_groups* g, uint32_t* status) {
@@ -456,9 +457,10 @@ size_t gdn_shared_attention_workspace_bytes(const gdn_attn_desc* attn, const gdn
   const size_t whole = gdn_attention_workspace_bytes(attn, cache, rows);
   if (check_shape(cache) || check_table(cache) || check_attn(attn, cache) || check_kv_rows(rows)) return 0;
   AttnLaunch p = attn_args(attn, cache, rows);
-  if (pass_of(p, groups->num_groups, cache->dtype) == kNoPass) return whole;
-  all_parts(p, groups->num_groups);
-  return shared_ws(p, cache->dtype).end;
+  const Pass pass = pass_of(p, groups->num_groups, cache->dtype);
+  if (pass == kNoPass) return whole;
+  all_parts(p, groups->num_groups, pass);
+  return shared_ws(p).end;
 }
 
 int gdn_shared_attention(const gdn_attn_desc* attn, const gdn_kv_cache* cache, const gdn_kv_rows* rows,
@@ -474,8 +476,8 @@ int gdn_shared_attention(const gdn_attn_desc* attn, const gdn_kv_cache* cache, c
     return rc;
   const Pass pass = pass_of(p, groups->num_groups, cache->dtype);
   if (pass == kNoPass) return attend_whole(p, cache->dtype, (cudaStream_t)stream);
-  all_parts(p, groups->num_groups);
-  const SharedWs w = shared_ws(p, cache->dtype);
+  all_parts(p, groups->num_groups, pass);
+  const SharedWs w = shared_ws(p);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   GroupsLaunch plan = groups_args(cache, rows, groups, d_status);
   plan.window = p.window;
@@ -486,12 +488,10 @@ int gdn_shared_attention(const gdn_attn_desc* attn, const gdn_kv_cache* cache, c
   p.part.token = plan.token;
   p.part.start = plan.start;
   p.part.prefix = plan.prefix;
-  p.part.plan_here = group_plan_here(p) ? 1 : 0;
   p.part.range = reinterpret_cast<PieceRange*>(ws + w.range);
   p.part.ml = reinterpret_cast<float*>(ws + w.ml);
   p.part.o = reinterpret_cast<float*>(ws + w.o);
   p.ws = ws + w.pass;
-  p.part.quads = pass != kFmaPass;
   const cudaStream_t s = (cudaStream_t)stream;
   if (!p.part.plan_here && (rc = cuda_rc(launch_group_plan(plan, s)))) return rc;
   PartPieces pieces;

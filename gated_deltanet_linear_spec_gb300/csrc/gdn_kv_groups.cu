@@ -50,7 +50,8 @@ __device__ __forceinline__ const int32_t* entries_of(const GroupsLaunch& p, int 
 
 // A cluster per group.  Its warps take runs of kRun entries of the rows in turn, those of all rows' beginnings first, and
 // compare them with those of the group's first row; what lies behind a place where rows were seen to part is left out.
-// 16 groups of 9 to 24 rows that share up to 8192 entries: 59 us with a warp per row, XX so.
+// 16 groups of 9 to 24 rows that share up to 8192 entries: 59 us with a warp per row, 11 so; what bounds it is
+// its chain of loads: bounds, rows, two entries (5 MB in all; 4 rows of 777 tokens take 3.2).
 constexpr int kAhead = 8;  // entries of a lane that are on their way
 constexpr int kRun = 32 * kAhead;
 
@@ -142,10 +143,16 @@ __global__ void __cluster_dims__(kCluster) __launch_bounds__(kThreads) group_pla
     }
     if (!lanes || lane == 0) p.recs[p.num_groups + n] = rec;
   }
+  bool none = false;  // nothing is shared
+  for (int g = threadIdx.x; g < p.num_groups; g += kThreads) {
+    int a, b;
+    none |= !group_rows(p, g, a, b, p.status);
+  }
+  none = __syncthreads_or(none);
   cluster_sync();
   for (int g = me >> 5; g < p.num_groups; g += kAll / 32) {
     int a, b;
-    if (!group_rows(p, g, a, b, lane == 0 ? p.status : nullptr)) a = b = 0;
+    if (none || !group_rows(p, g, a, b, nullptr)) a = b = 0;
     GroupRows s;
     for (int n = a + lane; n < b; n += 32) add_row(p, n, s, nullptr);
     s.warp_meet();
@@ -180,17 +187,21 @@ cudaError_t launch_cluster(void (*kernel)(GroupsLaunch), int clusters, int threa
 
 }  // namespace
 
-// Blocks of 1024 threads where a group's rows may have more entries than a cluster of smaller ones takes at once.
+// Blocks of 1024 threads where a group's rows may have more entries than a cluster of smaller ones takes at once: those 16
+// groups 11 us, with blocks of 256 19; 4 rows of 64 entries 3.6 us with blocks of 1024, 3.2 with 256.
 cudaError_t launch_kv_common_prefix(const GroupsLaunch& p, cudaStream_t s) {
   const int64_t entries = (int64_t)p.cache.max_pages * p.rows.num_seqs / p.num_groups;
   return entries > kCluster * kThreads * kAhead ? launch_cluster(common_kernel<1024>, p.num_groups, 1024, p, s)
                                                 : launch_cluster(common_kernel<kThreads>, p.num_groups, kThreads, p, s);
 }
 
-// Every CTA goes over all rows, groups and tokens then, which takes it longer than the launch of a kernel would for more of
-// them.
+// Every CTA goes over all rows, groups and tokens then, a warp per group.  Against a kernel for the plan, us a call: 4 rows of a
+// group 12.1 (13.6), 256 rows 24 (30), 16 groups of 16 rows of 4 tokens 29 (32), 32 of 8 28 (30), 64 of 4 32 (32); in the pass on
+// the CUDA cores, whose CTAs have 4 warps for 12 (of 8), 1 x 64 x 4 17 (20), 16 x 16 x 4 32 (33), 32 x 8 x 4 35 (33), 64 x 4 x 4
+// 40 (33).
 bool group_plan_here(const AttnLaunch& p) {
-  return p.rows.num_seqs <= kPlanRows && p.part.groups <= kPlanGroups && p.rows.num_tokens <= 4 * kPlanRows;
+  return p.rows.num_seqs <= kPlanRows && p.part.groups <= (p.part.quads ? kPlanGroups : kPlanGroups / 2) &&
+         p.rows.num_tokens <= 4 * kPlanRows;
 }
 
 cudaError_t launch_group_plan(const GroupsLaunch& p, cudaStream_t s) {

@@ -405,8 +405,8 @@ typedef struct {
  * shared and over the row's own tokens meet as those of a split row do.
  * Shared are min(prefix_lens[g], kv_lens[n] - L of the rows with new tokens) tokens, down to whole pages, where at least
  * two rows of the group have new tokens; prefix_lens <= 0 shares nothing.  They are read by the table row of the
- * first such row: where the rows' entries differ after all, its pages count.  Rows of one call are in one group at most
- * (group bounds that do not ascend or leave the rows: GDN_STATUS_ROW_RANGE, that group shares nothing).
+ * first such row: where the rows' entries differ after all, its pages count.  A row is in one group at most: where
+ * group bounds do not ascend or leave the rows (GDN_STATUS_ROW_RANGE), nothing is shared.
  * bf16 rows of more than 256 queries per kv-head (d = 64, 128; 128 at d = 256; max_query_len decides) go over their whole
  * caches as in gdn_paged_attention: they fill the tensor cores by themselves.  Else bf16 weights (d = 64, 128, 256) go into the
  * second sum as one bf16.  Groups pay from three or four rows on; pairs that share a few thousand tokens take up to a half
@@ -497,8 +497,8 @@ int gdn_rope(const gdn_rope_desc* rope, int32_t num_heads, int32_t head_dim, gdn
  * turned into their pages, their values copied, and the q heads of the same tokens turned from q to q_out (which may be q).
  * Everything that gdn_kv_append says holds; q_out is written for every token of a well-formed row, wherever its page
  * is.  num_q_heads = 0: keys and values only.
- *   q, q_out [num_global_tokens, num_q_heads, d], read and written at token_indx; q_out overlaps neither k nor v, and q
- *   only as in gdn_rope.
+ *   q, q_out [num_global_tokens, num_q_heads, d], read and written at token_indx (which then names no token twice);
+ *   q_out overlaps neither k nor v, and q only as in gdn_rope.
  */
 int gdn_kv_append_rope(const gdn_kv_cache* cache, const gdn_kv_rows* rows, const gdn_rope_desc* rope, const void* k,
                        int64_t k_stride, const void* v, int64_t v_stride, int32_t num_q_heads, const void* q,

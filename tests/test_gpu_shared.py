@@ -219,6 +219,79 @@ def test_bad_rows_and_groups(dtype):
         s.check(want_status=gdn.STATUS_ROW_RANGE)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("many", [False, True])
+def test_a_row_in_two_groups(dtype, many):
+    """Bounds that do not ascend would put rows into two groups: nothing is shared then, whoever makes the plan."""
+    groups = [(48, [(1 + i % 2, 50 + i % 7) for i in range(5)]) for _ in range(53 if many else 2)]
+    s = Groups(groups, dtype=dtype, heads=2, kv_heads=1, seed=11)
+    bounds = [0, 6, 3, 9] + s.bounds[3:]
+    s.groups = gdn.KvGroups(i32(bounds), i32([48] * (len(bounds) - 1)))
+    s.check(want_status=gdn.STATUS_ROW_RANGE)
+
+
+@pytest.mark.parametrize("dim,dtype", [(64, BF16), (256, BF16), (96, BF16), (64, F32)])
+def test_padded_batch(dim, dtype):
+    """Rows without tokens at the end, and tokens behind the last row's."""
+    s = Groups([(64, [(2, 70), (1, 80), (1, 90)]), (32, [(0, 40), (0, 33), (0, 64)])], dim=dim, dtype=dtype, gather=False)
+    q = torch.cat([s.q, torch.full((7, *s.q.shape[1:]), float("nan"), dtype=dtype)])
+    s.q, s.qd, s.out = q, q.cuda(), torch.full_like(q, 7.0, device="cuda")
+    r = s.kv_rows
+    s.kv_rows = gdn.KvRows(r.query_start_loc, q.shape[0], r.kv_lens, s.max_q, r.table_rows)
+    s.check()
+
+
+@pytest.mark.parametrize("dim,dtype", [(128, BF16), (64, F32)])
+def test_two_graphs_share_a_workspace(dim, dtype):
+    one = Groups([(160, [(1, 170 + i) for i in range(9)])], dim=dim, dtype=dtype, seed=1)
+    two = Groups([(96, [(2, 100), (1, 200), (4, 111)]), (32, [(1, 50), (1, 40), (1, 33)])], dim=dim, dtype=dtype, seed=2, window=70)
+    want = [s.check().clone() for s in (one, two)]
+    need = [gdn.gdn_shared_attention_workspace_bytes(s.attn, s.cache, s.kv_rows, s.groups) for s in (one, two)]
+    ws = torch.empty(max(need), dtype=torch.uint8, device="cuda")
+    graphs = []
+    for s in (one, two):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            gdn.gdn_shared_attention(s.attn, s.cache, s.kv_rows, s.groups, s.qd, s.out, workspace=ws)
+        graphs.append(g)
+    for s in (one, two):
+        s.out.fill_(7.0)
+    for _ in range(10):
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    for s, w in zip((one, two), want):
+        assert torch.equal(s.out.cpu(), w)
+
+
+@pytest.mark.parametrize("dim,dtype", [(128, BF16), (64, F32)])
+def test_two_streams_at_once(dim, dtype):
+    """Calls that run beside one another, each with a workspace of its own, give what they give alone."""
+    pair = [Groups([(640, [(1 + i % 3, 650 + 9 * i) for i in range(20)])], dim=dim, dtype=dtype, seed=7 + j, heads=8) for j in range(2)]
+    want = [s.check().clone() for s in pair]
+    streams = [torch.cuda.Stream() for _ in pair]
+    ws = [torch.empty(gdn.gdn_shared_attention_workspace_bytes(s.attn, s.cache, s.kv_rows, s.groups), dtype=torch.uint8,
+                      device="cuda") for s in pair]
+    for s in pair:
+        s.out.fill_(7.0)
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, stream, w in zip(pair, streams, ws):
+            gdn.gdn_shared_attention(s.attn, s.cache, s.kv_rows, s.groups, s.qd, s.out, workspace=w, stream=stream)
+    torch.cuda.synchronize()
+    for s, w in zip(pair, want):
+        assert torch.equal(s.out.cpu(), w)
+
+
+@pytest.mark.parametrize("dim,dtype", [(64, BF16), (128, BF16), (64, F32)])
+def test_one_key_and_one_page(dim, dtype):
+    """The smallest calls: a row whose only key is its own, groups of one row, one page shared and nothing else."""
+    Groups([(0, [(1, 1)])], dim=dim, dtype=dtype, heads=1, kv_heads=1).check()
+    Groups([(16, [(1, 17)])], dim=dim, dtype=dtype, heads=1, kv_heads=1).check()
+    Groups([(16, [(1, 17), (1, 17)])], dim=dim, dtype=dtype, heads=1, kv_heads=1).check()
+    Groups([(16, [(1, 17)] * 9)], dim=dim, dtype=dtype, heads=64, kv_heads=1, window=1).check()
+
+
 def test_no_groups_and_no_tokens():
     s = Groups([], lone=[(1, 30), (2, 40)])
     s.check()
