@@ -43,7 +43,7 @@ struct GroupRows {
   // nothing in front that stays visible, none does.)
   __device__ __forceinline__ int shared(int prefix, int page_size, int window, int sinks, bool& seen) const {
     int n = count >= 2 ? min(max(prefix, 0), least) : 0;
-    n -= n % page_size;
+    n &= -page_size;
     const int low = window > 0 ? max(0, least - window + 1) : 0;
     seen = n > low || (n > 0 && min(sinks, low) > 0);
     return n;
@@ -73,6 +73,14 @@ __device__ const PartRec* plan_here(const AttnLaunch& p, int* scratch) {
   int* start = own + kPlanRows;        // of a group
   int* prefix = start + kPlanGroups + 1;
   uint32_t* st = blockIdx.x == 0 ? p.status : nullptr;
+  // (groups' loads go out before rows' come back)
+  static_assert(kPlanGroups < THREADS, "a thread per group");
+  int g0 = 0, g1 = 0, given = 0;
+  if (tid <= part.groups) g0 = load(part.start + tid);
+  if (tid < part.groups) {
+    g1 = load(part.start + tid + 1);
+    given = load(part.prefix + tid);
+  }
   for (int n = tid; n < R.num_seqs; n += THREADS) {
     KvRow r;
     const bool there = load_kv_row(R, p.cache, n, r, st);
@@ -82,14 +90,9 @@ __device__ const PartRec* plan_here(const AttnLaunch& p, int* scratch) {
     trow[n] = r.trow;
     own[n] = 0;
   }
-  bool none = false;  // nothing is shared
-  for (int g = tid; g <= part.groups; g += THREADS) {
-    start[g] = load(part.start + g);
-    if (g == part.groups) break;
-    prefix[g] = load(part.prefix + g);
-    none |= !group_bounds(start[g], load(part.start + g + 1), R.num_seqs, st);
-  }
-  none = __syncthreads_or(none);
+  if (tid <= part.groups) start[tid] = g0;
+  if (tid < part.groups) prefix[tid] = given;
+  const bool none = __syncthreads_or(tid < part.groups && !group_bounds(g0, g1, R.num_seqs, st));  // nothing is shared
   PartRec* recs = part_recs(part);
   int2* token = part_tokens(part);
   for (int g = tid >> 5; g < part.groups; g += THREADS / 32) {
@@ -110,15 +113,16 @@ __device__ const PartRec* plan_here(const AttnLaunch& p, int* scratch) {
   for (int n = tid; n < R.num_seqs; n += THREADS)
     recs[part.groups + n] = near[part.groups + n] =
         len[n] > 0 ? PartRec{first[n], len[n], own[n] & ~1, kv[n], trow[n], kv[n] - len[n], kv[n] - 1, 0} : PartRec{};
-  // (the pass itself looks tokens up under a window; the join does in any case)
-  if (p.window > 0 || blockIdx.x == 0) {
-    for (int i = tid; i < R.num_tokens; i += THREADS) {
-      int n = 0;  // the last row that begins at or before the token
-      for (int step = kPlanRows / 2; step; step >>= 1)
-        if (n + step < R.num_seqs && first[n + step] <= i) n += step;
-      const bool there = i >= first[n] && i < first[n] + len[n];
-      token[i] = there ? make_int2(kv[n] - len[n] + i - first[n], own[n] & 1) : make_int2(-1, 0);
-    }
+  // The pass itself looks tokens up under a window, in its CTA's copy; the join does in any case, in the first, which the
+  // CTAs fill together where they need none of their own.
+  const bool all = p.window > 0;
+  if (!all) token = part.token;
+  for (int i = all ? tid : tid * gridDim.x + blockIdx.x; i < R.num_tokens; i += all ? THREADS : THREADS * gridDim.x) {
+    int n = 0;  // the last row that begins at or before the token
+    for (int step = kPlanRows / 2; step; step >>= 1)
+      if (n + step < R.num_seqs && first[n + step] <= i) n += step;
+    const bool there = i >= first[n] && i < first[n] + len[n];
+    token[i] = there ? make_int2(kv[n] - len[n] + i - first[n], own[n] & 1) : make_int2(-1, 0);
   }
   __syncthreads();
   return near;
