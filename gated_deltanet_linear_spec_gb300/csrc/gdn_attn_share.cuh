@@ -109,10 +109,10 @@ __device__ __forceinline__ Unit unit_of(const AttnLaunch& p, const RawRow<PART>&
   }
 }
 // The cost in tiles of all units of row n.
-template <int QG, bool PART, int TN, int START>
-__device__ __forceinline__ int64_t row_cost(const AttnLaunch& p, int n, uint32_t* st, const PartRec* near) {
+template <int QG, bool PART, int TN>
+__device__ __forceinline__ int64_t row_cost(const AttnLaunch& p, int n, int start, uint32_t* st, const PartRec* near) {
   const Unit u = unit_of<QG, PART, TN>(p, raw_row<PART>(p, n, near), st);
-  return (int64_t)u.cost(START) * u.per;
+  return (int64_t)u.cost(start) * u.per;
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -124,6 +124,7 @@ __device__ __forceinline__ float ex2(float x) {
 struct Deal {
   int64_t each;
   int more;
+  int start;  // tiles that a unit's beginning counts
   __device__ int64_t first(int worker) const { return each * worker + min(worker, more); }
   __device__ int owner(int64_t tile) const;
 };
@@ -147,16 +148,31 @@ struct Share {
   RawRow<PART> raw;  // that row
 };
 
-// The shares of the CTA's workers; part: one value per warp; near: the parts in shared memory, if they are there.  All
-// threads call.
-template <int QG, int NW, int THREADS, bool PART = false, int TN = kTN, int START = kStart>
+// The shares of the CTA's workers; part: one value per warp; near: the parts in shared memory, if they are there.  A unit's
+// beginning counts START tiles, or HALF where no unit has more than half of QG queries.  All threads call.
+template <int QG, int NW, int THREADS, bool PART = false, int TN = kTN, int START = kStart, int HALF = START>
 __device__ void find_shares(const AttnLaunch& p, int64_t* part, Deal& deal, Share<PART>* shares,
                             const PartRec* near = nullptr) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rows = rows_of<PART>(p), per = (rows + THREADS - 1) / THREADS;
   const int n0 = min(tid * per, rows), n1 = min(n0 + per, rows);
   int64_t mine = 0;
-  for (int n = n0; n < n1; ++n) mine += row_cost<QG, PART, TN, START>(p, n, blockIdx.x == 0 ? p.status : nullptr, near);
+  int start = START;
+  if constexpr (HALF != START) {
+    int64_t units = 0;
+    bool full = false;
+    for (int n = n0; n < n1; ++n) {
+      const Unit u = unit_of<QG, PART, TN>(p, raw_row<PART>(p, n, near), nullptr);
+      if (u.tiles == 0) continue;
+      mine += (int64_t)u.tiles * u.per;
+      units += u.per;
+      full |= (int64_t)u.r.len * p.G > QG / 2;
+    }
+    if (!__syncthreads_or(full)) start = HALF;
+    mine += units * start;
+  } else {
+    for (int n = n0; n < n1; ++n) mine += row_cost<QG, PART, TN>(p, n, START, blockIdx.x == 0 ? p.status : nullptr, near);
+  }
   int64_t inc = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -175,6 +191,7 @@ __device__ void find_shares(const AttnLaunch& p, int64_t* part, Deal& deal, Shar
   const int workers = gridDim.x * NW;
   d.each = quotient(total, workers);
   d.more = (int)(total - d.each * workers);
+  d.start = start;
   if (tid == 0) deal = d;
 #pragma unroll 1
   for (int w = 0; w < NW; ++w) {
@@ -191,7 +208,7 @@ __device__ void find_shares(const AttnLaunch& p, int64_t* part, Deal& deal, Shar
       int n = n0;
       if (per > 1) {
         for (; n < n1; ++n) {
-          const int64_t t = row_cost<QG, PART, TN, START>(p, n, nullptr, near);
+          const int64_t t = row_cost<QG, PART, TN>(p, n, start, nullptr, near);
           if (s.first < at + t) break;
           at += t;
         }
@@ -209,18 +226,20 @@ __device__ void find_shares(const AttnLaunch& p, int64_t* part, Deal& deal, Shar
 // Walks the units of a share: (row, unit of the row, tiles [j0, j0 + len) of the unit).  A warp holds the raw
 // values of the next 32 rows, one per lane, so that going on to the next row waits for no memory.
 // All lanes call together.
-template <int QG, bool PART = false, int TN = kTN, int START = kStart>
+template <int QG, bool PART = false, int TN = kTN>
 struct Walk {
   const AttnLaunch& p;
+  const int start;  // the deal's
   int left;
   int n, h, j0, len;  // h: unit of the row
   Unit u;
-  __device__ Walk(const AttnLaunch& launch, const Share<PART>& s) : p(launch), left(s.span), n(s.row), len(0) {
+  __device__ Walk(const AttnLaunch& launch, const Share<PART>& s, int start_ = kStart)
+      : p(launch), start(start_), left(s.span), n(s.row), len(0) {
     if (left <= 0) return;
     fill(n + 1);
     u = unit_of<QG, PART, TN>(p, s.raw, nullptr);
-    h = (int)quotient(s.into, u.cost(START));
-    piece((int)(s.into - (int64_t)h * u.cost(START)));
+    h = (int)quotient(s.into, u.cost(start));
+    piece((int)(s.into - (int64_t)h * u.cost(start)));
   }
   __device__ bool valid() const { return left > 0; }
   __device__ void next() {
@@ -244,15 +263,15 @@ struct Walk {
     return PART ? u.from + at : at;
   }
   // Where the unit ends in the deal.
-  __device__ int64_t unit_last(const Share<PART>& s) const { return s.first + s.span - left - from + u.cost(START) - 1; }
+  __device__ int64_t unit_last(const Share<PART>& s) const { return s.first + s.span - left - from + u.cost(start) - 1; }
 
  private:
   int from, span;  // the piece in the unit's tiles with those that stand for its beginning
   __device__ void piece(int at) {
     from = at;
-    span = min(u.cost(START) - at, left);
-    j0 = max(at - START, 0);
-    len = at + span - START - j0;
+    span = min(u.cost(start) - at, left);
+    j0 = max(at - start, 0);
+    len = at + span - start - j0;
     if (len <= 0) left = 0;  // the share ends before the unit's first tile
   }
   int base;

@@ -26,8 +26,10 @@ namespace {
 
 using namespace tile;
 
-// Beginning a unit -- its queries, the first scores, its results -- takes about as long as so many 64-token steps.
-constexpr int kBegin = 2;
+// Beginning a unit -- its queries, the first scores, its results -- takes about as long as so many 64-token steps: steps of two
+// query tiles, where the call has units of two, or the shorter ones of one.  (16 groups of 4 rows of 4 tokens behind 8192, 20 own
+// ones each: 72 us with 4, 92 with 2; behind 512 30.6 and 28.3.  One group of 64 rows of 1 behind 8200: 38.6 with 4, 36.1 with 2.)
+constexpr int kBegin = 2, kBeginOne = 4;
 
 // K and V pairs in the ring: 128 KB, which keeps HBM busy under short steps too.
 __host__ __device__ constexpr int phases_of(int d) { return 512 / d; }
@@ -57,7 +59,7 @@ template <int D>
 __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     shared_kernel(SharedParams P, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
   using C = Cfg<D>;
-  using Units = split::Walk<C::kRows, true, kTN, kBegin>;
+  using Units = split::Walk<C::kRows, true, kTN>;
   constexpr int NT = C::kTiles, kPh = phases_of(D), R = 2 * kPh, CB = D / 64;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* ring = smem + NT * C::kQ;
@@ -89,7 +91,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
   if (warp == 4 * NT) tc::tmem_alloc(&sm.tmem, 512);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const PartRec* near = p.part.plan_here ? plan_here<C::kThreads>(p, reinterpret_cast<int*>(ring)) : nullptr;
-  split::find_shares<C::kRows, 1, C::kThreads, true, kTN, kBegin>(p, sm.sum, sm.deal, &sm.share, near);
+  split::find_shares<C::kRows, 1, C::kThreads, true, kTN, kBegin, NT == 2 ? kBeginOne : kBegin>(p, sm.sum, sm.deal, &sm.share, near);
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
@@ -97,7 +99,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
   const int ps = kv.page_size, shift = __ffs(ps) - 1, box = min(ps, kTN), boxes = kTN / box;
   const int bshift = __ffs(box) - 1;
 
-  Units w(p, sm.share);
+  Units w(p, sm.share, sm.deal.start);
   bool ok = true;
   uint32_t at = 0;        // K and V tiles gone by; a K tile is entry at % R of the ring, its V tile the next
   uint32_t tiles = 0;     // cached tiles gone by
