@@ -39,7 +39,13 @@ struct SharedParams {
   float* o;      // [2 * kSms][kRows][D]
   float* stats;  // [2 * kSms][kRows][2]
   uint64_t wait_ns;
+  uint64_t g_magic, h_magic;  // magic_of G and Hkv
 };
+
+// n / by for 0 <= n < 2^31: a division by a value that only the call knows takes 100 cycles and more, and a unit's beginning
+// and end are full of them.  (magic is off by less than 1, so the product is by less than n 2^-63 < 1 / by.)
+inline uint64_t magic_of(int by) { return (1ull << 63) / by + 1; }
+__device__ __forceinline__ int divide(int n, uint64_t magic) { return (int)__umul64hi((uint64_t)n << 1, magic); }
 
 template <int D>
 struct Small {
@@ -107,8 +113,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
   const int role = warp - 4 * NT;  // < 0: softmax
 
   // Of the unit at hand: its kv-head, first query, and how many query tiles it has; the highest position of a query.
-  const auto head_of = [&]() { return w.h % kv.Hkv; };
-  const auto first_of = [&]() { return w.h / kv.Hkv * C::kRows; };
+  const auto first_of = [&]() { return divide(w.h, P.h_magic) * C::kRows; };
+  const auto head_of = [&]() { return w.h - divide(w.h, P.h_magic) * kv.Hkv; };
   const auto tiles_of = [&]() { return NT == 2 && w.u.r.len * p.G - first_of() > 128 ? 2 : 1; };
   const auto highest = [&]() { return p.window > 0 ? load(&part_recs(p.part)[w.n].hi) : 0; };
   // Some query may not see some token of [b, b + kTN).  (A row has one unit of a kv-head, so its first query is `lo`'s.)
@@ -129,9 +135,10 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       if (!w.valid() || tile >= tiles_of()) return;
       const int qi = first_of() + tile * 128 + row;
       const bool there = qi < w.u.r.len * p.G;
+      const int t = divide(qi, P.g_magic);  // token of the part
       int g = -1;
-      if (there) g = kv_token(p.rows, w.u.r.bos + qi / p.G, p.num_global, p.status);
-      const int64_t head = (int64_t)(head_of() * p.G + (there ? qi % p.G : 0)) * D;
+      if (there) g = kv_token(p.rows, w.u.r.bos + t, p.num_global, p.status);
+      const int64_t head = (int64_t)(head_of() * p.G + (there ? qi - t * p.G : 0)) * D;
       load_queries<D>(p, qt, 32 * (warp & 3), g >= 0 ? (int64_t)g * p.q_stride + head : -1);
       tc::fence_async_smem();
       tc::mbar_arrive(&sm.q_ready[tile]);
@@ -148,9 +155,10 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       }
       const int qi = first_of() + tile * 128 + row;
       const bool there = qi < w.u.r.len * p.G;
+      const int t = divide(qi, P.g_magic);
       // (without a window it does not matter how far behind a group's part its queries stand)
-      const int pos = p.window > 0 && there ? load(&part_tokens(p.part)[w.u.r.bos + qi / p.G].x)
-                                            : min(w.u.lo + qi / p.G, w.u.r.kv - 1);
+      const int pos = p.window > 0 && there ? load(&part_tokens(p.part)[w.u.r.bos + t].x)
+                                            : min(w.u.lo + t, w.u.r.kv - 1);
       float m = -INFINITY, l = 0.f;  // the maximum that the weights refer to (of scores before their scale); their
                                      // sum, both l's and O's 2^-kGrow of e^(s - m)'s
       bool wrote = false;            // O holds something, or will
@@ -230,12 +238,12 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       if (!ok) break;
       // where this piece goes
       const bool whole = w.j0 == 0 && w.len == w.u.tiles;
-      const int64_t place = ((int64_t)(w.n < p.part.groups ? 0 : p.part.tokens) + w.u.r.bos + qi / p.G) * p.Hq +
-                            head_of() * p.G + qi % p.G;
+      const int64_t place = ((int64_t)(w.n < p.part.groups ? 0 : p.part.tokens) + w.u.r.bos + t) * p.Hq +
+                            head_of() * p.G + qi - t * p.G;
       const int slot = 2 * blockIdx.x + (w.j0 == 0 ? 1 : 0), at_tile = tile * 128 + row;
       const int64_t to = whole ? place : (int64_t)slot * C::kRows + at_tile;
       if (there && w.j0 == 0)
-        p.part.range[place] = {whole ? -1 : (int)blockIdx.x, sm.deal.owner(w.unit_last(sm.share)), tile * 128 + row, 0};
+        p.part.range[place] = {whole ? -1 : (int)blockIdx.x, whole ? 0 : sm.deal.owner(w.unit_last(sm.share)), tile * 128 + row, 0};
       w.next();
       begin();  // the next unit's first scores come up while O goes out
       const uint32_t last = mine - 1;
@@ -445,6 +453,8 @@ cudaError_t launch_d(const AttnLaunch& a, cudaStream_t s) {
   P.stats = pieces.stats;
   P.o = pieces.o;
   P.wait_ns = kDefaultWaitNs;
+  P.g_magic = magic_of(a.G);
+  P.h_magic = magic_of(a.cache.Hkv);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
