@@ -39,13 +39,7 @@ struct SharedParams {
   float* o;      // [2 * kSms][kRows][D]
   float* stats;  // [2 * kSms][kRows][2]
   uint64_t wait_ns;
-  uint64_t g_magic, h_magic;  // magic_of G and Hkv
 };
-
-// n / by for 0 <= n < 2^31: a division by a value that only the call knows takes 100 cycles and more, and a unit's beginning
-// and end are full of them.  (magic is off by less than 1, so the product is by less than n 2^-63 < 1 / by.)
-inline uint64_t magic_of(int by) { return (1ull << 63) / by + 1; }
-__device__ __forceinline__ int divide(int n, uint64_t magic) { return (int)__umul64hi((uint64_t)n << 1, magic); }
 
 template <int D>
 struct Small {
@@ -113,8 +107,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
   const int role = warp - 4 * NT;  // < 0: softmax
 
   // Of the unit at hand: its kv-head, first query, and how many query tiles it has; the highest position of a query.
-  const auto first_of = [&]() { return divide(w.h, P.h_magic) * C::kRows; };
-  const auto head_of = [&]() { return w.h - divide(w.h, P.h_magic) * kv.Hkv; };
+  const auto first_of = [&]() { return by_magic(w.h, p.part.h_magic) * C::kRows; };
+  const auto head_of = [&]() { return w.h - by_magic(w.h, p.part.h_magic) * kv.Hkv; };
   const auto tiles_of = [&]() { return NT == 2 && w.u.r.len * p.G - first_of() > 128 ? 2 : 1; };
   const auto highest = [&]() { return p.window > 0 ? load(&part_recs(p.part)[w.n].hi) : 0; };
   // Some query may not see some token of [b, b + kTN).  (A row has one unit of a kv-head, so its first query is `lo`'s.)
@@ -135,7 +129,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       if (!w.valid() || tile >= tiles_of()) return;
       const int qi = first_of() + tile * 128 + row;
       const bool there = qi < w.u.r.len * p.G;
-      const int t = divide(qi, P.g_magic);  // token of the part
+      const int t = by_magic(qi, p.part.g_magic);  // token of the part
       int g = -1;
       if (there) g = kv_token(p.rows, w.u.r.bos + t, p.num_global, p.status);
       const int64_t head = (int64_t)(head_of() * p.G + (there ? qi - t * p.G : 0)) * D;
@@ -155,7 +149,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       }
       const int qi = first_of() + tile * 128 + row;
       const bool there = qi < w.u.r.len * p.G;
-      const int t = divide(qi, P.g_magic);
+      const int t = by_magic(qi, p.part.g_magic);
       // (without a window it does not matter how far behind a group's part its queries stand)
       const int pos = p.window > 0 && there ? load(&part_tokens(p.part)[w.u.r.bos + t].x)
                                             : min(w.u.lo + t, w.u.r.kv - 1);
@@ -453,8 +447,6 @@ cudaError_t launch_d(const AttnLaunch& a, cudaStream_t s) {
   P.stats = pieces.stats;
   P.o = pieces.o;
   P.wait_ns = kDefaultWaitNs;
-  P.g_magic = magic_of(a.G);
-  P.h_magic = magic_of(a.cache.Hkv);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;

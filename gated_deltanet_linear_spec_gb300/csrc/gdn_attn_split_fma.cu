@@ -117,24 +117,27 @@ __global__ void __launch_bounds__(32 * kWarps, per_sm(32 * E, PART)) split_fma_k
 
   for (Walk<kNQ, PART> w(p, share); w.valid(); w.next()) {
     const KvRow row = w.u.r;
-    const int h = w.h % kv.Hkv, q0 = w.h / kv.Hkv * kNQ, nq = min(kNQ, row.len * p.G - q0);
+    const auto by_g = [&](int n) { return PART ? by_magic(n, p.part.g_magic) : n / p.G; };
+    const int unit = PART ? by_magic(w.h, p.part.h_magic) : w.h / kv.Hkv;
+    const int h = w.h - unit * kv.Hkv, q0 = unit * kNQ, nq = min(kNQ, row.len * p.G - q0);
+    const int token = by_g(q0 + lane), head = q0 + lane - token * p.G;  // lane i: of query i
     const int first = PART ? w.u.lo : row.kv - row.len;  // position of the first new token, or the lowest of a query
     int g = -1;                          // lane i < nq: the query's global token
-    if (lane < nq) g = kv_token(p.rows, row.bos + (q0 + lane) / p.G, p.num_global, p.status);
+    if (lane < nq) g = kv_token(p.rows, row.bos + token, p.num_global, p.status);
     float q[kNQ][E];
 #pragma unroll
     for (int i = 0; i < kNQ; ++i) {
       const int gi = __shfl_sync(0xffffffffu, g, i);
       const T* from = static_cast<const T*>(p.q) + (int64_t)max(gi, 0) * p.q_stride;
-      load_row<E>(from + (int64_t)(h * p.G + (q0 + i) % p.G) * D + lane * E, columns && gi >= 0, q[i]);
+      load_row<E>(from + (int64_t)(h * p.G + __shfl_sync(0xffffffffu, head, i)) * D + lane * E, columns && gi >= 0, q[i]);
     }
     // the lowest position of a query of the unit, and the last token that one sees
-    const int pos0 = PART && p.window > 0 ? first : first + q0 / p.G;
-    const int pos1 = PART ? min(p.window > 0 ? INT32_MAX : first + (q0 + nq - 1) / p.G, row.kv - 1) : first + (q0 + nq - 1) / p.G;
+    const int pos0 = PART && p.window > 0 ? first : first + by_g(q0);
+    const int pos1 = PART ? min(p.window > 0 ? INT32_MAX : first + by_g(q0 + nq - 1), row.kv - 1) : first + by_g(q0 + nq - 1);
     const int mine = lane >> 2;  // the query whose scores, maximum and sum this lane has, those of every 4th token
-    int pos = min(first + (q0 + mine) / p.G, pos1);
+    int pos = min(first + by_g(q0 + mine), pos1);
     // (without a window it does not matter how far behind a group's part its queries stand)
-    if (PART && p.window > 0 && mine < nq) pos = load(&part_tokens(p.part)[row.bos + (q0 + mine) / p.G].x);
+    if (PART && p.window > 0 && mine < nq) pos = load(&part_tokens(p.part)[row.bos + by_g(q0 + mine)].x);
     float o[kNQ][E], m = -INFINITY, l = 0.f;
 #pragma unroll
     for (int i = 0; i < kNQ; ++i)
@@ -270,9 +273,9 @@ __global__ void __launch_bounds__(32 * kWarps, per_sm(32 * E, PART)) split_fma_k
 #pragma unroll
       for (int i = 0; i < kNQ; ++i) {
         const float li = __shfl_sync(0xffffffffu, l, 4 * i), mi = __shfl_sync(0xffffffffu, m, 4 * i);
+        const int ti = __shfl_sync(0xffffffffu, token, i), hi = __shfl_sync(0xffffffffu, head, i);
         if (i >= nq) continue;
-        const int64_t place = ((int64_t)(w.n < p.part.groups ? 0 : p.part.tokens) + row.bos + (q0 + i) / p.G) * p.Hq + h * p.G +
-                              (q0 + i) % p.G;
+        const int64_t place = ((int64_t)(w.n < p.part.groups ? 0 : p.part.tokens) + row.bos + ti) * p.Hq + h * p.G + hi;
         const int64_t at = whole ? place : (int64_t)slot * kNQ + i;
         float* dst = (whole ? p.part.o : P.part) + at * D + lane * E;
 #pragma unroll

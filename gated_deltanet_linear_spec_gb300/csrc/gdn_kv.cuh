@@ -109,6 +109,11 @@ struct PieceRange {
   int32_t c0, c1, qi, pad;
 };
 
+// n / by for 0 <= n < 2^31.  (A division by a value that only the call knows takes 100 cycles and more, and the beginnings and
+// ends of a pass's units are full of them.  magic is off by less than 1, so the product is by less than n 2^-63 < 1 / by.)
+inline uint64_t magic_of(int by) { return (1ull << 63) / by + 1; }
+__device__ __forceinline__ int by_magic(int n, uint64_t magic) { return (int)__umul64hi((uint64_t)n << 1, magic); }
+
 // A pass over parts, and where it leaves (m, l, o) of its pieces.  Queries are numbered (local token, q-head), those of groups'
 // parts first, then those of rows' own.
 struct PartDev {
@@ -123,6 +128,7 @@ struct PartDev {
   PieceRange* range;    // [2][tokens][Hq]
   float* ml;            // [2][tokens][Hq][2]: m (of the scores before their scale), l of a query in one piece
   float* o;             // [2][tokens][Hq][d], or with `quads` [2][d / 4][tokens][Hq][4]
+  uint64_t g_magic, h_magic;  // magic_of q-heads per kv-head and kv-heads
   int32_t quads;        // o, here and in pieces, by four columns: what neighbouring queries write is side by side
 };
 

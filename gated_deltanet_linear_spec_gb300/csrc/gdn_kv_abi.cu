@@ -268,6 +268,8 @@ void all_parts(AttnLaunch& p, int32_t num_groups, Pass pass) {
   p.part.groups = num_groups;
   p.part.count = num_groups + p.rows.num_seqs;
   p.part.tokens = p.rows.num_tokens;
+  p.part.g_magic = magic_of(p.G);
+  p.part.h_magic = magic_of(p.cache.Hkv);
   p.part.quads = pass == kTilePass;
   p.part.plan_here = group_plan_here(p);
 }
