@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(32 * kWarps) join_parts_kernel(JoinParams J) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int64_t all = (int64_t)part.tokens * p.Hq, q = (int64_t)blockIdx.x * (kWarps / J.team) + warp / J.team;
-  const int token = q < all ? (int)(q / p.Hq) : 0;
+  const int token = q < all ? (int)((uint32_t)q / (uint32_t)p.Hq) : 0;  // (a call has fewer than 2^31 queries)
   int2 rec = make_int2(-1, 0);
   PieceRange r[2] = {};
   int g = -1;
