@@ -2,6 +2,8 @@
 //
 // Both read a few integers per row and entry, 4 bytes an entry and row: what takes time is the launch and the loads that
 // depend on one another (bounds, rows, table).
+#include <algorithm>
+
 #include "gdn_attn_plan.cuh"
 
 namespace gdn {
@@ -48,26 +50,34 @@ __device__ __forceinline__ const int32_t* entries_of(const GroupsLaunch& p, int 
   return p.cache.table + (int64_t)table_row_of(p, n) * p.cache.max_pages;
 }
 
-// A cluster per group.  Its warps take runs of kRun entries of the rows in turn, those of all rows' beginnings first, and
+// A cluster per group, or `clusters` of them, which meet in prefix[g] (set to the highest value before).  Its warps take runs of kRun entries of the rows in turn, those of all rows' beginnings first, and
 // compare them with those of the group's first row; what lies behind a place where rows were seen to part is left out.
-// 16 groups of 9 to 24 rows that share up to 8192 entries: 59 us with a warp per row, 11 so; what bounds it is
-// its chain of loads: bounds, rows, two entries (5 MB in all; 4 rows of 777 tokens take 3.2).
+// 16 groups of 9 to 24 rows that share up to 8192 entries: 59 us with a warp per row, 9 so; what bounds it is its chain of
+// loads: bounds, rows, entries (5 MB in all; 4 rows of 777 tokens take 3.2).
 constexpr int kAhead = 8;  // entries of a lane that are on their way
 constexpr int kRun = 32 * kAhead;
 
+__global__ void __launch_bounds__(kThreads) begin_kernel(GroupsLaunch p) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int g = blockIdx.x * kThreads + threadIdx.x;
+  if (g < p.num_groups) p.prefix[g] = INT32_MAX;
+}
+
 template <int THREADS>
-__global__ void __cluster_dims__(kCluster) __launch_bounds__(THREADS) common_kernel(GroupsLaunch p) {
+__global__ void __cluster_dims__(kCluster) __launch_bounds__(THREADS) common_kernel(GroupsLaunch p, int clusters) {
   constexpr int kWarps = THREADS / 32;
   __shared__ int least[kWarps], first[kWarps];
   __shared__ int agree;
-  const int g = blockIdx.x / kCluster, rank = cluster_rank();
+  const int cluster = blockIdx.x / kCluster, g = cluster / clusters, mine = cluster - g * clusters, rank = cluster_rank();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   int a, b;
-  if (!group_rows(p, g, a, b, rank == 0 ? p.status : nullptr)) a = b = 0;
+  uint32_t* st = mine == 0 && rank == 0 ? p.status : nullptr;
+  if (!group_rows(p, g, a, b, st)) a = b = 0;
   GroupRows s;
-  for (int n = a + (int)threadIdx.x; n < b; n += THREADS) add_row(p, n, s, rank == 0 ? p.status : nullptr);
+  for (int n = a + (int)threadIdx.x; n < b; n += THREADS) add_row(p, n, s, st);
   s.warp_meet();
   if (lane == 0) {
     least[warp] = s.least;
@@ -83,18 +93,18 @@ __global__ void __cluster_dims__(kCluster) __launch_bounds__(THREADS) common_ker
     const int32_t* of_first = entries_of(p, s.first);
     const int rows = b - a;
     const int64_t runs = (int64_t)((whole + kRun - 1) / kRun) * rows;
-    for (int64_t i = rank * kWarps + warp; i < runs; i += kCluster * kWarps) {
+    for (int64_t i = (mine * kCluster + rank) * kWarps + warp; i < runs; i += clusters * kCluster * kWarps) {
       const int n = a + (int)(i % rows), e0 = (int)(i / rows) * kRun;
       if (e0 >= *(volatile int*)&agree) break;
       KvRow r;
       if (n == s.first || !load_kv_row(p.rows, p.cache, n, r, nullptr) || r.len == 0) continue;
-      const int32_t* mine = p.cache.table + (int64_t)r.trow * p.cache.max_pages;
+      const int32_t* of_row = p.cache.table + (int64_t)r.trow * p.cache.max_pages;
       bool differs[kAhead];
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
         const int e = e0 + 32 * u + lane;
         differs[u] = e < whole && page_or_null(load(of_first + e), p.cache, p.status) !=
-                                      page_or_null(load(mine + e), p.cache, p.status);
+                                      page_or_null(load(of_row + e), p.cache, p.status);
       }
       int at = whole;
 #pragma unroll
@@ -110,7 +120,8 @@ __global__ void __cluster_dims__(kCluster) __launch_bounds__(THREADS) common_ker
   if (rank == 0 && warp == 0) {
     int v = lane < kCluster ? from_rank(&agree, lane) : INT32_MAX;
     v = __reduce_min_sync(0xffffffffu, v);
-    if (lane == 0) p.prefix[g] = v * p.cache.page_size;
+    if (lane == 0 && clusters == 1) p.prefix[g] = v * p.cache.page_size;
+    if (lane == 0 && clusters > 1) atomicMin(p.prefix + g, v * p.cache.page_size);
   }
   cluster_sync();  // (no CTA ends while another reads its shared memory)
 }
@@ -172,27 +183,34 @@ __global__ void __cluster_dims__(kCluster) __launch_bounds__(kThreads) group_pla
   }
 }
 
-cudaError_t launch_cluster(void (*kernel)(GroupsLaunch), int clusters, int threads, const GroupsLaunch& p, cudaStream_t s) {
+template <typename... Args>
+cudaError_t launch(void (*kernel)(Args...), int blocks, int threads, cudaStream_t s, Args... args) {
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(clusters * kCluster);
+  cfg.gridDim = dim3(blocks);
   cfg.blockDim = dim3(threads);
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p);
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 }  // namespace
 
 // Blocks of 1024 threads where a group's rows may have more entries than a cluster of smaller ones takes at once: those 16
-// groups 11 us, with blocks of 256 19; 4 rows of 64 entries 3.6 us with blocks of 1024, 3.2 with 256.
+// groups 11 us, with blocks of 256 19; 4 rows of 64 entries 3.6 us with blocks of 1024, 3.2 with 256.  And as many clusters
+// a group as have 65536 entries each to go over at once, behind a launch that sets what they meet in: one group of 16 rows of
+// 8192 entries 5.7 us instead of 6.8, of 64 6 (18), of 256 7.5 (60); those 16 groups 9.2.
 cudaError_t launch_kv_common_prefix(const GroupsLaunch& p, cudaStream_t s) {
   const int64_t entries = (int64_t)p.cache.max_pages * p.rows.num_seqs / p.num_groups;
-  return entries > kCluster * kThreads * kAhead ? launch_cluster(common_kernel<1024>, p.num_groups, 1024, p, s)
-                                                : launch_cluster(common_kernel<kThreads>, p.num_groups, kThreads, p, s);
+  if (entries <= kCluster * kThreads * kAhead)
+    return launch(common_kernel<kThreads>, p.num_groups * kCluster, kThreads, s, p, 1);
+  const int clusters = (int)std::min<int64_t>(entries / (kCluster * 1024 * kAhead), 2 * kSms / kCluster / p.num_groups);
+  if (clusters < 2) return launch(common_kernel<1024>, p.num_groups * kCluster, 1024, s, p, 1);
+  const cudaError_t e = launch(begin_kernel, (p.num_groups + kThreads - 1) / kThreads, kThreads, s, p);
+  return e != cudaSuccess ? e : launch(common_kernel<1024>, p.num_groups * clusters * kCluster, 1024, s, p, clusters);
 }
 
 // Every CTA goes over all rows, groups and tokens then, a warp per group.  Against a kernel for the plan, us a call: 4 rows of a
@@ -205,7 +223,7 @@ bool group_plan_here(const AttnLaunch& p) {
 }
 
 cudaError_t launch_group_plan(const GroupsLaunch& p, cudaStream_t s) {
-  return launch_cluster(group_plan_kernel, 1, kThreads, p, s);
+  return launch(group_plan_kernel, kCluster, kThreads, s, p);
 }
 
 }  // namespace gdn

@@ -386,6 +386,28 @@ def test_common_prefix_ends_where_one_row_leaves(at):
     assert s.groups.prefix_lens.tolist() == [16 * at]
 
 
+@pytest.mark.parametrize("rows,entries,at", [(256, 8192, 8192), (256, 8192, 8000), (200, 8192, 31), (64, 8192, 4097), (40, 8000, 0)])
+@pytest.mark.parametrize("groups", [1, 3])
+def test_common_prefix_of_many_long_rows(rows, entries, at, groups):
+    """More entries than one cluster should go over alone; a row late in the group leaves at `at`, which may be the end."""
+    gen = torch.Generator().manual_seed(at)
+    first = torch.randint(1, 1000, (groups, entries), generator=gen, dtype=torch.int32)
+    table = first.repeat_interleave(rows, 0)
+    if at < entries:
+        table[rows - 2, at] = 1000  # (of the first group)
+    pool = torch.zeros(1001, 1, 16, 16, device="cuda")
+    n = rows * groups
+    cache = gdn.KvCache(pool, pool, table.cuda())
+    kv_rows = gdn.KvRows(i32(list(range(n + 1))), n, i32([entries * 16] * n), 1)
+    of_groups = gdn.KvGroups(i32([g * rows for g in range(groups + 1)]), i32([-7] * groups))
+    status = i32([0])
+    for _ in range(2):
+        gdn.gdn_kv_common_prefix(cache, kv_rows, of_groups, status=status)
+        # the last entry holds the new token's page, so it is no whole page before it
+        want = [16 * min(at, entries - 1)] + [16 * (entries - 1)] * (groups - 1)
+        assert of_groups.prefix_lens.tolist() == want and int(status) == 0
+
+
 # ------------------------------------------------------------------------------------------
 # all of it together
 
