@@ -12,7 +12,7 @@
 // its scores, softmax and second product wait for one another.
 //
 // Measured (32 q-heads, 4 kv-heads, d = 128): 64 rows of 4 tokens behind 32768 shared ones 145 us, 0.96 PFLOP/s; 64 of 1 behind
-// 8200, up to 1024 own tokens each, 36 us (two thirds of the tiles are own ones).  With 128 tokens a step, which leave room for
+// 8200, up to 1024 own tokens each, 35 us (two thirds of the tiles are own ones).  With 128 tokens a step, which leave room for
 // one score buffer, the first took 155 us (151 at that time); with the rows' own parts on mma.sync beside this kernel's
 // end 158 and the second 49 (151 and 40).
 #include <algorithm>

@@ -28,8 +28,9 @@ constexpr int kWarps = 4;   // workers of a CTA
 constexpr int kPerSm = 2;   // CTAs
 constexpr int kNQ = 8;      // queries of a unit
 // CTAs of an SM in a pass over parts: with few columns a lane its registers leave room for more.  (3 groups of 5 to 8 rows of 3
-// tokens behind 300 to 4096 shared ones, 8 q-heads, 2 kv-heads, 32 bits, d = 64: 34.5 us, with two 35.4; 64-query tiles
-// staged in shared memory 36 to 38.  FMAs and exchanges bound it, 60% of the issue slots.)
+// tokens behind 300 to 4096 shared ones, 8 q-heads, 2 kv-heads, 32 bits, d = 64: 34.5 us, with two 35.4; 33.3
+// since quotients go by multiplication.  64-query tiles staged in shared memory took 36 to 38.  FMAs and exchanges bound it,
+// 63% of the issue slots.)
 constexpr int kPartsPerSm = 3;
 constexpr int per_sm(int d, bool part) { return part && d <= 64 ? kPartsPerSm : kPerSm; }
 static_assert(kSms * kPartsPerSm <= kMaxPassCtas, "copies of the plan");

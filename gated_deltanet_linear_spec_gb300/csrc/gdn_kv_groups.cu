@@ -50,8 +50,9 @@ __device__ __forceinline__ const int32_t* entries_of(const GroupsLaunch& p, int 
   return p.cache.table + (int64_t)table_row_of(p, n) * p.cache.max_pages;
 }
 
-// A cluster per group, or `clusters` of them, which meet in prefix[g] (set to the highest value before).  Its warps take runs of kRun entries of the rows in turn, those of all rows' beginnings first, and
-// compare them with those of the group's first row; what lies behind a place where rows were seen to part is left out.
+// A cluster per group, or `clusters` of them, which meet in prefix[g] (set to the highest value before).  Its warps take runs
+// of kRun entries of the rows in turn, those of all rows' beginnings first, and compare them with those of the group's
+// first row; what lies behind a place where rows were seen to part is left out.
 // 16 groups of 9 to 24 rows that share up to 8192 entries: 59 us with a warp per row, 9 so; what bounds it is its chain of
 // loads: bounds, rows, entries (5 MB in all; 4 rows of 777 tokens take 3.2).
 constexpr int kAhead = 8;  // entries of a lane that are on their way
