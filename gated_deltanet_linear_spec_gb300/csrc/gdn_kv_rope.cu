@@ -6,11 +6,12 @@
 // 0.06 at 10^6.  The turn's quarter comes from the top bits, and what is left, at most an eighth of a turn, goes
 // through sincospi in 32 bits: cosine and sine are off by 2^-23 at most.
 //
-// Every value is read and written once, so HBM bounds long calls and the launch short ones: 8192 tokens of 32 heads (bf16, d =
-// 128, 134 MB) take 20.7 us, 6.5 TB/s; 8192 into the cache (16 q, 2 kv heads, d = 256, 168 MB) 30.4, 5.5 TB/s, as every store
-// to a page waits for a chain of token, row, table and page; one token 1.8.  A block takes a few tokens with all their heads: its threads' values are on their way while it looks up the tokens' rows and pages and works
-// out the tokens' cosines and sines, which all heads share, in shared memory.  A thread reads and writes both values of a
-// pair, so a call may work in place.
+// Every value is read and written once, so HBM bounds long calls and the launch short ones: 8192 tokens of 32 heads (bf16, d
+// = 128, 134 MB) take 20.7 us, 6.5 TB/s; 8192 into the cache (16 q, 2 kv heads, d = 256, 168 MB) 30.4, 5.5 TB/s, as every
+// store to a page waits for a chain of token, row, table and page; one token 1.8.  A block takes a few tokens with all their
+// heads: its threads' values are on their way while it looks up the tokens' rows and pages and works out the tokens' cosines
+// and sines, which all heads share, in shared memory.  A thread reads and writes both values of a pair, so a call may work
+// in place.
 #include <algorithm>
 
 #include "gdn_kv.cuh"
@@ -117,7 +118,8 @@ struct Vec {
 // would leave every 32 bytes to two stores.
 template <typename T, int PAIRS, bool APPEND>
 __global__ void __launch_bounds__(threads_of(PAIRS), 1024 / threads_of(PAIRS)) turn_kernel(TurnParams P) {
-  constexpr int kThreads = threads_of(PAIRS), VE = 16 / (int)sizeof(T), E = PAIRS == kHalfAny ? 1 : PAIRS == kHalf ? VE : VE / 2;  // E: pairs of a vector
+  constexpr int kThreads = threads_of(PAIRS), VE = 16 / (int)sizeof(T);
+  constexpr int E = PAIRS == kHalfAny ? 1 : PAIRS == kHalf ? VE : VE / 2;  // pairs of a vector
   __shared__ float2 cs[kTokens][kPairs];
   __shared__ Place places[kTokens];
   const TurnLaunch& p = P.a;

@@ -407,10 +407,11 @@ typedef struct {
  * two rows of the group have new tokens; prefix_lens <= 0 shares nothing.  They are read by the table row of the
  * first such row: where the rows' entries differ after all, its pages count.  A row is in one group at most: where
  * group bounds do not ascend or leave the rows (GDN_STATUS_ROW_RANGE), nothing is shared.
- * bf16 rows of more than 256 queries per kv-head (d = 64, 128; 128 at d = 256; max_query_len decides) go over their whole
- * caches as in gdn_paged_attention, whatever the groups are: they fill the tensor cores by themselves.  Else bf16 weights (d = 64,
- * 128, 256) go into the second sum as one bf16.  Sharing pays from about a thousand tokens on for groups of four rows or more, from several thousand on
- * for pairs; below, a call takes up to twice as long as in gdn_paged_attention, which finds the other rows' pages in the L2.
+ * bf16 rows of more than 256 queries per kv-head (d = 64, 128; 128 at d = 256; max_query_len decides) go over their
+ * whole caches as in gdn_paged_attention, whatever the groups are: they fill the tensor cores by themselves.  Else bf16
+ * weights (d = 64, 128, 256) go into the second sum as one bf16.  Sharing pays from about a thousand tokens on for
+ * groups of four rows or more, from several thousand on for pairs; below, a call takes up to twice as long as in
+ * gdn_paged_attention, which finds the other rows' pages in the L2.
  * workspace: at least gdn_shared_attention_workspace_bytes(attn, cache, rows, groups) bytes, 256-byte aligned; it holds
  * the plan (a copy for each CTA that makes its own), two states of (2 + d) fp32 per query and head, and partial results.
  */
