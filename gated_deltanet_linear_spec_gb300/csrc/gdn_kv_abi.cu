@@ -93,7 +93,8 @@ bool entangled(const void* x, int64_t x_stride, int64_t x_width, const void* out
   if (tokens < 1) return false;
   const int64_t a = (int64_t)reinterpret_cast<uintptr_t>(x), b = (int64_t)reinterpret_cast<uintptr_t>(out);
   const int64_t aw = x_width * es, bw = out_width * es, stride = x_stride * es;
-  const int64_t a_end = a + (tokens - 1) * stride + aw, b_end = b + (tokens - 1) * out_stride * es + bw;
+  const __int128 steps = tokens - 1;  // (2^31 tokens of 2^42 bytes are more than 64 bits hold)
+  const __int128 a_end = a + steps * stride + aw, b_end = b + steps * (out_stride * es) + bw;
   if (a_end <= b || b_end <= a || (in_place && a == b && (tokens == 1 || x_stride == out_stride))) return false;
   if (tokens == 1 || x_stride != out_stride) return true;
   const int64_t between = ((b - a) % stride + stride) % stride;

@@ -157,6 +157,9 @@ def test_overlaps_are_refused(lib):  # noqa: F811
     assert call_rope(lib, rope(), xs=512, os_=512, out=FAKE + 1024 + 768) == SHAPE
     assert call_rope(lib, rope(), xs=512, out=FAKE) == SHAPE                   # in place with another stride
     assert call_rope(lib, rope(), n=1, out=FAKE + 16) == SHAPE
+    far = dict(xs=1 << 40, os_=1 << 40)                                         # 2^64 bytes and more from first to last
+    assert call_rope(lib, rope(), n=1 << 23, out=FAKE + 256, **far) == SHAPE
+    assert call_rope(lib, rope(), n=(1 << 31) - 1, out=FAKE - 256, **far) == SHAPE
     # queries into keys' or values' places
     wide = dict(ks=1024, vs=1024, qs=1024, os_=1024)
     assert call_append(lib, cache(), rows(), rope(), k=FAKE, v=FAKE + 256, q=FAKE + 512, out=FAKE, **wide) == SHAPE
