@@ -242,7 +242,7 @@ cudaError_t launch_pairs(const TurnLaunch& a, cudaStream_t s) {
   const auto rounds = [&](int tokens) { return (tokens * P.heads + held - 1) / held; };
   P.tb = 1;
   for (int t = 2; t <= kTokens; ++t)
-    if (rounds(t) * P.tb < rounds(P.tb) * t) P.tb = t;
+    if ((int64_t)t * P.heads * P.heads < (1ll << 32) && rounds(t) * P.tb < rounds(P.tb) * t) P.tb = t;  // (see divide)
   P.tb = std::max(1, std::min(P.tb, a.num_tokens / (4 * kSms)));
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -328,3 +328,20 @@ def test_append_in_a_graph():
     b.k_pool.fill_(5.0)
     gdn.gdn_kv_append_rope(b.cache, b.kv_rows, rope, b.k, b.v, b.q, out)
     assert torch.equal(got, out) and torch.equal(pool, b.k_pool)
+
+
+def test_more_heads_than_quotients_of_a_block_of_tokens_hold():
+    """33308 heads: the last of a block's fourth token would be taken for one of a fifth.  Against calls of so few tokens that a
+    block has one."""
+    tokens, heads, dim = 2432, 33308, 16
+    rope = gdn.Rope(dim)
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(tokens, heads, dim, generator=gen, device="cuda", dtype=torch.bfloat16)
+    positions = torch.arange(tokens, dtype=torch.int32, device="cuda")
+    got = torch.full_like(x, 7.0)
+    gdn.gdn_rope(rope, positions, x, got)
+    for at in range(0, tokens, 608):
+        part = slice(at, at + 608)
+        want = torch.empty_like(x[part])
+        gdn.gdn_rope(rope, positions[part], x[part], want)
+        assert torch.equal(got[part], want)
