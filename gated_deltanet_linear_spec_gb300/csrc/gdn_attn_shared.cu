@@ -11,10 +11,13 @@
 // does not have (few queries, a row's own part) takes no part in its steps; a step takes little less time for that, as
 // its scores, softmax and second product wait for one another.
 //
-// Measured (32 q-heads, 4 kv-heads, d = 128): 64 rows of 4 tokens behind 32768 shared ones 145 us, 0.96 PFLOP/s; 64 of 1 behind
-// 8200, up to 1024 own tokens each, 35 us (two thirds of the tiles are own ones).  With 128 tokens a step, which leave room for
-// one score buffer, the first took 155 us (151 at that time); with the rows' own parts on mma.sync beside this kernel's
-// end 158 and the second 49 (151 and 40).
+// Weights go into the second product as two bf16 terms, 16 bits, in calls whose rows attention without groups gives as many:
+// the scores' 64 columns of TMEM hold both.  With one term the first call below took 145 us and the second 35.
+//
+// Measured (32 q-heads, 4 kv-heads, d = 128): 64 rows of 4 tokens behind 32768 shared ones 164 us, 0.84 PFLOP/s; 64 of 1 behind
+// 8200, up to 1024 own tokens each, 39 us (two thirds of the tiles are own ones).  With 128 tokens a step, which leave room for
+// one score buffer, the first took 155 us (151 at that time, with one term); with the rows' own parts on mma.sync beside
+// this kernel's end 158 and the second 49 (151 and 40).
 #include <algorithm>
 
 #include "gdn_attn_share.cuh"
@@ -55,7 +58,8 @@ struct Small {
   uint32_t tmem;
 };
 
-template <int D>
+// PAIR: weights go into the second product as two bf16 terms (over the scores, which take twice the room).
+template <int D, bool PAIR>
 __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     shared_kernel(SharedParams P, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
   using C = Cfg<D>;
@@ -202,10 +206,20 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         const float ms = m == -INFINITY ? 0.f : fmaf(-m, sl2, -kGrow);  // so that no weight passes 1
         const uint64_t scale = pair(sl2, sl2), shift2 = pair(ms, ms);
         uint64_t sum[2] = {0, 0};
-        float u[32];
-        weights32(r[0], scale, shift2, sum, u);
-        weights32(r[1], scale, shift2, sum, u + 16);
-        tc::tmem_st32(s_col, u);
+        if constexpr (PAIR) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float u[16], low[16];
+            weights32<true>(r[i], scale, shift2, sum, u, low);
+            tc::tmem_st16(s_col + 16 * i, u);
+            tc::tmem_st16(s_col + 32 + 16 * i, low);
+          }
+        } else {
+          float u[32];
+          weights32(r[0], scale, shift2, sum, u);
+          weights32(r[1], scale, shift2, sum, u + 16);
+          tc::tmem_st32(s_col, u);
+        }
         {
           float a0, a1;
           unpair(add2(sum[0], sum[1]), a0, a1);
@@ -222,7 +236,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             } else {
               clear_o<D>(o_col);
             }
-            add_listed<D>(p, w.u.r.trow, head_of(), sm.bad[phase], b, pos, s_col, o_col);
+            add_listed<D, PAIR>(p, w.u.r.trow, head_of(), sm.bad[phase], b, pos, s_col, o_col);
           }
         }
         tc::fence_before();
@@ -305,7 +319,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             if (i >= nt) continue;
             const uint32_t d = done[i] + j, buf = d & 1;
             if (!wait(&sm.p_ready[i][buf], d >> 1)) break;
-            pv_products<D>(base, i, phase, i * 128 + buf * 64, onto);
+            pv_products<D, PAIR>(base, i, phase, i * 128 + buf * 64, onto);
             tc::commit(&sm.pv_done[i][buf]);
           }
           tc::commit(&sm.empty[2 * phase + 1]);
@@ -428,14 +442,14 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
   }
 }
 
-template <int D>
+template <int D, bool PAIR>
 cudaError_t launch_d(const AttnLaunch& a, cudaStream_t s) {
   using C = Cfg<D>;
   static std::atomic<uint64_t> done{0};
   constexpr int smem = (int)(C::kTiles * C::kQ + 2 * phases_of(D) * C::kKv + sizeof(Small<D>));
   static_assert(smem <= 232448, "shared memory");
   cudaError_t e = once_per_device(done, [&] {
-    return cudaFuncSetAttribute(shared_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    return cudaFuncSetAttribute(shared_kernel<D, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   });
   if (e != cudaSuccess) return e;
   CUtensorMap kmap, vmap;
@@ -457,7 +471,14 @@ cudaError_t launch_d(const AttnLaunch& a, cudaStream_t s) {
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, shared_kernel<D>, P, kmap, vmap);
+  return cudaLaunchKernelEx(&cfg, shared_kernel<D, PAIR>, P, kmap, vmap);
+}
+
+template <bool PAIR>
+cudaError_t launch_any(const AttnLaunch& a, cudaStream_t s) {
+  return a.cache.d == 64    ? launch_d<64, PAIR>(a, s)
+         : a.cache.d == 128 ? launch_d<128, PAIR>(a, s)
+                            : launch_d<256, PAIR>(a, s);
 }
 
 int rows_of_cta(const AttnLaunch& a) { return a.cache.d <= 128 ? Cfg<128>::kRows : Cfg<256>::kRows; }
@@ -476,8 +497,10 @@ PartPieces attn_shared_pieces(const AttnLaunch& a, void* ws) {
   return {stats, stats + (size_t)4 * kSms * rows, rows};
 }
 
+// Two terms a weight wherever attention without groups would take some row of the call to the split kernel, which keeps 16 bits.
 cudaError_t launch_attn_shared(const AttnLaunch& a, cudaStream_t s) {
-  return a.cache.d == 64 ? launch_d<64>(a, s) : a.cache.d == 128 ? launch_d<128>(a, s) : launch_d<256>(a, s);
+  const bool pair = attn_split_supported(a, GDN_BF16) || attn_few(a, GDN_BF16) > 0;
+  return pair ? launch_any<true>(a, s) : launch_any<false>(a, s);
 }
 
 }  // namespace gdn

@@ -68,15 +68,18 @@ __device__ __forceinline__ void s_products(uint32_t smem, uint32_t tile, uint32_
     tc::mma(to, q + ((s >> 2) * 16384 + (s & 3) * 32) / 16, k + ((s >> 2) * 1024 + (s & 3) * 32) / 16,
             tc::idesc_bf16(128, kTN), s > 0);
 }
-// O += P V of a query tile with the V tile of a ring phase; the weights stand from TMEM column `from` on.
-template <int D>
+// O += P V of a query tile with the V tile of a ring phase; the weights stand from TMEM column `from` on, with PAIR what
+// their first 8 bits leave from column `from` + 32 on.
+template <int D, bool PAIR = false>
 __device__ __forceinline__ void pv_products(uint32_t smem, uint32_t tile, uint32_t phase, uint32_t from, bool onto) {
   using C = Cfg<D>;
   const uint64_t v = tc::sdesc_lbo(smem + C::kTiles * C::kQ + (2 * phase + 1) * C::kKv, 1024, D / 64 * 1024);
 #pragma unroll
-  for (int s = 0; s < kTN / 16; ++s)
-    mma_ts(C::kO + tile * D, from + s * 8, v + s * 2 * (D / 64) * 1024 / 16, tc::idesc_bf16_bmn(128, D),
-           s == 0 ? (uint32_t)onto : 1u);
+  for (int s = 0; s < kTN / 16; ++s) {
+    const uint64_t b = v + s * 2 * (D / 64) * 1024 / 16;
+    mma_ts(C::kO + tile * D, from + s * 8, b, tc::idesc_bf16_bmn(128, D), s == 0 ? (uint32_t)onto : 1u);
+    if (PAIR) mma_ts(C::kO + tile * D, from + 32 + s * 8, b, tc::idesc_bf16_bmn(128, D), 1u);
+  }
 }
 
 // 32 columns of this thread's TMEM lane: the load is on its way until ld_wait, which the values pass through.
@@ -152,9 +155,12 @@ __device__ __forceinline__ void hide(uint32_t (&r)[32], uint32_t vis) {
   for (int i = 0; i < 32; ++i) r[i] = vis >> i & 1u ? r[i] : 0xff800000u;
 }
 
-// The weights 2^(sl2 s + ms) of 32 scores as 16 bf16 pairs; added to sum.
+// The weights 2^(sl2 s + ms) of 32 scores as 16 bf16 pairs; added to sum.  With PAIR they are cut to their first 8 bits, and `low`
+// takes what that leaves, below 2^-7 of the weight and rounded to 8 bits: off by 2^-16 of the weight at most.  (Rounding
+// the first term too would make it 2^-17, for 2 us of 164 where units have two query tiles and 1.4 of 39 where they have one.)
+template <bool PAIR = false>
 __device__ __forceinline__ void weights32(const uint32_t (&r)[32], uint64_t scale, uint64_t shift, uint64_t (&sum)[2],
-                                          float* u) {
+                                          float* u, float* low = nullptr) {
 #pragma unroll
   for (int i = 0; i < 32; i += 2) {
     float a, b;
@@ -162,7 +168,15 @@ __device__ __forceinline__ void weights32(const uint32_t (&r)[32], uint64_t scal
     a = ex2(a);
     b = ex2(b);
     sum[i / 2 & 1] = add2(sum[i / 2 & 1], pair(a, b));
-    u[i / 2] = pack2f(a, b);
+    if constexpr (PAIR) {
+      u[i / 2] = __uint_as_float(__byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632));
+      const uint64_t h = pair(__uint_as_float(__float_as_uint(a) & 0xffff0000u), __uint_as_float(__float_as_uint(b) & 0xffff0000u));
+      float la, lb;
+      unpair(fma2(h, pair(-1.f, -1.f), pair(a, b)), la, lb);
+      low[i / 2] = pack2f(la, lb);
+    } else {
+      u[i / 2] = pack2f(a, b);
+    }
   }
 }
 
@@ -190,23 +204,27 @@ __device__ __forceinline__ void clear_o(uint32_t o_col) {
   tc::tmem_st_wait();
 }
 
-// Adds the listed tokens' share to O where the query, at `pos`, sees them: their weights from P, their values from
-// the cache.  O is complete up to the tile before; the warp's lanes go together, as TMEM loads and stores need
+// Adds the listed tokens' share to O where the query, at `pos`, sees them: their weights from P (PAIR: both terms of them), their
+// values from the cache.  O is complete up to the tile before; the warp's lanes go together, as TMEM loads and stores need
 // them all.
-template <int D>
+template <int D, bool PAIR = false>
 __device__ __forceinline__ void add_listed(const AttnLaunch& p, int trow, int h, const uint32_t* bad, int b, int pos,
                                            uint32_t p_col, uint32_t o_col) {
   const KvDev& kv = p.cache;
 #pragma unroll 1
   for (int t = 0; t < kTN; ++t) {
     if (!(bad[t >> 5] >> (t & 31) & 1u)) continue;
-    float x[8];
-    uint32_t u = 0;
-    tc::tmem_ld8(p_col + (t >> 1 & ~7), x);
+    float weight = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if ((t >> 1 & 7) == i) u = __float_as_uint(x[i]);
-    const float weight = __uint_as_float(t & 1 ? u & 0xffff0000u : u << 16);
+    for (int term = 0; term < (PAIR ? 2 : 1); ++term) {
+      float x[8];
+      uint32_t u = 0;
+      tc::tmem_ld8(p_col + 32 * term + (t >> 1 & ~7), x);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if ((t >> 1 & 7) == i) u = __float_as_uint(x[i]);
+      weight += __uint_as_float(t & 1 ? u & 0xffff0000u : u << 16);
+    }
     const int tok = b + t;  // below the row's end, in a page that is not NULL
     const bool seen = tok <= pos && (p.window <= 0 || tok > pos - p.window || tok < p.sinks);
     const int page = kv.table[(int64_t)trow * kv.max_pages + tok / kv.page_size];

@@ -408,8 +408,10 @@ typedef struct {
  * first such row: where the rows' entries differ after all, its pages count.  A row is in one group at most: where
  * group bounds do not ascend or leave the rows (GDN_STATUS_ROW_RANGE), nothing is shared.
  * bf16 rows of more than 256 queries per kv-head (d = 64, 128; 128 at d = 256; max_query_len decides) go over their
- * whole caches as in gdn_paged_attention, whatever the groups are: they fill the tensor cores by themselves.  Else bf16
- * weights (d = 64, 128, 256) go into the second sum as one bf16.  Sharing pays from about a thousand tokens on for
+ * whole caches as in gdn_paged_attention, whatever the groups are: they fill the tensor cores by themselves.  Weights go
+ * into the second sum with the bits that gdn_paged_attention keeps of them: 16 of bf16 rows (d = 64, 128, 256) in calls
+ * without a row of more than 64 queries per kv-head, and of all rows in calls that it would take both ways; 8 in the rest.
+ * Sharing pays from about a thousand tokens on for
  * groups of four rows or more, from several thousand on for pairs; below, a call takes up to twice as long as in
  * gdn_paged_attention, which finds the other rows' pages in the L2.
  * workspace: at least gdn_shared_attention_workspace_bytes(attn, cache, rows, groups) bytes, 256-byte aligned; it holds
