@@ -107,7 +107,7 @@ EXPORTS = ("gdn_workspace_bytes", "gdn_prefill_workspace_bytes", "gdn_conv_updat
            "gdn_shared_attention_workspace_bytes", "gdn_kv_common_prefix", "gdn_rope", "gdn_rope_turns", "gdn_rope_turns_of",
            "gdn_kv_append_rope")
 # include/gdn_testing.h: hooks that let tests drive the kernels' failure paths
-TESTING_EXPORTS = ("gdn_testing_set_prefill_faults",)
+TESTING_EXPORTS = ("gdn_testing_set_prefill_faults", "gdn_testing_set_shared_faults")
 STATIC_WORKSPACE_BYTES = 16 << 20
 
 _lib = None
@@ -170,8 +170,9 @@ def library() -> ctypes.CDLL:
                                                           I64, VP, I64, I32, VP, VP])):
                 fn = getattr(lib, name)
                 fn.restype, fn.argtypes = res, args
-            lib.gdn_testing_set_prefill_faults.restype = ctypes.c_int
-            lib.gdn_testing_set_prefill_faults.argtypes = [ctypes.c_uint64, I32]
+            for hook in TESTING_EXPORTS:
+                getattr(lib, hook).restype = ctypes.c_int
+                getattr(lib, hook).argtypes = [ctypes.c_uint64, I32]
             _lib = lib
     return _lib
 
@@ -816,10 +817,16 @@ def gdn_testing_set_prefill_faults(wait_ns: int = 0, drop_copy_chunk: int = -1) 
     _check(library().gdn_testing_set_prefill_faults(int(wait_ns), int(drop_copy_chunk)))
 
 
+def gdn_testing_set_shared_faults(wait_ns: int = 0, stop_tile: int = -1) -> None:
+    """Test hook (include/gdn_testing.h): the limit of the waits in gdn_shared_attention's tensor-core pass (0 = the default) and
+    the tile of a CTA's share at which its fetches end (< 0 = none), for every later call in this process."""
+    _check(library().gdn_testing_set_shared_faults(int(wait_ns), int(stop_tile)))
+
+
 __all__ = ["Layer", "Params", "Pools", "Rows", "GdnError", "library", "LIB_PATH", "EXPORTS",
            "gdn_workspace_bytes", "gdn_prefill_workspace_bytes", "mixed_batch_workspace_bytes", "STATUS_WAIT_TIMEOUT", "gdn_conv_update", "gdn_recurrent_step", "gdn_chunk_prefill",
            "gdn_mixed_batch", "gdn_mixed_batch_static_workspace", "STATIC_WORKSPACE_BYTES",
-           "TESTING_EXPORTS", "gdn_testing_set_prefill_faults", "GDN_F32", "GDN_BF16", "STATUS_SLOT_RANGE", "STATUS_NUM_ACCEPTED",
+           "TESTING_EXPORTS", "gdn_testing_set_prefill_faults", "gdn_testing_set_shared_faults", "GDN_F32", "GDN_BF16", "STATUS_SLOT_RANGE", "STATUS_NUM_ACCEPTED",
            "STATUS_TOKEN_RANGE", "STATUS_ROW_RANGE", "KvCache", "KvRows", "Attention", "gdn_kv_append",
            "gdn_paged_attention", "gdn_attention_workspace_bytes", "gdn_kv_reserve", "gdn_kv_release", "gdn_kv_fork",
            "gdn_kv_copy_pages", "gdn_kv_compact", "gdn_kv_workspace_bytes", "gdn_copy_slots", "STATUS_PAGE_RANGE",

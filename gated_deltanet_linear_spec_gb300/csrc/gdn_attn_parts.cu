@@ -21,6 +21,12 @@ struct JoinParams {
   int team;  // warps of a query
 };
 
+// Whether a range names pieces that there are: one that a pass did not write, because a wait of it gave up, holds whatever the
+// workspace held before.
+__device__ __forceinline__ bool names_pieces(const PieceRange& r, const PartPieces& of) {
+  return r.c0 < 0 || (r.c0 <= r.c1 && r.c1 < of.workers && r.qi >= 0 && r.qi < of.queries);
+}
+
 template <int E>
 __device__ __forceinline__ void load_row(const float* v, bool there, float (&x)[E]) {
   if constexpr (E == 1) {
@@ -68,7 +74,8 @@ __global__ void __launch_bounds__(32 * kWarps) join_parts_kernel(JoinParams J) {
       r[s] = {x.x, x.y, x.z, 0};
     }
   }
-  const bool there = rec.x >= 0 && g >= 0 && g < p.num_global;
+  const bool there = rec.x >= 0 && g >= 0 && g < p.num_global && (!rec.y || names_pieces(r[0], J.from)) &&
+                     names_pieces(r[1], J.from);
   const int n0 = !there || !rec.y ? 0 : r[0].c0 < 0 ? 1 : r[0].c1 - r[0].c0 + 1;
   const int n = !there ? 0 : n0 + (r[1].c0 < 0 ? 1 : r[1].c1 - r[1].c0 + 1);
   float m = -INFINITY, l = 0.f, o[E];

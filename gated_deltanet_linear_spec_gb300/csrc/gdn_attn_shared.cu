@@ -19,9 +19,11 @@
 // one score buffer, the first took 155 us (151 at that time, with one term); with the rows' own parts on mma.sync beside
 // this kernel's end 158 and the second 49 (151 and 40).
 #include <algorithm>
+#include <atomic>
 
 #include "gdn_attn_share.cuh"
 #include "gdn_attn_tile.cuh"
+#include "gdn_testing.h"
 
 namespace gdn {
 
@@ -42,7 +44,11 @@ struct SharedParams {
   float* o;      // [2 * kSms][kRows][D]
   float* stats;  // [2 * kSms][kRows][2]
   uint64_t wait_ns;
+  int32_t stop_tile;  // fetches end in front of a CTA's so manieth tile; -1: they do not
 };
+// Test hook (gdn_testing.h).
+std::atomic<uint64_t> g_test_wait_ns{0};
+std::atomic<int32_t> g_test_stop_tile{-1};
 
 template <int D>
 struct Small {
@@ -355,6 +361,10 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       const int entries = (w.u.r.kv + ps - 1) >> shift, h = head_of();
       int eb = -64, ids = 0, ahead = 0;  // 32 table entries are held, one per lane, and the 32 behind them
       for (int j = w.j0; j < w.j0 + w.len && ok; ++j, at += 2, ++tiles) {
+        if (tiles == (uint32_t)P.stop_tile) {
+          ok = false;
+          break;
+        }
         const int b = w.tile_at(j), pos = b + bi * box, e = b >> shift;
         if (e >= eb + 32) {
           if (e < eb + 64) {
@@ -460,7 +470,9 @@ cudaError_t launch_d(const AttnLaunch& a, cudaStream_t s) {
   const PartPieces pieces = attn_shared_pieces(a, a.ws);
   P.stats = pieces.stats;
   P.o = pieces.o;
-  P.wait_ns = kDefaultWaitNs;
+  const uint64_t wait = g_test_wait_ns.load(std::memory_order_relaxed);
+  P.wait_ns = wait ? wait : kDefaultWaitNs;
+  P.stop_tile = g_test_stop_tile.load(std::memory_order_relaxed);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -494,7 +506,7 @@ size_t attn_shared_workspace(const AttnLaunch& a) { return (size_t)2 * kSms * ro
 PartPieces attn_shared_pieces(const AttnLaunch& a, void* ws) {
   const int rows = rows_of_cta(a);
   float* stats = static_cast<float*>(ws);
-  return {stats, stats + (size_t)4 * kSms * rows, rows};
+  return {stats, stats + (size_t)4 * kSms * rows, rows, kSms};
 }
 
 // Two terms a weight wherever attention without groups would take some row of the call to the split kernel, which keeps 16 bits.
@@ -504,3 +516,9 @@ cudaError_t launch_attn_shared(const AttnLaunch& a, cudaStream_t s) {
 }
 
 }  // namespace gdn
+
+extern "C" int gdn_testing_set_shared_faults(uint64_t wait_ns, int32_t stop_tile) {
+  gdn::g_test_wait_ns.store(wait_ns, std::memory_order_relaxed);
+  gdn::g_test_stop_tile.store(stop_tile < 0 ? -1 : stop_tile, std::memory_order_relaxed);
+  return GDN_OK;
+}

@@ -382,7 +382,7 @@ size_t attn_split_fma_parts_workspace(const AttnLaunch& a) {
 PartPieces attn_split_fma_parts_pieces(const AttnLaunch& a, void* ws) {
   const int workers = kSms * per_sm(a.cache.d, true) * kWarps;
   float* stats = static_cast<float*>(ws) + 8 * workers;
-  return {stats, stats + (size_t)4 * workers * kNQ, kNQ};
+  return {stats, stats + (size_t)4 * workers * kNQ, kNQ, workers};
 }
 
 cudaError_t launch_attn_split_fma_parts(const AttnLaunch& a, gdn_dtype dtype, cudaStream_t s) {

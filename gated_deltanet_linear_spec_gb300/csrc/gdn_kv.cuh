@@ -256,6 +256,7 @@ struct PartPieces {
   float* stats;
   float* o;
   int32_t queries;
+  int32_t workers;
 };
 bool attn_shared_supported(const AttnLaunch& p, gdn_dtype dtype);  // on tcgen05: rows of up to a CTA's queries
 size_t attn_shared_workspace(const AttnLaunch& p);

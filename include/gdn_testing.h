@@ -7,7 +7,7 @@
  * after a wall-clock limit, ORs GDN_STATUS_WAIT_TIMEOUT into the call's status word, waits (again
  * with the limit) for the products and copies that block still has in flight, frees its tensor
  * memory and returns ("[XE2] Support MTP of QWEN model", review notes: problems are reported,
- * never undefined behaviour).  The hook below makes one of those waits run out on purpose.
+ * never undefined behaviour).  The hooks below make one of those waits run out on purpose.
  */
 #ifndef GDN_TESTING_H
 #define GDN_TESTING_H
@@ -30,6 +30,16 @@ extern "C" {
  * returns 0 (GDN_OK).  Reset with gdn_testing_set_prefill_faults(0, -1).
  */
 int gdn_testing_set_prefill_faults(uint64_t wait_ns, int32_t drop_copy_chunk);
+
+/*
+ * The same for gdn_shared_attention's tensor-core pass, whose waits are bounded likewise:
+ *   wait_ns    as above;
+ *   stop_tile  every CTA fetches no cached tile from this one of its share on (none of their
+ *              copies is issued), so that the waits for it run out; < 0 for none (the default).
+ * Queries whose results the pass did not leave are not written.  Always returns 0 (GDN_OK).  Reset
+ * with gdn_testing_set_shared_faults(0, -1).
+ */
+int gdn_testing_set_shared_faults(uint64_t wait_ns, int32_t stop_tile);
 
 #ifdef __cplusplus
 }
