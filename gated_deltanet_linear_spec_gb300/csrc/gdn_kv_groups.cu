@@ -96,7 +96,9 @@ __global__ void __cluster_dims__(kCluster) __launch_bounds__(THREADS) common_ker
     const int64_t runs = (int64_t)((whole + kRun - 1) / kRun) * rows;
     for (int64_t i = (mine * kCluster + rank) * kWarps + warp; i < runs; i += clusters * kCluster * kWarps) {
       const int n = a + (int)(i % rows), e0 = (int)(i / rows) * kRun;
-      if (e0 >= *(volatile int*)&agree) break;
+      // (one lane reads it, as others' warps lower it and this one's first lane just did: all lanes stay or all leave)
+      const int until = lane == 0 ? *(volatile int*)&agree : 0;
+      if (e0 >= __shfl_sync(0xffffffffu, until, 0)) break;
       KvRow r;
       if (n == s.first || !load_kv_row(p.rows, p.cache, n, r, nullptr) || r.len == 0) continue;
       const int32_t* of_row = p.cache.table + (int64_t)r.trow * p.cache.max_pages;
