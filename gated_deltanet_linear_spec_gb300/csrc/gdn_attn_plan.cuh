@@ -15,6 +15,14 @@ __device__ __forceinline__ bool group_bounds(int a, int b, int num_seqs, uint32_
   return false;
 }
 
+// Whether row n's local tokens are some of the call's.  (Where all rows' are, rows follow one another and no token is in two.  With
+// one that is not, a token may be in several rows, or between a group's first and last without being of its rows: nothing is
+// shared then, and every row that is well formed goes over its own cache.)
+__device__ __forceinline__ bool row_bounds(const KvRowsDev& R, int n) {
+  const int a = load(R.qsl + n), b = load(R.qsl + n + 1);
+  return a >= 0 && b >= a && b <= R.num_tokens;
+}
+
 // What a group's rows say together: those with new tokens that are well formed.
 struct GroupRows {
   int count;
@@ -81,9 +89,11 @@ __device__ const PartRec* plan_here(const AttnLaunch& p, int* scratch) {
     g1 = load(part.start + tid + 1);
     given = load(part.prefix + tid);
   }
+  bool ascend = true;
   for (int n = tid; n < R.num_seqs; n += THREADS) {
     KvRow r;
     const bool there = load_kv_row(R, p.cache, n, r, st);
+    ascend &= row_bounds(R, n);
     first[n] = r.bos;
     len[n] = there ? r.len : 0;
     kv[n] = r.kv;
@@ -92,7 +102,8 @@ __device__ const PartRec* plan_here(const AttnLaunch& p, int* scratch) {
   }
   if (tid <= part.groups) start[tid] = g0;
   if (tid < part.groups) prefix[tid] = given;
-  const bool none = __syncthreads_or(tid < part.groups && !group_bounds(g0, g1, R.num_seqs, st));  // nothing is shared
+  ascend = __syncthreads_and(ascend);
+  const bool none = __syncthreads_or(tid < part.groups && !group_bounds(g0, g1, R.num_seqs, st)) || !ascend;  // nothing is shared
   PartRec* recs = part_recs(part);
   int2* token = part_tokens(part);
   for (int g = tid >> 5; g < part.groups; g += THREADS / 32) {
@@ -118,9 +129,13 @@ __device__ const PartRec* plan_here(const AttnLaunch& p, int* scratch) {
   const bool all = p.window > 0;
   if (!all) token = part.token;
   for (int i = all ? tid : tid * gridDim.x + blockIdx.x; i < R.num_tokens; i += all ? THREADS : THREADS * gridDim.x) {
-    int n = 0;  // the last row that begins at or before the token
-    for (int step = kPlanRows / 2; step; step >>= 1)
-      if (n + step < R.num_seqs && first[n + step] <= i) n += step;
+    int n = 0;  // the last row that begins at or before the token, or, of bounds that do not ascend, the last one that holds it
+    if (ascend) {
+      for (int step = kPlanRows / 2; step; step >>= 1)
+        if (n + step < R.num_seqs && first[n + step] <= i) n += step;
+    } else {
+      for (n = R.num_seqs - 1; n > 0 && !(i >= first[n] && i < first[n] + len[n]);) --n;
+    }
     const bool there = i >= first[n] && i < first[n] + len[n];
     token[i] = there ? make_int2(kv[n] - len[n] + i - first[n], own[n] & 1) : make_int2(-1, 0);
   }

@@ -141,6 +141,7 @@ __device__ __forceinline__ void place_tokens(int2* token, const KvRow& r, int fr
 // move the beginnings of their rows' own parts.
 __global__ void __cluster_dims__(kCluster) __launch_bounds__(kThreads) group_plan_kernel(GroupsLaunch p) {
   constexpr int kAll = kCluster * kThreads;
+  __shared__ int bad_bounds;  // a row's or a group's, of those that this CTA looks at
   const int lane = threadIdx.x & 31;
   const int me = blockIdx.x * kThreads + threadIdx.x;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -148,6 +149,7 @@ __global__ void __cluster_dims__(kCluster) __launch_bounds__(kThreads) group_pla
   for (int i = me; i < p.rows.num_tokens; i += kAll) p.token[i] = make_int2(-1, 0);
   cluster_sync();
   const bool lanes = p.rows.max_q > 64;  // a row's tokens go to a warp's lanes
+  bool bad = false;
   for (int n = lanes ? me >> 5 : me; n < p.rows.num_seqs; n += lanes ? kAll / 32 : kAll) {
     KvRow r;
     PartRec rec{};
@@ -156,14 +158,18 @@ __global__ void __cluster_dims__(kCluster) __launch_bounds__(kThreads) group_pla
       place_tokens(p.token, r, lanes ? lane : 0, lanes ? 32 : 1, 0);
     }
     if (!lanes || lane == 0) p.recs[p.num_groups + n] = rec;
+    bad |= !row_bounds(p.rows, n);
   }
-  bool none = false;  // nothing is shared
-  for (int g = threadIdx.x; g < p.num_groups; g += kThreads) {
+  for (int g = me; g < p.num_groups; g += kAll) {
     int a, b;
-    none |= !group_rows(p, g, a, b, p.status);
+    bad |= !group_rows(p, g, a, b, p.status);
   }
-  none = __syncthreads_or(none);
+  bad = __syncthreads_or(bad);
+  if (threadIdx.x == 0) bad_bounds = bad;
+  __syncthreads();
   cluster_sync();
+  // nothing is shared where some are
+  const bool none = __any_sync(0xffffffffu, lane < kCluster && from_rank(&bad_bounds, lane));
   for (int g = me >> 5; g < p.num_groups; g += kAll / 32) {
     int a, b;
     if (none || !group_rows(p, g, a, b, nullptr)) a = b = 0;
@@ -184,6 +190,7 @@ __global__ void __cluster_dims__(kCluster) __launch_bounds__(kThreads) group_pla
       p.recs[g] = rec;
     }
   }
+  cluster_sync();  // (no CTA ends while another reads its shared memory)
 }
 
 template <typename... Args>

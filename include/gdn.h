@@ -405,8 +405,9 @@ typedef struct {
  * shared and over the row's own tokens meet as those of a split row do.
  * Shared are min(prefix_lens[g], kv_lens[n] - L of the rows with new tokens) tokens, down to whole pages, where at least
  * two rows of the group have new tokens; prefix_lens <= 0 shares nothing.  They are read by the table row of the
- * first such row: where the rows' entries differ after all, its pages count.  A row is in one group at most: where
- * group bounds do not ascend or leave the rows (GDN_STATUS_ROW_RANGE), nothing is shared.
+ * first such row: where the rows' entries differ after all, its pages count.  A row is in one group at most, a token in
+ * one row: where the bounds of a group do not ascend or leave the rows, or those of a row do not ascend or leave the
+ * tokens (GDN_STATUS_ROW_RANGE), nothing is shared, and rows that are well formed go over their own caches.
  * bf16 rows of more than 256 queries per kv-head (d = 64, 128; 128 at d = 256; max_query_len decides) go over their
  * whole caches as in gdn_paged_attention, whatever the groups are: they fill the tensor cores by themselves.  Weights go
  * into the second sum with the bits that gdn_paged_attention keeps of them: 16 of bf16 rows (d = 64, 128, 256) in calls
