@@ -65,6 +65,31 @@ __device__ __forceinline__ bool load_kv_row(const KvRowsDev& R, const KvDev& C, 
                       R.table_rows ? load(R.table_rows + n) : n, r, st);
 }
 
+// A row that holds a local token, for one that a search among ascending bounds did not find: the bounds of a bad row may have
+// stood in its way.  -1 for none, at once for tokens behind the last row.  All lanes of a warp call together.
+__device__ __forceinline__ int row_past_bad_bounds(const KvRowsDev& R, int local) {
+  const int lane = threadIdx.x & 31, end = load(R.qsl + R.num_seqs);
+  if (end >= 0 && end <= local) return -1;
+  for (int n0 = 0; n0 < R.num_seqs; n0 += 32) {
+    const int n = n0 + lane;
+    bool holds = false;
+    if (n < R.num_seqs) {
+      const int a = load(R.qsl + n), b = load(R.qsl + n + 1);
+      holds = a >= 0 && a <= local && local < b && b <= R.num_tokens && b - a <= R.max_q;
+    }
+    const uint32_t m = __ballot_sync(0xffffffffu, holds);
+    if (m) return n0 + __ffs(m) - 1;
+  }
+  return -1;
+}
+// The row of a local token, which a search among ascending bounds found to be row n; false for a token of no good row.
+__device__ __forceinline__ bool load_row_of_token(const KvRowsDev& R, const KvDev& C, int local, int n, KvRow& r, uint32_t* st) {
+  const auto of_row = [&](int i) { return load_kv_row(R, C, i, r, st) && local >= r.bos && local < r.bos + r.len; };
+  if (of_row(n)) return true;
+  n = row_past_bad_bounds(R, local);
+  return n >= 0 && of_row(n);
+}
+
 // Global token of local token i (identity when there is no token_indx), or -1 if out of range.
 __device__ __forceinline__ int32_t kv_token(const KvRowsDev& R, int32_t i, int32_t num_global, uint32_t* st) {
   const int32_t g = R.tok ? load(R.tok + i) : i;

@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendLaunch p) {
     if (load(p.rows.qsl + mid) <= local) lo = mid; else hi = mid - 1;
   }
   KvRow r;
-  if (!load_kv_row(p.rows, C, lo, r, p.status) || local < r.bos || local >= r.bos + r.len) return;
+  if (!load_row_of_token(p.rows, C, local, lo, r, p.status)) return;
   const int pos = r.kv - r.len + (local - r.bos);
   const int32_t raw = C.table[(int64_t)r.trow * C.max_pages + pos / C.page_size];
   const int32_t page = page_or_null(raw, C, p.status);

@@ -86,7 +86,7 @@ __device__ __forceinline__ Place place_of(const TurnLaunch& p, int local, int32_
   const KvDev& C = p.cache;
   Place w{-1, 0, 0, 0};
   KvRow r;
-  if (!load_kv_row(p.rows, C, row_of(p.rows, local), r, p.status) || local < r.bos || local >= r.bos + r.len) return w;
+  if (!load_row_of_token(p.rows, C, local, row_of(p.rows, local), r, p.status)) return w;
   w.pos = r.kv - r.len + (local - r.bos);
   w.slot = w.pos & (C.page_size - 1);
   w.page = page_or_null(load(C.table + (int64_t)r.trow * C.max_pages + w.pos / C.page_size), C, p.status);

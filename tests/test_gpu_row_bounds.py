@@ -6,6 +6,7 @@ import torch
 import gated_deltanet_linear_spec_gb300 as gdn
 from tests import kv_reference as ref
 from tests.test_gpu_attention import BF16, F32, i32
+from tests.test_gpu_rope import Batch
 from tests.test_gpu_shared import Groups, weight_bits
 
 pytestmark = pytest.mark.gpu
@@ -84,3 +85,68 @@ def test_a_bad_bound_beside_long_rows(many, dtype):
     starts[2] = -1
     spoiled(s, starts)
     check(s)
+
+
+# ------------------------------------------------------------------------------------------
+# appending
+
+@pytest.mark.parametrize("turned", [False, True], ids=["append", "append_rope"])
+@pytest.mark.parametrize("rows", [9, 100, 3000])
+@pytest.mark.parametrize("value", [1000000, -5, 0, 1 << 31])
+@pytest.mark.parametrize("at", [0, 2, 5, -2, -1])
+def test_append_behind_a_bound_that_is_none(at, value, rows, turned):
+    b = Batch([(1 + i % 3, 20 + i % 5) for i in range(rows)], gather=False, seed=rows)
+    starts, total = list(b.starts), b.starts[-1]
+    starts[at] = value - (1 << 32) if value >> 31 == 1 else value
+    if starts == b.starts:
+        return
+    r = b.kv_rows
+    kv_rows = gdn.KvRows(i32(starts), total, r.kv_lens, 3, r.table_rows)
+    k, v = torch.full_like(b.k_pool, 5.0), torch.full_like(b.v_pool, 5.0)
+    left, places = 0, []
+    for i, (lo, hi, (_, kv)) in enumerate(zip(starts, starts[1:], b.rows)):
+        if not 0 <= lo <= hi <= total or hi - lo > 3:
+            continue
+        left += 1
+        for t in range(lo, hi):
+            pos = kv - (hi - lo) + t - lo
+            places.append((t, pos, int(b.table[b.table_rows[i], pos // b.page]), pos % b.page))
+    assert left >= rows - 2
+    token, pos, page, slot = (list(x) for x in zip(*places))
+    status, out = i32([0]), torch.full_like(b.q.contiguous(), 7.0)
+    if turned:
+        rope = gdn.Rope(64)
+        positions = torch.zeros(b.q.shape[0], dtype=torch.int32)
+        positions[token] = torch.tensor(pos, dtype=torch.int32)
+        want_q, want_k = torch.empty_like(out), torch.empty_like(b.k.contiguous())
+        gdn.gdn_rope(rope, positions.cuda(), b.q, want_q)
+        gdn.gdn_rope(rope, positions.cuda(), b.k, want_k)
+        gdn.gdn_kv_append_rope(b.cache, kv_rows, rope, b.k, b.v, b.q, out, status=status)
+        mine = torch.zeros(out.shape[0], dtype=torch.bool, device="cuda")
+        mine[token] = True
+        assert torch.equal(out[mine], want_q[mine]) and torch.all(out[~mine] == 7.0)
+    else:
+        want_k = b.k
+        gdn.gdn_kv_append(b.cache, kv_rows, b.k, b.v, status=status)
+    k[page, :, slot], v[page, :, slot] = want_k[token], b.v[token]
+    assert torch.equal(b.k_pool, k) and torch.equal(b.v_pool, v)
+    assert int(status) == gdn.STATUS_ROW_RANGE
+
+
+@pytest.mark.parametrize("turned", [False, True], ids=["append", "append_rope"])
+def test_append_of_a_padded_batch(turned):
+    """Tokens behind the last row, and rows without tokens at the end, are nobody's."""
+    b = Batch([(2, 40), (1, 33), (3, 50), (0, 20), (0, 30)], gather=False)
+    r, n = b.kv_rows, b.q.shape[0]
+    kv_rows = gdn.KvRows(r.query_start_loc, n, r.kv_lens, 3, r.table_rows)
+    status, out = i32([0]), torch.full_like(b.q.contiguous(), 7.0)
+    if turned:
+        gdn.gdn_kv_append_rope(b.cache, kv_rows, gdn.Rope(64), b.k, b.v, b.q, out, status=status)
+        assert torch.all(out[6:] == 7.0) and not torch.any(out[:6] == 7.0)
+    else:
+        gdn.gdn_kv_append(b.cache, kv_rows, b.k, b.v, status=status)
+    written = {(page, slot) for _, _, page, slot in b.positions()}
+    for page in range(b.v_pool.shape[0]):
+        for slot in range(b.page):
+            assert bool(torch.all(b.v_pool[page, :, slot] == 5.0)) == ((page, slot) not in written)
+    assert int(status) == 0
