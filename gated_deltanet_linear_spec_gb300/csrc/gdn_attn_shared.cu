@@ -41,7 +41,7 @@ __host__ __device__ constexpr int phases_of(int d) { return 512 / d; }
 
 struct SharedParams {
   AttnLaunch a;
-  float* o;      // [2 * kSms][kRows][D]
+  float* o;      // [2 * kSms][D / 4][kRows][4]
   float* stats;  // [2 * kSms][kRows][2]
   uint64_t wait_ns;
   int32_t stop_tile;  // fetches end in front of a CTA's so manieth tile; -1: they do not
@@ -384,8 +384,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
           const uint32_t a = at + v, en = a % R;
           ok = __all_sync(0xffffffffu, a < R || tc::mbar_wait(&sm.empty[en], (a / R - 1) & 1, P.wait_ns));
           if (!ok) break;
+          if (lane == 0 && v == 0) sm.held[tiles & 15] = mask;  // (before the arrival, which releases it to those who wait)
           if (bi == 0) tc::expect_tx(&sm.full[en], C::kKv);
-          if (lane == 0 && v == 0) sm.held[tiles & 15] = mask;
           __syncwarp();
           if (active) tc::tma_page(ring + en * C::kKv + bi * box * D * 2, v ? &vmap : &kmap, slot, slab, &sm.full[en]);
           fetched = kTogether ? at + 2 : a + 1;

@@ -152,7 +152,7 @@ struct PartDev {
   int32_t plan_here;    // the pass makes recs and token itself, a copy of them for each CTA
   PieceRange* range;    // [2][tokens][Hq]
   float* ml;            // [2][tokens][Hq][2]: m (of the scores before their scale), l of a query in one piece
-  float* o;             // [2][tokens][Hq][d], or with `quads` [2][d / 4][tokens][Hq][4]
+  float* o;             // [2][tokens][Hq][d], or with `quads` [d / 4][2][tokens][Hq][4]
   uint64_t g_magic, h_magic;  // magic_of q-heads per kv-head and kv-heads
   int32_t quads;        // o, here and in pieces, by four columns: what neighbouring queries write is side by side
 };
