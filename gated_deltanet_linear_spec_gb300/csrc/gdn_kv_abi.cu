@@ -142,7 +142,8 @@ bool rope_turns(const gdn_rope_freq& f, uint64_t* turns, float* magnitude) {
     }
     if (!turn_fraction(w, turns[i])) return false;
   }
-  if (magnitude) *magnitude = f.scaling == GDN_ROPE_RAMP ? (float)(0.1 * log(f.factor) + 1.0) : 1.f;
+  // (a context that is not stretched needs none)
+  if (magnitude) *magnitude = f.scaling == GDN_ROPE_RAMP && f.factor > 1.0 ? (float)(0.1 * log(f.factor) + 1.0) : 1.f;
   return true;
 }
 

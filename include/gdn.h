@@ -462,7 +462,8 @@ typedef struct {
  *   BANDS   pairs that turn `high` times or more over original_len are kept, those of `low` or fewer are divided by factor,
  *           and between them w f_i + (1-w) f_i / factor with w linear in the number of turns (0: low 1, high 4);
  *   RAMP    as BANDS, with w linear in the pair's number between the pair that turns `high` times (rounded down, at least
- *           0) and the one that turns `low` times (rounded up, at most r-1) (0: low 1, high 32); magnitude 0.1 ln factor + 1.
+ *           0) and the one that turns `low` times (rounded up, at most r-1) (0: low 1, high 32); magnitude 0.1 ln factor + 1,
+ *           for factors up to 1 it is 1.
  */
 typedef enum {
   GDN_ROPE_PLAIN = 0,
