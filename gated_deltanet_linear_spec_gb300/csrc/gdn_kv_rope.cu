@@ -2,9 +2,10 @@
 //
 // Pair i of a head's first r = rotary_dim values is (x_i, x_{i+r/2}) or (x_2i, x_2i+1); at position p it turns by the
 // angle p f_i.  Frequencies are 64-bit fractions of a turn, so p f_i mod 1 is a product of whole numbers that wraps
-// around: exact to 2^-33 of a turn for every 32-bit position, where a 32-bit product of position and frequency is off by
-// 0.06 at 10^6.  The turn's quarter comes from the top bits, and what is left, at most an eighth of a turn, goes
-// through sincospi in 32 bits: cosine and sine are off by 2^-23 at most.
+// around: exact for the stored fraction and every 32-bit position, and then rounded by 2^-33 of a turn, where a 32-bit product
+// of position and frequency is off by 0.06 at 10^6.  (The fraction itself comes from doubles; what it is off by, 2^-53 of a
+// turn at most, the position multiplies.)  The turn's quarter comes from the top bits, and what is left, at most an eighth of a
+// turn, goes through sincospi in 32 bits: cosine and sine of the stored angle are off by 2^-23 at most.
 //
 // Every value is read and written once, so HBM bounds long calls and the launch short ones: 8192 tokens of 32 heads (bf16, d
 // = 128, 134 MB) take 20.7 us, 6.5 TB/s; 8192 into the cache (16 q, 2 kv heads, d = 256, 168 MB) 30.4, 5.5 TB/s, as every

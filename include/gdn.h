@@ -443,7 +443,9 @@ int gdn_kv_common_prefix(const gdn_kv_cache* cache, const gdn_kv_rows* rows, con
  *   (x cos a - y sin a, y cos a + x sin a) * magnitude,   a = p * f_i,
  * in fp32, rounded once to the dtype; values from rotary_dim on are copied.  A negative position turns back, so the same
  * call at -p is the transposed map: the gradient of the inputs, and (magnitude 1) the inverse.
- * Frequencies are 64-bit binary fractions of a turn, so p * f_i is exact to 2^-33 of a turn at every 32-bit position.
+ * Frequencies are 64-bit binary fractions of a turn: the product of a position and a stored fraction is exact modulo a turn and
+ * then rounded by 2^-33 of a turn.  The fractions of gdn_rope_turns are made in doubles, off by 2^-53 of a turn at most (of
+ * frequencies up to 1 radian a position), which the position multiplies: 2^-33 of a turn at 2^20, 2^-22 at 2^31.
  */
 typedef enum { GDN_ROPE_HALF = 0, GDN_ROPE_INTERLEAVED = 1 } gdn_rope_layout;
 
