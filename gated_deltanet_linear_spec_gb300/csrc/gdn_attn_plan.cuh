@@ -92,8 +92,8 @@ __device__ const PartRec* plan_here(const AttnLaunch& p, int* scratch) {
   bool ascend = true;
   for (int n = tid; n < R.num_seqs; n += THREADS) {
     KvRow r;
-    const bool there = load_kv_row(R, p.cache, n, r, st);
     ascend &= row_bounds(R, n);
+    const bool there = load_kv_row(R, p.cache, n, r, st);
     first[n] = r.bos;
     len[n] = there ? r.len : 0;
     kv[n] = r.kv;

@@ -33,7 +33,7 @@ using namespace tile;
 
 // Beginning a unit -- its queries, the first scores, its results -- takes about as long as so many 64-token steps: steps of two
 // query tiles, where the call has units of two, or the shorter ones of one.  (16 groups of 4 rows of 4 tokens behind 8192, 20 own
-// ones each: 72 us with 4, 92 with 2; behind 512 30.6 and 28.3.  One group of 64 rows of 1 behind 8200: 38.6 with 4, 36.1 with 2.)
+// ones each: 77 us with 4, 83 with 2; behind 512 31.5 and 28.2.  One group of 64 rows of 1 behind 8200: 42.3 with 4, 39.1 with 2.)
 constexpr int kBegin = 2, kBeginOne = 4;
 
 // K and V pairs in the ring: 128 KB, which keeps HBM busy under short steps too.
@@ -349,7 +349,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
   } else if (role == 2) {
     // ---- fetches: a lane per page of the tile ----
     // With a long ring K's pages and V's go together, a half of the warp each, in half the time (a step of one query tile is
-    // short: 64 rows of 8000 own tokens, pages of 16, d = 64, 327 us one after the other, 283 together); with a short one K does
+    // short: 64 rows of 8000 own tokens, pages of 16, d = 64, 385 us one after the other, 353 together); with a short one K does
     // not wait for V's place.
     constexpr bool kTogether = kPh > 2;
     const int bi = kTogether ? lane & 15 : lane, spp = slabs_per_page(kv);

@@ -31,6 +31,13 @@ __device__ __forceinline__ int from_rank(const int* mine, int rank) {
   return v;
 }
 
+// Sets `mine` of CTA `rank` of the cluster.
+__device__ __forceinline__ void to_rank(int* mine, int rank, int v) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"((uint32_t)__cvta_generic_to_shared(mine)), "r"(rank));
+  asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+
 __device__ __forceinline__ bool group_rows(const GroupsLaunch& p, int g, int& a, int& b, uint32_t* st) {
   a = load(p.start + g);
   b = load(p.start + g + 1);
@@ -53,7 +60,7 @@ __device__ __forceinline__ const int32_t* entries_of(const GroupsLaunch& p, int 
 // A cluster per group, or `clusters` of them, which meet in prefix[g] (set to the highest value before).  Its warps take runs
 // of kRun entries of the rows in turn, those of all rows' beginnings first, and compare them with those of the group's
 // first row; what lies behind a place where rows were seen to part is left out.
-// 16 groups of 9 to 24 rows that share up to 8192 entries: 59 us with a warp per row, 9 so; what bounds it is its chain of
+// 16 groups of 9 to 24 rows that share up to 8192 entries: 59 us with a warp per row, 9.6 so; what bounds it is its chain of
 // loads: bounds, rows, entries (5 MB in all; 4 rows of 777 tokens take 3.2).
 constexpr int kAhead = 8;  // entries of a lane that are on their way
 constexpr int kRun = 32 * kAhead;
@@ -141,35 +148,32 @@ __device__ __forceinline__ void place_tokens(int2* token, const KvRow& r, int fr
 // move the beginnings of their rows' own parts.
 __global__ void __cluster_dims__(kCluster) __launch_bounds__(kThreads) group_plan_kernel(GroupsLaunch p) {
   constexpr int kAll = kCluster * kThreads;
-  __shared__ int bad_bounds;  // a row's or a group's, of those that this CTA looks at
+  __shared__ int none;  // nothing is shared
   const int lane = threadIdx.x & 31;
   const int me = blockIdx.x * kThreads + threadIdx.x;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   for (int i = me; i < p.rows.num_tokens; i += kAll) p.token[i] = make_int2(-1, 0);
+  if (threadIdx.x == 0) none = 0;
   cluster_sync();
   const bool lanes = p.rows.max_q > 64;  // a row's tokens go to a warp's lanes
-  bool bad = false;
+  bool bad = false;  // bounds of a row or a group
   for (int n = lanes ? me >> 5 : me; n < p.rows.num_seqs; n += lanes ? kAll / 32 : kAll) {
     KvRow r;
     PartRec rec{};
+    bad |= !row_bounds(p.rows, n);
     if (load_kv_row(p.rows, p.cache, n, r, p.status) && r.len > 0) {
       rec = {r.bos, r.len, 0, r.kv, r.trow, r.kv - r.len, r.kv - 1, 0};
       place_tokens(p.token, r, lanes ? lane : 0, lanes ? 32 : 1, 0);
     }
     if (!lanes || lane == 0) p.recs[p.num_groups + n] = rec;
-    bad |= !row_bounds(p.rows, n);
   }
   for (int g = me; g < p.num_groups; g += kAll) {
     int a, b;
     bad |= !group_rows(p, g, a, b, p.status);
   }
-  bad = __syncthreads_or(bad);
-  if (threadIdx.x == 0) bad_bounds = bad;
-  __syncthreads();
+  for (int rank = 0; bad && rank < kCluster; ++rank) to_rank(&none, rank, 1);
   cluster_sync();
-  // nothing is shared where some are
-  const bool none = __any_sync(0xffffffffu, lane < kCluster && from_rank(&bad_bounds, lane));
   for (int g = me >> 5; g < p.num_groups; g += kAll / 32) {
     int a, b;
     if (none || !group_rows(p, g, a, b, nullptr)) a = b = 0;
@@ -190,7 +194,6 @@ __global__ void __cluster_dims__(kCluster) __launch_bounds__(kThreads) group_pla
       p.recs[g] = rec;
     }
   }
-  cluster_sync();  // (no CTA ends while another reads its shared memory)
 }
 
 template <typename... Args>
@@ -212,7 +215,7 @@ cudaError_t launch(void (*kernel)(Args...), int blocks, int threads, cudaStream_
 // Blocks of 1024 threads where a group's rows may have more entries than a cluster of smaller ones takes at once: those 16
 // groups 11 us, with blocks of 256 19; 4 rows of 64 entries 3.6 us with blocks of 1024, 3.2 with 256.  And as many clusters
 // a group as have 65536 entries each to go over at once, behind a launch that sets what they meet in: one group of 16 rows of
-// 8192 entries 5.7 us instead of 6.8, of 64 6 (18), of 256 7.5 (60); those 16 groups 9.2.
+// 8192 entries 5.7 us instead of 6.8, of 64 6 (18), of 256 7.5 (60); those 16 groups 9.6.
 cudaError_t launch_kv_common_prefix(const GroupsLaunch& p, cudaStream_t s) {
   const int64_t entries = (int64_t)p.cache.max_pages * p.rows.num_seqs / p.num_groups;
   if (entries <= kCluster * kThreads * kAhead)
@@ -223,10 +226,10 @@ cudaError_t launch_kv_common_prefix(const GroupsLaunch& p, cudaStream_t s) {
   return e != cudaSuccess ? e : launch(common_kernel<1024>, p.num_groups * clusters * kCluster, 1024, s, p, clusters);
 }
 
-// Every CTA goes over all rows, groups and tokens then, a warp per group.  Against a kernel for the plan, us a call: 4 rows of a
-// group 12.1 (13.6), 256 rows 24 (30), 16 groups of 16 rows of 4 tokens 29 (32), 32 of 8 28 (30), 64 of 4 32 (32); in the pass on
-// the CUDA cores, whose CTAs have 4 warps for 12 (of 8), 1 x 64 x 4 17 (20), 16 x 16 x 4 32 (33), 32 x 8 x 4 35 (33), 64 x 4 x 4
-// 40 (33).
+// Every CTA goes over all rows, groups and tokens then, a warp per group.  Against a kernel for the plan, us a call behind 777 shared
+// tokens, 20 own ones each (d = 128, 16/2 heads): 4 rows of a group 12.3 (14.5), 256 rows 33 (38); d = 64, 8/2 heads: 16 groups
+// of 16 rows of 4 tokens 35 (37), 32 of 8 38 (40); 64 of 4 were even.  In the pass on the CUDA cores, whose CTAs have 4 warps for
+// 12 (of 8), behind a shorter prefix 1 x 64 x 4 17 (20), 16 x 16 x 4 32 (33), 32 x 8 x 4 35 (33), 64 x 4 x 4 40 (33).
 bool group_plan_here(const AttnLaunch& p) {
   return p.rows.num_seqs <= kPlanRows && p.part.groups <= (p.part.quads ? kPlanGroups : kPlanGroups / 2) &&
          p.rows.num_tokens <= 4 * kPlanRows;
