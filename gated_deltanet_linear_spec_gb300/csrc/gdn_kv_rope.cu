@@ -7,9 +7,11 @@
 // turn at most, the position multiplies.)  The turn's quarter comes from the top bits, and what is left, at most an eighth of a
 // turn, goes through sincospi in 32 bits: cosine and sine of the stored angle are off by 2^-23 at most.
 //
-// Every value is read and written once, so HBM bounds long calls and the launch short ones: 8192 tokens of 32 heads (bf16, d
-// = 128, 134 MB) take 20.7 us, 6.5 TB/s; 8192 into the cache (16 q, 2 kv heads, d = 256, 168 MB) 30.4, 5.5 TB/s, as every
-// store to a page waits for a chain of token, row, table and page; one token 1.8.  A block takes a few tokens with all their
+// Every value is read and written once, so HBM bounds long calls and the launch short ones: 65536 tokens of 32 heads (bf16, d
+// = 128, 1.1 GB) take 153 us, 7.0 TB/s, 65536 into the cache (16 q, 2 kv heads, d = 256) 196, 6.8 TB/s; one token 1.8.  Of 8192
+// tokens the L2 keeps most of what is written (20.5 us, 134 MB, of them 67 read and 14 to 17 written in HBM; 59% of the issue
+// slots): blocks' waves of loads and stores bound them, and of the append (30.4 us, 168 MB) also that every
+// store to a page waits for a chain of token, row, table and page.  A block takes a few tokens with all their
 // heads: its threads' values are on their way while it looks up the tokens' rows and pages and works out the tokens' cosines
 // and sines, which all heads share, in shared memory.  A thread reads and writes both values of a pair, so a call may work
 // in place.

@@ -411,10 +411,11 @@ typedef struct {
  * bf16 rows of more than 256 queries per kv-head (d = 64, 128; 128 at d = 256; max_query_len decides) go over their
  * whole caches as in gdn_paged_attention, whatever the groups are: they fill the tensor cores by themselves.  Weights go
  * into the second sum with the bits that gdn_paged_attention keeps of them: 16 of bf16 rows (d = 64, 128, 256) in calls
- * without a row of more than 64 queries per kv-head, and of all rows in calls that it would take both ways; 8 in the rest.
- * Sharing pays from about a thousand tokens on for
- * groups of four rows or more, from several thousand on for pairs; below, a call takes up to twice as long as in
- * gdn_paged_attention, which finds the other rows' pages in the L2.
+ * without a row of more than 64 queries per kv-head, and of all rows in calls that it would take both ways; else 8 of bf16
+ * rows of these head dimensions, 24 of all others.
+ * Sharing pays from a few thousand tokens on for groups of four rows or more, hardly for pairs, and not for rows that have as
+ * many tokens of their own; then a call takes up to 2.3 times as long as in gdn_paged_attention, which finds the other rows'
+ * pages in the L2.
  * workspace: at least gdn_shared_attention_workspace_bytes(attn, cache, rows, groups) bytes, 256-byte aligned; it holds
  * the plan (a copy for each CTA that makes its own), two states of (2 + d) fp32 per query and head, and partial results.
  */
